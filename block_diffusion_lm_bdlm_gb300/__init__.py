@@ -14,6 +14,13 @@ The C functions are declared in include/bdlm.h; the Python names are the same:
   bdlm_attn_bwd_tasks(q, k, v, o, lse, dO, block, tasks, n_slots) -> (dq, dk [S,L,Hk,d], dv)
   bdlm_attn_fwd_noalloc(...)        forward without a caller workspace
   bdlm_selftest_timeout(workspace)  device wait-timeout self-test
+The paged 8-bit cache for answering (see PageCache in cache.py; decode.py
+drives it block by block):
+  bdlm_cache_write(cache, k_new, v_new, cu_rows)      quantise rows into the pages
+  bdlm_cache_attn_fwd(cache, q, cu_rows, block) -> (o, lse)
+  bdlm_cache_reserve(cache, new_lens)                 lengths, free pages
+  bdlm_cache_fork(cache, parents, children)           share pages, copy the last
+  bdlm_cache_compact(cache) -> n_live                 live pages to the front
 Restrictions of a call (see Partial):
   Partial.window(lo, hi)                     keys at positions [lo, hi) (a clean shard)
   Partial.window(lo, hi, accumulate=True)    merge into a running (out, lse)
@@ -38,6 +45,9 @@ __all__ = [
     "bdlm_attn_bwd_tasks", "bdlm_attn_bwd_tasks_workspace_bytes", "bdlm_attn_fwd_noalloc", "bdlm_attn_bwd", "bdlm_lse_merge", "bdlm_read_error",
     "bdlm_attn_fwd_workspace_bytes", "bdlm_attn_bwd_workspace_bytes", "bdlm_last_launch_count",
     "bdlm_selftest_timeout", "load_library", "EXPORTED_SYMBOLS",
+    "PageCache", "bdlm_cache_write", "bdlm_cache_attn_fwd", "bdlm_cache_reserve", "bdlm_cache_fork",
+    "bdlm_cache_compact", "bdlm_cache_write_workspace_bytes", "bdlm_cache_attn_fwd_workspace_bytes",
+    "bdlm_cache_pages_workspace_bytes",
 ]
 
 BDLM_OK = 0
@@ -52,6 +62,9 @@ EXPORTED_SYMBOLS = (
     "bdlm_attn_fwd_tasks_workspace_bytes", "bdlm_attn_fwd_tasks",
     "bdlm_attn_bwd_tasks_workspace_bytes", "bdlm_attn_bwd_tasks",
     "bdlm_selftest_timeout",
+    "bdlm_cache_write_workspace_bytes", "bdlm_cache_write", "bdlm_cache_attn_fwd_workspace_bytes",
+    "bdlm_cache_attn_fwd", "bdlm_cache_pages_workspace_bytes", "bdlm_cache_reserve", "bdlm_cache_fork",
+    "bdlm_cache_compact",
 )
 
 
@@ -110,6 +123,14 @@ class Partial:
             nb, ptr = b.numel(), b.data_ptr()
         flags = PART_ACCUMULATE if self.accumulate else 0
         return _CPartial(self.kind, nb, self.key_lo, self.key_hi, ptr, flags, o_dtype, self.q_lo, self.q_hi)
+
+
+class _CCache(ctypes.Structure):
+    _fields_ = [("k", ctypes.c_void_p), ("v", ctypes.c_void_p), ("k_scale", ctypes.c_void_p),
+                ("v_scale", ctypes.c_void_p), ("table", ctypes.c_void_p), ("lens", ctypes.c_void_p),
+                ("n_layers", ctypes.c_int32), ("n_pages", ctypes.c_int32), ("page", ctypes.c_int32),
+                ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("n_seqs", ctypes.c_int32),
+                ("max_pages", ctypes.c_int32), ("reserved", ctypes.c_int32)]
 
 
 class _CTask(ctypes.Structure):
@@ -184,6 +205,21 @@ def load_library() -> ctypes.CDLL:
     lib.bdlm_attn_bwd_tasks.restype = ctypes.c_int
     lib.bdlm_selftest_timeout.argtypes = [vp, sz, ctypes.c_uint32, vp]
     lib.bdlm_selftest_timeout.restype = ctypes.c_int
+    cache = ctypes.POINTER(_CCache)
+    lib.bdlm_cache_write_workspace_bytes.argtypes = []
+    lib.bdlm_cache_write_workspace_bytes.restype = sz
+    lib.bdlm_cache_write.argtypes = [cache, i32, vp, vp, i64, vp, vp, sz, vp]
+    lib.bdlm_cache_attn_fwd_workspace_bytes.argtypes = [i64, i32, i32, i32, i32]
+    lib.bdlm_cache_attn_fwd_workspace_bytes.restype = sz
+    lib.bdlm_cache_attn_fwd.argtypes = [cache, i32, vp, vp, vp, i64, i32, i32, vp, vp, f32, i32, vp, sz, vp]
+    lib.bdlm_cache_pages_workspace_bytes.argtypes = [i32, i32]
+    lib.bdlm_cache_pages_workspace_bytes.restype = sz
+    lib.bdlm_cache_reserve.argtypes = [cache, vp, vp, sz, vp]
+    lib.bdlm_cache_fork.argtypes = [cache, vp, vp, vp, i32, vp, sz, vp]
+    lib.bdlm_cache_compact.argtypes = [cache, vp, vp, sz, vp]
+    for f in (lib.bdlm_cache_write, lib.bdlm_cache_attn_fwd, lib.bdlm_cache_reserve, lib.bdlm_cache_fork,
+              lib.bdlm_cache_compact):
+        f.restype = ctypes.c_int
     _lib = lib
     return lib
 
@@ -510,3 +546,8 @@ def bdlm_read_error(workspace: Optional[torch.Tensor], stream=None) -> int:
     bdlm_attn_fwd_noalloc on the current device."""
     ptr = None if workspace is None else workspace.data_ptr()
     return int(load_library().bdlm_read_error(ptr, _stream(stream)))
+
+
+from .cache import (  # noqa: E402  (needs the names above)
+    PageCache, bdlm_cache_attn_fwd, bdlm_cache_attn_fwd_workspace_bytes, bdlm_cache_compact, bdlm_cache_fork,
+    bdlm_cache_pages_workspace_bytes, bdlm_cache_reserve, bdlm_cache_write, bdlm_cache_write_workspace_bytes)

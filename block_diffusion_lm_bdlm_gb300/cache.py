@@ -1,0 +1,241 @@
+"""Python binding of the paged 8-bit cache (the bdlm_cache_* calls of
+include/bdlm.h). Argument checks and marshalling only; see the header for the
+layout, the mask and what each call leaves undone on an error.
+
+A model that answers block by block uses the calls in this order, for every
+block (decode.BlockDecoder does it):
+
+  bdlm_cache_reserve(cache, lens + rows)            once
+  bdlm_cache_write(cache, k, v, cu, layer=i)        each layer, each denoising step
+  bdlm_cache_attn_fwd(cache, q, cu, B, layer=i)     likewise
+
+Problems found on the device (malformed offsets or tables, too few pages) are
+written to the error word of the workspace: pass `workspace` and read it with
+bdlm_read_error(workspace), or pass check=True, which synchronises and raises.
+"""
+from __future__ import annotations
+
+import ctypes
+from contextlib import nullcontext
+
+import torch
+
+from . import BDLM_BF16, BDLM_F32, _bf16_cuda, _CCache, _check, _shape, load_library
+
+PAGE_SIZES = (16, 32, 64, 128)
+
+
+class PageCache:
+    """The cache's device tensors, with their sizes:
+
+      k, v             float8_e4m3fn [n_layers, n_pages, Hk, page, d]
+      k_scale, v_scale fp32 [n_layers, n_pages, Hk]
+      table            int32 [n_seqs, max_pages]
+      lens             int32 [n_seqs]
+
+    All contiguous and on one device. The object holds no state of its own:
+    table and lens are the truth, and the calls and the program write them in
+    stream order. To end sequences, set their lens to 0.
+    """
+
+    __slots__ = ("k", "v", "k_scale", "v_scale", "table", "lens", "n_layers", "n_pages", "page", "kv_heads",
+                 "head_dim", "n_seqs", "max_pages", "device", "c")
+
+    def __init__(self, k, v, k_scale, v_scale, table, lens):
+        for nm, t, dt, dims in (("k", k, torch.float8_e4m3fn, 5), ("v", v, torch.float8_e4m3fn, 5),
+                                ("k_scale", k_scale, torch.float32, 3), ("v_scale", v_scale, torch.float32, 3),
+                                ("table", table, torch.int32, 2), ("lens", lens, torch.int32, 1)):
+            if not isinstance(t, torch.Tensor) or not t.is_cuda or t.dtype != dt or t.dim() != dims \
+                    or not t.is_contiguous() or t.numel() == 0:
+                raise ValueError(f"{nm} must be a contiguous {dt} CUDA tensor of {dims} dimensions")
+            if t.device != k.device:
+                raise ValueError(f"{nm} is on {t.device}, k on {k.device}")
+        self.n_layers, self.n_pages, self.kv_heads, self.page, self.head_dim = k.shape
+        self.n_seqs, self.max_pages = table.shape
+        if self.page not in PAGE_SIZES:
+            raise ValueError(f"the page size must be one of {PAGE_SIZES}, got {self.page}")
+        if self.head_dim not in (64, 128):
+            raise ValueError(f"head_dim must be 64 or 128, got {self.head_dim}")
+        _shape("v", v, k.shape)
+        _shape("k_scale", k_scale, k.shape[:3])
+        _shape("v_scale", v_scale, k.shape[:3])
+        _shape("lens", lens, (self.n_seqs,))
+        self.k, self.v, self.k_scale, self.v_scale, self.table, self.lens = k, v, k_scale, v_scale, table, lens
+        self.device = k.device
+        self.c = _CCache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), table.data_ptr(),
+                         lens.data_ptr(), self.n_layers, self.n_pages, self.page, self.kv_heads, self.head_dim,
+                         self.n_seqs, self.max_pages, 0)
+
+    @staticmethod
+    def empty(n_layers: int, n_pages: int, page: int, kv_heads: int, head_dim: int, n_seqs: int, max_pages: int,
+              device="cuda") -> "PageCache":
+        """A cache of n_pages free pages and n_seqs empty sequences."""
+        codes = [torch.empty((n_layers, n_pages, kv_heads, page, head_dim), dtype=torch.float8_e4m3fn, device=device)
+                 for _ in range(2)]
+        scales = [torch.ones((n_layers, n_pages, kv_heads), dtype=torch.float32, device=device) for _ in range(2)]
+        return PageCache(*codes, *scales, torch.zeros((n_seqs, max_pages), dtype=torch.int32, device=device),
+                         torch.zeros(n_seqs, dtype=torch.int32, device=device))
+
+
+def bdlm_cache_write_workspace_bytes() -> int:
+    return int(load_library().bdlm_cache_write_workspace_bytes())
+
+
+def bdlm_cache_attn_fwd_workspace_bytes(total_rows: int, heads: int, kv_heads: int, head_dim: int,
+                                        n_seqs: int) -> int:
+    return int(load_library().bdlm_cache_attn_fwd_workspace_bytes(total_rows, heads, kv_heads, head_dim, n_seqs))
+
+
+def bdlm_cache_pages_workspace_bytes(n_pages: int, n_seqs: int) -> int:
+    return int(load_library().bdlm_cache_pages_workspace_bytes(n_pages, n_seqs))
+
+
+_NULL = nullcontext()
+
+
+class _On:
+    """The device and stream of a call: launches go to the cache's device, and
+    what the call allocates belongs to the stream that uses it."""
+
+    __slots__ = ("handle", "device", "stream")
+
+    def __init__(self, cache, stream):
+        self.device = _NULL if cache.device.index == torch.cuda.current_device() else torch.cuda.device(cache.device)
+        if stream is None:
+            self.stream = _NULL
+            self.handle = torch.cuda.current_stream(cache.device).cuda_stream
+        else:
+            if not hasattr(stream, "cuda_stream"):
+                stream = torch.cuda.ExternalStream(int(stream), device=cache.device)
+            elif stream.device != cache.device:
+                raise ValueError(f"the stream is on {stream.device}, the cache on {cache.device}")
+            self.stream = torch.cuda.stream(stream)
+            self.handle = stream.cuda_stream
+
+
+def _workspace(cache, workspace, need):
+    if workspace is None:
+        return torch.empty(need, dtype=torch.uint8, device=cache.device)
+    if not workspace.is_cuda or workspace.dtype != torch.uint8 or not workspace.is_contiguous() \
+            or workspace.device != cache.device:
+        raise ValueError("workspace must be a contiguous uint8 CUDA tensor on the cache's device")
+    return workspace
+
+
+def _ints(name, cache, t, n):
+    if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous() \
+            or t.device != cache.device:
+        raise ValueError(f"{name} must be a contiguous int32 tensor of one dimension on the cache's device")
+    if n is not None and t.shape[0] != n:
+        raise ValueError(f"{name} must have {n} entries, got {t.shape[0]}")
+    return t.data_ptr()
+
+
+def _layer(cache, layer):
+    if not 0 <= layer < cache.n_layers:
+        raise ValueError(f"layer {layer} is outside the cache's {cache.n_layers}")
+
+
+def _read(lib, workspace, on, where):
+    _check(lib.bdlm_read_error(workspace.data_ptr(), on.handle), where + " (device)")
+
+
+def bdlm_cache_write(cache: PageCache, k_new, v_new, cu_rows, *, layer: int = 0, workspace=None, stream=None,
+                     check: bool = False) -> None:
+    """Quantise the new key and value rows k_new, v_new [T,Hk,d] (bf16) into
+    the pages: rows cu_rows[s] .. cu_rows[s+1]-1 become the last positions of
+    sequence s, whose lens already counts them."""
+    lib = load_library()
+    _bf16_cuda("k_new", k_new)
+    _bf16_cuda("v_new", v_new)
+    _shape("k_new", k_new, (k_new.shape[0], cache.kv_heads, cache.head_dim))
+    _shape("v_new", v_new, k_new.shape)
+    if k_new.device != cache.device or v_new.device != cache.device:
+        raise ValueError("k_new and v_new must be on the cache's device")
+    cu = _ints("cu_rows", cache, cu_rows, cache.n_seqs + 1)
+    _layer(cache, layer)
+    on = _On(cache, stream)
+    with on.device, on.stream:
+        ws = _workspace(cache, workspace, 256)
+        _check(lib.bdlm_cache_write(cache.c, layer, k_new.data_ptr(), v_new.data_ptr(), k_new.shape[0], cu,
+                                    ws.data_ptr(), ws.numel(), on.handle), "bdlm_cache_write")
+        if check:
+            _read(lib, ws, on, "bdlm_cache_write")
+
+
+def bdlm_cache_attn_fwd(cache: PageCache, q, cu_rows, block: int, *, layer: int = 0, q_pos=None,
+                        softmax_scale: float = 0.0, out=None, lse=None, workspace=None, stream=None,
+                        check: bool = False):
+    """Attention of the rows q [T,H,d] (bf16) over the cache under the
+    block-causal mask; returns (o [T,H,d], lse [H,T] fp32). o is bf16 unless
+    `out` is fp32. With q_pos (int32 [n_seqs], the position of each sequence's
+    first row) the rows need not be in the cache, and the result is a partial
+    one for bdlm_lse_merge. Rows of q behind cu_rows[-1] are left unwritten."""
+    lib = load_library()
+    _bf16_cuda("q", q)
+    if q.dim() != 3 or q.shape[2] != cache.head_dim or q.device != cache.device:
+        raise ValueError(f"q must be [T, H, {cache.head_dim}] on the cache's device")
+    T, H, d = q.shape
+    cu = _ints("cu_rows", cache, cu_rows, cache.n_seqs + 1)
+    pos = None if q_pos is None else _ints("q_pos", cache, q_pos, cache.n_seqs)
+    _layer(cache, layer)
+    need = lib.bdlm_cache_attn_fwd_workspace_bytes(T, H, cache.kv_heads, d, cache.n_seqs)
+    on = _On(cache, stream)
+    with on.device, on.stream:
+        if out is None:
+            out = torch.empty_like(q)
+        elif out.dtype not in (torch.bfloat16, torch.float32) or out.shape != q.shape or out.device != cache.device \
+                or not out.is_contiguous():
+            raise ValueError("out must be a contiguous bf16 or fp32 CUDA tensor shaped like q")
+        if lse is None:
+            lse = torch.empty((H, T), dtype=torch.float32, device=cache.device)
+        elif lse.shape != (H, T) or lse.dtype != torch.float32 or lse.device != cache.device \
+                or not lse.is_contiguous():
+            raise ValueError("lse must be a contiguous fp32 CUDA tensor [H, T]")
+        ws = _workspace(cache, workspace, max(need, 256))
+        st = lib.bdlm_cache_attn_fwd(cache.c, layer, q.data_ptr(), out.data_ptr(), lse.data_ptr(), T, H, block, cu, pos,
+                                     softmax_scale, BDLM_F32 if out.dtype == torch.float32 else BDLM_BF16,
+                                     ws.data_ptr(), ws.numel(), on.handle)
+        _check(st, "bdlm_cache_attn_fwd")
+        if check:
+            _read(lib, ws, on, "bdlm_cache_attn_fwd")
+    return out, lse
+
+
+def _pages_call(cache, name, args, workspace, stream, check, make=None):
+    lib = load_library()
+    on = _On(cache, stream)
+    with on.device, on.stream:
+        ws = _workspace(cache, workspace, max(lib.bdlm_cache_pages_workspace_bytes(cache.n_pages, cache.n_seqs), 256))
+        made = None if make is None else make()
+        if made is not None:
+            args = (made.data_ptr(),)
+        _check(getattr(lib, name)(cache.c, *args, ws.data_ptr(), ws.numel(), on.handle), name)
+        if check:
+            _read(lib, ws, on, name)
+    return made
+
+
+def bdlm_cache_reserve(cache: PageCache, new_lens, *, workspace=None, stream=None, check: bool = False) -> None:
+    """Set cache.lens to new_lens (int32 [n_seqs]) and enter free pages for
+    the positions gained; pages that shorter lengths give up become free."""
+    _pages_call(cache, "bdlm_cache_reserve", (_ints("new_lens", cache, new_lens, cache.n_seqs),), workspace, stream,
+                check)
+
+
+def bdlm_cache_fork(cache: PageCache, parents, children, fork_lens=None, *, workspace=None, stream=None,
+                    check: bool = False) -> None:
+    """Sequence children[i] (empty) becomes a copy of the first fork_lens[i]
+    positions (None: all) of parents[i]: full pages are shared, a partly
+    filled last page is copied, in all layers."""
+    n = parents.shape[0] if isinstance(parents, torch.Tensor) and parents.dim() == 1 else None
+    args = (_ints("parents", cache, parents, n), _ints("children", cache, children, n),
+            None if fork_lens is None else _ints("fork_lens", cache, fork_lens, n), n)
+    _pages_call(cache, "bdlm_cache_fork", args, workspace, stream, check)
+
+
+def bdlm_cache_compact(cache: PageCache, *, workspace=None, stream=None, check: bool = False) -> torch.Tensor:
+    """Move the live pages to the front of the pool; returns their number
+    (int32 [1], on the device). Pages from there on are free afterwards."""
+    return _pages_call(cache, "bdlm_cache_compact", (), workspace, stream, check,
+                       make=lambda: torch.zeros(1, dtype=torch.int32, device=cache.device))

@@ -212,6 +212,11 @@ float pick_scale(float s, int d) { return s > 0.f ? s : 1.0f / std::sqrt((float)
 
 }  // namespace
 
+namespace bdlm {
+int device_sms() { return num_sms(); }
+void set_last_launches(int n) { g_launches = n; }
+}  // namespace bdlm
+
 extern "C" {
 
 size_t bdlm_attn_fwd_workspace_bytes(int64_t L, int32_t heads, int32_t head_dim, int32_t n_docs) {
@@ -531,6 +536,7 @@ const char* bdlm_status_string(int status) {
         case BDLM_ERR_CUDA: return "BDLM_ERR_CUDA";
         case BDLM_ERR_TIMEOUT: return "BDLM_ERR_TIMEOUT";
         case BDLM_ERR_DEVICE_CHECK: return "BDLM_ERR_DEVICE_CHECK";
+        case BDLM_ERR_NO_PAGES: return "BDLM_ERR_NO_PAGES";
         default: return "BDLM_ERR_UNKNOWN";
     }
 }

@@ -1,0 +1,60 @@
+"""Block-by-block answering over a paged 8-bit cache: the order of the
+bdlm_cache_* calls that one model's attention layers need.
+
+    dec = BlockDecoder(cache, block=32)
+    cu = dec.begin(rows)              # rows: int32 [n_seqs], new rows of every sequence (0: takes no part)
+    for step in range(steps):         # a prompt takes one step, a block several: its rows are written anew in each
+        for layer in range(n_layers):
+            o, _ = dec.attend(layer, q, k, v)
+    ...                               # keep the rows: begin the next block; or dec.rewind() and begin again
+    dec.branch(parents, children)     # candidates that share what was written so far
+    dec.end(seqs)                     # their pages are free again
+
+All state is the cache's table and lens, on the device: begin, attend, rewind,
+branch and end only launch work on the current stream. begin's first step of a
+whole prompt and a denoising step of one block are the same call: under the
+block-causal mask a prompt's rows see the blocks up to their own, and the rows
+of a block that starts at a block boundary see everything before it and each
+other.
+"""
+from __future__ import annotations
+
+import torch
+
+from . import PageCache, bdlm_cache_attn_fwd, bdlm_cache_fork, bdlm_cache_reserve, bdlm_cache_write
+
+
+class BlockDecoder:
+    def __init__(self, cache: PageCache, block: int, softmax_scale: float = 0.0):
+        if block < 1:
+            raise ValueError("block must be positive")
+        self.cache, self.block, self.softmax_scale = cache, int(block), float(softmax_scale)
+        self.cu_rows = torch.zeros(cache.n_seqs + 1, dtype=torch.int32, device=cache.device)
+        self._kept = cache.lens.clone()
+
+    def begin(self, rows: torch.Tensor, *, check: bool = False) -> torch.Tensor:
+        """Make room for `rows` new rows of every sequence behind what it
+        holds; returns their offsets (int32 [n_seqs + 1]). check=True raises
+        if the cache has no room."""
+        self._kept.copy_(self.cache.lens)
+        torch.cumsum(rows, 0, dtype=torch.int32, out=self.cu_rows[1:])
+        bdlm_cache_reserve(self.cache, self._kept + rows, check=check)
+        return self.cu_rows
+
+    def attend(self, layer: int, q, k, v, *, out=None, lse=None):
+        """Write the rows' keys and values and attend; (o, lse)."""
+        bdlm_cache_write(self.cache, k, v, self.cu_rows, layer=layer)
+        return bdlm_cache_attn_fwd(self.cache, q, self.cu_rows, self.block, layer=layer,
+                                   softmax_scale=self.softmax_scale, out=out, lse=lse)
+
+    def rewind(self) -> None:
+        """Drop the rows of the last begin."""
+        self.cache.lens.copy_(self._kept)
+
+    def branch(self, parents: torch.Tensor, children: torch.Tensor, *, check: bool = False) -> None:
+        """children[i] (empty) continue what parents[i] hold."""
+        bdlm_cache_fork(self.cache, parents, children, check=check)
+
+    def end(self, seqs: torch.Tensor) -> None:
+        """Empty the sequences; pages that no other one names are free."""
+        self.cache.lens[seqs.long()] = 0

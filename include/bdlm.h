@@ -63,7 +63,8 @@ enum bdlm_status {
     BDLM_ERR_WORKSPACE = 3,    /* workspace missing or smaller than required      */
     BDLM_ERR_CUDA = 4,         /* a CUDA runtime/driver call failed               */
     BDLM_ERR_TIMEOUT = 5,      /* device: a bounded wait ran out                  */
-    BDLM_ERR_DEVICE_CHECK = 6  /* device: cu_seqlens or block list is malformed   */
+    BDLM_ERR_DEVICE_CHECK = 6, /* device: cu_seqlens or block list is malformed   */
+    BDLM_ERR_NO_PAGES = 7      /* device: the cache has too few free pages        */
 };
 
 enum bdlm_dtype { BDLM_BF16 = 0, BDLM_F32 = 1 };
@@ -337,8 +338,155 @@ BDLM_API int bdlm_lse_merge(const void* const* partials, const float* const* lse
                    int32_t partial_dtype, int64_t rows, int32_t heads, int32_t head_dim,
                    void* o, float* lse, bdlm_stream_t stream);
 
+/* ------------------------------------------------------------------------
+ * Paged 8-bit cache: the answering side of a block diffusion model.
+ *
+ * A model that answers block by block keeps the keys and values of its
+ * committed (clean) blocks and lets the rows of the block in work read them:
+ * a row of block b sees the keys of blocks <= b that the cache holds, the
+ * same block-causal mask as the clean half of training (with B = 1 causal
+ * attention; the rows of one block, written behind the committed ones, see
+ * them all and each other). The calls below hold such a cache, fill it, read
+ * it and manage its pages. (The pages this library follows describe training
+ * only; these calls have no counterpart there.)
+ *
+ * Layout
+ *   k, v             e4m3 [n_layers, n_pages, Hk, page, d], 16-byte aligned
+ *   k_scale, v_scale fp32 [n_layers, n_pages, Hk]: one positive, finite scale
+ *                    per page and kv head; a key is k_scale * code
+ *   table            int32 [n_seqs, max_pages]: the pages of each sequence in
+ *                    order; position p of sequence s is row p % page of page
+ *                    table[s][p / page]
+ *   lens             int32 [n_seqs]: positions that sequence s holds
+ * page is 16, 32, 64 or 128; d is 64 or 128. All are device buffers of the
+ * caller. Entries of a table row beyond ceil(lens / page) are not read.
+ * A page is live while one of the first ceil(lens / page) entries of some
+ * sequence names it, and free otherwise: to end a sequence, set its length
+ * to 0. Several sequences may share pages that lie wholly below the length at
+ * which they were forked.
+ *
+ * Rows of a call: `cu_rows` is a DEVICE int32 [n_seqs + 1] of row offsets;
+ * rows cu_rows[s] .. cu_rows[s + 1] - 1 (none, for sequences that take no part)
+ * belong to sequence s. cu_rows[0] is 0, and cu_rows[n_seqs] may be less than
+ * total_rows: rows behind it are neither read nor written.
+ *
+ * Problems found on the device are written to the error word of the
+ * workspace (bdlm_read_error); each call says what it leaves undone then.
+ * ------------------------------------------------------------------------ */
+typedef struct {
+    void* k;                 /* e4m3 [n_layers, n_pages, Hk, page, d]             */
+    void* v;
+    float* k_scale;          /* fp32 [n_layers, n_pages, Hk]                      */
+    float* v_scale;
+    int32_t* table;          /* int32 [n_seqs, max_pages]                         */
+    int32_t* lens;           /* int32 [n_seqs]                                    */
+    int32_t n_layers, n_pages, page, kv_heads, head_dim, n_seqs, max_pages;
+    int32_t reserved;        /* must be 0                                         */
+} bdlm_cache;
+
+/* Workspace (bytes, 256-byte aligned) of bdlm_cache_write (its header alone). */
+BDLM_API size_t bdlm_cache_write_workspace_bytes(void);
+
+/*
+ * bdlm_cache_write - quantise new key and value rows into the pages.
+ *
+ *   k_new, v_new  bf16 [total_rows, Hk, d]. The r rows of sequence s become
+ *                 its positions [lens[s] - r, lens[s]): the lengths are set
+ *                 (bdlm_cache_reserve) before the write, and writing the same
+ *                 positions again replaces them (a block that is denoised in
+ *                 several steps).
+ *   layer         0 <= layer < n_layers.
+ * Every page that receives rows gets a new scale for each kv head, the
+ * smallest power of two s >= 2^-126 with |x| <= 448 s for all finite x among
+ * the page's new rows and the rows before them that it keeps (1 if they are
+ * all 0). New rows are stored as x / s rounded to nearest, ties to even;
+ * kept rows are expressed in the new scale (exactly, unless the scale grows
+ * and a value falls below the smallest normal 2^-6 s). Values that are not
+ * finite are stored as NaN. Rows of a page from lens[s] on are left as they
+ * were. A page that is written must belong to one sequence only.
+ * A sequence with malformed offsets, length or pages is skipped
+ * (BDLM_ERR_DEVICE_CHECK); the others are written.
+ */
+BDLM_API int bdlm_cache_write(const bdlm_cache* cache, int32_t layer, const void* k_new, const void* v_new,
+                  int64_t total_rows, const int32_t* cu_rows, void* workspace, size_t workspace_bytes,
+                  bdlm_stream_t stream);
+
+/* Workspace (bytes, 256-byte aligned) of bdlm_cache_attn_fwd; 0 for sizes the
+ * library does not support. */
+BDLM_API size_t bdlm_cache_attn_fwd_workspace_bytes(int64_t total_rows, int32_t heads, int32_t kv_heads,
+                  int32_t head_dim, int32_t n_seqs);
+
+/*
+ * bdlm_cache_attn_fwd - attention of new rows over the cache:
+ *   o = softmax(scale * q k^T under the mask) v, lse per row,
+ * with k = k_scale * code, v = v_scale * code.
+ *
+ *   q      bf16 [total_rows, H, d]; query head h reads kv head h / (H / Hk).
+ *   o      o_dtype (BDLM_BF16 or BDLM_F32) [total_rows, H, d]
+ *   lse    fp32 [H, total_rows]
+ *   block  B >= 1. Row i of sequence s, at position p, sees the keys at
+ *          positions j < min(lens[s], (p / B + 1) B).
+ *   q_pos  NULL: the r rows of a sequence are its last ones, p = lens[s] - r +
+ *          i (they were written to the cache before). Else a DEVICE int32
+ *          [n_seqs], p = q_pos[s] + i >= 0: the cache may hold only other keys
+ *          of the sequence (its committed blocks, or one shard of them), and
+ *          the result is a partial one for bdlm_lse_merge.
+ * A row that sees no key gets o = 0, lse = -inf. What a masked key or value
+ * holds (NaN among it) reaches no row that does not see it.
+ * Malformed offsets or lengths (BDLM_ERR_DEVICE_CHECK) leave o and lse
+ * unwritten; a table entry outside [0, n_pages) turns the rows of its
+ * sequence that see it into NaN.
+ */
+BDLM_API int bdlm_cache_attn_fwd(const bdlm_cache* cache, int32_t layer, const void* q, void* o, float* lse,
+                  int64_t total_rows, int32_t heads, int32_t block, const int32_t* cu_rows, const int32_t* q_pos,
+                  float softmax_scale, int32_t o_dtype, void* workspace, size_t workspace_bytes,
+                  bdlm_stream_t stream);
+
+/* Workspace (bytes, 256-byte aligned) of bdlm_cache_reserve, _fork and
+ * _compact; 0 for sizes the library does not support. */
+BDLM_API size_t bdlm_cache_pages_workspace_bytes(int32_t n_pages, int32_t n_seqs);
+
+/*
+ * The page calls below serve all layers at once. They read and write table
+ * and lens on the device, in stream order. On an error (malformed lengths or
+ * entries: BDLM_ERR_DEVICE_CHECK; too few free pages: BDLM_ERR_NO_PAGES) they
+ * change nothing. Free pages are taken lowest number first.
+ *
+ * bdlm_cache_reserve - set every length to new_lens[s] (DEVICE int32
+ *   [n_seqs]) and enter free pages, sequences in order, for the positions that
+ *   are gained. Pages that a shorter length gives up are free for the others
+ *   of the same call. A sequence may not grow inside a page that another one
+ *   names too (BDLM_ERR_DEVICE_CHECK; fork it at that length instead).
+ */
+BDLM_API int bdlm_cache_reserve(const bdlm_cache* cache, const int32_t* new_lens, void* workspace,
+                  size_t workspace_bytes, bdlm_stream_t stream);
+
+/*
+ * bdlm_cache_fork - sequence children[i] becomes a copy of the first
+ *   fork_lens[i] positions (NULL: all) of sequence parents[i], i < n. It shares
+ *   the pages that lie wholly below that length; of a last, partly filled page
+ *   it gets a copy of its own (the rows below the length, and the scales) in a
+ *   free page, in the order of i. The children are distinct and empty (length
+ *   0) before the call, and none of them is named as a parent; a parent may be
+ *   named several times.
+ *   parents, children, fork_lens: DEVICE int32 [n].
+ */
+BDLM_API int bdlm_cache_fork(const bdlm_cache* cache, const int32_t* parents, const int32_t* children,
+                  const int32_t* fork_lens, int32_t n, void* workspace, size_t workspace_bytes,
+                  bdlm_stream_t stream);
+
+/*
+ * bdlm_cache_compact - move the live pages with numbers >= n_live (the count
+ *   of live pages) into the free ones below, both in ascending order, and
+ *   rewrite the table; afterwards pages n_live .. n_pages - 1 are free.
+ *   n_live: NULL, or a DEVICE int32 that receives the count.
+ */
+BDLM_API int bdlm_cache_compact(const bdlm_cache* cache, int32_t* n_live, void* workspace, size_t workspace_bytes,
+                  bdlm_stream_t stream);
+
 /* Synchronises `stream`, then returns the device error word of the last call
- * that used `workspace` (BDLM_OK, BDLM_ERR_TIMEOUT or BDLM_ERR_DEVICE_CHECK),
+ * that used `workspace` (BDLM_OK, BDLM_ERR_TIMEOUT, BDLM_ERR_DEVICE_CHECK or
+ * BDLM_ERR_NO_PAGES),
  * or BDLM_ERR_CUDA if the stream reports a CUDA error. workspace == NULL
  * reads the fixed scratch of bdlm_attn_fwd_noalloc on the current device. */
 BDLM_API int bdlm_read_error(const void* workspace, bdlm_stream_t stream);
