@@ -1,129 +1,112 @@
-// cache_attn.cu - attention of new rows over the paged 8-bit cache.
+// cache_attn.cu - launches the attention over the paged cache and joins its
+// partial results (cache_attn.cuh says how the work is cut).
 //
-// One CTA per (row, query head): the keys that the row sees pass in chunks of
-// 128, one key per thread for the scores, one column per thread for the
-// weighted sum of the values, with the running maximum and sum of an online
-// softmax in fp32.
-#include "cache.cuh"
+// The merge has one CTA per boundary between two shares. The CTAs whose
+// boundaries fall into one unit take equal runs of its rows, read the rows of
+// all its partials (a warp's 32 rows are 512 consecutive bytes of every float4
+// column) and write o and lse. It is launched with programmatic dependence:
+// its CTAs come up as the attention's leave, and wait for its memory.
+#include "cache_attn.cuh"
 
 namespace bdlm {
 namespace {
 
-constexpr int kThreads = 128;
+using namespace cattn;
 
-__global__ void __launch_bounds__(256) check_kernel(const CacheAttnArgs a) {
-    __shared__ int s_bad;
-    if (threadIdx.x == 0) s_bad = 0x7fffffff;
-    __syncthreads();
-    for (int s = threadIdx.x; s < a.c.n_seqs; s += 256)
-        if (!seq_rows(a.c, a.cu_rows, a.q_pos, a.total_rows, s).ok) atomicMin(&s_bad, s);
-    __syncthreads();
-    if (threadIdx.x == 0) {
-        a.hdr->error = s_bad == 0x7fffffff ? DEV_OK : DEV_CHECK;
-        a.hdr->info = s_bad == 0x7fffffff ? 0 : s_bad;
-        a.hdr->counter = s_bad != 0x7fffffff;  // nothing is written
-    }
-}
+constexpr int kMergeThreads = 256;
 
-__device__ __forceinline__ float code_value(uint8_t c) {
-    return __half2float(__half(__nv_cvt_fp8_to_halfraw(c, __NV_E4M3)));
-}
-
-__device__ float block_max(float x, float* buf) {
-    for (int o = 16; o; o >>= 1) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
-    if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = x;
-    __syncthreads();
-    x = fmaxf(fmaxf(buf[0], buf[1]), fmaxf(buf[2], buf[3]));
-    __syncthreads();
-    return x;
-}
-__device__ float block_sum(float x, float* buf) {
-    for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
-    if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = x;
-    __syncthreads();
-    x = buf[0] + buf[1] + (buf[2] + buf[3]);
-    __syncthreads();
-    return x;
-}
-
-__global__ void __launch_bounds__(kThreads) simple_kernel(const CacheAttnArgs a) {
-    __shared__ float s_q[128], s_p[kThreads], buf[4];
-    __shared__ int s_bad;
-    const CacheView& c = a.c;
-    if (a.hdr->counter) return;
-    const int row = blockIdx.x, h = blockIdx.y, kh = h / a.G, tid = threadIdx.x, D = c.D;
-    if (tid == 0) s_bad = 0;
-    if (row >= __ldg(a.cu_rows + c.n_seqs)) return;
-    int lo = 0, hi = c.n_seqs;  // the last sequence with cu_rows[s] <= row
-    while (hi - lo > 1) {
-        const int mid = (lo + hi) >> 1;
-        if (__ldg(a.cu_rows + mid) <= row) lo = mid; else hi = mid;
-    }
-    const SeqRows r = seq_rows(c, a.cu_rows, a.q_pos, a.total_rows, lo);
-    const int end = key_end(r.len, a.block, r.pos0 + row - r.row0);
-    const int* pages = c.table + (long long)lo * c.max_pages;
-    if (tid < D) s_q[tid] = __bfloat162float(a.q[((long long)row * a.H + h) * D + tid]);
-    __syncthreads();
-    float m = -INFINITY, l = 0.f, acc = 0.f;
-    for (int k0 = 0; k0 < end; k0 += kThreads) {
-        float x = -INFINITY;
-        const int j = k0 + tid;
-        if (j < end) {
-            const int id = __ldg(pages + (j >> c.page_shift));
-            if (id < 0 || id >= c.n_pages) {
-                s_bad = 1;
-            } else {
-                const long long unit = (long long)id * c.Hk + kh;
-                const uint4* k = reinterpret_cast<const uint4*>(c.k + (unit * c.page + (j & (c.page - 1))) * D);
-                float dot = 0.f;
-                for (int e = 0; e < D / 16; ++e) {
-                    const uint4 u = __ldg(k + e);
-                    const uint32_t w[4] = {u.x, u.y, u.z, u.w};
-                    for (int b = 0; b < 16; ++b)
-                        dot = fmaf(s_q[16 * e + b], code_value((uint8_t)(w[b >> 2] >> (8 * (b & 3)))), dot);
-                }
-                x = dot * __ldg(c.k_scale + unit) * a.scale_log2;
+template <int D>
+__global__ void __launch_bounds__(kMergeThreads) cache_merge_kernel(const CacheAttnArgs a) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    const ShareRec* recs = share_recs(a.scratch);
+    const int c = blockIdx.x + 1;
+    if (blockIdx.x == 0) {  // the shares' errors
+        const int n = gridDim.x + 1;
+        int err = 0, info = 0;
+        for (int i = threadIdx.x; i < n; i += kMergeThreads)
+            if (recs[i].error) {
+                err = recs[i].error;
+                info = recs[i].info;
             }
-        }
-        const float big = block_max(x, buf);
-        const bool nan = __syncthreads_or(x != x);
-        const float m_new = nan ? NAN : fmaxf(m, big);
-        const float p = j < end ? exp2f(x - m_new) : 0.f;
-        const float fade = m == -INFINITY ? 0.f : exp2f(m - m_new);
-        s_p[tid] = p;
-        l = l * fade + block_sum(p, buf);
-        acc *= fade;
-        m = m_new;
-        if (tid < D)
-            for (int e = 0; e < kThreads && k0 + e < end; ++e) {
-                const int id = __ldg(pages + ((k0 + e) >> c.page_shift));
-                if (id < 0 || id >= c.n_pages) continue;
-                const long long unit = (long long)id * c.Hk + kh;
-                const uint8_t v = __ldg(c.v + (unit * c.page + ((k0 + e) & (c.page - 1))) * D + tid);
-                acc = fmaf(s_p[e] * __ldg(c.v_scale + unit), code_value(v), acc);
-            }
+        __shared__ int s_err[2];
+        if (threadIdx.x == 0) s_err[0] = s_err[1] = 0;
         __syncthreads();
+        if (err && atomicCAS(&s_err[0], 0, err) == 0) s_err[1] = info;
+        __syncthreads();
+        if (threadIdx.x == 0) {
+            a.hdr->error = s_err[0];
+            a.hdr->info = s_err[1];
+        }
     }
-    float out = end > 0 ? acc / l : 0.f, lse = end > 0 ? (m + log2f(l)) * 0.69314718055994531f : -INFINITY;
-    if (s_bad) out = lse = NAN;
-    if (tid < D) {
-        const long long at = ((long long)row * a.H + h) * D + tid;
-        if (a.o_f32) a.o_f32[at] = out; else a.o[at] = __float2bfloat16(out);
-    }
-    if (tid == 0) {
-        a.lse[(long long)h * a.total_rows + row] = lse;
-        if (s_bad) set_error(a.hdr, DEV_CHECK, -1);
+    const ShareRec r = recs[c];
+    if (c >= r.C || r.kt0 == 0) return;  // no share begins here, or it begins with its unit
+    const long long g0 = share_begin(r.W, r.C, c) - r.kt0;
+    int c0 = c, c1 = c;  // boundaries inside the unit: shares c0 - 1 .. c1 hold its partials
+    while (c0 > 1 && share_begin(r.W, r.C, c0 - 1) > g0) --c0;
+    while (c1 + 1 < r.C && share_begin(r.W, r.C, c1 + 1) < g0 + r.cost) ++c1;
+    const int rows = imin(kUnitRows, r.rows * a.G - r.m0), parts = c1 - c0 + 2;
+    const int lo = rows * (c - c0) / (c1 - c0 + 1), hi = rows * (c - c0 + 1) / (c1 - c0 + 1);
+    const int R = slot_rows(a.total_rows, a.G);
+    auto slot = [&](int p) { return slot_at(a.scratch, p == 0 ? 2 * (c0 - 1) + 1 : 2 * (c0 - 1 + p), R, D); };
+    // item: one float4 of columns of one row; consecutive threads take consecutive rows
+    const int n = hi - lo;
+    for (int it = threadIdx.x; it < n * (D / 4); it += kMergeThreads) {
+        const int i = lo + it % n, q = it / n, m = r.m0 + i;
+        float mx = -INFINITY;
+        bool nan = false;
+        for (int p = 0; p < parts; ++p) {
+            const float x = __ldcg(slot(p) + (long long)R * D + i);
+            mx = fmaxf(mx, x);
+            nan = nan || x != x;
+        }
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        float z = 0.f;
+        for (int p = 0; p < parts; ++p) {
+            const float* s = slot(p);
+            const float x = __ldcg(s + (long long)R * D + i);
+            if (x == -INFINITY) continue;
+            const float w = exp2f(x - mx);
+            const float4 v = __ldcg(reinterpret_cast<const float4*>(s) + (long long)q * R + i);
+            z += w;
+            o.x = fmaf(w, v.x, o.x);
+            o.y = fmaf(w, v.y, o.y);
+            o.z = fmaf(w, v.z, o.z);
+            o.w = fmaf(w, v.w, o.w);
+        }
+        const float inv = nan ? NAN : z > 0.f ? 1.f / z : 0.f;
+        const int row = r.row0 + m / a.G, h = r.head * a.G + m % a.G;
+        const long long at = ((long long)row * a.H + h) * D + 4 * q;
+        if (a.o_f32) {
+            *reinterpret_cast<float4*>(a.o_f32 + at) = make_float4(o.x * inv, o.y * inv, o.z * inv, o.w * inv);
+        } else {
+            const __nv_bfloat162 b0 = __floats2bfloat162_rn(o.x * inv, o.y * inv), b1 = __floats2bfloat162_rn(o.z * inv, o.w * inv);
+            *reinterpret_cast<uint2*>(a.o + at) = make_uint2(*reinterpret_cast<const uint32_t*>(&b0), *reinterpret_cast<const uint32_t*>(&b1));
+        }
+        if (q == 0) a.lse[(long long)h * a.total_rows + row] = nan ? NAN : z > 0.f ? (mx + log2f(z)) * 0.69314718055994531f : -INFINITY;
     }
 }
 
 }  // namespace
 
-size_t cache_attn_scratch_bytes(long long, int, int, int, int) { return 256; }
+size_t cache_attn_scratch_bytes(long long total_rows, int H, int Hk, int D, int) {
+    const int rows = slot_rows(total_rows, H / Hk);
+    return sizeof(ShareRec) * kMaxCtas + sizeof(float) * 2 * kMaxCtas * (size_t)slot_floats(rows, D);
+}
 
-cudaError_t launch_cache_attn(const CacheAttnArgs& a, int, cudaStream_t st, int* launches) {
-    check_kernel<<<1, 256, 0, st>>>(a);
-    simple_kernel<<<dim3(a.total_rows, a.H), kThreads, 0, st>>>(a);
-    const cudaError_t e = cudaGetLastError();
+cudaError_t launch_cache_attn(const CacheAttnArgs& a, int num_sms, cudaStream_t st, int* launches) {
+    const int ctas = num_sms < kMaxCtas ? num_sms : kMaxCtas;
+    cudaError_t e = a.c.D == 128 ? launch_cache_attn_d128(a, ctas, st) : launch_cache_attn_d64(a, ctas, st);
+    if (e != cudaSuccess) return e;
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)(ctas > 1 ? ctas - 1 : 1));
+    cfg.blockDim = dim3(kMergeThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    e = a.c.D == 128 ? cudaLaunchKernelEx(&cfg, cache_merge_kernel<128>, a) : cudaLaunchKernelEx(&cfg, cache_merge_kernel<64>, a);
     if (e == cudaSuccess) *launches += 2;
     return e;
 }

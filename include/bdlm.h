@@ -435,7 +435,7 @@ BDLM_API size_t bdlm_cache_attn_fwd_workspace_bytes(int64_t total_rows, int32_t 
  * holds (NaN among it) reaches no row that does not see it.
  * Malformed offsets or lengths (BDLM_ERR_DEVICE_CHECK) leave o and lse
  * unwritten; a table entry outside [0, n_pages) turns the rows of its
- * sequence that see it into NaN.
+ * sequence that see it, and possibly others of that sequence, into NaN.
  */
 BDLM_API int bdlm_cache_attn_fwd(const bdlm_cache* cache, int32_t layer, const void* q, void* o, float* lse,
                   int64_t total_rows, int32_t heads, int32_t block, const int32_t* cu_rows, const int32_t* q_pos,
