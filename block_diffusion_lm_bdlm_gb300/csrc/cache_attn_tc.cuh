@@ -21,19 +21,21 @@
 // for up to 128 flat rows, so these calls are bound by memory, and calls with
 // 256 and more flat rows by the tensor pipe.
 //
-// Roles (384 threads, one CTA per SM, each role walks the CTA's share alone):
+// Roles (512 threads, one CTA per SM, each role walks the CTA's share alone):
 //   warps 0-3, 4-7  softmax groups 0 and 1; one TMEM lane = one flat row. They
 //                   also split Q into its two terms, and write the results
 //   warp 8          page table, scales and TMA loads of K and V pages (3 stages)
 //   warp 9          issues the MMAs (one thread), owns TMEM
-//   warps 10-11     widen V from e4m3 to fp16 (2 stages), zero the rows behind
+//   warps 10-11     spare
+//   warps 12-15     widen V from e4m3 to fp16 (2 stages), zero the rows behind
 //                   the last key and take out masked NaN
-// A unit of up to 128 flat rows is one MMA tile: the two groups take its key
-// tiles in turn, each with its own sums, and join them at the end, so that one
-// group's softmax runs under the other's MMAs. A larger unit is two MMA tiles,
-// one for each group, over the same keys.
+// A unit of up to 128 flat rows is one MMA tile: group 0 takes the first 64
+// keys of every key tile, group 1 the others, each with sums and an O of its
+// own that are joined at the end. Two S buffers take turns, so that a tile's
+// softmax (64 keys per thread) runs under the MMAs of its neighbours. A larger
+// unit is two MMA tiles, one for each group, over the same keys.
 // TMEM (512 columns): S0 | S1 | O0 | O1; p' overwrites S as fp16.
-// MMAs of one thread run in issue order, so the next S of a group is issued
+// MMAs of one thread run in issue order, so the next S of a buffer is issued
 // right behind the PV that reads the p' it overwrites.
 // Every mbarrier wait is bounded (2 s); on a timeout the roles drain and the
 // share's record carries BDLM_ERR_TIMEOUT.
@@ -48,21 +50,26 @@
 namespace bdlm {
 namespace cattn {
 
-constexpr int kThreads = 384;
-constexpr int kRegsSoftmax = 224;
-constexpr int kRegsOther = 56;
+constexpr int kThreads = 512;
+// 8 softmax warps and 8 others at 128 registers each, redistributed
+constexpr int kRegsSoftmax = 176;
+constexpr int kRegsOther = 80;
+static_assert(8 * kRegsSoftmax + 8 * kRegsOther <= 16 * 128, "registers");
 constexpr int kTmemCols = 512;
 constexpr int kStages = 3;
-constexpr int kScaleSlots = 8;
+constexpr int kScaleSlots = 6;
 constexpr uint64_t kTimeoutNs = 2000000000ull;
 
-// barriers
+// Barriers. Tiles are numbered through the CTA's share; t is a tile's number.
 enum : int {
-    B_KFULL = 0, B_KEMPTY = 3, B_VFULL = 6, B_VEMPTY = 9,  // rings of 3
-    B_WFULL = 12, B_WEMPTY = 14,                           // ring of 2
-    B_S = 16, B_P = 18, B_O = 20, B_Q = 22,
-    B_SC = 23,                                             // ring of 8: scales written
-    B_COUNT = 31
+    B_KFULL = 0, B_VFULL = 3, B_VEMPTY = 6,  // t % 3
+    B_S0 = 9,                                // t % 3: group 0's S of a unit of two MMA tiles
+    B_S1 = 12,                               // t % 3: the tile's last S; it also frees the K stage
+    B_P = 15,                                // 2 (t & 1) + group: p' in TMEM; for group 0 also: V in fp16
+    B_PV = 19,                               // t & 1: the tile's products with V; frees the fp16 stage
+    B_Q = 21,
+    B_SC = 22,                               // t % 6: scales written
+    B_COUNT = 28
 };
 
 template <int D>
@@ -73,12 +80,13 @@ struct Smem {
     static constexpr int kK = 8 * kT8;         // 3 stages
     static constexpr int kV = kK + kStages * kT8;
     static constexpr int kMisc = kV + kStages * kT8;
-    static constexpr int kScale = kMisc;                          // float [8 slots][16]: ks, log2 vs of 16-key groups
+    static constexpr int kScale = kMisc;                          // float [slots][16]: ks, log2 vs of 16-key groups
     static constexpr int kNan = kScale + kScaleSlots * 64;        // int [4][D]: first key whose value is NaN, per column
     static constexpr int kBar = kNan + 4 * D * 4;
     static constexpr int kWords = kBar + B_COUNT * 8;             // tmem, abort, error, info
     static constexpr int kStart = kWords + 16;                    // Start
-    static constexpr int kBytes = kStart + 64;
+    static constexpr int kQExp = kStart + 64;                     // uint8 [256]: exponent of the rows' scale
+    static constexpr int kBytes = kQExp + kUnitRows;
 };
 static_assert(Smem<128>::kBytes <= 232448, "shared memory");
 
@@ -153,12 +161,20 @@ __device__ __forceinline__ uint32_t pack_bf2(float lo, float hi) {
     asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
-__device__ __forceinline__ uint32_t widen2(uint32_t c2) {  // two e4m3 codes -> two fp16
-    const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)(c2 & 0xffffu), __NV_E4M3);
-    return (uint32_t)h.x | (uint32_t)h.y << 16;
+// four e4m3 codes -> four fp16
+__device__ __forceinline__ void widen4(uint32_t c, uint32_t& lo, uint32_t& hi) {
+    asm("{\n\t.reg .b16 a, b;\n\tmov.b32 {a, b}, %2;\n\tcvt.rn.f16x2.e4m3x2 %0, a;\n\tcvt.rn.f16x2.e4m3x2 %1, b;\n\t}"
+        : "=r"(lo), "=r"(hi)
+        : "r"(c));
 }
-__device__ __forceinline__ uint32_t narrow2(float lo, float hi) {
-    return __nv_cvt_float2_to_fp8x2(make_float2(lo, hi), __NV_SATFINITE, __NV_E4M3);
+// four fp32 -> four e4m3 codes (nearest even, saturating)
+__device__ __forceinline__ uint32_t narrow4(float x0, float x1, float x2, float x3) {
+    uint32_t r;
+    asm("{\n\t.reg .b16 a, b;\n\tcvt.rn.satfinite.e4m3x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e4m3x2.f32 b, %4, %3;\n\t"
+        "mov.b32 %0, {a, b};\n\t}"
+        : "=r"(r)
+        : "f"(x0), "f"(x1), "f"(x2), "f"(x3));
+    return r;
 }
 
 // D[tmem] (+)= A[smem] B[smem], e4m3 operands
@@ -198,13 +214,33 @@ __device__ __forceinline__ void tmem_ld4(uint32_t taddr, uint32_t (&r)[4]) {
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
                  : "r"(taddr));
 }
+__device__ __forceinline__ void tmem_ld16(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr));
+}
 __device__ __forceinline__ void sts16(uint32_t addr, uint32_t a, uint32_t b, uint32_t c, uint32_t d) {
     asm volatile("st.shared.v4.b32 [%0], {%1,%2,%3,%4};" ::"r"(addr), "r"(a), "r"(b), "r"(c), "r"(d) : "memory");
+}
+__device__ __forceinline__ void sts8(uint32_t addr, uint32_t a, uint32_t b) {
+    asm volatile("st.shared.v2.b32 [%0], {%1,%2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
 }
 __device__ __forceinline__ void lds16(uint32_t addr, uint32_t (&v)[4]) {
     asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(addr));
 }
 __device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+
+template <int N>
+struct Const {
+    static constexpr int value = N;
+};
+__device__ __forceinline__ bool elect_one() {
+    uint32_t p;
+    asm volatile("{\n\t.reg .pred e;\n\telect.sync _|e, 0xffffffff;\n\tselp.u32 %0, 1, 0, e;\n\t}" : "=r"(p));
+    return p != 0;
+}
 
 struct Ctx {
     uint8_t* smem;
@@ -379,7 +415,7 @@ __device__ __forceinline__ void produce(const Ctx& x, const CacheAttnArgs& a, co
         const float lvs = __log2f(b0.vs);
         for (int i = 0; i < b0.n; ++i, ++t) {
             const uint32_t stage = t % kStages, ph = (t / kStages) & 1, slot = t % kScaleSlots;
-            ok = x.wait(B_KEMPTY, stage, ph ^ 1) && x.wait(B_VEMPTY, stage, ph ^ 1);
+            ok = x.wait(B_S1, stage, ph ^ 1) && x.wait(B_VEMPTY, stage, ph ^ 1);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             const bool mine = (lane >> 3) == i;
@@ -423,10 +459,19 @@ __device__ __forceinline__ void produce(const Ctx& x, const CacheAttnArgs& a, co
 template <int D>
 __device__ __forceinline__ void widen(const Ctx& x, const CacheAttnArgs& a, const Start& st) {
     using L = Smem<D>;
-    constexpr int PER = D / 16;             // 16-byte chunks per key
-    constexpr int ROWS = 32 / PER;          // keys per warp and step
-    const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) - 10;
-    const int c = lane % PER, r0 = lane / PER + warp * ROWS;
+    constexpr int PER = D / 16;                  // 16-byte chunks per key
+    constexpr int ROWS = 4 * (32 / PER);         // keys that the four warps take at a time
+    constexpr int STEPS = kTileKeys / ROWS;
+    const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) - 12;
+    const int c = lane % PER, r0 = lane / PER + warp * (32 / PER);
+    // 16 columns are two 16-byte chunks of the 64-column half they lie in; the lanes of the upper half store theirs in
+    // the other order, so that eight lanes meet eight bank groups. The rows of a thread are ROWS (a multiple of 8)
+    // apart, so its swizzle is the same in every step.
+    const uint32_t src0 = x.sbase + L::kV + swz8<D>(r0, c);
+    const uint32_t row_dst = x.sbase + L::kW + (c >> 2) * 16384 + r0 * 128;
+    const bool swap = c >= 4;
+    const uint32_t d0 = row_dst + ((((2 * c + (swap ? 1 : 0)) & 7) ^ (r0 & 7)) << 4);
+    const uint32_t d1 = row_dst + ((((2 * c + (swap ? 0 : 1)) & 7) ^ (r0 & 7)) << 4);
     Walk w;
     w.begin(a, st);
     Seg g;
@@ -439,215 +484,249 @@ __device__ __forceinline__ void widen(const Ctx& x, const CacheAttnArgs& a, cons
         const int all = key_end(g.len, a.block, g.pos0 + g.m0 / a.G);
         for (int kt = g.kt0; kt < g.kt1; ++kt, ++t) {
             const uint32_t stage = t % kStages, ws = t & 1;
-            bool ok = x.wait(B_VFULL, stage, (t / kStages) & 1) && x.wait(B_WEMPTY, ws, ((t >> 1) & 1) ^ 1);
+            bool ok = x.wait(B_VFULL, stage, (t / kStages) & 1);
+            const uint32_t src = src0 + stage * L::kT8, off = ws * 2 * L::kT8;
+            uint32_t v[STEPS][4];
+#pragma unroll
+            for (int j = 0; j < STEPS; ++j) lds16(src + j * ROWS * D, v[j]);
+            ok = ok && x.wait(B_PV, ws, ((t >> 1) & 1) ^ 1);
             if (!__all_sync(0xffffffffu, ok)) return;
-            const uint32_t src = x.sbase + L::kV + stage * L::kT8, dst = x.sbase + L::kW + ws * 2 * L::kT8;
             const int valid = imin(kTileKeys, g.end - kt * kTileKeys);
-            const bool check = kt * kTileKeys + valid > all;
-            for (int i0 = 0; i0 < kTileKeys; i0 += 8 * ROWS) {
-                uint32_t v[4][4];
+            if (valid < kTileKeys || kt * kTileKeys + valid > all) {
 #pragma unroll
-                for (int j = 0; j < 4; ++j) lds16(src + swz8<D>(i0 + 2 * ROWS * j + r0, c), v[j]);
-#pragma unroll
-                for (int j = 0; j < 4; ++j) {
-                    const int r = i0 + 2 * ROWS * j + r0;
+                for (int j = 0; j < STEPS; ++j) {
+                    const int r = j * ROWS + r0;
                     if (r >= valid) v[j][0] = v[j][1] = v[j][2] = v[j][3] = 0;
-                    if (check) {
-                        uint32_t any = 0;
+                    uint32_t any = 0;
 #pragma unroll
-                        for (int e = 0; e < 4; ++e) any |= ((v[j][e] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
-                        if (any)
-                            for (int e = 0; e < 16; ++e) {
-                                const uint32_t sh = 8 * (e & 3);
-                                // the element's word by selection, so that v stays in registers
-                                const uint32_t word = e < 4 ? v[j][0] : e < 8 ? v[j][1] : e < 12 ? v[j][2] : v[j][3];
-                                if (((word >> sh) & 0x7f) == 0x7f) {
-                                    atomicMin(nan_first + 16 * c + e, kt * kTileKeys + r);
-                                    const uint32_t m = ~(0xffu << sh);
-                                    if (e < 4) v[j][0] &= m; else if (e < 8) v[j][1] &= m;
-                                    else if (e < 12) v[j][2] &= m; else v[j][3] &= m;
-                                }
+                    for (int e = 0; e < 4; ++e) any |= ((v[j][e] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+                    if (any) {
+#pragma unroll
+                        for (int e = 0; e < 16; ++e) {
+                            const uint32_t sh = 8 * (e & 3);
+                            if (((v[j][e >> 2] >> sh) & 0x7f) == 0x7f) {
+                                atomicMin(nan_first + 16 * c + e, kt * kTileKeys + r);
+                                v[j][e >> 2] &= ~(0xffu << sh);
                             }
-                    }
-                    uint32_t h[8];
-#pragma unroll
-                    for (int e = 0; e < 4; ++e) {
-                        h[2 * e] = widen2(v[j][e]);
-                        h[2 * e + 1] = widen2(v[j][e] >> 16);
-                    }
-                    // 16 columns are two 16-byte chunks of the 64-column half they lie in; the lanes of the upper half
-                    // store theirs in the other order, so that eight lanes meet eight bank groups
-                    const uint32_t base = dst + (c >> 2) * 16384 + r * 128;
-                    const uint32_t u = (2 * c) & 7, a0 = base + ((u ^ (r & 7)) << 4), a1 = base + (((u + 1) ^ (r & 7)) << 4);
-                    if (c < 4) {
-                        sts16(a0, h[0], h[1], h[2], h[3]);
-                        sts16(a1, h[4], h[5], h[6], h[7]);
-                    } else {
-                        sts16(a1, h[4], h[5], h[6], h[7]);
-                        sts16(a0, h[0], h[1], h[2], h[3]);
+                        }
                     }
                 }
+            }
+#pragma unroll
+            for (int j = 0; j < STEPS; ++j) {
+                uint32_t h[8];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) widen4(v[j][e], h[2 * e], h[2 * e + 1]);
+                sts16(d0 + off + j * ROWS * 128, swap ? h[4] : h[0], swap ? h[5] : h[1], swap ? h[6] : h[2], swap ? h[7] : h[3]);
+                sts16(d1 + off + j * ROWS * 128, swap ? h[0] : h[4], swap ? h[1] : h[5], swap ? h[2] : h[6], swap ? h[3] : h[7]);
             }
             tc::fence_proxy_async_smem();
             __syncwarp();
             if (lane == 0) {
                 tc::mbar_arrive(x.bar(B_VEMPTY, stage));
-                tc::mbar_arrive(x.bar(B_WFULL, ws));
+                tc::mbar_arrive(x.bar(B_P, 2 * ws));
             }
         }
     }
 }
 
 // ---------------------------------------------------------------------- MMA
+// The whole warp walks the share, so that addresses and descriptors are warp-
+// uniform values; one elected lane issues. The tensor pipe queues little, so
+// what stands between two groups of MMAs is kept short: one wait for a tile's
+// keys, taken before the pipe needs them, one for p' of each group (which
+// counts the fp16 values as well) and one commit for each S and each PV.
 template <int D>
 __device__ __forceinline__ void issue(const Ctx& x, const CacheAttnArgs& a, const Start& st) {
     using L = Smem<D>;
     constexpr uint32_t id_s = idesc_fmt0(128, kTileKeys, 0), id_o = idesc_fmt0(128, D, 1);
-    const uint64_t k8 = sdesc_k8<D>(x.sbase), mn = tc::sdesc_sw128(x.sbase, 16384, 1024);
+    const uint32_t sbase = __shfl_sync(0xffffffffu, x.sbase, 0), tmem = __shfl_sync(0xffffffffu, x.tmem, 0);
+    const uint64_t k8 = sdesc_k8<D>(sbase), mn = tc::sdesc_sw128(sbase, 16384, 1024);
+    const bool leader = elect_one();
+    auto wait = [&](int base, int i, uint32_t parity) { return __all_sync(0xffffffffu, x.wait(base, i, parity)) != 0; };
+    // S of tile t from Q tile qt into S buffer b
+    auto issue_s = [&](uint32_t t, uint32_t qt, uint32_t b, uint32_t bar) {
+        const uint32_t stage = t % kStages;
+        const uint64_t dk = tc::sdesc_add(k8, L::kK + stage * L::kT8);
+        const uint64_t dq = tc::sdesc_add(k8, L::kQ + qt * 2 * L::kT8);
+        const uint32_t to = tmem + 128 * b;
+        if (leader) {
+#pragma unroll
+            for (int k = 0; k < 2 * D / 32; ++k)  // the high terms, then the low ones
+                mma_ss_f8(to, tc::sdesc_add(dq, k * 32 < D ? k * 32 : L::kT8 + k * 32 - D), tc::sdesc_add(dk, k * 32 % D), id_s, k > 0);
+            tc::mma_commit(x.bar(bar, stage));
+        }
+    };
+    // N / 16 steps of p' (from S buffer column p) times the fp16 values from key `key` on, into O buffer o
+    auto issue_pv = [&](uint32_t t, uint32_t p, uint32_t o, int key, auto steps, bool fresh) {
+        const uint64_t dv = tc::sdesc_add(mn, L::kW + (t & 1) * 2 * L::kT8 + key * 128);
+        const uint32_t to = tmem + 256 + D * o, from = tmem + p;
+        if (leader) {
+#pragma unroll
+            for (int k = 0; k < decltype(steps)::value; ++k)
+                tc::mma_ts(to, from + 8 * k, tc::sdesc_add(dv, 2048 * k), id_o, (k > 0 || !fresh) ? 1u : 0u);
+        }
+    };
     Walk w;
     w.begin(a, st);
     Seg g;
-    uint32_t t_base = 0, seg = 0, n_p[2] = {0, 0};
+    uint32_t t0 = 0, seg = 0;
     while (w.next(a, &g)) {
-        const int nt = g.tiles(), jobs = g.two ? 2 * nt : nt;
+        const int nt = __shfl_sync(0xffffffffu, g.tiles(), 0);
         if (nt == 0) continue;
-        if (!x.wait(B_Q, 0, seg & 1)) return;
+        const bool two = __shfl_sync(0xffffffffu, (int)g.two, 0) != 0;
+        if (!wait(B_Q, 0, seg & 1)) return;
         ++seg;
         tc::tc_fence_after();
-        // S of job j: group j & 1; its tile is j (one MMA tile) or j / 2 (two)
-        auto issue_s = [&](int j) -> bool {
-            const uint32_t t = t_base + (g.two ? j >> 1 : j), stage = t % kStages;
-            const int i = j & 1;
-            if (!g.two || i == 0) {
-                if (!x.wait(B_KFULL, stage, (t / kStages) & 1)) return false;
-                tc::tc_fence_after();
-            }
-            const uint64_t dk = tc::sdesc_add(k8, L::kK + stage * L::kT8);
-            const uint64_t dq = tc::sdesc_add(k8, L::kQ + (g.two ? i * 2 * L::kT8 : 0));
+        if (two) {
+            if (!wait(B_KFULL, t0 % kStages, (t0 / kStages) & 1)) return;
+            issue_s(t0, 0, 0, B_S0);
+            issue_s(t0, 1, 1, B_S1);
+            for (int j = 0; j < nt; ++j) {
+                const uint32_t t = t0 + j, b = t & 1, ph = (t >> 1) & 1;
+                const bool more = j + 1 < nt;
+                if (more && !wait(B_KFULL, (t + 1) % kStages, ((t + 1) / kStages) & 1)) return;
 #pragma unroll
-            for (int k = 0; k < 2 * D / 32; ++k)  // the high terms, then the low ones
-                mma_ss_f8(x.tmem + 128 * i, tc::sdesc_add(dq, k * 32 < D ? k * 32 : L::kT8 + k * 32 - D),
-                          tc::sdesc_add(dk, k * 32 % D), id_s, k > 0);
-            tc::mma_commit(x.bar(B_S, i));
-            if (!g.two || i == 1) tc::mma_commit(x.bar(B_KEMPTY, stage));
-            return true;
-        };
-        if (!issue_s(0)) return;
-        if (jobs > 1 && !issue_s(1)) return;
-        for (int j = 0; j < jobs; ++j) {
-            const int i = j & 1;
-            const uint32_t t = t_base + (g.two ? j >> 1 : j), ws = t & 1;
-            if (!g.two || i == 0) {
-                if (!x.wait(B_WFULL, ws, (t >> 1) & 1)) return;
+                for (uint32_t i = 0; i < 2; ++i) {
+                    if (!wait(B_P, 2 * b + i, ph)) return;
+                    tc::tc_fence_after();
+                    issue_pv(t, 128 * i, i, 0, Const<kTileKeys / 16>{}, j == 0);
+                    if (i == 1 && leader) tc::mma_commit(x.bar(B_PV, b));
+                    if (more) issue_s(t + 1, i, i, i == 0 ? B_S0 : B_S1);
+                }
             }
-            const uint32_t ph = n_p[i] & 1;
-            ++n_p[i];
-            if (!x.wait(B_P, i, ph)) return;
-            tc::tc_fence_after();
-            const uint64_t dv = tc::sdesc_add(mn, L::kW + ws * 2 * L::kT8);
+        } else {
 #pragma unroll
-            for (int k = 0; k < kTileKeys / 16; ++k)
-                tc::mma_ts(x.tmem + 256 + D * i, x.tmem + 128 * i + 8 * k, tc::sdesc_add(dv, 2048 * k), id_o,
-                           (j > 1 || k > 0) ? 1u : 0u);
-            if (!g.two || i == 1) tc::mma_commit(x.bar(B_WEMPTY, ws));
-            if (j + 2 >= jobs) tc::mma_commit(x.bar(B_O, i));  // the group's last; waited for, so it comes last
-            if (j + 2 < jobs && !issue_s(j + 2)) return;
+            for (int j = 0; j < 2; ++j)
+                if (j < nt) {
+                    const uint32_t t = t0 + j;
+                    if (!wait(B_KFULL, t % kStages, (t / kStages) & 1)) return;
+                    issue_s(t, 0, t & 1, B_S1);
+                }
+            for (int j = 0; j < nt; ++j) {
+                const uint32_t t = t0 + j, b = t & 1, ph = (t >> 1) & 1;
+                const bool more = j + 2 < nt;
+                if (more && !wait(B_KFULL, (t + 2) % kStages, ((t + 2) / kStages) & 1)) return;
+#pragma unroll
+                for (uint32_t h = 0; h < 2; ++h) {  // each group's 64 keys into its own O
+                    if (!wait(B_P, 2 * b + h, ph)) return;
+                    tc::tc_fence_after();
+                    issue_pv(t, 128 * b + 64 * h, h, 64 * h, Const<kTileKeys / 32>{}, j == 0);
+                }
+                if (leader) tc::mma_commit(x.bar(B_PV, b));
+                if (more) issue_s(t + 2, 0, b, B_S1);
+            }
         }
-        t_base += nt;
+        t0 += nt;
     }
 }
 
 // ------------------------------------------------------------------ softmax
-// Splits flat row m0 + row of the unit into its two e4m3 terms; returns the factor that turns the tensor core's q . k8
-// into base-2 scores (NaN for a row that is not finite, so that the row becomes NaN and no other).
+// Splits the unit's rows into their two e4m3 terms and notes the exponents of their power-of-two scales (255 for a row
+// that is not finite). Eight values per thread, so that a row is read and reduced by D / 8 lanes; rows behind the last
+// one of a warp's 32 are zeros.
 template <int D>
-__device__ __forceinline__ float split_q(const Ctx& x, const CacheAttnArgs& a, const Seg& g, int m, int row, uint32_t dst,
-                                         bool hi, bool lo) {
+__device__ __forceinline__ void split_q(const Ctx& x, const CacheAttnArgs& a, const Seg& g) {
     using L = Smem<D>;
-    const __nv_bfloat16* q = a.q + ((long long)(g.row0 + m / a.G) * a.H + g.h * a.G + m % a.G) * D;
-    uint4 v[D / 8];
-    const bool live = m < g.last;
+    constexpr int PER = D / 8, ROWS = 256 / PER, BATCH = 4;
+    const int chunk = threadIdx.x % PER, r0 = threadIdx.x / PER;
+    const int n = g.last - g.m0, padded = (n + 31) & ~31;
+    uint8_t* exps = x.smem + L::kQExp;
+    for (int b = 0; b < padded; b += BATCH * ROWS) {
+        uint4 v[BATCH];
 #pragma unroll
-    for (int i = 0; i < D / 8; ++i) v[i] = live ? __ldg(reinterpret_cast<const uint4*>(q) + i) : make_uint4(0, 0, 0, 0);
-    uint32_t big = 0;
-#pragma unroll
-    for (int i = 0; i < D / 8; ++i) {
-        const uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const uint32_t p = (u[e] << 16) & 0x7fffffffu, r = u[e] & 0x7fff0000u;
-            big = p > big ? p : big;
-            big = r > big ? r : big;
-        }
-    }
-    const float amax = __uint_as_float(big);
-    const float s = is_finite(amax) ? pow2_scale(amax) : 1.f, inv = 1.f / s;
-#pragma unroll
-    for (int c = 0; c < D / 16; ++c) {
-        uint32_t wh[4], wl[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            uint32_t ph[2], pl[2];
-#pragma unroll
-            for (int k = 0; k < 2; ++k) {
-                const uint4 y = v[2 * c + (e >> 1)];
-                const uint32_t u = (e & 1) ? (k ? y.w : y.z) : (k ? y.y : y.x);
-                const float f0 = __uint_as_float(u << 16) * inv, f1 = __uint_as_float(u & 0xffff0000u) * inv;
-                ph[k] = narrow2(f0, f1);
-                const uint32_t back = widen2(ph[k]);
-                const float2 b = __half22float2(*reinterpret_cast<const __half2*>(&back));
-                pl[k] = narrow2(f0 - b.x, f1 - b.y);
+        for (int i = 0; i < BATCH; ++i) {
+            const int r = b + i * ROWS + r0, m = g.m0 + r;
+            v[i] = make_uint4(0, 0, 0, 0);
+            if (r < n) {
+                const int row = m / a.G, head = g.h * a.G + (m - row * a.G);
+                v[i] = __ldg(reinterpret_cast<const uint4*>(a.q + ((long long)(g.row0 + row) * a.H + head) * D) + chunk);
             }
-            wh[e] = ph[0] | ph[1] << 16;
-            wl[e] = pl[0] | pl[1] << 16;
         }
-        if (hi) sts16(dst + swz8<D>(row, c), wh[0], wh[1], wh[2], wh[3]);
-        if (lo) sts16(dst + L::kT8 + swz8<D>(row, c), wl[0], wl[1], wl[2], wl[3]);
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) {
+            const int r = b + i * ROWS + r0;
+            const uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+            uint32_t big = 0;
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const uint32_t p = (u[e] << 16) & 0x7fffffffu, q = u[e] & 0x7fff0000u;
+                big = p > big ? p : big;
+                big = q > big ? q : big;
+            }
+#pragma unroll
+            for (int o = PER / 2; o; o >>= 1) {
+                const uint32_t y = __shfl_xor_sync(0xffffffffu, big, o);
+                big = y > big ? y : big;
+            }
+            const bool fine = big < 0x7f800000u;
+            const float sc = fine ? pow2_scale(__uint_as_float(big)) : 1.f, inv = 1.f / sc;
+            uint32_t hi[2], lo[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float f0 = __uint_as_float(u[2 * e] << 16) * inv, f1 = __uint_as_float(u[2 * e] & 0xffff0000u) * inv;
+                const float f2 = __uint_as_float(u[2 * e + 1] << 16) * inv, f3 = __uint_as_float(u[2 * e + 1] & 0xffff0000u) * inv;
+                hi[e] = narrow4(f0, f1, f2, f3);
+                uint32_t b0, b1;
+                widen4(hi[e], b0, b1);
+                const float2 h0 = __half22float2(*reinterpret_cast<const __half2*>(&b0));
+                const float2 h1 = __half22float2(*reinterpret_cast<const __half2*>(&b1));
+                lo[e] = narrow4(f0 - h0.x, f1 - h0.y, f2 - h1.x, f3 - h1.y);
+            }
+            if (r < padded) {
+                const uint32_t at = x.sbase + L::kQ + (r >> 7) * 2 * L::kT8 + swz8<D>(r & 127, chunk >> 1) + 8 * (chunk & 1);
+                sts8(at, hi[0], hi[1]);
+                sts8(at + L::kT8, lo[0], lo[1]);
+                if (chunk == 0) exps[r] = fine ? (uint8_t)(__float_as_uint(sc) >> 23) : (uint8_t)255;
+            }
+        }
     }
-    return is_finite(amax) ? a.scale_log2 * s : NAN;
 }
 
-// One key tile of one row: scores out of TMEM, p' back into it.
-template <int D, int NG>
-__device__ __forceinline__ void softmax_tile(const Ctx& x, int i, uint32_t slot, uint32_t tS, uint32_t tO, float cs,
-                                             int visible, bool full, bool first, float& m, float& mo, float& l) {
-    constexpr int GK = kTileKeys / NG;  // keys per page in a tile
+// COLS keys of one key tile for one row: scores out of TMEM (columns from tC on), p' back into them. NG pages of GK keys
+// each; sc points at the first one's key scale. `settle` waits until the row's O may be rescaled.
+template <int D, int NG, int COLS, typename Settle>
+__device__ __forceinline__ void softmax_part(uint32_t tC, uint32_t tO, const float* sc, float cs, int visible, bool full,
+                                             bool first, float& m, float& mo, float& l, Settle settle) {
+    constexpr int GK = COLS / NG, Q = COLS / 32;
     if (!full) {
         // masked entries become -inf in TMEM first, so that other tiles run no mask code
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
+        for (int q = 0; q < Q; ++q) {
             uint32_t v[32];
-            tc::tmem_ld32(tS + 32 * q, v);
+            tc::tmem_ld32(tC + 32 * q, v);
             tc::tmem_ld_wait();
 #pragma unroll
             for (int e = 0; e < 32; ++e)
                 if (32 * q + e >= visible) v[e] = 0xff800000u;
-            tc::tmem_st32(tS + 32 * q, v);
+            tc::tmem_st32(tC + 32 * q, v);
         }
         tc::tmem_st_wait();
     }
-    uint32_t r[4][32];
+    uint32_t r[Q][32];
 #pragma unroll
-    for (int q = 0; q < 4; ++q) tc::tmem_ld32(tS + 32 * q, r[q]);
-    const float* sc = reinterpret_cast<const float*>(x.smem + Smem<D>::kScale) + slot * 16;
+    for (int q = 0; q < Q; ++q) tc::tmem_ld32(tC + 32 * q, r[q]);
     float ks[NG], lv[NG];
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
-        ks[g] = cs * sc[g * (8 / NG)];
-        lv[g] = sc[8 + g * (8 / NG)];
+        ks[g] = cs * sc[g * (GK / 16)];
+        lv[g] = sc[8 + g * (GK / 16)];
     }
     tc::tmem_ld_wait();
+    auto at = [&](int k) { return __uint_as_float(r[k >> 5][k & 31]); };
     float mx = -INFINITY, mxo = -INFINITY;
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
-        float c0 = -INFINITY, c1 = -INFINITY;
+        float c0 = -INFINITY, c1 = -INFINITY, c2 = -INFINITY, c3 = -INFINITY;
 #pragma unroll
-        for (int e = 0; e < GK; e += 4) {
+        for (int e = 0; e < GK; e += 8) {
             const int k = g * GK + e;
-            c0 = tc::fmax3(c0, __uint_as_float(r[k >> 5][k & 31]), __uint_as_float(r[(k + 1) >> 5][(k + 1) & 31]));
-            c1 = tc::fmax3(c1, __uint_as_float(r[(k + 2) >> 5][(k + 2) & 31]), __uint_as_float(r[(k + 3) >> 5][(k + 3) & 31]));
+            c0 = tc::fmax3(c0, at(k), at(k + 1));
+            c1 = tc::fmax3(c1, at(k + 2), at(k + 3));
+            c2 = tc::fmax3(c2, at(k + 4), at(k + 5));
+            c3 = tc::fmax3(c3, at(k + 6), at(k + 7));
         }
-        const float y = fmaxf(c0, c1) * ks[g];
+        const float y = fmaxf(fmaxf(c0, c1), fmaxf(c2, c3)) * ks[g];
         mx = fmaxf(mx, y);
         mxo = fmaxf(mxo, y + lv[g]);
     }
@@ -662,59 +741,49 @@ __device__ __forceinline__ void softmax_tile(const Ctx& x, int i, uint32_t slot,
         mo = mxo - 7.f;
     }
     if (!first && __any_sync(0xffffffffu, move)) {
+        settle();
 #pragma unroll
-        for (int q = 0; q < D / 32; ++q) {
-            uint32_t o[32];
-            tc::tmem_ld32(tO + 32 * q, o);
+        for (int q = 0; q < D / 16; ++q) {
+            uint32_t o[16];
+            tmem_ld16(tO + 16 * q, o);
             tc::tmem_ld_wait();
 #pragma unroll
-            for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-            tc::tmem_st32(tO + 32 * q, o);
+            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+            tc::tmem_st16(tO + 16 * q, o);
         }
     }
     const float m_use = m == -INFINITY ? 0.f : m, mo_use = mo == -INFINITY ? 0.f : mo;
-    uint32_t pk[2][32];
+    uint32_t pk[16];
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
-        const float b = lv[g] - mo_use;
-        const float2 a2 = make_float2(ks[g], ks[g]), b2 = make_float2(b, b);
-        float2 sum = make_float2(0.f, 0.f);
+        const float b = lv[g] - mo_use, shift = b + m_use;
+        // The page's share of l is the sum of its p' times 2^-shift; where its value scale is so small that p' may have
+        // fallen below what fp32 holds, it is the sum of the weights themselves.
+        const bool tiny = __any_sync(0xffffffffu, shift < -60.f);
+        if (tiny) {
+            float w = 0.f;
 #pragma unroll
-        for (int e = 0; e < GK; e += 2) {
+            for (int e = 0; e < GK; ++e) w += ex2f(fmaf(at(g * GK + e), ks[g], -m_use));
+            l += w;
+        }
+        const float2 a2 = make_float2(ks[g], ks[g]), b2 = make_float2(b, b);
+        float2 s0 = make_float2(0.f, 0.f), s1 = make_float2(0.f, 0.f);
+#pragma unroll
+        for (int e = 0; e < GK; e += 4) {
             const int k = g * GK + e;
-            const float2 y = tc::fma2(make_float2(__uint_as_float(r[k >> 5][k & 31]), __uint_as_float(r[k >> 5][(k & 31) + 1])), a2, b2);
-            const float2 p = make_float2(ex2f(y.x), ex2f(y.y));
-            sum = tc::add2(sum, p);
-            pk[k >> 6][(k & 63) >> 1] = pack_h2(p.x, p.y);
+            const float2 y0 = tc::fma2(make_float2(at(k), at(k + 1)), a2, b2), y1 = tc::fma2(make_float2(at(k + 2), at(k + 3)), a2, b2);
+            const float2 p0 = make_float2(ex2f(y0.x), ex2f(y0.y)), p1 = make_float2(ex2f(y1.x), ex2f(y1.y));
+            s0 = tc::add2(s0, p0);
+            s1 = tc::add2(s1, p1);
+            pk[(k & 31) >> 1] = pack_h2(p0.x, p0.y);
+            pk[((k & 31) >> 1) + 1] = pack_h2(p1.x, p1.y);
+            if ((k & 31) == 28) tc::tmem_st16(tC + 16 * (k >> 5), pk);
         }
-        // the page's share of l; where its value scale is so small that p' may have fallen below what fp32 holds, l
-        // takes the weights themselves
-        const float shift = b + m_use;
-        if (__any_sync(0xffffffffu, shift < -60.f)) {
-            sum = make_float2(0.f, 0.f);
-            for (int e = 0; e < GK; e += 2) {
-                const int k = g * GK + e;
-                float v0, v1;
-                uint32_t s0, s1;
-                // the scores again, out of the registers' copy in TMEM (p' is stored below)
-                asm volatile("tcgen05.ld.sync.aligned.32x32b.x2.b32 {%0,%1}, [%2];" : "=r"(s0), "=r"(s1) : "r"(tS + k));
-                tc::tmem_ld_wait();
-                v0 = __uint_as_float(s0);
-                v1 = __uint_as_float(s1);
-                sum.x += ex2f(fmaf(v0, ks[g], -m_use));
-                sum.y += ex2f(fmaf(v1, ks[g], -m_use));
-            }
-            l += sum.x + sum.y;
-        } else {
-            l = fmaf(sum.x + sum.y, ex2f(-shift), l);
-        }
+        if (!tiny) l = fmaf(s0.x + s1.x + (s0.y + s1.y), ex2f(-shift), l);
     }
-    tc::tmem_st32(tS, pk[0]);
-    tc::tmem_st32(tS + 32, pk[1]);
     tc::tmem_st_wait();
     tc::tc_fence_before();
     __syncwarp();
-    if ((threadIdx.x & 31) == 0) tc::mbar_arrive(x.bar(B_P, i));
 }
 
 // Writes 32 columns of a row: normalised values v.
@@ -751,7 +820,7 @@ __device__ __forceinline__ void softmax(const Ctx& x, const CacheAttnArgs& a, co
     Walk w;
     w.begin(a, st);
     Seg g;
-    uint32_t t_base = 0, seg = 0, n_s = 0, n_o = 0;
+    uint32_t t_base = 0, seg = 0, s0_phases = 0;  // s0_phases: bit of each B_S0 stage's next phase
     bool ok = true;  // warp-uniform; the loops run on without waiting once it is false
     while (w.next(a, &g)) {
         const int nt = g.tiles();
@@ -766,39 +835,53 @@ __device__ __forceinline__ void softmax(const Ctx& x, const CacheAttnArgs& a, co
             }
             continue;
         }
-        // Q of the unit: with one MMA tile group 0 writes the high terms, group 1 the low ones
-        const float cs = split_q<D>(x, a, g, m, row, x.sbase + L::kQ + (g.two ? i * 2 * L::kT8 : 0), g.two || i == 0, g.two || i == 1);
+        split_q<D>(x, a, g);
         tc::fence_proxy_async_smem();
         tc::tc_fence_before();
         __syncwarp();
         if (lane == 0) tc::mbar_arrive(x.bar(B_Q, 0));
+        softmax_sync();  // the rows' exponents
+        // the factor that turns the tensor core's q . k8 into base-2 scores; a row that is not finite becomes NaN, and no other
+        const int qe = x.smem[L::kQExp + (g.two ? 128 * i : 0) + row];
+        const float cs = qe == 255 ? NAN : a.scale_log2 * __uint_as_float((uint32_t)qe << 23);
 
         const int end = live ? key_end(g.len, a.block, g.pos0 + m / a.G) : 0;
         const int full_end = __shfl_sync(0xffffffffu, end, 0);  // the warp's first row sees the fewest keys
         const bool warp_live = __shfl_sync(0xffffffffu, (int)live, 0);
-        const int step = g.two ? 1 : 2, first = g.two ? 0 : i;
         float mm = -INFINITY, mo = -INFINITY, l = 0.f;
-        for (int j = first; j < nt; j += step) {
-            const uint32_t t = t_base + j, slot_no = t % kScaleSlots;
-            if (ok) ok = __all_sync(0xffffffffu, x.wait(B_S, i, n_s & 1) && x.wait(B_SC, slot_no, (t / kScaleSlots) & 1));
-            ++n_s;
+        for (int j = 0; j < nt; ++j) {
+            const uint32_t t = t_base + j, slot_no = t % kScaleSlots, stage = t % kStages;
+            const uint32_t buf = g.two ? (uint32_t)i : t & 1;
+            if (ok) {
+                const bool got = (g.two && i == 0 ? x.wait(B_S0, stage, (s0_phases >> stage) & 1) : x.wait(B_S1, stage, (t / kStages) & 1)) &&
+                                 x.wait(B_SC, slot_no, (t / kScaleSlots) & 1);
+                ok = __all_sync(0xffffffffu, got);
+            }
+            if (g.two) s0_phases ^= 1u << stage;
             tc::tc_fence_after();
             const int k0 = (g.kt0 + j) * kTileKeys;
+            const float* sc = reinterpret_cast<const float*>(x.smem + L::kScale) + slot_no * 16;
             if (warp_live && ok) {
-                softmax_tile<D, NG>(x, i, slot_no, tS, tO, cs, end - k0, k0 + kTileKeys <= full_end, j == first, mm, mo, l);
-            } else if (lane == 0) {
-                tc::mbar_arrive(x.bar(B_P, i));
+                if (g.two) {
+                    // S of a tile is issued behind the PV of the one before, so O is settled
+                    softmax_part<D, NG, 128>(tS, tO, sc, cs, end - k0, k0 + kTileKeys <= full_end, j == 0, mm, mo, l, [] {});
+                } else {
+                    const int h0 = k0 + 64 * i;
+                    softmax_part<D, (NG > 1 ? NG / 2 : 1), 64>(x.tmem + 128 * buf + 64 * i + lane_base, tO, sc + 4 * i, cs, end - h0,
+                                                               h0 + 64 <= full_end, j == 0, mm, mo, l, [&] {
+                                                                   ok = __all_sync(0xffffffffu, x.wait(B_PV, (t - 1) & 1, ((t - 1) >> 1) & 1));
+                                                                   tc::tc_fence_after();
+                                                               });
+                }
             }
+            if (lane == 0) tc::mbar_arrive(x.bar(B_P, 2 * (t & 1) + i));
         }
-        const bool mine = nt > first;  // the group had a tile
-        if (mine) {
-            if (ok) ok = __all_sync(0xffffffffu, x.wait(B_O, i, n_o & 1));
-            ++n_o;
-        }
+        t_base += nt;
+        // every product of the unit is done
+        if (ok) ok = __all_sync(0xffffffffu, x.wait(B_PV, (t_base - 1) & 1, ((t_base - 1) >> 1) & 1));
         tc::tc_fence_after();
         int* nan_first = reinterpret_cast<int*>(x.smem + L::kNan) + (seg & 3) * D;
         ++seg;
-        t_base += nt;
         if (g.two) {
             // o = O 2^(mo - m) / l
             const bool some = l != 0.f;  // NaN counts as something
@@ -836,8 +919,8 @@ __device__ __forceinline__ void softmax(const Ctx& x, const CacheAttnArgs& a, co
             const float lj = (mm == -INFINITY && l == 0.f ? 0.f : l * ex2f(mm - mj)) + (m1 == -INFINITY && l1 == 0.f ? 0.f : l1 * ex2f(m1 - mj));
             const bool some = lj != 0.f;
             const float f = some ? ex2f(moj - mj) / lj : 0.f;
-            // this group's and the other's factor; a group without a tile or a row without keys in it adds nothing
-            const bool use0 = l != 0.f && mine, use1 = l1 != 0.f && nt > (first ^ 1);
+            // this group's and the other's factor; one without keys that the row sees adds nothing
+            const bool use0 = l != 0.f, use1 = l1 != 0.f;
             const float f0 = use0 ? f * ex2f(mo - moj) : 0.f, f1 = use1 ? f * ex2f(mo1 - moj) : 0.f;
             const float l2 = some ? mj + __log2f(lj) : -INFINITY;
             const uint32_t tO1 = x.tmem + 256 + D * (i ^ 1) + lane_base;
@@ -886,16 +969,15 @@ __global__ void __launch_bounds__(kThreads, 1)
         x.words[1] = x.words[2] = x.words[3] = 0;
         for (int s = 0; s < kStages; ++s) {
             tc::mbar_init(x.bar(B_KFULL, s), 1);
-            tc::mbar_init(x.bar(B_KEMPTY, s), 1);
             tc::mbar_init(x.bar(B_VFULL, s), 1);
-            tc::mbar_init(x.bar(B_VEMPTY, s), 2);  // lane 0 of both widening warps
+            tc::mbar_init(x.bar(B_VEMPTY, s), 4);  // lane 0 of the widening warps
+            tc::mbar_init(x.bar(B_S0, s), 1);
+            tc::mbar_init(x.bar(B_S1, s), 1);
         }
         for (int s = 0; s < 2; ++s) {
-            tc::mbar_init(x.bar(B_WFULL, s), 2);
-            tc::mbar_init(x.bar(B_WEMPTY, s), 1);
-            tc::mbar_init(x.bar(B_S, s), 1);
-            tc::mbar_init(x.bar(B_P, s), 4);  // lane 0 of each warp of the group
-            tc::mbar_init(x.bar(B_O, s), 1);
+            tc::mbar_init(x.bar(B_P, 2 * s), 8);  // lane 0 of group 0's warps and of the widening warps
+            tc::mbar_init(x.bar(B_P, 2 * s + 1), 4);
+            tc::mbar_init(x.bar(B_PV, s), 1);
         }
         tc::mbar_init(x.bar(B_Q, 0), 8);
         for (int s = 0; s < kScaleSlots; ++s) tc::mbar_init(x.bar(B_SC, s), 1);
@@ -909,7 +991,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::prefetch_tmap(&tk);
         tc::prefetch_tmap(&tv);
     }
-    find_start(a, st, reinterpret_cast<long long*>(smem));  // the scan's 96 bytes lie where Q will
+    find_start(a, st, reinterpret_cast<long long*>(smem));  // the scan's words lie where Q will
     tc::tc_fence_before();
     __syncthreads();
     tc::tc_fence_after();
@@ -920,10 +1002,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         if (warp >= 8) {
             tc::regs_dec<kRegsOther>();
             if (warp == 8) produce<D>(x, a, *st, &tk, &tv);
-            else if (warp == 9) {
-                if (lane == 0) issue<D>(x, a, *st);
-                __syncwarp();
-            } else widen<D>(x, a, *st);
+            else if (warp == 9) issue<D>(x, a, *st);
+            else if (warp >= 12) widen<D>(x, a, *st);
         } else {
             tc::regs_inc<kRegsSoftmax>();
             softmax<D, NG>(x, a, *st);
