@@ -3,13 +3,15 @@
 //
 // A unit is (sequence, kv head, run of 256 flat rows): the rows r * G + g of a
 // sequence's new rows r and of the G query heads g that share the kv head,
-// which all read the same keys. Its work is its key tiles of 128 keys, up to
-// the last key that its last row sees (one, without keys, if it sees none).
-// All units' tiles, laid end to end (sequence, head, run, tile), are cut into
-// equal shares, one per CTA: CTA c takes the tiles [W c / C, W (c + 1) / C).
-// A share that begins or ends inside a unit leaves a partial result; at most
-// two per CTA, slot 2 c for a unit begun by an earlier CTA and slot 2 c + 1
-// for one that a later CTA goes on with.
+// which all read the same keys. Its tiles are its runs of 128 keys, up to the
+// last key that its last row sees (one, without keys, if it sees none). Its
+// cost is its tiles and kUnitTiles more for what it takes to begin and to end
+// it (query, results), twice that for a unit of two MMA tiles. All units'
+// costs, laid end to end (sequence, head, run), are cut into equal shares, one
+// per CTA: CTA c takes [W c / C, W (c + 1) / C). A share that begins or ends
+// between the tiles of a unit leaves a partial result; at most two per CTA,
+// slot 2 c for a unit begun by an earlier CTA and slot 2 c + 1 for one that a
+// later CTA goes on with.
 #pragma once
 
 #include "cache.cuh"
@@ -20,16 +22,17 @@ namespace cattn {
 constexpr int kTileKeys = 128;
 constexpr int kUnitRows = 256;
 constexpr int kMaxCtas = 256;
-// A CTA takes at least this many tiles where there are too few for all: below it the partial results cost more than
-// the shorter shares save.
-constexpr int kMinTiles = 2;
+constexpr int kUnitTiles = 4;
+// A share is at least this long where there is too little work for all CTAs: below it the partial results cost more
+// than the shorter shares save. (At least 2, so that each of the shares of a unit holds a tile of it.)
+constexpr int kMinShare = 6;
 
 // What CTA c leaves for the merge: where its share begins, and its errors.
 struct ShareRec {
     int row0, rows, pos0, len;  // the sequence (SeqRows) whose unit the share begins in
     int head, m0;               // kv head and first flat row of that unit
-    int kt0, cost;              // first tile of the share in the unit, tiles of the unit
-    long long W;                // tiles of the whole call (0: nothing to do)
+    int off, cost;              // where in the unit's cost the share begins, the unit's cost
+    long long W;                // cost of the whole call (0: nothing to do)
     int C;                      // shares
     int error, info;
     int pad[3];
@@ -53,17 +56,22 @@ __device__ __forceinline__ float* slot_at(uint8_t* scratch, int slot, int rows, 
 __device__ __forceinline__ long long share_begin(long long W, int C, int c) { return W * c / C; }
 
 struct Unit {
-    int last;  // last flat row + 1
-    int end;   // keys that the last row sees
-    int cost;  // tiles, at least 1
+    int last;   // last flat row + 1
+    int end;    // keys that the last row sees
+    int tiles;  // at least 1
+    int two;    // 1: two MMA tiles
+    __device__ __forceinline__ int cost() const { return (kUnitTiles + tiles) << two; }
 };
 __device__ __forceinline__ Unit unit_of(const CacheAttnArgs& a, const SeqRows& r, int m0) {
     Unit u;
     u.last = imin(r.rows * a.G, m0 + kUnitRows);
     u.end = key_end(r.len, a.block, r.pos0 + (u.last - 1) / a.G);
-    u.cost = imax(1, (u.end + kTileKeys - 1) / kTileKeys);
+    u.tiles = imax(1, (u.end + kTileKeys - 1) / kTileKeys);
+    u.two = u.last - m0 > kUnitRows / 2;
     return u;
 }
+// First tile that lies at or behind offset `off` of a unit's cost.
+__device__ __forceinline__ int tile_at(int off, int two) { return imax(0, (off >> two) - kUnitTiles); }
 
 }  // namespace cattn
 

@@ -82,7 +82,8 @@ struct Smem {
     static constexpr int kMisc = kV + kStages * kT8;
     static constexpr int kScale = kMisc;                          // float [slots][16]: ks, log2 vs of 16-key groups
     static constexpr int kNan = kScale + kScaleSlots * 64;        // int [4][D]: first key whose value is NaN, per column
-    static constexpr int kBar = kNan + 4 * D * 4;
+    static constexpr int kNanAny = kNan + 4 * D * 4;              // int [4]: first key with a NaN in any column
+    static constexpr int kBar = kNanAny + 16;
     static constexpr int kWords = kBar + B_COUNT * 8;             // tmem, abort, error, info
     static constexpr int kStart = kWords + 16;                    // Start
     static constexpr int kQExp = kStart + 64;                     // uint8 [256]: exponent of the rows' scale
@@ -92,31 +93,30 @@ static_assert(Smem<128>::kBytes <= 232448, "shared memory");
 
 // Where the CTA's share begins, found once by the whole CTA.
 struct Start {
-    long long W, begin, left;
-    int C, s, h, m0, kt, bad;
+    long long W, left;
+    int C, s, h, m0, off, bad;
 };
 static_assert(sizeof(Start) <= 64, "");
 
 // A run of tiles of one unit.
 struct Seg {
-    int row0, rows, pos0, len;  // the sequence
-    int s, h, m0, last, end;    // unit
-    int kt0, kt1, cost;
-    bool two;                   // two MMA tiles
+    int row0, pos0, len;  // the sequence
+    int s, h, m0, last, end;
+    int kt0, kt1;
+    bool two, whole;
     __device__ __forceinline__ int tiles() const { return end ? kt1 - kt0 : 0; }
-    __device__ __forceinline__ bool whole() const { return kt0 == 0 && kt1 == cost; }
 };
 
 struct Walk {
     SeqRows r;
     Unit u;
-    int s, h, m0, kt;
+    int s, h, m0, off;
     long long left;
     __device__ __forceinline__ void begin(const CacheAttnArgs& a, const Start& st) {
         s = st.s;
         h = st.h;
         m0 = st.m0;
-        kt = st.kt;
+        off = st.off;
         left = st.left;
         if (left > 0) {
             r = seq_rows(a.c, a.cu_rows, a.q_pos, a.total_rows, s);
@@ -124,25 +124,28 @@ struct Walk {
         }
     }
     __device__ __forceinline__ bool next(const CacheAttnArgs& a, Seg* g) {
-        if (left <= 0) return false;
-        const int n = left < u.cost - kt ? (int)left : u.cost - kt;
-        *g = Seg{r.row0, r.rows, r.pos0, r.len, s, h, m0, u.last, u.end, kt, kt + n, u.cost, u.last - m0 > 128};
-        left -= n;
-        kt += n;
-        if (left > 0) {  // the unit is done
-            kt = 0;
-            m0 += kUnitRows;
-            if (m0 >= r.rows * a.G) {
-                m0 = 0;
-                if (++h == a.c.Hk) {
-                    h = 0;
-                    do r = seq_rows(a.c, a.cu_rows, a.q_pos, a.total_rows, ++s);
-                    while (r.rows == 0);
+        while (left > 0) {
+            const int c = u.cost(), n = left < c - off ? (int)left : c - off;
+            const int kt0 = tile_at(off, u.two), kt1 = tile_at(off + n, u.two);
+            *g = Seg{r.row0, r.pos0, r.len, s, h, m0, u.last, u.end, kt0, kt1, u.two != 0, kt0 == 0 && kt1 == u.tiles};
+            left -= n;
+            off += n;
+            if (left > 0) {  // the unit is done
+                off = 0;
+                m0 += kUnitRows;
+                if (m0 >= r.rows * a.G) {
+                    m0 = 0;
+                    if (++h == a.c.Hk) {
+                        h = 0;
+                        do r = seq_rows(a.c, a.cu_rows, a.q_pos, a.total_rows, ++s);
+                        while (r.rows == 0);
+                    }
                 }
+                u = unit_of(a, r, m0);
             }
-            u = unit_of(a, r, m0);
+            if (kt1 > kt0) return true;
         }
-        return true;
+        return false;
     }
 };
 
@@ -281,7 +284,7 @@ __device__ __forceinline__ long long cta_scan(long long x, long long* total, lon
 
 __device__ __forceinline__ long long head_cost(const CacheAttnArgs& a, const SeqRows& r) {
     long long c = 0;
-    for (int m0 = 0; m0 < r.rows * a.G; m0 += kUnitRows) c += unit_of(a, r, m0).cost;
+    for (int m0 = 0; m0 < r.rows * a.G; m0 += kUnitRows) c += unit_of(a, r, m0).cost();
     return c;
 }
 
@@ -306,16 +309,15 @@ __device__ __forceinline__ void find_start(const CacheAttnArgs& a, Start* st, lo
     __syncthreads();
     bad = st->bad;
     if (bad != 0x7fffffff) W = 0;
-    long long C = W / kMinTiles;
+    long long C = W / kMinShare;
     C = C < 1 ? 1 : C > (long long)gridDim.x ? (long long)gridDim.x : C;
     const int c = (int)blockIdx.x;
     const long long begin = c < C ? share_begin(W, (int)C, c) : 0, end = c < C ? share_begin(W, (int)C, c + 1) : 0;
     if (tid == 0) {
         st->W = W;
         st->C = (int)C;
-        st->begin = begin;
         st->left = end - begin;
-        st->s = st->h = st->m0 = st->kt = 0;
+        st->s = st->h = st->m0 = st->off = 0;
     }
     __syncthreads();
     if (end > begin) {
@@ -335,9 +337,9 @@ __device__ __forceinline__ void find_start(const CacheAttnArgs& a, Start* st, lo
                 st->h = (int)(off / per);
                 off %= per;
                 int m0 = 0;
-                for (int u; off >= (u = unit_of(a, r, m0).cost); m0 += kUnitRows) off -= u;
+                for (int u; off >= (u = unit_of(a, r, m0).cost()); m0 += kUnitRows) off -= u;
                 st->m0 = m0;
-                st->kt = (int)off;
+                st->off = (int)off;
             }
         }
     }
@@ -479,6 +481,7 @@ __device__ __forceinline__ void widen(const Ctx& x, const CacheAttnArgs& a, cons
     while (w.next(a, &g)) {
         if (g.tiles() == 0) continue;
         int* nan_first = reinterpret_cast<int*>(x.smem + L::kNan) + (seg & 3) * D;
+        int* nan_any = reinterpret_cast<int*>(x.smem + L::kNanAny) + (seg & 3);
         ++seg;
         // keys that every row of the unit sees; a NaN among the others must not reach a row that does not see it
         const int all = key_end(g.len, a.block, g.pos0 + g.m0 / a.G);
@@ -506,6 +509,7 @@ __device__ __forceinline__ void widen(const Ctx& x, const CacheAttnArgs& a, cons
                             const uint32_t sh = 8 * (e & 3);
                             if (((v[j][e >> 2] >> sh) & 0x7f) == 0x7f) {
                                 atomicMin(nan_first + 16 * c + e, kt * kTileKeys + r);
+                                atomicMin(nan_any, kt * kTileKeys + r);
                                 v[j][e >> 2] &= ~(0xffu << sh);
                             }
                         }
@@ -628,63 +632,76 @@ __device__ __forceinline__ void issue(const Ctx& x, const CacheAttnArgs& a, cons
 template <int D>
 __device__ __forceinline__ void split_q(const Ctx& x, const CacheAttnArgs& a, const Seg& g) {
     using L = Smem<D>;
-    constexpr int PER = D / 8, ROWS = 256 / PER, BATCH = 4;
+    constexpr int PER = D / 8, ROWS = 256 / PER, BATCH = 128 / ROWS;
     const int chunk = threadIdx.x % PER, r0 = threadIdx.x / PER;
     const int n = g.last - g.m0, padded = (n + 31) & ~31;
     uint8_t* exps = x.smem + L::kQExp;
-    for (int b = 0; b < padded; b += BATCH * ROWS) {
-        uint4 v[BATCH];
+    uint4 v[2][BATCH];  // every load before the first use
+    {
+        const int m = g.m0 + r0;
+        int row = m / a.G, rem = m - row * a.G;
+        const int dr = ROWS / a.G, dm = ROWS - dr * a.G;
+        const __nv_bfloat16* q = a.q + ((long long)g.row0 * a.H + g.h * a.G) * D + 8 * chunk;
 #pragma unroll
-        for (int i = 0; i < BATCH; ++i) {
-            const int r = b + i * ROWS + r0, m = g.m0 + r;
-            v[i] = make_uint4(0, 0, 0, 0);
-            if (r < n) {
-                const int row = m / a.G, head = g.h * a.G + (m - row * a.G);
-                v[i] = __ldg(reinterpret_cast<const uint4*>(a.q + ((long long)(g.row0 + row) * a.H + head) * D) + chunk);
+        for (int i = 0; i < 2 * BATCH; ++i) {
+            uint4 y = make_uint4(0, 0, 0, 0);
+            if (i * ROWS + r0 < n) y = __ldg(reinterpret_cast<const uint4*>(q + ((long long)row * a.H + rem) * D));
+            v[i / BATCH][i % BATCH] = y;
+            row += dr;
+            rem += dm;
+            if (rem >= a.G) {
+                rem -= a.G;
+                ++row;
             }
         }
+    }
 #pragma unroll
-        for (int i = 0; i < BATCH; ++i) {
-            const int r = b + i * ROWS + r0;
-            const uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
-            uint32_t big = 0;
+    for (int i = 0; i < 2 * BATCH; ++i) {
+        if (i * ROWS >= padded) break;  // the same for all threads
+        const int r = i * ROWS + r0;
+        const uint4 y = v[i / BATCH][i % BATCH];
+        const uint32_t u[4] = {y.x, y.y, y.z, y.w};
+        uint32_t big = 0;
 #pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                const uint32_t p = (u[e] << 16) & 0x7fffffffu, q = u[e] & 0x7fff0000u;
-                big = p > big ? p : big;
-                big = q > big ? q : big;
-            }
-#pragma unroll
-            for (int o = PER / 2; o; o >>= 1) {
-                const uint32_t y = __shfl_xor_sync(0xffffffffu, big, o);
-                big = y > big ? y : big;
-            }
-            const bool fine = big < 0x7f800000u;
-            const float sc = fine ? pow2_scale(__uint_as_float(big)) : 1.f, inv = 1.f / sc;
-            uint32_t hi[2], lo[2];
-#pragma unroll
-            for (int e = 0; e < 2; ++e) {
-                const float f0 = __uint_as_float(u[2 * e] << 16) * inv, f1 = __uint_as_float(u[2 * e] & 0xffff0000u) * inv;
-                const float f2 = __uint_as_float(u[2 * e + 1] << 16) * inv, f3 = __uint_as_float(u[2 * e + 1] & 0xffff0000u) * inv;
-                hi[e] = narrow4(f0, f1, f2, f3);
-                uint32_t b0, b1;
-                widen4(hi[e], b0, b1);
-                const float2 h0 = __half22float2(*reinterpret_cast<const __half2*>(&b0));
-                const float2 h1 = __half22float2(*reinterpret_cast<const __half2*>(&b1));
-                lo[e] = narrow4(f0 - h0.x, f1 - h0.y, f2 - h1.x, f3 - h1.y);
-            }
-            if (r < padded) {
-                const uint32_t at = x.sbase + L::kQ + (r >> 7) * 2 * L::kT8 + swz8<D>(r & 127, chunk >> 1) + 8 * (chunk & 1);
-                sts8(at, hi[0], hi[1]);
-                sts8(at + L::kT8, lo[0], lo[1]);
-                if (chunk == 0) exps[r] = fine ? (uint8_t)(__float_as_uint(sc) >> 23) : (uint8_t)255;
-            }
+        for (int e = 0; e < 4; ++e) {
+            const uint32_t p = (u[e] << 16) & 0x7fffffffu, q = u[e] & 0x7fff0000u;
+            big = p > big ? p : big;
+            big = q > big ? q : big;
         }
+#pragma unroll
+        for (int o = PER / 2; o; o >>= 1) {
+            const uint32_t z = __shfl_xor_sync(0xffffffffu, big, o);
+            big = z > big ? z : big;
+        }
+        const bool fine = big < 0x7f800000u;
+        const uint32_t sc = fine ? __float_as_uint(pow2_scale(__uint_as_float(big))) : 0x3f800000u;
+        const float inv = __uint_as_float(0x7f000000u - sc);  // 2^-k for 2^k, -126 <= k <= 120
+        uint32_t hi[2], lo[2];
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+            const float f0 = __uint_as_float(u[2 * e] << 16) * inv, f1 = __uint_as_float(u[2 * e] & 0xffff0000u) * inv;
+            const float f2 = __uint_as_float(u[2 * e + 1] << 16) * inv, f3 = __uint_as_float(u[2 * e + 1] & 0xffff0000u) * inv;
+            hi[e] = narrow4(f0, f1, f2, f3);
+            uint32_t b0, b1;
+            widen4(hi[e], b0, b1);
+            const float2 h0 = __half22float2(*reinterpret_cast<const __half2*>(&b0));
+            const float2 h1 = __half22float2(*reinterpret_cast<const __half2*>(&b1));
+            lo[e] = narrow4(f0 - h0.x, f1 - h0.y, f2 - h1.x, f3 - h1.y);
+        }
+        const uint32_t at = x.sbase + L::kQ + (r >> 7) * 2 * L::kT8 + swz8<D>(r & 127, chunk >> 1) + 8 * (chunk & 1);
+        sts8(at, hi[0], hi[1]);
+        sts8(at + L::kT8, lo[0], lo[1]);
+        if (chunk == 0) exps[r] = fine ? (uint8_t)(sc >> 23) : (uint8_t)255;
     }
 }
 
 // COLS keys of one key tile for one row: scores out of TMEM (columns from tC on), p' back into them. NG pages of GK keys
 // each; sc points at the first one's key scale. `settle` waits until the row's O may be rescaled.
+//
+// Tiles are first taken with the row's present offsets, the maximum of the exponents alongside: it is at most 15 (p' fits
+// fp16) for all but a few tiles of a sequence. Where a row of the warp finds a larger one (its first keys among them), or
+// a page's value scale is so small that its p' may fall below what fp32 holds, the warp takes the tile again: new offsets
+// from the tile's maxima, O and l rescaled, and l from the weights themselves where p' says too little.
 template <int D, int NG, int COLS, typename Settle>
 __device__ __forceinline__ void softmax_part(uint32_t tC, uint32_t tO, const float* sc, float cs, int visible, bool full,
                                              bool first, float& m, float& mo, float& l, Settle settle) {
@@ -714,72 +731,96 @@ __device__ __forceinline__ void softmax_part(uint32_t tC, uint32_t tO, const flo
     }
     tc::tmem_ld_wait();
     auto at = [&](int k) { return __uint_as_float(r[k >> 5][k & 31]); };
-    float mx = -INFINITY, mxo = -INFINITY;
-#pragma unroll
-    for (int g = 0; g < NG; ++g) {
-        float c0 = -INFINITY, c1 = -INFINITY, c2 = -INFINITY, c3 = -INFINITY;
-#pragma unroll
-        for (int e = 0; e < GK; e += 8) {
-            const int k = g * GK + e;
-            c0 = tc::fmax3(c0, at(k), at(k + 1));
-            c1 = tc::fmax3(c1, at(k + 2), at(k + 3));
-            c2 = tc::fmax3(c2, at(k + 4), at(k + 5));
-            c3 = tc::fmax3(c3, at(k + 6), at(k + 7));
-        }
-        const float y = fmaxf(fmaxf(c0, c1), fmaxf(c2, c3)) * ks[g];
-        mx = fmaxf(mx, y);
-        mxo = fmaxf(mxo, y + lv[g]);
-    }
-    if (mx > m + 8.f) {
-        l *= ex2f(m - mx);
-        m = mx;
-    }
-    const bool move = mxo > mo + 15.f;
-    float alpha = 1.f;
-    if (move) {
-        alpha = ex2f(mo - (mxo - 7.f));
-        mo = mxo - 7.f;
-    }
-    if (!first && __any_sync(0xffffffffu, move)) {
-        settle();
-#pragma unroll
-        for (int q = 0; q < D / 16; ++q) {
-            uint32_t o[16];
-            tmem_ld16(tO + 16 * q, o);
-            tc::tmem_ld_wait();
-#pragma unroll
-            for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-            tc::tmem_st16(tO + 16 * q, o);
-        }
-    }
-    const float m_use = m == -INFINITY ? 0.f : m, mo_use = mo == -INFINITY ? 0.f : mo;
-    uint32_t pk[16];
-#pragma unroll
-    for (int g = 0; g < NG; ++g) {
-        const float b = lv[g] - mo_use, shift = b + m_use;
-        // The page's share of l is the sum of its p' times 2^-shift; where its value scale is so small that p' may have
-        // fallen below what fp32 holds, it is the sum of the weights themselves.
-        const bool tiny = __any_sync(0xffffffffu, shift < -60.f);
-        if (tiny) {
-            float w = 0.f;
-#pragma unroll
-            for (int e = 0; e < GK; ++e) w += ex2f(fmaf(at(g * GK + e), ks[g], -m_use));
-            l += w;
-        }
+    uint32_t pk[COLS / 2];
+    // p' of page g with exponents s ks + b into pk; returns their sum, and the largest exponent in *top
+    auto weigh = [&](int g, float b, float* top) {
         const float2 a2 = make_float2(ks[g], ks[g]), b2 = make_float2(b, b);
         float2 s0 = make_float2(0.f, 0.f), s1 = make_float2(0.f, 0.f);
+        float t0 = *top, t1 = *top;
 #pragma unroll
         for (int e = 0; e < GK; e += 4) {
             const int k = g * GK + e;
             const float2 y0 = tc::fma2(make_float2(at(k), at(k + 1)), a2, b2), y1 = tc::fma2(make_float2(at(k + 2), at(k + 3)), a2, b2);
+            t0 = tc::fmax3(t0, y0.x, y0.y);
+            t1 = tc::fmax3(t1, y1.x, y1.y);
             const float2 p0 = make_float2(ex2f(y0.x), ex2f(y0.y)), p1 = make_float2(ex2f(y1.x), ex2f(y1.y));
             s0 = tc::add2(s0, p0);
             s1 = tc::add2(s1, p1);
-            pk[(k & 31) >> 1] = pack_h2(p0.x, p0.y);
-            pk[((k & 31) >> 1) + 1] = pack_h2(p1.x, p1.y);
-            if ((k & 31) == 28) tc::tmem_st16(tC + 16 * (k >> 5), pk);
+            pk[k >> 1] = pack_h2(p0.x, p0.y);
+            pk[(k >> 1) + 1] = pack_h2(p1.x, p1.y);
         }
-        if (!tiny) l = fmaf(s0.x + s1.x + (s0.y + s1.y), ex2f(-shift), l);
+        *top = fmaxf(t0, t1);
+        return s0.x + s1.x + (s0.y + s1.y);
+    };
+    const float m_was = m == -INFINITY ? 0.f : m, mo_was = mo == -INFINITY ? 0.f : mo;
+    float sum = 0.f, top = -INFINITY, low = INFINITY;
+#pragma unroll
+    for (int g = 0; g < NG; ++g) {
+        const float b = lv[g] - mo_was, shift = b + m_was;
+        low = fminf(low, shift);
+        sum = fmaf(weigh(g, b, &top), ex2f(-shift), sum);
+    }
+    if (__any_sync(0xffffffffu, top > 15.f || low < -60.f || (mo == -INFINITY && top > -INFINITY))) {
+#pragma unroll
+        for (int q = 0; q < Q; ++q) tc::tmem_ld32(tC + 32 * q, r[q]);
+        tc::tmem_ld_wait();
+        float mx = -INFINITY, mxo = -INFINITY;
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+            float c0 = -INFINITY, c1 = -INFINITY;
+#pragma unroll
+            for (int e = 0; e < GK; e += 4) {
+                const int k = g * GK + e;
+                c0 = tc::fmax3(c0, at(k), at(k + 1));
+                c1 = tc::fmax3(c1, at(k + 2), at(k + 3));
+            }
+            const float y = fmaxf(c0, c1) * ks[g];
+            mx = fmaxf(mx, y);
+            mxo = fmaxf(mxo, y + lv[g]);
+        }
+        if (mx > m) {
+            l *= ex2f(m - mx);
+            m = mx;
+        }
+        const bool move = mxo > mo + 15.f;
+        float alpha = 1.f;
+        if (move) {
+            alpha = ex2f(mo - (mxo - 7.f));
+            mo = mxo - 7.f;
+        }
+        if (!first && __any_sync(0xffffffffu, move)) {
+            settle();
+#pragma unroll
+            for (int q = 0; q < D / 16; ++q) {
+                uint32_t o[16];
+                tmem_ld16(tO + 16 * q, o);
+                tc::tmem_ld_wait();
+#pragma unroll
+                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                tc::tmem_st16(tO + 16 * q, o);
+            }
+        }
+        const float m_use = m == -INFINITY ? 0.f : m, mo_use = mo == -INFINITY ? 0.f : mo;
+        sum = 0.f;
+#pragma unroll
+        for (int g = 0; g < NG; ++g) {
+            const float b = lv[g] - mo_use, shift = b + m_use;
+            if (__any_sync(0xffffffffu, shift < -60.f)) {
+#pragma unroll
+                for (int e = 0; e < GK; ++e) sum += ex2f(fmaf(at(g * GK + e), ks[g], -m_use));
+                weigh(g, b, &top);
+            } else {
+                sum = fmaf(weigh(g, b, &top), ex2f(-shift), sum);
+            }
+        }
+    }
+    l += sum;
+#pragma unroll
+    for (int q = 0; q < COLS / 32; ++q) {
+        uint32_t w[16];
+#pragma unroll
+        for (int e = 0; e < 16; ++e) w[e] = pk[16 * q + e];
+        tc::tmem_st16(tC + 16 * q, w);
     }
     tc::tmem_st_wait();
     tc::tc_fence_before();
@@ -826,7 +867,7 @@ __device__ __forceinline__ void softmax(const Ctx& x, const CacheAttnArgs& a, co
         const int nt = g.tiles();
         const int m = g.m0 + (g.two ? 128 * i : 0) + row;  // this thread's flat row
         const bool live = m < g.last;
-        float* slot = g.whole() ? nullptr : slot_at(a.scratch, 2 * (int)blockIdx.x + (g.kt0 > 0 ? 0 : 1), slot_r, D);
+        float* slot = g.whole ? nullptr : slot_at(a.scratch, 2 * (int)blockIdx.x + (g.kt0 > 0 ? 0 : 1), slot_r, D);
         if (nt == 0) {  // rows without keys
             if (live && (g.two || i == 0)) {
                 const float v[32] = {};
@@ -881,6 +922,8 @@ __device__ __forceinline__ void softmax(const Ctx& x, const CacheAttnArgs& a, co
         if (ok) ok = __all_sync(0xffffffffu, x.wait(B_PV, (t_base - 1) & 1, ((t_base - 1) >> 1) & 1));
         tc::tc_fence_after();
         int* nan_first = reinterpret_cast<int*>(x.smem + L::kNan) + (seg & 3) * D;
+        int* nan_any = reinterpret_cast<int*>(x.smem + L::kNanAny) + (seg & 3);
+        const bool nans = *nan_any < g.end;
         ++seg;
         if (g.two) {
             // o = O 2^(mo - m) / l
@@ -895,7 +938,7 @@ __device__ __forceinline__ void softmax(const Ctx& x, const CacheAttnArgs& a, co
 #pragma unroll
                 for (int e = 0; e < 32; ++e) {
                     v[e] = some ? __uint_as_float(o[e]) * f : 0.f;
-                    if (nan_first[32 * q + e] < end) v[e] = NAN;
+                    if (nans && nan_first[32 * q + e] < end) v[e] = NAN;
                 }
                 if (live) store_cols<D>(a, g, m, q, v, slot, slot_r);
             }
@@ -933,7 +976,7 @@ __device__ __forceinline__ void softmax(const Ctx& x, const CacheAttnArgs& a, co
 #pragma unroll
                 for (int e = 0; e < 32; ++e) {
                     v[e] = (use0 ? __uint_as_float(o[e]) * f0 : 0.f) + (use1 ? __uint_as_float(o1[e]) * f1 : 0.f);
-                    if (nan_first[32 * q + e] < end) v[e] = NAN;
+                    if (nans && nan_first[32 * q + e] < end) v[e] = NAN;
                 }
                 if (live) store_cols<D>(a, g, m, q, v, slot, slot_r);
             }
@@ -946,7 +989,7 @@ __device__ __forceinline__ void softmax(const Ctx& x, const CacheAttnArgs& a, co
         // The next unit's Q may be written once both groups are done with this one. The widening warps are at most two
         // tiles ahead of the PV products, so they come back to these words only after three more units have begun.
         softmax_sync();
-        if (threadIdx.x < D) nan_first[threadIdx.x] = 0x7fffffff;
+        if (nans && threadIdx.x < D) nan_first[threadIdx.x] = *nan_any = 0x7fffffff;
     }
 }
 
@@ -964,7 +1007,7 @@ __global__ void __launch_bounds__(kThreads, 1)
     Start* st = reinterpret_cast<Start*>(smem + L::kStart);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    for (int i = tid; i < 4 * D; i += kThreads) reinterpret_cast<int*>(smem + L::kNan)[i] = 0x7fffffff;
+    for (int i = tid; i < 4 * D + 4; i += kThreads) reinterpret_cast<int*>(smem + L::kNan)[i] = 0x7fffffff;
     if (tid == 0) {
         x.words[1] = x.words[2] = x.words[3] = 0;
         for (int s = 0; s < kStages; ++s) {
@@ -1027,8 +1070,8 @@ __global__ void __launch_bounds__(kThreads, 1)
             r.len = q.len;
             r.head = st->h;
             r.m0 = st->m0;
-            r.kt0 = st->kt;
-            r.cost = unit_of(a, q, st->m0).cost;
+            r.off = st->off;
+            r.cost = unit_of(a, q, st->m0).cost();
         }
         r.error = x.words[1] ? DEV_TIMEOUT : st->bad != 0x7fffffff ? DEV_CHECK : x.words[2];
         r.info = st->bad != 0x7fffffff ? st->bad : (int)blockIdx.x;
