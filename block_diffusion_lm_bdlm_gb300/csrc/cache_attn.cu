@@ -41,10 +41,11 @@ __global__ void __launch_bounds__(kMergeThreads) cache_merge_kernel(const CacheA
     const ShareRec r = recs[c];
     const int two = r.rows * a.G - r.m0 > kUnitRows / 2;
     if (c >= r.C || tile_at(r.off, two) == 0) return;  // no share begins here, or it begins with its unit's first tile
-    const long long g0 = share_begin(r.W, r.C, c) - r.off;
+    auto begin = [&](int i) { return share_begin(r.per, r.more, i); };
+    const long long g0 = begin(c) - r.off;
     int c0 = c, c1 = c;  // boundaries inside the unit: shares c0 - 1 .. c1 hold its partials
-    while (c0 > 1 && share_begin(r.W, r.C, c0 - 1) > g0 && tile_at((int)(share_begin(r.W, r.C, c0 - 1) - g0), two) > 0) --c0;
-    while (c1 + 1 < r.C && share_begin(r.W, r.C, c1 + 1) < g0 + r.cost) ++c1;
+    while (c0 > 1 && begin(c0 - 1) > g0 && tile_at((int)(begin(c0 - 1) - g0), two) > 0) --c0;
+    while (c1 + 1 < r.C && begin(c1 + 1) < g0 + r.cost) ++c1;
     const int rows = imin(kUnitRows, r.rows * a.G - r.m0), parts = c1 - c0 + 2;
     const int lo = rows * (c - c0) / (c1 - c0 + 1), hi = rows * (c - c0 + 1) / (c1 - c0 + 1);
     const int R = slot_rows(a.total_rows, a.G);

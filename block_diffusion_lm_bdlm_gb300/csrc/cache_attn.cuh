@@ -8,7 +8,7 @@
 // cost is its tiles and kUnitTiles more for what it takes to begin and to end
 // it (query, results), twice that for a unit of two MMA tiles. All units'
 // costs, laid end to end (sequence, head, run), are cut into equal shares, one
-// per CTA: CTA c takes [W c / C, W (c + 1) / C). A share that begins or ends
+// per CTA (the first W % C of them one longer). A share that begins or ends
 // between the tiles of a unit leaves a partial result; at most two per CTA,
 // slot 2 c for a unit begun by an earlier CTA and slot 2 c + 1 for one that a
 // later CTA goes on with.
@@ -32,10 +32,10 @@ struct ShareRec {
     int row0, rows, pos0, len;  // the sequence (SeqRows) whose unit the share begins in
     int head, m0;               // kv head and first flat row of that unit
     int off, cost;              // where in the unit's cost the share begins, the unit's cost
-    long long W;                // cost of the whole call (0: nothing to do)
-    int C;                      // shares
+    long long per;              // share_begin's constants
+    int more, C;                // C: shares
     int error, info;
-    int pad[3];
+    int pad[2];
 };
 static_assert(sizeof(ShareRec) == 64, "share record is 64 bytes");
 
@@ -53,7 +53,8 @@ __device__ __forceinline__ float* slot_at(uint8_t* scratch, int slot, int rows, 
     return reinterpret_cast<float*>(scratch + sizeof(ShareRec) * kMaxCtas) + slot * slot_floats(rows, D);
 }
 
-__device__ __forceinline__ long long share_begin(long long W, int C, int c) { return W * c / C; }
+// Where share c of C begins; per = W / C, more = W % C.
+__device__ __forceinline__ long long share_begin(long long per, int more, int c) { return per * c + imin(c, more); }
 
 struct Unit {
     int last;   // last flat row + 1

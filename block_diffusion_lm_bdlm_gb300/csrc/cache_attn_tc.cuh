@@ -68,8 +68,7 @@ enum : int {
     B_P = 15,                                // 2 (t & 1) + group: p' in TMEM; for group 0 also: V in fp16
     B_PV = 19,                               // t & 1: the tile's products with V; frees the fp16 stage
     B_Q = 21,
-    B_SC = 22,                               // t % 6: scales written
-    B_COUNT = 28
+    B_COUNT = 22
 };
 
 template <int D>
@@ -93,8 +92,8 @@ static_assert(Smem<128>::kBytes <= 232448, "shared memory");
 
 // Where the CTA's share begins, found once by the whole CTA.
 struct Start {
-    long long W, left;
-    int C, s, h, m0, off, bad;
+    long long per, left;
+    int more, C, s, h, m0, off, bad;
 };
 static_assert(sizeof(Start) <= 64, "");
 
@@ -233,6 +232,7 @@ __device__ __forceinline__ void sts8(uint32_t addr, uint32_t a, uint32_t b) {
 __device__ __forceinline__ void lds16(uint32_t addr, uint32_t (&v)[4]) {
     asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(addr));
 }
+__device__ __forceinline__ void group_sync(int i) { asm volatile("bar.sync %0, 128;" ::"r"(2 + i) : "memory"); }
 __device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
 
 template <int N>
@@ -282,64 +282,118 @@ __device__ __forceinline__ long long cta_scan(long long x, long long* total, lon
     return before + v - x;
 }
 
-__device__ __forceinline__ long long head_cost(const CacheAttnArgs& a, const SeqRows& r) {
+// Cost of one head of sequence s of this lane; the units of long sequences are shared out over the warp.
+__device__ __forceinline__ long long head_cost(const CacheAttnArgs& a, const SeqRows& r, bool have) {
+    constexpr int kFew = 2;
+    const int units = have ? (r.rows * a.G + kUnitRows - 1) / kUnitRows : 0, lane = threadIdx.x & 31;
     long long c = 0;
-    for (int m0 = 0; m0 < r.rows * a.G; m0 += kUnitRows) c += unit_of(a, r, m0).cost();
+    if (units <= kFew)
+        for (int i = 0; i < units; ++i) c += unit_of(a, r, i * kUnitRows).cost();
+    for (unsigned todo = __ballot_sync(0xffffffffu, units > kFew); todo; todo &= todo - 1) {
+        const int src = __ffs(todo) - 1, n = __shfl_sync(0xffffffffu, units, src);
+        SeqRows q;
+        q.rows = __shfl_sync(0xffffffffu, r.rows, src);
+        q.len = __shfl_sync(0xffffffffu, r.len, src);
+        q.pos0 = __shfl_sync(0xffffffffu, r.pos0, src);
+        long long x = 0;
+        for (int i = lane; i < n; i += 32) x += unit_of(a, q, i * kUnitRows).cost();
+#pragma unroll
+        for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
+        if (lane == src) c = x;
+    }
     return c;
+}
+
+// The unit of sequence r that holds offset *off of a head's cost, by one whole warp; *off becomes the offset in it.
+__device__ __forceinline__ int find_unit(const CacheAttnArgs& a, const SeqRows& r, long long* off) {
+    const int lane = threadIdx.x & 31;
+    for (int i0 = 0;; i0 += 32) {
+        const int m0 = (i0 + lane) * kUnitRows;
+        const long long c = m0 < r.rows * a.G ? unit_of(a, r, m0).cost() : 0;
+        long long v = c;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const long long y = __shfl_up_sync(0xffffffffu, v, o);
+            if (lane >= o) v += y;
+        }
+        const unsigned hit = __ballot_sync(0xffffffffu, v > *off);
+        if (hit) {
+            const int k = __ffs(hit) - 1;
+            *off -= __shfl_sync(0xffffffffu, v - c, k);
+            return (i0 + k) * kUnitRows;
+        }
+        const long long all = __shfl_sync(0xffffffffu, v, 31);
+        if (all == 0) return 0;  // not reached: the offset lies within the head's cost
+        *off -= all;
+    }
 }
 
 __device__ __forceinline__ void find_start(const CacheAttnArgs& a, Start* st, long long* buf) {
     const int tid = threadIdx.x, n = a.c.n_seqs;
-    long long W = 0, before = 0, cost = 0, sum;
-    int bad = 0x7fffffff;
-    for (int s0 = 0; s0 < n; s0 += kThreads) {
-        const int s = s0 + tid;
-        cost = 0;
-        if (s < n) {
-            const SeqRows r = seq_rows(a.c, a.cu_rows, a.q_pos, a.total_rows, s);
-            if (!r.ok) bad = imin(bad, s);
-            else cost = head_cost(a, r) * a.c.Hk;
-        }
-        before = W + cta_scan(cost, &sum, buf);
-        W += sum;
-    }
-    if (tid == 0) st->bad = 0x7fffffff;
-    __syncthreads();
-    if (bad != 0x7fffffff) atomicMin(&st->bad, bad);
-    __syncthreads();
-    bad = st->bad;
-    if (bad != 0x7fffffff) W = 0;
-    long long C = W / kMinShare;
-    C = C < 1 ? 1 : C > (long long)gridDim.x ? (long long)gridDim.x : C;
-    const int c = (int)blockIdx.x;
-    const long long begin = c < C ? share_begin(W, (int)C, c) : 0, end = c < C ? share_begin(W, (int)C, c + 1) : 0;
     if (tid == 0) {
-        st->W = W;
-        st->C = (int)C;
-        st->left = end - begin;
+        st->left = 0;
+        st->bad = 0x7fffffff;
         st->s = st->h = st->m0 = st->off = 0;
     }
     __syncthreads();
-    if (end > begin) {
+    long long W = 0, before = 0, cost = 0, sum;
+    SeqRows r{};
+    for (int s0 = 0; s0 < n; s0 += kThreads) {
+        const int s = s0 + tid;
+        bool have = s < n;
+        if (have) {
+            r = seq_rows(a.c, a.cu_rows, a.q_pos, a.total_rows, s);
+            if (!r.ok) atomicMin(&st->bad, s);
+            have = r.ok;
+        }
+        cost = head_cost(a, r, have);
+        before = W + cta_scan(cost * a.c.Hk, &sum, buf);
+        W += sum;
+    }
+    // (the scan's barriers order the writes of st->bad)
+    const int c = (int)blockIdx.x;
+    if (st->bad != 0x7fffffff) W = 0;
+    const long long most = W / kMinShare;
+    const int C = most < 1 ? 1 : most > (long long)gridDim.x ? (int)gridDim.x : (int)most;
+    const long long per = W / C;
+    const int more = (int)(W - per * C);
+    const long long begin = share_begin(per, more, c), left = c < C ? share_begin(per, more, c + 1) - begin : 0;
+    if (tid == 0) {
+        st->per = per;
+        st->more = more;
+        st->C = C;
+        st->left = left;
+    }
+    if (left > 0) {
         long long base = 0;
         for (int s0 = 0; s0 < n; s0 += kThreads) {
             const int s = s0 + tid;
             if (n > kThreads) {  // more than one pass: the costs again
-                cost = s < n ? head_cost(a, seq_rows(a.c, a.cu_rows, a.q_pos, a.total_rows, s)) * a.c.Hk : 0;
-                before = base + cta_scan(cost, &sum, buf);
+                if (s < n) r = seq_rows(a.c, a.cu_rows, a.q_pos, a.total_rows, s);
+                cost = head_cost(a, r, s < n);
+                before = base + cta_scan(cost * a.c.Hk, &sum, buf);
                 base += sum;
             }
-            if (begin >= before && begin < before + cost) {
-                const SeqRows r = seq_rows(a.c, a.cu_rows, a.q_pos, a.total_rows, s);
-                const long long per = cost / a.c.Hk;
+            const bool mine = begin >= before && begin < before + cost * a.c.Hk;
+            const unsigned who = __ballot_sync(0xffffffffu, mine);
+            if (who) {  // one warp of the CTA
+                const int src = __ffs(who) - 1;
                 long long off = begin - before;
-                st->s = s;
-                st->h = (int)(off / per);
-                off %= per;
-                int m0 = 0;
-                for (int u; off >= (u = unit_of(a, r, m0).cost()); m0 += kUnitRows) off -= u;
-                st->m0 = m0;
-                st->off = (int)off;
+                int h = 0;
+                if (mine)
+                    for (; off >= cost; ++h) off -= cost;
+                SeqRows q;
+                q.rows = __shfl_sync(0xffffffffu, r.rows, src);
+                q.len = __shfl_sync(0xffffffffu, r.len, src);
+                q.pos0 = __shfl_sync(0xffffffffu, r.pos0, src);
+                off = __shfl_sync(0xffffffffu, off, src);
+                const int m0 = find_unit(a, q, &off);
+                if (mine) {
+                    st->s = s;
+                    st->h = h;
+                    st->m0 = m0;
+                    st->off = (int)off;
+                }
             }
         }
     }
@@ -428,12 +482,14 @@ __device__ __forceinline__ void produce(const Ctx& x, const CacheAttnArgs& a, co
                 sc[0] = b0.ks;
                 sc[8] = lvs;
             }
+            // The scales are written before the arrival on the keys' barrier, which the MMA warp awaits before it issues and
+            // commits the S that the softmax warps await: they read them behind it.
+            __syncwarp();
             if (lane == 0) {
                 tc::mbar_arrive_expect_tx(x.bar(B_KFULL, stage), bytes);
                 tc::mbar_arrive_expect_tx(x.bar(B_VFULL, stage), bytes);
             }
             __syncwarp();
-            if (lane == 0) tc::mbar_arrive(x.bar(B_SC, slot));
             if (load) {
                 const uint32_t off = stage * L::kT8 + (lane & 7) * 16 * D;
                 tc::tma_load_3d(x.sbase + L::kK + off, tk, x.bar(B_KFULL, stage), 0, 0, b0.id * a.c.Hk + b0.h);
@@ -632,66 +688,71 @@ __device__ __forceinline__ void issue(const Ctx& x, const CacheAttnArgs& a, cons
 template <int D>
 __device__ __forceinline__ void split_q(const Ctx& x, const CacheAttnArgs& a, const Seg& g) {
     using L = Smem<D>;
-    constexpr int PER = D / 8, ROWS = 256 / PER, BATCH = 128 / ROWS;
+    constexpr int PER = D / 8, ROWS = 256 / PER, BATCH = 4;
     const int chunk = threadIdx.x % PER, r0 = threadIdx.x / PER;
     const int n = g.last - g.m0, padded = (n + 31) & ~31;
     uint8_t* exps = x.smem + L::kQExp;
-    uint4 v[2][BATCH];  // every load before the first use
-    {
-        const int m = g.m0 + r0;
-        int row = m / a.G, rem = m - row * a.G;
-        const int dr = ROWS / a.G, dm = ROWS - dr * a.G;
-        const __nv_bfloat16* q = a.q + ((long long)g.row0 * a.H + g.h * a.G) * D + 8 * chunk;
+    const __nv_bfloat16* q = a.q + ((long long)g.row0 * a.H + g.h * a.G) * D + 8 * chunk;
+    const int dr = ROWS / a.G, dm = ROWS - dr * a.G;
+    int row = (g.m0 + r0) / a.G, rem = g.m0 + r0 - row * a.G, next = r0;
+    auto load = [&]() {
+        uint4 y = make_uint4(0, 0, 0, 0);
+        if (next < n) y = __ldg(reinterpret_cast<const uint4*>(q + ((long long)row * a.H + rem) * D));
+        next += ROWS;
+        row += dr;
+        rem += dm;
+        if (rem >= a.G) {
+            rem -= a.G;
+            ++row;
+        }
+        return y;
+    };
+    // four rows at a time, the next four in flight; the loop is not unrolled further, since most of what a first pass
+    // through this code costs is fetching the code
+    uint4 v[BATCH], w[BATCH];
 #pragma unroll
-        for (int i = 0; i < 2 * BATCH; ++i) {
-            uint4 y = make_uint4(0, 0, 0, 0);
-            if (i * ROWS + r0 < n) y = __ldg(reinterpret_cast<const uint4*>(q + ((long long)row * a.H + rem) * D));
-            v[i / BATCH][i % BATCH] = y;
-            row += dr;
-            rem += dm;
-            if (rem >= a.G) {
-                rem -= a.G;
-                ++row;
+    for (int i = 0; i < BATCH; ++i) v[i] = load();
+#pragma unroll 1
+    for (int b = 0; b < padded; b += BATCH * ROWS) {
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) w[i] = load();
+        uint32_t big[BATCH];
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i)
+            big[i] = __vmaxu2(__vmaxu2(v[i].x & 0x7fff7fffu, v[i].y & 0x7fff7fffu), __vmaxu2(v[i].z & 0x7fff7fffu, v[i].w & 0x7fff7fffu));
+#pragma unroll
+        for (int o = PER / 2; o; o >>= 1)
+#pragma unroll
+            for (int i = 0; i < BATCH; ++i) big[i] = __vmaxu2(big[i], __shfl_xor_sync(0xffffffffu, big[i], o));
+#pragma unroll
+        for (int i = 0; i < BATCH; ++i) {
+            const int r = b + i * ROWS + r0;
+            const uint32_t u[4] = {v[i].x, v[i].y, v[i].z, v[i].w};
+            const uint32_t top = (uint32_t)imax((int)(big[i] & 0xffffu), (int)(big[i] >> 16)) << 16;
+            const bool fine = top < 0x7f800000u;
+            const uint32_t sc = fine ? __float_as_uint(pow2_scale(__uint_as_float(top))) : 0x3f800000u;
+            const float inv = __uint_as_float(0x7f000000u - sc);  // 2^-k for 2^k, -126 <= k <= 120
+            uint32_t hi[2], lo[2];
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float f0 = __uint_as_float(u[2 * e] << 16) * inv, f1 = __uint_as_float(u[2 * e] & 0xffff0000u) * inv;
+                const float f2 = __uint_as_float(u[2 * e + 1] << 16) * inv, f3 = __uint_as_float(u[2 * e + 1] & 0xffff0000u) * inv;
+                hi[e] = narrow4(f0, f1, f2, f3);
+                uint32_t b0, b1;
+                widen4(hi[e], b0, b1);
+                const float2 h0 = __half22float2(*reinterpret_cast<const __half2*>(&b0));
+                const float2 h1 = __half22float2(*reinterpret_cast<const __half2*>(&b1));
+                lo[e] = narrow4(f0 - h0.x, f1 - h0.y, f2 - h1.x, f3 - h1.y);
+            }
+            if (r < padded) {
+                const uint32_t at = x.sbase + L::kQ + (r >> 7) * 2 * L::kT8 + swz8<D>(r & 127, chunk >> 1) + 8 * (chunk & 1);
+                sts8(at, hi[0], hi[1]);
+                sts8(at + L::kT8, lo[0], lo[1]);
+                if (chunk == 0) exps[r] = fine ? (uint8_t)(sc >> 23) : (uint8_t)255;
             }
         }
-    }
 #pragma unroll
-    for (int i = 0; i < 2 * BATCH; ++i) {
-        if (i * ROWS >= padded) break;  // the same for all threads
-        const int r = i * ROWS + r0;
-        const uint4 y = v[i / BATCH][i % BATCH];
-        const uint32_t u[4] = {y.x, y.y, y.z, y.w};
-        uint32_t big = 0;
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const uint32_t p = (u[e] << 16) & 0x7fffffffu, q = u[e] & 0x7fff0000u;
-            big = p > big ? p : big;
-            big = q > big ? q : big;
-        }
-#pragma unroll
-        for (int o = PER / 2; o; o >>= 1) {
-            const uint32_t z = __shfl_xor_sync(0xffffffffu, big, o);
-            big = z > big ? z : big;
-        }
-        const bool fine = big < 0x7f800000u;
-        const uint32_t sc = fine ? __float_as_uint(pow2_scale(__uint_as_float(big))) : 0x3f800000u;
-        const float inv = __uint_as_float(0x7f000000u - sc);  // 2^-k for 2^k, -126 <= k <= 120
-        uint32_t hi[2], lo[2];
-#pragma unroll
-        for (int e = 0; e < 2; ++e) {
-            const float f0 = __uint_as_float(u[2 * e] << 16) * inv, f1 = __uint_as_float(u[2 * e] & 0xffff0000u) * inv;
-            const float f2 = __uint_as_float(u[2 * e + 1] << 16) * inv, f3 = __uint_as_float(u[2 * e + 1] & 0xffff0000u) * inv;
-            hi[e] = narrow4(f0, f1, f2, f3);
-            uint32_t b0, b1;
-            widen4(hi[e], b0, b1);
-            const float2 h0 = __half22float2(*reinterpret_cast<const __half2*>(&b0));
-            const float2 h1 = __half22float2(*reinterpret_cast<const __half2*>(&b1));
-            lo[e] = narrow4(f0 - h0.x, f1 - h0.y, f2 - h1.x, f3 - h1.y);
-        }
-        const uint32_t at = x.sbase + L::kQ + (r >> 7) * 2 * L::kT8 + swz8<D>(r & 127, chunk >> 1) + 8 * (chunk & 1);
-        sts8(at, hi[0], hi[1]);
-        sts8(at + L::kT8, lo[0], lo[1]);
-        if (chunk == 0) exps[r] = fine ? (uint8_t)(sc >> 23) : (uint8_t)255;
+        for (int i = 0; i < BATCH; ++i) v[i] = w[i];
     }
 }
 
@@ -721,9 +782,9 @@ __device__ __forceinline__ void softmax_part(uint32_t tC, uint32_t tO, const flo
         tc::tmem_st_wait();
     }
     uint32_t r[Q][32];
+    float ks[NG], lv[NG];
 #pragma unroll
     for (int q = 0; q < Q; ++q) tc::tmem_ld32(tC + 32 * q, r[q]);
-    float ks[NG], lv[NG];
 #pragma unroll
     for (int g = 0; g < NG; ++g) {
         ks[g] = cs * sc[g * (GK / 16)];
@@ -827,27 +888,67 @@ __device__ __forceinline__ void softmax_part(uint32_t tC, uint32_t tO, const flo
     __syncwarp();
 }
 
-// Writes 32 columns of a row: normalised values v.
+// Where the results of a unit's flat rows go.
+struct Out {
+    float* slot;  // partial: the share's slot (nullptr: the rows are complete)
+    int slot_r;   // its rows
+};
+
+// Writes 32 columns (from 32 q on) of flat row m: into the slot; as fp32 to o; or as bf16 into the staging tile at
+// `stage`, whose row `row` is this one.
 template <int D>
-__device__ __forceinline__ void store_cols(const CacheAttnArgs& a, const Seg& g, int m, int q, const float (&v)[32],
-                                           float* slot, int slot_r) {
-    if (slot) {
-        float4* dst = reinterpret_cast<float4*>(slot) + (long long)(8 * q) * slot_r + (m - g.m0);
+__device__ __forceinline__ void put_cols(const CacheAttnArgs& a, const Seg& g, const Out& out, int m, int row, uint32_t stage,
+                                         int q, const float (&v)[32]) {
+    if (out.slot) {
+        if (m < g.last) {
+            float4* dst = reinterpret_cast<float4*>(out.slot) + (8 * q) * out.slot_r + (m - g.m0);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) dst[(long long)e * slot_r] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
-        return;
-    }
-    const long long at = ((long long)(g.row0 + m / a.G) * a.H + g.h * a.G + m % a.G) * D + 32 * q;
-    if (a.o_f32) {
-        float4* dst = reinterpret_cast<float4*>(a.o_f32 + at);
+            for (int e = 0; e < 8; ++e) dst[e * out.slot_r] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+        }
+    } else if (a.o_f32) {
+        if (m < g.last) {
+            float4* dst = reinterpret_cast<float4*>(a.o_f32 + ((long long)(g.row0 + m / a.G) * a.H + g.h * a.G + m % a.G) * D + 32 * q);
 #pragma unroll
-        for (int e = 0; e < 8; ++e) dst[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+            for (int e = 0; e < 8; ++e) dst[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+        }
     } else {
-        uint4* dst = reinterpret_cast<uint4*>(a.o + at);
 #pragma unroll
         for (int e = 0; e < 4; ++e)
-            dst[e] = make_uint4(pack_bf2(v[8 * e], v[8 * e + 1]), pack_bf2(v[8 * e + 2], v[8 * e + 3]),
-                                pack_bf2(v[8 * e + 4], v[8 * e + 5]), pack_bf2(v[8 * e + 6], v[8 * e + 7]));
+            sts16(stage + row * 2 * D + (((4 * q + e) ^ (row & 7)) << 4), pack_bf2(v[8 * e], v[8 * e + 1]),
+                  pack_bf2(v[8 * e + 2], v[8 * e + 3]), pack_bf2(v[8 * e + 4], v[8 * e + 5]), pack_bf2(v[8 * e + 6], v[8 * e + 7]));
+    }
+}
+
+// Copies rows m_from .. of the staging tile to o, by THREADS threads of which this is number `id`: whole rows, so that
+// the stores of a warp are runs of 2 D bytes.
+template <int D, int THREADS>
+__device__ __forceinline__ void put_rows(const CacheAttnArgs& a, const Seg& g, int m_from, uint32_t stage, int id) {
+    constexpr int PER = D / 8, ROWS = THREADS / PER;
+    const int chunk = id % PER, dr = ROWS / a.G, dm = ROWS - dr * a.G;
+    int r = id / PER, row = (m_from + r) / a.G, rem = m_from + r - row * a.G;
+    const int n = imin(128, g.last - m_from);
+    __nv_bfloat16* o = a.o + ((long long)g.row0 * a.H + g.h * a.G) * D + 8 * chunk;
+#pragma unroll 4
+    for (; r < n; r += ROWS) {
+        uint32_t v[4];
+        lds16(stage + r * 2 * D + ((chunk ^ (r & 7)) << 4), v);
+        *reinterpret_cast<uint4*>(o + ((long long)row * a.H + rem) * D) = make_uint4(v[0], v[1], v[2], v[3]);
+        row += dr;
+        rem += dm;
+        if (rem >= a.G) {
+            rem -= a.G;
+            ++row;
+        }
+    }
+}
+
+__device__ __forceinline__ void put_lse(const CacheAttnArgs& a, const Seg& g, const Out& out, int D, int m, float l2) {
+    if (m >= g.last) return;
+    if (out.slot) {
+        out.slot[(long long)out.slot_r * D + m - g.m0] = l2;
+    } else {
+        const int row = m / a.G;
+        a.lse[(long long)(g.h * a.G + m - row * a.G) * a.total_rows + g.row0 + row] = l2 * 0.69314718055994531f;
     }
 }
 
@@ -856,23 +957,35 @@ __device__ __forceinline__ void softmax(const Ctx& x, const CacheAttnArgs& a, co
     using L = Smem<D>;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, i = warp >> 2, row = threadIdx.x & 127;
     const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
-    const uint32_t tS = x.tmem + 128 * i + lane_base, tO = x.tmem + 256 + D * i + lane_base;
-    const int slot_r = slot_rows(a.total_rows, a.G);
+    const uint32_t tS = x.tmem + lane_base, tO = x.tmem + 256 + D * i + lane_base, tO1 = x.tmem + 256 + D * (i ^ 1) + lane_base;
+    const float* scales = reinterpret_cast<const float*>(x.smem + L::kScale);
     Walk w;
     w.begin(a, st);
     Seg g;
-    uint32_t t_base = 0, seg = 0, s0_phases = 0;  // s0_phases: bit of each B_S0 stage's next phase
+    uint32_t t = 0, seg = 0, s0_phases = 0;  // s0_phases: bit of each B_S0 stage's next phase
     bool ok = true;  // warp-uniform; the loops run on without waiting once it is false
+    auto wait = [&](int base, int n, uint32_t parity) {
+        if (ok) ok = __all_sync(0xffffffffu, x.wait(base, n, parity));
+        tc::tc_fence_after();
+    };
     while (w.next(a, &g)) {
         const int nt = g.tiles();
         const int m = g.m0 + (g.two ? 128 * i : 0) + row;  // this thread's flat row
-        const bool live = m < g.last;
-        float* slot = g.whole ? nullptr : slot_at(a.scratch, 2 * (int)blockIdx.x + (g.kt0 > 0 ? 0 : 1), slot_r, D);
+        Out out;
+        out.slot_r = slot_rows(a.total_rows, a.G);
+        out.slot = g.whole ? nullptr : slot_at(a.scratch, 2 * (int)blockIdx.x + (g.kt0 > 0 ? 0 : 1), out.slot_r, D);
         if (nt == 0) {  // rows without keys
-            if (live && (g.two || i == 0)) {
-                const float v[32] = {};
-                for (int q = 0; q < D / 32; ++q) store_cols<D>(a, g, m, q, v, nullptr, 0);
-                a.lse[(long long)(g.h * a.G + m % a.G) * a.total_rows + g.row0 + m / a.G] = -INFINITY;
+            if (m < g.last && (g.two || i == 0)) {
+                const long long at = ((long long)(g.row0 + m / a.G) * a.H + g.h * a.G + m % a.G) * D;
+                for (int c = 0; c < D; c += 8) {
+                    if (a.o_f32) {
+                        *reinterpret_cast<float4*>(a.o_f32 + at + c) = make_float4(0.f, 0.f, 0.f, 0.f);
+                        *reinterpret_cast<float4*>(a.o_f32 + at + c + 4) = make_float4(0.f, 0.f, 0.f, 0.f);
+                    } else {
+                        *reinterpret_cast<uint4*>(a.o + at + c) = make_uint4(0, 0, 0, 0);
+                    }
+                }
+                put_lse(a, g, out, D, m, -INFINITY);
             }
             continue;
         }
@@ -885,77 +998,89 @@ __device__ __forceinline__ void softmax(const Ctx& x, const CacheAttnArgs& a, co
         // the factor that turns the tensor core's q . k8 into base-2 scores; a row that is not finite becomes NaN, and no other
         const int qe = x.smem[L::kQExp + (g.two ? 128 * i : 0) + row];
         const float cs = qe == 255 ? NAN : a.scale_log2 * __uint_as_float((uint32_t)qe << 23);
-
-        const int end = live ? key_end(g.len, a.block, g.pos0 + m / a.G) : 0;
-        const int full_end = __shfl_sync(0xffffffffu, end, 0);  // the warp's first row sees the fewest keys
-        const bool warp_live = __shfl_sync(0xffffffffu, (int)live, 0);
+        const int end = m < g.last ? key_end(g.len, a.block, g.pos0 + m / a.G) : 0;
+        const bool warp_live = __shfl_sync(0xffffffffu, (int)(m < g.last), 0);
+        // keys of a tile that this row sees, and that the warp's first row (which sees the fewest) does
+        int sees = end - g.kt0 * kTileKeys - (g.two ? 0 : 64 * i), all_see = __shfl_sync(0xffffffffu, sees, 0);
         float mm = -INFINITY, mo = -INFINITY, l = 0.f;
-        for (int j = 0; j < nt; ++j) {
-            const uint32_t t = t_base + j, slot_no = t % kScaleSlots, stage = t % kStages;
-            const uint32_t buf = g.two ? (uint32_t)i : t & 1;
-            if (ok) {
-                const bool got = (g.two && i == 0 ? x.wait(B_S0, stage, (s0_phases >> stage) & 1) : x.wait(B_S1, stage, (t / kStages) & 1)) &&
-                                 x.wait(B_SC, slot_no, (t / kScaleSlots) & 1);
-                ok = __all_sync(0xffffffffu, got);
-            }
-            if (g.two) s0_phases ^= 1u << stage;
-            tc::tc_fence_after();
-            const int k0 = (g.kt0 + j) * kTileKeys;
-            const float* sc = reinterpret_cast<const float*>(x.smem + L::kScale) + slot_no * 16;
-            if (warp_live && ok) {
-                if (g.two) {
-                    // S of a tile is issued behind the PV of the one before, so O is settled
-                    softmax_part<D, NG, 128>(tS, tO, sc, cs, end - k0, k0 + kTileKeys <= full_end, j == 0, mm, mo, l, [] {});
+        uint32_t stage = t % kStages, ph = (t / kStages) & 1, slot = t % kScaleSlots;
+        if (g.two) {
+            for (int j = 0; j < nt; ++j, ++t) {
+                if (i == 0) {
+                    wait(B_S0, stage, (s0_phases >> stage) & 1);
                 } else {
-                    const int h0 = k0 + 64 * i;
-                    softmax_part<D, (NG > 1 ? NG / 2 : 1), 64>(x.tmem + 128 * buf + 64 * i + lane_base, tO, sc + 4 * i, cs, end - h0,
-                                                               h0 + 64 <= full_end, j == 0, mm, mo, l, [&] {
-                                                                   ok = __all_sync(0xffffffffu, x.wait(B_PV, (t - 1) & 1, ((t - 1) >> 1) & 1));
-                                                                   tc::tc_fence_after();
-                                                               });
+                    wait(B_S1, stage, ph);
+                }
+                // S of a tile is issued behind the PV of the one before, so O is settled
+                if (warp_live && ok)
+                    softmax_part<D, NG, 128>(tS + 128 * i, tO, scales + 16 * slot, cs, sees, all_see >= 128, j == 0, mm, mo, l, [] {});
+                if (lane == 0) tc::mbar_arrive(x.bar(B_P, 2 * (t & 1) + i));
+                s0_phases ^= 1u << stage;
+                sees -= kTileKeys;
+                all_see -= kTileKeys;
+                slot = slot + 1 == kScaleSlots ? 0 : slot + 1;
+                if (++stage == kStages) {
+                    stage = 0;
+                    ph ^= 1;
                 }
             }
-            if (lane == 0) tc::mbar_arrive(x.bar(B_P, 2 * (t & 1) + i));
+        } else {
+            for (int j = 0; j < nt; ++j, ++t) {
+                wait(B_S1, stage, ph);
+                if (warp_live && ok)
+                    softmax_part<D, (NG > 1 ? NG / 2 : 1), 64>(tS + 128 * (t & 1) + 64 * i, tO, scales + 16 * slot + 4 * i, cs, sees,
+                                                               all_see >= 64, j == 0, mm, mo, l,
+                                                               [&] { wait(B_PV, (t - 1) & 1, ((t - 1) >> 1) & 1); });
+                if (lane == 0) tc::mbar_arrive(x.bar(B_P, 2 * (t & 1) + i));
+                sees -= kTileKeys;
+                all_see -= kTileKeys;
+                slot = slot + 1 == kScaleSlots ? 0 : slot + 1;
+                if (++stage == kStages) {
+                    stage = 0;
+                    ph ^= 1;
+                }
+            }
         }
-        t_base += nt;
-        // every product of the unit is done
-        if (ok) ok = __all_sync(0xffffffffu, x.wait(B_PV, (t_base - 1) & 1, ((t_base - 1) >> 1) & 1));
-        tc::tc_fence_after();
+        wait(B_PV, (t - 1) & 1, ((t - 1) >> 1) & 1);  // every product of the unit is done
         int* nan_first = reinterpret_cast<int*>(x.smem + L::kNan) + (seg & 3) * D;
         int* nan_any = reinterpret_cast<int*>(x.smem + L::kNanAny) + (seg & 3);
         const bool nans = *nan_any < g.end;
         ++seg;
+        const bool staged = !out.slot && !a.o_f32;
         if (g.two) {
-            // o = O 2^(mo - m) / l
+            // o = O 2^(mo - m) / l; the S products no longer need the group's Q tile, which takes the rows
             const bool some = l != 0.f;  // NaN counts as something
             const float f = some ? ex2f(mo - mm) / l : 0.f;
-            const float l2 = some ? mm + __log2f(l) : -INFINITY;
+            const uint32_t tile = x.sbase + L::kQ + i * 2 * L::kT8;
+#pragma unroll 1
             for (int q = 0; q < D / 32; ++q) {
                 uint32_t o[32];
                 tc::tmem_ld32(tO + 32 * q, o);
                 tc::tmem_ld_wait();
                 float v[32];
 #pragma unroll
-                for (int e = 0; e < 32; ++e) {
-                    v[e] = some ? __uint_as_float(o[e]) * f : 0.f;
-                    if (nans && nan_first[32 * q + e] < end) v[e] = NAN;
-                }
-                if (live) store_cols<D>(a, g, m, q, v, slot, slot_r);
+                for (int e = 0; e < 32; ++e) v[e] = some ? __uint_as_float(o[e]) * f : 0.f;
+                if (nans)
+#pragma unroll
+                    for (int e = 0; e < 32; ++e)
+                        if (nan_first[32 * q + e] < end) v[e] = NAN;
+                put_cols<D>(a, g, out, m, row, tile, q, v);
             }
-            if (live) {
-                if (slot) slot[(long long)slot_r * D + m - g.m0] = l2;
-                else a.lse[(long long)(g.h * a.G + m % a.G) * a.total_rows + g.row0 + m / a.G] = l2 * 0.69314718055994531f;
-            }
+            put_lse(a, g, out, D, m, some ? mm + __log2f(l) : -INFINITY);
             tc::tc_fence_before();
+            if (staged) {
+                group_sync(i);
+                put_rows<D, 128>(a, g, g.m0 + 128 * i, tile, row);
+            }
         } else {
-            // the groups exchange their sums through their S columns (same lanes) and each writes half of the columns
-            tmem_st4(tS, __float_as_uint(mm), __float_as_uint(mo), __float_as_uint(l), 0u);
+            // the groups exchange their sums through S columns (same lanes) and each writes half of the columns
+            tmem_st4(tS + 128 * i, __float_as_uint(mm), __float_as_uint(mo), __float_as_uint(l), 0u);
             tc::tmem_st_wait();
             tc::tc_fence_before();
             softmax_sync();
             tc::tc_fence_after();
             uint32_t ot[4];
-            tmem_ld4(x.tmem + 128 * (i ^ 1) + lane_base, ot);
+            tmem_ld4(tS + 128 * (i ^ 1), ot);
             tc::tmem_ld_wait();
             const float m1 = __uint_as_float(ot[0]), mo1 = __uint_as_float(ot[1]), l1 = __uint_as_float(ot[2]);
             const float mj = fmaxf(mm, m1), moj = fmaxf(mo, mo1);
@@ -965,26 +1090,30 @@ __device__ __forceinline__ void softmax(const Ctx& x, const CacheAttnArgs& a, co
             // this group's and the other's factor; one without keys that the row sees adds nothing
             const bool use0 = l != 0.f, use1 = l1 != 0.f;
             const float f0 = use0 ? f * ex2f(mo - moj) : 0.f, f1 = use1 ? f * ex2f(mo1 - moj) : 0.f;
-            const float l2 = some ? mj + __log2f(lj) : -INFINITY;
-            const uint32_t tO1 = x.tmem + 256 + D * (i ^ 1) + lane_base;
-            for (int q = i * (D / 64); q < (i + 1) * (D / 64); ++q) {
-                uint32_t o[32], o1[32];
-                tc::tmem_ld32(tO + 32 * q, o);
-                tc::tmem_ld32(tO1 + 32 * q, o1);
-                tc::tmem_ld_wait();
-                float v[32];
+            const uint32_t tile = x.sbase + L::kQ + 2 * L::kT8;
+            if (warp_live)
+#pragma unroll 1
+                for (int q = i * (D / 64); q < (i + 1) * (D / 64); ++q) {
+                    uint32_t o[32], o1[32];
+                    tc::tmem_ld32(tO + 32 * q, o);
+                    tc::tmem_ld32(tO1 + 32 * q, o1);
+                    tc::tmem_ld_wait();
+                    float v[32];
 #pragma unroll
-                for (int e = 0; e < 32; ++e) {
-                    v[e] = (use0 ? __uint_as_float(o[e]) * f0 : 0.f) + (use1 ? __uint_as_float(o1[e]) * f1 : 0.f);
-                    if (nans && nan_first[32 * q + e] < end) v[e] = NAN;
+                    for (int e = 0; e < 32; ++e)
+                        v[e] = (use0 ? __uint_as_float(o[e]) * f0 : 0.f) + (use1 ? __uint_as_float(o1[e]) * f1 : 0.f);
+                    if (nans)
+#pragma unroll
+                        for (int e = 0; e < 32; ++e)
+                            if (nan_first[32 * q + e] < end) v[e] = NAN;
+                    put_cols<D>(a, g, out, m, row, tile, q, v);
                 }
-                if (live) store_cols<D>(a, g, m, q, v, slot, slot_r);
-            }
-            if (live && i == 0) {
-                if (slot) slot[(long long)slot_r * D + m - g.m0] = l2;
-                else a.lse[(long long)(g.h * a.G + m % a.G) * a.total_rows + g.row0 + m / a.G] = l2 * 0.69314718055994531f;
-            }
+            if (i == 0) put_lse(a, g, out, D, m, some ? mj + __log2f(lj) : -INFINITY);
             tc::tc_fence_before();
+            if (staged) {
+                softmax_sync();
+                put_rows<D, 256>(a, g, g.m0, tile, threadIdx.x);
+            }
         }
         // The next unit's Q may be written once both groups are done with this one. The widening warps are at most two
         // tiles ahead of the PV products, so they come back to these words only after three more units have begun.
@@ -1023,7 +1152,6 @@ __global__ void __launch_bounds__(kThreads, 1)
             tc::mbar_init(x.bar(B_PV, s), 1);
         }
         tc::mbar_init(x.bar(B_Q, 0), 8);
-        for (int s = 0; s < kScaleSlots; ++s) tc::mbar_init(x.bar(B_SC, s), 1);
         tc::fence_barrier_init();
     }
     if (warp == 9) {
@@ -1060,7 +1188,8 @@ __global__ void __launch_bounds__(kThreads, 1)
     }
     if (tid == 0) {
         ShareRec r{};
-        r.W = st->W;
+        r.per = st->per;
+        r.more = st->more;
         r.C = st->C;
         if (st->left > 0) {
             const SeqRows q = seq_rows(a.c, a.cu_rows, a.q_pos, a.total_rows, st->s);
