@@ -21,19 +21,21 @@
 // for up to 128 flat rows, so these calls are bound by memory, and calls with
 // 256 and more flat rows by the tensor pipe.
 //
-// Roles (512 threads, one CTA per SM, each role walks the CTA's share alone):
-//   warps 0-3, 4-7  softmax groups 0 and 1; one TMEM lane = one flat row. They
-//                   also split Q into its two terms, and write the results
-//   warp 8          page table, scales and TMA loads of K and V pages (3 stages)
-//   warp 9          issues the MMAs (one thread), owns TMEM
-//   warps 10-11     spare
-//   warps 12-15     widen V from e4m3 to fp16 (2 stages), zero the rows behind
-//                   the last key and take out masked NaN
-// A unit of up to 128 flat rows is one MMA tile: group 0 takes the first 64
-// keys of every key tile, group 1 the others, each with sums and an O of its
-// own that are joined at the end. Two S buffers take turns, so that a tile's
-// softmax (64 keys per thread) runs under the MMAs of its neighbours. A larger
-// unit is two MMA tiles, one for each group, over the same keys.
+// Roles (640 threads, one CTA per SM, each role walks the CTA's share alone):
+//   warps 0-15   softmax, in four groups (i, h); one TMEM lane = one flat row.
+//                They also split Q into its two terms, widen V from e4m3 to
+//                fp16 (zero the rows behind the last key, take out masked NaN)
+//                and write the results
+//   warp 16      page table, scales and TMA loads of K (3 stages) and V (2)
+//   warp 17      issues the MMAs (one elected lane), owns TMEM
+//   warps 18-19  spare
+// A unit of up to 128 flat rows is one MMA tile: its products with the values
+// of keys 64 i .. of every tile add up in O_i, and group (i, h) takes the 32
+// keys from 64 i + 32 h on. Two S buffers take turns, so that a tile's softmax
+// runs under the MMAs of its neighbours. A larger unit is two MMA tiles over
+// the same keys, tile i with O_i, and group (i, h) takes keys 64 h .. of it.
+// Either way two threads share a row of an O: they keep one offset mo for it,
+// and agree before every tile's p' is passed on whether it may stay.
 // TMEM (512 columns): S0 | S1 | O0 | O1; p' overwrites S as fp16.
 // MMAs of one thread run in issue order, so the next S of a buffer is issued
 // right behind the PV that reads the p' it overwrites.
@@ -50,23 +52,27 @@
 namespace bdlm {
 namespace cattn {
 
-constexpr int kThreads = 512;
-// 8 softmax warps and 8 others at 128 registers each, redistributed
-constexpr int kRegsSoftmax = 176;
-constexpr int kRegsOther = 80;
-static_assert(8 * kRegsSoftmax + 8 * kRegsOther <= 16 * 128, "registers");
+constexpr int kThreads = 640;
+constexpr int kSoftmax = 512;
+// 20 warps at 96 registers each, redistributed. What a role keeps beyond its registers would be spilled to an L1 that
+// shared memory leaves next to no room.
+constexpr int kRegsSoftmax = 104;
+constexpr int kRegsOther = 64;
+static_assert(16 * kRegsSoftmax + 4 * kRegsOther <= 20 * 96, "registers");
 constexpr int kTmemCols = 512;
-constexpr int kStages = 3;
+constexpr int kStages = 3;  // of K; V has two as e4m3 and two as fp16
 constexpr int kScaleSlots = 6;
 constexpr uint64_t kTimeoutNs = 2000000000ull;
 
 // Barriers. Tiles are numbered through the CTA's share; t is a tile's number.
 enum : int {
-    B_KFULL = 0, B_VFULL = 3, B_VEMPTY = 6,  // t % 3
-    B_S0 = 9,                                // t % 3: group 0's S of a unit of two MMA tiles
-    B_S1 = 12,                               // t % 3: the tile's last S; it also frees the K stage
-    B_P = 15,                                // 2 (t & 1) + group: p' in TMEM; for group 0 also: V in fp16
-    B_PV = 19,                               // t & 1: the tile's products with V; frees the fp16 stage
+    B_KFULL = 0,                // t % 3
+    B_VFULL = 3, B_VEMPTY = 5,  // t & 1
+    B_S0 = 7,                   // t % 3: the first S of a unit of two MMA tiles
+    B_S1 = 10,                  // t % 3: the tile's last S; it also frees the K stage
+    B_P = 13,                   // 2 (t & 1) + i: p' for O_i in TMEM; in a unit of one MMA tile also V for O_i in fp16
+    B_W = 17,                   // t & 1: V in fp16
+    B_PV = 19,                  // t & 1: the tile's products with V; frees the fp16 stage
     B_Q = 21,
     B_COUNT = 22
 };
@@ -76,17 +82,19 @@ struct Smem {
     static constexpr int kT8 = 128 * D;        // bytes of a 128-row e4m3 tile
     static constexpr int kQ = 0;               // group 0 hi, lo, group 1 hi, lo
     static constexpr int kW = 4 * kT8;         // fp16 values, 2 stages of 2 * kT8
-    static constexpr int kK = 8 * kT8;         // 3 stages
-    static constexpr int kV = kK + kStages * kT8;
-    static constexpr int kMisc = kV + kStages * kT8;
+    static constexpr int kK = 8 * kT8;
+    static constexpr int kV = kK + kStages * kT8;  // 2 stages
+    static constexpr int kMisc = kV + 2 * kT8;
     static constexpr int kScale = kMisc;                          // float [slots][16]: ks, log2 vs of 16-key groups
-    static constexpr int kNan = kScale + kScaleSlots * 64;        // int [4][D]: first key whose value is NaN, per column
-    static constexpr int kNanAny = kNan + 4 * D * 4;              // int [4]: first key with a NaN in any column
-    static constexpr int kBar = kNanAny + 16;
+    static constexpr int kNan = kScale + kScaleSlots * 64;        // int [D]: first key whose value is NaN, per column
+    static constexpr int kNanAny = kNan + D * 4;                  // int: first key with a NaN in any column
+    static constexpr int kMax = kNanAny + 16;                     // float [8 pairs][2][32]: maxima that partners exchange
+    static constexpr int kBar = kMax + 2048;
     static constexpr int kWords = kBar + B_COUNT * 8;             // tmem, abort, error, info
     static constexpr int kStart = kWords + 16;                    // Start
     static constexpr int kQExp = kStart + 64;                     // uint8 [256]: exponent of the rows' scale
-    static constexpr int kBytes = kQExp + kUnitRows;
+    static constexpr int kPlace = kQExp + kUnitRows;              // Place of each warp
+    static constexpr int kBytes = kPlace + (kThreads / 32) * 128;
 };
 static_assert(Smem<128>::kBytes <= 232448, "shared memory");
 
@@ -106,47 +114,66 @@ struct Seg {
     __device__ __forceinline__ int tiles() const { return end ? kt1 - kt0 : 0; }
 };
 
-struct Walk {
+struct Place {
     SeqRows r;
     Unit u;
     int s, h, m0, off;
     long long left;
-    __device__ __forceinline__ void begin(const CacheAttnArgs& a, const Start& st) {
-        s = st.s;
-        h = st.h;
-        m0 = st.m0;
-        off = st.off;
-        left = st.left;
-        if (left > 0) {
-            r = seq_rows(a.c, a.cu_rows, a.q_pos, a.total_rows, s);
-            u = unit_of(a, r, m0);
-        }
-    }
-    __device__ __forceinline__ bool next(const CacheAttnArgs& a, Seg* g) {
-        while (left > 0) {
-            const int c = u.cost(), n = left < c - off ? (int)left : c - off;
-            const int kt0 = tile_at(off, u.two), kt1 = tile_at(off + n, u.two);
-            *g = Seg{r.row0, r.pos0, r.len, s, h, m0, u.last, u.end, kt0, kt1, u.two != 0, kt0 == 0 && kt1 == u.tiles};
-            left -= n;
-            off += n;
-            if (left > 0) {  // the unit is done
-                off = 0;
-                m0 += kUnitRows;
-                if (m0 >= r.rows * a.G) {
-                    m0 = 0;
-                    if (++h == a.c.Hk) {
-                        h = 0;
-                        do r = seq_rows(a.c, a.cu_rows, a.q_pos, a.total_rows, ++s);
-                        while (r.rows == 0);
-                    }
-                }
-                u = unit_of(a, r, m0);
-            }
-            if (kt1 > kt0) return true;
-        }
-        return false;
-    }
+    Seg g;    // the present run
+    int all;  // keys that every row of its unit sees
 };
+static_assert(sizeof(Place) <= 128, "");
+
+// Both are called by whole warps; the warp's lanes write the same values.
+__device__ __forceinline__ void begin_share(const CacheAttnArgs& a, const Start& st, Place* p) {
+    p->s = st.s;
+    p->h = st.h;
+    p->m0 = st.m0;
+    p->off = st.off;
+    p->left = st.left;
+    if (st.left > 0) {
+        p->r = seq_rows(a.c, a.cu_rows, a.q_pos, a.total_rows, st.s);
+        p->u = unit_of(a, p->r, st.m0);
+    }
+    __syncwarp();
+}
+// The next run of tiles, into p->g; false behind the last.
+__device__ __forceinline__ bool next_run(const CacheAttnArgs& a, Place* p) {
+    __syncwarp();
+    long long left = p->left;
+    bool found = false;
+    while (left > 0 && !found) {
+        const Unit u = p->u;
+        const int off = p->off, c = u.cost(), n = left < c - off ? (int)left : c - off;
+        const int kt0 = tile_at(off, u.two), kt1 = tile_at(off + n, u.two);
+        int s = p->s, h = p->h, m0 = p->m0;
+        SeqRows r = p->r;
+        found = kt1 > kt0;
+        __syncwarp();
+        if (found) p->g = Seg{r.row0, r.pos0, r.len, s, h, m0, u.last, u.end, kt0, kt1, u.two != 0, kt0 == 0 && kt1 == u.tiles};
+        left -= n;
+        if (left > 0) {  // the unit is done
+            m0 += kUnitRows;
+            if (m0 >= r.rows * a.G) {
+                m0 = 0;
+                if (++h == a.c.Hk) {
+                    h = 0;
+                    do r = seq_rows(a.c, a.cu_rows, a.q_pos, a.total_rows, ++s);
+                    while (r.rows == 0);
+                    p->r = r;
+                    p->s = s;
+                }
+                p->h = h;
+            }
+            p->m0 = m0;
+            p->off = 0;
+            p->u = unit_of(a, r, m0);
+        }
+        p->left = left;
+        __syncwarp();
+    }
+    return found;
+}
 
 __device__ __forceinline__ float ex2f(float x) {
     float y;
@@ -232,8 +259,19 @@ __device__ __forceinline__ void sts8(uint32_t addr, uint32_t a, uint32_t b) {
 __device__ __forceinline__ void lds16(uint32_t addr, uint32_t (&v)[4]) {
     asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(addr));
 }
-__device__ __forceinline__ void group_sync(int i) { asm volatile("bar.sync %0, 128;" ::"r"(2 + i) : "memory"); }
-__device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+__device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 512;" ::: "memory"); }
+__device__ __forceinline__ void tile_sync(int i) { asm volatile("bar.sync %0, 256;" ::"r"(2 + i) : "memory"); }
+// the two warps that share rows of an O
+__device__ __forceinline__ void pair_sync(int pair) { asm volatile("bar.sync %0, 64;" ::"r"(4 + pair) : "memory"); }
+__device__ __forceinline__ bool pair_any(int pair, bool p) {
+    uint32_t r;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, %2, 64, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
+        : "=r"(r)
+        : "r"((uint32_t)p), "r"(4 + pair)
+        : "memory");
+    return r != 0;
+}
 
 template <int N>
 struct Const {
@@ -245,17 +283,22 @@ __device__ __forceinline__ bool elect_one() {
     return p != 0;
 }
 
+extern __shared__ __align__(1024) uint8_t g_smem[];
+__device__ __forceinline__ uint32_t sbase() { return tc::smem_addr(g_smem); }
+
+template <int D>
 struct Ctx {
-    uint8_t* smem;
-    uint32_t sbase, tmem;
-    int* words;  // tmem, abort, error, info
-    __device__ __forceinline__ uint32_t bar(int base, int i) const { return bars + 8 * (base + i); }
-    uint32_t bars;
-    __device__ __forceinline__ volatile int* abort() const { return words + 1; }
+    using L = Smem<D>;
+    uint32_t tmem;
+    __device__ __forceinline__ uint32_t bar(int base, int i) const { return sbase() + L::kBar + 8 * (base + i); }
+    static __device__ __forceinline__ int* words() { return reinterpret_cast<int*>(g_smem + L::kWords); }  // tmem, abort, error
     // bounded wait; false once any role has given up
     __device__ __forceinline__ bool wait(int base, int i, uint32_t parity) const {
-        return tc::mbar_wait(bar(base, i), parity, abort(), kTimeoutNs);
+        return tc::mbar_wait(bar(base, i), parity, words() + 1, kTimeoutNs);
     }
+    // The warp's place in the share. It lies in shared memory: every lane of a warp has the same, it changes once per
+    // unit, and registers that hold it through the tile loops would be spilled, to an L1 that has next to no room.
+    static __device__ __forceinline__ Place* place() { return reinterpret_cast<Place*>(g_smem + L::kPlace + (threadIdx.x >> 5) * 128); }
 };
 
 // ------------------------------------------------------------ share's begin
@@ -411,15 +454,15 @@ struct Batch {
 };
 
 struct BatchWalk {
-    Walk w;
-    Seg g;
+    Place* p;
     int kt, left;
     __device__ __forceinline__ bool next(const CacheAttnArgs& a, Batch* b) {
         while (left == 0) {
-            if (!w.next(a, &g)) return false;
-            left = g.tiles();
-            kt = g.kt0;
+            if (!next_run(a, p)) return false;
+            left = p->g.tiles();
+            kt = p->g.kt0;
         }
+        const Seg& g = p->g;
         const int lane = threadIdx.x & 31;
         b->h = g.h;
         b->kt = kt;
@@ -448,14 +491,15 @@ __device__ __forceinline__ void load_scales(const CacheAttnArgs& a, Batch* b) {
 }
 
 template <int D>
-__device__ __forceinline__ void produce(const Ctx& x, const CacheAttnArgs& a, const Start& st, const CUtensorMap* tk,
+__device__ __forceinline__ void produce(const Ctx<D>& x, const CacheAttnArgs& a, const Start& st, const CUtensorMap* tk,
                                         const CUtensorMap* tv) {
     using L = Smem<D>;
     const int lane = threadIdx.x & 31;
     const int page = a.c.page, per_page = page / 16;
     BatchWalk bw;
     bw.left = 0;
-    bw.w.begin(a, st);
+    bw.p = x.place();
+    begin_share(a, st, bw.p);
     Batch b0, b1, b2;
     bool h0 = bw.next(a, &b0), h1 = h0 && bw.next(a, &b1), h2;
     if (h0) load_scales(a, &b0);
@@ -465,20 +509,20 @@ __device__ __forceinline__ void produce(const Ctx& x, const CacheAttnArgs& a, co
         if (h1) load_scales(a, &b1);
         h2 = h1 && bw.next(a, &b2);
         if (b0.id == -2) {  // the rows of this sequence become NaN through the key scale
-            atomicExch(x.words + 2, DEV_CHECK);
+            atomicExch(x.words() + 2, DEV_CHECK);
             b0.ks = NAN;
         }
         const float lvs = __log2f(b0.vs);
         for (int i = 0; i < b0.n; ++i, ++t) {
-            const uint32_t stage = t % kStages, ph = (t / kStages) & 1, slot = t % kScaleSlots;
-            ok = x.wait(B_S1, stage, ph ^ 1) && x.wait(B_VEMPTY, stage, ph ^ 1);
+            const uint32_t stage = t % kStages, vs = t & 1, slot = t % kScaleSlots;
+            ok = x.wait(B_S1, stage, ((t / kStages) & 1) ^ 1) && x.wait(B_VEMPTY, vs, ((t >> 1) & 1) ^ 1);
             ok = __all_sync(0xffffffffu, ok);
             if (!ok) break;
             const bool mine = (lane >> 3) == i;
             const bool load = mine && b0.id >= 0 && (lane & 7) % per_page == 0;
             const uint32_t bytes = (uint32_t)__popc(__ballot_sync(0xffffffffu, load)) * page * D;
             if (mine) {
-                float* sc = reinterpret_cast<float*>(x.smem + L::kScale) + slot * 16 + (lane & 7);
+                float* sc = reinterpret_cast<float*>(g_smem + L::kScale) + slot * 16 + (lane & 7);
                 sc[0] = b0.ks;
                 sc[8] = lvs;
             }
@@ -487,13 +531,13 @@ __device__ __forceinline__ void produce(const Ctx& x, const CacheAttnArgs& a, co
             __syncwarp();
             if (lane == 0) {
                 tc::mbar_arrive_expect_tx(x.bar(B_KFULL, stage), bytes);
-                tc::mbar_arrive_expect_tx(x.bar(B_VFULL, stage), bytes);
+                tc::mbar_arrive_expect_tx(x.bar(B_VFULL, vs), bytes);
             }
             __syncwarp();
             if (load) {
-                const uint32_t off = stage * L::kT8 + (lane & 7) * 16 * D;
-                tc::tma_load_3d(x.sbase + L::kK + off, tk, x.bar(B_KFULL, stage), 0, 0, b0.id * a.c.Hk + b0.h);
-                tc::tma_load_3d(x.sbase + L::kV + off, tv, x.bar(B_VFULL, stage), 0, 0, b0.id * a.c.Hk + b0.h);
+                const uint32_t off = (lane & 7) * 16 * D;
+                tc::tma_load_3d(sbase() + L::kK + stage * L::kT8 + off, tk, x.bar(B_KFULL, stage), 0, 0, b0.id * a.c.Hk + b0.h);
+                tc::tma_load_3d(sbase() + L::kV + vs * L::kT8 + off, tv, x.bar(B_VFULL, vs), 0, 0, b0.id * a.c.Hk + b0.h);
             }
             __syncwarp();
         }
@@ -507,86 +551,59 @@ __device__ __forceinline__ void produce(const Ctx& x, const CacheAttnArgs& a, co
         for (uint32_t i = t > kStages ? t - kStages : 0; i < t; ++i) {
             tc::mbar_wait(x.bar(B_KFULL, i % kStages), (i / kStages) & 1, &never, kTimeoutNs);
             never = 0;
-            tc::mbar_wait(x.bar(B_VFULL, i % kStages), (i / kStages) & 1, &never, kTimeoutNs);
+            if (i + 2 >= t) tc::mbar_wait(x.bar(B_VFULL, i & 1), (i >> 1) & 1, &never, kTimeoutNs);
             never = 0;
         }
     }
 }
 
 // ------------------------------------------------------------ V: e4m3 -> fp16
+// Tile t's values, by the softmax warps: thread `id` of the 256 with the same i takes keys 64 i .. 64 i + 63, which are
+// the ones that O_i's products read in a unit of one MMA tile. Keys from `valid` on become zeros; with `check` NaN
+// codes do too, and their first key is noted for each column (`key0`: the tile's first key).
 template <int D>
-__device__ __forceinline__ void widen(const Ctx& x, const CacheAttnArgs& a, const Start& st) {
+__device__ __forceinline__ void widen(uint32_t t, int i, int id, int valid, bool check, int key0) {
     using L = Smem<D>;
-    constexpr int PER = D / 16;                  // 16-byte chunks per key
-    constexpr int ROWS = 4 * (32 / PER);         // keys that the four warps take at a time
-    constexpr int STEPS = kTileKeys / ROWS;
-    const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) - 12;
-    const int c = lane % PER, r0 = lane / PER + warp * (32 / PER);
-    // 16 columns are two 16-byte chunks of the 64-column half they lie in; the lanes of the upper half store theirs in
-    // the other order, so that eight lanes meet eight bank groups. The rows of a thread are ROWS (a multiple of 8)
-    // apart, so its swizzle is the same in every step.
-    const uint32_t src0 = x.sbase + L::kV + swz8<D>(r0, c);
-    const uint32_t row_dst = x.sbase + L::kW + (c >> 2) * 16384 + r0 * 128;
-    const bool swap = c >= 4;
-    const uint32_t d0 = row_dst + ((((2 * c + (swap ? 1 : 0)) & 7) ^ (r0 & 7)) << 4);
-    const uint32_t d1 = row_dst + ((((2 * c + (swap ? 0 : 1)) & 7) ^ (r0 & 7)) << 4);
-    Walk w;
-    w.begin(a, st);
-    Seg g;
-    uint32_t t = 0, seg = 0;
-    while (w.next(a, &g)) {
-        if (g.tiles() == 0) continue;
-        int* nan_first = reinterpret_cast<int*>(x.smem + L::kNan) + (seg & 3) * D;
-        int* nan_any = reinterpret_cast<int*>(x.smem + L::kNanAny) + (seg & 3);
-        ++seg;
-        // keys that every row of the unit sees; a NaN among the others must not reach a row that does not see it
-        const int all = key_end(g.len, a.block, g.pos0 + g.m0 / a.G);
-        for (int kt = g.kt0; kt < g.kt1; ++kt, ++t) {
-            const uint32_t stage = t % kStages, ws = t & 1;
-            bool ok = x.wait(B_VFULL, stage, (t / kStages) & 1);
-            const uint32_t src = src0 + stage * L::kT8, off = ws * 2 * L::kT8;
-            uint32_t v[STEPS][4];
+    constexpr int PER = D / 16, ROWS = 256 / PER;  // 16-byte chunks per key, keys per step
+    const int c = id % PER;
+    uint32_t v[64 / ROWS][4];
 #pragma unroll
-            for (int j = 0; j < STEPS; ++j) lds16(src + j * ROWS * D, v[j]);
-            ok = ok && x.wait(B_PV, ws, ((t >> 1) & 1) ^ 1);
-            if (!__all_sync(0xffffffffu, ok)) return;
-            const int valid = imin(kTileKeys, g.end - kt * kTileKeys);
-            if (valid < kTileKeys || kt * kTileKeys + valid > all) {
+    for (int j = 0; j < 64 / ROWS; ++j) lds16(sbase() + L::kV + (t & 1) * L::kT8 + swz8<D>(64 * i + j * ROWS + id / PER, c), v[j]);
+    if (check) {
 #pragma unroll
-                for (int j = 0; j < STEPS; ++j) {
-                    const int r = j * ROWS + r0;
-                    if (r >= valid) v[j][0] = v[j][1] = v[j][2] = v[j][3] = 0;
-                    uint32_t any = 0;
+        for (int j = 0; j < 64 / ROWS; ++j) {
+            const int r = 64 * i + j * ROWS + id / PER;
+            if (r >= valid) v[j][0] = v[j][1] = v[j][2] = v[j][3] = 0;
+            uint32_t any = 0;
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) any |= ((v[j][e] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
-                    if (any) {
+            for (int e = 0; e < 4; ++e) any |= ((v[j][e] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+            if (any) {
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            const uint32_t sh = 8 * (e & 3);
-                            if (((v[j][e >> 2] >> sh) & 0x7f) == 0x7f) {
-                                atomicMin(nan_first + 16 * c + e, kt * kTileKeys + r);
-                                atomicMin(nan_any, kt * kTileKeys + r);
-                                v[j][e >> 2] &= ~(0xffu << sh);
-                            }
-                        }
+                for (int e = 0; e < 16; ++e) {
+                    const uint32_t sh = 8 * (e & 3);
+                    if (((v[j][e >> 2] >> sh) & 0x7f) == 0x7f) {
+                        atomicMin(reinterpret_cast<int*>(g_smem + L::kNan) + 16 * c + e, key0 + r);
+                        atomicMin(reinterpret_cast<int*>(g_smem + L::kNanAny), key0 + r);
+                        v[j][e >> 2] &= ~(0xffu << sh);
                     }
                 }
             }
-#pragma unroll
-            for (int j = 0; j < STEPS; ++j) {
-                uint32_t h[8];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) widen4(v[j][e], h[2 * e], h[2 * e + 1]);
-                sts16(d0 + off + j * ROWS * 128, swap ? h[4] : h[0], swap ? h[5] : h[1], swap ? h[6] : h[2], swap ? h[7] : h[3]);
-                sts16(d1 + off + j * ROWS * 128, swap ? h[0] : h[4], swap ? h[1] : h[5], swap ? h[2] : h[6], swap ? h[3] : h[7]);
-            }
-            tc::fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) {
-                tc::mbar_arrive(x.bar(B_VEMPTY, stage));
-                tc::mbar_arrive(x.bar(B_P, 2 * ws));
-            }
         }
+    }
+#pragma unroll
+    for (int j = 0; j < 64 / ROWS; ++j) {
+        const int r = 64 * i + j * ROWS + id / PER;
+        uint32_t h[8];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) widen4(v[j][e], h[2 * e], h[2 * e + 1]);
+        // 16 columns are two 16-byte chunks of the 64-column half they lie in; the lanes of the upper half store theirs
+        // in the other order, so that eight lanes meet eight bank groups
+        const uint32_t dst = sbase() + L::kW + (t & 1) * 2 * L::kT8 + (c >> 2) * 16384 + r * 128;
+        const bool swap = c >= 4;
+        const uint32_t d0 = dst + ((((2 * c + (swap ? 1 : 0)) & 7) ^ (r & 7)) << 4);
+        const uint32_t d1 = dst + ((((2 * c + (swap ? 0 : 1)) & 7) ^ (r & 7)) << 4);
+        sts16(d0, swap ? h[4] : h[0], swap ? h[5] : h[1], swap ? h[6] : h[2], swap ? h[7] : h[3]);
+        sts16(d1, swap ? h[0] : h[4], swap ? h[1] : h[5], swap ? h[2] : h[6], swap ? h[3] : h[7]);
     }
 }
 
@@ -594,14 +611,14 @@ __device__ __forceinline__ void widen(const Ctx& x, const CacheAttnArgs& a, cons
 // The whole warp walks the share, so that addresses and descriptors are warp-
 // uniform values; one elected lane issues. The tensor pipe queues little, so
 // what stands between two groups of MMAs is kept short: one wait for a tile's
-// keys, taken before the pipe needs them, one for p' of each group (which
-// counts the fp16 values as well) and one commit for each S and each PV.
+// keys, one for p' of each O (and one for the values, where p' does not count
+// them) and one commit for each S and each PV.
 template <int D>
-__device__ __forceinline__ void issue(const Ctx& x, const CacheAttnArgs& a, const Start& st) {
+__device__ __forceinline__ void issue(const Ctx<D>& x, const CacheAttnArgs& a, const Start& st) {
     using L = Smem<D>;
     constexpr uint32_t id_s = idesc_fmt0(128, kTileKeys, 0), id_o = idesc_fmt0(128, D, 1);
-    const uint32_t sbase = __shfl_sync(0xffffffffu, x.sbase, 0), tmem = __shfl_sync(0xffffffffu, x.tmem, 0);
-    const uint64_t k8 = sdesc_k8<D>(sbase), mn = tc::sdesc_sw128(sbase, 16384, 1024);
+    const uint32_t tmem = __shfl_sync(0xffffffffu, x.tmem, 0);
+    const uint64_t k8 = sdesc_k8<D>(sbase()), mn = tc::sdesc_sw128(sbase(), 16384, 1024);
     const bool leader = elect_one();
     auto wait = [&](int base, int i, uint32_t parity) { return __all_sync(0xffffffffu, x.wait(base, i, parity)) != 0; };
     // S of tile t from Q tile qt into S buffer b
@@ -617,24 +634,25 @@ __device__ __forceinline__ void issue(const Ctx& x, const CacheAttnArgs& a, cons
             tc::mma_commit(x.bar(bar, stage));
         }
     };
-    // N / 16 steps of p' (from S buffer column p) times the fp16 values from key `key` on, into O buffer o
+    // 2 N steps of p' times the fp16 values from key `key` on, into O buffer o: N steps from TMEM column p on, which the
+    // groups (o, 0) wrote, and N from column p + 16 N on
     auto issue_pv = [&](uint32_t t, uint32_t p, uint32_t o, int key, auto steps, bool fresh) {
+        constexpr int N = decltype(steps)::value;
         const uint64_t dv = tc::sdesc_add(mn, L::kW + (t & 1) * 2 * L::kT8 + key * 128);
         const uint32_t to = tmem + 256 + D * o, from = tmem + p;
         if (leader) {
 #pragma unroll
-            for (int k = 0; k < decltype(steps)::value; ++k)
-                tc::mma_ts(to, from + 8 * k, tc::sdesc_add(dv, 2048 * k), id_o, (k > 0 || !fresh) ? 1u : 0u);
+            for (int k = 0; k < 2 * N; ++k)
+                tc::mma_ts(to, from + 16 * N * (k / N) + 8 * (k % N), tc::sdesc_add(dv, 2048 * k), id_o, (k > 0 || !fresh) ? 1u : 0u);
         }
     };
-    Walk w;
-    w.begin(a, st);
-    Seg g;
+    Place* place = x.place();
+    begin_share(a, st, place);
     uint32_t t0 = 0, seg = 0;
-    while (w.next(a, &g)) {
-        const int nt = __shfl_sync(0xffffffffu, g.tiles(), 0);
+    while (next_run(a, place)) {
+        const int nt = __shfl_sync(0xffffffffu, place->g.tiles(), 0);
         if (nt == 0) continue;
-        const bool two = __shfl_sync(0xffffffffu, (int)g.two, 0) != 0;
+        const bool two = __shfl_sync(0xffffffffu, (int)place->g.two, 0) != 0;
         if (!wait(B_Q, 0, seg & 1)) return;
         ++seg;
         tc::tc_fence_after();
@@ -645,13 +663,14 @@ __device__ __forceinline__ void issue(const Ctx& x, const CacheAttnArgs& a, cons
             for (int j = 0; j < nt; ++j) {
                 const uint32_t t = t0 + j, b = t & 1, ph = (t >> 1) & 1;
                 const bool more = j + 1 < nt;
-                if (more && !wait(B_KFULL, (t + 1) % kStages, ((t + 1) / kStages) & 1)) return;
+                if (!wait(B_W, b, ph)) return;
 #pragma unroll
                 for (uint32_t i = 0; i < 2; ++i) {
                     if (!wait(B_P, 2 * b + i, ph)) return;
                     tc::tc_fence_after();
-                    issue_pv(t, 128 * i, i, 0, Const<kTileKeys / 16>{}, j == 0);
+                    issue_pv(t, 128 * i, i, 0, Const<4>{}, j == 0);
                     if (i == 1 && leader) tc::mma_commit(x.bar(B_PV, b));
+                    if (i == 0 && more && !wait(B_KFULL, (t + 1) % kStages, ((t + 1) / kStages) & 1)) return;
                     if (more) issue_s(t + 1, i, i, i == 0 ? B_S0 : B_S1);
                 }
             }
@@ -666,14 +685,14 @@ __device__ __forceinline__ void issue(const Ctx& x, const CacheAttnArgs& a, cons
             for (int j = 0; j < nt; ++j) {
                 const uint32_t t = t0 + j, b = t & 1, ph = (t >> 1) & 1;
                 const bool more = j + 2 < nt;
-                if (more && !wait(B_KFULL, (t + 2) % kStages, ((t + 2) / kStages) & 1)) return;
 #pragma unroll
-                for (uint32_t h = 0; h < 2; ++h) {  // each group's 64 keys into its own O
-                    if (!wait(B_P, 2 * b + h, ph)) return;
+                for (uint32_t i = 0; i < 2; ++i) {  // each half of the keys into its own O
+                    if (!wait(B_P, 2 * b + i, ph)) return;
                     tc::tc_fence_after();
-                    issue_pv(t, 128 * b + 64 * h, h, 64 * h, Const<kTileKeys / 32>{}, j == 0);
+                    issue_pv(t, 128 * b + 64 * i, i, 64 * i, Const<2>{}, j == 0);
                 }
                 if (leader) tc::mma_commit(x.bar(B_PV, b));
+                if (more && !wait(B_KFULL, (t + 2) % kStages, ((t + 2) / kStages) & 1)) return;
                 if (more) issue_s(t + 2, 0, b, B_S1);
             }
         }
@@ -686,12 +705,12 @@ __device__ __forceinline__ void issue(const Ctx& x, const CacheAttnArgs& a, cons
 // that is not finite). Eight values per thread, so that a row is read and reduced by D / 8 lanes; rows behind the last
 // one of a warp's 32 are zeros.
 template <int D>
-__device__ __forceinline__ void split_q(const Ctx& x, const CacheAttnArgs& a, const Seg& g) {
+__device__ __forceinline__ void split_q(const Ctx<D>& x, const CacheAttnArgs& a, const Seg& g) {
     using L = Smem<D>;
-    constexpr int PER = D / 8, ROWS = 256 / PER, BATCH = 4;
+    constexpr int PER = D / 8, ROWS = kSoftmax / PER, BATCH = 2;
     const int chunk = threadIdx.x % PER, r0 = threadIdx.x / PER;
     const int n = g.last - g.m0, padded = (n + 31) & ~31;
-    uint8_t* exps = x.smem + L::kQExp;
+    uint8_t* exps = g_smem + L::kQExp;
     const __nv_bfloat16* q = a.q + ((long long)g.row0 * a.H + g.h * a.G) * D + 8 * chunk;
     const int dr = ROWS / a.G, dm = ROWS - dr * a.G;
     int row = (g.m0 + r0) / a.G, rem = g.m0 + r0 - row * a.G, next = r0;
@@ -707,7 +726,7 @@ __device__ __forceinline__ void split_q(const Ctx& x, const CacheAttnArgs& a, co
         }
         return y;
     };
-    // four rows at a time, the next four in flight; the loop is not unrolled further, since most of what a first pass
+    // two rows at a time, the next two in flight; the loop is not unrolled further, since most of what a first pass
     // through this code costs is fetching the code
     uint4 v[BATCH], w[BATCH];
 #pragma unroll
@@ -745,7 +764,7 @@ __device__ __forceinline__ void split_q(const Ctx& x, const CacheAttnArgs& a, co
                 lo[e] = narrow4(f0 - h0.x, f1 - h0.y, f2 - h1.x, f3 - h1.y);
             }
             if (r < padded) {
-                const uint32_t at = x.sbase + L::kQ + (r >> 7) * 2 * L::kT8 + swz8<D>(r & 127, chunk >> 1) + 8 * (chunk & 1);
+                const uint32_t at = sbase() + L::kQ + (r >> 7) * 2 * L::kT8 + swz8<D>(r & 127, chunk >> 1) + 8 * (chunk & 1);
                 sts8(at, hi[0], hi[1]);
                 sts8(at + L::kT8, lo[0], lo[1]);
                 if (chunk == 0) exps[r] = fine ? (uint8_t)(sc >> 23) : (uint8_t)255;
@@ -756,20 +775,23 @@ __device__ __forceinline__ void split_q(const Ctx& x, const CacheAttnArgs& a, co
     }
 }
 
-// COLS keys of one key tile for one row: scores out of TMEM (columns from tC on), p' back into them. NG pages of GK keys
-// each; sc points at the first one's key scale. `settle` waits until the row's O may be rescaled.
+// COLS keys of one key tile for one row: scores out of TMEM (columns from tC on), p' back into them, in chunks of 32
+// keys. GK keys in a row share a page (of 32; larger pages count as several); sc points at the first one's key scale.
+// `settle` waits until the row's O may be rescaled, `mx_own` and `mx_other` are the partners' places for a maximum.
 //
 // Tiles are first taken with the row's present offsets, the maximum of the exponents alongside: it is at most 15 (p' fits
-// fp16) for all but a few tiles of a sequence. Where a row of the warp finds a larger one (its first keys among them), or
-// a page's value scale is so small that its p' may fall below what fp32 holds, the warp takes the tile again: new offsets
-// from the tile's maxima, O and l rescaled, and l from the weights themselves where p' says too little.
-template <int D, int NG, int COLS, typename Settle>
-__device__ __forceinline__ void softmax_part(uint32_t tC, uint32_t tO, const float* sc, float cs, int visible, bool full,
-                                             bool first, float& m, float& mo, float& l, Settle settle) {
-    constexpr int GK = COLS / NG, Q = COLS / 32;
+// fp16) for all but a few tiles of a sequence. Where a row of the two warps that share it finds a larger one (its first
+// keys among them), or a page's value scale is so small that its p' may fall below what fp32 holds, both warps take the
+// tile again: new offsets from the tile's maxima, O (each warp half of its columns) and l rescaled, and l from the
+// weights themselves where p' says too little.
+template <int D, int GK, int COLS, typename Settle>
+__device__ __forceinline__ void softmax_part(uint32_t tC, uint32_t tO, int pair, float* mx_own, const float* mx_other,
+                                             const float* sc, float cs, int visible, bool full, bool first, float& m, float& mo,
+                                             float& l, Settle settle) {
+    constexpr int Q = COLS / 32, NG = 32 / GK;
     if (!full) {
         // masked entries become -inf in TMEM first, so that other tiles run no mask code
-#pragma unroll
+#pragma unroll 1
         for (int q = 0; q < Q; ++q) {
             uint32_t v[32];
             tc::tmem_ld32(tC + 32 * q, v);
@@ -781,34 +803,25 @@ __device__ __forceinline__ void softmax_part(uint32_t tC, uint32_t tO, const flo
         }
         tc::tmem_st_wait();
     }
-    uint32_t r[Q][32];
-    float ks[NG], lv[NG];
-#pragma unroll
-    for (int q = 0; q < Q; ++q) tc::tmem_ld32(tC + 32 * q, r[q]);
-#pragma unroll
-    for (int g = 0; g < NG; ++g) {
-        ks[g] = cs * sc[g * (GK / 16)];
-        lv[g] = sc[8 + g * (GK / 16)];
-    }
-    tc::tmem_ld_wait();
-    auto at = [&](int k) { return __uint_as_float(r[k >> 5][k & 31]); };
     uint32_t pk[COLS / 2];
-    // p' of page g with exponents s ks + b into pk; returns their sum, and the largest exponent in *top
-    auto weigh = [&](int g, float b, float* top) {
-        const float2 a2 = make_float2(ks[g], ks[g]), b2 = make_float2(b, b);
+    // p' of keys [GK g, GK g + GK) of chunk q with exponents s ks + b into pk; returns their sum, and the largest exponent
+    // in *top
+    auto weigh = [&](const uint32_t(&r)[32], int q, int g, float ks, float b, float* top) {
+        const float2 a2 = make_float2(ks, ks), b2 = make_float2(b, b);
         float2 s0 = make_float2(0.f, 0.f), s1 = make_float2(0.f, 0.f);
         float t0 = *top, t1 = *top;
 #pragma unroll
         for (int e = 0; e < GK; e += 4) {
             const int k = g * GK + e;
-            const float2 y0 = tc::fma2(make_float2(at(k), at(k + 1)), a2, b2), y1 = tc::fma2(make_float2(at(k + 2), at(k + 3)), a2, b2);
+            const float2 y0 = tc::fma2(make_float2(__uint_as_float(r[k]), __uint_as_float(r[k + 1])), a2, b2);
+            const float2 y1 = tc::fma2(make_float2(__uint_as_float(r[k + 2]), __uint_as_float(r[k + 3])), a2, b2);
             t0 = tc::fmax3(t0, y0.x, y0.y);
             t1 = tc::fmax3(t1, y1.x, y1.y);
             const float2 p0 = make_float2(ex2f(y0.x), ex2f(y0.y)), p1 = make_float2(ex2f(y1.x), ex2f(y1.y));
             s0 = tc::add2(s0, p0);
             s1 = tc::add2(s1, p1);
-            pk[k >> 1] = pack_h2(p0.x, p0.y);
-            pk[(k >> 1) + 1] = pack_h2(p1.x, p1.y);
+            pk[16 * q + (k >> 1)] = pack_h2(p0.x, p0.y);
+            pk[16 * q + (k >> 1) + 1] = pack_h2(p1.x, p1.y);
         }
         *top = fmaxf(t0, t1);
         return s0.x + s1.x + (s0.y + s1.y);
@@ -816,33 +829,41 @@ __device__ __forceinline__ void softmax_part(uint32_t tC, uint32_t tO, const flo
     const float m_was = m == -INFINITY ? 0.f : m, mo_was = mo == -INFINITY ? 0.f : mo;
     float sum = 0.f, top = -INFINITY, low = INFINITY;
 #pragma unroll
-    for (int g = 0; g < NG; ++g) {
-        const float b = lv[g] - mo_was, shift = b + m_was;
-        low = fminf(low, shift);
-        sum = fmaf(weigh(g, b, &top), ex2f(-shift), sum);
-    }
-    if (__any_sync(0xffffffffu, top > 15.f || low < -60.f || (mo == -INFINITY && top > -INFINITY))) {
-#pragma unroll
-        for (int q = 0; q < Q; ++q) tc::tmem_ld32(tC + 32 * q, r[q]);
+    for (int q = 0; q < Q; ++q) {
+        uint32_t r[32];
+        tc::tmem_ld32(tC + 32 * q, r);
         tc::tmem_ld_wait();
-        float mx = -INFINITY, mxo = -INFINITY;
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
-            float c0 = -INFINITY, c1 = -INFINITY;
+            const float b = sc[8 + 2 * q + g] - mo_was, shift = b + m_was;
+            low = fminf(low, shift);
+            sum = fmaf(weigh(r, q, g, cs * sc[2 * q + g], b, &top), ex2f(-shift), sum);
+        }
+    }
+    if (pair_any(pair, top > 15.f || low < -60.f || (mo == -INFINITY && top > -INFINITY))) {
+        float mx = -INFINITY, mxo = -INFINITY;
+#pragma unroll 1
+        for (int q = 0; q < Q; ++q) {
+            uint32_t r[32];
+            tc::tmem_ld32(tC + 32 * q, r);
+            tc::tmem_ld_wait();
 #pragma unroll
-            for (int e = 0; e < GK; e += 4) {
-                const int k = g * GK + e;
-                c0 = tc::fmax3(c0, at(k), at(k + 1));
-                c1 = tc::fmax3(c1, at(k + 2), at(k + 3));
+            for (int g = 0; g < NG; ++g) {
+                float c = -INFINITY;
+#pragma unroll
+                for (int e = 0; e < GK; e += 2) c = tc::fmax3(c, __uint_as_float(r[g * GK + e]), __uint_as_float(r[g * GK + e + 1]));
+                const float y = c * (cs * sc[2 * q + g]);
+                mx = fmaxf(mx, y);
+                mxo = fmaxf(mxo, y + sc[8 + 2 * q + g]);
             }
-            const float y = fmaxf(c0, c1) * ks[g];
-            mx = fmaxf(mx, y);
-            mxo = fmaxf(mxo, y + lv[g]);
         }
         if (mx > m) {
             l *= ex2f(m - mx);
             m = mx;
         }
+        *mx_own = mxo;
+        pair_sync(pair);
+        mxo = fmaxf(mxo, *mx_other);
         const bool move = mxo > mo + 15.f;
         float alpha = 1.f;
         if (move) {
@@ -851,8 +872,8 @@ __device__ __forceinline__ void softmax_part(uint32_t tC, uint32_t tO, const flo
         }
         if (!first && __any_sync(0xffffffffu, move)) {
             settle();
-#pragma unroll
-            for (int q = 0; q < D / 16; ++q) {
+#pragma unroll 1
+            for (int q = 0; q < D / 32; ++q) {
                 uint32_t o[16];
                 tmem_ld16(tO + 16 * q, o);
                 tc::tmem_ld_wait();
@@ -864,28 +885,33 @@ __device__ __forceinline__ void softmax_part(uint32_t tC, uint32_t tO, const flo
         const float m_use = m == -INFINITY ? 0.f : m, mo_use = mo == -INFINITY ? 0.f : mo;
         sum = 0.f;
 #pragma unroll
-        for (int g = 0; g < NG; ++g) {
-            const float b = lv[g] - mo_use, shift = b + m_use;
-            if (__any_sync(0xffffffffu, shift < -60.f)) {
+        for (int q = 0; q < Q; ++q) {
+            uint32_t r[32];
+            tc::tmem_ld32(tC + 32 * q, r);
+            tc::tmem_ld_wait();
 #pragma unroll
-                for (int e = 0; e < GK; ++e) sum += ex2f(fmaf(at(g * GK + e), ks[g], -m_use));
-                weigh(g, b, &top);
-            } else {
-                sum = fmaf(weigh(g, b, &top), ex2f(-shift), sum);
+            for (int g = 0; g < NG; ++g) {
+                const float ks = cs * sc[2 * q + g], b = sc[8 + 2 * q + g] - mo_use, shift = b + m_use;
+                if (__any_sync(0xffffffffu, shift < -60.f)) {
+#pragma unroll
+                    for (int e = 0; e < GK; ++e) sum += ex2f(fmaf(__uint_as_float(r[g * GK + e]), ks, -m_use));
+                    weigh(r, q, g, ks, b, &top);
+                } else {
+                    sum = fmaf(weigh(r, q, g, ks, b, &top), ex2f(-shift), sum);
+                }
             }
         }
+        pair_sync(pair);  // the partner has read *mx_own
     }
     l += sum;
 #pragma unroll
-    for (int q = 0; q < COLS / 32; ++q) {
+    for (int q = 0; q < Q; ++q) {
         uint32_t w[16];
 #pragma unroll
         for (int e = 0; e < 16; ++e) w[e] = pk[16 * q + e];
         tc::tmem_st16(tC + 16 * q, w);
     }
     tc::tmem_st_wait();
-    tc::tc_fence_before();
-    __syncwarp();
 }
 
 // Where the results of a unit's flat rows go.
@@ -894,27 +920,27 @@ struct Out {
     int slot_r;   // its rows
 };
 
-// Writes 32 columns (from 32 q on) of flat row m: into the slot; as fp32 to o; or as bf16 into the staging tile at
+// Writes 16 columns (from 16 q on) of flat row m: into the slot; as fp32 to o; or as bf16 into the staging tile at
 // `stage`, whose row `row` is this one.
 template <int D>
 __device__ __forceinline__ void put_cols(const CacheAttnArgs& a, const Seg& g, const Out& out, int m, int row, uint32_t stage,
-                                         int q, const float (&v)[32]) {
+                                         int q, const float (&v)[16]) {
     if (out.slot) {
         if (m < g.last) {
-            float4* dst = reinterpret_cast<float4*>(out.slot) + (8 * q) * out.slot_r + (m - g.m0);
+            float4* dst = reinterpret_cast<float4*>(out.slot) + (4 * q) * out.slot_r + (m - g.m0);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) dst[e * out.slot_r] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+            for (int e = 0; e < 4; ++e) dst[e * out.slot_r] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
         }
     } else if (a.o_f32) {
         if (m < g.last) {
-            float4* dst = reinterpret_cast<float4*>(a.o_f32 + ((long long)(g.row0 + m / a.G) * a.H + g.h * a.G + m % a.G) * D + 32 * q);
+            float4* dst = reinterpret_cast<float4*>(a.o_f32 + ((long long)(g.row0 + m / a.G) * a.H + g.h * a.G + m % a.G) * D + 16 * q);
 #pragma unroll
-            for (int e = 0; e < 8; ++e) dst[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+            for (int e = 0; e < 4; ++e) dst[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
         }
     } else {
 #pragma unroll
-        for (int e = 0; e < 4; ++e)
-            sts16(stage + row * 2 * D + (((4 * q + e) ^ (row & 7)) << 4), pack_bf2(v[8 * e], v[8 * e + 1]),
+        for (int e = 0; e < 2; ++e)
+            sts16(stage + row * 2 * D + (((2 * q + e) ^ (row & 7)) << 4), pack_bf2(v[8 * e], v[8 * e + 1]),
                   pack_bf2(v[8 * e + 2], v[8 * e + 3]), pack_bf2(v[8 * e + 4], v[8 * e + 5]), pack_bf2(v[8 * e + 6], v[8 * e + 7]));
     }
 }
@@ -952,59 +978,84 @@ __device__ __forceinline__ void put_lse(const CacheAttnArgs& a, const Seg& g, co
     }
 }
 
-template <int D, int NG>
-__device__ __forceinline__ void softmax(const Ctx& x, const CacheAttnArgs& a, const Start& st) {
+template <int D, int GK>
+__device__ __forceinline__ void softmax(const Ctx<D>& x, const CacheAttnArgs& a, const Start& st) {
     using L = Smem<D>;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, i = warp >> 2, row = threadIdx.x & 127;
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, i = warp >> 3, h = (warp >> 2) & 1, row = threadIdx.x & 127;
+    const int pair = 4 * i + (warp & 3);
     const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
-    const uint32_t tS = x.tmem + lane_base, tO = x.tmem + 256 + D * i + lane_base, tO1 = x.tmem + 256 + D * (i ^ 1) + lane_base;
-    const float* scales = reinterpret_cast<const float*>(x.smem + L::kScale);
-    Walk w;
-    w.begin(a, st);
-    Seg g;
-    uint32_t t = 0, seg = 0, s0_phases = 0;  // s0_phases: bit of each B_S0 stage's next phase
-    bool ok = true;  // warp-uniform; the loops run on without waiting once it is false
+    const uint32_t tS = x.tmem + lane_base, tO = x.tmem + 256 + lane_base;
+    const float* scales = reinterpret_cast<const float*>(g_smem + L::kScale);
+    Place* place = x.place();
+    begin_share(a, st, place);
+    float* const mx_own = reinterpret_cast<float*>(g_smem + L::kMax) + pair * 64 + 32 * h + lane;
+    const float* const mx_other = reinterpret_cast<const float*>(g_smem + L::kMax) + pair * 64 + 32 * (h ^ 1) + lane;
+    uint32_t t = 0, s0_phases = 0;  // s0_phases: bit of each B_S0 stage's next phase
+    bool ok = true;  // warp-uniform; once it is false the loops run on without waiting, through the same barriers
     auto wait = [&](int base, int n, uint32_t parity) {
         if (ok) ok = __all_sync(0xffffffffu, x.wait(base, n, parity));
         tc::tc_fence_after();
     };
-    while (w.next(a, &g)) {
-        const int nt = g.tiles();
-        const int m = g.m0 + (g.two ? 128 * i : 0) + row;  // this thread's flat row
-        Out out;
-        out.slot_r = slot_rows(a.total_rows, a.G);
-        out.slot = g.whole ? nullptr : slot_at(a.scratch, 2 * (int)blockIdx.x + (g.kt0 > 0 ? 0 : 1), out.slot_r, D);
-        if (nt == 0) {  // rows without keys
-            if (m < g.last && (g.two || i == 0)) {
-                const long long at = ((long long)(g.row0 + m / a.G) * a.H + g.h * a.G + m % a.G) * D;
-                for (int c = 0; c < D; c += 8) {
-                    if (a.o_f32) {
-                        *reinterpret_cast<float4*>(a.o_f32 + at + c) = make_float4(0.f, 0.f, 0.f, 0.f);
-                        *reinterpret_cast<float4*>(a.o_f32 + at + c + 4) = make_float4(0.f, 0.f, 0.f, 0.f);
-                    } else {
-                        *reinterpret_cast<uint4*>(a.o + at + c) = make_uint4(0, 0, 0, 0);
-                    }
-                }
-                put_lse(a, g, out, D, m, -INFINITY);
-            }
-            continue;
-        }
-        split_q<D>(x, a, g);
+    // the values of tile j of the run, which is tile n of the share
+    auto take_v = [&](uint32_t n, int j) {
+        if (ok) ok = __all_sync(0xffffffffu, x.wait(B_VFULL, n & 1, (n >> 1) & 1) && x.wait(B_PV, n & 1, ((n >> 1) & 1) ^ 1));
+        const int key0 = (place->g.kt0 + j) * kTileKeys, valid = imin(kTileKeys, place->g.end - key0);
+        widen<D>(n, i, threadIdx.x & 255, valid, valid < kTileKeys || key0 + valid > place->all, key0);
         tc::fence_proxy_async_smem();
-        tc::tc_fence_before();
         __syncwarp();
-        if (lane == 0) tc::mbar_arrive(x.bar(B_Q, 0));
-        softmax_sync();  // the rows' exponents
-        // the factor that turns the tensor core's q . k8 into base-2 scores; a row that is not finite becomes NaN, and no other
-        const int qe = x.smem[L::kQExp + (g.two ? 128 * i : 0) + row];
-        const float cs = qe == 255 ? NAN : a.scale_log2 * __uint_as_float((uint32_t)qe << 23);
-        const int end = m < g.last ? key_end(g.len, a.block, g.pos0 + m / a.G) : 0;
-        const bool warp_live = __shfl_sync(0xffffffffu, (int)(m < g.last), 0);
-        // keys of a tile that this row sees, and that the warp's first row (which sees the fewest) does
-        int sees = end - g.kt0 * kTileKeys - (g.two ? 0 : 64 * i), all_see = __shfl_sync(0xffffffffu, sees, 0);
+        if (lane == 0) {
+            tc::mbar_arrive(x.bar(B_VEMPTY, n & 1));
+            tc::mbar_arrive(x.bar(B_W, n & 1));
+        }
+    };
+    while (next_run(a, place)) {
+        const int nt = place->g.tiles();
+        const bool two = place->g.two;
+        float cs;
+        int sees, all_see;
+        bool warp_live;
+        {
+            const Seg g = place->g;
+            const int m = g.m0 + (two ? 128 * i : 0) + row;  // this thread's flat row
+            if (nt == 0) {                                   // rows without keys
+                if (m < g.last && h == 0 && (two || i == 0)) {
+                    const long long at = ((long long)(g.row0 + m / a.G) * a.H + g.h * a.G + m % a.G) * D;
+                    for (int c = 0; c < D; c += 8) {
+                        if (a.o_f32) {
+                            *reinterpret_cast<float4*>(a.o_f32 + at + c) = make_float4(0.f, 0.f, 0.f, 0.f);
+                            *reinterpret_cast<float4*>(a.o_f32 + at + c + 4) = make_float4(0.f, 0.f, 0.f, 0.f);
+                        } else {
+                            *reinterpret_cast<uint4*>(a.o + at + c) = make_uint4(0, 0, 0, 0);
+                        }
+                    }
+                    put_lse(a, g, Out{nullptr, 0}, D, m, -INFINITY);
+                }
+                continue;
+            }
+            split_q<D>(x, a, g);
+            tc::fence_proxy_async_smem();
+            tc::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(x.bar(B_Q, 0));
+            softmax_sync();  // the rows' exponents
+            // the factor that turns the tensor core's q . k8 into base-2 scores; a row that is not finite becomes NaN, and
+            // no other
+            const int qe = g_smem[L::kQExp + (two ? 128 * i : 0) + row];
+            cs = qe == 255 ? NAN : a.scale_log2 * __uint_as_float((uint32_t)qe << 23);
+            const int end = m < g.last ? key_end(g.len, a.block, g.pos0 + m / a.G) : 0;
+            warp_live = __shfl_sync(0xffffffffu, (int)(m < g.last), 0);
+            // keys of a tile that this row sees of the thread's part, and that the warp's first row (which sees the
+            // fewest) does
+            sees = end - g.kt0 * kTileKeys - (two ? 64 * h : 64 * i + 32 * h);
+            all_see = __shfl_sync(0xffffffffu, sees, 0);
+            // keys that every row of the unit sees; a NaN among the others must not reach a row that does not see it
+            place->all = imin(key_end(g.len, a.block, g.pos0 + g.m0 / a.G), g.end);
+            __syncwarp();
+        }
+        take_v(t, 0);
         float mm = -INFINITY, mo = -INFINITY, l = 0.f;
         uint32_t stage = t % kStages, ph = (t / kStages) & 1, slot = t % kScaleSlots;
-        if (g.two) {
+        if (two) {
             for (int j = 0; j < nt; ++j, ++t) {
                 if (i == 0) {
                     wait(B_S0, stage, (s0_phases >> stage) & 1);
@@ -1012,9 +1063,13 @@ __device__ __forceinline__ void softmax(const Ctx& x, const CacheAttnArgs& a, co
                     wait(B_S1, stage, ph);
                 }
                 // S of a tile is issued behind the PV of the one before, so O is settled
-                if (warp_live && ok)
-                    softmax_part<D, NG, 128>(tS + 128 * i, tO, scales + 16 * slot, cs, sees, all_see >= 128, j == 0, mm, mo, l, [] {});
+                if (warp_live)
+                    softmax_part<D, GK, 64>(tS + 128 * i + 64 * h, tO + D * i + h * (D / 2), pair, mx_own, mx_other,
+                                            scales + 16 * slot + 4 * h, cs, sees, all_see >= 64, j == 0, mm, mo, l, [] {});
+                tc::tc_fence_before();
+                __syncwarp();
                 if (lane == 0) tc::mbar_arrive(x.bar(B_P, 2 * (t & 1) + i));
+                if (j + 1 < nt) take_v(t + 1, j + 1);
                 s0_phases ^= 1u << stage;
                 sees -= kTileKeys;
                 all_see -= kTileKeys;
@@ -1027,11 +1082,14 @@ __device__ __forceinline__ void softmax(const Ctx& x, const CacheAttnArgs& a, co
         } else {
             for (int j = 0; j < nt; ++j, ++t) {
                 wait(B_S1, stage, ph);
-                if (warp_live && ok)
-                    softmax_part<D, (NG > 1 ? NG / 2 : 1), 64>(tS + 128 * (t & 1) + 64 * i, tO, scales + 16 * slot + 4 * i, cs, sees,
-                                                               all_see >= 64, j == 0, mm, mo, l,
-                                                               [&] { wait(B_PV, (t - 1) & 1, ((t - 1) >> 1) & 1); });
+                if (warp_live)
+                    softmax_part<D, GK, 32>(tS + 128 * (t & 1) + 64 * i + 32 * h, tO + D * i + h * (D / 2), pair, mx_own, mx_other,
+                                            scales + 16 * slot + 4 * i + 2 * h, cs, sees, all_see >= 32, j == 0, mm, mo, l,
+                                            [&] { wait(B_PV, (t - 1) & 1, ((t - 1) >> 1) & 1); });
+                tc::tc_fence_before();
+                __syncwarp();
                 if (lane == 0) tc::mbar_arrive(x.bar(B_P, 2 * (t & 1) + i));
+                if (j + 1 < nt) take_v(t + 1, j + 1);
                 sees -= kTileKeys;
                 all_see -= kTileKeys;
                 slot = slot + 1 == kScaleSlots ? 0 : slot + 1;
@@ -1042,147 +1100,149 @@ __device__ __forceinline__ void softmax(const Ctx& x, const CacheAttnArgs& a, co
             }
         }
         wait(B_PV, (t - 1) & 1, ((t - 1) >> 1) & 1);  // every product of the unit is done
-        int* nan_first = reinterpret_cast<int*>(x.smem + L::kNan) + (seg & 3) * D;
-        int* nan_any = reinterpret_cast<int*>(x.smem + L::kNanAny) + (seg & 3);
-        const bool nans = *nan_any < g.end;
-        ++seg;
+        const Seg g = place->g;
+        const int m = g.m0 + (two ? 128 * i : 0) + row, end = m < g.last ? key_end(g.len, a.block, g.pos0 + m / a.G) : 0;
+        Out out;
+        out.slot_r = slot_rows(a.total_rows, a.G);
+        out.slot = g.whole ? nullptr : slot_at(a.scratch, 2 * (int)blockIdx.x + (g.kt0 > 0 ? 0 : 1), out.slot_r, D);
+        int* nan_first = reinterpret_cast<int*>(g_smem + L::kNan);
+        int* nan_any = reinterpret_cast<int*>(g_smem + L::kNanAny);
         const bool staged = !out.slot && !a.o_f32;
-        if (g.two) {
-            // o = O 2^(mo - m) / l; the S products no longer need the group's Q tile, which takes the rows
-            const bool some = l != 0.f;  // NaN counts as something
-            const float f = some ? ex2f(mo - mm) / l : 0.f;
-            const uint32_t tile = x.sbase + L::kQ + i * 2 * L::kT8;
-#pragma unroll 1
-            for (int q = 0; q < D / 32; ++q) {
-                uint32_t o[32];
-                tc::tmem_ld32(tO + 32 * q, o);
-                tc::tmem_ld_wait();
-                float v[32];
-#pragma unroll
-                for (int e = 0; e < 32; ++e) v[e] = some ? __uint_as_float(o[e]) * f : 0.f;
-                if (nans)
-#pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        if (nan_first[32 * q + e] < end) v[e] = NAN;
-                put_cols<D>(a, g, out, m, row, tile, q, v);
-            }
-            put_lse(a, g, out, D, m, some ? mm + __log2f(l) : -INFINITY);
-            tc::tc_fence_before();
-            if (staged) {
-                group_sync(i);
-                put_rows<D, 128>(a, g, g.m0 + 128 * i, tile, row);
-            }
-        } else {
-            // the groups exchange their sums through S columns (same lanes) and each writes half of the columns
-            tmem_st4(tS + 128 * i, __float_as_uint(mm), __float_as_uint(mo), __float_as_uint(l), 0u);
-            tc::tmem_st_wait();
-            tc::tc_fence_before();
-            softmax_sync();
-            tc::tc_fence_after();
-            uint32_t ot[4];
-            tmem_ld4(tS + 128 * (i ^ 1), ot);
+        // The threads of a row exchange their sums through columns of S (same lanes): (m, mo, l) of group (i, h) at
+        // column 4 (2 i + h), or, in a unit of two MMA tiles, at column 4 h of S_i.
+        const uint32_t tX = tS + (g.two ? 128 * i : 0);
+        tmem_st4(tX + (g.two ? 4 * h : 4 * (2 * i + h)), __float_as_uint(mm), __float_as_uint(mo), __float_as_uint(l), 0u);
+        tc::tmem_st_wait();
+        tc::tc_fence_before();
+        softmax_sync();
+        tc::tc_fence_after();
+        const bool nans = *nan_any < g.end;
+        float mj, f0, f1 = 0.f, lj;
+        bool use0, use1 = false;
+        {
+            uint32_t y[16];
+            tmem_ld16(tX, y);
             tc::tmem_ld_wait();
-            const float m1 = __uint_as_float(ot[0]), mo1 = __uint_as_float(ot[1]), l1 = __uint_as_float(ot[2]);
-            const float mj = fmaxf(mm, m1), moj = fmaxf(mo, mo1);
-            const float lj = (mm == -INFINITY && l == 0.f ? 0.f : l * ex2f(mm - mj)) + (m1 == -INFINITY && l1 == 0.f ? 0.f : l1 * ex2f(m1 - mj));
-            const bool some = lj != 0.f;
-            const float f = some ? ex2f(moj - mj) / lj : 0.f;
-            // this group's and the other's factor; one without keys that the row sees adds nothing
-            const bool use0 = l != 0.f, use1 = l1 != 0.f;
-            const float f0 = use0 ? f * ex2f(mo - moj) : 0.f, f1 = use1 ? f * ex2f(mo1 - moj) : 0.f;
-            const uint32_t tile = x.sbase + L::kQ + 2 * L::kT8;
-            if (warp_live)
-#pragma unroll 1
-                for (int q = i * (D / 64); q < (i + 1) * (D / 64); ++q) {
-                    uint32_t o[32], o1[32];
-                    tc::tmem_ld32(tO + 32 * q, o);
-                    tc::tmem_ld32(tO1 + 32 * q, o1);
-                    tc::tmem_ld_wait();
-                    float v[32];
+            const int n = g.two ? 2 : 4;
+            mj = -INFINITY;
 #pragma unroll
-                    for (int e = 0; e < 32; ++e)
-                        v[e] = (use0 ? __uint_as_float(o[e]) * f0 : 0.f) + (use1 ? __uint_as_float(o1[e]) * f1 : 0.f);
-                    if (nans)
+            for (int e = 0; e < 4; ++e)
+                if (e < n) mj = fmaxf(mj, __uint_as_float(y[4 * e]));
+            lj = 0.f;
 #pragma unroll
-                        for (int e = 0; e < 32; ++e)
-                            if (nan_first[32 * q + e] < end) v[e] = NAN;
-                    put_cols<D>(a, g, out, m, row, tile, q, v);
+            for (int e = 0; e < 4; ++e)
+                if (e < n) {
+                    const float me = __uint_as_float(y[4 * e]), le = __uint_as_float(y[4 * e + 2]);
+                    if (le != 0.f) lj += me == mj ? le : le * ex2f(me - mj);  // NaN counts as something
                 }
-            if (i == 0) put_lse(a, g, out, D, m, some ? mj + __log2f(lj) : -INFINITY);
-            tc::tc_fence_before();
-            if (staged) {
-                softmax_sync();
-                put_rows<D, 256>(a, g, g.m0, tile, threadIdx.x);
+            const float inv = 1.f / lj;  // used only where lj is not 0
+            // o = sum of O_i 2^(mo_i - m) / l over the unit's O of this row; one without keys that the row sees adds nothing
+            use0 = __uint_as_float(y[2]) != 0.f || __uint_as_float(y[6]) != 0.f;
+            f0 = use0 ? ex2f(__uint_as_float(y[1]) - mj) * inv : 0.f;
+            if (!g.two) {
+                use1 = __uint_as_float(y[10]) != 0.f || __uint_as_float(y[14]) != 0.f;
+                f1 = use1 ? ex2f(__uint_as_float(y[9]) - mj) * inv : 0.f;
             }
         }
-        // The next unit's Q may be written once both groups are done with this one. The widening warps are at most two
-        // tiles ahead of the PV products, so they come back to these words only after three more units have begun.
+        // The S products no longer need Q: the rows of tile i take the place of Q tile i (a unit of one tile: the second)
+        const uint32_t tile = sbase() + L::kQ + (g.two ? i : 1) * 2 * L::kT8;
+        const int part = g.two ? h : 2 * i + h, parts = g.two ? 2 : 4;
+        if (warp_live) {
+#pragma unroll 1
+            for (int q = part * (D / 16) / parts; q < (part + 1) * (D / 16) / parts; ++q) {
+                uint32_t o[16], o1[16];
+                tmem_ld16(tO + (g.two ? D * i : 0) + 16 * q, o);
+                if (!g.two) tmem_ld16(tO + D + 16 * q, o1);
+                tc::tmem_ld_wait();
+                float v[16];
+#pragma unroll
+                for (int e = 0; e < 16; ++e)
+                    v[e] = (use0 ? __uint_as_float(o[e]) * f0 : 0.f) + (use1 ? __uint_as_float(o1[e]) * f1 : 0.f);
+                if (nans)
+#pragma unroll 1
+                    for (int e = 0; e < 16; ++e)
+                        if (nan_first[16 * q + e] < end) {
+#pragma unroll
+                            for (int k = 0; k < 16; ++k)
+                                if (k == e) v[k] = NAN;
+                        }
+                put_cols<D>(a, g, out, m, row, tile, q, v);
+            }
+        }
+        if (part == 0) put_lse(a, g, out, D, m, lj != 0.f ? mj + __log2f(lj) : -INFINITY);
+        tc::tc_fence_before();
+        if (staged) {
+            if (g.two) {
+                tile_sync(i);
+                put_rows<D, 256>(a, g, g.m0 + 128 * i, tile, threadIdx.x & 255);
+            } else {
+                softmax_sync();
+                put_rows<D, 512>(a, g, g.m0, tile, threadIdx.x);
+            }
+        }
+        // The next unit's Q may be written once all groups are done with this one, and its values are taken behind one
+        // more of these barriers.
         softmax_sync();
         if (nans && threadIdx.x < D) nan_first[threadIdx.x] = *nan_any = 0x7fffffff;
     }
 }
 
 // ------------------------------------------------------------------- kernel
-template <int D, int NG>
+template <int D, int GK>
 __global__ void __launch_bounds__(kThreads, 1)
     cache_attn_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, const CacheAttnArgs a) {
     using L = Smem<D>;
-    extern __shared__ __align__(1024) uint8_t smem[];
-    Ctx x;
-    x.smem = smem;
-    x.sbase = tc::smem_addr(smem);
-    x.bars = x.sbase + L::kBar;
-    x.words = reinterpret_cast<int*>(smem + L::kWords);
-    Start* st = reinterpret_cast<Start*>(smem + L::kStart);
+    Ctx<D> x;
+    Start* st = reinterpret_cast<Start*>(g_smem + L::kStart);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    for (int i = tid; i < 4 * D + 4; i += kThreads) reinterpret_cast<int*>(smem + L::kNan)[i] = 0x7fffffff;
+    for (int i = tid; i < D + 1; i += kThreads) reinterpret_cast<int*>(g_smem + L::kNan)[i] = 0x7fffffff;
     if (tid == 0) {
-        x.words[1] = x.words[2] = x.words[3] = 0;
+        x.words()[1] = x.words()[2] = 0;
         for (int s = 0; s < kStages; ++s) {
             tc::mbar_init(x.bar(B_KFULL, s), 1);
-            tc::mbar_init(x.bar(B_VFULL, s), 1);
-            tc::mbar_init(x.bar(B_VEMPTY, s), 4);  // lane 0 of the widening warps
             tc::mbar_init(x.bar(B_S0, s), 1);
             tc::mbar_init(x.bar(B_S1, s), 1);
         }
         for (int s = 0; s < 2; ++s) {
-            tc::mbar_init(x.bar(B_P, 2 * s), 8);  // lane 0 of group 0's warps and of the widening warps
-            tc::mbar_init(x.bar(B_P, 2 * s + 1), 4);
+            tc::mbar_init(x.bar(B_VFULL, s), 1);
+            tc::mbar_init(x.bar(B_VEMPTY, s), kSoftmax / 32);
+            tc::mbar_init(x.bar(B_W, s), kSoftmax / 32);
+            tc::mbar_init(x.bar(B_P, 2 * s), kSoftmax / 64);
+            tc::mbar_init(x.bar(B_P, 2 * s + 1), kSoftmax / 64);
             tc::mbar_init(x.bar(B_PV, s), 1);
         }
-        tc::mbar_init(x.bar(B_Q, 0), 8);
+        tc::mbar_init(x.bar(B_Q, 0), kSoftmax / 32);
         tc::fence_barrier_init();
     }
-    if (warp == 9) {
-        tc::tmem_alloc(tc::smem_addr(x.words), kTmemCols);
+    if (warp == 17) {
+        tc::tmem_alloc(tc::smem_addr(x.words()), kTmemCols);
         tc::tmem_relinquish();
     }
-    if (warp == 8 && lane == 0) {
+    if (warp == 16 && lane == 0) {
         tc::prefetch_tmap(&tk);
         tc::prefetch_tmap(&tv);
     }
-    find_start(a, st, reinterpret_cast<long long*>(smem));  // the scan's words lie where Q will
+    find_start(a, st, reinterpret_cast<long long*>(g_smem));  // the scan's words lie where Q will
     tc::tc_fence_before();
     __syncthreads();
     tc::tc_fence_after();
-    x.tmem = (uint32_t)x.words[0];
-    const bool aligned = (x.sbase & 1023u) == 0;  // the swizzled tiles need it; a launch that has not is refused
-    if (tid == 0 && !aligned) x.words[1] = 1;
+    x.tmem = (uint32_t)x.words()[0];
+    const bool aligned = (sbase() & 1023u) == 0;  // the swizzled tiles need it; a launch that has not is refused
+    if (tid == 0 && !aligned) x.words()[1] = 1;
     if (st->left > 0 && aligned) {
-        if (warp >= 8) {
+        if (warp >= 16) {
             tc::regs_dec<kRegsOther>();
-            if (warp == 8) produce<D>(x, a, *st, &tk, &tv);
-            else if (warp == 9) issue<D>(x, a, *st);
-            else if (warp >= 12) widen<D>(x, a, *st);
+            if (warp == 16) produce<D>(x, a, *st, &tk, &tv);
+            else if (warp == 17) issue<D>(x, a, *st);
         } else {
             tc::regs_inc<kRegsSoftmax>();
-            softmax<D, NG>(x, a, *st);
+            softmax<D, GK>(x, a, *st);
         }
     }
     tc::tc_fence_before();
     __syncthreads();
-    if (warp == 9) {
+    if (warp == 17) {
         tc::tc_fence_after();
         tc::tmem_dealloc(x.tmem, kTmemCols);
     }
@@ -1202,7 +1262,7 @@ __global__ void __launch_bounds__(kThreads, 1)
             r.off = st->off;
             r.cost = unit_of(a, q, st->m0).cost();
         }
-        r.error = x.words[1] ? DEV_TIMEOUT : st->bad != 0x7fffffff ? DEV_CHECK : x.words[2];
+        r.error = x.words()[1] ? DEV_TIMEOUT : st->bad != 0x7fffffff ? DEV_CHECK : x.words()[2];
         r.info = st->bad != 0x7fffffff ? st->bad : (int)blockIdx.x;
         share_recs(a.scratch)[blockIdx.x] = r;
     }
@@ -1239,24 +1299,19 @@ bool make_map(CUtensorMap* m, const CacheView& c, const void* base) {
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, int NG>
-cudaError_t launch_ng(const CacheAttnArgs& a, int ctas, cudaStream_t st) {
+template <int D, int GK>
+cudaError_t launch_gk(const CacheAttnArgs& a, int ctas, cudaStream_t st) {
     CUtensorMap tk, tv;
     if (!make_map<D>(&tk, a.c, a.c.k) || !make_map<D>(&tv, a.c, a.c.v)) return cudaErrorInvalidValue;
-    const cudaError_t e = cudaFuncSetAttribute(cache_attn_kernel<D, NG>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::kBytes);
+    const cudaError_t e = cudaFuncSetAttribute(cache_attn_kernel<D, GK>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::kBytes);
     if (e != cudaSuccess) return e;
-    cache_attn_kernel<D, NG><<<ctas, kThreads, Smem<D>::kBytes, st>>>(tk, tv, a);
+    cache_attn_kernel<D, GK><<<ctas, kThreads, Smem<D>::kBytes, st>>>(tk, tv, a);
     return cudaGetLastError();
 }
 
 template <int D>
 cudaError_t launch_d(const CacheAttnArgs& a, int ctas, cudaStream_t st) {
-    switch (a.c.page) {
-        case 16: return launch_ng<D, 8>(a, ctas, st);
-        case 32: return launch_ng<D, 4>(a, ctas, st);
-        case 64: return launch_ng<D, 2>(a, ctas, st);
-        default: return launch_ng<D, 1>(a, ctas, st);
-    }
+    return a.c.page == 16 ? launch_gk<D, 16>(a, ctas, st) : launch_gk<D, 32>(a, ctas, st);
 }
 
 }  // namespace cattn
