@@ -21,14 +21,14 @@
 // for up to 128 flat rows, so these calls are bound by memory, and calls with
 // 256 and more flat rows by the tensor pipe.
 //
-// Roles (640 threads, one CTA per SM, each role walks the CTA's share alone):
+// Roles (768 threads, one CTA per SM, each role walks the CTA's share alone):
 //   warps 0-15   softmax, in four groups (i, h); one TMEM lane = one flat row.
-//                They also split Q into its two terms, widen V from e4m3 to
-//                fp16 (zero the rows behind the last key, take out masked NaN)
-//                and write the results
+//                They also split Q into its two terms, and write the results
 //   warp 16      page table, scales and TMA loads of K (3 stages) and V (2)
 //   warp 17      issues the MMAs (one elected lane), owns TMEM
 //   warps 18-19  spare
+//   warps 20-23  widen V from e4m3 to fp16 (2 stages), zero the rows behind
+//                the last key and take out masked NaN
 // A unit of up to 128 flat rows is one MMA tile: its products with the values
 // of keys 64 i .. of every tile add up in O_i, and group (i, h) takes the 32
 // keys from 64 i + 32 h on. Two S buffers take turns, so that a tile's softmax
@@ -52,13 +52,13 @@
 namespace bdlm {
 namespace cattn {
 
-constexpr int kThreads = 640;
+constexpr int kThreads = 768;
 constexpr int kSoftmax = 512;
-// 20 warps at 96 registers each, redistributed. What a role keeps beyond its registers would be spilled to an L1 that
+// 24 warps at 80 registers each, redistributed. What a role keeps beyond its registers would be spilled to an L1 that
 // shared memory leaves next to no room.
-constexpr int kRegsSoftmax = 104;
-constexpr int kRegsOther = 64;
-static_assert(16 * kRegsSoftmax + 4 * kRegsOther <= 20 * 96, "registers");
+constexpr int kRegsSoftmax = 96;
+constexpr int kRegsOther = 48;
+static_assert(16 * kRegsSoftmax + 8 * kRegsOther <= 24 * 80, "registers");
 constexpr int kTmemCols = 512;
 constexpr int kStages = 3;  // of K; V has two as e4m3 and two as fp16
 constexpr int kScaleSlots = 6;
@@ -70,11 +70,10 @@ enum : int {
     B_VFULL = 3, B_VEMPTY = 5,  // t & 1
     B_S0 = 7,                   // t % 3: the first S of a unit of two MMA tiles
     B_S1 = 10,                  // t % 3: the tile's last S; it also frees the K stage
-    B_P = 13,                   // 2 (t & 1) + i: p' for O_i in TMEM; in a unit of one MMA tile also V for O_i in fp16
-    B_W = 17,                   // t & 1: V in fp16
-    B_PV = 19,                  // t & 1: the tile's products with V; frees the fp16 stage
-    B_Q = 21,
-    B_COUNT = 22
+    B_P = 13,                   // 2 (t & 1) + i: p' for O_i in TMEM; for O_0 also V in fp16
+    B_PV = 17,                  // t & 1: the tile's products with V; frees the fp16 stage
+    B_Q = 19,
+    B_COUNT = 20
 };
 
 template <int D>
@@ -86,8 +85,8 @@ struct Smem {
     static constexpr int kV = kK + kStages * kT8;  // 2 stages
     static constexpr int kMisc = kV + 2 * kT8;
     static constexpr int kScale = kMisc;                          // float [slots][16]: ks, log2 vs of 16-key groups
-    static constexpr int kNan = kScale + kScaleSlots * 64;        // int [D]: first key whose value is NaN, per column
-    static constexpr int kNanAny = kNan + D * 4;                  // int: first key with a NaN in any column
+    static constexpr int kNan = kScale + kScaleSlots * 64;        // int [4][D]: first key whose value is NaN, per column
+    static constexpr int kNanAny = kNan + 4 * D * 4;              // int [4]: first key with a NaN in any column
     static constexpr int kMax = kNanAny + 16;                     // float [8 pairs][2][32]: maxima that partners exchange
     static constexpr int kBar = kMax + 2048;
     static constexpr int kWords = kBar + B_COUNT * 8;             // tmem, abort, error, info
@@ -119,8 +118,7 @@ struct Place {
     Unit u;
     int s, h, m0, off;
     long long left;
-    Seg g;    // the present run
-    int all;  // keys that every row of its unit sees
+    Seg g;  // the present run
 };
 static_assert(sizeof(Place) <= 128, "");
 
@@ -289,12 +287,20 @@ __device__ __forceinline__ uint32_t sbase() { return tc::smem_addr(g_smem); }
 template <int D>
 struct Ctx {
     using L = Smem<D>;
-    uint32_t tmem;
-    __device__ __forceinline__ uint32_t bar(int base, int i) const { return sbase() + L::kBar + 8 * (base + i); }
+    uint32_t tmem, base;
+    // Values of the role's own: the compiler would else compute what the roles have in common before it branches into
+    // them, and carry it through all of them in registers that they do not have.
+    __device__ __forceinline__ Ctx own() const {
+        Ctx c;
+        asm volatile("mov.u32 %0, %1;" : "=r"(c.tmem) : "r"(tmem));
+        asm volatile("mov.u32 %0, %1;" : "=r"(c.base) : "r"(base));
+        return c;
+    }
+    __device__ __forceinline__ uint32_t bar(int b, int i) const { return base + L::kBar + 8 * (b + i); }
     static __device__ __forceinline__ int* words() { return reinterpret_cast<int*>(g_smem + L::kWords); }  // tmem, abort, error
     // bounded wait; false once any role has given up
-    __device__ __forceinline__ bool wait(int base, int i, uint32_t parity) const {
-        return tc::mbar_wait(bar(base, i), parity, words() + 1, kTimeoutNs);
+    __device__ __forceinline__ bool wait(int b, int i, uint32_t parity) const {
+        return tc::mbar_wait(bar(b, i), parity, words() + 1, kTimeoutNs);
     }
     // The warp's place in the share. It lies in shared memory: every lane of a warp has the same, it changes once per
     // unit, and registers that hold it through the tile loops would be spilled, to an L1 that has next to no room.
@@ -536,8 +542,8 @@ __device__ __forceinline__ void produce(const Ctx<D>& x, const CacheAttnArgs& a,
             __syncwarp();
             if (load) {
                 const uint32_t off = (lane & 7) * 16 * D;
-                tc::tma_load_3d(sbase() + L::kK + stage * L::kT8 + off, tk, x.bar(B_KFULL, stage), 0, 0, b0.id * a.c.Hk + b0.h);
-                tc::tma_load_3d(sbase() + L::kV + vs * L::kT8 + off, tv, x.bar(B_VFULL, vs), 0, 0, b0.id * a.c.Hk + b0.h);
+                tc::tma_load_3d(x.base + L::kK + stage * L::kT8 + off, tk, x.bar(B_KFULL, stage), 0, 0, b0.id * a.c.Hk + b0.h);
+                tc::tma_load_3d(x.base + L::kV + vs * L::kT8 + off, tv, x.bar(B_VFULL, vs), 0, 0, b0.id * a.c.Hk + b0.h);
             }
             __syncwarp();
         }
@@ -558,145 +564,188 @@ __device__ __forceinline__ void produce(const Ctx<D>& x, const CacheAttnArgs& a,
 }
 
 // ------------------------------------------------------------ V: e4m3 -> fp16
-// Tile t's values, by the softmax warps: thread `id` of the 256 with the same i takes keys 64 i .. 64 i + 63, which are
-// the ones that O_i's products read in a unit of one MMA tile. Keys from `valid` on become zeros; with `check` NaN
-// codes do too, and their first key is noted for each column (`key0`: the tile's first key).
 template <int D>
-__device__ __forceinline__ void widen(uint32_t t, int i, int id, int valid, bool check, int key0) {
+__device__ __forceinline__ void widen(const Ctx<D>& x, const CacheAttnArgs& a, const Start& st) {
     using L = Smem<D>;
-    constexpr int PER = D / 16, ROWS = 256 / PER;  // 16-byte chunks per key, keys per step
-    const int c = id % PER;
-    uint32_t v[64 / ROWS][4];
+    constexpr int PER = D / 16;                  // 16-byte chunks per key
+    constexpr int ROWS = 4 * (32 / PER);         // keys that the four warps take at a time
+    constexpr int STEPS = kTileKeys / ROWS, HALF = STEPS / 2;
+    const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) - 20;
+    const int c = lane % PER, r0 = lane / PER + warp * (32 / PER);
+    // 16 columns are two 16-byte chunks of the 64-column half they lie in; the lanes of the upper half store theirs in
+    // the other order, so that eight lanes meet eight bank groups. The rows of a thread are ROWS (a multiple of 8)
+    // apart, so its swizzle is the same in every step.
+    const uint32_t src0 = x.base + L::kV + swz8<D>(r0, c);
+    const uint32_t row_dst = x.base + L::kW + (c >> 2) * 16384 + r0 * 128;
+    const bool swap = c >= 4;
+    const uint32_t d0 = row_dst + ((((2 * c + (swap ? 1 : 0)) & 7) ^ (r0 & 7)) << 4);
+    const uint32_t d1 = row_dst + ((((2 * c + (swap ? 0 : 1)) & 7) ^ (r0 & 7)) << 4);
+    Place* place = x.place();
+    begin_share(a, st, place);
+    uint32_t t = 0, seg = 0;
+    while (next_run(a, place)) {
+        if (place->g.tiles() == 0) continue;
+        // keys that every row of the unit sees; a NaN among the others must not reach a row that does not see it
+        const int all = key_end(place->g.len, a.block, place->g.pos0 + place->g.m0 / a.G), end = place->g.end, kt1 = place->g.kt1;
+        for (int kt = place->g.kt0; kt < kt1; ++kt, ++t) {
+            const uint32_t ws = t & 1;
+            bool ok = x.wait(B_VFULL, ws, (t >> 1) & 1);
+            const int valid = imin(kTileKeys, end - kt * kTileKeys);
+            const bool check = valid < kTileKeys || kt * kTileKeys + valid > all;
 #pragma unroll
-    for (int j = 0; j < 64 / ROWS; ++j) lds16(sbase() + L::kV + (t & 1) * L::kT8 + swz8<D>(64 * i + j * ROWS + id / PER, c), v[j]);
-    if (check) {
+            for (int half = 0; half < 2; ++half) {
+                uint32_t v[HALF][4];
 #pragma unroll
-        for (int j = 0; j < 64 / ROWS; ++j) {
-            const int r = 64 * i + j * ROWS + id / PER;
-            if (r >= valid) v[j][0] = v[j][1] = v[j][2] = v[j][3] = 0;
-            uint32_t any = 0;
+                for (int j = 0; j < HALF; ++j) lds16(src0 + ws * L::kT8 + (half * HALF + j) * ROWS * D, v[j]);
+                if (half == 0) {
+                    ok = ok && x.wait(B_PV, ws, ((t >> 1) & 1) ^ 1);
+                    if (!__all_sync(0xffffffffu, ok)) return;
+                }
+                if (check) {
 #pragma unroll
-            for (int e = 0; e < 4; ++e) any |= ((v[j][e] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
-            if (any) {
+                    for (int j = 0; j < HALF; ++j) {
+                        const int r = (half * HALF + j) * ROWS + r0;
+                        if (r >= valid) v[j][0] = v[j][1] = v[j][2] = v[j][3] = 0;
+                        uint32_t any = 0;
 #pragma unroll
-                for (int e = 0; e < 16; ++e) {
-                    const uint32_t sh = 8 * (e & 3);
-                    if (((v[j][e >> 2] >> sh) & 0x7f) == 0x7f) {
-                        atomicMin(reinterpret_cast<int*>(g_smem + L::kNan) + 16 * c + e, key0 + r);
-                        atomicMin(reinterpret_cast<int*>(g_smem + L::kNanAny), key0 + r);
-                        v[j][e >> 2] &= ~(0xffu << sh);
+                        for (int e = 0; e < 4; ++e) any |= ((v[j][e] & 0x7f7f7f7fu) + 0x01010101u) & 0x80808080u;
+                        if (any) {
+                            int* nan_first = reinterpret_cast<int*>(g_smem + L::kNan) + (seg & 3) * D + 16 * c;
+                            atomicMin(reinterpret_cast<int*>(g_smem + L::kNanAny) + (seg & 3), kt * kTileKeys + r);
+#pragma unroll
+                            for (int e = 0; e < 16; ++e) {
+                                const uint32_t sh = 8 * (e & 3);
+                                if (((v[j][e >> 2] >> sh) & 0x7f) == 0x7f) {
+                                    atomicMin(nan_first + e, kt * kTileKeys + r);
+                                    v[j][e >> 2] &= ~(0xffu << sh);
+                                }
+                            }
+                        }
                     }
                 }
+#pragma unroll
+                for (int j = 0; j < HALF; ++j) {
+                    const uint32_t to = ws * 2 * L::kT8 + (half * HALF + j) * ROWS * 128;
+                    uint32_t h[8];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) widen4(v[j][e], h[2 * e], h[2 * e + 1]);
+                    sts16(d0 + to, swap ? h[4] : h[0], swap ? h[5] : h[1], swap ? h[6] : h[2], swap ? h[7] : h[3]);
+                    sts16(d1 + to, swap ? h[0] : h[4], swap ? h[1] : h[5], swap ? h[2] : h[6], swap ? h[3] : h[7]);
+                }
+            }
+            tc::fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) {
+                tc::mbar_arrive(x.bar(B_VEMPTY, ws));
+                tc::mbar_arrive(x.bar(B_P, 2 * ws));
             }
         }
-    }
-#pragma unroll
-    for (int j = 0; j < 64 / ROWS; ++j) {
-        const int r = 64 * i + j * ROWS + id / PER;
-        uint32_t h[8];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) widen4(v[j][e], h[2 * e], h[2 * e + 1]);
-        // 16 columns are two 16-byte chunks of the 64-column half they lie in; the lanes of the upper half store theirs
-        // in the other order, so that eight lanes meet eight bank groups
-        const uint32_t dst = sbase() + L::kW + (t & 1) * 2 * L::kT8 + (c >> 2) * 16384 + r * 128;
-        const bool swap = c >= 4;
-        const uint32_t d0 = dst + ((((2 * c + (swap ? 1 : 0)) & 7) ^ (r & 7)) << 4);
-        const uint32_t d1 = dst + ((((2 * c + (swap ? 0 : 1)) & 7) ^ (r & 7)) << 4);
-        sts16(d0, swap ? h[4] : h[0], swap ? h[5] : h[1], swap ? h[6] : h[2], swap ? h[7] : h[3]);
-        sts16(d1, swap ? h[0] : h[4], swap ? h[1] : h[5], swap ? h[2] : h[6], swap ? h[3] : h[7]);
+        ++seg;
     }
 }
 
 // ---------------------------------------------------------------------- MMA
-// The whole warp walks the share, so that addresses and descriptors are warp-
-// uniform values; one elected lane issues. The tensor pipe queues little, so
-// what stands between two groups of MMAs is kept short: one wait for a tile's
-// keys, one for p' of each O (and one for the values, where p' does not count
-// them) and one commit for each S and each PV.
+// The whole warp walks the share, and everything that an address or a
+// descriptor is made of is warp-uniform to the compiler too (constants, counts
+// and results of reductions), so that it keeps them in uniform registers, where
+// the MMA reads them; one elected lane issues. The tensor pipe queues little,
+// so what stands between two groups of MMAs is kept short: one wait for a
+// tile's keys, one for p' of each O (which counts the fp16 values as well) and
+// one commit for each S and each PV.
 template <int D>
-__device__ __forceinline__ void issue(const Ctx<D>& x, const CacheAttnArgs& a, const Start& st) {
+__device__ __forceinline__ void issue(const CacheAttnArgs& a, const Start& st) {
     using L = Smem<D>;
     constexpr uint32_t id_s = idesc_fmt0(128, kTileKeys, 0), id_o = idesc_fmt0(128, D, 1);
-    const uint32_t tmem = __shfl_sync(0xffffffffu, x.tmem, 0);
+    Ctx<D> x;
+    x.tmem = 0;  // all of TMEM is this CTA's (the kernel has checked it)
+    x.base = sbase();
     const uint64_t k8 = sdesc_k8<D>(sbase()), mn = tc::sdesc_sw128(sbase(), 16384, 1024);
     const bool leader = elect_one();
     auto wait = [&](int base, int i, uint32_t parity) { return __all_sync(0xffffffffu, x.wait(base, i, parity)) != 0; };
-    // S of tile t from Q tile qt into S buffer b
-    auto issue_s = [&](uint32_t t, uint32_t qt, uint32_t b, uint32_t bar) {
-        const uint32_t stage = t % kStages;
-        const uint64_t dk = tc::sdesc_add(k8, L::kK + stage * L::kT8);
-        const uint64_t dq = tc::sdesc_add(k8, L::kQ + qt * 2 * L::kT8);
-        const uint32_t to = tmem + 128 * b;
+    // S of the tile in K stage `stage`, from Q tile qt into S buffer b
+    auto issue_s = [&](uint32_t stage, uint32_t qt, uint32_t b, int bar) {
+        const uint64_t dk = tc::sdesc_add(k8, L::kK + stage * L::kT8), dq = tc::sdesc_add(k8, L::kQ + qt * 2 * L::kT8);
         if (leader) {
 #pragma unroll
             for (int k = 0; k < 2 * D / 32; ++k)  // the high terms, then the low ones
-                mma_ss_f8(to, tc::sdesc_add(dq, k * 32 < D ? k * 32 : L::kT8 + k * 32 - D), tc::sdesc_add(dk, k * 32 % D), id_s, k > 0);
+                mma_ss_f8(128 * b, tc::sdesc_add(dq, k * 32 < D ? k * 32 : L::kT8 + k * 32 - D), tc::sdesc_add(dk, k * 32 % D), id_s, k > 0);
             tc::mma_commit(x.bar(bar, stage));
         }
     };
-    // 2 N steps of p' times the fp16 values from key `key` on, into O buffer o: N steps from TMEM column p on, which the
-    // groups (o, 0) wrote, and N from column p + 16 N on
-    auto issue_pv = [&](uint32_t t, uint32_t p, uint32_t o, int key, auto steps, bool fresh) {
+    // 2 N steps of p' times the fp16 values in stage b from key `key` on, into O buffer o: N steps from TMEM column p on,
+    // which the groups (o, 0) wrote, and N from column p + 16 N on
+    auto issue_pv = [&](uint32_t b, uint32_t p, uint32_t o, int key, auto steps, bool fresh) {
         constexpr int N = decltype(steps)::value;
-        const uint64_t dv = tc::sdesc_add(mn, L::kW + (t & 1) * 2 * L::kT8 + key * 128);
-        const uint32_t to = tmem + 256 + D * o, from = tmem + p;
+        const uint64_t dv = tc::sdesc_add(mn, L::kW + b * 2 * L::kT8 + key * 128);
         if (leader) {
 #pragma unroll
             for (int k = 0; k < 2 * N; ++k)
-                tc::mma_ts(to, from + 16 * N * (k / N) + 8 * (k % N), tc::sdesc_add(dv, 2048 * k), id_o, (k > 0 || !fresh) ? 1u : 0u);
+                tc::mma_ts(256 + D * o, p + 16 * N * (k / N) + 8 * (k % N), tc::sdesc_add(dv, 2048 * k), id_o, (k > 0 || !fresh) ? 1u : 0u);
+        }
+    };
+    auto up = [](uint32_t& stage, uint32_t& ph) {  // the next stage of a ring of three, and its phase
+        if (++stage == kStages) {
+            stage = 0;
+            ph ^= 1;
         }
     };
     Place* place = x.place();
     begin_share(a, st, place);
-    uint32_t t0 = 0, seg = 0;
-    while (next_run(a, place)) {
-        const int nt = __shfl_sync(0xffffffffu, place->g.tiles(), 0);
+    uint32_t b = 0, ph = 0;            // t & 1 and (t >> 1) & 1 of the tile whose p' comes next
+    uint32_t stage = 0, ks = 0, q = 0;  // the K stage whose keys come next, its phase, and Q's
+    while (__any_sync(0xffffffffu, next_run(a, place))) {
+        const int nt = __reduce_max_sync(0xffffffffu, place->g.tiles());
         if (nt == 0) continue;
-        const bool two = __shfl_sync(0xffffffffu, (int)place->g.two, 0) != 0;
-        if (!wait(B_Q, 0, seg & 1)) return;
-        ++seg;
+        const int two = __reduce_max_sync(0xffffffffu, (int)place->g.two);
+        if (!wait(B_Q, 0, q)) return;
+        q ^= 1;
         tc::tc_fence_after();
         if (two) {
-            if (!wait(B_KFULL, t0 % kStages, (t0 / kStages) & 1)) return;
-            issue_s(t0, 0, 0, B_S0);
-            issue_s(t0, 1, 1, B_S1);
+            if (!wait(B_KFULL, stage, ks)) return;
+            issue_s(stage, 0, 0, B_S0);
+            issue_s(stage, 1, 1, B_S1);
+            up(stage, ks);
             for (int j = 0; j < nt; ++j) {
-                const uint32_t t = t0 + j, b = t & 1, ph = (t >> 1) & 1;
                 const bool more = j + 1 < nt;
-                if (!wait(B_W, b, ph)) return;
 #pragma unroll
                 for (uint32_t i = 0; i < 2; ++i) {
                     if (!wait(B_P, 2 * b + i, ph)) return;
                     tc::tc_fence_after();
-                    issue_pv(t, 128 * i, i, 0, Const<4>{}, j == 0);
+                    issue_pv(b, 128 * i, i, 0, Const<4>{}, j == 0);
                     if (i == 1 && leader) tc::mma_commit(x.bar(B_PV, b));
-                    if (i == 0 && more && !wait(B_KFULL, (t + 1) % kStages, ((t + 1) / kStages) & 1)) return;
-                    if (more) issue_s(t + 1, i, i, i == 0 ? B_S0 : B_S1);
+                    if (more) {
+                        if (i == 0 && !wait(B_KFULL, stage, ks)) return;
+                        issue_s(stage, i, i, i == 0 ? B_S0 : B_S1);
+                    }
                 }
+                if (more) up(stage, ks);
+                ph ^= b;
+                b ^= 1;
             }
         } else {
-#pragma unroll
-            for (int j = 0; j < 2; ++j)
-                if (j < nt) {
-                    const uint32_t t = t0 + j;
-                    if (!wait(B_KFULL, t % kStages, (t / kStages) & 1)) return;
-                    issue_s(t, 0, t & 1, B_S1);
-                }
+#pragma unroll 1
+            for (int j = 0; j < 2 && j < nt; ++j) {
+                if (!wait(B_KFULL, stage, ks)) return;
+                issue_s(stage, 0, b ^ j, B_S1);
+                up(stage, ks);
+            }
             for (int j = 0; j < nt; ++j) {
-                const uint32_t t = t0 + j, b = t & 1, ph = (t >> 1) & 1;
-                const bool more = j + 2 < nt;
 #pragma unroll
                 for (uint32_t i = 0; i < 2; ++i) {  // each half of the keys into its own O
                     if (!wait(B_P, 2 * b + i, ph)) return;
                     tc::tc_fence_after();
-                    issue_pv(t, 128 * b + 64 * i, i, 64 * i, Const<2>{}, j == 0);
+                    issue_pv(b, 128 * b + 64 * i, i, 64 * i, Const<2>{}, j == 0);
                 }
                 if (leader) tc::mma_commit(x.bar(B_PV, b));
-                if (more && !wait(B_KFULL, (t + 2) % kStages, ((t + 2) / kStages) & 1)) return;
-                if (more) issue_s(t + 2, 0, b, B_S1);
+                if (j + 2 < nt) {
+                    if (!wait(B_KFULL, stage, ks)) return;
+                    issue_s(stage, 0, b, B_S1);
+                    up(stage, ks);
+                }
+                ph ^= b;
+                b ^= 1;
             }
         }
-        t0 += nt;
     }
 }
 
@@ -764,7 +813,7 @@ __device__ __forceinline__ void split_q(const Ctx<D>& x, const CacheAttnArgs& a,
                 lo[e] = narrow4(f0 - h0.x, f1 - h0.y, f2 - h1.x, f3 - h1.y);
             }
             if (r < padded) {
-                const uint32_t at = sbase() + L::kQ + (r >> 7) * 2 * L::kT8 + swz8<D>(r & 127, chunk >> 1) + 8 * (chunk & 1);
+                const uint32_t at = x.base + L::kQ + (r >> 7) * 2 * L::kT8 + swz8<D>(r & 127, chunk >> 1) + 8 * (chunk & 1);
                 sts8(at, hi[0], hi[1]);
                 sts8(at + L::kT8, lo[0], lo[1]);
                 if (chunk == 0) exps[r] = fine ? (uint8_t)(sc >> 23) : (uint8_t)255;
@@ -990,23 +1039,11 @@ __device__ __forceinline__ void softmax(const Ctx<D>& x, const CacheAttnArgs& a,
     begin_share(a, st, place);
     float* const mx_own = reinterpret_cast<float*>(g_smem + L::kMax) + pair * 64 + 32 * h + lane;
     const float* const mx_other = reinterpret_cast<const float*>(g_smem + L::kMax) + pair * 64 + 32 * (h ^ 1) + lane;
-    uint32_t t = 0, s0_phases = 0;  // s0_phases: bit of each B_S0 stage's next phase
+    uint32_t t = 0, seg = 0, s0_phases = 0;  // s0_phases: bit of each B_S0 stage's next phase
     bool ok = true;  // warp-uniform; once it is false the loops run on without waiting, through the same barriers
     auto wait = [&](int base, int n, uint32_t parity) {
         if (ok) ok = __all_sync(0xffffffffu, x.wait(base, n, parity));
         tc::tc_fence_after();
-    };
-    // the values of tile j of the run, which is tile n of the share
-    auto take_v = [&](uint32_t n, int j) {
-        if (ok) ok = __all_sync(0xffffffffu, x.wait(B_VFULL, n & 1, (n >> 1) & 1) && x.wait(B_PV, n & 1, ((n >> 1) & 1) ^ 1));
-        const int key0 = (place->g.kt0 + j) * kTileKeys, valid = imin(kTileKeys, place->g.end - key0);
-        widen<D>(n, i, threadIdx.x & 255, valid, valid < kTileKeys || key0 + valid > place->all, key0);
-        tc::fence_proxy_async_smem();
-        __syncwarp();
-        if (lane == 0) {
-            tc::mbar_arrive(x.bar(B_VEMPTY, n & 1));
-            tc::mbar_arrive(x.bar(B_W, n & 1));
-        }
     };
     while (next_run(a, place)) {
         const int nt = place->g.tiles();
@@ -1048,11 +1085,7 @@ __device__ __forceinline__ void softmax(const Ctx<D>& x, const CacheAttnArgs& a,
             // fewest) does
             sees = end - g.kt0 * kTileKeys - (two ? 64 * h : 64 * i + 32 * h);
             all_see = __shfl_sync(0xffffffffu, sees, 0);
-            // keys that every row of the unit sees; a NaN among the others must not reach a row that does not see it
-            place->all = imin(key_end(g.len, a.block, g.pos0 + g.m0 / a.G), g.end);
-            __syncwarp();
         }
-        take_v(t, 0);
         float mm = -INFINITY, mo = -INFINITY, l = 0.f;
         uint32_t stage = t % kStages, ph = (t / kStages) & 1, slot = t % kScaleSlots;
         if (two) {
@@ -1069,7 +1102,6 @@ __device__ __forceinline__ void softmax(const Ctx<D>& x, const CacheAttnArgs& a,
                 tc::tc_fence_before();
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(x.bar(B_P, 2 * (t & 1) + i));
-                if (j + 1 < nt) take_v(t + 1, j + 1);
                 s0_phases ^= 1u << stage;
                 sees -= kTileKeys;
                 all_see -= kTileKeys;
@@ -1089,7 +1121,6 @@ __device__ __forceinline__ void softmax(const Ctx<D>& x, const CacheAttnArgs& a,
                 tc::tc_fence_before();
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(x.bar(B_P, 2 * (t & 1) + i));
-                if (j + 1 < nt) take_v(t + 1, j + 1);
                 sees -= kTileKeys;
                 all_see -= kTileKeys;
                 slot = slot + 1 == kScaleSlots ? 0 : slot + 1;
@@ -1105,8 +1136,9 @@ __device__ __forceinline__ void softmax(const Ctx<D>& x, const CacheAttnArgs& a,
         Out out;
         out.slot_r = slot_rows(a.total_rows, a.G);
         out.slot = g.whole ? nullptr : slot_at(a.scratch, 2 * (int)blockIdx.x + (g.kt0 > 0 ? 0 : 1), out.slot_r, D);
-        int* nan_first = reinterpret_cast<int*>(g_smem + L::kNan);
-        int* nan_any = reinterpret_cast<int*>(g_smem + L::kNanAny);
+        int* nan_first = reinterpret_cast<int*>(g_smem + L::kNan) + (seg & 3) * D;
+        int* nan_any = reinterpret_cast<int*>(g_smem + L::kNanAny) + (seg & 3);
+        ++seg;
         const bool staged = !out.slot && !a.o_f32;
         // The threads of a row exchange their sums through columns of S (same lanes): (m, mo, l) of group (i, h) at
         // column 4 (2 i + h), or, in a unit of two MMA tiles, at column 4 h of S_i.
@@ -1145,7 +1177,7 @@ __device__ __forceinline__ void softmax(const Ctx<D>& x, const CacheAttnArgs& a,
             }
         }
         // The S products no longer need Q: the rows of tile i take the place of Q tile i (a unit of one tile: the second)
-        const uint32_t tile = sbase() + L::kQ + (g.two ? i : 1) * 2 * L::kT8;
+        const uint32_t tile = x.base + L::kQ + (g.two ? i : 1) * 2 * L::kT8;
         const int part = g.two ? h : 2 * i + h, parts = g.two ? 2 : 4;
         if (warp_live) {
 #pragma unroll 1
@@ -1180,8 +1212,8 @@ __device__ __forceinline__ void softmax(const Ctx<D>& x, const CacheAttnArgs& a,
                 put_rows<D, 512>(a, g, g.m0, tile, threadIdx.x);
             }
         }
-        // The next unit's Q may be written once all groups are done with this one, and its values are taken behind one
-        // more of these barriers.
+        // The next unit's Q may be written once all groups are done with this one. The widening warps are at most two
+        // tiles ahead of the PV products, so they come back to these words only after three more units have begun.
         softmax_sync();
         if (nans && threadIdx.x < D) nan_first[threadIdx.x] = *nan_any = 0x7fffffff;
     }
@@ -1193,10 +1225,11 @@ __global__ void __launch_bounds__(kThreads, 1)
     cache_attn_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, const CacheAttnArgs a) {
     using L = Smem<D>;
     Ctx<D> x;
+    x.base = sbase();
     Start* st = reinterpret_cast<Start*>(g_smem + L::kStart);
     const int tid = threadIdx.x, warp = tid >> 5, lane = tid & 31;
     asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
-    for (int i = tid; i < D + 1; i += kThreads) reinterpret_cast<int*>(g_smem + L::kNan)[i] = 0x7fffffff;
+    for (int i = tid; i < 4 * D + 4; i += kThreads) reinterpret_cast<int*>(g_smem + L::kNan)[i] = 0x7fffffff;
     if (tid == 0) {
         x.words()[1] = x.words()[2] = 0;
         for (int s = 0; s < kStages; ++s) {
@@ -1206,9 +1239,8 @@ __global__ void __launch_bounds__(kThreads, 1)
         }
         for (int s = 0; s < 2; ++s) {
             tc::mbar_init(x.bar(B_VFULL, s), 1);
-            tc::mbar_init(x.bar(B_VEMPTY, s), kSoftmax / 32);
-            tc::mbar_init(x.bar(B_W, s), kSoftmax / 32);
-            tc::mbar_init(x.bar(B_P, 2 * s), kSoftmax / 64);
+            tc::mbar_init(x.bar(B_VEMPTY, s), 4);  // lane 0 of the widening warps
+            tc::mbar_init(x.bar(B_P, 2 * s), kSoftmax / 64 + 4);  // lane 0 of the groups (0, h) and of the widening warps
             tc::mbar_init(x.bar(B_P, 2 * s + 1), kSoftmax / 64);
             tc::mbar_init(x.bar(B_PV, s), 1);
         }
@@ -1228,16 +1260,18 @@ __global__ void __launch_bounds__(kThreads, 1)
     __syncthreads();
     tc::tc_fence_after();
     x.tmem = (uint32_t)x.words()[0];
-    const bool aligned = (sbase() & 1023u) == 0;  // the swizzled tiles need it; a launch that has not is refused
+    // the swizzled tiles need the one, the MMA warp counts on the other; a launch that has not is refused
+    const bool aligned = (sbase() & 1023u) == 0 && x.tmem == 0;
     if (tid == 0 && !aligned) x.words()[1] = 1;
     if (st->left > 0 && aligned) {
         if (warp >= 16) {
             tc::regs_dec<kRegsOther>();
-            if (warp == 16) produce<D>(x, a, *st, &tk, &tv);
-            else if (warp == 17) issue<D>(x, a, *st);
+            if (warp == 16) produce<D>(x.own(), a, *st, &tk, &tv);
+            else if (warp == 17) issue<D>(a, *st);
+            else if (warp >= 20) widen<D>(x.own(), a, *st);
         } else {
             tc::regs_inc<kRegsSoftmax>();
-            softmax<D, GK>(x, a, *st);
+            softmax<D, GK>(x.own(), a, *st);
         }
     }
     tc::tc_fence_before();
