@@ -34,8 +34,8 @@
 // keys from 64 i + 32 h on. Two S buffers take turns, so that a tile's softmax
 // runs under the MMAs of its neighbours. A larger unit is two MMA tiles over
 // the same keys, tile i with O_i, and group (i, h) takes keys 64 h .. of it.
-// Either way two threads share a row of an O: they keep one offset mo for it,
-// and agree before every tile's p' is passed on whether it may stay.
+// Either way two threads share a row of an O: they keep the same offsets for
+// it, and agree before every tile's p' is passed on whether these may stay.
 // TMEM (512 columns): S0 | S1 | O0 | O1; p' overwrites S as fp16.
 // MMAs of one thread run in issue order, so the next S of a buffer is issued
 // right behind the PV that reads the p' it overwrites.
@@ -87,8 +87,8 @@ struct Smem {
     static constexpr int kScale = kMisc;                          // float [slots][16]: ks, log2 vs of 16-key groups
     static constexpr int kNan = kScale + kScaleSlots * 64;        // int [4][D]: first key whose value is NaN, per column
     static constexpr int kNanAny = kNan + 4 * D * 4;              // int [4]: first key with a NaN in any column
-    static constexpr int kMax = kNanAny + 16;                     // float [8 pairs][2][32]: maxima that partners exchange
-    static constexpr int kBar = kMax + 2048;
+    static constexpr int kMax = kNanAny + 16;                     // float2 [8 pairs][2][32]: maxima that partners exchange
+    static constexpr int kBar = kMax + 4096;
     static constexpr int kWords = kBar + B_COUNT * 8;             // tmem, abort, error, info
     static constexpr int kStart = kWords + 16;                    // Start
     static constexpr int kQExp = kStart + 64;                     // uint8 [256]: exponent of the rows' scale
@@ -831,10 +831,10 @@ __device__ __forceinline__ void split_q(const Ctx<D>& x, const CacheAttnArgs& a,
 // Tiles are first taken with the row's present offsets, the maximum of the exponents alongside: it is at most 15 (p' fits
 // fp16) for all but a few tiles of a sequence. Where a row of the two warps that share it finds a larger one (its first
 // keys among them), or a page's value scale is so small that its p' may fall below what fp32 holds, both warps take the
-// tile again: new offsets from the tile's maxima, O (each warp half of its columns) and l rescaled, and l from the
-// weights themselves where p' says too little.
+// tile again: new offsets (m of l, mo of O) from the maxima of both, O (each warp half of its columns) and l rescaled,
+// and l from the weights themselves where p' says too little.
 template <int D, int GK, int COLS, typename Settle>
-__device__ __forceinline__ void softmax_part(uint32_t tC, uint32_t tO, int pair, float* mx_own, const float* mx_other,
+__device__ __forceinline__ void softmax_part(uint32_t tC, uint32_t tO, int pair, float2* mx_own, const float2* mx_other,
                                              const float* sc, float cs, int visible, bool full, bool first, float& m, float& mo,
                                              float& l, Settle settle) {
     constexpr int Q = COLS / 32, NG = 32 / GK;
@@ -906,13 +906,14 @@ __device__ __forceinline__ void softmax_part(uint32_t tC, uint32_t tO, int pair,
                 mxo = fmaxf(mxo, y + sc[8 + 2 * q + g]);
             }
         }
+        *mx_own = make_float2(mx, mxo);
+        pair_sync(pair);
+        mx = fmaxf(mx, mx_other->x);
+        mxo = fmaxf(mxo, mx_other->y);
         if (mx > m) {
             l *= ex2f(m - mx);
             m = mx;
         }
-        *mx_own = mxo;
-        pair_sync(pair);
-        mxo = fmaxf(mxo, *mx_other);
         const bool move = mxo > mo + 15.f;
         float alpha = 1.f;
         if (move) {
@@ -1037,8 +1038,8 @@ __device__ __forceinline__ void softmax(const Ctx<D>& x, const CacheAttnArgs& a,
     const float* scales = reinterpret_cast<const float*>(g_smem + L::kScale);
     Place* place = x.place();
     begin_share(a, st, place);
-    float* const mx_own = reinterpret_cast<float*>(g_smem + L::kMax) + pair * 64 + 32 * h + lane;
-    const float* const mx_other = reinterpret_cast<const float*>(g_smem + L::kMax) + pair * 64 + 32 * (h ^ 1) + lane;
+    float2* const mx_own = reinterpret_cast<float2*>(g_smem + L::kMax) + pair * 64 + 32 * h + lane;
+    const float2* const mx_other = reinterpret_cast<const float2*>(g_smem + L::kMax) + pair * 64 + 32 * (h ^ 1) + lane;
     uint32_t t = 0, seg = 0, s0_phases = 0;  // s0_phases: bit of each B_S0 stage's next phase
     bool ok = true;  // warp-uniform; once it is false the loops run on without waiting, through the same barriers
     auto wait = [&](int base, int n, uint32_t parity) {
