@@ -254,6 +254,9 @@ __device__ __forceinline__ void sts16(uint32_t addr, uint32_t a, uint32_t b, uin
 __device__ __forceinline__ void sts8(uint32_t addr, uint32_t a, uint32_t b) {
     asm volatile("st.shared.v2.b32 [%0], {%1,%2};" ::"r"(addr), "r"(a), "r"(b) : "memory");
 }
+__device__ __forceinline__ void lds8(uint32_t addr, uint32_t& a, uint32_t& b) {
+    asm volatile("ld.shared.v2.b32 {%0,%1}, [%2];" : "=r"(a), "=r"(b) : "r"(addr));
+}
 __device__ __forceinline__ void lds16(uint32_t addr, uint32_t (&v)[4]) {
     asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(addr));
 }
@@ -572,12 +575,12 @@ __device__ __forceinline__ void widen(const Ctx<D>& x, const CacheAttnArgs& a, c
     constexpr int STEPS = kTileKeys / ROWS, HALF = STEPS / 2;
     const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) - 20;
     const int c = lane % PER, r0 = lane / PER + warp * (32 / PER);
-    // 16 columns are two 16-byte chunks of the 64-column half they lie in; the lanes of the upper half store theirs in
-    // the other order, so that eight lanes meet eight bank groups. The rows of a thread are ROWS (a multiple of 8)
+    // 16 columns are two 16-byte chunks of the 64-column half they lie in; the lanes of the upper half read and store
+    // theirs in the other order, so that eight lanes meet eight bank groups. The rows of a thread are ROWS (a multiple of 8)
     // apart, so its swizzle is the same in every step.
-    const uint32_t src0 = x.base + L::kV + swz8<D>(r0, c);
     const uint32_t row_dst = x.base + L::kW + (c >> 2) * 16384 + r0 * 128;
     const bool swap = c >= 4;
+    const uint32_t src0 = x.base + L::kV + swz8<D>(r0, c) + (swap ? 8 : 0), src1 = src0 ^ 8;
     const uint32_t d0 = row_dst + ((((2 * c + (swap ? 1 : 0)) & 7) ^ (r0 & 7)) << 4);
     const uint32_t d1 = row_dst + ((((2 * c + (swap ? 0 : 1)) & 7) ^ (r0 & 7)) << 4);
     Place* place = x.place();
@@ -596,7 +599,11 @@ __device__ __forceinline__ void widen(const Ctx<D>& x, const CacheAttnArgs& a, c
             for (int half = 0; half < 2; ++half) {
                 uint32_t v[HALF][4];
 #pragma unroll
-                for (int j = 0; j < HALF; ++j) lds16(src0 + ws * L::kT8 + (half * HALF + j) * ROWS * D, v[j]);
+                for (int j = 0; j < HALF; ++j) {
+                    const uint32_t from = ws * L::kT8 + (half * HALF + j) * ROWS * D;
+                    lds8(src0 + from, v[j][0], v[j][1]);
+                    lds8(src1 + from, v[j][2], v[j][3]);
+                }
                 if (half == 0) {
                     ok = ok && x.wait(B_PV, ws, ((t >> 1) & 1) ^ 1);
                     if (!__all_sync(0xffffffffu, ok)) return;
@@ -616,7 +623,7 @@ __device__ __forceinline__ void widen(const Ctx<D>& x, const CacheAttnArgs& a, c
                             for (int e = 0; e < 16; ++e) {
                                 const uint32_t sh = 8 * (e & 3);
                                 if (((v[j][e >> 2] >> sh) & 0x7f) == 0x7f) {
-                                    atomicMin(nan_first + e, kt * kTileKeys + r);
+                                    atomicMin(nan_first + (e ^ (swap ? 8 : 0)), kt * kTileKeys + r);
                                     v[j][e >> 2] &= ~(0xffu << sh);
                                 }
                             }
@@ -629,8 +636,8 @@ __device__ __forceinline__ void widen(const Ctx<D>& x, const CacheAttnArgs& a, c
                     uint32_t h[8];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) widen4(v[j][e], h[2 * e], h[2 * e + 1]);
-                    sts16(d0 + to, swap ? h[4] : h[0], swap ? h[5] : h[1], swap ? h[6] : h[2], swap ? h[7] : h[3]);
-                    sts16(d1 + to, swap ? h[0] : h[4], swap ? h[1] : h[5], swap ? h[2] : h[6], swap ? h[3] : h[7]);
+                    sts16(d0 + to, h[0], h[1], h[2], h[3]);
+                    sts16(d1 + to, h[4], h[5], h[6], h[7]);
                 }
             }
             tc::fence_proxy_async_smem();
@@ -828,11 +835,12 @@ __device__ __forceinline__ void split_q(const Ctx<D>& x, const CacheAttnArgs& a,
 // keys. GK keys in a row share a page (of 32; larger pages count as several); sc points at the first one's key scale.
 // `settle` waits until the row's O may be rescaled, `mx_own` and `mx_other` are the partners' places for a maximum.
 //
-// Tiles are first taken with the row's present offsets, the maximum of the exponents alongside: it is at most 15 (p' fits
-// fp16) for all but a few tiles of a sequence. Where a row of the two warps that share it finds a larger one (its first
-// keys among them), or a page's value scale is so small that its p' may fall below what fp32 holds, both warps take the
-// tile again: new offsets (m of l, mo of O) from the maxima of both, O (each warp half of its columns) and l rescaled,
-// and l from the weights themselves where p' says too little.
+// Tiles are first taken with the row's present offsets. p' is positive, so a sum of at most 2^15 says that every p' fits
+// fp16, and no maximum is needed; it holds for all but a few tiles of a sequence. Where a row of the two warps that share
+// it has a larger sum or sees its first keys, or a page's value scale is so small that its p' may fall below what fp32
+// holds, both warps take the tile again: new offsets (m of l, mo of O) from the maxima of both, O (each warp half of its
+// columns) and l rescaled, and l from the weights themselves where p' says too little. (A sum over 2^15 of 64 keys has a
+// p' of 2^9, which moves mo; the largest is 2^7 then, and the sum at most 2^13.)
 template <int D, int GK, int COLS, typename Settle>
 __device__ __forceinline__ void softmax_part(uint32_t tC, uint32_t tO, int pair, float2* mx_own, const float2* mx_other,
                                              const float* sc, float cs, int visible, bool full, bool first, float& m, float& mo,
@@ -853,30 +861,25 @@ __device__ __forceinline__ void softmax_part(uint32_t tC, uint32_t tO, int pair,
         tc::tmem_st_wait();
     }
     uint32_t pk[COLS / 2];
-    // p' of keys [GK g, GK g + GK) of chunk q with exponents s ks + b into pk; returns their sum, and the largest exponent
-    // in *top
-    auto weigh = [&](const uint32_t(&r)[32], int q, int g, float ks, float b, float* top) {
+    // p' of keys [GK g, GK g + GK) of chunk q with exponents s ks + b into pk; returns their sum
+    auto weigh = [&](const uint32_t(&r)[32], int q, int g, float ks, float b) {
         const float2 a2 = make_float2(ks, ks), b2 = make_float2(b, b);
         float2 s0 = make_float2(0.f, 0.f), s1 = make_float2(0.f, 0.f);
-        float t0 = *top, t1 = *top;
 #pragma unroll
         for (int e = 0; e < GK; e += 4) {
             const int k = g * GK + e;
             const float2 y0 = tc::fma2(make_float2(__uint_as_float(r[k]), __uint_as_float(r[k + 1])), a2, b2);
             const float2 y1 = tc::fma2(make_float2(__uint_as_float(r[k + 2]), __uint_as_float(r[k + 3])), a2, b2);
-            t0 = tc::fmax3(t0, y0.x, y0.y);
-            t1 = tc::fmax3(t1, y1.x, y1.y);
             const float2 p0 = make_float2(ex2f(y0.x), ex2f(y0.y)), p1 = make_float2(ex2f(y1.x), ex2f(y1.y));
             s0 = tc::add2(s0, p0);
             s1 = tc::add2(s1, p1);
             pk[16 * q + (k >> 1)] = pack_h2(p0.x, p0.y);
             pk[16 * q + (k >> 1) + 1] = pack_h2(p1.x, p1.y);
         }
-        *top = fmaxf(t0, t1);
         return s0.x + s1.x + (s0.y + s1.y);
     };
     const float m_was = m == -INFINITY ? 0.f : m, mo_was = mo == -INFINITY ? 0.f : mo;
-    float sum = 0.f, top = -INFINITY, low = INFINITY;
+    float sum = 0.f, all = 0.f, low = INFINITY;
 #pragma unroll
     for (int q = 0; q < Q; ++q) {
         uint32_t r[32];
@@ -886,10 +889,12 @@ __device__ __forceinline__ void softmax_part(uint32_t tC, uint32_t tO, int pair,
         for (int g = 0; g < NG; ++g) {
             const float b = sc[8 + 2 * q + g] - mo_was, shift = b + m_was;
             low = fminf(low, shift);
-            sum = fmaf(weigh(r, q, g, cs * sc[2 * q + g], b, &top), ex2f(-shift), sum);
+            const float part = weigh(r, q, g, cs * sc[2 * q + g], b);
+            all += part;
+            sum = fmaf(part, ex2f(-shift), sum);
         }
     }
-    if (pair_any(pair, top > 15.f || low < -60.f || (mo == -INFINITY && top > -INFINITY))) {
+    if (pair_any(pair, all > 32768.f || low < -60.f || (mo == -INFINITY && visible > 0))) {
         float mx = -INFINITY, mxo = -INFINITY;
 #pragma unroll 1
         for (int q = 0; q < Q; ++q) {
@@ -914,7 +919,7 @@ __device__ __forceinline__ void softmax_part(uint32_t tC, uint32_t tO, int pair,
             l *= ex2f(m - mx);
             m = mx;
         }
-        const bool move = mxo > mo + 15.f;
+        const bool move = mxo > mo + 8.f;
         float alpha = 1.f;
         if (move) {
             alpha = ex2f(mo - (mxo - 7.f));
@@ -945,9 +950,9 @@ __device__ __forceinline__ void softmax_part(uint32_t tC, uint32_t tO, int pair,
                 if (__any_sync(0xffffffffu, shift < -60.f)) {
 #pragma unroll
                     for (int e = 0; e < GK; ++e) sum += ex2f(fmaf(__uint_as_float(r[g * GK + e]), ks, -m_use));
-                    weigh(r, q, g, ks, b, &top);
+                    weigh(r, q, g, ks, b);
                 } else {
-                    sum = fmaf(weigh(r, q, g, ks, b, &top), ex2f(-shift), sum);
+                    sum = fmaf(weigh(r, q, g, ks, b), ex2f(-shift), sum);
                 }
             }
         }
