@@ -21,21 +21,20 @@
 // for up to 128 flat rows, so these calls are bound by memory, and calls with
 // 256 and more flat rows by the tensor pipe.
 //
-// Roles (768 threads, one CTA per SM, each role walks the CTA's share alone):
-//   warps 0-15   softmax, in four groups (i, h); one TMEM lane = one flat row.
-//                They also split Q into its two terms, and write the results
-//   warp 16      page table, scales and TMA loads of K (3 stages) and V (2)
-//   warp 17      issues the MMAs (one elected lane), owns TMEM
-//   warps 18-19  spare
-//   warps 20-23  widen V from e4m3 to fp16 (2 stages), zero the rows behind
-//                the last key and take out masked NaN
-// A unit of up to 128 flat rows is one MMA tile: its products with the values
-// of keys 64 i .. of every tile add up in O_i, and group (i, h) takes the 32
-// keys from 64 i + 32 h on. Two S buffers take turns, so that a tile's softmax
-// runs under the MMAs of its neighbours. A larger unit is two MMA tiles over
-// the same keys, tile i with O_i, and group (i, h) takes keys 64 h .. of it.
-// Either way two threads share a row of an O: they keep the same offsets for
-// it, and agree before every tile's p' is passed on whether these may stay.
+// Roles (512 threads, one CTA per SM, each role walks the CTA's share alone):
+//   warps 0-3, 4-7  softmax groups 0 and 1; one TMEM lane = one flat row. They
+//                   also split Q into its two terms, and write the results
+//   warp 8          page table, scales and TMA loads of K (3 stages) and V (2)
+//   warp 9          issues the MMAs (one elected lane), owns TMEM
+//   warps 10-11     spare
+//   warps 12-15     widen V from e4m3 to fp16 (2 stages), zero the rows behind
+//                   the last key and take out masked NaN
+// A unit of up to 128 flat rows is one MMA tile: group i takes keys 64 i .. of
+// every key tile, with sums of its own and O_i, which are joined at the end.
+// Two S buffers take turns, so that a tile's softmax runs under the MMAs of
+// its neighbours, and the next tile's scores come out of TMEM under this one's
+// last steps. A larger unit is two MMA tiles over the same keys, one for each
+// group.
 // TMEM (512 columns): S0 | S1 | O0 | O1; p' overwrites S as fp16.
 // MMAs of one thread run in issue order, so the next S of a buffer is issued
 // right behind the PV that reads the p' it overwrites.
@@ -52,13 +51,13 @@
 namespace bdlm {
 namespace cattn {
 
-constexpr int kThreads = 768;
-constexpr int kSoftmax = 512;
-// 24 warps at 80 registers each, redistributed. What a role keeps beyond its registers would be spilled to an L1 that
+constexpr int kThreads = 512;
+constexpr int kSoftmax = 256;
+// 16 warps at 128 registers each, redistributed. What a role keeps beyond its registers would be spilled to an L1 that
 // shared memory leaves next to no room.
-constexpr int kRegsSoftmax = 96;
-constexpr int kRegsOther = 48;
-static_assert(16 * kRegsSoftmax + 8 * kRegsOther <= 24 * 80, "registers");
+constexpr int kRegsSoftmax = 176;
+constexpr int kRegsOther = 80;
+static_assert(8 * kRegsSoftmax + 8 * kRegsOther <= 16 * 128, "registers");
 constexpr int kTmemCols = 512;
 constexpr int kStages = 3;  // of K; V has two as e4m3 and two as fp16
 constexpr int kScaleSlots = 6;
@@ -70,7 +69,7 @@ enum : int {
     B_VFULL = 3, B_VEMPTY = 5,  // t & 1
     B_S0 = 7,                   // t % 3: the first S of a unit of two MMA tiles
     B_S1 = 10,                  // t % 3: the tile's last S; it also frees the K stage
-    B_P = 13,                   // 2 (t & 1) + i: p' for O_i in TMEM; for O_0 also V in fp16
+    B_P = 13,                   // 2 (t & 1) + i: p' of group i in TMEM; for group 0 also V in fp16
     B_PV = 17,                  // t & 1: the tile's products with V; frees the fp16 stage
     B_Q = 19,
     B_COUNT = 20
@@ -87,8 +86,7 @@ struct Smem {
     static constexpr int kScale = kMisc;                          // float [slots][16]: ks, log2 vs of 16-key groups
     static constexpr int kNan = kScale + kScaleSlots * 64;        // int [4][D]: first key whose value is NaN, per column
     static constexpr int kNanAny = kNan + 4 * D * 4;              // int [4]: first key with a NaN in any column
-    static constexpr int kMax = kNanAny + 16;                     // float2 [8 pairs][2][32]: maxima that partners exchange
-    static constexpr int kBar = kMax + 4096;
+    static constexpr int kBar = kNanAny + 16;
     static constexpr int kWords = kBar + B_COUNT * 8;             // tmem, abort, error, info
     static constexpr int kStart = kWords + 16;                    // Start
     static constexpr int kQExp = kStart + 64;                     // uint8 [256]: exponent of the rows' scale
@@ -260,19 +258,8 @@ __device__ __forceinline__ void lds8(uint32_t addr, uint32_t& a, uint32_t& b) {
 __device__ __forceinline__ void lds16(uint32_t addr, uint32_t (&v)[4]) {
     asm volatile("ld.shared.v4.b32 {%0,%1,%2,%3}, [%4];" : "=r"(v[0]), "=r"(v[1]), "=r"(v[2]), "=r"(v[3]) : "r"(addr));
 }
-__device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 512;" ::: "memory"); }
-__device__ __forceinline__ void tile_sync(int i) { asm volatile("bar.sync %0, 256;" ::"r"(2 + i) : "memory"); }
-// the two warps that share rows of an O
-__device__ __forceinline__ void pair_sync(int pair) { asm volatile("bar.sync %0, 64;" ::"r"(4 + pair) : "memory"); }
-__device__ __forceinline__ bool pair_any(int pair, bool p) {
-    uint32_t r;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\tsetp.ne.u32 p, %1, 0;\n\tbar.red.or.pred q, %2, 64, p;\n\tselp.u32 %0, 1, 0, q;\n\t}"
-        : "=r"(r)
-        : "r"((uint32_t)p), "r"(4 + pair)
-        : "memory");
-    return r != 0;
-}
+__device__ __forceinline__ void softmax_sync() { asm volatile("bar.sync 1, 256;" ::: "memory"); }
+__device__ __forceinline__ void group_sync(int i) { asm volatile("bar.sync %0, 128;" ::"r"(2 + i) : "memory"); }
 
 template <int N>
 struct Const {
@@ -573,7 +560,7 @@ __device__ __forceinline__ void widen(const Ctx<D>& x, const CacheAttnArgs& a, c
     constexpr int PER = D / 16;                  // 16-byte chunks per key
     constexpr int ROWS = 4 * (32 / PER);         // keys that the four warps take at a time
     constexpr int STEPS = kTileKeys / ROWS, HALF = STEPS / 2;
-    const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) - 20;
+    const int lane = threadIdx.x & 31, warp = (threadIdx.x >> 5) - 12;
     const int c = lane % PER, r0 = lane / PER + warp * (32 / PER);
     // 16 columns are two 16-byte chunks of the 64-column half they lie in; the lanes of the upper half read and store
     // theirs in the other order, so that eight lanes meet eight bank groups. The rows of a thread are ROWS (a multiple of 8)
@@ -679,15 +666,13 @@ __device__ __forceinline__ void issue(const CacheAttnArgs& a, const Start& st) {
             tc::mma_commit(x.bar(bar, stage));
         }
     };
-    // 2 N steps of p' times the fp16 values in stage b from key `key` on, into O buffer o: N steps from TMEM column p on,
-    // which the groups (o, 0) wrote, and N from column p + 16 N on
+    // N steps of p' (from TMEM column p on) times the fp16 values in stage b from key `key` on, into O buffer o
     auto issue_pv = [&](uint32_t b, uint32_t p, uint32_t o, int key, auto steps, bool fresh) {
         constexpr int N = decltype(steps)::value;
         const uint64_t dv = tc::sdesc_add(mn, L::kW + b * 2 * L::kT8 + key * 128);
         if (leader) {
 #pragma unroll
-            for (int k = 0; k < 2 * N; ++k)
-                tc::mma_ts(256 + D * o, p + 16 * N * (k / N) + 8 * (k % N), tc::sdesc_add(dv, 2048 * k), id_o, (k > 0 || !fresh) ? 1u : 0u);
+            for (int k = 0; k < N; ++k) tc::mma_ts(256 + D * o, p + 8 * k, tc::sdesc_add(dv, 2048 * k), id_o, (k > 0 || !fresh) ? 1u : 0u);
         }
     };
     auto up = [](uint32_t& stage, uint32_t& ph) {  // the next stage of a ring of three, and its phase
@@ -718,7 +703,7 @@ __device__ __forceinline__ void issue(const CacheAttnArgs& a, const Start& st) {
                 for (uint32_t i = 0; i < 2; ++i) {
                     if (!wait(B_P, 2 * b + i, ph)) return;
                     tc::tc_fence_after();
-                    issue_pv(b, 128 * i, i, 0, Const<4>{}, j == 0);
+                    issue_pv(b, 128 * i, i, 0, Const<8>{}, j == 0);
                     if (i == 1 && leader) tc::mma_commit(x.bar(B_PV, b));
                     if (more) {
                         if (i == 0 && !wait(B_KFULL, stage, ks)) return;
@@ -741,7 +726,7 @@ __device__ __forceinline__ void issue(const CacheAttnArgs& a, const Start& st) {
                 for (uint32_t i = 0; i < 2; ++i) {  // each half of the keys into its own O
                     if (!wait(B_P, 2 * b + i, ph)) return;
                     tc::tc_fence_after();
-                    issue_pv(b, 128 * b + 64 * i, i, 64 * i, Const<2>{}, j == 0);
+                    issue_pv(b, 128 * b + 64 * i, i, 64 * i, Const<4>{}, j == 0);
                 }
                 if (leader) tc::mma_commit(x.bar(B_PV, b));
                 if (j + 2 < nt) {
@@ -763,7 +748,7 @@ __device__ __forceinline__ void issue(const CacheAttnArgs& a, const Start& st) {
 template <int D>
 __device__ __forceinline__ void split_q(const Ctx<D>& x, const CacheAttnArgs& a, const Seg& g) {
     using L = Smem<D>;
-    constexpr int PER = D / 8, ROWS = kSoftmax / PER, BATCH = 2;
+    constexpr int PER = D / 8, ROWS = kSoftmax / PER, BATCH = 4;
     const int chunk = threadIdx.x % PER, r0 = threadIdx.x / PER;
     const int n = g.last - g.m0, padded = (n + 31) & ~31;
     uint8_t* exps = g_smem + L::kQExp;
@@ -782,7 +767,7 @@ __device__ __forceinline__ void split_q(const Ctx<D>& x, const CacheAttnArgs& a,
         }
         return y;
     };
-    // two rows at a time, the next two in flight; the loop is not unrolled further, since most of what a first pass
+    // four rows at a time, the next four in flight; the loop is not unrolled further, since most of what a first pass
     // through this code costs is fetching the code
     uint4 v[BATCH], w[BATCH];
 #pragma unroll
@@ -831,142 +816,119 @@ __device__ __forceinline__ void split_q(const Ctx<D>& x, const CacheAttnArgs& a,
     }
 }
 
-// COLS keys of one key tile for one row: scores out of TMEM (columns from tC on), p' back into them, in chunks of 32
-// keys. GK keys in a row share a page (of 32; larger pages count as several); sc points at the first one's key scale.
-// `settle` waits until the row's O may be rescaled, `mx_own` and `mx_other` are the partners' places for a maximum.
+// One row's running sums: l = sum 2^(s - m), and O = sum 2^(s + log2 vs - mo) v8.
+struct RowSums {
+    float m, mo, l;
+};
+
+// p' of the 64 keys of a row whose scores were loaded from TMEM column tC on into r; p' goes to pk as fp16 pairs. NG pages
+// of GK keys each; sc points at the first one's key scale. The row sees the first `visible` keys; `full`: all of the
+// warp's rows see all. `settle(alpha)` waits until the row's O (at tO) may be rescaled, and rescales by the power of two
+// alpha what p' of this tile has been passed to TMEM already.
 //
-// Tiles are first taken with the row's present offsets. p' is positive, so a sum of at most 2^15 says that every p' fits
-// fp16, and no maximum is needed; it holds for all but a few tiles of a sequence. Where a row of the two warps that share
-// it has a larger sum or sees its first keys, or a page's value scale is so small that its p' may fall below what fp32
-// holds, both warps take the tile again: new offsets (m of l, mo of O) from the maxima of both, O (each warp half of its
-// columns) and l rescaled, and l from the weights themselves where p' says too little. (A sum over 2^15 of 64 keys has a
-// p' of 2^9, which moves mo; the largest is 2^7 then, and the sum at most 2^13.)
-template <int D, int GK, int COLS, typename Settle>
-__device__ __forceinline__ void softmax_part(uint32_t tC, uint32_t tO, int pair, float2* mx_own, const float2* mx_other,
-                                             const float* sc, float cs, int visible, bool full, bool first, float& m, float& mo,
-                                             float& l, Settle settle) {
-    constexpr int Q = COLS / 32, NG = 32 / GK;
-    if (!full) {
-        // masked entries become -inf in TMEM first, so that other tiles run no mask code
-#pragma unroll 1
-        for (int q = 0; q < Q; ++q) {
-            uint32_t v[32];
-            tc::tmem_ld32(tC + 32 * q, v);
-            tc::tmem_ld_wait();
+// Keys are first taken with the row's present offsets. p' is positive, so a sum of at most 2^15 says that every p' fits
+// fp16, and no maximum is needed; it holds for all but a few tiles of a sequence. Where a row of the warp has a larger
+// sum or sees its first keys, or a page's value scale is so small that its p' may fall below what fp32 holds, the warp
+// takes the keys again: new offsets from their maxima, O and l rescaled, and l from the weights themselves where p' says
+// too little. (A sum over 2^15 of 64 keys has a p' of 2^9, which moves mo; the largest is 2^7 then, and the sum at most
+// 2^13.)
+template <int D, int NG, typename Settle>
+__device__ __forceinline__ void softmax_part(uint32_t (&r)[2][32], uint32_t (&pk)[32], uint32_t tC, uint32_t tO, const float* sc,
+                                             float cs, int visible, bool full, bool first, RowSums& s, Settle settle) {
+    constexpr int GK = 64 / NG;
+    auto at = [&](int k) { return __uint_as_float(r[k >> 5][k & 31]); };
+    auto mask = [&]() {
+        if (!full) {
 #pragma unroll
-            for (int e = 0; e < 32; ++e)
-                if (32 * q + e >= visible) v[e] = 0xff800000u;
-            tc::tmem_st32(tC + 32 * q, v);
+            for (int k = 0; k < 64; ++k)
+                if (k >= visible) r[k >> 5][k & 31] = 0xff800000u;  // -inf
         }
-        tc::tmem_st_wait();
-    }
-    uint32_t pk[COLS / 2];
-    // p' of keys [GK g, GK g + GK) of chunk q with exponents s ks + b into pk; returns their sum
-    auto weigh = [&](const uint32_t(&r)[32], int q, int g, float ks, float b) {
+    };
+    // p' of page g, with exponents s ks + b; returns their sum
+    auto weigh = [&](int g, float ks, float b) {
         const float2 a2 = make_float2(ks, ks), b2 = make_float2(b, b);
         float2 s0 = make_float2(0.f, 0.f), s1 = make_float2(0.f, 0.f);
 #pragma unroll
         for (int e = 0; e < GK; e += 4) {
             const int k = g * GK + e;
-            const float2 y0 = tc::fma2(make_float2(__uint_as_float(r[k]), __uint_as_float(r[k + 1])), a2, b2);
-            const float2 y1 = tc::fma2(make_float2(__uint_as_float(r[k + 2]), __uint_as_float(r[k + 3])), a2, b2);
+            const float2 y0 = tc::fma2(make_float2(at(k), at(k + 1)), a2, b2), y1 = tc::fma2(make_float2(at(k + 2), at(k + 3)), a2, b2);
             const float2 p0 = make_float2(ex2f(y0.x), ex2f(y0.y)), p1 = make_float2(ex2f(y1.x), ex2f(y1.y));
             s0 = tc::add2(s0, p0);
             s1 = tc::add2(s1, p1);
-            pk[16 * q + (k >> 1)] = pack_h2(p0.x, p0.y);
-            pk[16 * q + (k >> 1) + 1] = pack_h2(p1.x, p1.y);
+            pk[k >> 1] = pack_h2(p0.x, p0.y);
+            pk[(k >> 1) + 1] = pack_h2(p1.x, p1.y);
         }
         return s0.x + s1.x + (s0.y + s1.y);
     };
-    const float m_was = m == -INFINITY ? 0.f : m, mo_was = mo == -INFINITY ? 0.f : mo;
+    mask();
+    const float m_was = s.m == -INFINITY ? 0.f : s.m, mo_was = s.mo == -INFINITY ? 0.f : s.mo;
     float sum = 0.f, all = 0.f, low = INFINITY;
 #pragma unroll
-    for (int q = 0; q < Q; ++q) {
-        uint32_t r[32];
-        tc::tmem_ld32(tC + 32 * q, r);
+    for (int g = 0; g < NG; ++g) {
+        const float b = sc[8 + g * (GK / 16)] - mo_was, shift = b + m_was;
+        low = fminf(low, shift);
+        const float part = weigh(g, cs * sc[g * (GK / 16)], b);
+        all += part;
+        sum = fmaf(part, ex2f(-shift), sum);
+    }
+    if (__any_sync(0xffffffffu, all > 32768.f || low < -60.f || (s.mo == -INFINITY && visible > 0))) {
+        tc::tmem_ld32(tC, r[0]);
+        tc::tmem_ld32(tC + 32, r[1]);
         tc::tmem_ld_wait();
+        mask();
+        float mx = -INFINITY, mxo = -INFINITY;
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
-            const float b = sc[8 + 2 * q + g] - mo_was, shift = b + m_was;
-            low = fminf(low, shift);
-            const float part = weigh(r, q, g, cs * sc[2 * q + g], b);
-            all += part;
-            sum = fmaf(part, ex2f(-shift), sum);
-        }
-    }
-    if (pair_any(pair, all > 32768.f || low < -60.f || (mo == -INFINITY && visible > 0))) {
-        float mx = -INFINITY, mxo = -INFINITY;
-#pragma unroll 1
-        for (int q = 0; q < Q; ++q) {
-            uint32_t r[32];
-            tc::tmem_ld32(tC + 32 * q, r);
-            tc::tmem_ld_wait();
+            float c0 = -INFINITY, c1 = -INFINITY;
 #pragma unroll
-            for (int g = 0; g < NG; ++g) {
-                float c = -INFINITY;
-#pragma unroll
-                for (int e = 0; e < GK; e += 2) c = tc::fmax3(c, __uint_as_float(r[g * GK + e]), __uint_as_float(r[g * GK + e + 1]));
-                const float y = c * (cs * sc[2 * q + g]);
-                mx = fmaxf(mx, y);
-                mxo = fmaxf(mxo, y + sc[8 + 2 * q + g]);
+            for (int e = 0; e < GK; e += 4) {
+                const int k = g * GK + e;
+                c0 = tc::fmax3(c0, at(k), at(k + 1));
+                c1 = tc::fmax3(c1, at(k + 2), at(k + 3));
             }
+            const float y = fmaxf(c0, c1) * (cs * sc[g * (GK / 16)]);
+            mx = fmaxf(mx, y);
+            mxo = fmaxf(mxo, y + sc[8 + g * (GK / 16)]);
         }
-        *mx_own = make_float2(mx, mxo);
-        pair_sync(pair);
-        mx = fmaxf(mx, mx_other->x);
-        mxo = fmaxf(mxo, mx_other->y);
-        if (mx > m) {
-            l *= ex2f(m - mx);
-            m = mx;
+        if (mx > s.m) {
+            s.l *= ex2f(s.m - mx);
+            s.m = mx;
         }
-        const bool move = mxo > mo + 8.f;
+        const bool move = mxo > s.mo + 8.f;
         float alpha = 1.f;
         if (move) {
-            alpha = ex2f(mo - (mxo - 7.f));
-            mo = mxo - 7.f;
+            const float to = ceilf(mxo) - 7.f;  // whole numbers, so that rescaling loses nothing
+            alpha = ex2f(s.mo - to);
+            s.mo = to;
         }
-        if (!first && __any_sync(0xffffffffu, move)) {
-            settle();
-#pragma unroll 1
-            for (int q = 0; q < D / 32; ++q) {
-                uint32_t o[16];
-                tmem_ld16(tO + 16 * q, o);
-                tc::tmem_ld_wait();
-#pragma unroll
-                for (int e = 0; e < 16; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-                tc::tmem_st16(tO + 16 * q, o);
-            }
-        }
-        const float m_use = m == -INFINITY ? 0.f : m, mo_use = mo == -INFINITY ? 0.f : mo;
+        const float m_use = s.m == -INFINITY ? 0.f : s.m, mo_use = s.mo == -INFINITY ? 0.f : s.mo;
         sum = 0.f;
 #pragma unroll
-        for (int q = 0; q < Q; ++q) {
-            uint32_t r[32];
-            tc::tmem_ld32(tC + 32 * q, r);
-            tc::tmem_ld_wait();
+        for (int g = 0; g < NG; ++g) {
+            const float ks = cs * sc[g * (GK / 16)], b = sc[8 + g * (GK / 16)] - mo_use, shift = b + m_use;
+            if (__any_sync(0xffffffffu, shift < -60.f)) {
 #pragma unroll
-            for (int g = 0; g < NG; ++g) {
-                const float ks = cs * sc[2 * q + g], b = sc[8 + 2 * q + g] - mo_use, shift = b + m_use;
-                if (__any_sync(0xffffffffu, shift < -60.f)) {
-#pragma unroll
-                    for (int e = 0; e < GK; ++e) sum += ex2f(fmaf(__uint_as_float(r[g * GK + e]), ks, -m_use));
-                    weigh(r, q, g, ks, b);
-                } else {
-                    sum = fmaf(weigh(r, q, g, ks, b), ex2f(-shift), sum);
-                }
+                for (int e = 0; e < GK; ++e) sum += ex2f(fmaf(at(g * GK + e), ks, -m_use));
+                weigh(g, ks, b);
+            } else {
+                sum = fmaf(weigh(g, ks, b), ex2f(-shift), sum);
             }
         }
-        pair_sync(pair);  // the partner has read *mx_own
-    }
-    l += sum;
+        if (__any_sync(0xffffffffu, move)) {  // last: the wait for the products in flight comes late
+            settle(alpha);
+            if (!first)
 #pragma unroll
-    for (int q = 0; q < Q; ++q) {
-        uint32_t w[16];
+                for (int q = 0; q < D / 32; ++q) {
+                    uint32_t o[32];
+                    tc::tmem_ld32(tO + 32 * q, o);
+                    tc::tmem_ld_wait();
 #pragma unroll
-        for (int e = 0; e < 16; ++e) w[e] = pk[16 * q + e];
-        tc::tmem_st16(tC + 16 * q, w);
+                    for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
+                    tc::tmem_st32(tO + 32 * q, o);
+                }
+        }
     }
-    tc::tmem_st_wait();
+    s.l += sum;
 }
 
 // Where the results of a unit's flat rows go.
@@ -1033,18 +995,15 @@ __device__ __forceinline__ void put_lse(const CacheAttnArgs& a, const Seg& g, co
     }
 }
 
-template <int D, int GK>
+template <int D, int NG>
 __device__ __forceinline__ void softmax(const Ctx<D>& x, const CacheAttnArgs& a, const Start& st) {
     using L = Smem<D>;
-    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, i = warp >> 3, h = (warp >> 2) & 1, row = threadIdx.x & 127;
-    const int pair = 4 * i + (warp & 3);
+    const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, i = warp >> 2, row = threadIdx.x & 127;
     const uint32_t lane_base = (uint32_t)(32 * (warp & 3)) << 16;
     const uint32_t tS = x.tmem + lane_base, tO = x.tmem + 256 + lane_base;
     const float* scales = reinterpret_cast<const float*>(g_smem + L::kScale);
     Place* place = x.place();
     begin_share(a, st, place);
-    float2* const mx_own = reinterpret_cast<float2*>(g_smem + L::kMax) + pair * 64 + 32 * h + lane;
-    const float2* const mx_other = reinterpret_cast<const float2*>(g_smem + L::kMax) + pair * 64 + 32 * (h ^ 1) + lane;
     uint32_t t = 0, seg = 0, s0_phases = 0;  // s0_phases: bit of each B_S0 stage's next phase
     bool ok = true;  // warp-uniform; once it is false the loops run on without waiting, through the same barriers
     auto wait = [&](int base, int n, uint32_t parity) {
@@ -1061,7 +1020,7 @@ __device__ __forceinline__ void softmax(const Ctx<D>& x, const CacheAttnArgs& a,
             const Seg g = place->g;
             const int m = g.m0 + (two ? 128 * i : 0) + row;  // this thread's flat row
             if (nt == 0) {                                   // rows without keys
-                if (m < g.last && h == 0 && (two || i == 0)) {
+                if (m < g.last && (two || i == 0)) {
                     const long long at = ((long long)(g.row0 + m / a.G) * a.H + g.h * a.G + m % a.G) * D;
                     for (int c = 0; c < D; c += 8) {
                         if (a.o_f32) {
@@ -1089,51 +1048,85 @@ __device__ __forceinline__ void softmax(const Ctx<D>& x, const CacheAttnArgs& a,
             warp_live = __shfl_sync(0xffffffffu, (int)(m < g.last), 0);
             // keys of a tile that this row sees of the thread's part, and that the warp's first row (which sees the
             // fewest) does
-            sees = end - g.kt0 * kTileKeys - (two ? 64 * h : 64 * i + 32 * h);
+            sees = end - g.kt0 * kTileKeys - (two ? 0 : 64 * i);
             all_see = __shfl_sync(0xffffffffu, sees, 0);
         }
-        float mm = -INFINITY, mo = -INFINITY, l = 0.f;
+        RowSums sums{-INFINITY, -INFINITY, 0.f};
         uint32_t stage = t % kStages, ph = (t / kStages) & 1, slot = t % kScaleSlots;
+        auto up = [&]() {
+            sees -= kTileKeys;
+            all_see -= kTileKeys;
+            slot = slot + 1 == kScaleSlots ? 0 : slot + 1;
+            if (++stage == kStages) {
+                stage = 0;
+                ph ^= 1;
+            }
+        };
+        auto pass_on = [&](uint32_t n) {  // p' of tile n is in TMEM
+            tc::tmem_st_wait();
+            tc::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(x.bar(B_P, 2 * (n & 1) + i));
+        };
+        constexpr int NGP = NG > 1 ? NG / 2 : 1;  // pages in 64 keys
         if (two) {
+#pragma unroll 1
             for (int j = 0; j < nt; ++j, ++t) {
                 if (i == 0) {
                     wait(B_S0, stage, (s0_phases >> stage) & 1);
                 } else {
                     wait(B_S1, stage, ph);
                 }
-                // S of a tile is issued behind the PV of the one before, so O is settled
-                if (warp_live)
-                    softmax_part<D, GK, 64>(tS + 128 * i + 64 * h, tO + D * i + h * (D / 2), pair, mx_own, mx_other,
-                                            scales + 16 * slot + 4 * h, cs, sees, all_see >= 64, j == 0, mm, mo, l, [] {});
-                tc::tc_fence_before();
-                __syncwarp();
-                if (lane == 0) tc::mbar_arrive(x.bar(B_P, 2 * (t & 1) + i));
-                s0_phases ^= 1u << stage;
-                sees -= kTileKeys;
-                all_see -= kTileKeys;
-                slot = slot + 1 == kScaleSlots ? 0 : slot + 1;
-                if (++stage == kStages) {
-                    stage = 0;
-                    ph ^= 1;
+                if (warp_live) {
+                    // S of a tile is issued behind the PV of the one before, so O is settled
+                    uint32_t r[2][32], pk[32];
+                    const uint32_t tC = tS + 128 * i;
+                    const float* sc = scales + 16 * slot;
+                    tc::tmem_ld32(tC, r[0]);
+                    tc::tmem_ld32(tC + 32, r[1]);
+                    tc::tmem_ld_wait();
+                    softmax_part<D, NGP>(r, pk, tC, tO + D * i, sc, cs, sees, all_see >= 64, j == 0, sums, [](float) {});
+                    tc::tmem_ld32(tC + 64, r[0]);
+                    tc::tmem_ld32(tC + 96, r[1]);
+                    tc::tmem_st32(tC, pk);
+                    tc::tmem_ld_wait();
+                    softmax_part<D, NGP>(r, pk, tC + 64, tO + D * i, sc + 4, cs, sees - 64, all_see >= 128, j == 0, sums, [&](float alpha) {
+                        // the first half's p'
+                        uint32_t w[32];
+                        tc::tmem_st_wait();
+                        tc::tmem_ld32(tC, w);
+                        tc::tmem_ld_wait();
+                        const __half2 f = __float2half2_rn(alpha);
+#pragma unroll
+                        for (int e = 0; e < 32; ++e) {
+                            const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&w[e]), f);
+                            w[e] = *reinterpret_cast<const uint32_t*>(&y);
+                        }
+                        tc::tmem_st32(tC, w);
+                    });
+                    tc::tmem_st32(tC + 32, pk);
                 }
+                pass_on(t);
+                s0_phases ^= 1u << stage;
+                up();
             }
         } else {
+#pragma unroll 1
             for (int j = 0; j < nt; ++j, ++t) {
                 wait(B_S1, stage, ph);
-                if (warp_live)
-                    softmax_part<D, GK, 32>(tS + 128 * (t & 1) + 64 * i + 32 * h, tO + D * i + h * (D / 2), pair, mx_own, mx_other,
-                                            scales + 16 * slot + 4 * i + 2 * h, cs, sees, all_see >= 32, j == 0, mm, mo, l,
-                                            [&] { wait(B_PV, (t - 1) & 1, ((t - 1) >> 1) & 1); });
-                tc::tc_fence_before();
-                __syncwarp();
-                if (lane == 0) tc::mbar_arrive(x.bar(B_P, 2 * (t & 1) + i));
-                sees -= kTileKeys;
-                all_see -= kTileKeys;
-                slot = slot + 1 == kScaleSlots ? 0 : slot + 1;
-                if (++stage == kStages) {
-                    stage = 0;
-                    ph ^= 1;
+                if (warp_live) {
+                    uint32_t r[2][32], pk[32];
+                    const uint32_t tC = tS + 128 * (t & 1) + 64 * i;
+                    tc::tmem_ld32(tC, r[0]);
+                    tc::tmem_ld32(tC + 32, r[1]);
+                    tc::tmem_ld_wait();
+                    softmax_part<D, NGP>(r, pk, tC, tO + D * i, scales + 16 * slot + 4 * i, cs, sees, all_see >= 64, j == 0, sums, [&](float) {
+                        if (j > 0) wait(B_PV, (t - 1) & 1, ((t - 1) >> 1) & 1);
+                    });
+                    tc::tmem_st32(tC, pk);
                 }
+                pass_on(t);
+                up();
             }
         }
         wait(B_PV, (t - 1) & 1, ((t - 1) >> 1) & 1);  // every product of the unit is done
@@ -1146,79 +1139,66 @@ __device__ __forceinline__ void softmax(const Ctx<D>& x, const CacheAttnArgs& a,
         int* nan_any = reinterpret_cast<int*>(g_smem + L::kNanAny) + (seg & 3);
         ++seg;
         const bool staged = !out.slot && !a.o_f32;
-        // The threads of a row exchange their sums through columns of S (same lanes): (m, mo, l) of group (i, h) at
-        // column 4 (2 i + h), or, in a unit of two MMA tiles, at column 4 h of S_i.
-        const uint32_t tX = tS + (g.two ? 128 * i : 0);
-        tmem_st4(tX + (g.two ? 4 * h : 4 * (2 * i + h)), __float_as_uint(mm), __float_as_uint(mo), __float_as_uint(l), 0u);
-        tc::tmem_st_wait();
-        tc::tc_fence_before();
-        softmax_sync();
-        tc::tc_fence_after();
         const bool nans = *nan_any < g.end;
-        float mj, f0, f1 = 0.f, lj;
-        bool use0, use1 = false;
-        {
-            uint32_t y[16];
-            tmem_ld16(tX, y);
+        float mj = sums.m, lj = sums.l, f0, f1 = 0.f;
+        bool use0 = sums.l != 0.f, use1 = false;  // NaN counts as something
+        // o = sum of O_i 2^(mo_i - m) / l over the row's O; one without keys that the row sees adds nothing
+        if (two) {
+            f0 = use0 ? ex2f(sums.mo - mj) / lj : 0.f;
+        } else {
+            // the groups exchange their sums through S columns (same lanes); f0 is the own O's factor, f1 the other's
+            tmem_st4(tS + 128 * i, __float_as_uint(sums.m), __float_as_uint(sums.mo), __float_as_uint(sums.l), 0u);
+            tc::tmem_st_wait();
+            tc::tc_fence_before();
+            softmax_sync();
+            tc::tc_fence_after();
+            uint32_t y[4];
+            tmem_ld4(tS + 128 * (i ^ 1), y);
             tc::tmem_ld_wait();
-            const int n = g.two ? 2 : 4;
-            mj = -INFINITY;
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (e < n) mj = fmaxf(mj, __uint_as_float(y[4 * e]));
+            const float m1 = __uint_as_float(y[0]), l1 = __uint_as_float(y[2]);
+            use1 = l1 != 0.f;
+            mj = fmaxf(sums.m, m1);
             lj = 0.f;
-#pragma unroll
-            for (int e = 0; e < 4; ++e)
-                if (e < n) {
-                    const float me = __uint_as_float(y[4 * e]), le = __uint_as_float(y[4 * e + 2]);
-                    if (le != 0.f) lj += me == mj ? le : le * ex2f(me - mj);  // NaN counts as something
-                }
+            if (use0) lj += sums.m == mj ? sums.l : sums.l * ex2f(sums.m - mj);
+            if (use1) lj += m1 == mj ? l1 : l1 * ex2f(m1 - mj);
             const float inv = 1.f / lj;  // used only where lj is not 0
-            // o = sum of O_i 2^(mo_i - m) / l over the unit's O of this row; one without keys that the row sees adds nothing
-            use0 = __uint_as_float(y[2]) != 0.f || __uint_as_float(y[6]) != 0.f;
-            f0 = use0 ? ex2f(__uint_as_float(y[1]) - mj) * inv : 0.f;
-            if (!g.two) {
-                use1 = __uint_as_float(y[10]) != 0.f || __uint_as_float(y[14]) != 0.f;
-                f1 = use1 ? ex2f(__uint_as_float(y[9]) - mj) * inv : 0.f;
-            }
+            f0 = use0 ? ex2f(sums.mo - mj) * inv : 0.f;
+            f1 = use1 ? ex2f(__uint_as_float(y[1]) - mj) * inv : 0.f;
         }
         // The S products no longer need Q: the rows of tile i take the place of Q tile i (a unit of one tile: the second)
-        const uint32_t tile = x.base + L::kQ + (g.two ? i : 1) * 2 * L::kT8;
-        const int part = g.two ? h : 2 * i + h, parts = g.two ? 2 : 4;
+        const uint32_t tile = x.base + L::kQ + (two ? i : 1) * 2 * L::kT8;
         if (warp_live) {
+            const int n = two ? D / 16 : D / 32;
 #pragma unroll 1
-            for (int q = part * (D / 16) / parts; q < (part + 1) * (D / 16) / parts; ++q) {
+            for (int k = 0; k < n; ++k) {
+                const int q = two ? k : i * n + k;
                 uint32_t o[16], o1[16];
-                tmem_ld16(tO + (g.two ? D * i : 0) + 16 * q, o);
-                if (!g.two) tmem_ld16(tO + D + 16 * q, o1);
+                tmem_ld16(tO + D * i + 16 * q, o);
+                if (!two) tmem_ld16(tO + D * (i ^ 1) + 16 * q, o1);
                 tc::tmem_ld_wait();
                 float v[16];
 #pragma unroll
                 for (int e = 0; e < 16; ++e)
                     v[e] = (use0 ? __uint_as_float(o[e]) * f0 : 0.f) + (use1 ? __uint_as_float(o1[e]) * f1 : 0.f);
                 if (nans)
-#pragma unroll 1
-                    for (int e = 0; e < 16; ++e)
-                        if (nan_first[16 * q + e] < end) {
 #pragma unroll
-                            for (int k = 0; k < 16; ++k)
-                                if (k == e) v[k] = NAN;
-                        }
+                    for (int e = 0; e < 16; ++e)
+                        if (nan_first[16 * q + e] < end) v[e] = NAN;
                 put_cols<D>(a, g, out, m, row, tile, q, v);
             }
         }
-        if (part == 0) put_lse(a, g, out, D, m, lj != 0.f ? mj + __log2f(lj) : -INFINITY);
+        if (two || i == 0) put_lse(a, g, out, D, m, lj != 0.f ? mj + __log2f(lj) : -INFINITY);
         tc::tc_fence_before();
         if (staged) {
-            if (g.two) {
-                tile_sync(i);
-                put_rows<D, 256>(a, g, g.m0 + 128 * i, tile, threadIdx.x & 255);
+            if (two) {
+                group_sync(i);
+                put_rows<D, 128>(a, g, g.m0 + 128 * i, tile, row);
             } else {
                 softmax_sync();
-                put_rows<D, 512>(a, g, g.m0, tile, threadIdx.x);
+                put_rows<D, 256>(a, g, g.m0, tile, threadIdx.x);
             }
         }
-        // The next unit's Q may be written once all groups are done with this one. The widening warps are at most two
+        // The next unit's Q may be written once both groups are done with this one. The widening warps are at most two
         // tiles ahead of the PV products, so they come back to these words only after three more units have begun.
         softmax_sync();
         if (nans && threadIdx.x < D) nan_first[threadIdx.x] = *nan_any = 0x7fffffff;
@@ -1226,7 +1206,7 @@ __device__ __forceinline__ void softmax(const Ctx<D>& x, const CacheAttnArgs& a,
 }
 
 // ------------------------------------------------------------------- kernel
-template <int D, int GK>
+template <int D, int NG>
 __global__ void __launch_bounds__(kThreads, 1)
     cache_attn_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, const CacheAttnArgs a) {
     using L = Smem<D>;
@@ -1246,18 +1226,18 @@ __global__ void __launch_bounds__(kThreads, 1)
         for (int s = 0; s < 2; ++s) {
             tc::mbar_init(x.bar(B_VFULL, s), 1);
             tc::mbar_init(x.bar(B_VEMPTY, s), 4);  // lane 0 of the widening warps
-            tc::mbar_init(x.bar(B_P, 2 * s), kSoftmax / 64 + 4);  // lane 0 of the groups (0, h) and of the widening warps
+            tc::mbar_init(x.bar(B_P, 2 * s), kSoftmax / 64 + 4);  // lane 0 of group 0's warps and of the widening warps
             tc::mbar_init(x.bar(B_P, 2 * s + 1), kSoftmax / 64);
             tc::mbar_init(x.bar(B_PV, s), 1);
         }
         tc::mbar_init(x.bar(B_Q, 0), kSoftmax / 32);
         tc::fence_barrier_init();
     }
-    if (warp == 17) {
+    if (warp == 9) {
         tc::tmem_alloc(tc::smem_addr(x.words()), kTmemCols);
         tc::tmem_relinquish();
     }
-    if (warp == 16 && lane == 0) {
+    if (warp == 8 && lane == 0) {
         tc::prefetch_tmap(&tk);
         tc::prefetch_tmap(&tv);
     }
@@ -1270,19 +1250,19 @@ __global__ void __launch_bounds__(kThreads, 1)
     const bool aligned = (sbase() & 1023u) == 0 && x.tmem == 0;
     if (tid == 0 && !aligned) x.words()[1] = 1;
     if (st->left > 0 && aligned) {
-        if (warp >= 16) {
+        if (warp >= 8) {
             tc::regs_dec<kRegsOther>();
-            if (warp == 16) produce<D>(x.own(), a, *st, &tk, &tv);
-            else if (warp == 17) issue<D>(a, *st);
-            else if (warp >= 20) widen<D>(x.own(), a, *st);
+            if (warp == 8) produce<D>(x.own(), a, *st, &tk, &tv);
+            else if (warp == 9) issue<D>(a, *st);
+            else if (warp >= 12) widen<D>(x.own(), a, *st);
         } else {
             tc::regs_inc<kRegsSoftmax>();
-            softmax<D, GK>(x.own(), a, *st);
+            softmax<D, NG>(x.own(), a, *st);
         }
     }
     tc::tc_fence_before();
     __syncthreads();
-    if (warp == 17) {
+    if (warp == 9) {
         tc::tc_fence_after();
         tc::tmem_dealloc(x.tmem, kTmemCols);
     }
@@ -1339,19 +1319,24 @@ bool make_map(CUtensorMap* m, const CacheView& c, const void* base) {
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, int GK>
-cudaError_t launch_gk(const CacheAttnArgs& a, int ctas, cudaStream_t st) {
+template <int D, int NG>
+cudaError_t launch_ng(const CacheAttnArgs& a, int ctas, cudaStream_t st) {
     CUtensorMap tk, tv;
     if (!make_map<D>(&tk, a.c, a.c.k) || !make_map<D>(&tv, a.c, a.c.v)) return cudaErrorInvalidValue;
-    const cudaError_t e = cudaFuncSetAttribute(cache_attn_kernel<D, GK>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::kBytes);
+    const cudaError_t e = cudaFuncSetAttribute(cache_attn_kernel<D, NG>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::kBytes);
     if (e != cudaSuccess) return e;
-    cache_attn_kernel<D, GK><<<ctas, kThreads, Smem<D>::kBytes, st>>>(tk, tv, a);
+    cache_attn_kernel<D, NG><<<ctas, kThreads, Smem<D>::kBytes, st>>>(tk, tv, a);
     return cudaGetLastError();
 }
 
 template <int D>
 cudaError_t launch_d(const CacheAttnArgs& a, int ctas, cudaStream_t st) {
-    return a.c.page == 16 ? launch_gk<D, 16>(a, ctas, st) : launch_gk<D, 32>(a, ctas, st);
+    switch (a.c.page) {
+        case 16: return launch_ng<D, 8>(a, ctas, st);
+        case 32: return launch_ng<D, 4>(a, ctas, st);
+        case 64: return launch_ng<D, 2>(a, ctas, st);
+        default: return launch_ng<D, 1>(a, ctas, st);
+    }
 }
 
 }  // namespace cattn
