@@ -22,7 +22,7 @@ namespace cattn {
 constexpr int kTileKeys = 128;
 constexpr int kUnitRows = 256;
 constexpr int kMaxCtas = 256;
-constexpr int kUnitTiles = 4;
+constexpr int kUnitTiles = 6;
 // A share is at least this long where there is too little work for all CTAs: below it the partial results cost more
 // than the shorter shares save. (At least 2, so that each of the shares of a unit holds a tile of it.)
 constexpr int kMinShare = 6;

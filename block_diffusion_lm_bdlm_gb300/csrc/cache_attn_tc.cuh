@@ -11,8 +11,8 @@
 // times a hundred thousand keys counts), so the values are widened to fp16
 // (exact) on their way and the weights are fp16: p'_j = 2^(log2 p_j + log2 vs_j
 // - mo), with the value scale vs of the page in the exponent, where it costs
-// nothing, and an offset mo per row that keeps the largest p' between 2^7 and
-// 2^15 (fp16 ends at 2^16; what falls below 2^-24 is 2^-31 of the largest).
+// nothing, and an offset mo per row that keeps the largest p' between 2^3 and
+// 2^15 (fp16 ends at 2^16; what falls below 2^-24 is 2^-27 of the largest).
 // l = sum 2^(s_j - m) is kept in fp32 with an offset m of its own: the sum of
 // each page's p' times 2^(mo - m - log2 vs).
 //
@@ -192,13 +192,13 @@ __device__ __forceinline__ void widen4(uint32_t c, uint32_t& lo, uint32_t& hi) {
         : "=r"(lo), "=r"(hi)
         : "r"(c));
 }
-// four fp32 -> four e4m3 codes (nearest even, saturating)
-__device__ __forceinline__ uint32_t narrow4(float x0, float x1, float x2, float x3) {
+// four fp16 -> four e4m3 codes (nearest even, saturating)
+__device__ __forceinline__ uint32_t narrow4(uint32_t lo, uint32_t hi) {
     uint32_t r;
-    asm("{\n\t.reg .b16 a, b;\n\tcvt.rn.satfinite.e4m3x2.f32 a, %2, %1;\n\tcvt.rn.satfinite.e4m3x2.f32 b, %4, %3;\n\t"
+    asm("{\n\t.reg .b16 a, b;\n\tcvt.rn.satfinite.e4m3x2.f16x2 a, %1;\n\tcvt.rn.satfinite.e4m3x2.f16x2 b, %2;\n\t"
         "mov.b32 %0, {a, b};\n\t}"
         : "=r"(r)
-        : "f"(x0), "f"(x1), "f"(x2), "f"(x3));
+        : "r"(lo), "r"(hi));
     return r;
 }
 
@@ -791,18 +791,28 @@ __device__ __forceinline__ void split_q(const Ctx<D>& x, const CacheAttnArgs& a,
             const uint32_t top = (uint32_t)imax((int)(big[i] & 0xffffu), (int)(big[i] >> 16)) << 16;
             const bool fine = top < 0x7f800000u;
             const uint32_t sc = fine ? __float_as_uint(pow2_scale(__uint_as_float(top))) : 0x3f800000u;
-            const float inv = __uint_as_float(0x7f000000u - sc);  // 2^-k for 2^k, -126 <= k <= 120
+            // 2^-k for 2^k, -126 <= k <= 120, twice as bf16; the products are exact, and in fp16 too (at most 448, and what
+            // fp16 drops is 2^-33 of the row's largest)
+            const uint32_t inv2 = __byte_perm(0x7f000000u - sc, 0, 0x3232);
+            const __nv_bfloat162 inv = *reinterpret_cast<const __nv_bfloat162*>(&inv2);
             uint32_t hi[2], lo[2];
 #pragma unroll
             for (int e = 0; e < 2; ++e) {
-                const float f0 = __uint_as_float(u[2 * e] << 16) * inv, f1 = __uint_as_float(u[2 * e] & 0xffff0000u) * inv;
-                const float f2 = __uint_as_float(u[2 * e + 1] << 16) * inv, f3 = __uint_as_float(u[2 * e + 1] & 0xffff0000u) * inv;
-                hi[e] = narrow4(f0, f1, f2, f3);
-                uint32_t b0, b1;
-                widen4(hi[e], b0, b1);
-                const float2 h0 = __half22float2(*reinterpret_cast<const __half2*>(&b0));
-                const float2 h1 = __half22float2(*reinterpret_cast<const __half2*>(&b1));
-                lo[e] = narrow4(f0 - h0.x, f1 - h0.y, f2 - h1.x, f3 - h1.y);
+                uint32_t f[2], h[2], d[2];
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const __nv_bfloat162 y = __hmul2(*reinterpret_cast<const __nv_bfloat162*>(&u[2 * e + k]), inv);
+                    const uint32_t w = *reinterpret_cast<const uint32_t*>(&y);
+                    f[k] = pack_h2(__uint_as_float(w << 16), __uint_as_float(w & 0xffff0000u));
+                }
+                hi[e] = narrow4(f[0], f[1]);
+                widen4(hi[e], h[0], h[1]);
+#pragma unroll
+                for (int k = 0; k < 2; ++k) {
+                    const __half2 y = __hsub2(*reinterpret_cast<const __half2*>(&f[k]), *reinterpret_cast<const __half2*>(&h[k]));
+                    d[k] = *reinterpret_cast<const uint32_t*>(&y);
+                }
+                lo[e] = narrow4(d[0], d[1]);
             }
             if (r < padded) {
                 const uint32_t at = x.base + L::kQ + (r >> 7) * 2 * L::kT8 + swz8<D>(r & 127, chunk >> 1) + 8 * (chunk & 1);
@@ -823,15 +833,15 @@ struct RowSums {
 
 // p' of the 64 keys of a row whose scores were loaded from TMEM column tC on into r; p' goes to pk as fp16 pairs. NG pages
 // of GK keys each; sc points at the first one's key scale. The row sees the first `visible` keys; `full`: all of the
-// warp's rows see all. `settle(alpha)` waits until the row's O (at tO) may be rescaled, and rescales by the power of two
-// alpha what p' of this tile has been passed to TMEM already.
+// warp's rows see all; `first`: the row's O holds nothing yet. `settle(alpha)` waits until O (at tO) may be rescaled, and
+// rescales by the power of two alpha what the tile has stored of p' already.
 //
 // Keys are first taken with the row's present offsets. p' is positive, so a sum of at most 2^15 says that every p' fits
 // fp16, and no maximum is needed; it holds for all but a few tiles of a sequence. Where a row of the warp has a larger
 // sum or sees its first keys, or a page's value scale is so small that its p' may fall below what fp32 holds, the warp
 // takes the keys again: new offsets from their maxima, O and l rescaled, and l from the weights themselves where p' says
-// too little. (A sum over 2^15 of 64 keys has a p' of 2^9, which moves mo; the largest is 2^7 then, and the sum at most
-// 2^13.)
+// too little. (A sum over 2^15 of 64 keys has a p' of 2^9, which moves mo; the largest is at most 2^4 then, which leaves
+// room for scores that grow, and n keys below 2^-14 of fp16's normal range lose at most n 2^-29 of the largest weight.)
 template <int D, int NG, typename Settle>
 __device__ __forceinline__ void softmax_part(uint32_t (&r)[2][32], uint32_t (&pk)[32], uint32_t tC, uint32_t tO, const float* sc,
                                              float cs, int visible, bool full, bool first, RowSums& s, Settle settle) {
@@ -860,18 +870,23 @@ __device__ __forceinline__ void softmax_part(uint32_t (&r)[2][32], uint32_t (&pk
         }
         return s0.x + s1.x + (s0.y + s1.y);
     };
-    mask();
-    const float m_was = s.m == -INFINITY ? 0.f : s.m, mo_was = s.mo == -INFINITY ? 0.f : s.mo;
-    float sum = 0.f, all = 0.f, low = INFINITY;
+    float sum = 0.f;
+    bool again = first;
+    if (!first) {
+        mask();
+        const float m_was = s.m == -INFINITY ? 0.f : s.m, mo_was = s.mo == -INFINITY ? 0.f : s.mo;
+        float all = 0.f, low = INFINITY;
 #pragma unroll
-    for (int g = 0; g < NG; ++g) {
-        const float b = sc[8 + g * (GK / 16)] - mo_was, shift = b + m_was;
-        low = fminf(low, shift);
-        const float part = weigh(g, cs * sc[g * (GK / 16)], b);
-        all += part;
-        sum = fmaf(part, ex2f(-shift), sum);
+        for (int g = 0; g < NG; ++g) {
+            const float b = sc[8 + g * (GK / 16)] - mo_was, shift = b + m_was;
+            low = fminf(low, shift);
+            const float part = weigh(g, cs * sc[g * (GK / 16)], b);
+            all += part;
+            sum = fmaf(part, ex2f(-shift), sum);
+        }
+        again = __any_sync(0xffffffffu, all > 32768.f || low < -60.f || (s.mo == -INFINITY && visible > 0));
     }
-    if (__any_sync(0xffffffffu, all > 32768.f || low < -60.f || (s.mo == -INFINITY && visible > 0))) {
+    if (again) {
         tc::tmem_ld32(tC, r[0]);
         tc::tmem_ld32(tC + 32, r[1]);
         tc::tmem_ld_wait();
@@ -897,7 +912,7 @@ __device__ __forceinline__ void softmax_part(uint32_t (&r)[2][32], uint32_t (&pk
         const bool move = mxo > s.mo + 8.f;
         float alpha = 1.f;
         if (move) {
-            const float to = ceilf(mxo) - 7.f;  // whole numbers, so that rescaling loses nothing
+            const float to = ceilf(mxo) - 4.f;  // whole numbers, so that rescaling loses nothing
             alpha = ex2f(s.mo - to);
             s.mo = to;
         }
@@ -937,27 +952,27 @@ struct Out {
     int slot_r;   // its rows
 };
 
-// Writes 16 columns (from 16 q on) of flat row m: into the slot; as fp32 to o; or as bf16 into the staging tile at
+// Writes 32 columns (from 32 q on) of flat row m: into the slot; as fp32 to o; or as bf16 into the staging tile at
 // `stage`, whose row `row` is this one.
 template <int D>
 __device__ __forceinline__ void put_cols(const CacheAttnArgs& a, const Seg& g, const Out& out, int m, int row, uint32_t stage,
-                                         int q, const float (&v)[16]) {
+                                         int q, const float (&v)[32]) {
     if (out.slot) {
         if (m < g.last) {
-            float4* dst = reinterpret_cast<float4*>(out.slot) + (4 * q) * out.slot_r + (m - g.m0);
+            float4* dst = reinterpret_cast<float4*>(out.slot) + (8 * q) * out.slot_r + (m - g.m0);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) dst[e * out.slot_r] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+            for (int e = 0; e < 8; ++e) dst[e * out.slot_r] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
         }
     } else if (a.o_f32) {
         if (m < g.last) {
-            float4* dst = reinterpret_cast<float4*>(a.o_f32 + ((long long)(g.row0 + m / a.G) * a.H + g.h * a.G + m % a.G) * D + 16 * q);
+            float4* dst = reinterpret_cast<float4*>(a.o_f32 + ((long long)(g.row0 + m / a.G) * a.H + g.h * a.G + m % a.G) * D + 32 * q);
 #pragma unroll
-            for (int e = 0; e < 4; ++e) dst[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
+            for (int e = 0; e < 8; ++e) dst[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
         }
     } else {
 #pragma unroll
-        for (int e = 0; e < 2; ++e)
-            sts16(stage + row * 2 * D + (((2 * q + e) ^ (row & 7)) << 4), pack_bf2(v[8 * e], v[8 * e + 1]),
+        for (int e = 0; e < 4; ++e)
+            sts16(stage + row * 2 * D + (((4 * q + e) ^ (row & 7)) << 4), pack_bf2(v[8 * e], v[8 * e + 1]),
                   pack_bf2(v[8 * e + 2], v[8 * e + 3]), pack_bf2(v[8 * e + 4], v[8 * e + 5]), pack_bf2(v[8 * e + 6], v[8 * e + 7]));
     }
 }
@@ -1062,11 +1077,11 @@ __device__ __forceinline__ void softmax(const Ctx<D>& x, const CacheAttnArgs& a,
                 ph ^= 1;
             }
         };
-        auto pass_on = [&](uint32_t n) {  // p' of tile n is in TMEM
+        auto pass_on = [&](int n) {  // p' is in TMEM
             tc::tmem_st_wait();
             tc::tc_fence_before();
             __syncwarp();
-            if (lane == 0) tc::mbar_arrive(x.bar(B_P, 2 * (n & 1) + i));
+            if (lane == 0) tc::mbar_arrive(x.bar(B_P, n));
         };
         constexpr int NGP = NG > 1 ? NG / 2 : 1;  // pages in 64 keys
         if (two) {
@@ -1078,20 +1093,20 @@ __device__ __forceinline__ void softmax(const Ctx<D>& x, const CacheAttnArgs& a,
                     wait(B_S1, stage, ph);
                 }
                 if (warp_live) {
-                    // S of a tile is issued behind the PV of the one before, so O is settled
                     uint32_t r[2][32], pk[32];
                     const uint32_t tC = tS + 128 * i;
                     const float* sc = scales + 16 * slot;
                     tc::tmem_ld32(tC, r[0]);
                     tc::tmem_ld32(tC + 32, r[1]);
                     tc::tmem_ld_wait();
+                    // S of a tile is issued behind the PV of the one before, so O is settled
                     softmax_part<D, NGP>(r, pk, tC, tO + D * i, sc, cs, sees, all_see >= 64, j == 0, sums, [](float) {});
+                    tc::tmem_st32(tC, pk);
                     tc::tmem_ld32(tC + 64, r[0]);
                     tc::tmem_ld32(tC + 96, r[1]);
-                    tc::tmem_st32(tC, pk);
                     tc::tmem_ld_wait();
                     softmax_part<D, NGP>(r, pk, tC + 64, tO + D * i, sc + 4, cs, sees - 64, all_see >= 128, j == 0, sums, [&](float alpha) {
-                        // the first half's p'
+                        // what the first half has stored
                         uint32_t w[32];
                         tc::tmem_st_wait();
                         tc::tmem_ld32(tC, w);
@@ -1106,7 +1121,7 @@ __device__ __forceinline__ void softmax(const Ctx<D>& x, const CacheAttnArgs& a,
                     });
                     tc::tmem_st32(tC + 32, pk);
                 }
-                pass_on(t);
+                pass_on(2 * (t & 1) + i);
                 s0_phases ^= 1u << stage;
                 up();
             }
@@ -1125,7 +1140,7 @@ __device__ __forceinline__ void softmax(const Ctx<D>& x, const CacheAttnArgs& a,
                     });
                     tc::tmem_st32(tC, pk);
                 }
-                pass_on(t);
+                pass_on(2 * (t & 1) + i);
                 up();
             }
         }
@@ -1168,22 +1183,22 @@ __device__ __forceinline__ void softmax(const Ctx<D>& x, const CacheAttnArgs& a,
         // The S products no longer need Q: the rows of tile i take the place of Q tile i (a unit of one tile: the second)
         const uint32_t tile = x.base + L::kQ + (two ? i : 1) * 2 * L::kT8;
         if (warp_live) {
-            const int n = two ? D / 16 : D / 32;
+            const int n = two ? D / 32 : D / 64;
 #pragma unroll 1
             for (int k = 0; k < n; ++k) {
                 const int q = two ? k : i * n + k;
-                uint32_t o[16], o1[16];
-                tmem_ld16(tO + D * i + 16 * q, o);
-                if (!two) tmem_ld16(tO + D * (i ^ 1) + 16 * q, o1);
+                uint32_t o[32], o1[32];
+                tc::tmem_ld32(tO + D * i + 32 * q, o);
+                if (!two) tc::tmem_ld32(tO + D * (i ^ 1) + 32 * q, o1);
                 tc::tmem_ld_wait();
-                float v[16];
+                float v[32];
 #pragma unroll
-                for (int e = 0; e < 16; ++e)
+                for (int e = 0; e < 32; ++e)
                     v[e] = (use0 ? __uint_as_float(o[e]) * f0 : 0.f) + (use1 ? __uint_as_float(o1[e]) * f1 : 0.f);
                 if (nans)
 #pragma unroll
-                    for (int e = 0; e < 16; ++e)
-                        if (nan_first[16 * q + e] < end) v[e] = NAN;
+                    for (int e = 0; e < 32; ++e)
+                        if (nan_first[32 * q + e] < end) v[e] = NAN;
                 put_cols<D>(a, g, out, m, row, tile, q, v);
             }
         }
