@@ -93,24 +93,19 @@ def bdlm_cache_pages_workspace_bytes(n_pages: int, n_seqs: int) -> int:
 _NULL = nullcontext()
 
 
-class _On:
-    """The device and stream of a call: launches go to the cache's device, and
-    what the call allocates belongs to the stream that uses it."""
-
-    __slots__ = ("handle", "device", "stream")
-
-    def __init__(self, cache, stream):
-        self.device = _NULL if cache.device.index == torch.cuda.current_device() else torch.cuda.device(cache.device)
-        if stream is None:
-            self.stream = _NULL
-            self.handle = torch.cuda.current_stream(cache.device).cuda_stream
-        else:
-            if not hasattr(stream, "cuda_stream"):
-                stream = torch.cuda.ExternalStream(int(stream), device=cache.device)
-            elif stream.device != cache.device:
-                raise ValueError(f"the stream is on {stream.device}, the cache on {cache.device}")
-            self.stream = torch.cuda.stream(stream)
-            self.handle = stream.cuda_stream
+def _on(cache, stream):
+    """(handle of the call's stream, context to make the call in): launches go
+    to the cache's device, and what the call allocates belongs to the stream
+    that uses it."""
+    if stream is None:
+        index = cache.device.index
+        here = _NULL if index == torch.cuda.current_device() else torch.cuda.device(index)
+        return torch._C._cuda_getCurrentRawStream(index), here
+    if not hasattr(stream, "cuda_stream"):
+        stream = torch.cuda.ExternalStream(int(stream), device=cache.device)
+    elif stream.device != cache.device:
+        raise ValueError(f"the stream is on {stream.device}, the cache on {cache.device}")
+    return stream.cuda_stream, torch.cuda.stream(stream)
 
 
 def _workspace(cache, workspace, need):
@@ -136,8 +131,8 @@ def _layer(cache, layer):
         raise ValueError(f"layer {layer} is outside the cache's {cache.n_layers}")
 
 
-def _read(lib, workspace, on, where):
-    _check(lib.bdlm_read_error(workspace.data_ptr(), on.handle), where + " (device)")
+def _read(lib, workspace, handle, where):
+    _check(lib.bdlm_read_error(workspace.data_ptr(), handle), where + " (device)")
 
 
 def bdlm_cache_write(cache: PageCache, k_new, v_new, cu_rows, *, layer: int = 0, workspace=None, stream=None,
@@ -148,19 +143,22 @@ def bdlm_cache_write(cache: PageCache, k_new, v_new, cu_rows, *, layer: int = 0,
     lib = load_library()
     _bf16_cuda("k_new", k_new)
     _bf16_cuda("v_new", v_new)
-    _shape("k_new", k_new, (k_new.shape[0], cache.kv_heads, cache.head_dim))
-    _shape("v_new", v_new, k_new.shape)
+    shape = k_new.shape
+    if len(shape) != 3 or shape[1] != cache.kv_heads or shape[2] != cache.head_dim:
+        raise ValueError(f"k_new must be [T, {cache.kv_heads}, {cache.head_dim}], got {tuple(shape)}")
+    if v_new.shape != shape:
+        raise ValueError(f"v_new must be shaped {tuple(shape)}, got {tuple(v_new.shape)}")
     if k_new.device != cache.device or v_new.device != cache.device:
         raise ValueError("k_new and v_new must be on the cache's device")
     cu = _ints("cu_rows", cache, cu_rows, cache.n_seqs + 1)
     _layer(cache, layer)
-    on = _On(cache, stream)
-    with on.device, on.stream:
+    handle, here = _on(cache, stream)
+    with here:
         ws = _workspace(cache, workspace, 256)
-        _check(lib.bdlm_cache_write(cache.c, layer, k_new.data_ptr(), v_new.data_ptr(), k_new.shape[0], cu,
-                                    ws.data_ptr(), ws.numel(), on.handle), "bdlm_cache_write")
+        _check(lib.bdlm_cache_write(cache.c, layer, k_new.data_ptr(), v_new.data_ptr(), shape[0], cu,
+                                    ws.data_ptr(), ws.numel(), handle), "bdlm_cache_write")
         if check:
-            _read(lib, ws, on, "bdlm_cache_write")
+            _read(lib, ws, handle, "bdlm_cache_write")
 
 
 def bdlm_cache_attn_fwd(cache: PageCache, q, cu_rows, block: int, *, layer: int = 0, q_pos=None,
@@ -180,8 +178,8 @@ def bdlm_cache_attn_fwd(cache: PageCache, q, cu_rows, block: int, *, layer: int 
     pos = None if q_pos is None else _ints("q_pos", cache, q_pos, cache.n_seqs)
     _layer(cache, layer)
     need = lib.bdlm_cache_attn_fwd_workspace_bytes(T, H, cache.kv_heads, d, cache.n_seqs)
-    on = _On(cache, stream)
-    with on.device, on.stream:
+    handle, here = _on(cache, stream)
+    with here:
         if out is None:
             out = torch.empty_like(q)
         elif out.dtype not in (torch.bfloat16, torch.float32) or out.shape != q.shape or out.device != cache.device \
@@ -195,24 +193,24 @@ def bdlm_cache_attn_fwd(cache: PageCache, q, cu_rows, block: int, *, layer: int 
         ws = _workspace(cache, workspace, max(need, 256))
         st = lib.bdlm_cache_attn_fwd(cache.c, layer, q.data_ptr(), out.data_ptr(), lse.data_ptr(), T, H, block, cu, pos,
                                      softmax_scale, BDLM_F32 if out.dtype == torch.float32 else BDLM_BF16,
-                                     ws.data_ptr(), ws.numel(), on.handle)
+                                     ws.data_ptr(), ws.numel(), handle)
         _check(st, "bdlm_cache_attn_fwd")
         if check:
-            _read(lib, ws, on, "bdlm_cache_attn_fwd")
+            _read(lib, ws, handle, "bdlm_cache_attn_fwd")
     return out, lse
 
 
 def _pages_call(cache, name, args, workspace, stream, check, make=None):
     lib = load_library()
-    on = _On(cache, stream)
-    with on.device, on.stream:
+    handle, here = _on(cache, stream)
+    with here:
         ws = _workspace(cache, workspace, max(lib.bdlm_cache_pages_workspace_bytes(cache.n_pages, cache.n_seqs), 256))
         made = None if make is None else make()
         if made is not None:
             args = (made.data_ptr(),)
-        _check(getattr(lib, name)(cache.c, *args, ws.data_ptr(), ws.numel(), on.handle), name)
+        _check(getattr(lib, name)(cache.c, *args, ws.data_ptr(), ws.numel(), handle), name)
         if check:
-            _read(lib, ws, on, name)
+            _read(lib, ws, handle, name)
     return made
 
 

@@ -110,7 +110,7 @@ struct CachePagesArgs {
 
 size_t cache_attn_scratch_bytes(long long total_rows, int H, int Hk, int D, int n_seqs);
 size_t cache_pages_scratch_bytes(int n_pages, int n_seqs);
-cudaError_t launch_cache_write(const CacheWriteArgs& a, cudaStream_t st, int* launches);
+cudaError_t launch_cache_write(const CacheWriteArgs& a, int num_sms, cudaStream_t st, int* launches);
 cudaError_t launch_cache_attn(const CacheAttnArgs& a, int num_sms, cudaStream_t st, int* launches);
 cudaError_t launch_cache_pages(const CachePagesArgs& a, int num_sms, cudaStream_t st, int* launches);
 

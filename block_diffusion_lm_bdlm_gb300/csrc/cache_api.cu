@@ -96,8 +96,10 @@ int bdlm_cache_write(const bdlm_cache* cache, int32_t layer, const void* k_new, 
     a.cu_rows = cu_rows;
     a.total_rows = (int)total_rows;
     a.hdr = static_cast<WsHeader*>(workspace);
+    const int sms = device_sms();
     int launches = 0;
-    if (launch_cache_write(a, reinterpret_cast<cudaStream_t>(stream), &launches) != cudaSuccess) return BDLM_ERR_CUDA;
+    if (sms <= 0 || launch_cache_write(a, sms, reinterpret_cast<cudaStream_t>(stream), &launches) != cudaSuccess)
+        return BDLM_ERR_CUDA;
     set_last_launches(launches);
     return BDLM_OK;
 }

@@ -16,18 +16,21 @@
 namespace bdlm {
 namespace {
 
-constexpr int kThreads = 256;
+constexpr int kV = 4;
+constexpr int kThreadsPerSm = 2048;
+constexpr uint32_t kInf = 0x7f800000u;
 
 __device__ __forceinline__ long long slot_base(const int* cu, int s, int shift) {
     return ((long long)__ldg(cu + s) >> shift) + 2LL * s;
 }
 
 // Block-wide check of every sequence; one thread writes the header.
+template <int T>
 __device__ void check_rows(const CacheWriteArgs& a) {
     __shared__ int s_bad;
     if (threadIdx.x == 0) s_bad = 0x7fffffff;
     __syncthreads();
-    for (int s = threadIdx.x; s < a.c.n_seqs; s += kThreads) {
+    for (int s = threadIdx.x; s < a.c.n_seqs; s += T) {
         const SeqRows r = seq_rows(a.c, a.cu_rows, nullptr, a.total_rows, s);
         bool bad = !r.ok;
         if (r.ok && r.rows > 0)
@@ -44,40 +47,69 @@ __device__ void check_rows(const CacheWriteArgs& a) {
     }
 }
 
-// eight e4m3 codes of x * inv; values that are not finite become NaN
-__device__ __forceinline__ uint2 encode8(const float (&x)[8], float inv) {
+// Eight e4m3 codes of x * inv. Values that are not finite become NaN, where
+// `some` says that there may be any.
+__device__ __forceinline__ uint2 encode8(const float (&x)[8], float inv, bool some) {
     uint32_t w[4];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
+    for (int i = 0; i < 4; ++i)
         w[i] = __nv_cvt_float2_to_fp8x2(make_float2(x[2 * i] * inv, x[2 * i + 1] * inv), __NV_SATFINITE, __NV_E4M3);
-        if (!is_finite(x[2 * i])) w[i] = (w[i] & 0xff00u) | 0x7fu;
-        if (!is_finite(x[2 * i + 1])) w[i] = (w[i] & 0x00ffu) | 0x7f00u;
-    }
-    return make_uint2(w[0] | w[1] << 16, w[2] | w[3] << 16);
-}
-
-__device__ __forceinline__ void decode8(uint2 c, float scale, float (&x)[8]) {
-    const uint32_t w[4] = {c.x & 0xffffu, c.x >> 16, c.y & 0xffffu, c.y >> 16};
+    if (some)
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-        const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)w[i], __NV_E4M3);
-        const float2 f = __half22float2(__half2(h));
-        x[2 * i] = f.x * scale;
-        x[2 * i + 1] = f.y * scale;
+        for (int i = 0; i < 4; ++i) {
+            if (!is_finite(x[2 * i])) w[i] = (w[i] & 0xff00u) | 0x7fu;
+            if (!is_finite(x[2 * i + 1])) w[i] = (w[i] & 0x00ffu) | 0x7f00u;
+        }
+    return make_uint2(__byte_perm(w[0], w[1], 0x5410), __byte_perm(w[2], w[3], 0x5410));
+}
+
+// A chunk of eight values as it was loaded: bf16 (a new row), or e4m3 codes in
+// x and y with the page's old scale (a kept one).
+__device__ __forceinline__ void values8(uint4 u, bool kept, float scale, float (&x)[8]) {
+    if (kept) {
+        const uint32_t w[4] = {u.x & 0xffffu, u.x >> 16, u.y & 0xffffu, u.y >> 16};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const __half2_raw h = __nv_cvt_fp8x2_to_halfraw2((__nv_fp8x2_storage_t)w[i], __NV_E4M3);
+            const float2 f = __half22float2(__half2(h));
+            x[2 * i] = f.x * scale;
+            x[2 * i + 1] = f.y * scale;
+        }
+    } else {
+        const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            x[2 * i] = __uint_as_float(w[i] << 16);
+            x[2 * i + 1] = __uint_as_float(w[i] & 0xffff0000u);
+        }
     }
 }
 
-// V: 16-byte loads of new rows per thread (page * d / 2048, at least 1)
-template <int V>
-__global__ void __launch_bounds__(kThreads) cache_write_kernel(const CacheWriteArgs a) {
+__device__ __forceinline__ uint32_t umax(uint32_t x, uint32_t y) { return x > y ? x : y; }
+
+// The CTA's largest x; one barrier.
+template <int T>
+__device__ __forceinline__ uint32_t cta_max(uint32_t x, uint32_t* buf) {
+    x = __reduce_max_sync(0xffffffffu, x);
+    if ((threadIdx.x & 31) == 0) buf[threadIdx.x >> 5] = x;
+    __syncthreads();
+    return __reduce_max_sync(0xffffffffu, buf[threadIdx.x & (T / 32 - 1)]);
+}
+
+// T threads with kV chunks of eight values each: T = page * d / 32. A CTA
+// takes `per_cta` of the 2 Hk (head, K or V) of a page, one after the other.
+template <int T>
+__global__ void __launch_bounds__(T, T == 32 ? 24 : 1024 / T) cache_write_kernel(const CacheWriteArgs a, int per_cta) {
     const CacheView& c = a.c;
     if (blockIdx.x == gridDim.x - 1) {
-        if (blockIdx.y == 0 && blockIdx.z == 0) check_rows(a);
+        check_rows<T>(a);
         return;
     }
     const int tid = threadIdx.x, lane = tid & 31;
+    const unsigned parts = 2u * c.Hk / (unsigned)per_cta;
+    const long long slot = blockIdx.x / parts;
+    const int kind0 = (int)(blockIdx.x - (unsigned)slot * parts) * per_cta;
     // the sequence of this slot: the last s with slot_base(s) <= slot, 32 ways at a time
-    const long long slot = blockIdx.x;
     int lo = 0, hi = c.n_seqs;  // in [lo, hi)
     while (hi - lo > 1) {
         const int step = (hi - lo + 31) / 32;
@@ -94,73 +126,127 @@ __global__ void __launch_bounds__(kThreads) cache_write_kernel(const CacheWriteA
     const long long page_no = (r.pos0 >> c.page_shift) + j;
     if (j < 0 || page_no > (r.len - 1) >> c.page_shift) return;
     const int id = __ldg(c.table + (long long)s * c.max_pages + page_no);
-    if (id < 0 || id >= c.n_pages) return;
 
-    const int head = blockIdx.y, D = c.D;
-    const __nv_bfloat16* src = blockIdx.z ? a.v_new : a.k_new;
-    const long long unit = (long long)id * c.Hk + head;
-    uint8_t* dst = (blockIdx.z ? c.v : c.k) + unit * c.page * D;
-    float* scale_at = (blockIdx.z ? c.v_scale : c.k_scale) + unit;
+    const int D = c.D, row_shift = D == 128 ? 4 : 3;   // 2^row_shift chunks are a row
     const int first = (int)(page_no << c.page_shift);  // position of the page's row 0
-    const int per_row = D / 8;
-    const float was = *scale_at;
+    const int kept = imax(0, r.pos0 - first);          // rows of the page that stay
+    const int rows = imin(c.page, r.len - first);      // and that are there in the end
+    // chunk i of the thread is at row row0 + i * step, columns col .. col + 7
+    const int row0 = tid >> row_shift, col = (tid & ((1 << row_shift) - 1)) * 8, step = T >> row_shift;
+    const long long src0 = ((long long)(r.row0 + first - r.pos0) * c.Hk) * D + col;
 
-    float x[V][8];
-    float amax = 0.f;
+    auto fetch = [&](int kind, uint4 (&u)[kV]) {
+        const __nv_bfloat16* src = (kind & 1 ? a.v_new : a.k_new) + src0 + (kind >> 1) * D;
 #pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const int chunk = tid + i * kThreads, row = chunk / per_row, col = chunk % per_row * 8;
-        const int pos = first + row;
+        for (int i = 0; i < kV; ++i) {
+            const int row = row0 + i * step;
+            u[i] = make_uint4(0, 0, 0, 0);
+            if (row >= kept && row < rows) u[i] = __ldg(reinterpret_cast<const uint4*>(src + (long long)row * c.Hk * D));
+        }
+    };
+    uint4 next[kV];
+    fetch(kind0, next);
+    if (id < 0 || id >= c.n_pages) return;
+    __shared__ uint32_t s_max[2][T / 32];
+#pragma unroll 1
+    for (int k = 0; k < per_cta; ++k) {
+        const int kind = kind0 + k;
+        uint4 u[kV];
 #pragma unroll
-        for (int e = 0; e < 8; ++e) x[i][e] = 0.f;
-        if (row < c.page && pos < r.len) {
-            if (pos >= r.pos0) {
-                const uint4 u = __ldg(reinterpret_cast<const uint4*>(
-                    src + ((long long)(r.row0 + pos - r.pos0) * c.Hk + head) * D + col));
-                const uint32_t w[4] = {u.x, u.y, u.z, u.w};
+        for (int i = 0; i < kV; ++i) u[i] = next[i];
+        if (k + 1 < per_cta) fetch(kind + 1, next);
+        const long long unit = (long long)id * c.Hk + (kind >> 1);
+        uint8_t* dst = (kind & 1 ? c.v : c.k) + unit * c.page * D + col;
+        float* scale_at = (kind & 1 ? c.v_scale : c.k_scale) + unit;
+        float was = 1.f;
+        uint32_t top = 0;  // the largest |x| as bits, which order as the values do; above kInf: NaN
+        if (kept == 0) {
 #pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    x[i][2 * e] = __uint_as_float(w[e] << 16);
-                    x[i][2 * e + 1] = __uint_as_float(w[e] & 0xffff0000u);
+            for (int i = 0; i < kV; ++i) {
+                const uint32_t m = __vmaxu2(__vmaxu2(u[i].x & 0x7fff7fffu, u[i].y & 0x7fff7fffu),
+                                            __vmaxu2(u[i].z & 0x7fff7fffu, u[i].w & 0x7fff7fffu));
+                top = __vmaxu2(top, m);
+            }
+            top = umax(top << 16, top & 0xffff0000u);
+        } else {
+            was = *scale_at;
+#pragma unroll
+            for (int i = 0; i < kV; ++i) {
+                const int row = row0 + i * step;
+                if (row < kept) {
+                    const uint2 w = *reinterpret_cast<const uint2*>(dst + row * D);
+                    u[i] = make_uint4(w.x, w.y, 0, 0);
                 }
-            } else {
-                decode8(*reinterpret_cast<const uint2*>(dst + row * D + col), was, x[i]);
+                float x[8];
+                values8(u[i], row < kept, was, x);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) top = umax(top, __float_as_uint(x[e]) & 0x7fffffffu);
             }
         }
+        top = cta_max<T>(top, s_max[k & 1]);  // also: every thread has read the old scale and the kept rows
+        const bool some = top >= kInf;
+        if (some) {  // the largest of the finite ones
+            top = 0;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) amax = fmaxf(amax, is_finite(x[i][e]) ? fabsf(x[i][e]) : 0.f);
+            for (int i = 0; i < kV; ++i) {
+                float x[8];
+                values8(u[i], row0 + i * step < kept, was, x);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) top = umax(top, is_finite(x[e]) ? __float_as_uint(x[e]) & 0x7fffffffu : 0u);
+            }
+            __syncthreads();  // s_max has been read
+            top = cta_max<T>(top, s_max[k & 1]);
+        }
+        const float scale = pow2_scale(__uint_as_float(top));
+        const float inv = 1.f / scale;  // exact: 2^-126 <= scale <= 2^120
+        if (tid == 0) *scale_at = scale;
+        if (kept == 0 && !some) {
+#pragma unroll
+            for (int i = 0; i < kV; ++i) {
+                const int row = row0 + i * step;
+                if (row < rows) {
+                    float x[8];
+                    values8(u[i], false, 1.f, x);
+                    *reinterpret_cast<uint2*>(dst + row * D) = encode8(x, inv, false);
+                }
+            }
+        } else {
+#pragma unroll 1
+            for (int i = 0; i < kV; ++i) {
+                const int row = row0 + i * step;
+                if (row < rows && (row >= kept || scale != was)) {
+                    float x[8];
+                    values8(u[0], row < kept, was, x);
+                    *reinterpret_cast<uint2*>(dst + row * D) = encode8(x, inv, true);
+                }
+#pragma unroll
+                for (int e = 0; e + 1 < kV; ++e) u[e] = u[e + 1];
+            }
+        }
     }
-#pragma unroll
-    for (int o = 16; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    __shared__ float s_max[kThreads / 32];
-    if (lane == 0) s_max[tid >> 5] = amax;
-    __syncthreads();  // also: every thread has read the old scale and the kept rows
-    amax = s_max[lane & (kThreads / 32 - 1)];
-#pragma unroll
-    for (int o = 4; o; o >>= 1) amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, o));
-    const float scale = pow2_scale(amax);
-    const float inv = 1.f / scale;  // exact: 2^-126 <= scale <= 2^120
-    if (tid == 0) *scale_at = scale;
-#pragma unroll
-    for (int i = 0; i < V; ++i) {
-        const int chunk = tid + i * kThreads, row = chunk / per_row, col = chunk % per_row * 8;
-        const int pos = first + row;
-        if (row < c.page && pos < r.len && (pos >= r.pos0 || scale != was))
-            *reinterpret_cast<uint2*>(dst + row * D + col) = encode8(x[i], inv);
-    }
+}
+
+template <int T>
+void launch(const CacheWriteArgs& a, long long slots, int per_cta, cudaStream_t st) {
+    cache_write_kernel<T><<<(unsigned)(slots * (2 * a.c.Hk / per_cta) + 1), T, 0, st>>>(a, per_cta);
 }
 
 }  // namespace
 
-cudaError_t launch_cache_write(const CacheWriteArgs& a, cudaStream_t st, int* launches) {
+cudaError_t launch_cache_write(const CacheWriteArgs& a, int num_sms, cudaStream_t st, int* launches) {
     const long long slots = ((long long)a.total_rows >> a.c.page_shift) + 2LL * a.c.n_seqs + 1;
-    const dim3 grid((unsigned)(slots + 1), (unsigned)a.c.Hk, 2);
-    switch (a.c.page * a.c.D / (8 * kThreads)) {
-        case 0:
-        case 1: cache_write_kernel<1><<<grid, kThreads, 0, st>>>(a); break;
-        case 2: cache_write_kernel<2><<<grid, kThreads, 0, st>>>(a); break;
-        case 4: cache_write_kernel<4><<<grid, kThreads, 0, st>>>(a); break;
-        default: cache_write_kernel<8><<<grid, kThreads, 0, st>>>(a); break;
+    const int threads = a.c.page * a.c.D / (8 * kV);
+    int per_cta = 1;
+    while (2 * a.c.Hk % (2 * per_cta) == 0 &&
+           slots * (2 * a.c.Hk / (2 * per_cta)) * threads >= (long long)kThreadsPerSm * num_sms)
+        per_cta *= 2;
+    if (slots * (2 * a.c.Hk / per_cta) >= 0x7fffffffLL) return cudaErrorInvalidConfiguration;
+    switch (threads) {
+        case 32: launch<32>(a, slots, per_cta, st); break;
+        case 64: launch<64>(a, slots, per_cta, st); break;
+        case 128: launch<128>(a, slots, per_cta, st); break;
+        case 256: launch<256>(a, slots, per_cta, st); break;
+        default: launch<512>(a, slots, per_cta, st); break;
     }
     const cudaError_t e = cudaGetLastError();
     if (e == cudaSuccess) ++*launches;
