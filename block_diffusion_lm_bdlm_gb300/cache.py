@@ -39,7 +39,7 @@ class PageCache:
     """
 
     __slots__ = ("k", "v", "k_scale", "v_scale", "table", "lens", "n_layers", "n_pages", "page", "kv_heads",
-                 "head_dim", "n_seqs", "max_pages", "device", "c")
+                 "head_dim", "n_seqs", "max_pages", "device", "index", "pages_bytes", "c")
 
     def __init__(self, k, v, k_scale, v_scale, table, lens):
         for nm, t, dt, dims in (("k", k, torch.float8_e4m3fn, 5), ("v", v, torch.float8_e4m3fn, 5),
@@ -61,7 +61,8 @@ class PageCache:
         _shape("v_scale", v_scale, k.shape[:3])
         _shape("lens", lens, (self.n_seqs,))
         self.k, self.v, self.k_scale, self.v_scale, self.table, self.lens = k, v, k_scale, v_scale, table, lens
-        self.device = k.device
+        self.device, self.index = k.device, k.get_device()
+        self.pages_bytes = max(bdlm_cache_pages_workspace_bytes(self.n_pages, self.n_seqs), 256)
         self.c = _CCache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), table.data_ptr(),
                          lens.data_ptr(), self.n_layers, self.n_pages, self.page, self.kv_heads, self.head_dim,
                          self.n_seqs, self.max_pages, 0)
@@ -98,9 +99,8 @@ def _on(cache, stream):
     to the cache's device, and what the call allocates belongs to the stream
     that uses it."""
     if stream is None:
-        index = cache.device.index
-        here = _NULL if index == torch.cuda.current_device() else torch.cuda.device(index)
-        return torch._C._cuda_getCurrentRawStream(index), here
+        here = _NULL if cache.index == torch.cuda.current_device() else torch.cuda.device(cache.index)
+        return torch._C._cuda_getCurrentRawStream(cache.index), here
     if not hasattr(stream, "cuda_stream"):
         stream = torch.cuda.ExternalStream(int(stream), device=cache.device)
     elif stream.device != cache.device:
@@ -119,7 +119,7 @@ def _workspace(cache, workspace, need):
 
 def _ints(name, cache, t, n):
     if not isinstance(t, torch.Tensor) or t.dtype != torch.int32 or t.dim() != 1 or not t.is_contiguous() \
-            or t.device != cache.device:
+            or t.get_device() != cache.index:
         raise ValueError(f"{name} must be a contiguous int32 tensor of one dimension on the cache's device")
     if n is not None and t.shape[0] != n:
         raise ValueError(f"{name} must have {n} entries, got {t.shape[0]}")
@@ -148,7 +148,7 @@ def bdlm_cache_write(cache: PageCache, k_new, v_new, cu_rows, *, layer: int = 0,
         raise ValueError(f"k_new must be [T, {cache.kv_heads}, {cache.head_dim}], got {tuple(shape)}")
     if v_new.shape != shape:
         raise ValueError(f"v_new must be shaped {tuple(shape)}, got {tuple(v_new.shape)}")
-    if k_new.device != cache.device or v_new.device != cache.device:
+    if k_new.get_device() != cache.index or v_new.get_device() != cache.index:
         raise ValueError("k_new and v_new must be on the cache's device")
     cu = _ints("cu_rows", cache, cu_rows, cache.n_seqs + 1)
     _layer(cache, layer)
@@ -171,7 +171,7 @@ def bdlm_cache_attn_fwd(cache: PageCache, q, cu_rows, block: int, *, layer: int 
     one for bdlm_lse_merge. Rows of q behind cu_rows[-1] are left unwritten."""
     lib = load_library()
     _bf16_cuda("q", q)
-    if q.dim() != 3 or q.shape[2] != cache.head_dim or q.device != cache.device:
+    if q.dim() != 3 or q.shape[2] != cache.head_dim or q.get_device() != cache.index:
         raise ValueError(f"q must be [T, H, {cache.head_dim}] on the cache's device")
     T, H, d = q.shape
     cu = _ints("cu_rows", cache, cu_rows, cache.n_seqs + 1)
@@ -204,7 +204,7 @@ def _pages_call(cache, name, args, workspace, stream, check, make=None):
     lib = load_library()
     handle, here = _on(cache, stream)
     with here:
-        ws = _workspace(cache, workspace, max(lib.bdlm_cache_pages_workspace_bytes(cache.n_pages, cache.n_seqs), 256))
+        ws = _workspace(cache, workspace, cache.pages_bytes)
         made = None if make is None else make()
         if made is not None:
             args = (made.data_ptr(),)

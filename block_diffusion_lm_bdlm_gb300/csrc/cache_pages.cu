@@ -84,6 +84,7 @@ __device__ __forceinline__ void run_of(int n, int rank, int* lo, int* hi) {
 }
 
 __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads, 1) plan_kernel(const CachePagesArgs a) {
+    asm volatile("griddepcontrol.launch_dependents;" ::: "memory");
     cg::cluster_group cluster = cg::this_cluster();
     __shared__ int buf[32];
     __shared__ long long wide[32];
@@ -304,7 +305,8 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const CachePagesArgs
     const Scratch s = carve(a.scratch, c.n_pages, c.n_seqs);
     const int lane = threadIdx.x & 31;
     const long long per = 2LL * c.n_layers * c.Hk;
-    const long long total = __ldg(s.n_copies) * per;
+    asm volatile("griddepcontrol.wait;" ::: "memory");  // for the plan's writes
+    const long long total = __ldcg(s.n_copies) * per;
     const long long stride = (long long)gridDim.x * (kCopyThreads / 32);
     for (long long u = (long long)blockIdx.x * (kCopyThreads / 32) + (threadIdx.x >> 5); u < total; u += stride) {
         const int i = (int)(u / per);
@@ -312,7 +314,7 @@ __global__ void __launch_bounds__(kCopyThreads) copy_kernel(const CachePagesArgs
         const int h = rest % c.Hk;
         rest /= c.Hk;
         const int layer = rest >> 1;
-        const int src = __ldg(s.src + i), dst = __ldg(s.dst + i), rows = __ldg(s.rows + i);
+        const int src = __ldcg(s.src + i), dst = __ldcg(s.dst + i), rows = __ldcg(s.rows + i);
         const long long from = ((long long)layer * c.n_pages + src) * c.Hk + h;
         const long long to = ((long long)layer * c.n_pages + dst) * c.Hk + h;
         uint8_t* base = (rest & 1) ? c.v : c.k;
@@ -346,8 +348,16 @@ cudaError_t launch_cache_pages(const CachePagesArgs& a, int num_sms, cudaStream_
     if (e != cudaSuccess) return e;
     ++*launches;
     if (a.op == PAGES_RESERVE) return e;
-    copy_kernel<<<num_sms * 4, kCopyThreads, 0, st>>>(a);
-    e = cudaGetLastError();
+    cudaLaunchConfig_t cfg{};
+    cfg.gridDim = dim3((unsigned)num_sms * 4);
+    cfg.blockDim = dim3(kCopyThreads);
+    cfg.stream = st;
+    cudaLaunchAttribute at{};
+    at.id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    at.val.programmaticStreamSerializationAllowed = 1;
+    cfg.attrs = &at;
+    cfg.numAttrs = 1;
+    e = cudaLaunchKernelEx(&cfg, copy_kernel, a);
     if (e == cudaSuccess) ++*launches;
     return e;
 }
