@@ -209,6 +209,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads,
                 const int before = base + block_scan((int)f, &t, buf);
                 if (i < phi) {
                     if (f && i < live) s.dst[before] = i;
+                    if (i == live) *s.n_copies = before;  // as many pages move as there are holes
                     if (!f && i >= live) s.rank[i] = live - 1 - (i - before);
                 }
                 base += t;
@@ -265,11 +266,8 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads,
         if (gtid == 0) *s.n_copies = all_need;
         return;
     }
-    // compact: there are as many movers as holes, so the mover with r movers behind it is number moves - 1 - r
-    int holes = 0;
-    for (int i = tid; i < live; i += kPlanThreads) holes += __ldcg(s.count + i) == 0;
-    block_scan(holes, &t, buf);
-    const int moves = t;
+    // compact: the mover with r movers behind it is number moves - 1 - r
+    const int moves = __ldcg(s.n_copies);  // 0 without a free page
     for (int i = imax(plo, live) + tid; i < phi; i += kPlanThreads)
         if (__ldcg(s.count + i) != 0) {
             const int k = moves - 1 - __ldcg(s.rank + i), to = __ldcg(s.dst + k);
@@ -277,10 +275,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads,
             s.rows[k] = c.page;
             s.rank[i] = to;
         }
-    if (gtid == 0) {
-        *s.n_copies = moves;
-        if (a.n_live) *a.n_live = live;
-    }
+    if (gtid == 0 && a.n_live) *a.n_live = live;
     cluster.sync();
     for (int q = gwarp; q < c.n_seqs; q += kAll / 32) {
         const int n = pages_of(__ldcg(c.lens + q), shift);
