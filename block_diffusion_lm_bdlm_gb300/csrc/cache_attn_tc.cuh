@@ -831,6 +831,13 @@ struct RowSums {
     float m, mo, l;
 };
 
+// A factor of scores: not so small that it turns the -inf of a masked key into NaN (NaN stays).
+__device__ __forceinline__ float at_least(float x) {
+    float y;
+    asm("max.NaN.f32 %0, %1, %2;" : "=f"(y) : "f"(x), "f"(1.17549435e-38f));
+    return y;
+}
+
 // p' of the 64 keys of a row whose scores were loaded from TMEM column tC on into r; p' goes to pk as fp16 pairs. NG pages
 // of GK keys each; sc points at the first one's key scale. The row sees the first `visible` keys; `full`: all of the
 // warp's rows see all; `first`: the row's O holds nothing yet. `settle(alpha)` waits until O (at tO) may be rescaled, and
@@ -880,7 +887,7 @@ __device__ __forceinline__ void softmax_part(uint32_t (&r)[2][32], uint32_t (&pk
         for (int g = 0; g < NG; ++g) {
             const float b = sc[8 + g * (GK / 16)] - mo_was, shift = b + m_was;
             low = fminf(low, shift);
-            const float part = weigh(g, cs * sc[g * (GK / 16)], b);
+            const float part = weigh(g, at_least(cs * sc[g * (GK / 16)]), b);
             all += part;
             sum = fmaf(part, ex2f(-shift), sum);
         }
@@ -901,7 +908,7 @@ __device__ __forceinline__ void softmax_part(uint32_t (&r)[2][32], uint32_t (&pk
                 c0 = tc::fmax3(c0, at(k), at(k + 1));
                 c1 = tc::fmax3(c1, at(k + 2), at(k + 3));
             }
-            const float y = fmaxf(c0, c1) * (cs * sc[g * (GK / 16)]);
+            const float y = fmaxf(c0, c1) * at_least(cs * sc[g * (GK / 16)]);
             mx = fmaxf(mx, y);
             mxo = fmaxf(mxo, y + sc[8 + g * (GK / 16)]);
         }
@@ -920,7 +927,7 @@ __device__ __forceinline__ void softmax_part(uint32_t (&r)[2][32], uint32_t (&pk
         sum = 0.f;
 #pragma unroll
         for (int g = 0; g < NG; ++g) {
-            const float ks = cs * sc[g * (GK / 16)], b = sc[8 + g * (GK / 16)] - mo_use, shift = b + m_use;
+            const float ks = at_least(cs * sc[g * (GK / 16)]), b = sc[8 + g * (GK / 16)] - mo_use, shift = b + m_use;
             if (__any_sync(0xffffffffu, shift < -60.f)) {
 #pragma unroll
                 for (int e = 0; e < GK; ++e) sum += ex2f(fmaf(at(g * GK + e), ks, -m_use));

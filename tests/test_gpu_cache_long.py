@@ -93,6 +93,15 @@ def test_a_query_that_is_not_finite_in_a_two_tile_unit(bd):
     cu.check_attention(o, lse, ref)
 
 
+@pytest.mark.parametrize("rows", [3, 90])
+def test_scores_too_small_for_fp32_hide_masked_keys_all_the_same(bd, rows):
+    # queries and key scales whose product underflows: every visible key weighs the same, and no masked key counts
+    c, off, q, qh = attn_case(191, [200], [rows], 16, 2, 1, 64, 1)
+    q *= 2.0 ** -120
+    c["ks"][:] = 2.0 ** -40
+    check(bd, c, off, q, q.double().cpu().numpy(), 1)
+
+
 # --------------------------------------------------------------------- writing
 @pytest.mark.parametrize("Hk,page,d,n", [(8, 64, 128, 11000), (3, 128, 64, 30000), (4, 16, 64, 45000)])
 def test_write_with_several_heads_per_cta(bd, Hk, page, d, n):
