@@ -5,8 +5,8 @@
 // sequence's new rows r and of the G query heads g that share the kv head,
 // which all read the same keys. Its tiles are its runs of 128 keys, up to the
 // last key that its last row sees (one, without keys, if it sees none). Its
-// cost is its tiles and kUnitTiles more for what it takes to begin and to end
-// it (query, results), twice that for a unit of two MMA tiles. All units'
+// cost is its tiles and a lead for what it takes to begin and to end it (query,
+// results), twice that for a unit of two MMA tiles. All units'
 // costs, laid end to end (sequence, head, run), are cut into equal shares, one
 // per CTA (the first W % C of them one longer). A share that begins or ends
 // between the tiles of a unit leaves a partial result; at most two per CTA,
@@ -22,10 +22,15 @@ namespace cattn {
 constexpr int kTileKeys = 128;
 constexpr int kUnitRows = 256;
 constexpr int kMaxCtas = 256;
-constexpr int kUnitTiles = 6;
+// What beginning and ending a unit costs, in tiles of 128 keys, besides a tile for every 32 rows of an MMA tile that is
+// alive (lead_of). Measured with 3, 4, 5, 6: 64 sequences of one row (4 flat rows per unit, 512 to 30912 keys) 230, 219,
+// 212, 210 us; 37 ragged ones (1 to 47 rows, up to 9001 keys) 37.6, 38.3, 38.6, 40.2 us. Without the tiles for the rows,
+// 64 sequences of 32 rows (128 flat rows per unit) took 251 instead of 235 us.
+constexpr int kLead = 5;
 // A share is at least this long where there is too little work for all CTAs: below it the partial results cost more
-// than the shorter shares save. (At least 2, so that each of the shares of a unit holds a tile of it.)
-constexpr int kMinShare = 6;
+// than the shorter shares save. One row over 600 keys takes 15.3, 16.0, 16.8, 18.3 us with 2, 3, 4, 6; three rows over
+// 56 to 277 keys 17.9, 17.6, 17.7, 16.3. (At least 2, so that each of the shares of a unit holds a tile of it.)
+constexpr int kMinShare = 3;
 
 // What CTA c leaves for the merge: where its share begins, and its errors.
 struct ShareRec {
@@ -61,18 +66,22 @@ struct Unit {
     int end;    // keys that the last row sees
     int tiles;  // at least 1
     int two;    // 1: two MMA tiles
-    __device__ __forceinline__ int cost() const { return (kUnitTiles + tiles) << two; }
+    int lead;   // what it costs besides, in tiles
+    __device__ __forceinline__ int cost() const { return (lead + tiles) << two; }
 };
+__device__ __forceinline__ int is_two(int rows) { return rows > kUnitRows / 2; }
+__device__ __forceinline__ int lead_of(int rows) { return kLead + ((rows + 31) >> (5 + is_two(rows))); }
 __device__ __forceinline__ Unit unit_of(const CacheAttnArgs& a, const SeqRows& r, int m0) {
     Unit u;
     u.last = imin(r.rows * a.G, m0 + kUnitRows);
     u.end = key_end(r.len, a.block, r.pos0 + (u.last - 1) / a.G);
     u.tiles = imax(1, (u.end + kTileKeys - 1) / kTileKeys);
-    u.two = u.last - m0 > kUnitRows / 2;
+    u.two = is_two(u.last - m0);
+    u.lead = lead_of(u.last - m0);
     return u;
 }
 // First tile that lies at or behind offset `off` of a unit's cost.
-__device__ __forceinline__ int tile_at(int off, int two) { return imax(0, (off >> two) - kUnitTiles); }
+__device__ __forceinline__ int tile_at(int off, int two, int lead) { return imax(0, (off >> two) - lead); }
 
 }  // namespace cattn
 

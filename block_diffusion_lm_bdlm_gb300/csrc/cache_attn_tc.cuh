@@ -141,7 +141,7 @@ __device__ __forceinline__ bool next_run(const CacheAttnArgs& a, Place* p) {
     while (left > 0 && !found) {
         const Unit u = p->u;
         const int off = p->off, c = u.cost(), n = left < c - off ? (int)left : c - off;
-        const int kt0 = tile_at(off, u.two), kt1 = tile_at(off + n, u.two);
+        const int kt0 = tile_at(off, u.two, u.lead), kt1 = tile_at(off + n, u.two, u.lead);
         int s = p->s, h = p->h, m0 = p->m0;
         SeqRows r = p->r;
         found = kt1 > kt0;
