@@ -34,11 +34,12 @@ class BlockDecoder:
 
     def begin(self, rows: torch.Tensor, *, check: bool = False) -> torch.Tensor:
         """Make room for `rows` new rows of every sequence behind what it
-        holds; returns their offsets (int32 [n_seqs + 1]). check=True raises
-        if the cache has no room."""
+        holds; returns their offsets (int32 [n_seqs + 1]). If the cache has no
+        room, no sequence gets any row: check=True raises, and without it the
+        offsets are all 0, so that attend does nothing."""
         self._kept.copy_(self.cache.lens)
-        torch.cumsum(rows, 0, dtype=torch.int32, out=self.cu_rows[1:])
         bdlm_cache_reserve(self.cache, self._kept + rows, check=check)
+        torch.cumsum(self.cache.lens - self._kept, 0, dtype=torch.int32, out=self.cu_rows[1:])
         return self.cu_rows
 
     def attend(self, layer: int, q, k, v, *, out=None, lse=None):

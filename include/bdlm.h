@@ -404,8 +404,10 @@ BDLM_API size_t bdlm_cache_write_workspace_bytes(void);
  * and a value falls below the smallest normal 2^-6 s). Values that are not
  * finite are stored as NaN. Rows of a page from lens[s] on are left as they
  * were. A page that is written must belong to one sequence only.
- * A sequence with malformed offsets, length or pages is skipped
- * (BDLM_ERR_DEVICE_CHECK); the others are written.
+ * A sequence with fewer positions than new rows, or more than its table
+ * holds, and a page outside the pool are skipped (BDLM_ERR_DEVICE_CHECK); the
+ * others are written. (Offsets that do not ascend give the same error, and
+ * may leave other sequences unwritten as well.)
  */
 BDLM_API int bdlm_cache_write(const bdlm_cache* cache, int32_t layer, const void* k_new, const void* v_new,
                   int64_t total_rows, const int32_t* cu_rows, void* workspace, size_t workspace_bytes,

@@ -197,3 +197,60 @@ def test_two_graphs_replayed_at_once(bd):
     torch.cuda.synchronize()
     for o, lse in outs:
         cu.check_attention(o, lse, ref)
+
+
+def test_a_block_without_room_writes_nothing(bd):
+    from block_diffusion_lm_bdlm_gb300.decode import BlockDecoder
+
+    c = cu.make(193, lens=[30, 17], page=16, Hk=1, d=64, spare=1, max_pages=4)
+    cache = cu.to_device(bd, c)
+    dec = BlockDecoder(cache, 16)
+    q = torch.ones(32, 2, 64, dtype=torch.bfloat16, device="cuda")
+    out, lse = torch.full_like(q, 5.0), torch.full((2, 32), 5.0, device="cuda")
+    assert dec.begin(dev([16, 16], torch.int32)).tolist() == [0, 0, 0]  # two pages would be needed
+    dec.attend(0, q, q[:, :1].contiguous(), q[:, :1].contiguous(), out=out, lse=lse)
+    assert bool((out == 5).all()) and bool((lse == 5).all())
+    cu.check_same(cu.to_host(cache), c)
+    with pytest.raises(bd.BDLMError, match="NO_PAGES"):
+        dec.begin(dev([16, 16], torch.int32), check=True)
+    assert dec.begin(dev([16, 0], torch.int32), check=True).tolist() == [0, 16, 16]
+
+
+# ---------------------------------------------------------------- large caches
+def test_pages_far_beyond_4_gb(bd):
+    # 5 GB of keys and of values in two layers, with the used pages at the far end: byte offsets pass 2^32
+    page, Hk, d, H, B = 128, 8, 128, 16, 32
+    lens, rows = [700, 130, 64], [64, 32, 7]
+    c, off, q, qh = attn_case(197, lens, rows, page, H, Hk, d, B)
+    n, far = c["k"].shape[1], 19000
+    small = cu.to_device(bd, c)
+    big = [torch.empty((2, far + n + 4, Hk, page, d), dtype=torch.float8_e4m3fn, device="cuda") for _ in range(2)]
+    scales = [torch.ones((2, far + n + 4, Hk), device="cuda") for _ in range(2)]
+    for b, s, src, src_s in zip(big, scales, (small.k, small.v), (small.k_scale, small.v_scale)):
+        b[1, far:far + n].view(torch.uint8).copy_(src[0].view(torch.uint8))
+        s[1, far:far + n] = src_s[0]
+    table = torch.zeros((4, 8), dtype=torch.int32, device="cuda")
+    table[:3, :small.table.shape[1]] = small.table + far
+    cache = bd.PageCache(*big, *scales, table, torch.cat([small.lens, torch.zeros(1, dtype=torch.int32, device="cuda")]))
+    cu_rows = dev(list(off) + [off[-1]], torch.int32)
+    rng = np.random.default_rng(199)
+    (k, kh), (v, vh) = rows_of(rng, int(off[-1]), Hk, d), rows_of(rng, int(off[-1]), Hk, d)
+
+    def back():
+        host = {x: c[x].copy() for x in c}
+        for x, b, s in (("k", big[0], scales[0]), ("v", big[1], scales[1])):
+            host[x][0] = b[1, far:far + n].view(torch.uint8).cpu().numpy()
+            host[x + "s"][0] = s[1, far:far + n].double().cpu().numpy()
+        return host
+
+    bd.bdlm_cache_write(cache, k, v, cu_rows, layer=1, check=True)
+    co.write(c, 0, kh, vh, off)
+    cu.check_same(back(), c)
+    ref = co.attention(c, 0, qh, off, B, d ** -0.5)
+    cu.check_attention(*bd.bdlm_cache_attn_fwd(cache, q, cu_rows, B, layer=1), ref)
+    bd.bdlm_cache_fork(cache, dev([0], torch.int32), dev([3], torch.int32), check=True)  # its last page comes to page 0
+    o, lse = bd.bdlm_cache_attn_fwd(cache, q[:64].contiguous(), dev([0, 0, 0, 0, 64], torch.int32), B, layer=1)
+    cu.check_attention(o, lse, [x[:64] if i in (0, 2) else x[:, :64] for i, x in enumerate(ref)], "forked")
+    live = int(bd.bdlm_cache_compact(cache, check=True))
+    assert live == sum(co.pages_of(x, page) for x in lens) + 1 and int(cache.table[:3, 0].max()) < live
+    cu.check_attention(*bd.bdlm_cache_attn_fwd(cache, q, cu_rows, B, layer=1), ref, "compacted")
