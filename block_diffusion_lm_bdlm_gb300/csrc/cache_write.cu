@@ -96,6 +96,13 @@ __device__ __forceinline__ uint32_t cta_max(uint32_t x, uint32_t* buf) {
     return __reduce_max_sync(0xffffffffu, buf[threadIdx.x & (T / 32 - 1)]);
 }
 
+__device__ __forceinline__ void rotate(uint4 (&u)[kV]) {
+    const uint4 w = u[0];
+#pragma unroll
+    for (int e = 0; e + 1 < kV; ++e) u[e] = u[e + 1];
+    u[kV - 1] = w;
+}
+
 // T threads with kV chunks of eight values each: T = page * d / 32. A CTA
 // takes `per_cta` of the 2 Hk (head, K or V) of a page, one after the other.
 template <int T>
@@ -131,33 +138,37 @@ __global__ void __launch_bounds__(T, T == 32 ? 24 : 1024 / T) cache_write_kernel
     const int first = (int)(page_no << c.page_shift);  // position of the page's row 0
     const int kept = imax(0, r.pos0 - first);          // rows of the page that stay
     const int rows = imin(c.page, r.len - first);      // and that are there in the end
-    // chunk i of the thread is at row row0 + i * step, columns col .. col + 7
+    const bool whole = kept == 0 && rows == c.page;    // no row is missing (the same for the whole CTA)
+    // chunk i of the thread is at row row0 + i * step, columns col .. col + 7: 8 T i bytes behind its first one in the page
     const int row0 = tid >> row_shift, col = (tid & ((1 << row_shift) - 1)) * 8, step = T >> row_shift;
-    const long long src0 = ((long long)(r.row0 + first - r.pos0) * c.Hk) * D + col;
+    const int src_step = step * c.Hk * D;
+    const long long src0 = (long long)(r.row0 + first - r.pos0 + row0) * c.Hk * D + col;
+    const __nv_bfloat16 *k_src = a.k_new + src0, *v_src = a.v_new + src0;
 
     auto fetch = [&](int kind, uint4 (&u)[kV]) {
-        const __nv_bfloat16* src = (kind & 1 ? a.v_new : a.k_new) + src0 + (kind >> 1) * D;
+        const __nv_bfloat16* src = (kind & 1 ? v_src : k_src) + (kind >> 1) * D;
+        if (whole) {
 #pragma unroll
-        for (int i = 0; i < kV; ++i) {
-            const int row = row0 + i * step;
-            u[i] = make_uint4(0, 0, 0, 0);
-            if (row >= kept && row < rows) u[i] = __ldg(reinterpret_cast<const uint4*>(src + (long long)row * c.Hk * D));
+            for (int i = 0; i < kV; ++i) u[i] = __ldg(reinterpret_cast<const uint4*>(src + (long long)i * src_step));
+        } else {
+#pragma unroll
+            for (int i = 0; i < kV; ++i) {
+                const int row = row0 + i * step;
+                u[i] = make_uint4(0, 0, 0, 0);
+                if (row >= kept && row < rows) u[i] = __ldg(reinterpret_cast<const uint4*>(src + (long long)i * src_step));
+            }
         }
     };
     uint4 next[kV];
     fetch(kind0, next);
     if (id < 0 || id >= c.n_pages) return;
     __shared__ uint32_t s_max[2][T / 32];
-#pragma unroll 1
-    for (int k = 0; k < per_cta; ++k) {
-        const int kind = kind0 + k;
-        uint4 u[kV];
-#pragma unroll
-        for (int i = 0; i < kV; ++i) u[i] = next[i];
-        if (k + 1 < per_cta) fetch(kind + 1, next);
-        const long long unit = (long long)id * c.Hk + (kind >> 1);
-        uint8_t* dst = (kind & 1 ? c.v : c.k) + unit * c.page * D + col;
-        float* scale_at = (kind & 1 ? c.v_scale : c.k_scale) + unit;
+    const long long unit0 = (long long)id * c.Hk;
+    uint8_t *k_dst = c.k + unit0 * c.page * D + tid * 8, *v_dst = c.v + unit0 * c.page * D + tid * 8;
+    // one (head, K or V) from u
+    auto item = [&](int kind, uint32_t* s_buf, uint4 (&u)[kV]) {
+        uint8_t* dst = (kind & 1 ? v_dst : k_dst) + (kind >> 1) * c.page * D;
+        float* scale_at = (kind & 1 ? c.v_scale : c.k_scale) + unit0 + (kind >> 1);
         float was = 1.f;
         uint32_t top = 0;  // the largest |x| as bits, which order as the values do; above kInf: NaN
         if (kept == 0) {
@@ -170,45 +181,44 @@ __global__ void __launch_bounds__(T, T == 32 ? 24 : 1024 / T) cache_write_kernel
             top = umax(top << 16, top & 0xffff0000u);
         } else {
             was = *scale_at;
-#pragma unroll
+#pragma unroll 1
             for (int i = 0; i < kV; ++i) {
                 const int row = row0 + i * step;
                 if (row < kept) {
-                    const uint2 w = *reinterpret_cast<const uint2*>(dst + row * D);
-                    u[i] = make_uint4(w.x, w.y, 0, 0);
+                    const uint2 w = *reinterpret_cast<const uint2*>(dst + i * 8 * T);
+                    u[0] = make_uint4(w.x, w.y, 0, 0);
                 }
                 float x[8];
-                values8(u[i], row < kept, was, x);
+                values8(u[0], row < kept, was, x);
 #pragma unroll
                 for (int e = 0; e < 8; ++e) top = umax(top, __float_as_uint(x[e]) & 0x7fffffffu);
+                rotate(u);
             }
         }
-        top = cta_max<T>(top, s_max[k & 1]);  // also: every thread has read the old scale and the kept rows
+        top = cta_max<T>(top, s_buf);  // also: every thread has read the old scale and the kept rows
         const bool some = top >= kInf;
         if (some) {  // the largest of the finite ones
             top = 0;
+#pragma unroll 1
+            for (int i = 0; i < kV; ++i) {
+                float x[8];
+                values8(u[0], row0 + i * step < kept, was, x);
+#pragma unroll
+                for (int e = 0; e < 8; ++e) top = umax(top, is_finite(x[e]) ? __float_as_uint(x[e]) & 0x7fffffffu : 0u);
+                rotate(u);
+            }
+            __syncthreads();  // s_buf has been read
+            top = cta_max<T>(top, s_buf);
+        }
+        const float scale = pow2_scale(__uint_as_float(top));
+        const float inv = __uint_as_float(0x7f000000u - __float_as_uint(scale));  // 1 / scale: 2^-126 <= scale <= 2^120
+        if (tid == 0) *scale_at = scale;
+        if (whole && !some) {
 #pragma unroll
             for (int i = 0; i < kV; ++i) {
                 float x[8];
-                values8(u[i], row0 + i * step < kept, was, x);
-#pragma unroll
-                for (int e = 0; e < 8; ++e) top = umax(top, is_finite(x[e]) ? __float_as_uint(x[e]) & 0x7fffffffu : 0u);
-            }
-            __syncthreads();  // s_max has been read
-            top = cta_max<T>(top, s_max[k & 1]);
-        }
-        const float scale = pow2_scale(__uint_as_float(top));
-        const float inv = 1.f / scale;  // exact: 2^-126 <= scale <= 2^120
-        if (tid == 0) *scale_at = scale;
-        if (kept == 0 && !some) {
-#pragma unroll
-            for (int i = 0; i < kV; ++i) {
-                const int row = row0 + i * step;
-                if (row < rows) {
-                    float x[8];
-                    values8(u[i], false, 1.f, x);
-                    *reinterpret_cast<uint2*>(dst + row * D) = encode8(x, inv, false);
-                }
+                values8(u[i], false, 1.f, x);
+                *reinterpret_cast<uint2*>(dst + i * 8 * T) = encode8(x, inv, false);
             }
         } else {
 #pragma unroll 1
@@ -217,12 +227,21 @@ __global__ void __launch_bounds__(T, T == 32 ? 24 : 1024 / T) cache_write_kernel
                 if (row < rows && (row >= kept || scale != was)) {
                     float x[8];
                     values8(u[0], row < kept, was, x);
-                    *reinterpret_cast<uint2*>(dst + row * D) = encode8(x, inv, true);
+                    *reinterpret_cast<uint2*>(dst + i * 8 * T) = encode8(x, inv, true);
                 }
-#pragma unroll
-                for (int e = 0; e + 1 < kV; ++e) u[e] = u[e + 1];
+                rotate(u);
             }
         }
+    };
+    // two at a time, so that the rows of the next one come in without moving
+#pragma unroll 1
+    for (int k = 0; k < per_cta; k += 2) {
+        uint4 u[kV];
+        if (k + 1 < per_cta) fetch(kind0 + k + 1, u);
+        item(kind0 + k, s_max[0], next);
+        if (k + 1 == per_cta) break;
+        if (k + 2 < per_cta) fetch(kind0 + k + 2, next);
+        item(kind0 + k + 1, s_max[1], u);
     }
 }
 
