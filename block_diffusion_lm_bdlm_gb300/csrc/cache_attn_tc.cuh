@@ -16,10 +16,25 @@
 // l = sum 2^(s_j - m) is kept in fp32 with an offset m of its own: the sum of
 // each page's p' times 2^(mo - m - log2 vs).
 //
-// Bound. A tile of 128 keys is 32 KB from memory at d = 128: about 1490 clocks
-// at the measured copy rate shared by 152 SMs. Its MMAs take about 1040 clocks
-// for up to 128 flat rows, so these calls are bound by memory, and calls with
-// 256 and more flat rows by the tensor pipe.
+// Bound. A tile of 128 keys is 32 KB from memory at d = 128: about 1430 clocks
+// at the measured copy rate shared by 152 SMs. Its MMAs take 1024 clocks for up
+// to 128 flat rows, so these calls are bound by memory, and calls with 256 and
+// more flat rows by the tensor pipe.
+//
+// Measured (32 query heads, 8 kv heads, d = 128, whole calls with the merge):
+// 64 single rows over 512 to 30912 keys 213 us (4.4 TB/s; a copy of the bytes
+// 139), 64 blocks of 32 rows over the same 235 us (1025 TFLOP/s), 64 rows over
+// 131072 keys 140 us (980 TFLOP/s), 3 prompts of 5000 to 9000 rows 950 us (900
+// TFLOP/s). A tile of a one-tile unit takes 1500 clocks, of a two-tile unit
+// 2900 for both: softmax 1450, PV and the next S 1024, four hand-overs 400, one
+// after the other, since TMEM has no room for a third S nor shared memory for
+// p'. Halving S (64 keys at a time) would break that chain, but 8-bit MMAs with
+// N = 64 take 384 clocks instead of 256 for the same work (they read more from
+// shared memory than they multiply). Tiles whose offsets move cost 1600 clocks
+// more; a unit's query split 2500 to 8000, its results 3500 to 8000, most of it
+// the fetching of code that runs once. Tried: sixteen softmax warps, two to a
+// row, with shared offsets: 269 and 354 us for the first two calls above when
+// eight warps of 64 keys took 216 and 251.
 //
 // Roles (512 threads, one CTA per SM, each role walks the CTA's share alone):
 //   warps 0-3, 4-7  softmax groups 0 and 1; one TMEM lane = one flat row. They

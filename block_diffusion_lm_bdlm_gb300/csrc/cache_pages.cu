@@ -7,10 +7,15 @@
 // a prefix sum, check that the call can be done, and only then write table and
 // lens. Its phases meet at the cluster's hardware barrier, which also orders
 // their global reads and writes, so one launch does what would otherwise take
-// one for each phase; it moves a few bytes per page and is bound by latency.
+// one for each phase; it moves a few bytes per page and is bound by latency
+// (about 13 us for 256 sequences over 16k positions each).
 // A copy kernel then moves the pages of fork and compact, one warp for each
 // (copy, layer, K or V, head): a run of contiguous bytes, eight 16-byte loads
-// per lane in flight.
+// per lane in flight. It is launched with programmatic dependence, so that its
+// CTAs are there when the plan ends. Bound by memory: 128 forks of a part of a
+// page in 32 layers move 1.2 GB in 165 us (7.2 TB/s, more than a plain copy's
+// 6.8, since some of it stays in L2), a compaction of 8 layers 1.05 GB in 182
+// us with its plan.
 #include <cooperative_groups.h>
 
 #include "cache.cuh"
@@ -20,8 +25,12 @@ namespace {
 
 namespace cg = cooperative_groups;
 
+// CTAs of the plan: 8, 4, 2 take 14.6, 16.0, 20.1 us for reserving a block for 256 sequences, 15.0, 13.1, 13.5 for one
+// fork into four, 183.5, 181.8, 182.5 for a compaction that moves 0.5 GB (with the calls' copies): more CTAs are worth
+// it where there are many pages.
 constexpr int kCluster = 8;
 constexpr int kPlanThreads = 1024;
+static_assert(kPlanThreads == 32 * 32, "block_scan scans the sums of 32 warps");
 constexpr int kAll = kCluster * kPlanThreads;
 constexpr int kCopyThreads = 256;
 

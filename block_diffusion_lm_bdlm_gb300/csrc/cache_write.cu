@@ -1,12 +1,25 @@
 // cache_write.cu - quantises new key and value rows into the pages of the cache.
 //
-// One CTA takes one (touched page, kv head) of K or of V: at most page x d
-// values, held in registers from their one read to their one write. Rows of
-// the page before the sequence's first new row are read back (code * scale),
-// the amax over both gives the new power-of-two scale (see pow2_scale), and
-// every value is stored as x / s, rounded once to nearest even: the division
-// by a power of two is exact, so the codes are those of the definition bit by
-// bit. Kept rows are stored again only where the scale has changed.
+// A CTA takes one touched page, and of its 2 Hk blocks of page x d values (a kv
+// head of K or of V) one or more. A block is held in registers from its one
+// read to its one write: rows of the page before the sequence's first new row
+// are read back (code * scale), the amax over both gives the new power-of-two
+// scale (see pow2_scale), and every value is stored as x / s, rounded once to
+// nearest even: the division by a power of two is exact, so the codes are those
+// of the definition bit by bit. Kept rows are stored again only where the scale
+// has changed.
+//
+// Bound: memory (2 bytes read and 1 written per value), at small calls the
+// latency of offsets, lengths and table in turn. A row of one head is only
+// 2 d bytes, so CTAs that run together take the heads of one page, whose rows
+// are consecutive bytes (with the heads far apart in the grid 8 prompts of 8192
+// rows, 8 heads, d = 128, took 232 us; side by side 101). While a block is
+// quantised the next one's rows are on their way, and a page that is new as a
+// whole is taken without bounds; its maxima are taken on packed bf16 bits, and
+// values that are not finite are looked for only where the maximum says that
+// there are some (instruction issue was the limit before: 97 us). Now 63 us for
+// 64-row pages, 69 for 128, 71 for 16 (6.4, 5.8, 5.6 TB/s of the 403 MB that
+// must move; a copy of them would take 59), and 4.1 us for 16 blocks of 32 rows.
 //
 // The pages that a call touches are numbered without knowing the lengths: the
 // slots of sequence s start at cu_rows[s] / page + 2 s, which leaves room for
@@ -17,6 +30,9 @@ namespace bdlm {
 namespace {
 
 constexpr int kV = 4;
+// A CTA takes more blocks of its page while as many threads as this per SM remain: half and twice as many take 66.3 and
+// 63.9 instead of 64.9 us for 8 prompts of 8192 rows, but 10.3 and 11.0 instead of 9.7 us for 64 blocks of 32 rows that
+// begin inside a page, and 12.6 and 12.7 instead of 11.4 us for 256 blocks of 32 rows.
 constexpr int kThreadsPerSm = 2048;
 constexpr uint32_t kInf = 0x7f800000u;
 
@@ -103,10 +119,11 @@ __device__ __forceinline__ void rotate(uint4 (&u)[kV]) {
     u[kV - 1] = w;
 }
 
-// T threads with kV chunks of eight values each: T = page * d / 32. A CTA
-// takes `per_cta` of the 2 Hk (head, K or V) of a page, one after the other.
+// T threads with kV chunks of eight values each: T = page * d / 32. A CTA takes `per_cta` of the 2 Hk (head, K or V) of a
+// page, one after the other. (Registers for 1024, 1280, 1536 threads per SM: 64.9, 62.6, 66.8 us for 8 prompts of 8192
+// rows.)
 template <int T>
-__global__ void __launch_bounds__(T, T == 32 ? 24 : 1024 / T) cache_write_kernel(const CacheWriteArgs a, int per_cta) {
+__global__ void __launch_bounds__(T, 1280 / T) cache_write_kernel(const CacheWriteArgs a, int per_cta) {
     const CacheView& c = a.c;
     if (blockIdx.x == gridDim.x - 1) {
         check_rows<T>(a);
