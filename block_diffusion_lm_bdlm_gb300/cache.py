@@ -16,6 +16,7 @@ bdlm_read_error(workspace), or pass check=True, which synchronises and raises.
 from __future__ import annotations
 
 import ctypes
+import threading
 from contextlib import nullcontext
 
 import torch
@@ -33,13 +34,17 @@ class PageCache:
       table            int32 [n_seqs, max_pages]
       lens             int32 [n_seqs]
 
-    All contiguous and on one device. The object holds no state of its own:
-    table and lens are the truth, and the calls and the program write them in
-    stream order. To end sequences, set their lens to 0.
+    All contiguous and on one device. The object holds no state of the cache
+    itself: table and lens are the truth, and the calls and the program write
+    them in stream order. To end sequences, set their lens to 0.
+
+    It keeps one workspace for calls that bring none, come on the stream that
+    the first such call came on, are not captured into a graph and do not ask
+    for their error word; other calls get one of their own.
     """
 
     __slots__ = ("k", "v", "k_scale", "v_scale", "table", "lens", "n_layers", "n_pages", "page", "kv_heads",
-                 "head_dim", "n_seqs", "max_pages", "device", "index", "pages_bytes", "c")
+                 "head_dim", "n_seqs", "max_pages", "device", "index", "pages_bytes", "c", "ref", "home", "scratch", "lock")
 
     def __init__(self, k, v, k_scale, v_scale, table, lens):
         for nm, t, dt, dims in (("k", k, torch.float8_e4m3fn, 5), ("v", v, torch.float8_e4m3fn, 5),
@@ -66,6 +71,8 @@ class PageCache:
         self.c = _CCache(k.data_ptr(), v.data_ptr(), k_scale.data_ptr(), v_scale.data_ptr(), table.data_ptr(),
                          lens.data_ptr(), self.n_layers, self.n_pages, self.page, self.kv_heads, self.head_dim,
                          self.n_seqs, self.max_pages, 0)
+        self.ref = ctypes.byref(self.c)
+        self.home, self.scratch, self.lock = None, None, threading.Lock()
 
     @staticmethod
     def empty(n_layers: int, n_pages: int, page: int, kv_heads: int, head_dim: int, n_seqs: int, max_pages: int,
@@ -108,11 +115,20 @@ def _on(cache, stream):
     return stream.cuda_stream, torch.cuda.stream(stream)
 
 
-def _workspace(cache, workspace, need):
+def _workspace(cache, workspace, need, handle, private):
+    """The caller's workspace, or one of at least `need` bytes. Calls on one
+    stream follow one another, so they may share the cache's; the lock that the
+    callers hold keeps the launches of one call together. Whatever may run at
+    another time (another stream, a graph that is replayed, an error word that
+    is read later: `private`) gets memory of its own."""
     if workspace is None:
-        return torch.empty(need, dtype=torch.uint8, device=cache.device)
+        if private or (cache.home is not None and handle != cache.home) or torch.cuda.is_current_stream_capturing():
+            return torch.empty(need, dtype=torch.uint8, device=cache.device)
+        if cache.scratch is None or cache.scratch.numel() < need:
+            cache.home, cache.scratch = handle, torch.empty(need, dtype=torch.uint8, device=cache.device)
+        return cache.scratch
     if not workspace.is_cuda or workspace.dtype != torch.uint8 or not workspace.is_contiguous() \
-            or workspace.device != cache.device:
+            or workspace.get_device() != cache.index:
         raise ValueError("workspace must be a contiguous uint8 CUDA tensor on the cache's device")
     return workspace
 
@@ -154,9 +170,11 @@ def bdlm_cache_write(cache: PageCache, k_new, v_new, cu_rows, *, layer: int = 0,
     _layer(cache, layer)
     handle, here = _on(cache, stream)
     with here:
-        ws = _workspace(cache, workspace, 256)
-        _check(lib.bdlm_cache_write(cache.c, layer, k_new.data_ptr(), v_new.data_ptr(), shape[0], cu,
-                                    ws.data_ptr(), ws.numel(), handle), "bdlm_cache_write")
+        with cache.lock:
+            ws = _workspace(cache, workspace, 256, handle, check or stream is not None)
+            st = lib.bdlm_cache_write(cache.ref, layer, k_new.data_ptr(), v_new.data_ptr(), shape[0], cu, ws.data_ptr(),
+                                      ws.numel(), handle)
+        _check(st, "bdlm_cache_write")
         if check:
             _read(lib, ws, handle, "bdlm_cache_write")
 
@@ -190,10 +208,11 @@ def bdlm_cache_attn_fwd(cache: PageCache, q, cu_rows, block: int, *, layer: int 
         elif lse.shape != (H, T) or lse.dtype != torch.float32 or lse.device != cache.device \
                 or not lse.is_contiguous():
             raise ValueError("lse must be a contiguous fp32 CUDA tensor [H, T]")
-        ws = _workspace(cache, workspace, max(need, 256))
-        st = lib.bdlm_cache_attn_fwd(cache.c, layer, q.data_ptr(), out.data_ptr(), lse.data_ptr(), T, H, block, cu, pos,
-                                     softmax_scale, BDLM_F32 if out.dtype == torch.float32 else BDLM_BF16,
-                                     ws.data_ptr(), ws.numel(), handle)
+        with cache.lock:
+            ws = _workspace(cache, workspace, max(need, 256), handle, check or stream is not None)
+            st = lib.bdlm_cache_attn_fwd(cache.ref, layer, q.data_ptr(), out.data_ptr(), lse.data_ptr(), T, H, block, cu,
+                                         pos, softmax_scale, BDLM_F32 if out.dtype == torch.float32 else BDLM_BF16,
+                                         ws.data_ptr(), ws.numel(), handle)
         _check(st, "bdlm_cache_attn_fwd")
         if check:
             _read(lib, ws, handle, "bdlm_cache_attn_fwd")
@@ -204,11 +223,13 @@ def _pages_call(cache, name, args, workspace, stream, check, make=None):
     lib = load_library()
     handle, here = _on(cache, stream)
     with here:
-        ws = _workspace(cache, workspace, cache.pages_bytes)
         made = None if make is None else make()
         if made is not None:
             args = (made.data_ptr(),)
-        _check(getattr(lib, name)(cache.c, *args, ws.data_ptr(), ws.numel(), handle), name)
+        with cache.lock:
+            ws = _workspace(cache, workspace, cache.pages_bytes, handle, check or stream is not None)
+            st = getattr(lib, name)(cache.ref, *args, ws.data_ptr(), ws.numel(), handle)
+        _check(st, name)
         if check:
             _read(lib, ws, handle, name)
     return made

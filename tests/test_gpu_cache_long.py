@@ -173,6 +173,42 @@ def test_calls_at_once_on_two_streams(bd):
             cu.check_attention(*pair[la], refs[la], f"turn {i}, layer {la}")
 
 
+def test_calls_without_a_workspace(bd):
+    # small, large, from another current stream, from two threads, small again: the outputs are those of calls with
+    # workspaces of their own
+    from threading import Thread
+
+    c, off, q, _ = attn_case(211, [3000, 500, 90], [40, 40, 40], 32, 8, 2, 128, 8)
+    cache = cu.to_device(bd, c)
+    sizes = {}
+    for n in (1, 40):
+        cu_rows = dev([0, n, 2 * n, 3 * n], torch.int32)
+        rows = q[:3 * n].contiguous()
+        ws = torch.empty(bd.bdlm_cache_attn_fwd_workspace_bytes(3 * n, 8, 2, 128, 3), dtype=torch.uint8, device="cuda")
+        sizes[n] = rows, cu_rows, bd.bdlm_cache_attn_fwd(cache, rows, cu_rows, 8, workspace=ws)
+    torch.cuda.synchronize()
+    got = []
+
+    def run(n):
+        rows, cu_rows, want = sizes[n]
+        got.append((bd.bdlm_cache_attn_fwd(cache, rows, cu_rows, 8), want))
+
+    side = torch.cuda.Stream()
+    for _ in range(3):
+        run(1), run(40)
+        with torch.cuda.stream(side):
+            run(40), run(1)
+    threads = [Thread(target=lambda n=n: [run(n) for _ in range(20)]) for n in (1, 40, 40)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    torch.cuda.synchronize()
+    assert len(got) == 72
+    for (o, lse), want in got:
+        assert torch.equal(o, want[0]) and torch.equal(lse, want[1])
+
+
 def test_two_graphs_replayed_at_once(bd):
     c, off, q, qh = attn_case(181, [700, 2000], [8, 8], 64, 8, 2, 64, 8)
     cache = cu.to_device(bd, c)
