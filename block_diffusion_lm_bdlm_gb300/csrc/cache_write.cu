@@ -12,14 +12,16 @@
 // Bound: memory (2 bytes read and 1 written per value), at small calls the
 // latency of offsets, lengths and table in turn. A row of one head is only
 // 2 d bytes, so CTAs that run together take the heads of one page, whose rows
-// are consecutive bytes (with the heads far apart in the grid 8 prompts of 8192
-// rows, 8 heads, d = 128, took 232 us; side by side 101). While a block is
+// are consecutive bytes (8 prompts of 69500 rows in all, 8 heads, d = 128, page
+// 128: 232 us with a page's heads far apart in the grid, 101 side by side, 74
+// with all that follows). While a block is
 // quantised the next one's rows are on their way, and a page that is new as a
 // whole is taken without bounds; its maxima are taken on packed bf16 bits, and
 // values that are not finite are looked for only where the maximum says that
-// there are some (instruction issue was the limit before: 97 us). Now 63 us for
-// 64-row pages, 69 for 128, 71 for 16 (6.4, 5.8, 5.6 TB/s of the 403 MB that
-// must move; a copy of them would take 59), and 4.1 us for 16 blocks of 32 rows.
+// there are some (instruction issue was the limit before). 8 prompts of 8192
+// rows take 63 us with 64-row pages (97 before those two), 69 with 128, 71 with
+// 16: 6.4, 5.8, 5.6 TB/s of the 403 MB that must move (a copy of them: 59 us).
+// 16 blocks of 32 rows take 4.1 us.
 //
 // The pages that a call touches are numbered without knowing the lengths: the
 // slots of sequence s start at cu_rows[s] / page + 2 s, which leaves room for
