@@ -101,6 +101,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads,
     const int tid = threadIdx.x, lane = tid & 31, rank = (int)cluster.block_rank();
     const int gtid = rank * kPlanThreads + tid, gwarp = gtid >> 5;
     const int shift = c.page_shift, cap = c.max_pages;
+    const int split = imax(1, kAll / 32 / c.n_seqs);  // warps that share the entries of a sequence
     const Scratch s = carve(a.scratch, c.n_pages, c.n_seqs);
 
     // ---- clear
@@ -114,7 +115,8 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads,
     cluster.sync();
 
     // ---- check the lengths and entries, count the pages' users
-    for (int q = gwarp; q < c.n_seqs; q += kAll / 32) {
+    for (int u = gwarp; u < c.n_seqs * split; u += kAll / 32) {
+        const int q = u / split, first = (u - q * split) * 32 + lane;
         int len = __ldcg(c.lens + q);
         bool bad = len < 0 || pages_of(len, shift) > cap;
         if (a.op == PAGES_RESERVE) {
@@ -124,7 +126,8 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads,
         }
         if (!bad) {
             const int n = pages_of(len, shift);
-            for (int i = lane; i < n; i += 32) {
+#pragma unroll 4
+            for (int i = first; i < n; i += 32 * split) {
                 const int id = __ldcg(c.table + (long long)q * c.max_pages + i);
                 if (id < 0 || id >= c.n_pages) bad = true;
                 else atomicAdd(s.count + id, 1);
@@ -239,11 +242,18 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads,
             const int i = i0 + tid;
             const int n = i < hi ? need_of(i) : 0;
             const int at = base + block_scan(n, &t, buf);
-            if (i < hi) {
-                int* row = c.table + (long long)i * c.max_pages + pages_of(__ldcg(c.lens + i), shift);
+            int* row = i < hi ? c.table + (long long)i * c.max_pages + pages_of(__ldcg(c.lens + i), shift) : nullptr;
+            constexpr int kFew = 4;
+            if (n <= kFew)
                 for (int k = 0; k < n; ++k) row[k] = __ldcg(s.rank + at + k);
-                c.lens[i] = __ldg(a.new_lens + i);
+            for (unsigned todo = __ballot_sync(0xffffffffu, n > kFew); todo; todo &= todo - 1) {  // the warp together
+                const int src = __ffs(todo) - 1, m = __shfl_sync(0xffffffffu, n, src);
+                const int* from = s.rank + __shfl_sync(0xffffffffu, at, src);
+                int* to = reinterpret_cast<int*>(__shfl_sync(0xffffffffu, reinterpret_cast<long long>(row), src));
+#pragma unroll 4
+                for (int k = lane; k < m; k += 32) to[k] = __ldcg(from + k);
             }
+            if (i < hi) c.lens[i] = __ldg(a.new_lens + i);
             base += t;
         }
         return;
@@ -264,13 +274,16 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads,
             }
             base += t;
         }
-        for (int i = gwarp; i < a.n; i += kAll / 32) {
+        const int share = imax(1, kAll / 32 / imax(1, a.n));
+        for (int u = gwarp; u < a.n * share; u += kAll / 32) {
+            const int i = u / share, part = u - i * share;
             const int p = __ldg(a.parents + i), k = __ldg(a.children + i);
             const int len = a.fork_lens ? __ldg(a.fork_lens + i) : __ldcg(c.lens + p);
             const int* from = c.table + (long long)p * c.max_pages;
             int* to = c.table + (long long)k * c.max_pages;
-            for (int e = lane; e < len >> shift; e += 32) to[e] = __ldcg(from + e);
-            if (lane == 0) c.lens[k] = len;
+#pragma unroll 4
+            for (int e = part * 32 + lane; e < len >> shift; e += 32 * share) to[e] = __ldcg(from + e);
+            if (part == 0 && lane == 0) c.lens[k] = len;
         }
         if (gtid == 0) *s.n_copies = all_need;
         return;
@@ -286,10 +299,11 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads,
         }
     if (gtid == 0 && a.n_live) *a.n_live = live;
     cluster.sync();
-    for (int q = gwarp; q < c.n_seqs; q += kAll / 32) {
-        const int n = pages_of(__ldcg(c.lens + q), shift);
+    for (int u = gwarp; u < c.n_seqs * split; u += kAll / 32) {
+        const int q = u / split, n = pages_of(__ldcg(c.lens + q), shift);
         int* row = c.table + (long long)q * c.max_pages;
-        for (int i = lane; i < n; i += 32) {
+#pragma unroll 4
+        for (int i = (u - q * split) * 32 + lane; i < n; i += 32 * split) {
             const int id = __ldcg(row + i);
             if (id >= live) row[i] = __ldcg(s.rank + id);
         }

@@ -42,21 +42,37 @@ __device__ __forceinline__ long long slot_base(const int* cu, int s, int shift) 
     return ((long long)__ldg(cu + s) >> shift) + 2LL * s;
 }
 
-// Block-wide check of every sequence; one thread writes the header.
+// Block-wide check of every sequence, a thread for each, and a warp for each that has many pages; one thread writes the
+// header.
 template <int T>
 __device__ void check_rows(const CacheWriteArgs& a) {
     __shared__ int s_bad;
     if (threadIdx.x == 0) s_bad = 0x7fffffff;
     __syncthreads();
-    for (int s = threadIdx.x; s < a.c.n_seqs; s += T) {
-        const SeqRows r = seq_rows(a.c, a.cu_rows, nullptr, a.total_rows, s);
-        bool bad = !r.ok;
-        if (r.ok && r.rows > 0)
-            for (int p = r.pos0 >> a.c.page_shift; p <= (r.len - 1) >> a.c.page_shift; ++p) {
-                const int id = __ldg(a.c.table + (long long)s * a.c.max_pages + p);
-                bad = bad || id < 0 || id >= a.c.n_pages;
-            }
+    constexpr int kFew = 4;
+    const int lane = threadIdx.x & 31;
+    for (int s0 = 0; s0 < a.c.n_seqs; s0 += T) {
+        const int s = s0 + threadIdx.x;
+        int first = 0, n = 0;  // the touched pages
+        if (s < a.c.n_seqs) {
+            const SeqRows r = seq_rows(a.c, a.cu_rows, nullptr, a.total_rows, s);
+            if (!r.ok) atomicMin(&s_bad, s);
+            first = r.pos0 >> a.c.page_shift;
+            if (r.ok && r.rows > 0) n = ((r.len - 1) >> a.c.page_shift) - first + 1;
+        }
+        const int* ids = a.c.table + (long long)s * a.c.max_pages + first;
+        bool bad = false;
+        if (n <= kFew)
+            for (int p = 0; p < n; ++p) bad = bad || (unsigned)__ldg(ids + p) >= (unsigned)a.c.n_pages;
         if (bad) atomicMin(&s_bad, s);
+        for (unsigned todo = __ballot_sync(0xffffffffu, n > kFew); todo; todo &= todo - 1) {
+            const int src = __ffs(todo) - 1, m = __shfl_sync(0xffffffffu, n, src);
+            const int* row = reinterpret_cast<const int*>(__shfl_sync(0xffffffffu, reinterpret_cast<long long>(ids), src));
+            bad = false;
+#pragma unroll 8
+            for (int p = lane; p < m; p += 32) bad = bad || (unsigned)__ldg(row + p) >= (unsigned)a.c.n_pages;
+            if (bad) atomicMin(&s_bad, s0 + (int)(threadIdx.x & ~31u) + src);
+        }
     }
     __syncthreads();
     if (threadIdx.x == 0) {
@@ -125,16 +141,16 @@ __device__ __forceinline__ void rotate(uint4 (&u)[kV]) {
 // page, one after the other. (Registers for 1024, 1280, 1536 threads per SM: 64.9, 62.6, 66.8 us for 8 prompts of 8192
 // rows.)
 template <int T>
-__global__ void __launch_bounds__(T, 1280 / T) cache_write_kernel(const CacheWriteArgs a, int per_cta) {
+__global__ void __launch_bounds__(T, T == 32 ? 24 : 1280 / T) cache_write_kernel(const CacheWriteArgs a, int per_cta) {
     const CacheView& c = a.c;
-    if (blockIdx.x == gridDim.x - 1) {
+    if (blockIdx.x == 0) {
         check_rows<T>(a);
         return;
     }
     const int tid = threadIdx.x, lane = tid & 31;
     const unsigned parts = 2u * c.Hk / (unsigned)per_cta;
-    const long long slot = blockIdx.x / parts;
-    const int kind0 = (int)(blockIdx.x - (unsigned)slot * parts) * per_cta;
+    const long long slot = (blockIdx.x - 1) / parts;
+    const int kind0 = (int)(blockIdx.x - 1 - (unsigned)slot * parts) * per_cta;
     // the sequence of this slot: the last s with slot_base(s) <= slot, 32 ways at a time
     int lo = 0, hi = c.n_seqs;  // in [lo, hi)
     while (hi - lo > 1) {

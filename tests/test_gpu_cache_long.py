@@ -253,6 +253,33 @@ def test_a_block_without_room_writes_nothing(bd):
 
 
 # ---------------------------------------------------------------- large caches
+def test_page_calls_on_long_sequences(bd):
+    # thousands of pages per sequence: entries are shared out over warps; then shrunk, forked, compacted, written
+    c = cu.make(223, lens=[40, 3, 0], page=16, Hk=1, d=64, spare=9000, max_pages=5000, extra_seqs=2)
+    cache = cu.to_device(bd, c)
+    for lens in ([70000, 33, 0, 0, 0], [70001, 30000, 77, 0, 0], [50000, 30000, 5, 0, 0]):
+        bd.bdlm_cache_reserve(cache, dev(lens, torch.int32), check=True)
+        assert co.reserve(c, np.array(lens)) == ""
+        cu.check_same(cu.to_host(cache), c, str(lens))
+    bd.bdlm_cache_fork(cache, dev([0, 1], torch.int32), dev([3, 4], torch.int32), dev([49999, 30000], torch.int32), check=True)
+    assert co.fork(c, [0, 1], [3, 4], [49999, 30000]) == ""
+    cu.check_same(cu.to_host(cache), c, "fork")
+    cache.lens[0], c["lens"][0] = 0, 0
+    assert int(bd.bdlm_cache_compact(cache, check=True)) == co.compact(c)
+    cu.check_same(cu.to_host(cache), c, "compact")
+    bad = cu.to_device(bd, {**c, "table": c["table"].copy()})
+    ws = torch.empty(bd.bdlm_cache_pages_workspace_bytes(c["k"].shape[1], 5), dtype=torch.uint8, device="cuda")
+    k = torch.ones(40000, 1, 64, dtype=torch.bfloat16, device="cuda")
+    rows = dev([0, 0, 20, 20, 40000, 40000], torch.int32)
+    bd.bdlm_cache_write(bad, k, k, rows, workspace=ws)
+    assert bd.bdlm_read_error(ws) == 0
+    bad.table[3, 1000] = -1  # one page in the middle of the 39980 rows
+    bd.bdlm_cache_write(bad, k, k, rows, workspace=ws)
+    assert bd.bdlm_read_error(ws) == 6
+    bd.bdlm_cache_compact(bad, workspace=ws)
+    assert bd.bdlm_read_error(ws) == 6
+
+
 def test_pages_far_beyond_4_gb(bd):
     # 5 GB of keys and of values in two layers, with the used pages at the far end: byte offsets pass 2^32
     page, Hk, d, H, B = 128, 8, 128, 16, 32
