@@ -139,9 +139,9 @@ __device__ __forceinline__ void rotate(uint4 (&u)[kV]) {
 
 // T threads with kV chunks of eight values each: T = page * d / 32. A CTA takes `per_cta` of the 2 Hk (head, K or V) of a
 // page, one after the other. (Registers for 1024, 1280, 1536 threads per SM: 64.9, 62.6, 66.8 us for 8 prompts of 8192
-// rows.)
+// rows and 64-row pages; 70, 87 us for 1024, 1280 and 16-row ones.)
 template <int T>
-__global__ void __launch_bounds__(T, T == 32 ? 24 : 1280 / T) cache_write_kernel(const CacheWriteArgs a, int per_cta) {
+__global__ void __launch_bounds__(T, (T >= 128 ? 1280 : 1024) / T) cache_write_kernel(const CacheWriteArgs a, int per_cta) {
     const CacheView& c = a.c;
     if (blockIdx.x == 0) {
         check_rows<T>(a);
