@@ -865,9 +865,10 @@ __device__ __forceinline__ float at_least(float x) {
 // too little. (A sum over 2^15 of 64 keys has a p' of 2^9, which moves mo; the largest is at most 2^4 then, which leaves
 // room for scores that grow, and n keys below 2^-14 of fp16's normal range lose at most n 2^-29 of the largest weight.)
 template <int D, int NG, typename Settle>
-__device__ __forceinline__ void softmax_part(uint32_t (&r)[2][32], uint32_t (&pk)[32], uint32_t tC, uint32_t tO, const float* sc,
+__device__ __forceinline__ void softmax_part(uint32_t (&r)[2][32], uint32_t tC, uint32_t tP, uint32_t tO, const float* sc,
                                              float cs, int visible, bool full, bool first, RowSums& s, Settle settle) {
     constexpr int GK = 64 / NG;
+    uint32_t pk[32];
     auto at = [&](int k) { return __uint_as_float(r[k >> 5][k & 31]); };
     auto mask = [&]() {
         if (!full) {
@@ -908,7 +909,9 @@ __device__ __forceinline__ void softmax_part(uint32_t (&r)[2][32], uint32_t (&pk
         }
         again = __any_sync(0xffffffffu, all > 32768.f || low < -60.f || (s.mo == -INFINITY && visible > 0));
     }
-    if (again) {
+    if (!again) {
+        tc::tmem_st32(tP, pk);
+    } else {
         tc::tmem_ld32(tC, r[0]);
         tc::tmem_ld32(tC + 32, r[1]);
         tc::tmem_ld_wait();
@@ -951,17 +954,20 @@ __device__ __forceinline__ void softmax_part(uint32_t (&r)[2][32], uint32_t (&pk
                 sum = fmaf(weigh(g, ks, b), ex2f(-shift), sum);
             }
         }
+        tc::tmem_st32(tP, pk);
         if (__any_sync(0xffffffffu, move)) {  // last: the wait for the products in flight comes late
             settle(alpha);
             if (!first)
 #pragma unroll
-                for (int q = 0; q < D / 32; ++q) {
-                    uint32_t o[32];
-                    tc::tmem_ld32(tO + 32 * q, o);
+                for (int q = 0; q < D / 64; ++q) {
+                    uint32_t o[2][32];
+                    tc::tmem_ld32(tO + 64 * q, o[0]);
+                    tc::tmem_ld32(tO + 64 * q + 32, o[1]);
                     tc::tmem_ld_wait();
 #pragma unroll
-                    for (int e = 0; e < 32; ++e) o[e] = __float_as_uint(__uint_as_float(o[e]) * alpha);
-                    tc::tmem_st32(tO + 32 * q, o);
+                    for (int e = 0; e < 64; ++e) o[e >> 5][e & 31] = __float_as_uint(__uint_as_float(o[e >> 5][e & 31]) * alpha);
+                    tc::tmem_st32(tO + 64 * q, o[0]);
+                    tc::tmem_st32(tO + 64 * q + 32, o[1]);
                 }
         }
     }
@@ -1115,19 +1121,18 @@ __device__ __forceinline__ void softmax(const Ctx<D>& x, const CacheAttnArgs& a,
                     wait(B_S1, stage, ph);
                 }
                 if (warp_live) {
-                    uint32_t r[2][32], pk[32];
+                    uint32_t r[2][32];
                     const uint32_t tC = tS + 128 * i;
                     const float* sc = scales + 16 * slot;
                     tc::tmem_ld32(tC, r[0]);
                     tc::tmem_ld32(tC + 32, r[1]);
                     tc::tmem_ld_wait();
                     // S of a tile is issued behind the PV of the one before, so O is settled
-                    softmax_part<D, NGP>(r, pk, tC, tO + D * i, sc, cs, sees, all_see >= 64, j == 0, sums, [](float) {});
-                    tc::tmem_st32(tC, pk);
+                    softmax_part<D, NGP>(r, tC, tC, tO + D * i, sc, cs, sees, all_see >= 64, j == 0, sums, [](float) {});
                     tc::tmem_ld32(tC + 64, r[0]);
                     tc::tmem_ld32(tC + 96, r[1]);
                     tc::tmem_ld_wait();
-                    softmax_part<D, NGP>(r, pk, tC + 64, tO + D * i, sc + 4, cs, sees - 64, all_see >= 128, j == 0, sums, [&](float alpha) {
+                    softmax_part<D, NGP>(r, tC + 64, tC + 32, tO + D * i, sc + 4, cs, sees - 64, all_see >= 128, j == 0, sums, [&](float alpha) {
                         // what the first half has stored
                         uint32_t w[32];
                         tc::tmem_st_wait();
@@ -1141,7 +1146,6 @@ __device__ __forceinline__ void softmax(const Ctx<D>& x, const CacheAttnArgs& a,
                         }
                         tc::tmem_st32(tC, w);
                     });
-                    tc::tmem_st32(tC + 32, pk);
                 }
                 pass_on(2 * (t & 1) + i);
                 s0_phases ^= 1u << stage;
@@ -1152,15 +1156,14 @@ __device__ __forceinline__ void softmax(const Ctx<D>& x, const CacheAttnArgs& a,
             for (int j = 0; j < nt; ++j, ++t) {
                 wait(B_S1, stage, ph);
                 if (warp_live) {
-                    uint32_t r[2][32], pk[32];
+                    uint32_t r[2][32];
                     const uint32_t tC = tS + 128 * (t & 1) + 64 * i;
                     tc::tmem_ld32(tC, r[0]);
                     tc::tmem_ld32(tC + 32, r[1]);
                     tc::tmem_ld_wait();
-                    softmax_part<D, NGP>(r, pk, tC, tO + D * i, scales + 16 * slot + 4 * i, cs, sees, all_see >= 64, j == 0, sums, [&](float) {
+                    softmax_part<D, NGP>(r, tC, tC, tO + D * i, scales + 16 * slot + 4 * i, cs, sees, all_see >= 64, j == 0, sums, [&](float) {
                         if (j > 0) wait(B_PV, (t - 1) & 1, ((t - 1) >> 1) & 1);
                     });
-                    tc::tmem_st32(tC, pk);
                 }
                 pass_on(2 * (t & 1) + i);
                 up();
