@@ -22,9 +22,9 @@
 // more flat rows by the tensor pipe.
 //
 // Measured (32 query heads, 8 kv heads, d = 128, whole calls with the merge):
-// 64 single rows over 512 to 30912 keys 213 us (4.4 TB/s; a copy of the bytes
-// 139), 64 blocks of 32 rows over the same 235 us (1025 TFLOP/s), 64 rows over
-// 131072 keys 140 us (980 TFLOP/s), 3 prompts of 5000 to 9000 rows 950 us (900
+// 64 single rows over 512 to 30912 keys 210 us (4.5 TB/s; a copy of the bytes
+// 139), 64 blocks of 32 rows over the same 233 us (1035 TFLOP/s), 64 rows over
+// 131072 keys 139 us (990 TFLOP/s), 3 prompts of 5000 to 9000 rows 956 us (890
 // TFLOP/s). A tile of a one-tile unit takes 1500 clocks, of a two-tile unit
 // 2900 for both: softmax 1450, PV and the next S 1024, four hand-overs 400, one
 // after the other, since TMEM has no room for a third S nor shared memory for
@@ -32,7 +32,8 @@
 // N = 64 take 384 clocks instead of 256 for the same work (they read more from
 // shared memory than they multiply). Tiles whose offsets move cost 1600 clocks
 // more; a unit's query split 2500 to 8000, its results 3500 to 8000, most of it
-// the fetching of code that runs once. Tried: sixteen softmax warps, two to a
+// the fetching of code that runs once. O is rescaled 64 columns at a time, after p'
+// has left its registers (956 against 969 us for the prompts). Tried: sixteen softmax warps, two to a
 // row, with shared offsets: 269 and 354 us for the first two calls above when
 // eight warps of 64 keys took 216 and 251.
 //
@@ -853,8 +854,8 @@ __device__ __forceinline__ float at_least(float x) {
     return y;
 }
 
-// p' of the 64 keys of a row whose scores were loaded from TMEM column tC on into r; p' goes to pk as fp16 pairs. NG pages
-// of GK keys each; sc points at the first one's key scale. The row sees the first `visible` keys; `full`: all of the
+// p' of the 64 keys of a row whose scores were loaded from TMEM column tC on into r; p' goes to the columns from tP on as
+// fp16 pairs. NG pages of GK keys each; sc points at the first one's key scale. The row sees the first `visible` keys; `full`: all of the
 // warp's rows see all; `first`: the row's O holds nothing yet. `settle(alpha)` waits until O (at tO) may be rescaled, and
 // rescales by the power of two alpha what the tile has stored of p' already.
 //
