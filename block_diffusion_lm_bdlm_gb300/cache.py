@@ -38,9 +38,10 @@ class PageCache:
     itself: table and lens are the truth, and the calls and the program write
     them in stream order. To end sequences, set their lens to 0.
 
-    It keeps one workspace for calls that bring none, come on the stream that
-    the first such call came on, are not captured into a graph and do not ask
-    for their error word; other calls get one of their own.
+    It keeps one workspace for calls that bring neither workspace nor stream,
+    come on the current stream that the first such call came on, are not
+    captured into a graph and do not ask for their error word; other calls get
+    one of their own.
     """
 
     __slots__ = ("k", "v", "k_scale", "v_scale", "table", "lens", "n_layers", "n_pages", "page", "kv_heads",
