@@ -45,7 +45,8 @@ class PageCache:
     """
 
     __slots__ = ("k", "v", "k_scale", "v_scale", "table", "lens", "n_layers", "n_pages", "page", "kv_heads",
-                 "head_dim", "n_seqs", "max_pages", "device", "index", "pages_bytes", "c", "ref", "home", "scratch", "lock")
+                 "head_dim", "n_seqs", "max_pages", "device", "index", "pages_bytes", "c", "ref", "home", "scratch", "lock",
+                 "need")
 
     def __init__(self, k, v, k_scale, v_scale, table, lens):
         for nm, t, dt, dims in (("k", k, torch.float8_e4m3fn, 5), ("v", v, torch.float8_e4m3fn, 5),
@@ -74,6 +75,7 @@ class PageCache:
                          self.n_seqs, self.max_pages, 0)
         self.ref = ctypes.byref(self.c)
         self.home, self.scratch, self.lock = None, None, threading.Lock()
+        self.need = None, 0  # (rows, heads) of the last attention call, and the workspace that they need
 
     @staticmethod
     def empty(n_layers: int, n_pages: int, page: int, kv_heads: int, head_dim: int, n_seqs: int, max_pages: int,
@@ -196,7 +198,10 @@ def bdlm_cache_attn_fwd(cache: PageCache, q, cu_rows, block: int, *, layer: int 
     cu = _ints("cu_rows", cache, cu_rows, cache.n_seqs + 1)
     pos = None if q_pos is None else _ints("q_pos", cache, q_pos, cache.n_seqs)
     _layer(cache, layer)
-    need = lib.bdlm_cache_attn_fwd_workspace_bytes(T, H, cache.kv_heads, d, cache.n_seqs)
+    sized, need = cache.need
+    if sized != (T, H):
+        need = max(lib.bdlm_cache_attn_fwd_workspace_bytes(T, H, cache.kv_heads, d, cache.n_seqs), 256)
+        cache.need = (T, H), need
     handle, here = _on(cache, stream)
     with here:
         if out is None:
@@ -210,7 +215,7 @@ def bdlm_cache_attn_fwd(cache: PageCache, q, cu_rows, block: int, *, layer: int 
                 or not lse.is_contiguous():
             raise ValueError("lse must be a contiguous fp32 CUDA tensor [H, T]")
         with cache.lock:
-            ws = _workspace(cache, workspace, max(need, 256), handle, check or stream is not None)
+            ws = _workspace(cache, workspace, need, handle, check or stream is not None)
             st = lib.bdlm_cache_attn_fwd(cache.ref, layer, q.data_ptr(), out.data_ptr(), lse.data_ptr(), T, H, block, cu,
                                          pos, softmax_scale, BDLM_F32 if out.dtype == torch.float32 else BDLM_BF16,
                                          ws.data_ptr(), ws.numel(), handle)
