@@ -35,7 +35,8 @@ constexpr int kAll = kCluster * kPlanThreads;
 constexpr int kCopyThreads = 256;
 
 struct Scratch {
-    int* n_copies;  // [1], then padding
+    int* n_copies;  // [1]
+    int* refused;   // [1] 0, or 1 + the item that the third phase refuses; then padding
     long long* totals;  // [2][kCluster] pages needed, pages free, of each CTA's run
     int* count;     // [n_pages] sequences that name the page
     int* rank;      // [n_pages] free pages in order (reserve, fork); new number of a page that moves (compact)
@@ -49,6 +50,7 @@ __host__ __device__ __forceinline__ Scratch carve(int* p, int n_pages, int n_seq
     Scratch s;
     const long long m = n_pages > n_seqs ? n_pages : n_seqs;
     s.n_copies = p;
+    s.refused = p + 1;
     s.totals = reinterpret_cast<long long*>(p + 32);
     s.count = p + 64;
     s.rank = s.count + n_pages;
@@ -111,6 +113,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads,
         a.hdr->error = DEV_OK;
         a.hdr->info = 0;
         *s.n_copies = 0;
+        *s.refused = 0;
     }
     cluster.sync();
 
@@ -152,7 +155,9 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads,
     int lo, hi, plo, phi, t;
     run_of(a.op == PAGES_FORK ? a.n : c.n_seqs, rank, &lo, &hi);
     run_of(c.n_pages, rank, &plo, &phi);
-    bool ok = __ldcg(&a.hdr->error) == DEV_OK;  // the same for the whole cluster
+    // The same for the whole cluster, which the barriers inside `if (ok)` need: nobody writes the word between the barriers
+    // on either side of this read. What this phase itself refuses goes to a word of its own.
+    bool ok = __ldcg(&a.hdr->error) == DEV_OK;
     auto need_of = [&](int i) {
         if (a.op == PAGES_COMPACT) return 0;
         if (a.op == PAGES_FORK) {
@@ -178,11 +183,11 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads,
                 const int len = __ldcg(c.lens + i);
                 if (__ldg(a.new_lens + i) > len && (len & (c.page - 1)) &&
                     __ldcg(s.count + __ldcg(c.table + (long long)i * c.max_pages + (len >> shift))) > 1)
-                    set_error(a.hdr, DEV_CHECK, i);
+                    atomicCAS(s.refused, 0, i + 1);
             }
         if (a.op == PAGES_FORK)  // nobody is a parent and a child of one call
             for (int i = lo + tid; i < hi; i += kPlanThreads)
-                if (__ldcg(s.child + __ldg(a.parents + i))) set_error(a.hdr, DEV_CHECK, i);
+                if (__ldcg(s.child + __ldg(a.parents + i))) atomicCAS(s.refused, 0, i + 1);
     }
     cluster.sync();
 
@@ -196,7 +201,8 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads,
             need64 += x;
             all_free += (int)y;
         }
-    ok = ok && __ldcg(&a.hdr->error) == DEV_OK;
+    const int refused = ok ? __ldcg(s.refused) : 0;  // the same for the whole cluster: nobody writes it any more
+    ok = ok && refused == 0;
     const bool fits = need64 <= all_free;
     const int all_need = fits ? (int)need64 : 0;
     const int live = c.n_pages - all_free;
@@ -228,7 +234,11 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads,
             }
         }
     }
-    if (ok && !fits && gtid == 0) {
+    if (gtid == 0 && refused) {  // the word is not read again
+        a.hdr->error = DEV_CHECK;
+        a.hdr->info = refused - 1;
+    }
+    if (gtid == 0 && ok && !fits) {
         a.hdr->error = DEV_NO_PAGES;
         a.hdr->info = (int)(need64 - all_free > 0x7fffffff ? 0x7fffffff : need64 - all_free);
     }

@@ -1,0 +1,60 @@
+"""Page calls that refuse an item in their last check, where every CTA of the plan's cluster has items of its own: they
+leave the cache as it was, and the next call works."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import cache_oracle as co
+
+import cache_util as cu
+from test_gpu_cache import bd, dev  # noqa: F401  (bd is a fixture)
+
+pytestmark = pytest.mark.gpu
+
+
+def shared_pairs(n):
+    """n parents of 20 positions and n children that share page 0 of theirs and stop inside it: none may grow."""
+    c = cu.make(301, lens=[20] * n, page=16, Hk=1, d=64, spare=4 * n, max_pages=4, extra_seqs=n)
+    assert co.fork(c, list(range(n)), list(range(n, 2 * n))) == ""
+    c["lens"][n:] = 9
+    return c
+
+
+@pytest.mark.parametrize("who", ["one", "every eighth", "all"])
+def test_growth_inside_shared_pages_is_refused_wherever_it_is_asked_for(bd, who):
+    n = 1200
+    c = shared_pairs(n)
+    cache = cu.to_device(bd, c)
+    ws = torch.empty(bd.bdlm_cache_pages_workspace_bytes(c["k"].shape[1], 2 * n), dtype=torch.uint8, device="cuda")
+    grow = {"one": [2 * n - 1], "every eighth": range(n, 2 * n, n // 8), "all": range(n, 2 * n)}[who]
+    want = c["lens"].copy()
+    want[list(grow)] += 1
+    new = dev(want, torch.int32)
+    for _ in range(50):
+        bd.bdlm_cache_reserve(cache, new, workspace=ws)
+    assert bd.bdlm_read_error(ws) == 6
+    cu.check_same(cu.to_host(cache), c)
+    info = int(ws[4:8].view(torch.int32))
+    assert info in grow
+    want[n:] = 0
+    bd.bdlm_cache_reserve(cache, dev(want, torch.int32), workspace=ws)
+    assert bd.bdlm_read_error(ws) == 0 and co.reserve(c, want) == ""
+    cu.check_same(cu.to_host(cache), c)
+
+
+@pytest.mark.parametrize("n", [1, 8, 3000])
+def test_a_parent_that_is_a_child_of_the_same_call_is_refused(bd, n):
+    c = cu.make(307, lens=[20], page=16, Hk=1, d=64, spare=2 * n + 4, max_pages=4, extra_seqs=2 * n)
+    cache = cu.to_device(bd, c)
+    ws = torch.empty(bd.bdlm_cache_pages_workspace_bytes(c["k"].shape[1], 2 * n + 1), dtype=torch.uint8, device="cuda")
+    # every second fork takes the child of the one before as its parent
+    parents = dev([x for i in range(n) for x in (0, 1 + 2 * i)], torch.int32)
+    children = dev(list(range(1, 2 * n + 1)), torch.int32)
+    for _ in range(50):
+        bd.bdlm_cache_fork(cache, parents, children, workspace=ws)
+    assert bd.bdlm_read_error(ws) == 6
+    cu.check_same(cu.to_host(cache), c)
+    parents.zero_()
+    bd.bdlm_cache_fork(cache, parents, children, workspace=ws)
+    assert bd.bdlm_read_error(ws) == 0 and co.fork(c, [0] * 2 * n, list(range(1, 2 * n + 1))) == ""
+    cu.check_same(cu.to_host(cache), c)
