@@ -57,5 +57,18 @@ class BlockDecoder:
         bdlm_cache_fork(self.cache, parents, children, check=check)
 
     def end(self, seqs: torch.Tensor) -> None:
-        """Empty the sequences; pages that no other one names are free."""
-        self.cache.lens[seqs.long()] = 0
+        """Empty the sequences; pages that no other one names are free. seqs
+        holds their numbers (int32 or int64; negative ones count from the end);
+        a number that no sequence has is passed over."""
+        self.cache.lens.masked_fill_(self._named(seqs), 0)
+
+    def _named(self, seqs: torch.Tensor) -> torch.Tensor:
+        """Which sequences the numbers name (bool [n_seqs]). A number out of
+        range must not index anything: on the device that ends the process."""
+        if seqs.dtype not in (torch.int32, torch.int64):
+            raise ValueError(f"sequence numbers must be int32 or int64, got {seqs.dtype}")
+        n = self.cache.n_seqs
+        at = seqs.to(self.cache.device, torch.int64).reshape(-1)
+        at = torch.where(at < 0, at + n, at)
+        hit = torch.zeros(n + 1, dtype=torch.bool, device=self.cache.device)
+        return hit.index_fill_(0, torch.where((at < 0) | (at >= n), n, at), True)[:n]

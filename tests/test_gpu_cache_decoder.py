@@ -1,0 +1,40 @@
+"""BlockDecoder where a program leaves the plain order of prompt, blocks and endings: numbers that name no sequence,
+blocks that are given up, sequences that end or branch between two steps of a block, calls without rows."""
+import numpy as np
+import pytest
+import torch
+
+from oracle import cache_oracle as co
+
+import cache_util as cu
+from test_gpu_cache import bd, dev, rows_of  # noqa: F401  (bd is a fixture)
+
+pytestmark = pytest.mark.gpu
+
+
+def decoder(bd, seed, lens, *, page=16, Hk=2, d=64, block=8, spare=20, extra_seqs=2, layers=1):
+    """(decoder, its cache, a host copy of it)"""
+    from block_diffusion_lm_bdlm_gb300.decode import BlockDecoder
+
+    c = cu.make(seed, lens=lens, page=page, Hk=Hk, d=d, spare=spare, extra_seqs=extra_seqs, layers=layers, max_pages=8)
+    cache = cu.to_device(bd, c)
+    return BlockDecoder(cache, block), cache, c
+
+
+def i32(*x):
+    return dev(list(x), torch.int32)
+
+
+def test_ending_numbers_that_name_no_sequence(bd):
+    dec, cache, c = decoder(bd, 401, [20, 9, 33])
+    for seqs in (i32(5, 99, -6, 2 ** 31 - 1), i32(), dev([2 ** 40], torch.int64)):
+        dec.end(seqs)
+        cu.check_same(cu.to_host(cache), c)
+    dec.end(i32(1, 77, 1))
+    dec.end(torch.tensor([-3]))  # from the end: sequence 2 of five
+    c["lens"][1:3] = 0
+    cu.check_same(cu.to_host(cache), c)
+    for seqs in (torch.tensor([True, False, False, False, False]), torch.tensor([0.0])):
+        with pytest.raises(ValueError):
+            dec.end(seqs)
+    cu.check_same(cu.to_host(cache), c)
