@@ -24,13 +24,17 @@ import torch
 from . import PageCache, bdlm_cache_attn_fwd, bdlm_cache_fork, bdlm_cache_reserve, bdlm_cache_write
 
 
+_NONE = -2 ** 31
+
+
 class BlockDecoder:
     def __init__(self, cache: PageCache, block: int, softmax_scale: float = 0.0):
         if block < 1:
             raise ValueError("block must be positive")
         self.cache, self.block, self.softmax_scale = cache, int(block), float(softmax_scale)
         self.cu_rows = torch.zeros(cache.n_seqs + 1, dtype=torch.int32, device=cache.device)
-        self._kept = cache.lens.clone()
+        self._kept = cache.lens.clone()          # lengths before the last begin
+        self._rows = torch.zeros_like(cache.lens)  # rows that it gave and rewind may still take; _NONE: none
 
     def begin(self, rows: torch.Tensor, *, check: bool = False) -> torch.Tensor:
         """Make room for `rows` new rows of every sequence behind what it
@@ -39,7 +43,8 @@ class BlockDecoder:
         offsets are all 0, so that attend does nothing."""
         self._kept.copy_(self.cache.lens)
         bdlm_cache_reserve(self.cache, self._kept + rows, check=check)
-        torch.cumsum(self.cache.lens - self._kept, 0, dtype=torch.int32, out=self.cu_rows[1:])
+        torch.sub(self.cache.lens, self._kept, out=self._rows)
+        torch.cumsum(self._rows, 0, dtype=torch.int32, out=self.cu_rows[1:])
         return self.cu_rows
 
     def attend(self, layer: int, q, k, v, *, out=None, lse=None):
@@ -49,11 +54,23 @@ class BlockDecoder:
                                    softmax_scale=self.softmax_scale, out=out, lse=lse)
 
     def rewind(self) -> None:
-        """Drop the rows of the last begin."""
-        self.cache.lens.copy_(self._kept)
+        """Drop the rows of the last begin. Sequences that have ended or
+        branched off since then stay as they are."""
+        lens = self.cache.lens
+        lens.copy_(torch.where(self._untouched(), self._kept, lens))
+
+    def _untouched(self) -> torch.Tensor:
+        """The sequences whose lengths are those that begin left."""
+        return self.cache.lens - self._kept == self._rows
+
+    def _settle(self) -> None:
+        """Take the others out of rewind's reach, before their lengths can
+        come to those of begin again."""
+        self._rows.masked_fill_(~self._untouched(), _NONE)
 
     def branch(self, parents: torch.Tensor, children: torch.Tensor, *, check: bool = False) -> None:
         """children[i] (empty) continue what parents[i] hold."""
+        self._settle()
         bdlm_cache_fork(self.cache, parents, children, check=check)
 
     def end(self, seqs: torch.Tensor) -> None:
@@ -61,6 +78,7 @@ class BlockDecoder:
         holds their numbers (int32 or int64; negative ones count from the end);
         a number that no sequence has is passed over."""
         self.cache.lens.masked_fill_(self._named(seqs), 0)
+        self._settle()
 
     def _named(self, seqs: torch.Tensor) -> torch.Tensor:
         """Which sequences the numbers name (bool [n_seqs]). A number out of

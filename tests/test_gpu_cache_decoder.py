@@ -38,3 +38,39 @@ def test_ending_numbers_that_name_no_sequence(bd):
         with pytest.raises(ValueError):
             dec.end(seqs)
     cu.check_same(cu.to_host(cache), c)
+
+
+def test_rewind_leaves_endings_and_candidates_as_they_are(bd):
+    # begin, end one sequence, branch into its pages and its place, compact, rewind: what ended stays ended, what
+    # branched stays, and only the others lose the block's rows
+    dec, cache, c = decoder(bd, 409, [24, 40, 16, 30])
+    dec.begin(i32(8, 8, 0, 8, 0, 0), check=True)
+    assert co.reserve(c, c["lens"] + [8, 8, 0, 8, 0, 0]) == ""
+    dec.end(i32(1))
+    c["lens"][1] = 0
+    dec.branch(i32(2, 0), i32(1, 4), check=True)  # 1 again, now 16 positions; 4 holds sequence 0's 32
+    assert co.fork(c, [2, 0], [1, 4]) == ""
+    assert int(bd.bdlm_cache_compact(cache, check=True)) == co.compact(c)
+    cu.check_same(cu.to_host(cache), c)
+    dec.rewind()
+    c["lens"] = np.array([24, 16, 16, 30, 32, 0])
+    cu.check_same(cu.to_host(cache), c)
+    dec.rewind()  # there is nothing left to drop
+    cu.check_same(cu.to_host(cache), c)
+
+
+@pytest.mark.parametrize("direct", [False, True])
+def test_rewind_passes_over_a_child_as_long_as_the_sequence_that_ended_in_its_place(bd, direct):
+    dec, cache, c = decoder(bd, 419, [24, 24])
+    dec.begin(i32(8, 8, 0, 0), check=True)
+    assert co.reserve(c, c["lens"] + [8, 8, 0, 0]) == ""
+    if direct:
+        cache.lens[0] = 0
+    else:
+        dec.end(i32(0))
+    c["lens"][0] = 0
+    dec.branch(i32(1), i32(0), check=True)
+    assert co.fork(c, [1], [0]) == ""
+    dec.rewind()
+    c["lens"] = np.array([32, 24, 0, 0])
+    cu.check_same(cu.to_host(cache), c)
