@@ -33,7 +33,8 @@ class BlockDecoder:
             raise ValueError("block must be positive")
         self.cache, self.block, self.softmax_scale = cache, int(block), float(softmax_scale)
         self.cu_rows = torch.zeros(cache.n_seqs + 1, dtype=torch.int32, device=cache.device)
-        self._kept = cache.lens.clone()          # lengths before the last begin
+        self._cu = torch.zeros_like(self.cu_rows)  # those of cu_rows that attend goes by: all 0 once the block is over
+        self._kept = cache.lens.clone()            # lengths before the last begin
         self._rows = torch.zeros_like(cache.lens)  # rows that it gave and rewind may still take; _NONE: none
 
     def begin(self, rows: torch.Tensor, *, check: bool = False) -> torch.Tensor:
@@ -44,20 +45,30 @@ class BlockDecoder:
         self._kept.copy_(self.cache.lens)
         bdlm_cache_reserve(self.cache, self._kept + rows, check=check)
         torch.sub(self.cache.lens, self._kept, out=self._rows)
-        torch.cumsum(self._rows, 0, dtype=torch.int32, out=self.cu_rows[1:])
+        torch.cumsum(self._rows, 0, dtype=torch.int32, out=self._cu[1:])
+        self.cu_rows.copy_(self._cu)
         return self.cu_rows
 
-    def attend(self, layer: int, q, k, v, *, out=None, lse=None):
-        """Write the rows' keys and values and attend; (o, lse)."""
-        bdlm_cache_write(self.cache, k, v, self.cu_rows, layer=layer)
-        return bdlm_cache_attn_fwd(self.cache, q, self.cu_rows, self.block, layer=layer,
-                                   softmax_scale=self.softmax_scale, out=out, lse=lse)
+    def attend(self, layer: int, q, k, v, *, out=None, lse=None, check: bool = False):
+        """Write the rows' keys and values and attend; (o, lse). The rows of a
+        sequence that has ended since begin are not written and see nothing
+        (o = 0, lse = -inf); the others keep their places in q, k and v. After
+        rewind there are no rows until the next begin, and o and lse stay
+        unwritten. check=True synchronises and raises where no sequence has
+        rows or the offsets do not fit q."""
+        if check and q.shape[0] > 0 and int(self._cu[-1]) == 0:
+            raise RuntimeError("no sequence has rows: begin a block before attend")
+        bdlm_cache_write(self.cache, k, v, self._cu, layer=layer)
+        # The positions come from begin: lengths say nothing about those of a sequence that has ended.
+        return bdlm_cache_attn_fwd(self.cache, q, self._cu, self.block, layer=layer, q_pos=self._kept,
+                                   softmax_scale=self.softmax_scale, out=out, lse=lse, check=check)
 
     def rewind(self) -> None:
         """Drop the rows of the last begin. Sequences that have ended or
         branched off since then stay as they are."""
         lens = self.cache.lens
         lens.copy_(torch.where(self._untouched(), self._kept, lens))
+        self._cu.zero_()
 
     def _untouched(self) -> torch.Tensor:
         """The sequences whose lengths are those that begin left."""

@@ -74,3 +74,65 @@ def test_rewind_passes_over_a_child_as_long_as_the_sequence_that_ended_in_its_pl
     dec.rewind()
     c["lens"] = np.array([32, 24, 0, 0])
     cu.check_same(cu.to_host(cache), c)
+
+
+def test_attending_after_rewind_touches_nothing(bd):
+    dec, cache, c = decoder(bd, 421, [24, 33])
+    rng = np.random.default_rng(1)
+    (q, _), (k, _), (v, _) = rows_of(rng, 16, 4, 64), rows_of(rng, 16, 2, 64), rows_of(rng, 16, 2, 64)
+    for again in (False, True):  # before the first begin, and after rewind
+        out, lse = torch.full_like(q, 5.0), torch.full((4, 16), 5.0, device="cuda")
+        dec.attend(0, q, k, v, out=out, lse=lse)
+        assert bool((out == 5).all()) and bool((lse == 5).all())
+        got = cu.to_host(cache)
+        cu.check_same({**got, "table": c["table"]}, c)
+        if again:
+            with pytest.raises(RuntimeError, match="begin"):
+                dec.attend(0, q, k, v, out=out, lse=lse, check=True)
+        else:
+            assert dec.begin(i32(8, 8, 0, 0), check=True).tolist() == [0, 8, 16, 16, 16]
+            dec.rewind()
+            assert dec.cu_rows.tolist() == [0, 8, 16, 16, 16]  # what begin has returned is the program's to read
+
+
+@pytest.mark.parametrize("direct", [False, True])
+def test_a_sequence_that_ends_between_two_steps(bd, direct):
+    # its rows are not written and see nothing; the others go on in their places of q, k and v, also behind a rewind
+    dec, cache, c = decoder(bd, 431, [24, 40, 16], Hk=2, d=64, block=8)
+    rows = np.array([8, 8, 8, 0, 0])
+    off = cu.offsets(rows)
+    rng = np.random.default_rng(2)
+
+    def step(dead):
+        (q, qh), (k, kh), (v, vh) = rows_of(rng, 24, 4, 64), rows_of(rng, 24, 2, 64), rows_of(rng, 24, 2, 64)
+        o, lse = dec.attend(0, q, k, v)
+        if not dead:
+            co.write(c, 0, kh, vh, off)
+            cu.check_attention(o, lse, co.attention(c, 0, qh, off, 8, 0.125))
+            return
+        co.write(c, 0, np.delete(kh, slice(8, 16), 0), np.delete(vh, slice(8, 16), 0), [0, 8, 8, 16, 16, 16])
+        cu.check_attention(o, lse, co.attention(c, 0, qh, off, 8, 0.125, q_pos=[24, 40, 16, 0, 0]))
+        assert bool((o[8:16] == 0).all()) and bool(torch.isneginf(lse[:, 8:16]).all())
+        cu.check_same(cu.to_host(cache), c)
+
+    dec.begin(dev(rows, torch.int32), check=True)
+    assert co.reserve(c, c["lens"] + rows) == ""
+    step(False)
+    if direct:
+        cache.lens[1] = 0
+    else:
+        dec.end(i32(1))
+    c["lens"][1] = 0
+    step(True)
+    step(True)
+    dec.rewind()
+    c["lens"] = np.array([24, 0, 16, 0, 0])
+    cu.check_same(cu.to_host(cache), c)
+
+
+def test_checked_attending_raises_for_offsets_that_do_not_fit(bd):
+    dec, _, _ = decoder(bd, 433, [24, 33])
+    dec.begin(i32(8, 8, 0, 0), check=True)
+    q, k = torch.ones(15, 4, 64, dtype=torch.bfloat16, device="cuda"), torch.ones(15, 2, 64, dtype=torch.bfloat16, device="cuda")
+    with pytest.raises(bd.BDLMError):
+        dec.attend(0, q, k, k, check=True)
