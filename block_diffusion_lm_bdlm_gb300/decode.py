@@ -80,9 +80,18 @@ class BlockDecoder:
         self._rows.masked_fill_(~self._untouched(), _NONE)
 
     def branch(self, parents: torch.Tensor, children: torch.Tensor, *, check: bool = False) -> None:
-        """children[i] (empty) continue what parents[i] hold."""
+        """children[i] (empty) continue what parents[i] hold. Where that shares
+        a page with rows of the present block, or a child has rows in it, the
+        block is over: as after rewind there are no rows until the next begin,
+        since another step would write into what the candidates share."""
         self._settle()
+        before = self.cache.lens.clone()
         bdlm_cache_fork(self.cache, parents, children, check=check)
+        lens, page = self.cache.lens, self.cache.page
+        took = self._cu[1:] > self._cu[:-1]
+        shared = took & (lens // page * page > self._kept) & self._named(parents)  # below lens // page * page pages are shared
+        over = (shared | took & self._named(children)).any() & (lens != before).any()  # a fork that failed shares nothing
+        self._cu.masked_fill_(over, 0)
 
     def end(self, seqs: torch.Tensor) -> None:
         """Empty the sequences; pages that no other one names are free. seqs

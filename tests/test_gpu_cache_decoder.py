@@ -136,3 +136,63 @@ def test_checked_attending_raises_for_offsets_that_do_not_fit(bd):
     q, k = torch.ones(15, 4, 64, dtype=torch.bfloat16, device="cuda"), torch.ones(15, 2, 64, dtype=torch.bfloat16, device="cuda")
     with pytest.raises(bd.BDLMError):
         dec.attend(0, q, k, k, check=True)
+
+
+@pytest.mark.parametrize("page,over", [(16, True), (64, False)])
+def test_branching_between_two_steps(bd, page, over):
+    # 24 positions and a block of 8: with 16-row pages parent and child share rows 16 .. 31 and the block is over; with
+    # 64-row pages the child has a copy of them and the parent goes on
+    dec, cache, c = decoder(bd, 439, [24, 40], page=page)
+    rng = np.random.default_rng(3)
+    off = [0, 8, 16, 16, 16]
+
+    def step(over):
+        (q, qh), (k, kh), (v, vh) = rows_of(rng, 16, 4, 64), rows_of(rng, 16, 2, 64), rows_of(rng, 16, 2, 64)
+        out, lse = torch.full_like(q, 5.0), torch.full((4, 16), 5.0, device="cuda")
+        dec.attend(0, q, k, v, out=out, lse=lse)
+        if over:
+            assert bool((out == 5).all()) and bool((lse == 5).all())
+        else:
+            co.write(c, 0, kh, vh, off)
+            cu.check_attention(out, lse, co.attention(c, 0, qh, off, 8, 0.125, q_pos=[24, 40, 0, 0]))
+        cu.check_same(cu.to_host(cache), c)
+
+    dec.begin(i32(8, 8, 0, 0), check=True)
+    assert co.reserve(c, c["lens"] + [8, 8, 0, 0]) == ""
+    step(False)
+    dec.branch(i32(0), i32(1))  # refused: child 1 is not empty; the block goes on
+    step(False)
+    dec.branch(i32(0), i32(2), check=True)
+    assert co.fork(c, [0], [2]) == ""
+    step(over)
+    dec.begin(i32(0, 8, 8, 0), check=True)
+    assert co.reserve(c, c["lens"] + [0, 8, 8, 0]) == ""
+    assert dec.cu_rows.tolist() == [0, 0, 8, 16, 16]
+
+
+def test_branching_what_takes_no_part_in_the_block(bd):
+    dec, cache, c = decoder(bd, 443, [24, 40])
+    rng = np.random.default_rng(4)
+    off = [0, 8, 8, 8, 8]
+    dec.begin(i32(8, 0, 0, 0), check=True)
+    assert co.reserve(c, c["lens"] + [8, 0, 0, 0]) == ""
+    dec.branch(i32(1), i32(3), check=True)
+    assert co.fork(c, [1], [3]) == ""
+    (q, qh), (k, kh), (v, vh) = rows_of(rng, 8, 4, 64), rows_of(rng, 8, 2, 64), rows_of(rng, 8, 2, 64)
+    o, lse = dec.attend(0, q, k, v, check=True)
+    co.write(c, 0, kh, vh, off)
+    cu.check_attention(o, lse, co.attention(c, 0, qh, off, 8, 0.125))
+    cu.check_same(cu.to_host(cache), c)
+
+
+def test_branching_into_the_place_of_a_sequence_with_rows(bd):
+    dec, cache, c = decoder(bd, 449, [24, 40, 20])
+    dec.begin(i32(8, 8, 0, 0, 0), check=True)
+    assert co.reserve(c, c["lens"] + [8, 8, 0, 0, 0]) == ""
+    dec.end(i32(0))
+    c["lens"][0] = 0
+    dec.branch(i32(2), i32(0), check=True)
+    assert co.fork(c, [2], [0]) == ""
+    q, k = torch.ones(16, 4, 64, dtype=torch.bfloat16, device="cuda"), torch.ones(16, 2, 64, dtype=torch.bfloat16, device="cuda")
+    dec.attend(0, q, k, k)  # sequence 0's rows are not the child's
+    cu.check_same(cu.to_host(cache), c)
