@@ -40,13 +40,17 @@ class BlockDecoder:
     def begin(self, rows: torch.Tensor, *, check: bool = False) -> torch.Tensor:
         """Make room for `rows` new rows of every sequence behind what it
         holds; returns their offsets (int32 [n_seqs + 1]). If the cache has no
-        room, no sequence gets any row: check=True raises, and without it the
-        offsets are all 0, so that attend does nothing."""
+        room, or rows are negative, no sequence gets any row: the offsets are
+        all 0, so that attend does nothing, and check=True raises."""
+        want = self.cache.lens + rows
+        want.masked_fill_(want < self.cache.lens, -1)  # too many rows, or fewer than none: refused like no room
         self._kept.copy_(self.cache.lens)
-        bdlm_cache_reserve(self.cache, self._kept + rows, check=check)
-        torch.sub(self.cache.lens, self._kept, out=self._rows)
-        torch.cumsum(self._rows, 0, dtype=torch.int32, out=self._cu[1:])
-        self.cu_rows.copy_(self._cu)
+        try:
+            bdlm_cache_reserve(self.cache, want, check=check)
+        finally:  # also where that raises: the rows of the block before are no longer to be written
+            torch.sub(self.cache.lens, self._kept, out=self._rows)
+            torch.cumsum(self._rows, 0, dtype=torch.int32, out=self._cu[1:])
+            self.cu_rows.copy_(self._cu)
         return self.cu_rows
 
     def attend(self, layer: int, q, k, v, *, out=None, lse=None, check: bool = False):

@@ -196,3 +196,23 @@ def test_branching_into_the_place_of_a_sequence_with_rows(bd):
     q, k = torch.ones(16, 4, 64, dtype=torch.bfloat16, device="cuda"), torch.ones(16, 2, 64, dtype=torch.bfloat16, device="cuda")
     dec.attend(0, q, k, k)  # sequence 0's rows are not the child's
     cu.check_same(cu.to_host(cache), c)
+
+
+@pytest.mark.parametrize("bad", ["room", "negative", "long", "type"])
+def test_a_block_that_is_refused_has_no_rows(bd, bad):
+    dec, cache, c = decoder(bd, 457, [24, 40], spare=3)
+    q, k = torch.ones(16, 4, 64, dtype=torch.bfloat16, device="cuda"), torch.ones(16, 2, 64, dtype=torch.bfloat16, device="cuda")
+    dec.begin(i32(8, 8, 0, 0), check=True)
+    assert co.reserve(c, c["lens"] + [8, 8, 0, 0]) == ""
+    rows = {"room": i32(64, 64, 0, 0), "negative": i32(8, -3, 0, 0), "long": i32(2 ** 31 - 1, 0, 0, 0),
+            "type": dev([8, 8, 0, 0], torch.int64)}[bad]
+    with pytest.raises(ValueError if bad == "type" else bd.BDLMError):
+        dec.begin(rows, check=True)
+    assert dec.cu_rows.tolist() == [0] * 5
+    dec.attend(0, q, k, k)  # not the block before's rows
+    dec.rewind()
+    cu.check_same(cu.to_host(cache), c)
+    if bad != "type":
+        assert dec.begin(rows).tolist() == [0] * 5
+        cu.check_same(cu.to_host(cache), c)
+    assert dec.begin(i32(8, 0, 0, 0), check=True).tolist() == [0, 8, 8, 8, 8]
