@@ -24,6 +24,7 @@ import torch
 from . import BDLM_BF16, BDLM_F32, _bf16_cuda, _CCache, _check, _shape, load_library
 
 PAGE_SIZES = (16, 32, 64, 128)
+BDLM_ERR_INVALID_ARG, BDLM_ERR_DEVICE_CHECK = 1, 6
 
 
 class PageCache:
@@ -154,11 +155,23 @@ def _read(lib, workspace, handle, where):
     _check(lib.bdlm_read_error(workspace.data_ptr(), handle), where + " (device)")
 
 
+def _no_rows(cache, cu_rows, workspace, handle, check, where):
+    """A call without rows launches none of the library's kernels; the error
+    word is what theirs would be: offsets that count any row are malformed."""
+    if workspace is None and not check:
+        return
+    bad = (cu_rows != 0).any().int() * BDLM_ERR_DEVICE_CHECK
+    if workspace is not None:
+        _workspace(cache, workspace, 256, handle, True)[:256].zero_()[:4].copy_(bad.reshape(1).view(torch.uint8))
+    if check:
+        _check(int(bad), where + " (device)")
+
+
 def bdlm_cache_write(cache: PageCache, k_new, v_new, cu_rows, *, layer: int = 0, workspace=None, stream=None,
                      check: bool = False) -> None:
     """Quantise the new key and value rows k_new, v_new [T,Hk,d] (bf16) into
     the pages: rows cu_rows[s] .. cu_rows[s+1]-1 become the last positions of
-    sequence s, whose lens already counts them."""
+    sequence s, whose lens already counts them. T may be 0."""
     lib = load_library()
     _bf16_cuda("k_new", k_new)
     _bf16_cuda("v_new", v_new)
@@ -173,6 +186,8 @@ def bdlm_cache_write(cache: PageCache, k_new, v_new, cu_rows, *, layer: int = 0,
     _layer(cache, layer)
     handle, here = _on(cache, stream)
     with here:
+        if shape[0] == 0:
+            return _no_rows(cache, cu_rows, workspace, handle, check, "bdlm_cache_write")
         with cache.lock:
             ws = _workspace(cache, workspace, 256, handle, check or stream is not None)
             st = lib.bdlm_cache_write(cache.ref, layer, k_new.data_ptr(), v_new.data_ptr(), shape[0], cu, ws.data_ptr(),
@@ -189,12 +204,15 @@ def bdlm_cache_attn_fwd(cache: PageCache, q, cu_rows, block: int, *, layer: int 
     block-causal mask; returns (o [T,H,d], lse [H,T] fp32). o is bf16 unless
     `out` is fp32. With q_pos (int32 [n_seqs], the position of each sequence's
     first row) the rows need not be in the cache, and the result is a partial
-    one for bdlm_lse_merge. Rows of q behind cu_rows[-1] are left unwritten."""
+    one for bdlm_lse_merge. Rows of q behind cu_rows[-1] are left unwritten. T
+    may be 0."""
     lib = load_library()
     _bf16_cuda("q", q)
     if q.dim() != 3 or q.shape[2] != cache.head_dim or q.get_device() != cache.index:
         raise ValueError(f"q must be [T, H, {cache.head_dim}] on the cache's device")
     T, H, d = q.shape
+    if H == 0 or H % cache.kv_heads or block <= 0:
+        _check(BDLM_ERR_INVALID_ARG, "bdlm_cache_attn_fwd")
     cu = _ints("cu_rows", cache, cu_rows, cache.n_seqs + 1)
     pos = None if q_pos is None else _ints("q_pos", cache, q_pos, cache.n_seqs)
     _layer(cache, layer)
@@ -214,6 +232,9 @@ def bdlm_cache_attn_fwd(cache: PageCache, q, cu_rows, block: int, *, layer: int 
         elif lse.shape != (H, T) or lse.dtype != torch.float32 or lse.device != cache.device \
                 or not lse.is_contiguous():
             raise ValueError("lse must be a contiguous fp32 CUDA tensor [H, T]")
+        if T == 0:
+            _no_rows(cache, cu_rows, workspace, handle, check, "bdlm_cache_attn_fwd")
+            return out, lse
         with cache.lock:
             ws = _workspace(cache, workspace, need, handle, check or stream is not None)
             st = lib.bdlm_cache_attn_fwd(cache.ref, layer, q.data_ptr(), out.data_ptr(), lse.data_ptr(), T, H, block, cu,

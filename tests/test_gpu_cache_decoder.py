@@ -216,3 +216,30 @@ def test_a_block_that_is_refused_has_no_rows(bd, bad):
         assert dec.begin(rows).tolist() == [0] * 5
         cu.check_same(cu.to_host(cache), c)
     assert dec.begin(i32(8, 0, 0, 0), check=True).tolist() == [0, 8, 8, 8, 8]
+
+
+def test_a_step_in_which_no_sequence_takes_part(bd):
+    dec, cache, c = decoder(bd, 461, [24, 40])
+    q, k = torch.ones(0, 4, 64, dtype=torch.bfloat16, device="cuda"), torch.ones(0, 2, 64, dtype=torch.bfloat16, device="cuda")
+    dec.begin(i32(0, 0, 0, 0), check=True)
+    for check in (False, True):
+        o, lse = dec.attend(0, q, k, k, check=check)
+        assert o.shape == (0, 4, 64) and lse.shape == (4, 0)
+    ws = torch.full((1 << 20,), 255, dtype=torch.uint8, device="cuda")
+    none, some = i32(0, 0, 0, 0, 0), i32(0, 0, 8, 8, 8)
+    for cu_rows, status in ((some, 6), (none, 0)):
+        bd.bdlm_cache_write(cache, k, k, cu_rows, workspace=ws)
+        assert bd.bdlm_read_error(ws) == status
+        ws.fill_(255)
+        bd.bdlm_cache_attn_fwd(cache, q, cu_rows, 8, workspace=ws)
+        assert bd.bdlm_read_error(ws) == status
+        if status:
+            for call in (lambda: bd.bdlm_cache_write(cache, k, k, cu_rows, check=True),
+                         lambda: bd.bdlm_cache_attn_fwd(cache, q, cu_rows, 8, check=True)):
+                with pytest.raises(bd.BDLMError):
+                    call()
+    with pytest.raises(bd.BDLMError):
+        bd.bdlm_cache_attn_fwd(cache, q[:, :3].contiguous(), none, 8)
+    with pytest.raises(ValueError):
+        bd.bdlm_cache_write(cache, k, k[:, :1].contiguous(), none)
+    cu.check_same(cu.to_host(cache), c)
