@@ -211,7 +211,7 @@ def bdlm_cache_attn_fwd(cache: PageCache, q, cu_rows, block: int, *, layer: int 
     if q.dim() != 3 or q.shape[2] != cache.head_dim or q.get_device() != cache.index:
         raise ValueError(f"q must be [T, H, {cache.head_dim}] on the cache's device")
     T, H, d = q.shape
-    if H == 0 or H % cache.kv_heads or block <= 0:
+    if H == 0 or H % cache.kv_heads or not 0 < block < 2 ** 31:  # ctypes would take block modulo 2^32
         _check(BDLM_ERR_INVALID_ARG, "bdlm_cache_attn_fwd")
     cu = _ints("cu_rows", cache, cu_rows, cache.n_seqs + 1)
     pos = None if q_pos is None else _ints("q_pos", cache, q_pos, cache.n_seqs)

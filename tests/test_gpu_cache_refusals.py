@@ -7,7 +7,7 @@ import torch
 from oracle import cache_oracle as co
 
 import cache_util as cu
-from test_gpu_cache import bd, dev  # noqa: F401  (bd is a fixture)
+from test_gpu_cache import attn_case, bd, dev  # noqa: F401  (bd is a fixture)
 
 pytestmark = pytest.mark.gpu
 
@@ -58,3 +58,13 @@ def test_a_parent_that_is_a_child_of_the_same_call_is_refused(bd, n):
     bd.bdlm_cache_fork(cache, parents, children, workspace=ws)
     assert bd.bdlm_read_error(ws) == 0 and co.fork(c, [0] * 2 * n, list(range(1, 2 * n + 1))) == ""
     cu.check_same(cu.to_host(cache), c)
+
+
+def test_a_block_size_beyond_32_bits_is_refused(bd):
+    c, off, q, qh = attn_case(311, [90], [6], 16, 4, 2, 64, 1)
+    cache = cu.to_device(bd, c)
+    for block in (2 ** 32 + 1, 2 ** 31, -2 ** 32 + 4):  # modulo 2^32 two of them would be taken as 1 and 4
+        with pytest.raises(bd.BDLMError):
+            bd.bdlm_cache_attn_fwd(cache, q, dev(off, torch.int32), block)
+    o, lse = bd.bdlm_cache_attn_fwd(cache, q, dev(off, torch.int32), 2 ** 31 - 1)  # every key is seen
+    cu.check_attention(o, lse, co.attention(c, 0, qh, off, 2 ** 31 - 1, 0.125))
