@@ -25,7 +25,7 @@ constexpr int kSlices = 3;
 constexpr int kMaxParts = kMaxCtas + 1;
 
 template <int D>
-__global__ void __launch_bounds__(kMergeThreads) cache_merge_kernel(const CacheAttnArgs a) {
+__global__ void __launch_bounds__(kMergeThreads) cache_merge_kernel(const CacheAttnArgs a, int ctas) {
     __shared__ float s_w[kMaxParts][32];  // weights of 32 rows at a time
     __shared__ float s_lse[32];
     __shared__ int s_err[2];
@@ -34,9 +34,8 @@ __global__ void __launch_bounds__(kMergeThreads) cache_merge_kernel(const CacheA
     const ShareRec* recs = share_recs(a.scratch);
     const int c = blockIdx.x + 1;
     if (blockIdx.x == 0 && blockIdx.y == 0) {  // the shares' errors
-        const int n = gridDim.x + 1;
         int err = 0, info = 0;
-        for (int i = tid; i < n; i += kMergeThreads)
+        for (int i = tid; i < ctas; i += kMergeThreads)
             if (recs[i].error) {
                 err = recs[i].error;
                 info = recs[i].info;
@@ -50,6 +49,7 @@ __global__ void __launch_bounds__(kMergeThreads) cache_merge_kernel(const CacheA
             a.hdr->info = s_err[1];
         }
     }
+    if (c >= ctas) return;  // a single CTA: it leaves one record and cuts nothing
     const ShareRec r = recs[c];
     const int rows = imin(kUnitRows, r.rows * a.G - r.m0), two = is_two(rows), lead = lead_of(rows);
     if (c >= r.C || tile_at(r.off, two, lead) == 0) return;  // no share begins here, or it begins with its unit's first tile
@@ -153,7 +153,8 @@ cudaError_t launch_cache_attn(const CacheAttnArgs& a, int num_sms, cudaStream_t 
     at.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &at;
     cfg.numAttrs = 1;
-    e = a.c.D == 128 ? cudaLaunchKernelEx(&cfg, cache_merge_kernel<128>, a) : cudaLaunchKernelEx(&cfg, cache_merge_kernel<64>, a);
+    e = a.c.D == 128 ? cudaLaunchKernelEx(&cfg, cache_merge_kernel<128>, a, ctas)
+                      : cudaLaunchKernelEx(&cfg, cache_merge_kernel<64>, a, ctas);
     if (e == cudaSuccess) *launches += 2;
     return e;
 }
