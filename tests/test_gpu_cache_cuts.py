@@ -1,5 +1,6 @@
 """Attention over the paged cache cut into another number of shares than one per SM: from one, which leaves the merge
-nothing to do, to as many as the workspace has room for."""
+nothing to do, to as many as the workspace has room for. And caches over which a tile that is lost or counted twice at a
+cut would show (cache_marks)."""
 import ctypes
 import os
 import subprocess
@@ -10,6 +11,7 @@ import torch
 
 from oracle import cache_oracle as co
 
+import cache_marks as cm
 import cache_util as cu
 from test_gpu_cache import attn_case, bd, dev  # noqa: F401  (bd is a fixture)
 
@@ -52,3 +54,17 @@ def test_any_number_of_shares_gives_the_same_attention(with_ctas, bd, d, page, G
     for ctas in (1, 2, 3, 7, 16, 61, 151, 256):
         o, lse = with_ctas(cache, q, dev(off, torch.int32), 16, ctas, f32=ctas % 2 == 0)
         cu.check_attention(o, lse, ref, f"{ctas} shares")
+
+
+@pytest.mark.parametrize("keys", ["any", "alike"])
+@pytest.mark.parametrize("name", list(cm.CASES))
+def test_no_tile_is_lost_or_counted_twice(with_ctas, bd, name, keys):
+    block, d = cm.CASES[name][6], cm.CASES[name][5]
+    c, off, q, qh = cm.make(name, keys)
+    ref = co.attention(c, 0, qh, off, block, d ** -0.5)
+    cache, q, cu_rows = cu.to_device(bd, c), q.cuda(), dev(off, torch.int32)
+    cu.check_attention(*bd.bdlm_cache_attn_fwd(cache, q, cu_rows, block, check=True), ref)
+    out = torch.empty(q.shape, dtype=torch.float32, device="cuda")
+    cu.check_attention(*bd.bdlm_cache_attn_fwd(cache, q, cu_rows, block, out=out), ref)
+    for ctas in (1, 7, 61, 200, 256):
+        cu.check_attention(*with_ctas(cache, q, cu_rows, block, ctas, f32=ctas % 2 == 0), ref, f"{ctas} shares")
