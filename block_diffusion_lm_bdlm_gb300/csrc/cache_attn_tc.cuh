@@ -1134,15 +1134,17 @@ __device__ __forceinline__ void softmax(const Ctx<D>& x, const CacheAttnArgs& a,
                     tc::tmem_ld32(tC + 96, r[1]);
                     tc::tmem_ld_wait();
                     softmax_part<D, NGP>(r, tC + 64, tC + 32, tO + D * i, sc + 4, cs, sees - 64, all_see >= 128, j == 0, sums, [&](float alpha) {
-                        // what the first half has stored
+                        // What the first half has stored. p' is up to 2^15, so an alpha below 2^-24, where fp16 ends,
+                        // leaves some of it: two factors, of which the first rounds only what ends below 2^-24.
                         uint32_t w[32];
                         tc::tmem_st_wait();
                         tc::tmem_ld32(tC, w);
                         tc::tmem_ld_wait();
-                        const __half2 f = __float2half2_rn(alpha);
+                        const bool far = alpha < 0x1p-15f;
+                        const __half2 f0 = __float2half2_rn(far ? 0x1p-15f : alpha), f1 = __float2half2_rn(far ? alpha * 0x1p15f : 1.f);
 #pragma unroll
                         for (int e = 0; e < 32; ++e) {
-                            const __half2 y = __hmul2(*reinterpret_cast<const __half2*>(&w[e]), f);
+                            const __half2 y = __hmul2(__hmul2(*reinterpret_cast<const __half2*>(&w[e]), f0), f1);
                             w[e] = *reinterpret_cast<const uint32_t*>(&y);
                         }
                         tc::tmem_st32(tC, w);
