@@ -16,6 +16,10 @@ constexpr int kMaxPages = 1 << 26;
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
 bool good_ptr(const void* p, uintptr_t a) { return p && aligned(p, a); }
+bool overlap(const void* x, size_t nx, const void* y, size_t ny) {
+    const uintptr_t a = reinterpret_cast<uintptr_t>(x), b = reinterpret_cast<uintptr_t>(y);
+    return x && y && a < b + ny && b < a + nx;
+}
 bool supported_d(int d) { return d == 64 || d == 128; }
 
 // Checks the cache and fills the kernels' view of its layer `layer`.
@@ -56,6 +60,12 @@ int view_of(const bdlm_cache* c, int layer, CacheView* w) {
     w->page_shift = shift;
     return BDLM_OK;
 }
+
+// Does an int32 array of a page call lie in the table or the lengths, which the call writes while it reads the array?
+bool in_table(const CacheView& c, const void* p, size_t n) {
+    return overlap(p, 4 * n, c.table, 4 * (size_t)c.n_seqs * c.max_pages);
+}
+bool in_lens(const CacheView& c, const void* p, size_t n) { return overlap(p, 4 * n, c.lens, 4 * (size_t)c.n_seqs); }
 
 int check_workspace(const void* ws, size_t have, size_t need) {
     return ws && aligned(ws, 256) && need > 0 && have >= need ? BDLM_OK : BDLM_ERR_WORKSPACE;
@@ -163,6 +173,8 @@ int bdlm_cache_reserve(const bdlm_cache* cache, const int32_t* new_lens, void* w
     const int st = view_of(cache, 0, &a.c);
     if (st != BDLM_OK) return st;
     if (!good_ptr(new_lens, 4)) return BDLM_ERR_INVALID_ARG;
+    if (in_table(a.c, new_lens, a.c.n_seqs) || (new_lens != a.c.lens && in_lens(a.c, new_lens, a.c.n_seqs)))
+        return BDLM_ERR_INVALID_ARG;
     a.op = PAGES_RESERVE;
     a.new_lens = new_lens;
     return run_pages(a, workspace, workspace_bytes, stream);
@@ -176,6 +188,9 @@ int bdlm_cache_fork(const bdlm_cache* cache, const int32_t* parents, const int32
     if (st != BDLM_OK) return st;
     if (!good_ptr(parents, 4) || !good_ptr(children, 4) || !aligned(fork_lens, 4)) return BDLM_ERR_INVALID_ARG;
     if (n < 1 || n > cache->n_seqs) return BDLM_ERR_INVALID_ARG;
+    if (in_table(a.c, parents, n) || in_lens(a.c, parents, n) || in_table(a.c, children, n) || in_lens(a.c, children, n) ||
+        in_table(a.c, fork_lens, n))
+        return BDLM_ERR_INVALID_ARG;
     a.op = PAGES_FORK;
     a.parents = parents;
     a.children = children;
@@ -190,7 +205,7 @@ int bdlm_cache_compact(const bdlm_cache* cache, int32_t* n_live, void* workspace
     CachePagesArgs a{};
     const int st = view_of(cache, 0, &a.c);
     if (st != BDLM_OK) return st;
-    if (!aligned(n_live, 4)) return BDLM_ERR_INVALID_ARG;
+    if (!aligned(n_live, 4) || in_table(a.c, n_live, 1) || in_lens(a.c, n_live, 1)) return BDLM_ERR_INVALID_ARG;
     a.op = PAGES_COMPACT;
     a.n_live = n_live;
     return run_pages(a, workspace, workspace_bytes, stream);

@@ -185,9 +185,12 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads,
                     __ldcg(s.count + __ldcg(c.table + (long long)i * c.max_pages + (len >> shift))) > 1)
                     atomicCAS(s.refused, 0, i + 1);
             }
-        if (a.op == PAGES_FORK)  // nobody is a parent and a child of one call
-            for (int i = lo + tid; i < hi; i += kPlanThreads)
-                if (__ldcg(s.child + __ldg(a.parents + i))) atomicCAS(s.refused, 0, i + 1);
+        if (a.op == PAGES_FORK)  // nobody is a parent and a child of one call, and no fork's length is one that the call sets
+            for (int i = lo + tid; i < hi; i += kPlanThreads) {
+                const long long at = (reinterpret_cast<long long>(a.fork_lens + i) - reinterpret_cast<long long>(c.lens)) / 4;
+                if (__ldcg(s.child + __ldg(a.parents + i)) || (a.fork_lens && at >= 0 && at < c.n_seqs && __ldcg(s.child + at)))
+                    atomicCAS(s.refused, 0, i + 1);
+            }
     }
     cluster.sync();
 

@@ -459,6 +459,7 @@ BDLM_API size_t bdlm_cache_pages_workspace_bytes(int32_t n_pages, int32_t n_seqs
  *   are gained. Pages that a shorter length gives up are free for the others
  *   of the same call. A sequence may not grow inside a page that another one
  *   names too (BDLM_ERR_DEVICE_CHECK; fork it at that length instead).
+ *   new_lens may be lens itself, but not otherwise overlap lens or table.
  */
 BDLM_API int bdlm_cache_reserve(const bdlm_cache* cache, const int32_t* new_lens, void* workspace,
                   size_t workspace_bytes, bdlm_stream_t stream);
@@ -471,7 +472,9 @@ BDLM_API int bdlm_cache_reserve(const bdlm_cache* cache, const int32_t* new_lens
  *   free page, in the order of i. The children are distinct and empty (length
  *   0) before the call, and none of them is named as a parent; a parent may be
  *   named several times.
- *   parents, children, fork_lens: DEVICE int32 [n].
+ *   parents, children, fork_lens: DEVICE int32 [n], outside table and lens;
+ *   but fork_lens may lie in lens where it covers no child's entry
+ *   (BDLM_ERR_DEVICE_CHECK).
  */
 BDLM_API int bdlm_cache_fork(const bdlm_cache* cache, const int32_t* parents, const int32_t* children,
                   const int32_t* fork_lens, int32_t n, void* workspace, size_t workspace_bytes,
@@ -481,7 +484,8 @@ BDLM_API int bdlm_cache_fork(const bdlm_cache* cache, const int32_t* parents, co
  * bdlm_cache_compact - move the live pages with numbers >= n_live (the count
  *   of live pages) into the free ones below, both in ascending order, and
  *   rewrite the table; afterwards pages n_live .. n_pages - 1 are free.
- *   n_live: NULL, or a DEVICE int32 that receives the count.
+ *   n_live: NULL, or a DEVICE int32, outside table and lens, that receives the
+ *   count.
  */
 BDLM_API int bdlm_cache_compact(const bdlm_cache* cache, int32_t* n_live, void* workspace, size_t workspace_bytes,
                   bdlm_stream_t stream);

@@ -68,3 +68,19 @@ def test_a_block_size_beyond_32_bits_is_refused(bd):
             bd.bdlm_cache_attn_fwd(cache, q, dev(off, torch.int32), block)
     o, lse = bd.bdlm_cache_attn_fwd(cache, q, dev(off, torch.int32), 2 ** 31 - 1)  # every key is seen
     cu.check_attention(o, lse, co.attention(c, 0, qh, off, 2 ** 31 - 1, 0.125))
+
+
+def test_fork_lengths_that_lie_in_the_lengths(bd):
+    # those of the parents themselves are fine; one that the same call sets (a child's) is refused
+    c = cu.make(313, lens=[20, 33], page=16, Hk=1, d=64, spare=12, max_pages=4, extra_seqs=4)
+    cache = cu.to_device(bd, c)
+    ws = torch.empty(bd.bdlm_cache_pages_workspace_bytes(c["k"].shape[1], 6), dtype=torch.uint8, device="cuda")
+    for _ in range(20):
+        bd.bdlm_cache_fork(cache, dev([1, 1], torch.int32), dev([2, 3], torch.int32), cache.lens[1:3], workspace=ws)
+    assert bd.bdlm_read_error(ws) == 6
+    cu.check_same(cu.to_host(cache), c)
+    bd.bdlm_cache_fork(cache, dev([0, 1], torch.int32), dev([2, 3], torch.int32), cache.lens[:2], check=True)
+    assert co.fork(c, [0, 1], [2, 3]) == ""
+    cu.check_same(cu.to_host(cache), c)
+    bd.bdlm_cache_reserve(cache, cache.lens, check=True)
+    cu.check_same(cu.to_host(cache), c)
