@@ -273,10 +273,16 @@ def bdlm_cache_fork(cache: PageCache, parents, children, fork_lens=None, *, work
                     check: bool = False) -> None:
     """Sequence children[i] (empty) becomes a copy of the first fork_lens[i]
     positions (None: all) of parents[i]: full pages are shared, a partly
-    filled last page is copied, in all layers."""
+    filled last page is copied, in all layers. There may be no forks."""
     n = parents.shape[0] if isinstance(parents, torch.Tensor) and parents.dim() == 1 else None
     args = (_ints("parents", cache, parents, n), _ints("children", cache, children, n),
             None if fork_lens is None else _ints("fork_lens", cache, fork_lens, n), n)
+    if n == 0:
+        if workspace is not None:
+            handle, here = _on(cache, stream)
+            with here:
+                _workspace(cache, workspace, 256, handle, True)[:256].zero_()
+        return
     _pages_call(cache, "bdlm_cache_fork", args, workspace, stream, check)
 
 

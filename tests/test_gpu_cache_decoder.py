@@ -243,3 +243,14 @@ def test_a_step_in_which_no_sequence_takes_part(bd):
     with pytest.raises(ValueError):
         bd.bdlm_cache_write(cache, k, k[:, :1].contiguous(), none)
     cu.check_same(cu.to_host(cache), c)
+
+
+def test_branching_nothing(bd):
+    dec, cache, c = decoder(bd, 463, [24, 40])
+    dec.branch(i32(), i32(), check=True)
+    ws = torch.full((4096,), 255, dtype=torch.uint8, device="cuda")
+    bd.bdlm_cache_fork(cache, i32(), i32(), i32(), workspace=ws)
+    assert bd.bdlm_read_error(ws) == 0
+    with pytest.raises(ValueError):
+        bd.bdlm_cache_fork(cache, i32(), i32(1))
+    cu.check_same(cu.to_host(cache), c)
