@@ -254,3 +254,58 @@ def test_branching_nothing(bd):
     with pytest.raises(ValueError):
         bd.bdlm_cache_fork(cache, i32(), i32(1))
     cu.check_same(cu.to_host(cache), c)
+
+
+def test_blocks_from_captured_graphs(bd):
+    # one graph gives every sequence a block, one attends, one gives the block up, one ends a sequence: replayed in any
+    # order, with eager calls between them
+    dec, cache, c = decoder(bd, 467, [24, 40], spare=30)
+    rows, gone = i32(8, 8, 0, 0), i32(1)
+    q, k, v, o = (torch.zeros(16, n, 64, dtype=torch.bfloat16, device="cuda") for n in (4, 2, 2, 4))
+    lse = torch.zeros(4, 16, device="cuda")
+    keep = [x.clone() for x in (cache.k.view(torch.uint8), cache.v.view(torch.uint8), cache.k_scale, cache.v_scale, cache.table, cache.lens)]
+    side = torch.cuda.Stream()
+    with torch.cuda.stream(side):
+        dec.begin(rows), dec.attend(0, q, k, v), dec.rewind(), dec.end(gone)
+    torch.cuda.synchronize()
+    for x, y in zip((cache.k.view(torch.uint8), cache.v.view(torch.uint8), cache.k_scale, cache.v_scale, cache.table, cache.lens), keep):
+        x.copy_(y)
+    graphs = []
+    for f in (lambda: dec.begin(rows), lambda: dec.attend(0, q, k, v, out=o, lse=lse), dec.rewind, lambda: dec.end(gone)):
+        graphs.append(torch.cuda.CUDAGraph())
+        with torch.cuda.graph(graphs[-1]):
+            f()
+    begin, attend, rewind, end = (g.replay for g in graphs)
+    rng = np.random.default_rng(5)
+    off, pos = [0, 8, 16, 16, 16], None
+
+    def step(alone=False):
+        (q1, qh), (k1, kh), (v1, vh) = rows_of(rng, 16, 4, 64), rows_of(rng, 16, 2, 64), rows_of(rng, 16, 2, 64)
+        q.copy_(q1), k.copy_(k1), v.copy_(v1)
+        attend()
+        if alone:
+            co.write(c, 0, kh[:8], vh[:8], [0, 8, 8, 8, 8])
+        else:
+            co.write(c, 0, kh, vh, off)
+        cu.check_attention(o, lse, co.attention(c, 0, qh, off, 8, 0.125, q_pos=pos))
+        cu.check_same(cu.to_host(cache), c)
+
+    for give_up in (False, True, False):
+        pos = list(c["lens"])
+        begin()
+        assert co.reserve(c, c["lens"] + [8, 8, 0, 0]) == ""
+        step(), step()
+        if give_up:
+            rewind()
+            c["lens"] = np.array(pos)
+            o.fill_(5.0)
+            attend()
+            assert bool((o == 5).all())
+            cu.check_same(cu.to_host(cache), c)
+    end()
+    c["lens"][1] = 0
+    step(alone=True)
+    pos = list(c["lens"])
+    dec.begin(rows, check=True)  # sequence 1 anew
+    assert co.reserve(c, c["lens"] + [8, 8, 0, 0]) == ""
+    step()
