@@ -10,12 +10,19 @@ bdlm_cache_* calls that one model's attention layers need.
     dec.branch(parents, children)     # candidates that share what was written so far
     dec.end(seqs)                     # their pages are free again
 
-All state is the cache's table and lens, on the device: begin, attend, rewind,
-branch and end only launch work on the current stream. begin's first step of a
-whole prompt and a denoising step of one block are the same call: under the
-block-causal mask a prompt's rows see the blocks up to their own, and the rows
-of a block that starts at a block boundary see everything before it and each
-other.
+All state is on the device, the cache's table and lens and the present block's
+offsets: begin, attend, rewind, branch and end only launch work on the current
+stream and can be captured into graphs. begin's first step of a whole prompt
+and a denoising step of one block are the same call: under the block-causal
+mask a prompt's rows see the blocks up to their own, and the rows of a block
+that starts at a block boundary see everything before it and each other.
+
+A page has one scale for each head, so a step rounds the committed rows of a
+page that its own rows share anew whenever it changes that scale: values below
+2^-6 of a larger scale lose bits, or become 0, and a later step with smaller
+rows does not bring them back. Where that matters, let every block (and the
+prompt's end) lie on a page boundary: with pages that divide the block, and
+prompts filled up to whole pages, a step's pages hold its own rows only.
 """
 from __future__ import annotations
 
@@ -40,8 +47,10 @@ class BlockDecoder:
     def begin(self, rows: torch.Tensor, *, check: bool = False) -> torch.Tensor:
         """Make room for `rows` new rows of every sequence behind what it
         holds; returns their offsets (int32 [n_seqs + 1]). If the cache has no
-        room, or rows are negative, no sequence gets any row: the offsets are
-        all 0, so that attend does nothing, and check=True raises."""
+        room, rows are negative, or a sequence would grow inside a page that
+        another one reads too (one that was rewound behind a branch), no
+        sequence gets any row: the offsets are all 0, so that attend does
+        nothing, and check=True raises."""
         want = self.cache.lens + rows
         want.masked_fill_(want < self.cache.lens, -1)  # too many rows, or fewer than none: refused like no room
         self._kept.copy_(self.cache.lens)

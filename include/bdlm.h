@@ -401,7 +401,10 @@ BDLM_API size_t bdlm_cache_write_workspace_bytes(void);
  * the page's new rows and the rows before them that it keeps (1 if they are
  * all 0). New rows are stored as x / s rounded to nearest, ties to even;
  * kept rows are expressed in the new scale (exactly, unless the scale grows
- * and a value falls below the smallest normal 2^-6 s). Values that are not
+ * and a value falls below the smallest normal 2^-6 s; such a value loses bits,
+ * or becomes 0, for good: a later write with smaller rows makes the scale
+ * small again, but does not bring them back. Rows that begin at a page's start
+ * share no page with kept ones). Values that are not
  * finite are stored as NaN. Rows of a page from lens[s] on are left as they
  * were. A page that is written must belong to one sequence only.
  * A sequence with fewer positions than new rows, or more than its table
