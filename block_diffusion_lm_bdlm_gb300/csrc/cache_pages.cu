@@ -197,6 +197,7 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads,
     // ---- ranks: free pages in order; for compact the new number of every page that moves
     long long need64 = 0;
     int need_before = 0, free_before = 0, all_free = 0;
+    const int refused = __ldcg(s.refused);  // the same for the whole cluster: nobody writes it any more
     if (ok)
         for (int i = 0; i < kCluster; ++i) {
             const long long x = __ldcg(s.totals + i), y = __ldcg(s.totals + kCluster + i);
@@ -204,7 +205,6 @@ __global__ void __cluster_dims__(kCluster, 1, 1) __launch_bounds__(kPlanThreads,
             need64 += x;
             all_free += (int)y;
         }
-    const int refused = ok ? __ldcg(s.refused) : 0;  // the same for the whole cluster: nobody writes it any more
     ok = ok && refused == 0;
     const bool fits = need64 <= all_free;
     const int all_need = fits ? (int)need64 : 0;

@@ -7,7 +7,7 @@ bdlm_cache_* calls that one model's attention layers need.
         for layer in range(n_layers):
             o, _ = dec.attend(layer, q, k, v)
     ...                               # keep the rows: begin the next block; or dec.rewind() and begin again
-    dec.branch(parents, children)     # candidates that share what was written so far
+    dec.branch(parents, children)     # candidates that share what was written so far; behind a block's last step
     dec.end(seqs)                     # their pages are free again
 
 All state is on the device, the cache's table and lens and the present block's
