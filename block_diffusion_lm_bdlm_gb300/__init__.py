@@ -21,6 +21,12 @@ drives it block by block):
   bdlm_cache_reserve(cache, new_lens)                 lengths, free pages
   bdlm_cache_fork(cache, parents, children)           share pages, copy the last
   bdlm_cache_compact(cache) -> n_live                 live pages to the front
+  bdlm_cache_prefixes(cache, cu_rows) -> runs         which sequences share which leading pages
+  bdlm_cache_attn_shared_fwd(cache, q, cu_rows, block, runs) -> (o, lse)
+                                                      pages that a run shares are read once
+From logits to tokens (see sample.py):
+  bdlm_sample(logits, u, temperature=...) -> (token, logprob)
+  bdlm_unmask(tokens, sampled, logprob, cu_rows, mask_id, ...) -> (tokens, left)
 Restrictions of a call (see Partial):
   Partial.window(lo, hi)                     keys at positions [lo, hi) (a clean shard)
   Partial.window(lo, hi, accumulate=True)    merge into a running (out, lse)
@@ -48,10 +54,12 @@ __all__ = [
     "PageCache", "bdlm_cache_write", "bdlm_cache_attn_fwd", "bdlm_cache_reserve", "bdlm_cache_fork",
     "bdlm_cache_compact", "bdlm_cache_write_workspace_bytes", "bdlm_cache_attn_fwd_workspace_bytes",
     "bdlm_cache_pages_workspace_bytes",
+    "bdlm_cache_prefixes", "bdlm_cache_prefixes_workspace_bytes", "bdlm_cache_attn_shared_fwd",
+    "bdlm_cache_attn_shared_fwd_workspace_bytes", "bdlm_sample", "bdlm_unmask", "bdlm_unmask_workspace_bytes",
 ]
 
 BDLM_OK = 0
-BDLM_BF16, BDLM_F32 = 0, 1
+BDLM_BF16, BDLM_F32, BDLM_F16 = 0, 1, 2
 PART_NONE, PART_KEY_WINDOW, PART_BLOCK_GROUP = 0, 1, 2
 PART_ACCUMULATE = 1
 
@@ -65,6 +73,9 @@ EXPORTED_SYMBOLS = (
     "bdlm_cache_write_workspace_bytes", "bdlm_cache_write", "bdlm_cache_attn_fwd_workspace_bytes",
     "bdlm_cache_attn_fwd", "bdlm_cache_pages_workspace_bytes", "bdlm_cache_reserve", "bdlm_cache_fork",
     "bdlm_cache_compact",
+    "bdlm_cache_prefixes_workspace_bytes", "bdlm_cache_prefixes",
+    "bdlm_cache_attn_shared_fwd_workspace_bytes", "bdlm_cache_attn_shared_fwd",
+    "bdlm_sample", "bdlm_unmask_workspace_bytes", "bdlm_unmask",
 )
 
 
@@ -131,6 +142,12 @@ class _CCache(ctypes.Structure):
                 ("n_layers", ctypes.c_int32), ("n_pages", ctypes.c_int32), ("page", ctypes.c_int32),
                 ("kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32), ("n_seqs", ctypes.c_int32),
                 ("max_pages", ctypes.c_int32), ("reserved", ctypes.c_int32)]
+
+
+class _CSampling(ctypes.Structure):
+    _fields_ = [("temperature", ctypes.c_void_p), ("top_k", ctypes.c_void_p), ("top_p", ctypes.c_void_p),
+                ("min_p", ctypes.c_void_p), ("temperature_all", ctypes.c_float), ("top_k_all", ctypes.c_int32),
+                ("top_p_all", ctypes.c_float), ("min_p_all", ctypes.c_float)]
 
 
 class _CTask(ctypes.Structure):
@@ -217,8 +234,19 @@ def load_library() -> ctypes.CDLL:
     lib.bdlm_cache_reserve.argtypes = [cache, vp, vp, sz, vp]
     lib.bdlm_cache_fork.argtypes = [cache, vp, vp, vp, i32, vp, sz, vp]
     lib.bdlm_cache_compact.argtypes = [cache, vp, vp, sz, vp]
+    lib.bdlm_cache_prefixes_workspace_bytes.argtypes = [i32]
+    lib.bdlm_cache_prefixes_workspace_bytes.restype = sz
+    lib.bdlm_cache_prefixes.argtypes = [cache, i64, vp, vp, vp, vp, sz, vp]
+    lib.bdlm_cache_attn_shared_fwd_workspace_bytes.argtypes = [i64, i32, i32, i32, i32]
+    lib.bdlm_cache_attn_shared_fwd_workspace_bytes.restype = sz
+    lib.bdlm_cache_attn_shared_fwd.argtypes = [cache, i32, vp, vp, vp, i64, i32, i32, vp, vp, vp, f32, i32, vp, sz, vp]
+    lib.bdlm_sample.argtypes = [vp, i32, i64, i32, i64, vp, ctypes.POINTER(_CSampling), vp, i32, vp, vp, vp]
+    lib.bdlm_unmask_workspace_bytes.argtypes = []
+    lib.bdlm_unmask_workspace_bytes.restype = sz
+    lib.bdlm_unmask.argtypes = [vp, vp, vp, i64, vp, i32, i32, vp, i32, vp, f32, vp, vp, vp, sz, vp]
     for f in (lib.bdlm_cache_write, lib.bdlm_cache_attn_fwd, lib.bdlm_cache_reserve, lib.bdlm_cache_fork,
-              lib.bdlm_cache_compact):
+              lib.bdlm_cache_compact, lib.bdlm_cache_prefixes, lib.bdlm_cache_attn_shared_fwd, lib.bdlm_sample,
+              lib.bdlm_unmask):
         f.restype = ctypes.c_int
     _lib = lib
     return lib
@@ -549,5 +577,8 @@ def bdlm_read_error(workspace: Optional[torch.Tensor], stream=None) -> int:
 
 
 from .cache import (  # noqa: E402  (needs the names above)
-    PageCache, bdlm_cache_attn_fwd, bdlm_cache_attn_fwd_workspace_bytes, bdlm_cache_compact, bdlm_cache_fork,
-    bdlm_cache_pages_workspace_bytes, bdlm_cache_reserve, bdlm_cache_write, bdlm_cache_write_workspace_bytes)
+    PageCache, bdlm_cache_attn_fwd, bdlm_cache_attn_fwd_workspace_bytes, bdlm_cache_attn_shared_fwd,
+    bdlm_cache_attn_shared_fwd_workspace_bytes, bdlm_cache_compact, bdlm_cache_fork, bdlm_cache_pages_workspace_bytes,
+    bdlm_cache_prefixes, bdlm_cache_prefixes_workspace_bytes, bdlm_cache_reserve, bdlm_cache_write,
+    bdlm_cache_write_workspace_bytes)
+from .sample import bdlm_sample, bdlm_unmask, bdlm_unmask_workspace_bytes  # noqa: E402

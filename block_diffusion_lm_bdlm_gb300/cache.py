@@ -9,6 +9,10 @@ block (decode.BlockDecoder does it):
   bdlm_cache_write(cache, k, v, cu, layer=i)        each layer, each denoising step
   bdlm_cache_attn_fwd(cache, q, cu, B, layer=i)     likewise
 
+Where sequences share pages (bdlm_cache_fork), bdlm_cache_prefixes finds once
+per block which do, and bdlm_cache_attn_shared_fwd takes the place of
+bdlm_cache_attn_fwd.
+
 Problems found on the device (malformed offsets or tables, too few pages) are
 written to the error word of the workspace: pass `workspace` and read it with
 bdlm_read_error(workspace), or pass check=True, which synchronises and raises.
@@ -47,7 +51,7 @@ class PageCache:
 
     __slots__ = ("k", "v", "k_scale", "v_scale", "table", "lens", "n_layers", "n_pages", "page", "kv_heads",
                  "head_dim", "n_seqs", "max_pages", "device", "index", "pages_bytes", "c", "ref", "home", "scratch", "lock",
-                 "need")
+                 "need", "need_shared")
 
     def __init__(self, k, v, k_scale, v_scale, table, lens):
         for nm, t, dt, dims in (("k", k, torch.float8_e4m3fn, 5), ("v", v, torch.float8_e4m3fn, 5),
@@ -76,7 +80,7 @@ class PageCache:
                          self.n_seqs, self.max_pages, 0)
         self.ref = ctypes.byref(self.c)
         self.home, self.scratch, self.lock = None, None, threading.Lock()
-        self.need = None, 0  # (rows, heads) of the last attention call, and the workspace that they need
+        self.need = self.need_shared = None, 0  # (rows, heads) of the last attention call, and the workspace that they need
 
     @staticmethod
     def empty(n_layers: int, n_pages: int, page: int, kv_heads: int, head_dim: int, n_seqs: int, max_pages: int,
@@ -96,6 +100,15 @@ def bdlm_cache_write_workspace_bytes() -> int:
 def bdlm_cache_attn_fwd_workspace_bytes(total_rows: int, heads: int, kv_heads: int, head_dim: int,
                                         n_seqs: int) -> int:
     return int(load_library().bdlm_cache_attn_fwd_workspace_bytes(total_rows, heads, kv_heads, head_dim, n_seqs))
+
+
+def bdlm_cache_attn_shared_fwd_workspace_bytes(total_rows: int, heads: int, kv_heads: int, head_dim: int,
+                                               n_seqs: int) -> int:
+    return int(load_library().bdlm_cache_attn_shared_fwd_workspace_bytes(total_rows, heads, kv_heads, head_dim, n_seqs))
+
+
+def bdlm_cache_prefixes_workspace_bytes(n_seqs: int) -> int:
+    return int(load_library().bdlm_cache_prefixes_workspace_bytes(n_seqs))
 
 
 def bdlm_cache_pages_workspace_bytes(n_pages: int, n_seqs: int) -> int:
@@ -206,20 +219,44 @@ def bdlm_cache_attn_fwd(cache: PageCache, q, cu_rows, block: int, *, layer: int 
     first row) the rows need not be in the cache, and the result is a partial
     one for bdlm_lse_merge. Rows of q behind cu_rows[-1] are left unwritten. T
     may be 0."""
+    return _attn("bdlm_cache_attn_fwd", cache, q, cu_rows, block, None, layer, q_pos, softmax_scale, out, lse, workspace,
+                 stream, check)
+
+
+def bdlm_cache_attn_shared_fwd(cache: PageCache, q, cu_rows, block: int, runs, *, layer: int = 0, q_pos=None,
+                               softmax_scale: float = 0.0, out=None, lse=None, workspace=None, stream=None,
+                               check: bool = False):
+    """bdlm_cache_attn_fwd in which what the sequences of a run share is read
+    once: `runs` (int32 [3, n_seqs]) comes from bdlm_cache_prefixes."""
+    _plan(cache, runs)
+    return _attn("bdlm_cache_attn_shared_fwd", cache, q, cu_rows, block, runs, layer, q_pos, softmax_scale, out, lse,
+                 workspace, stream, check)
+
+
+def _plan(cache, runs):
+    if not isinstance(runs, torch.Tensor) or runs.dtype != torch.int32 or not runs.is_contiguous() \
+            or runs.get_device() != cache.index or runs.shape != (3, cache.n_seqs):
+        raise ValueError(f"runs must be a contiguous int32 tensor [3, {cache.n_seqs}] on the cache's device")
+
+
+def _attn(name, cache, q, cu_rows, block, runs, layer, q_pos, softmax_scale, out, lse, workspace, stream, check):
     lib = load_library()
     _bf16_cuda("q", q)
     if q.dim() != 3 or q.shape[2] != cache.head_dim or q.get_device() != cache.index:
         raise ValueError(f"q must be [T, H, {cache.head_dim}] on the cache's device")
     T, H, d = q.shape
     if H == 0 or H % cache.kv_heads or not 0 < block < 2 ** 31:  # ctypes would take block modulo 2^32
-        _check(BDLM_ERR_INVALID_ARG, "bdlm_cache_attn_fwd")
+        _check(BDLM_ERR_INVALID_ARG, name)
     cu = _ints("cu_rows", cache, cu_rows, cache.n_seqs + 1)
     pos = None if q_pos is None else _ints("q_pos", cache, q_pos, cache.n_seqs)
     _layer(cache, layer)
-    sized, need = cache.need
+    sized, need = cache.need if runs is None else cache.need_shared
     if sized != (T, H):
-        need = max(lib.bdlm_cache_attn_fwd_workspace_bytes(T, H, cache.kv_heads, d, cache.n_seqs), 256)
-        cache.need = (T, H), need
+        need = max(getattr(lib, name + "_workspace_bytes")(T, H, cache.kv_heads, d, cache.n_seqs), 256)
+        if runs is None:
+            cache.need = (T, H), need
+        else:
+            cache.need_shared = (T, H), need
     handle, here = _on(cache, stream)
     with here:
         if out is None:
@@ -233,16 +270,17 @@ def bdlm_cache_attn_fwd(cache: PageCache, q, cu_rows, block: int, *, layer: int 
                 or not lse.is_contiguous():
             raise ValueError("lse must be a contiguous fp32 CUDA tensor [H, T]")
         if T == 0:
-            _no_rows(cache, cu_rows, workspace, handle, check, "bdlm_cache_attn_fwd")
+            _no_rows(cache, cu_rows, workspace, handle, check, name)
             return out, lse
         with cache.lock:
             ws = _workspace(cache, workspace, need, handle, check or stream is not None)
-            st = lib.bdlm_cache_attn_fwd(cache.ref, layer, q.data_ptr(), out.data_ptr(), lse.data_ptr(), T, H, block, cu,
-                                         pos, softmax_scale, BDLM_F32 if out.dtype == torch.float32 else BDLM_BF16,
-                                         ws.data_ptr(), ws.numel(), handle)
-        _check(st, "bdlm_cache_attn_fwd")
+            plan = () if runs is None else (runs.data_ptr(),)
+            st = getattr(lib, name)(cache.ref, layer, q.data_ptr(), out.data_ptr(), lse.data_ptr(), T, H, block, cu, pos,
+                                    *plan, softmax_scale, BDLM_F32 if out.dtype == torch.float32 else BDLM_BF16,
+                                    ws.data_ptr(), ws.numel(), handle)
+        _check(st, name)
         if check:
-            _read(lib, ws, handle, "bdlm_cache_attn_fwd")
+            _read(lib, ws, handle, name)
     return out, lse
 
 
@@ -291,3 +329,29 @@ def bdlm_cache_compact(cache: PageCache, *, workspace=None, stream=None, check: 
     (int32 [1], on the device). Pages from there on are free afterwards."""
     return _pages_call(cache, "bdlm_cache_compact", (), workspace, stream, check,
                        make=lambda: torch.zeros(1, dtype=torch.int32, device=cache.device))
+
+
+def bdlm_cache_prefixes(cache: PageCache, cu_rows, *, total_rows: int | None = None, q_pos=None, out=None, workspace=None,
+                        stream=None, check: bool = False) -> torch.Tensor:
+    """The runs of sequences that share leading pages (int32 [3, n_seqs]: first
+    sequence, number behind the last one, shared positions), for
+    bdlm_cache_attn_shared_fwd. They hold for all layers until the table, the
+    lengths or the rows change. total_rows bounds the offsets (None: any)."""
+    lib = load_library()
+    n = cache.n_seqs
+    cu = _ints("cu_rows", cache, cu_rows, n + 1)
+    pos = None if q_pos is None else _ints("q_pos", cache, q_pos, n)
+    if out is not None:
+        _plan(cache, out)
+    handle, here = _on(cache, stream)
+    with here:
+        if out is None:
+            out = torch.empty((3, n), dtype=torch.int32, device=cache.device)
+        with cache.lock:
+            ws = _workspace(cache, workspace, 256 + 4 * n, handle, check or stream is not None)
+            st = lib.bdlm_cache_prefixes(cache.ref, 2 ** 30 if total_rows is None else total_rows, cu, pos, out.data_ptr(),
+                                         ws.data_ptr(), ws.numel(), handle)
+        _check(st, "bdlm_cache_prefixes")
+        if check:
+            _read(lib, ws, handle, "bdlm_cache_prefixes")
+    return out

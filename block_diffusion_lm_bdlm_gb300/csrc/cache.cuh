@@ -93,6 +93,17 @@ struct CacheAttnArgs {
     float scale_log2;  // softmax scale * log2(e)
     WsHeader* hdr;
     uint8_t* scratch;  // behind the header
+    const int* runs;   // int32 [3, n_seqs]: sequences that share pages (nullptr: each reads its own)
+    float* planes;     // with runs: fp32 partial results, see cache_attn.cuh
+};
+struct CachePrefixArgs {
+    CacheView c;
+    const int* cu_rows;
+    const int* q_pos;
+    int total_rows;
+    int* runs;  // [3, n_seqs]
+    WsHeader* hdr;
+    int* scratch;  // [n_seqs]
 };
 enum PageOp : int { PAGES_RESERVE = 0, PAGES_FORK = 1, PAGES_COMPACT = 2 };
 struct CachePagesArgs {
@@ -109,10 +120,15 @@ struct CachePagesArgs {
 };
 
 size_t cache_attn_scratch_bytes(long long total_rows, int H, int Hk, int D, int n_seqs);
+size_t cache_attn_plane_bytes(long long total_rows, int H, int D);
 size_t cache_pages_scratch_bytes(int n_pages, int n_seqs);
 cudaError_t launch_cache_write(const CacheWriteArgs& a, int num_sms, cudaStream_t st, int* launches);
 cudaError_t launch_cache_attn(const CacheAttnArgs& a, int num_sms, cudaStream_t st, int* launches);
 cudaError_t launch_cache_pages(const CachePagesArgs& a, int num_sms, cudaStream_t st, int* launches);
+
+size_t cache_prefixes_scratch_bytes(int n_seqs);
+int cache_prefixes_most_seqs();
+cudaError_t launch_cache_prefixes(const CachePrefixArgs& a, cudaStream_t st, int* launches);
 
 int device_sms();
 void set_last_launches(int n);

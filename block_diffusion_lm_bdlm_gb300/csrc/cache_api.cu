@@ -85,6 +85,49 @@ int run_pages(const CachePagesArgs& args, void* workspace, size_t workspace_byte
     return BDLM_OK;
 }
 
+// Checks the arguments that the attention calls have in common and fills the kernels'.
+int attn_args(const bdlm_cache* cache, int layer, const void* q, void* o, float* lse, int64_t total_rows, int heads, int block,
+              const int32_t* cu_rows, const int32_t* q_pos, float softmax_scale, int o_dtype, CacheAttnArgs* a) {
+    const int st = view_of(cache, layer, &a->c);
+    if (st != BDLM_OK) return st;
+    if (!good_ptr(q, 16) || !good_ptr(o, 16) || !good_ptr(lse, 4) || !good_ptr(cu_rows, 4) || !aligned(q_pos, 4))
+        return BDLM_ERR_INVALID_ARG;
+    if (total_rows <= 0 || total_rows > kMaxRows || heads <= 0 || heads % cache->kv_heads != 0 || block <= 0)
+        return BDLM_ERR_INVALID_ARG;
+    if ((long long)total_rows * (heads / cache->kv_heads) > kMaxRows) return BDLM_ERR_INVALID_ARG;
+    if (o_dtype != BDLM_BF16 && o_dtype != BDLM_F32) return BDLM_ERR_INVALID_ARG;
+    a->q = static_cast<const __nv_bfloat16*>(q);
+    a->o = o_dtype == BDLM_F32 ? nullptr : static_cast<__nv_bfloat16*>(o);
+    a->o_f32 = o_dtype == BDLM_F32 ? static_cast<float*>(o) : nullptr;
+    a->lse = lse;
+    a->cu_rows = cu_rows;
+    a->q_pos = q_pos;
+    a->total_rows = (int)total_rows;
+    a->H = heads;
+    a->G = heads / cache->kv_heads;
+    a->block = block;
+    a->scale_log2 = (softmax_scale > 0.f ? softmax_scale : 1.0f / std::sqrt((float)cache->head_dim)) * 1.4426950408889634f;
+    return BDLM_OK;
+}
+
+// The workspace holds the header, with runs the two planes, and the shares' records and slots.
+int run_attn(CacheAttnArgs& a, void* workspace, size_t workspace_bytes, size_t need, bdlm_stream_t stream) {
+    const int st = check_workspace(workspace, workspace_bytes, need);
+    if (st != BDLM_OK) return st;
+    a.hdr = static_cast<WsHeader*>(workspace);
+    a.scratch = static_cast<uint8_t*>(workspace) + sizeof(WsHeader);
+    if (a.runs) {
+        a.planes = reinterpret_cast<float*>(a.scratch);
+        a.scratch += cache_attn_plane_bytes(a.total_rows, a.H, a.c.D);
+    }
+    const int sms = device_sms();
+    int launches = 0;
+    if (sms <= 0 || launch_cache_attn(a, sms, reinterpret_cast<cudaStream_t>(stream), &launches) != cudaSuccess)
+        return BDLM_ERR_CUDA;
+    set_last_launches(launches);
+    return BDLM_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -128,35 +171,61 @@ int bdlm_cache_attn_fwd(const bdlm_cache* cache, int32_t layer, const void* q, v
                         bdlm_stream_t stream) {
     set_last_launches(0);
     CacheAttnArgs a{};
-    int st = view_of(cache, layer, &a.c);
+    const int st = attn_args(cache, layer, q, o, lse, total_rows, heads, block, cu_rows, q_pos, softmax_scale, o_dtype, &a);
     if (st != BDLM_OK) return st;
-    if (!good_ptr(q, 16) || !good_ptr(o, 16) || !good_ptr(lse, 4) || !good_ptr(cu_rows, 4) || !aligned(q_pos, 4))
-        return BDLM_ERR_INVALID_ARG;
-    if (total_rows <= 0 || total_rows > kMaxRows || heads <= 0 || heads % cache->kv_heads != 0 || block <= 0)
-        return BDLM_ERR_INVALID_ARG;
-    if ((long long)total_rows * (heads / cache->kv_heads) > kMaxRows) return BDLM_ERR_INVALID_ARG;
-    if (o_dtype != BDLM_BF16 && o_dtype != BDLM_F32) return BDLM_ERR_INVALID_ARG;
-    st = check_workspace(workspace, workspace_bytes,
-                         bdlm_cache_attn_fwd_workspace_bytes(total_rows, heads, cache->kv_heads, cache->head_dim,
-                                                             cache->n_seqs));
+    return run_attn(a, workspace, workspace_bytes,
+                    bdlm_cache_attn_fwd_workspace_bytes(total_rows, heads, cache->kv_heads, cache->head_dim, cache->n_seqs), stream);
+}
+
+size_t bdlm_cache_attn_shared_fwd_workspace_bytes(int64_t total_rows, int32_t heads, int32_t kv_heads, int32_t head_dim,
+                                                  int32_t n_seqs) {
+    const size_t alone = bdlm_cache_attn_fwd_workspace_bytes(total_rows, heads, kv_heads, head_dim, n_seqs);
+    return alone ? cache_attn_plane_bytes(total_rows, heads, head_dim) + alone : 0;
+}
+
+int bdlm_cache_attn_shared_fwd(const bdlm_cache* cache, int32_t layer, const void* q, void* o, float* lse,
+                               int64_t total_rows, int32_t heads, int32_t block, const int32_t* cu_rows,
+                               const int32_t* q_pos, const int32_t* runs, float softmax_scale, int32_t o_dtype,
+                               void* workspace, size_t workspace_bytes, bdlm_stream_t stream) {
+    set_last_launches(0);
+    CacheAttnArgs a{};
+    const int st = attn_args(cache, layer, q, o, lse, total_rows, heads, block, cu_rows, q_pos, softmax_scale, o_dtype, &a);
     if (st != BDLM_OK) return st;
-    a.q = static_cast<const __nv_bfloat16*>(q);
-    a.o = o_dtype == BDLM_F32 ? nullptr : static_cast<__nv_bfloat16*>(o);
-    a.o_f32 = o_dtype == BDLM_F32 ? static_cast<float*>(o) : nullptr;
-    a.lse = lse;
+    if (!good_ptr(runs, 4)) return BDLM_ERR_INVALID_ARG;
+    a.runs = runs;
+    return run_attn(a, workspace, workspace_bytes,
+                    bdlm_cache_attn_shared_fwd_workspace_bytes(total_rows, heads, cache->kv_heads, cache->head_dim,
+                                                               cache->n_seqs), stream);
+}
+
+size_t bdlm_cache_prefixes_workspace_bytes(int32_t n_seqs) {
+    if (n_seqs < 1 || n_seqs > cache_prefixes_most_seqs()) return 0;
+    return sizeof(WsHeader) + cache_prefixes_scratch_bytes(n_seqs);
+}
+
+int bdlm_cache_prefixes(const bdlm_cache* cache, int64_t total_rows, const int32_t* cu_rows, const int32_t* q_pos,
+                        int32_t* runs, void* workspace, size_t workspace_bytes, bdlm_stream_t stream) {
+    set_last_launches(0);
+    CachePrefixArgs a{};
+    int st = view_of(cache, 0, &a.c);
+    if (st != BDLM_OK) return st;
+    if (!good_ptr(cu_rows, 4) || !aligned(q_pos, 4) || !good_ptr(runs, 4)) return BDLM_ERR_INVALID_ARG;
+    if (total_rows < 0 || total_rows > kMaxRows) return BDLM_ERR_INVALID_ARG;
+    const size_t n = a.c.n_seqs;
+    if (in_table(a.c, runs, 3 * n) || in_lens(a.c, runs, 3 * n) || overlap(runs, 12 * n, cu_rows, 4 * (n + 1)) ||
+        overlap(runs, 12 * n, q_pos, 4 * n))
+        return BDLM_ERR_INVALID_ARG;
+    if (a.c.n_seqs > cache_prefixes_most_seqs()) return BDLM_ERR_UNSUPPORTED;
+    st = check_workspace(workspace, workspace_bytes, bdlm_cache_prefixes_workspace_bytes(a.c.n_seqs));
+    if (st != BDLM_OK) return st;
     a.cu_rows = cu_rows;
     a.q_pos = q_pos;
     a.total_rows = (int)total_rows;
-    a.H = heads;
-    a.G = heads / cache->kv_heads;
-    a.block = block;
-    a.scale_log2 = (softmax_scale > 0.f ? softmax_scale : 1.0f / std::sqrt((float)cache->head_dim)) * 1.4426950408889634f;
+    a.runs = runs;
     a.hdr = static_cast<WsHeader*>(workspace);
-    a.scratch = static_cast<uint8_t*>(workspace) + sizeof(WsHeader);
-    const int sms = device_sms();
+    a.scratch = reinterpret_cast<int*>(static_cast<uint8_t*>(workspace) + sizeof(WsHeader));
     int launches = 0;
-    if (sms <= 0 || launch_cache_attn(a, sms, reinterpret_cast<cudaStream_t>(stream), &launches) != cudaSuccess)
-        return BDLM_ERR_CUDA;
+    if (launch_cache_prefixes(a, reinterpret_cast<cudaStream_t>(stream), &launches) != cudaSuccess) return BDLM_ERR_CUDA;
     set_last_launches(launches);
     return BDLM_OK;
 }

@@ -24,7 +24,7 @@ constexpr int kMergeThreads = 256;
 constexpr int kSlices = 3;
 constexpr int kMaxParts = kMaxCtas + 1;
 
-template <int D>
+template <int D, bool RUNS>
 __global__ void __launch_bounds__(kMergeThreads) cache_merge_kernel(const CacheAttnArgs a, int ctas) {
     __shared__ float s_w[kMaxParts][32];  // weights of 32 rows at a time
     __shared__ float s_lse[32];
@@ -62,6 +62,9 @@ __global__ void __launch_bounds__(kMergeThreads) cache_merge_kernel(const CacheA
     const int slices = (c1 - c0 + 1) * kSlices, slice = (c - c0) * kSlices + blockIdx.y;
     const int lo = rows * slice / slices, hi = rows * (slice + 1) / slices;
     const int R = slot_rows(a.total_rows, a.G);
+    const bool plane = RUNS && r.part != PART_WHOLE;
+    float* o_f32 = plane ? plane_o(a, D, r.part) : a.o_f32;
+    float* lse = plane ? plane_lse(a, D, r.part) : a.lse;
     auto slot = [&](int p) { return slot_at(a.scratch, p == 0 ? 2 * (c0 - 1) + 1 : 2 * (c0 - 1 + p), R, D); };
     for (int i0 = lo; i0 < hi; i0 += 32) {
         const int n = imin(32, hi - i0);
@@ -115,9 +118,9 @@ __global__ void __launch_bounds__(kMergeThreads) cache_merge_kernel(const CacheA
             }
             const int m = r.m0 + i0 + k, row = r.row0 + m / a.G, h = r.head * a.G + m % a.G;
             const long long at = ((long long)row * a.H + h) * D + 8 * q;
-            if (a.o_f32) {
-                *reinterpret_cast<float4*>(a.o_f32 + at) = make_float4(o[0], o[1], o[2], o[3]);
-                *reinterpret_cast<float4*>(a.o_f32 + at + 4) = make_float4(o[4], o[5], o[6], o[7]);
+            if (o_f32) {
+                *reinterpret_cast<float4*>(o_f32 + at) = make_float4(o[0], o[1], o[2], o[3]);
+                *reinterpret_cast<float4*>(o_f32 + at + 4) = make_float4(o[4], o[5], o[6], o[7]);
             } else {
                 uint32_t b[4];
 #pragma unroll
@@ -127,13 +130,66 @@ __global__ void __launch_bounds__(kMergeThreads) cache_merge_kernel(const CacheA
                 }
                 *reinterpret_cast<uint4*>(a.o + at) = make_uint4(b[0], b[1], b[2], b[3]);
             }
-            if (q == 0) a.lse[(long long)h * a.total_rows + row] = s_lse[k];
+            if (q == 0) lse[(long long)h * a.total_rows + row] = s_lse[k];
         }
         __syncthreads();
     }
 }
 
+// Joins the two planes for the rows of runs: a thread takes eight columns of a
+// (row, head). blockIdx.x is the sequence, blockIdx.y a run of its (row, head)s.
+// Bound by what it moves, 8 bytes a value read and 2 written, most of it out of L2.
+constexpr int kJoinThreads = 256;
+
+template <int D>
+__global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const CacheAttnArgs a) {
+    asm volatile("griddepcontrol.wait;" ::: "memory");
+    if (share_recs(a.scratch)[0].bad) return;
+    const int n = a.c.n_seqs, s = blockIdx.x;
+    if (__ldg(a.runs + 2 * (long long)n + s) == 0) return;
+    const int row0 = __ldg(a.cu_rows + s), rows = __ldg(a.cu_rows + s + 1) - row0;
+    constexpr int PER = D / 8;
+    const int c = threadIdx.x % PER;
+    const long long all = (long long)rows * a.H, step = (long long)gridDim.y * (kJoinThreads / PER);
+    for (long long i = (long long)blockIdx.y * (kJoinThreads / PER) + threadIdx.x / PER; i < all; i += step) {
+        const int h = (int)(i % a.H), row = row0 + (int)(i / a.H);
+        const long long at = ((long long)row * a.H + h) * D + 8 * c, al = (long long)h * a.total_rows + row;
+        const float l0 = __ldcg(plane_lse(a, D, PART_SHARED) + al), l1 = __ldcg(plane_lse(a, D, PART_OWN) + al);
+        const float4* p0 = reinterpret_cast<const float4*>(plane_o(a, D, PART_SHARED) + at);
+        const float4* p1 = reinterpret_cast<const float4*>(plane_o(a, D, PART_OWN) + at);
+        const float4 x0 = __ldcg(p0), x1 = __ldcg(p0 + 1), y0 = __ldcg(p1), y1 = __ldcg(p1 + 1);
+        const float mx = fmaxf(l0, l1);
+        const bool nan = l0 != l0 || l1 != l1;
+        float w0 = l0 == -INFINITY ? 0.f : expf(l0 - mx), w1 = l1 == -INFINITY ? 0.f : expf(l1 - mx);
+        const float z = w0 + w1, inv = nan ? NAN : z > 0.f ? 1.f / z : 0.f;
+        w0 *= inv;
+        w1 *= inv;
+        const float x[8] = {x0.x, x0.y, x0.z, x0.w, x1.x, x1.y, x1.z, x1.w}, y[8] = {y0.x, y0.y, y0.z, y0.w, y1.x, y1.y, y1.z, y1.w};
+        float o[8];
+#pragma unroll
+        for (int e = 0; e < 8; ++e)  // a part that sees no key holds zeros; a weight of 0 does not hide a NaN
+            o[e] = fmaf(w0, x[e], w1 * y[e]);
+        if (a.o_f32) {
+            *reinterpret_cast<float4*>(a.o_f32 + at) = make_float4(o[0], o[1], o[2], o[3]);
+            *reinterpret_cast<float4*>(a.o_f32 + at + 4) = make_float4(o[4], o[5], o[6], o[7]);
+        } else {
+            uint32_t b[4];
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                const __nv_bfloat162 v = __floats2bfloat162_rn(o[2 * e], o[2 * e + 1]);
+                b[e] = *reinterpret_cast<const uint32_t*>(&v);
+            }
+            *reinterpret_cast<uint4*>(a.o + at) = make_uint4(b[0], b[1], b[2], b[3]);
+        }
+        if (c == 0) a.lse[al] = nan ? NAN : z > 0.f ? mx + logf(z) : -INFINITY;
+    }
+}
+
 }  // namespace
+
+size_t cache_attn_plane_bytes(long long total_rows, int H, int D) {
+    return (sizeof(float) * 2 * (size_t)total_rows * H * (D + 1) + 255) / 256 * 256;
+}
 
 size_t cache_attn_scratch_bytes(long long total_rows, int H, int Hk, int D, int) {
     const int rows = slot_rows(total_rows, H / Hk);
@@ -142,7 +198,11 @@ size_t cache_attn_scratch_bytes(long long total_rows, int H, int Hk, int D, int)
 
 cudaError_t launch_cache_attn(const CacheAttnArgs& a, int num_sms, cudaStream_t st, int* launches) {
     const int ctas = num_sms < kMaxCtas ? num_sms : kMaxCtas;
-    cudaError_t e = a.c.D == 128 ? launch_cache_attn_d128(a, ctas, st) : launch_cache_attn_d64(a, ctas, st);
+    cudaError_t e;
+    if (a.runs)
+        e = a.c.D == 128 ? launch_cache_attn_runs_d128(a, ctas, st) : launch_cache_attn_runs_d64(a, ctas, st);
+    else
+        e = a.c.D == 128 ? launch_cache_attn_d128(a, ctas, st) : launch_cache_attn_d64(a, ctas, st);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(ctas > 1 ? ctas - 1 : 1), kSlices);
@@ -153,9 +213,21 @@ cudaError_t launch_cache_attn(const CacheAttnArgs& a, int num_sms, cudaStream_t 
     at.val.programmaticStreamSerializationAllowed = 1;
     cfg.attrs = &at;
     cfg.numAttrs = 1;
-    e = a.c.D == 128 ? cudaLaunchKernelEx(&cfg, cache_merge_kernel<128>, a, ctas)
-                      : cudaLaunchKernelEx(&cfg, cache_merge_kernel<64>, a, ctas);
-    if (e == cudaSuccess) *launches += 2;
+    if (a.runs)
+        e = a.c.D == 128 ? cudaLaunchKernelEx(&cfg, cache_merge_kernel<128, true>, a, ctas)
+                          : cudaLaunchKernelEx(&cfg, cache_merge_kernel<64, true>, a, ctas);
+    else
+        e = a.c.D == 128 ? cudaLaunchKernelEx(&cfg, cache_merge_kernel<128, false>, a, ctas)
+                          : cudaLaunchKernelEx(&cfg, cache_merge_kernel<64, false>, a, ctas);
+    if (e != cudaSuccess) return e;
+    *launches += 2;
+    if (!a.runs) return cudaSuccess;
+    const int per = kJoinThreads / (a.c.D / 8), n = a.c.n_seqs;
+    const long long most = ((long long)a.total_rows * a.H + per - 1) / per, fill = (4LL * num_sms + n - 1) / n;
+    cfg.gridDim = dim3((unsigned)n, (unsigned)(most < fill ? most : fill));
+    cfg.blockDim = dim3(kJoinThreads);
+    e = a.c.D == 128 ? cudaLaunchKernelEx(&cfg, cache_join_kernel<128>, a) : cudaLaunchKernelEx(&cfg, cache_join_kernel<64>, a);
+    if (e == cudaSuccess) *launches += 1;
     return e;
 }
 

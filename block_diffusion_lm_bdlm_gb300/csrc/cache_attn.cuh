@@ -12,6 +12,14 @@
 // between the tiles of a unit leaves a partial result; at most two per CTA,
 // slot 2 c for a unit begun by an earlier CTA and slot 2 c + 1 for one that a
 // later CTA goes on with.
+//
+// With runs (a.runs) the same is done over items instead of sequences. Item
+// 2 s is the pages that a run led by sequence s shares, read by the rows of
+// all of the run's sequences (they lie side by side) as if they were one
+// sequence's; item 2 s + 1 is what sequence s reads alone. Rows of a run get
+// two partial results, one of each kind, in two planes (o fp32 [T, H, d] twice,
+// then lse fp32 [H, T] twice), which are joined at the end. They lie in rows'
+// order, so that units of either kind may be cut anywhere.
 #pragma once
 
 #include "cache.cuh"
@@ -40,7 +48,8 @@ struct ShareRec {
     long long per;              // share_begin's constants
     int more, C;                // C: shares
     int error, info;
-    int pad[2];
+    int part;  // of the unit: Rows::part
+    int bad;   // malformed arguments: nothing was computed
 };
 static_assert(sizeof(ShareRec) == 64, "share record is 64 bytes");
 
@@ -61,6 +70,77 @@ __device__ __forceinline__ float* slot_at(uint8_t* scratch, int slot, int rows, 
 // Where share c of C begins; per = W / C, more = W % C.
 __device__ __forceinline__ long long share_begin(long long per, int more, int c) { return per * c + imin(c, more); }
 
+// The rows of an item, and the keys that they read: those of `seq` at
+// positions [key0, len) that each row sees.
+struct Rows : SeqRows {
+    int seq;
+    int key0;
+    int part;  // where results go: 0 to o and lse, 1 and 2 into the first and second plane
+};
+enum : int { PART_WHOLE = 0, PART_SHARED = 1, PART_OWN = 2 };
+
+// What the run of sequence s is, and whether it is well-formed: all of its
+// sequences name the same one, and share no more than each of their rows sees.
+struct Run {
+    int first, end, shared;
+    bool ok;
+};
+__device__ __forceinline__ Run run_of(const CacheAttnArgs& a, int s, const SeqRows& r) {
+    const int n = a.c.n_seqs;
+    const int *f = a.runs, *e = a.runs + n, *h = a.runs + 2 * (long long)n;
+    Run u{__ldg(f + s), __ldg(e + s), __ldg(h + s), true};
+    u.ok = u.first >= 0 && u.first <= s && u.end > s && u.end <= n && u.shared >= 0 && (u.shared & (a.c.page - 1)) == 0;
+    if (u.ok && u.first < s) u.ok = __ldg(f + s - 1) == u.first && __ldg(e + s - 1) == u.end && __ldg(h + s - 1) == u.shared;
+    if (u.ok && u.end > s + 1) u.ok = __ldg(f + s + 1) == u.first && __ldg(e + s + 1) == u.end && __ldg(h + s + 1) == u.shared;
+    if (u.shared > 0 && (s == u.first || r.rows > 0)) u.ok = u.ok && u.shared <= r.len && (r.rows == 0 || u.shared <= r.pos0);
+    return u;
+}
+
+template <bool RUNS>
+__device__ __forceinline__ int items_of(const CacheAttnArgs& a) { return RUNS ? 2 * a.c.n_seqs : a.c.n_seqs; }
+
+template <bool RUNS>
+__device__ __forceinline__ Rows item_rows(const CacheAttnArgs& a, int item) {
+    Rows r;
+    r.seq = RUNS ? item >> 1 : item;
+    static_cast<SeqRows&>(r) = seq_rows(a.c, a.cu_rows, a.q_pos, a.total_rows, r.seq);
+    r.key0 = 0;
+    r.part = PART_WHOLE;
+    if (RUNS) {
+        const Run u = run_of(a, r.seq, r);
+        r.ok = r.ok && u.ok;
+        if (item & 1) {
+            if (u.shared > 0) {
+                r.key0 = u.shared;
+                r.part = PART_OWN;
+            }
+        } else if (!r.ok || u.shared == 0 || u.first != r.seq) {
+            r.rows = 0;
+        } else {
+            const int b = __ldg(a.cu_rows + u.end);
+            r.ok = b >= r.row0 && b <= a.total_rows;
+            r.rows = r.ok ? b - r.row0 : 0;
+            r.len = u.shared;
+            r.pos0 = u.shared - 1;  // the first row sees them all, and so do the others
+            r.part = PART_SHARED;
+        }
+    }
+    return r;
+}
+
+// Keys of its item that the row at position p sees.
+template <bool RUNS, typename T>
+__device__ __forceinline__ int keys_of(const CacheAttnArgs& a, const T& r, int p) {
+    return key_end(r.len, a.block, p) - (RUNS ? r.key0 : 0);
+}
+
+__device__ __forceinline__ float* plane_o(const CacheAttnArgs& a, int D, int part) {
+    return a.planes + (long long)(part - 1) * a.total_rows * a.H * D;
+}
+__device__ __forceinline__ float* plane_lse(const CacheAttnArgs& a, int D, int part) {
+    return a.planes + ((long long)2 * D + (part - 1)) * a.total_rows * a.H;
+}
+
 struct Unit {
     int last;   // last flat row + 1
     int end;    // keys that the last row sees
@@ -71,10 +151,11 @@ struct Unit {
 };
 __device__ __forceinline__ int is_two(int rows) { return rows > kUnitRows / 2; }
 __device__ __forceinline__ int lead_of(int rows) { return kLead + ((rows + 31) >> (5 + is_two(rows))); }
-__device__ __forceinline__ Unit unit_of(const CacheAttnArgs& a, const SeqRows& r, int m0) {
+template <bool RUNS>
+__device__ __forceinline__ Unit unit_of(const CacheAttnArgs& a, const Rows& r, int m0) {
     Unit u;
     u.last = imin(r.rows * a.G, m0 + kUnitRows);
-    u.end = key_end(r.len, a.block, r.pos0 + (u.last - 1) / a.G);
+    u.end = keys_of<RUNS>(a, r, r.pos0 + (u.last - 1) / a.G);
     u.tiles = imax(1, (u.end + kTileKeys - 1) / kTileKeys);
     u.two = is_two(u.last - m0);
     u.lead = lead_of(u.last - m0);
@@ -87,5 +168,7 @@ __device__ __forceinline__ int tile_at(int off, int two, int lead) { return imax
 
 cudaError_t launch_cache_attn_d64(const CacheAttnArgs& a, int ctas, cudaStream_t st);
 cudaError_t launch_cache_attn_d128(const CacheAttnArgs& a, int ctas, cudaStream_t st);
+cudaError_t launch_cache_attn_runs_d64(const CacheAttnArgs& a, int ctas, cudaStream_t st);
+cudaError_t launch_cache_attn_runs_d128(const CacheAttnArgs& a, int ctas, cudaStream_t st);
 
 }  // namespace bdlm

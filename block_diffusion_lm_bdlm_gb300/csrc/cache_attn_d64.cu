@@ -2,5 +2,5 @@
 #include "cache_attn_tc.cuh"
 
 namespace bdlm {
-cudaError_t launch_cache_attn_d64(const CacheAttnArgs& a, int ctas, cudaStream_t st) { return cattn::launch_d<64>(a, ctas, st); }
+cudaError_t launch_cache_attn_d64(const CacheAttnArgs& a, int ctas, cudaStream_t st) { return cattn::launch_d<64, false>(a, ctas, st); }
 }  // namespace bdlm

@@ -77,6 +77,7 @@ static_assert(8 * kRegsSoftmax + 8 * kRegsOther <= 16 * 128, "registers");
 constexpr int kTmemCols = 512;
 constexpr int kStages = 3;  // of K; V has two as e4m3 and two as fp16
 constexpr int kScaleSlots = 6;
+constexpr int kPlaceBytes = 144;
 constexpr uint64_t kTimeoutNs = 2000000000ull;
 
 // Barriers. Tiles are numbered through the CTA's share; t is a tile's number.
@@ -107,7 +108,7 @@ struct Smem {
     static constexpr int kStart = kWords + 16;                    // Start
     static constexpr int kQExp = kStart + 64;                     // uint8 [256]: exponent of the rows' scale
     static constexpr int kPlace = kQExp + kUnitRows;              // Place of each warp
-    static constexpr int kBytes = kPlace + (kThreads / 32) * 128;
+    static constexpr int kBytes = kPlace + (kThreads / 32) * kPlaceBytes;
 };
 static_assert(Smem<128>::kBytes <= 232448, "shared memory");
 
@@ -123,20 +124,22 @@ struct Seg {
     int row0, pos0, len;  // the sequence
     int s, h, m0, last, end;
     int kt0, kt1;
+    int key0, part;  // with runs (Rows)
     bool two, whole;
     __device__ __forceinline__ int tiles() const { return end ? kt1 - kt0 : 0; }
 };
 
 struct Place {
-    SeqRows r;
+    Rows r;
     Unit u;
     int s, h, m0, off;
     long long left;
     Seg g;  // the present run
 };
-static_assert(sizeof(Place) <= 128, "");
+static_assert(sizeof(Place) <= kPlaceBytes && kPlaceBytes % 16 == 0, "");
 
 // Both are called by whole warps; the warp's lanes write the same values.
+template <bool RUNS>
 __device__ __forceinline__ void begin_share(const CacheAttnArgs& a, const Start& st, Place* p) {
     p->s = st.s;
     p->h = st.h;
@@ -144,12 +147,13 @@ __device__ __forceinline__ void begin_share(const CacheAttnArgs& a, const Start&
     p->off = st.off;
     p->left = st.left;
     if (st.left > 0) {
-        p->r = seq_rows(a.c, a.cu_rows, a.q_pos, a.total_rows, st.s);
-        p->u = unit_of(a, p->r, st.m0);
+        p->r = item_rows<RUNS>(a, st.s);
+        p->u = unit_of<RUNS>(a, p->r, st.m0);
     }
     __syncwarp();
 }
 // The next run of tiles, into p->g; false behind the last.
+template <bool RUNS>
 __device__ __forceinline__ bool next_run(const CacheAttnArgs& a, Place* p) {
     __syncwarp();
     long long left = p->left;
@@ -159,10 +163,12 @@ __device__ __forceinline__ bool next_run(const CacheAttnArgs& a, Place* p) {
         const int off = p->off, c = u.cost(), n = left < c - off ? (int)left : c - off;
         const int kt0 = tile_at(off, u.two, u.lead), kt1 = tile_at(off + n, u.two, u.lead);
         int s = p->s, h = p->h, m0 = p->m0;
-        SeqRows r = p->r;
+        Rows r = p->r;
         found = kt1 > kt0;
         __syncwarp();
-        if (found) p->g = Seg{r.row0, r.pos0, r.len, s, h, m0, u.last, u.end, kt0, kt1, u.two != 0, kt0 == 0 && kt1 == u.tiles};
+        if (found) {
+            p->g = Seg{r.row0, r.pos0, r.len, RUNS ? r.seq : s, h, m0, u.last, u.end, kt0, kt1, r.key0, r.part, u.two != 0, kt0 == 0 && kt1 == u.tiles};
+        }
         left -= n;
         if (left > 0) {  // the unit is done
             m0 += kUnitRows;
@@ -170,7 +176,7 @@ __device__ __forceinline__ bool next_run(const CacheAttnArgs& a, Place* p) {
                 m0 = 0;
                 if (++h == a.c.Hk) {
                     h = 0;
-                    do r = seq_rows(a.c, a.cu_rows, a.q_pos, a.total_rows, ++s);
+                    do r = item_rows<RUNS>(a, ++s);
                     while (r.rows == 0);
                     p->r = r;
                     p->s = s;
@@ -179,7 +185,7 @@ __device__ __forceinline__ bool next_run(const CacheAttnArgs& a, Place* p) {
             }
             p->m0 = m0;
             p->off = 0;
-            p->u = unit_of(a, r, m0);
+            p->u = unit_of<RUNS>(a, r, m0);
         }
         p->left = left;
         __syncwarp();
@@ -310,7 +316,7 @@ struct Ctx {
     }
     // The warp's place in the share. It lies in shared memory: every lane of a warp has the same, it changes once per
     // unit, and registers that hold it through the tile loops would be spilled, to an L1 that has next to no room.
-    static __device__ __forceinline__ Place* place() { return reinterpret_cast<Place*>(g_smem + L::kPlace + (threadIdx.x >> 5) * 128); }
+    static __device__ __forceinline__ Place* place() { return reinterpret_cast<Place*>(g_smem + L::kPlace + (threadIdx.x >> 5) * kPlaceBytes); }
 };
 
 // ------------------------------------------------------------ share's begin
@@ -337,21 +343,23 @@ __device__ __forceinline__ long long cta_scan(long long x, long long* total, lon
     return before + v - x;
 }
 
-// Cost of one head of sequence s of this lane; the units of long sequences are shared out over the warp.
-__device__ __forceinline__ long long head_cost(const CacheAttnArgs& a, const SeqRows& r, bool have) {
+// Cost of one head of this lane's item; the units of long sequences are shared out over the warp.
+template <bool RUNS>
+__device__ __forceinline__ long long head_cost(const CacheAttnArgs& a, const Rows& r, bool have) {
     constexpr int kFew = 2;
     const int units = have ? (r.rows * a.G + kUnitRows - 1) / kUnitRows : 0, lane = threadIdx.x & 31;
     long long c = 0;
     if (units <= kFew)
-        for (int i = 0; i < units; ++i) c += unit_of(a, r, i * kUnitRows).cost();
+        for (int i = 0; i < units; ++i) c += unit_of<RUNS>(a, r, i * kUnitRows).cost();
     for (unsigned todo = __ballot_sync(0xffffffffu, units > kFew); todo; todo &= todo - 1) {
         const int src = __ffs(todo) - 1, n = __shfl_sync(0xffffffffu, units, src);
-        SeqRows q;
+        Rows q;
         q.rows = __shfl_sync(0xffffffffu, r.rows, src);
         q.len = __shfl_sync(0xffffffffu, r.len, src);
         q.pos0 = __shfl_sync(0xffffffffu, r.pos0, src);
+        if (RUNS) q.key0 = __shfl_sync(0xffffffffu, r.key0, src);
         long long x = 0;
-        for (int i = lane; i < n; i += 32) x += unit_of(a, q, i * kUnitRows).cost();
+        for (int i = lane; i < n; i += 32) x += unit_of<RUNS>(a, q, i * kUnitRows).cost();
 #pragma unroll
         for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
         if (lane == src) c = x;
@@ -360,11 +368,12 @@ __device__ __forceinline__ long long head_cost(const CacheAttnArgs& a, const Seq
 }
 
 // The unit of sequence r that holds offset *off of a head's cost, by one whole warp; *off becomes the offset in it.
-__device__ __forceinline__ int find_unit(const CacheAttnArgs& a, const SeqRows& r, long long* off) {
+template <bool RUNS>
+__device__ __forceinline__ int find_unit(const CacheAttnArgs& a, const Rows& r, long long* off) {
     const int lane = threadIdx.x & 31;
     for (int i0 = 0;; i0 += 32) {
         const int m0 = (i0 + lane) * kUnitRows;
-        const long long c = m0 < r.rows * a.G ? unit_of(a, r, m0).cost() : 0;
+        const long long c = m0 < r.rows * a.G ? unit_of<RUNS>(a, r, m0).cost() : 0;
         long long v = c;
 #pragma unroll
         for (int o = 1; o < 32; o <<= 1) {
@@ -383,8 +392,9 @@ __device__ __forceinline__ int find_unit(const CacheAttnArgs& a, const SeqRows& 
     }
 }
 
+template <bool RUNS>
 __device__ __forceinline__ void find_start(const CacheAttnArgs& a, Start* st, long long* buf) {
-    const int tid = threadIdx.x, n = a.c.n_seqs;
+    const int tid = threadIdx.x, n = items_of<RUNS>(a);
     if (tid == 0) {
         st->left = 0;
         st->bad = 0x7fffffff;
@@ -392,16 +402,16 @@ __device__ __forceinline__ void find_start(const CacheAttnArgs& a, Start* st, lo
     }
     __syncthreads();
     long long W = 0, before = 0, cost = 0, sum;
-    SeqRows r{};
+    Rows r{};
     for (int s0 = 0; s0 < n; s0 += kThreads) {
         const int s = s0 + tid;
         bool have = s < n;
         if (have) {
-            r = seq_rows(a.c, a.cu_rows, a.q_pos, a.total_rows, s);
-            if (!r.ok) atomicMin(&st->bad, s);
+            r = item_rows<RUNS>(a, s);
+            if (!r.ok) atomicMin(&st->bad, r.seq);
             have = r.ok;
         }
-        cost = head_cost(a, r, have);
+        cost = head_cost<RUNS>(a, r, have);
         before = W + cta_scan(cost * a.c.Hk, &sum, buf);
         W += sum;
     }
@@ -424,8 +434,8 @@ __device__ __forceinline__ void find_start(const CacheAttnArgs& a, Start* st, lo
         for (int s0 = 0; s0 < n; s0 += kThreads) {
             const int s = s0 + tid;
             if (n > kThreads) {  // more than one pass: the costs again
-                if (s < n) r = seq_rows(a.c, a.cu_rows, a.q_pos, a.total_rows, s);
-                cost = head_cost(a, r, s < n);
+                if (s < n) r = item_rows<RUNS>(a, s);
+                cost = head_cost<RUNS>(a, r, s < n);
                 before = base + cta_scan(cost * a.c.Hk, &sum, buf);
                 base += sum;
             }
@@ -437,12 +447,13 @@ __device__ __forceinline__ void find_start(const CacheAttnArgs& a, Start* st, lo
                 int h = 0;
                 if (mine)
                     for (; off >= cost; ++h) off -= cost;
-                SeqRows q;
+                Rows q;
                 q.rows = __shfl_sync(0xffffffffu, r.rows, src);
                 q.len = __shfl_sync(0xffffffffu, r.len, src);
                 q.pos0 = __shfl_sync(0xffffffffu, r.pos0, src);
+                if (RUNS) q.key0 = __shfl_sync(0xffffffffu, r.key0, src);
                 off = __shfl_sync(0xffffffffu, off, src);
-                const int m0 = find_unit(a, q, &off);
+                const int m0 = find_unit<RUNS>(a, q, &off);
                 if (mine) {
                     st->s = s;
                     st->h = h;
@@ -465,12 +476,13 @@ struct Batch {
     float ks, vs;
 };
 
+template <bool RUNS>
 struct BatchWalk {
     Place* p;
     int kt, left;
     __device__ __forceinline__ bool next(const CacheAttnArgs& a, Batch* b) {
         while (left == 0) {
-            if (!next_run(a, p)) return false;
+            if (!next_run<RUNS>(a, p)) return false;
             left = p->g.tiles();
             kt = p->g.kt0;
         }
@@ -483,7 +495,7 @@ struct BatchWalk {
         const int key = (kt + (lane >> 3)) * kTileKeys + (lane & 7) * 16;
         b->id = -1;
         if ((lane >> 3) < b->n && key < g.end) {
-            const int id = __ldg(a.c.table + (long long)g.s * a.c.max_pages + (key >> a.c.page_shift));
+            const int id = __ldg(a.c.table + (long long)g.s * a.c.max_pages + (((RUNS ? g.key0 : 0) + key) >> a.c.page_shift));
             b->id = id >= 0 && id < a.c.n_pages ? id : -2;
         }
         kt += b->n;
@@ -502,16 +514,16 @@ __device__ __forceinline__ void load_scales(const CacheAttnArgs& a, Batch* b) {
     }
 }
 
-template <int D>
+template <int D, bool RUNS>
 __device__ __forceinline__ void produce(const Ctx<D>& x, const CacheAttnArgs& a, const Start& st, const CUtensorMap* tk,
                                         const CUtensorMap* tv) {
     using L = Smem<D>;
     const int lane = threadIdx.x & 31;
     const int page = a.c.page, per_page = page / 16;
-    BatchWalk bw;
+    BatchWalk<RUNS> bw;
     bw.left = 0;
     bw.p = x.place();
-    begin_share(a, st, bw.p);
+    begin_share<RUNS>(a, st, bw.p);
     Batch b0, b1, b2;
     bool h0 = bw.next(a, &b0), h1 = h0 && bw.next(a, &b1), h2;
     if (h0) load_scales(a, &b0);
@@ -570,7 +582,7 @@ __device__ __forceinline__ void produce(const Ctx<D>& x, const CacheAttnArgs& a,
 }
 
 // ------------------------------------------------------------ V: e4m3 -> fp16
-template <int D>
+template <int D, bool RUNS>
 __device__ __forceinline__ void widen(const Ctx<D>& x, const CacheAttnArgs& a, const Start& st) {
     using L = Smem<D>;
     constexpr int PER = D / 16;                  // 16-byte chunks per key
@@ -587,12 +599,12 @@ __device__ __forceinline__ void widen(const Ctx<D>& x, const CacheAttnArgs& a, c
     const uint32_t d0 = row_dst + ((((2 * c + (swap ? 1 : 0)) & 7) ^ (r0 & 7)) << 4);
     const uint32_t d1 = row_dst + ((((2 * c + (swap ? 0 : 1)) & 7) ^ (r0 & 7)) << 4);
     Place* place = x.place();
-    begin_share(a, st, place);
+    begin_share<RUNS>(a, st, place);
     uint32_t t = 0, seg = 0;
-    while (next_run(a, place)) {
+    while (next_run<RUNS>(a, place)) {
         if (place->g.tiles() == 0) continue;
         // keys that every row of the unit sees; a NaN among the others must not reach a row that does not see it
-        const int all = key_end(place->g.len, a.block, place->g.pos0 + place->g.m0 / a.G), end = place->g.end, kt1 = place->g.kt1;
+        const int all = keys_of<RUNS>(a, place->g, place->g.pos0 + place->g.m0 / a.G), end = place->g.end, kt1 = place->g.kt1;
         for (int kt = place->g.kt0; kt < kt1; ++kt, ++t) {
             const uint32_t ws = t & 1;
             bool ok = x.wait(B_VFULL, ws, (t >> 1) & 1);
@@ -662,7 +674,7 @@ __device__ __forceinline__ void widen(const Ctx<D>& x, const CacheAttnArgs& a, c
 // so what stands between two groups of MMAs is kept short: one wait for a
 // tile's keys, one for p' of each O (which counts the fp16 values as well) and
 // one commit for each S and each PV.
-template <int D>
+template <int D, bool RUNS>
 __device__ __forceinline__ void issue(const CacheAttnArgs& a, const Start& st) {
     using L = Smem<D>;
     constexpr uint32_t id_s = idesc_fmt0(128, kTileKeys, 0), id_o = idesc_fmt0(128, D, 1);
@@ -698,10 +710,10 @@ __device__ __forceinline__ void issue(const CacheAttnArgs& a, const Start& st) {
         }
     };
     Place* place = x.place();
-    begin_share(a, st, place);
+    begin_share<RUNS>(a, st, place);
     uint32_t b = 0, ph = 0;            // t & 1 and (t >> 1) & 1 of the tile whose p' comes next
     uint32_t stage = 0, ks = 0, q = 0;  // the K stage whose keys come next, its phase, and Q's
-    while (__any_sync(0xffffffffu, next_run(a, place))) {
+    while (__any_sync(0xffffffffu, next_run<RUNS>(a, place))) {
         const int nt = __reduce_max_sync(0xffffffffu, place->g.tiles());
         if (nt == 0) continue;
         const int two = __reduce_max_sync(0xffffffffu, (int)place->g.two);
@@ -977,9 +989,21 @@ __device__ __forceinline__ void softmax_part(uint32_t (&r)[2][32], uint32_t tC, 
 
 // Where the results of a unit's flat rows go.
 struct Out {
-    float* slot;  // partial: the share's slot (nullptr: the rows are complete)
+    float* slot;  // partial: the share's slot (nullptr: the unit is complete)
     int slot_r;   // its rows
+    float* o_f32;  // else: fp32 rows (nullptr: bf16 to a.o)
+    float* lse;
 };
+template <int D, bool RUNS>
+__device__ __forceinline__ Out out_of(const CacheAttnArgs& a, const Seg& g) {
+    Out out;
+    out.slot_r = slot_rows(a.total_rows, a.G);
+    out.slot = g.whole ? nullptr : slot_at(a.scratch, 2 * (int)blockIdx.x + (g.kt0 > 0 ? 0 : 1), out.slot_r, D);
+    const bool plane = RUNS && g.part != PART_WHOLE;
+    out.o_f32 = plane ? plane_o(a, D, g.part) : a.o_f32;
+    out.lse = plane ? plane_lse(a, D, g.part) : a.lse;
+    return out;
+}
 
 // Writes 32 columns (from 32 q on) of flat row m: into the slot; as fp32 to o; or as bf16 into the staging tile at
 // `stage`, whose row `row` is this one.
@@ -992,9 +1016,9 @@ __device__ __forceinline__ void put_cols(const CacheAttnArgs& a, const Seg& g, c
 #pragma unroll
             for (int e = 0; e < 8; ++e) dst[e * out.slot_r] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
         }
-    } else if (a.o_f32) {
+    } else if (out.o_f32) {
         if (m < g.last) {
-            float4* dst = reinterpret_cast<float4*>(a.o_f32 + ((long long)(g.row0 + m / a.G) * a.H + g.h * a.G + m % a.G) * D + 32 * q);
+            float4* dst = reinterpret_cast<float4*>(out.o_f32 + ((long long)(g.row0 + m / a.G) * a.H + g.h * a.G + m % a.G) * D + 32 * q);
 #pragma unroll
             for (int e = 0; e < 8; ++e) dst[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
         }
@@ -1035,11 +1059,11 @@ __device__ __forceinline__ void put_lse(const CacheAttnArgs& a, const Seg& g, co
         out.slot[(long long)out.slot_r * D + m - g.m0] = l2;
     } else {
         const int row = m / a.G;
-        a.lse[(long long)(g.h * a.G + m - row * a.G) * a.total_rows + g.row0 + row] = l2 * 0.69314718055994531f;
+        out.lse[(long long)(g.h * a.G + m - row * a.G) * a.total_rows + g.row0 + row] = l2 * 0.69314718055994531f;
     }
 }
 
-template <int D, int NG>
+template <int D, int NG, bool RUNS>
 __device__ __forceinline__ void softmax(const Ctx<D>& x, const CacheAttnArgs& a, const Start& st) {
     using L = Smem<D>;
     const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31, i = warp >> 2, row = threadIdx.x & 127;
@@ -1047,14 +1071,14 @@ __device__ __forceinline__ void softmax(const Ctx<D>& x, const CacheAttnArgs& a,
     const uint32_t tS = x.tmem + lane_base, tO = x.tmem + 256 + lane_base;
     const float* scales = reinterpret_cast<const float*>(g_smem + L::kScale);
     Place* place = x.place();
-    begin_share(a, st, place);
+    begin_share<RUNS>(a, st, place);
     uint32_t t = 0, seg = 0, s0_phases = 0;  // s0_phases: bit of each B_S0 stage's next phase
     bool ok = true;  // warp-uniform; once it is false the loops run on without waiting, through the same barriers
     auto wait = [&](int base, int n, uint32_t parity) {
         if (ok) ok = __all_sync(0xffffffffu, x.wait(base, n, parity));
         tc::tc_fence_after();
     };
-    while (next_run(a, place)) {
+    while (next_run<RUNS>(a, place)) {
         const int nt = place->g.tiles();
         const bool two = place->g.two;
         float cs;
@@ -1065,16 +1089,17 @@ __device__ __forceinline__ void softmax(const Ctx<D>& x, const CacheAttnArgs& a,
             const int m = g.m0 + (two ? 128 * i : 0) + row;  // this thread's flat row
             if (nt == 0) {                                   // rows without keys
                 if (m < g.last && (two || i == 0)) {
+                    const Out out = out_of<D, RUNS>(a, g);
                     const long long at = ((long long)(g.row0 + m / a.G) * a.H + g.h * a.G + m % a.G) * D;
                     for (int c = 0; c < D; c += 8) {
-                        if (a.o_f32) {
-                            *reinterpret_cast<float4*>(a.o_f32 + at + c) = make_float4(0.f, 0.f, 0.f, 0.f);
-                            *reinterpret_cast<float4*>(a.o_f32 + at + c + 4) = make_float4(0.f, 0.f, 0.f, 0.f);
+                        if (out.o_f32) {
+                            *reinterpret_cast<float4*>(out.o_f32 + at + c) = make_float4(0.f, 0.f, 0.f, 0.f);
+                            *reinterpret_cast<float4*>(out.o_f32 + at + c + 4) = make_float4(0.f, 0.f, 0.f, 0.f);
                         } else {
                             *reinterpret_cast<uint4*>(a.o + at + c) = make_uint4(0, 0, 0, 0);
                         }
                     }
-                    put_lse(a, g, Out{nullptr, 0}, D, m, -INFINITY);
+                    put_lse(a, g, out, D, m, -INFINITY);
                 }
                 continue;
             }
@@ -1088,7 +1113,7 @@ __device__ __forceinline__ void softmax(const Ctx<D>& x, const CacheAttnArgs& a,
             // no other
             const int qe = g_smem[L::kQExp + (two ? 128 * i : 0) + row];
             cs = qe == 255 ? NAN : a.scale_log2 * __uint_as_float((uint32_t)qe << 23);
-            const int end = m < g.last ? key_end(g.len, a.block, g.pos0 + m / a.G) : 0;
+            const int end = m < g.last ? keys_of<RUNS>(a, g, g.pos0 + m / a.G) : 0;
             warp_live = __shfl_sync(0xffffffffu, (int)(m < g.last), 0);
             // keys of a tile that this row sees of the thread's part, and that the warp's first row (which sees the
             // fewest) does
@@ -1174,14 +1199,12 @@ __device__ __forceinline__ void softmax(const Ctx<D>& x, const CacheAttnArgs& a,
         }
         wait(B_PV, (t - 1) & 1, ((t - 1) >> 1) & 1);  // every product of the unit is done
         const Seg g = place->g;
-        const int m = g.m0 + (two ? 128 * i : 0) + row, end = m < g.last ? key_end(g.len, a.block, g.pos0 + m / a.G) : 0;
-        Out out;
-        out.slot_r = slot_rows(a.total_rows, a.G);
-        out.slot = g.whole ? nullptr : slot_at(a.scratch, 2 * (int)blockIdx.x + (g.kt0 > 0 ? 0 : 1), out.slot_r, D);
+        const int m = g.m0 + (two ? 128 * i : 0) + row, end = m < g.last ? keys_of<RUNS>(a, g, g.pos0 + m / a.G) : 0;
+        const Out out = out_of<D, RUNS>(a, g);
         int* nan_first = reinterpret_cast<int*>(g_smem + L::kNan) + (seg & 3) * D;
         int* nan_any = reinterpret_cast<int*>(g_smem + L::kNanAny) + (seg & 3);
         ++seg;
-        const bool staged = !out.slot && !a.o_f32;
+        const bool staged = !out.slot && !out.o_f32;
         const bool nans = *nan_any < g.end;
         float mj = sums.m, lj = sums.l, f0, f1 = 0.f;
         bool use0 = sums.l != 0.f, use1 = false;  // NaN counts as something
@@ -1249,7 +1272,7 @@ __device__ __forceinline__ void softmax(const Ctx<D>& x, const CacheAttnArgs& a,
 }
 
 // ------------------------------------------------------------------- kernel
-template <int D, int NG>
+template <int D, int NG, bool RUNS>
 __global__ void __launch_bounds__(kThreads, 1)
     cache_attn_kernel(const __grid_constant__ CUtensorMap tk, const __grid_constant__ CUtensorMap tv, const CacheAttnArgs a) {
     using L = Smem<D>;
@@ -1284,7 +1307,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         tc::prefetch_tmap(&tk);
         tc::prefetch_tmap(&tv);
     }
-    find_start(a, st, reinterpret_cast<long long*>(g_smem));  // the scan's words lie where Q will
+    find_start<RUNS>(a, st, reinterpret_cast<long long*>(g_smem));  // the scan's words lie where Q will
     tc::tc_fence_before();
     __syncthreads();
     tc::tc_fence_after();
@@ -1295,12 +1318,12 @@ __global__ void __launch_bounds__(kThreads, 1)
     if (st->left > 0 && aligned) {
         if (warp >= 8) {
             tc::regs_dec<kRegsOther>();
-            if (warp == 8) produce<D>(x.own(), a, *st, &tk, &tv);
-            else if (warp == 9) issue<D>(a, *st);
-            else if (warp >= 12) widen<D>(x.own(), a, *st);
+            if (warp == 8) produce<D, RUNS>(x.own(), a, *st, &tk, &tv);
+            else if (warp == 9) issue<D, RUNS>(a, *st);
+            else if (warp >= 12) widen<D, RUNS>(x.own(), a, *st);
         } else {
             tc::regs_inc<kRegsSoftmax>();
-            softmax<D, NG>(x.own(), a, *st);
+            softmax<D, NG, RUNS>(x.own(), a, *st);
         }
     }
     tc::tc_fence_before();
@@ -1315,7 +1338,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         r.more = st->more;
         r.C = st->C;
         if (st->left > 0) {
-            const SeqRows q = seq_rows(a.c, a.cu_rows, a.q_pos, a.total_rows, st->s);
+            const Rows q = item_rows<RUNS>(a, st->s);
             r.row0 = q.row0;
             r.rows = q.rows;
             r.pos0 = q.pos0;
@@ -1323,10 +1346,12 @@ __global__ void __launch_bounds__(kThreads, 1)
             r.head = st->h;
             r.m0 = st->m0;
             r.off = st->off;
-            r.cost = unit_of(a, q, st->m0).cost();
+            r.cost = unit_of<RUNS>(a, q, st->m0).cost();
+            r.part = q.part;
         }
         r.error = x.words()[1] ? DEV_TIMEOUT : st->bad != 0x7fffffff ? DEV_CHECK : x.words()[2];
         r.info = st->bad != 0x7fffffff ? st->bad : (int)blockIdx.x;
+        r.bad = st->bad != 0x7fffffff;
         share_recs(a.scratch)[blockIdx.x] = r;
     }
 }
@@ -1362,23 +1387,23 @@ bool make_map(CUtensorMap* m, const CacheView& c, const void* base) {
               CU_TENSOR_MAP_L2_PROMOTION_L2_256B, CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE) == CUDA_SUCCESS;
 }
 
-template <int D, int NG>
+template <int D, int NG, bool RUNS>
 cudaError_t launch_ng(const CacheAttnArgs& a, int ctas, cudaStream_t st) {
     CUtensorMap tk, tv;
     if (!make_map<D>(&tk, a.c, a.c.k) || !make_map<D>(&tv, a.c, a.c.v)) return cudaErrorInvalidValue;
-    const cudaError_t e = cudaFuncSetAttribute(cache_attn_kernel<D, NG>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::kBytes);
+    const cudaError_t e = cudaFuncSetAttribute(cache_attn_kernel<D, NG, RUNS>, cudaFuncAttributeMaxDynamicSharedMemorySize, Smem<D>::kBytes);
     if (e != cudaSuccess) return e;
-    cache_attn_kernel<D, NG><<<ctas, kThreads, Smem<D>::kBytes, st>>>(tk, tv, a);
+    cache_attn_kernel<D, NG, RUNS><<<ctas, kThreads, Smem<D>::kBytes, st>>>(tk, tv, a);
     return cudaGetLastError();
 }
 
-template <int D>
+template <int D, bool RUNS>
 cudaError_t launch_d(const CacheAttnArgs& a, int ctas, cudaStream_t st) {
     switch (a.c.page) {
-        case 16: return launch_ng<D, 8>(a, ctas, st);
-        case 32: return launch_ng<D, 4>(a, ctas, st);
-        case 64: return launch_ng<D, 2>(a, ctas, st);
-        default: return launch_ng<D, 1>(a, ctas, st);
+        case 16: return launch_ng<D, 8, RUNS>(a, ctas, st);
+        case 32: return launch_ng<D, 4, RUNS>(a, ctas, st);
+        case 64: return launch_ng<D, 2, RUNS>(a, ctas, st);
+        default: return launch_ng<D, 1, RUNS>(a, ctas, st);
     }
 }
 

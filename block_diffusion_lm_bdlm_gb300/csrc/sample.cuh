@@ -1,0 +1,134 @@
+// sample.cuh - the weights of tokens, and what the sampling kernel is given.
+//
+// A token's weight is w = e^((x - m) / T) with the row's largest logit m. Two
+// forms of it are used. The quick one is a multiplication and an exponential of
+// the special-function unit. Its errors, 2^-22 of the exponential, the roundings
+// of the argument and those of the sums, move any sum of weights of a row by
+// less than kQuick of the row's sum Z: an argument t = -log2 w is off by at most
+// |t| 2^-23, and the sum of w |t| is at most Z log2(vocabulary), which gives
+// 18 * 2^-23 * ln 2 = 1.5e-6; 2.4e-7 come from the exponential, and at most
+// 20 * 2^-24 = 1.2e-6 from additions in 32 bits.
+//
+// The exact one is a whole multiple of 2^-44, from two-float arithmetic (sums
+// and products with their errors after Dekker and Knuth; a table of 2^(j/16)
+// and the series of e^y). Its relative error is below 2^-40, sums of it are
+// sums of integers, the same in any order, and equal logits weigh the same.
+#pragma once
+
+#include <cstdint>
+
+#include "common.cuh"
+
+namespace bdlm {
+namespace sample {
+
+constexpr double kQuick = 4e-6;
+constexpr int kFrac = 44;  // a weight of 1 is 2^44: 2^18 of them stay below 2^62
+
+#ifdef __CUDA_ARCH__
+#define BDLM_MUL(a, b) __fmul_rn(a, b)
+#define BDLM_ADD(a, b) __fadd_rn(a, b)
+#define BDLM_FMA(a, b, c) __fmaf_rn(a, b, c)
+#define BDLM_RINT(x) __float2int_rn(x)
+#else
+#include <cmath>
+#define BDLM_MUL(a, b) ((a) * (b))
+#define BDLM_ADD(a, b) ((a) + (b))
+#define BDLM_FMA(a, b, c) std::fma(a, b, c)
+#define BDLM_RINT(x) ((int)std::lrint(x))
+#endif
+
+struct F2 {
+    float hi, lo;
+};
+
+// 2^(j / 16), j = -8 .. 8, as two floats each.
+constexpr int kTable = 17;
+#define BDLM_POW2_TABLE                                                                                                      \
+    {0x1.6a09e6p-1f, 0x1.9fcef4p-27f}, {0x1.7a1148p-1f, -0x1.829fd0p-26f}, {0x1.8ace54p-1f, 0x1.15506ep-28f},                \
+        {0x1.9c4918p-1f, 0x1.51f848p-28f}, {0x1.ae89fap-1f, -0x1.a94b14p-27f}, {0x1.c199bep-1f, -0x1.3d56b2p-28f},           \
+        {0x1.d5818ep-1f, -0x1.822dbcp-28f}, {0x1.ea4afap-1f, 0x1.52486cp-28f}, {1.f, 0.f}, {0x1.0b5586p+0f, 0x1.9f3122p-25f}, \
+        {0x1.172b84p+0f, -0x1.c15742p-27f}, {0x1.2387a6p+0f, 0x1.ceac48p-25f}, {0x1.306fe0p+0f, 0x1.4636e2p-25f},            \
+        {0x1.3dea64p+0f, 0x1.824684p-25f}, {0x1.4bfdaep+0f, -0x1.593abcp-25f}, {0x1.5ab07ep+0f, -0x1.5bd5ecp-27f},           \
+    {0x1.6a09e6p+0f, 0x1.9fcef4p-26f}
+
+// 2^44 e^((x - m) / T), rounded; c = 2 log2(e) / T. Halves of x and m are taken, so that no difference overflows.
+__host__ __device__ __forceinline__ uint64_t exact_weight(float x, float m, F2 c, const F2* table) {
+    const float a = BDLM_MUL(0.5f, m), b = BDLM_MUL(-0.5f, x);
+    const float h = BDLM_ADD(a, b);  // half the distance, with its error
+    const float bb = BDLM_ADD(h, -a);
+    const float hl = BDLM_ADD(BDLM_ADD(a, -BDLM_ADD(h, -bb)), BDLM_ADD(b, -bb));
+    const float th = BDLM_MUL(h, c.hi);
+    if (!(th < 46.f)) return 0;  // below half of 2^-44 (and x = -inf)
+    const float tl = BDLM_ADD(BDLM_FMA(h, c.hi, -th), BDLM_FMA(h, c.lo, BDLM_MUL(hl, c.hi)));
+    const int n = BDLM_RINT(th);
+    const float f = BDLM_ADD((float)n, -th);  // exact; the weight is 2^-n 2^(f - tl)
+    const float gh = BDLM_ADD(f, -tl);
+    const float fb = BDLM_ADD(gh, -f);
+    const float gl = BDLM_ADD(BDLM_ADD(f, -BDLM_ADD(gh, -fb)), BDLM_ADD(-tl, -fb));
+    const int j = BDLM_RINT(BDLM_MUL(gh, 16.f));
+    const float r = BDLM_FMA((float)j, -0.0625f, gh);  // exact
+    constexpr float lh = 0x1.62e430p-1f, ll = -0x1.05c610p-29f;  // ln 2
+    const float y0 = BDLM_MUL(r, lh), y1 = BDLM_ADD(BDLM_FMA(r, lh, -y0), BDLM_FMA(r, ll, BDLM_MUL(gl, lh)));
+    const float yh = BDLM_ADD(y0, y1), yl = BDLM_ADD(y1, -BDLM_ADD(yh, -y0));
+    const float qh = BDLM_MUL(yh, yh), ql = BDLM_FMA(BDLM_MUL(2.f, yh), yl, BDLM_FMA(yh, yh, -qh));
+    float p = BDLM_FMA(yh, 1.f / 720.f, 1.f / 120.f);
+    p = BDLM_FMA(yh, p, 1.f / 24.f);
+    p = BDLM_FMA(yh, p, 1.f / 6.f);
+    const float q2 = BDLM_MUL(0.5f, qh), sh = BDLM_ADD(yh, q2), se = BDLM_ADD(q2, -BDLM_ADD(sh, -yh));
+    const float low = BDLM_ADD(BDLM_FMA(BDLM_MUL(qh, yh), p, se), BDLM_FMA(0.5f, ql, yl));
+    const F2 t = table[j + 8];
+    const float ph = BDLM_MUL(t.hi, sh), pl = BDLM_FMA(t.hi, sh, -ph);
+    const float rh = BDLM_ADD(t.hi, ph), re = BDLM_ADD(ph, -BDLM_ADD(rh, -t.hi));
+    const float rl = BDLM_ADD(BDLM_ADD(re, pl), BDLM_ADD(t.lo, BDLM_FMA(t.hi, low, BDLM_MUL(t.lo, sh))));
+    // rh is a multiple of 2^-24 (or of 2^-25 below one half, which 2^-44 holds as well)
+    const int64_t w = ((int64_t)BDLM_RINT(BDLM_MUL(rh, 0x1p25f)) << (kFrac - 25)) + BDLM_RINT(BDLM_MUL(rl, 0x1p44f));
+    return n <= 0 ? (uint64_t)w << -n : (uint64_t)((w + ((int64_t)1 << (n - 1))) >> n);
+}
+
+// A key that orders floats as their values do; -0 and 0 have the same.
+__host__ __device__ __forceinline__ uint32_t order_key(uint32_t bits) {
+    if (bits == 0x80000000u) bits = 0;
+    return bits & 0x80000000u ? ~bits : bits | 0x80000000u;
+}
+
+}  // namespace sample
+
+// What a call samples with: per-row arrays, or where they are null one value for all rows.
+struct SampleArgs {
+    const void* x;  // logits: row i begins at element i * stride
+    long long stride;
+    int rows, vocab;
+    const float* u;
+    const float* temperature;
+    const int* top_k;
+    const float* top_p;
+    const float* min_p;
+    float temperature_all, top_p_all, min_p_all;
+    int top_k_all;
+    const int* now;  // rows whose entry is not `want` are left (nullptr: none are)
+    int want;
+    int* token;
+    float* logprob;
+    int ctas;  // CTAs of a row, one cluster
+    int per;   // elements of each
+};
+cudaError_t launch_sample(SampleArgs a, int dtype, int num_sms, cudaStream_t st, int* launches);
+
+struct UnmaskArgs {
+    const int* now;
+    const int* sampled;
+    const float* logprob;
+    const int* cu_rows;
+    int n_seqs, total_rows, mask_id;
+    const int* n_min;
+    const float* threshold;
+    int n_min_all;
+    float threshold_all;
+    int* out;
+    int* left;
+    WsHeader* hdr;
+};
+cudaError_t launch_unmask(const UnmaskArgs& a, cudaStream_t st, int* launches);
+
+}  // namespace bdlm

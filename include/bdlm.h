@@ -67,7 +67,7 @@ enum bdlm_status {
     BDLM_ERR_NO_PAGES = 7      /* device: the cache has too few free pages        */
 };
 
-enum bdlm_dtype { BDLM_BF16 = 0, BDLM_F32 = 1 };
+enum bdlm_dtype { BDLM_BF16 = 0, BDLM_F32 = 1, BDLM_F16 = 2 /* logits of bdlm_sample only */ };
 
 enum bdlm_part_kind {
     BDLM_PART_NONE = 0,        /* full BDLM attention                             */
@@ -447,6 +447,60 @@ BDLM_API int bdlm_cache_attn_fwd(const bdlm_cache* cache, int32_t layer, const v
                   float softmax_scale, int32_t o_dtype, void* workspace, size_t workspace_bytes,
                   bdlm_stream_t stream);
 
+/* Workspace (bytes, 256-byte aligned) of bdlm_cache_prefixes; 0 for more than
+ * 16384 sequences. */
+BDLM_API size_t bdlm_cache_prefixes_workspace_bytes(int32_t n_seqs);
+
+/*
+ * bdlm_cache_prefixes - find the runs of sequences whose rows can read their
+ *   leading pages together (bdlm_cache_attn_shared_fwd), from the table alone.
+ *
+ *   cu_rows, q_pos  as for bdlm_cache_attn_fwd; total_rows >= 0.
+ *   runs            DEVICE int32 [3, n_seqs], outside table, lens, cu_rows and
+ *                   q_pos: of sequence s, in runs[0][s] the first sequence of
+ *                   its run, in runs[1][s] the number behind its last one, in
+ *                   runs[2][s] the leading positions, whole pages, that the
+ *                   run shares (0: s reads alone, and its run is s itself).
+ * Only sequences with rows join runs; one without that lies between them is
+ * counted in. Pages are shared that name the same page in the tables of all of
+ * a run and lie wholly below every row of it, so that all rows see them. Of
+ * all cuts of the sequences into runs of at most 256 with rows the one is taken
+ * that saves most pages: the sum of (sequences with rows - 1) times shared
+ * pages; of cuts as good, from the last run to the first, the shorter run. (At most 2^22
+ * pages of a run count.)
+ * One plan serves all layers and steps of a block: it changes with the table,
+ * the lengths and the rows.
+ * Malformed offsets or lengths (BDLM_ERR_DEVICE_CHECK): nothing is shared.
+ */
+BDLM_API int bdlm_cache_prefixes(const bdlm_cache* cache, int64_t total_rows, const int32_t* cu_rows,
+                  const int32_t* q_pos, int32_t* runs, void* workspace, size_t workspace_bytes, bdlm_stream_t stream);
+
+/* Workspace (bytes, 256-byte aligned) of bdlm_cache_attn_shared_fwd; 0 for
+ * sizes the library does not support. */
+BDLM_API size_t bdlm_cache_attn_shared_fwd_workspace_bytes(int64_t total_rows, int32_t heads, int32_t kv_heads,
+                  int32_t head_dim, int32_t n_seqs);
+
+/*
+ * bdlm_cache_attn_shared_fwd - bdlm_cache_attn_fwd in which the sequences of a
+ *   run read what they share once for all of their rows: the same result up to
+ *   the order of sums. What a run shares and what each sequence has of its own
+ *   are attended to apart, in fp32, and joined as by bdlm_lse_merge.
+ *
+ *   runs   DEVICE int32 [3, n_seqs] as bdlm_cache_prefixes writes it, or made
+ *          by the caller: first, end and shared positions of every sequence's
+ *          run. All sequences of a run, also those without rows, name the
+ *          same three; shared is a multiple of the page, and at most what the
+ *          run's first sequence holds and what each row's sequence holds below
+ *          its first row. The pages are read through the run's first table
+ *          row: whether the others name the same is the caller's to know.
+ * Malformed runs give BDLM_ERR_DEVICE_CHECK like malformed offsets, and leave o
+ * and lse unwritten. The other arguments are those of bdlm_cache_attn_fwd.
+ */
+BDLM_API int bdlm_cache_attn_shared_fwd(const bdlm_cache* cache, int32_t layer, const void* q, void* o, float* lse,
+                  int64_t total_rows, int32_t heads, int32_t block, const int32_t* cu_rows, const int32_t* q_pos,
+                  const int32_t* runs, float softmax_scale, int32_t o_dtype, void* workspace, size_t workspace_bytes,
+                  bdlm_stream_t stream);
+
 /* Workspace (bytes, 256-byte aligned) of bdlm_cache_reserve, _fork and
  * _compact; 0 for sizes the library does not support. */
 BDLM_API size_t bdlm_cache_pages_workspace_bytes(int32_t n_pages, int32_t n_seqs);
@@ -492,6 +546,79 @@ BDLM_API int bdlm_cache_fork(const bdlm_cache* cache, const int32_t* parents, co
  */
 BDLM_API int bdlm_cache_compact(const bdlm_cache* cache, int32_t* n_live, void* workspace, size_t workspace_bytes,
                   bdlm_stream_t stream);
+
+/* ------------------------------------------------------------------------
+ * From a denoising step's logits to tokens.
+ * ------------------------------------------------------------------------ */
+
+/* How tokens are drawn: of each an array [rows] on the device, or where it is
+ * NULL the one value behind it for all rows. */
+typedef struct {
+    const float* temperature;
+    const int32_t* top_k;
+    const float* top_p;
+    const float* min_p;
+    float temperature_all; /* below 2^-20 (and NaN): the largest logit; above 2^40: 2^40 */
+    int32_t top_k_all;     /* < 1 or >= vocab: off                                       */
+    float top_p_all;       /* >= 1 (and NaN): off; <= 0: the first token alone           */
+    float min_p_all;       /* <= 0 (and NaN): off; above 1: 1                            */
+} bdlm_sampling;
+
+/*
+ * bdlm_sample - draw a token for each row of logits with a random number that
+ *   the caller gives, and its log-probability.
+ *
+ *   logits      dtype (BDLM_BF16, BDLM_F16 or BDLM_F32) [rows, vocab], row i at
+ *               element i * row_stride (>= vocab; any alignment of the type).
+ *               1 <= vocab <= 262144. -inf masks a token, and so does NaN.
+ *   u           fp32 [rows], in [0, 1] (values outside count as the nearer end).
+ *   tokens      NULL, or int32 [rows]: only rows with tokens[i] == mask_id are
+ *               drawn, the others' logits are not read and token and logprob
+ *               stay as they were. token may be tokens itself.
+ *   token       int32 [rows]; logprob fp32 [rows].
+ * Tokens in the order of falling logits, of equal ones by number, have the
+ * weights w = exp((x - max) / temperature). top_k keeps the first k of them;
+ * top_p of those the ones with less than top_p of their weight before them;
+ * min_p the ones with w >= min_p. The token is the first kept one, by number, at which
+ * the sum of the kept weights exceeds u times all of it (if none does, the
+ * last one of any weight). With temperature 0 it is the first of the largest.
+ * If the largest logit is +inf, the logits that are +inf weigh the same and
+ * all others nothing. logprob is the token's under softmax(logits), without
+ * temperature and cuts. A row without any logit above -inf gets token -1,
+ * logprob -inf.
+ * The choice is made from weights that are exact to 2^-40, summed as whole
+ * numbers: it does not depend on the order of any sum. No workspace is used.
+ */
+BDLM_API int bdlm_sample(const void* logits, int32_t dtype, int64_t rows, int32_t vocab, int64_t row_stride,
+                  const float* u, const bdlm_sampling* how, const int32_t* tokens, int32_t mask_id, int32_t* token,
+                  float* logprob, bdlm_stream_t stream);
+
+/* Workspace (bytes, 256-byte aligned) of bdlm_unmask (its header alone). */
+BDLM_API size_t bdlm_unmask_workspace_bytes(void);
+
+/*
+ * bdlm_unmask - which rows keep the tokens that were drawn for them in this
+ *   denoising step.
+ *
+ *   tokens, sampled  int32 [total_rows]: the rows' present tokens (mask_id where
+ *                    there is none yet) and the drawn ones (< 0: none)
+ *   logprob          fp32 [total_rows]: the drawn ones' log-probabilities
+ *   cu_rows          as for the cache calls: DEVICE int32 [n_seqs + 1]
+ *   n_min            int32 [n_seqs] on the device, or NULL: n_min_all for all
+ *   threshold        fp32 [n_seqs] on the device, or NULL: threshold_all
+ *   out              int32 [total_rows], may be tokens itself
+ *   left             int32 [n_seqs]: rows of the sequence that are still masked
+ * Of a sequence's masked rows with a token those are kept whose logprob is at
+ * least the threshold (NaN: none) and, if they are fewer, the n_min of the
+ * largest logprob, of equal ones the first; a logprob of NaN comes last. out is
+ * the drawn token of kept rows and the present one of others. Rows behind
+ * cu_rows[n_seqs] are neither read nor written. Malformed offsets
+ * (BDLM_ERR_DEVICE_CHECK) leave their sequences' out and left unwritten.
+ */
+BDLM_API int bdlm_unmask(const int32_t* tokens, const int32_t* sampled, const float* logprob, int64_t total_rows,
+                  const int32_t* cu_rows, int32_t n_seqs, int32_t mask_id, const int32_t* n_min, int32_t n_min_all,
+                  const float* threshold, float threshold_all, int32_t* out, int32_t* left, void* workspace,
+                  size_t workspace_bytes, bdlm_stream_t stream);
 
 /* Synchronises `stream`, then returns the device error word of the last call
  * that used `workspace` (BDLM_OK, BDLM_ERR_TIMEOUT, BDLM_ERR_DEVICE_CHECK or
