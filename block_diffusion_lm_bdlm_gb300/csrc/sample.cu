@@ -30,6 +30,8 @@
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
 
+#include <utility>
+
 #include "sample.cuh"
 
 namespace bdlm {
@@ -128,36 +130,73 @@ __device__ __forceinline__ V warp_scan(V x) {  // inclusive
     return x;
 }
 
-// What is kept: tokens whose key is above `key`, and the first `ties` that have it.
-struct Cut {
-    uint32_t key;
-    long long ties;
-    float x;  // the logit of that key
-};
+using u64 = unsigned long long;
+
+// floor and ceiling of f * z, exactly; 0 <= f <= 1, z < 2^63.
+__device__ __forceinline__ u64 mul_floor(float f, u64 z, bool up = false) {
+    if (f >= 1.f) return z;
+    const uint32_t b = __float_as_uint(f);
+    const int e = imax((int)(b >> 23), 1);                      // f = mant 2^(e - 150)
+    const u64 mant = (b & 0x7fffffu) | (b >> 23 ? 0x800000u : 0u);
+    const u64 lo = mant * z, hi = __umul64hi(mant, z);
+    const int s = 150 - e;                                      // 24 <= s < 150
+    u64 got, rest;
+    if (s >= 128) {
+        got = 0;
+        rest = lo | hi;
+    } else if (s >= 64) {
+        got = hi >> (s - 64);
+        rest = lo | (hi & ((1ull << (s - 64)) - 1));
+    } else {
+        got = (hi << (64 - s)) | (lo >> s);
+        rest = lo & ((1ull << s) - 1);
+    }
+    return got + (up && rest ? 1 : 0);
+}
+__device__ __forceinline__ u64 mul_ceil(float f, u64 z) { return mul_floor(f, z, true); }
+
+constexpr int kList = kThreads;  // listed tokens of a row
+constexpr int kParts = kMaxCtas * kWarps;
+constexpr int kPer = kParts / 32;
 
 enum : int { COUNT = 0, MASS = 1 };
 
-// What a CTA shows the others of its cluster.
-struct Shown {
-    double quick[kWarps], whole[kWarps];  // per warp: quick weights at T, at T = 1
-    unsigned long long sum[kWarps];       // exact kept weights above the cut
-    int ties[kWarps];
-    float top;
-    unsigned int key_lo, key_hi;
-    int done;
+// What the cluster's CTAs tell each other: every CTA has all of it. Entry r * kWarps + w is of warp w of CTA r.
+struct All {
+    float top[kParts];   // largest logits of the threads in equal groups, 128 in the cluster
+    u64 quick[kParts];   // quick weights at T; later exact weights above the cut
+    u64 whole[kParts];   // quick weights at T = 1; later exact weights below the cut
+    int ties[kParts];    // tokens at the cut
+    u64 listed[kMaxCtas];  // weight and number of the listed tokens of each CTA
+    int n[kMaxCtas];
+    uint32_t key_lo[kMaxCtas], key_hi[kMaxCtas];
+    int done[kMaxCtas];
+};
+// The list of the row's first tokens, in the cluster's first CTA.
+struct List {
+    uint2 raw[kList];  // key, number; each CTA has an equal part of it
+    u64 order[kList], w[kList], kept[kList];
+};
+// Bins of a select; the list is done with by then.
+struct Bins {
+    uint32_t n[kBins];
+};
+union Work {
+    List list;
+    Bins bins;
 };
 
 template <typename T>
 struct Row {
     static constexpr int VE = Type<T>::VE, SHIFT = Type<T>::SHIFT;
-    uint4* data;       // this CTA's part, as 16-byte vectors
-    uint32_t* hist;    // [3][kBins]
-    Shown* shown;
+    uint4* data;  // this CTA's part, as 16-byte vectors
+    All* all;
+    Work* work;
     const F2* table;
-    unsigned long long* scan;  // [kWarps]
-    int* found;
+    u64* scan;   // [kWarps]
+    u64* found;  // [2]
     int nv, vw;  // vectors; vectors of each warp, a multiple of 32
-    int C;
+    int C, rank;
     float m, c2;  // largest logit; -2 log2(e) / T
     F2 c;
     float mine;  // largest logit of this thread
@@ -167,14 +206,18 @@ struct Row {
         const uint32_t u = k << SHIFT;
         return __uint_as_float(u & 0x80000000u ? u ^ 0x80000000u : ~(u | ((1u << SHIFT) - 1u)));
     }
-    __device__ __forceinline__ uint64_t exact(float x) const { return exact_weight(x, m, c, table); }
-    // a row's distance from the largest logit in octaves of weight, negative
-    __device__ __forceinline__ float octaves(float x) const { return fmaf(-0.5f, x, 0.5f * m) * c2; }
+    __device__ __forceinline__ u64 exact(float x) const { return exact_weight(x, m, c, table); }
     __device__ __forceinline__ int bin_of(float x) const {
-        const float t = octaves(x) * -kBinsPerOctave;
+        const float t = fmaf(-0.5f, x, 0.5f * m) * (c2 * -kBinsPerOctave);
         return t < (float)(kBins - 1) ? (int)t : kBins - 1;
     }
-    // f(v, x) for the vectors of this thread; skips those without a logit of at least `least`
+    // Tells every CTA of the cluster a value for this warp; all lanes hold it.
+    template <typename V>
+    __device__ __forceinline__ void tell(cg::cluster_group& cl, V* where, V x) const {
+        const int lane = threadIdx.x & 31;
+        if (lane < C) cl.map_shared_rank(where, lane)[rank * kWarps + (threadIdx.x >> 5)] = x;
+    }
+    // f(v, x) for the vectors of this thread, without those that have no logit of at least `least`
     template <typename F>
     __device__ __forceinline__ void each(float least, F f) const {
         const int lane = threadIdx.x & 31, v0 = (threadIdx.x >> 5) * vw, v1 = imin(nv, v0 + vw);
@@ -186,89 +229,93 @@ struct Row {
             f(v, x);
         }
     }
-    // Adds up the cluster's bins, in which each thread looks after one; returns this bin's sum and the sum of those
-    // before it, and their total. `n` bins are in use. All of the cluster's CTAs have filled theirs.
-    template <int MODE>
-    __device__ __forceinline__ unsigned long long gather(cg::cluster_group& cl, int n, unsigned long long& before,
-                                                         unsigned long long& total) {
-        const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
-        unsigned long long s = 0;
-        if (t < n)
-            for (int r = 0; r < C; ++r) {
-                const uint32_t* h = cl.map_shared_rank(hist, r);
-                if (MODE == COUNT) s += h[t];
-                else s += (unsigned long long)h[t] + ((unsigned long long)h[kBins + t] << 15) + ((unsigned long long)h[2 * kBins + t] << 30);
-            }
-        const unsigned long long in = warp_scan(s);
-        if (lane == 31) scan[warp] = in;
-        __syncthreads();
-        before = in - s;
-        total = 0;
-        for (int w = 0; w < kWarps; ++w) {
-            const unsigned long long y = scan[w];
-            if (w < warp) before += y;
-            total += y;
-        }
-        __syncthreads();
-        return s;
-    }
-    template <int MODE>
     __device__ __forceinline__ void clear() {
-        for (int i = threadIdx.x; i < (MODE == COUNT ? 1 : 3) * kBins; i += kThreads) hist[i] = 0;
-        if (threadIdx.x == 0) *found = kBins;
+        for (int i = threadIdx.x; i < kBins; i += kThreads) work->bins.n[i] = 0;
         __syncthreads();
     }
+    // MASS: the quick weight in units of 2^-16 of the bin's largest
     template <int MODE>
-    __device__ __forceinline__ void add(int b, float x) {
+    __device__ __forceinline__ void add(int at, int bin, float x) {
         if (MODE == COUNT) {
-            atomicAdd(hist + b, 1u);
-        } else {  // 15 bits each, so that 2^17 of them fit
-            const uint64_t w = exact(x);
-            if (const uint32_t p = (uint32_t)w & 0x7fffu) atomicAdd(hist + b, p);
-            if (const uint32_t p = (uint32_t)(w >> 15) & 0x7fffu) atomicAdd(hist + kBins + b, p);
-            if (const uint32_t p = (uint32_t)(w >> 30)) atomicAdd(hist + 2 * kBins + b, p);
+            atomicAdd(&work->bins.n[at], 1u);
+        } else {
+            const float t = fmaf(-0.5f, x, 0.5f * m) * c2 + (float)bin * (1.f / kBinsPerOctave);
+            atomicAdd(&work->bins.n[at], (uint32_t)__float2int_rn(ex2(t) * 65536.f));
         }
+    }
+    // Adds up the cluster's bins, each thread one, and finds the one in which the sum from `base` on passes the target:
+    // its number, and in *before the sum of those before it. Bin i holds weights of octave bin `bin0` + i (MASS, first
+    // level) or of `bin0` alone. A target that none passes is taken to be passed by the last bin with anything in it.
+    template <int MODE>
+    __device__ __forceinline__ int cross(cg::cluster_group& cl, int n, int bin0, bool spread, u64 target, u64 base, u64* before) {
+        const int t = threadIdx.x, lane = t & 31, warp = t >> 5;
+        u64 s = 0;
+        if (t < n) {
+#pragma unroll
+            for (int r = 0; r < kMaxCtas; ++r)
+                if (r < C) s += cl.map_shared_rank(&work->bins, r)->n[t];
+        }
+        if (MODE == MASS) {
+            const int b = spread ? bin0 + t : bin0;
+            // 2^16 weights of the bin's largest, 2^(-b / 8), in units of 2^-44
+            const int j = -(b & 7) * 2, shift = b >> 3;
+            const float top = table[j < -8 ? j + 24 : j + 8].hi;  // 2^(j / 16), or twice that below -8
+            const u64 f = (u64)__float2uint_rn(top * 65536.f) << (j < -8 ? 11 : 12);
+            s = shift < 44 ? (s * f) >> shift : 0;
+        }
+        const u64 in = warp_scan(s);
+        if (lane == 31) scan[warp] = in;
+        if (t == 0) found[0] = 0;
+        __syncthreads();
+        u64 at = base + in - s;
+        for (int w = 0; w < kWarps; ++w)
+            if (w < warp) at += scan[w];
+        // the bin that passes the target, else the last one with anything in it: the largest of (passes, ~number | number)
+        const bool passes = at < target && at + s >= target;
+        unsigned key = passes ? 0x80000000u | t : s > 0 ? (unsigned)t + 1 : 0u;
+        const unsigned top = __reduce_max_sync(0xffffffffu, key);
+        if (lane == 0 && top) atomicMax(reinterpret_cast<unsigned*>(found), top);
+        __syncthreads();
+        const unsigned got = *reinterpret_cast<unsigned*>(found);
+        const int bin = got & 0x80000000u ? (int)(got & 0x7fffffffu) : imax(0, (int)got - 1);
+        if (t == bin) found[1] = at;
+        __syncthreads();
+        *before = found[1];
+        return bin;
     }
 
-    // The cut of the tokens from key `floor` on at `target` (tokens, or weight in units of 2^-44), which is known to
-    // within `off`: a token is kept if those before it are less than the target. False if `off` leaves it open.
+    // The key of the token at which the sum over falling logits, of tokens (COUNT) or of quick weights (MASS), passes the
+    // target; only tokens from key `floor` on count. *before (COUNT): tokens above that key.
     template <int MODE>
-    __device__ bool select(cg::cluster_group& cl, double target, double off, uint32_t floor, float floor_x, Cut* cut) {
-        unsigned long long before, total, s;
-        // The threads' largest logits alone reach the target by bin `last`, so the cut lies no further.
-        clear<MODE>();
-        if (mine > -INFINITY && key_of(mine) >= floor) add<MODE>(bin_of(mine), mine);
+    __device__ __forceinline__ uint32_t select(cg::cluster_group& cl, u64 target, uint32_t floor, float floor_x, u64* before) {
+        // The threads' largest logits alone pass the target by bin `last`, so the cut lies no further.
         cl.sync();
-        s = gather<MODE>(cl, kBins, before, total);
-        if ((double)before < target + off && (double)(before + s) >= target + off) *found = threadIdx.x;
-        __syncthreads();
-        const int last = imin(*found, kBins - 1);
+        clear();
+        if (mine > -INFINITY && key_of(mine) >= floor) add<MODE>(bin_of(mine), bin_of(mine), mine);
+        cl.sync();
+        u64 base;
+        int last = cross<MODE>(cl, kBins, 0, true, MODE == MASS ? target + (target >> 14) : target, 0, &base);
+        {  // (`last` may be the last filled bin without passing)
+            const unsigned got = *reinterpret_cast<unsigned*>(found);
+            if (!(got & 0x80000000u)) last = kBins - 1;
+        }
         // no logit below this one lies in bin `last` (c2 is negative; the margin covers roundings)
         const float edge = last == kBins - 1 ? -INFINITY : m + (last + 1.01f) * 2.f / (kBinsPerOctave * c2) - fabsf(m) * 0x1p-20f;
-        const float least = fmaxf(edge, floor_x);
+        float least = fmaxf(edge, floor_x);
         cl.sync();
-        clear<MODE>();
+        clear();
         each(least, [&](int, const float(&x)[VE]) {
 #pragma unroll
             for (int e = 0; e < VE; ++e) {
                 if (!(x[e] >= least) || key_of(x[e]) < floor) continue;
                 const int b = bin_of(x[e]);
-                if (b <= last) add<MODE>(b, x[e]);
+                if (b <= last) add<MODE>(b, b, x[e]);
             }
         });
         cl.sync();
-        s = gather<MODE>(cl, last + 1, before, total);
-        if ((double)before < target && (double)(before + s) >= target) {
-            *found = threadIdx.x;
-            scan[0] = before;
-            if ((double)before >= target - off || (double)(before + s) < target + off) *found = kBins + 1;
-        }
-        __syncthreads();
-        const int bin = *found;
-        unsigned long long base = scan[0];
-        if (bin >= kBins) return false;
+        const int bin = cross<MODE>(cl, last + 1, 0, true, target, 0, &base);
         // the keys of that bin
-        unsigned lo = 0xffffffffu, hi = 0;
+        uint32_t lo = 0xffffffffu, hi = 0;
         each(least, [&](int, const float(&x)[VE]) {
 #pragma unroll
             for (int e = 0; e < VE; ++e) {
@@ -279,94 +326,125 @@ struct Row {
                 hi = max(hi, k);
             }
         });
-        lo = __reduce_min_sync(0xffffffffu, lo);
-        hi = __reduce_max_sync(0xffffffffu, hi);
-        if (threadIdx.x == 0) {
-            shown->key_lo = 0xffffffffu;
-            shown->key_hi = 0;
-        }
-        __syncthreads();
-        if ((threadIdx.x & 31) == 0) {
-            atomicMin(&shown->key_lo, lo);
-            atomicMax(&shown->key_hi, hi);
-        }
-        cl.sync();
-        for (int r = 0; r < C; ++r) {
-            const Shown* o = cl.map_shared_rank(shown, r);
-            lo = min(lo, o->key_lo);
-            hi = max(hi, o->key_hi);
-        }
-        const float x_lo = at_key(lo);
+        span(cl, lo, hi);
+        least = at_key(lo);
         while (lo < hi) {
             const int shift = imax(0, 32 - __clz(hi - lo) - 9);
             const int n = (int)((hi - lo) >> shift) + 1;
-            clear<MODE>();
-            each(x_lo, [&](int, const float(&x)[VE]) {
+            clear();
+            each(least, [&](int, const float(&x)[VE]) {
 #pragma unroll
                 for (int e = 0; e < VE; ++e) {
-                    if (!(x[e] >= x_lo)) continue;
                     const uint32_t k = key_of(x[e]);
-                    if (k < lo || k > hi) continue;
-                    add<MODE>((int)((hi - k) >> shift), x[e]);
+                    if (x[e] >= least && k >= lo && k <= hi) add<MODE>((int)((hi - k) >> shift), bin, x[e]);
                 }
             });
             cl.sync();
-            s = gather<MODE>(cl, n, before, total);
-            before += base;
-            if ((double)before < target && (double)(before + s) >= target) {
-                *found = threadIdx.x;
-                scan[0] = before;
-                if ((double)before >= target - off || (double)(before + s) < target + off) *found = kBins + 1;
-            }
-            __syncthreads();
-            const int sub = *found;
-            base = scan[0];
-            cl.sync();  // the bins are filled anew
-            if (sub >= kBins) return false;
+            const int sub = cross<MODE>(cl, n, bin, false, target, base, &base);
             hi -= (uint32_t)sub << shift;
             lo = max(lo, hi - ((1u << shift) - 1u));
+            cl.sync();  // the bins are filled anew
         }
-        cut->key = hi;
-        cut->x = at_key(hi);
-        const double w = MODE == COUNT ? 1.0 : (double)exact(cut->x);
-        const double rest = target - (double)base;
-        cut->ties = (long long)ceil(rest / w);
-        return off == 0.0 || (ceil((rest - off) / w) == ceil((rest + off) / w) && rest - off > 0.0);
+        *before = base;
+        return hi;
+    }
+    // The least and the largest of the cluster's keys.
+    __device__ __forceinline__ void span(cg::cluster_group& cl, uint32_t& lo, uint32_t& hi) {
+        lo = __reduce_min_sync(0xffffffffu, lo);
+        hi = __reduce_max_sync(0xffffffffu, hi);
+        uint32_t* mm = reinterpret_cast<uint32_t*>(found);
+        if (threadIdx.x == 0) {
+            mm[0] = 0xffffffffu;
+            mm[1] = 0;
+        }
+        __syncthreads();
+        const int lane = threadIdx.x & 31;
+        if (lane == 0) {
+            atomicMin(mm, lo);
+            atomicMax(mm + 1, hi);
+        }
+        __syncthreads();
+        if (threadIdx.x < C) {
+            All* o = cl.map_shared_rank(all, threadIdx.x);
+            o->key_lo[rank] = mm[0];
+            o->key_hi[rank] = mm[1];
+        }
+        cl.sync();
+        lo = __reduce_min_sync(0xffffffffu, all->key_lo[lane % C]);
+        hi = __reduce_max_sync(0xffffffffu, all->key_hi[lane % C]);
     }
 
-    // Exact weights of the tokens above the cut and the numbers of those at it, per warp, shown to the cluster.
-    __device__ __forceinline__ void show_kept(cg::cluster_group& cl, const Cut& cut) {
-        unsigned long long s = 0;
-        int n = 0;
-        each(cut.x, [&](int, const float(&x)[VE]) {
+    // The least key above `cut`, or the largest below it, in the row.
+    __device__ __forceinline__ uint32_t next_key(cg::cluster_group& cl, uint32_t cut, bool up) {
+        uint32_t lo = 0xffffffffu, hi = 0;
+        each(-INFINITY, [&](int, const float(&x)[VE]) {
 #pragma unroll
             for (int e = 0; e < VE; ++e) {
                 const uint32_t k = key_of(x[e]);
-                if (k > cut.key && x[e] > -INFINITY) s += exact(x[e]);
-                else if (k == cut.key) ++n;
+                if (k > cut) lo = min(lo, k);
+                if (k < cut) hi = max(hi, k);
             }
         });
-        s = warp_sum(s);
-        n = (int)__reduce_add_sync(0xffffffffu, (unsigned)n);
-        if ((threadIdx.x & 31) == 0) {
-            shown->sum[threadIdx.x >> 5] = s;
-            shown->ties[threadIdx.x >> 5] = n;
+        span(cl, lo, hi);
+        return up ? lo : hi;
+    }
+    // The least key whose weight is at least w (1 <= w <= 2^44): 32 keys at a time.
+    __device__ __forceinline__ uint32_t key_from(u64 w) const {
+        const int lane = threadIdx.x & 31;
+        uint32_t lo = key_of(-INFINITY), hi = key_of(m);  // of lo the weight is less, of hi it is not
+        while (hi - lo > 1) {
+            const uint32_t step = (hi - lo - 1) / 32 + 1, k = lo + (uint32_t)(lane + 1) * step;
+            const bool has = k >= hi || k < lo || exact(at_key(k)) >= w;
+            const int l = __ffs(__ballot_sync(0xffffffffu, has)) - 1;  // (the last lane's key is not below hi)
+            const uint32_t top = lo + (uint32_t)(l + 1) * step;
+            lo += (uint32_t)l * step;
+            hi = top < hi && top > lo ? top : hi;
         }
+        return hi;
+    }
+
+    // Exact weights of the tokens above key `cut` (in all->quick) and, if they are wanted, below it (all->whole), and the
+    // numbers of those at it, of every warp of the cluster.
+    __device__ __forceinline__ void weigh(cg::cluster_group& cl, uint32_t cut, bool below) {
+        u64 s = 0, z = 0;
+        int n = 0;
+        cl.sync();  // what is told is read no more
+        each(below || cut == 0 ? -INFINITY : at_key(cut), [&](int, const float(&x)[VE]) {
+#pragma unroll
+            for (int e = 0; e < VE; ++e) {
+                const uint32_t k = key_of(x[e]);
+                if (k == cut) {
+                    ++n;
+                } else if (k > cut || below) {
+                    const u64 w = exact(x[e]);
+                    if (k > cut) s += w;
+                    else z += w;
+                }
+            }
+        });
+        tell(cl, all->quick, warp_sum(s));
+        tell(cl, all->ties, (int)__reduce_add_sync(0xffffffffu, (unsigned)n));
+        if (below) tell(cl, all->whole, warp_sum(z));
         cl.sync();
     }
-    // The weight of what the cut keeps.
-    __device__ __forceinline__ unsigned long long kept_weight(cg::cluster_group& cl, const Cut& cut) {
-        unsigned long long s = 0;
-        long long n = 0;
-        for (int r = 0; r < C; ++r) {
-            const Shown* o = cl.map_shared_rank(shown, r);
-            for (int w = 0; w < kWarps; ++w) {
-                s += o->sum[w];
-                n += o->ties[w];
-            }
-        }
-        n = n < cut.ties ? n : cut.ties;
-        return s + (unsigned long long)n * exact(cut.x);
+    __device__ __forceinline__ u64 total(const u64* of) const {
+        u64 s = 0;
+        for (int i = threadIdx.x & 31; i < C * kWarps; i += 32) s += of[i];
+        return warp_sum(s);
+    }
+    __device__ __forceinline__ long long total_ties() const {
+        int n = 0;
+        for (int i = threadIdx.x & 31; i < C * kWarps; i += 32) n += all->ties[i];
+        return (int)__reduce_add_sync(0xffffffffu, (unsigned)n);
+    }
+    __device__ __forceinline__ u64 cta_sum(u64 x) {
+        x = warp_sum(x);
+        __syncthreads();
+        if ((threadIdx.x & 31) == 0) scan[threadIdx.x >> 5] = x;
+        __syncthreads();
+        u64 s = 0;
+        for (int w = 0; w < kWarps; ++w) s += scan[w];
+        return s;
     }
 };
 
@@ -374,38 +452,33 @@ template <typename T>
 __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a) {
     constexpr int VE = Type<T>::VE;
     extern __shared__ uint4 s_data[];
-    __shared__ Shown s_shown;
-    __shared__ uint32_t s_hist[3 * kBins];
+    __shared__ All s_all;
+    __shared__ Work s_work;
     __shared__ F2 s_table[kTable];
-    __shared__ unsigned long long s_scan[kWarps];
-    __shared__ float s_top[kWarps];
-    __shared__ int s_found;
+    __shared__ u64 s_scan[kWarps], s_found[2];
+    __shared__ int s_n;
+    __shared__ u64 s_listed;
     cg::cluster_group cl = cg::this_cluster();
+    // (rows that are left leave with all of their CTAs)
     const int rank = (int)cl.block_rank(), row = blockIdx.x / a.ctas;
     if (a.now && __ldg(a.now + row) != a.want) return;
+    auto started = cl.barrier_arrive();
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    if (tid < kTable) {
-        constexpr F2 t[kTable] = {BDLM_POW2_TABLE};
-        F2 v = t[0];
-#pragma unroll
-        for (int i = 1; i < kTable; ++i)
-            if (tid == i) v = t[i];
-        s_table[tid] = v;
-    }
     const int first = rank * a.per, n = imax(0, imin(a.per, a.vocab - first));
     const T* src = static_cast<const T*>(a.x) + (long long)row * a.stride + first;
     const int skew = (int)((reinterpret_cast<uintptr_t>(src) & 15) / sizeof(T));  // elements before ours in the first vector
 
     Row<T> R;
     R.data = s_data;
-    R.hist = s_hist;
-    R.shown = &s_shown;
+    R.all = &s_all;
+    R.work = &s_work;
     R.table = s_table;
     R.scan = s_scan;
-    R.found = &s_found;
+    R.found = s_found;
     R.nv = n ? (skew + n + VE - 1) / VE : 0;
     R.vw = ((R.nv + kWarps - 1) / kWarps + 31) & ~31;
     R.C = a.ctas;
+    R.rank = rank;
     const int v0 = warp * R.vw, v1 = imin(R.nv, v0 + R.vw);
     // Each thread copies the vectors that it will read, so it need only wait for its own.
     for (int v = v0 + lane; v < v1; v += 32) {
@@ -419,42 +492,67 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
             for (int e = 0; e < VE; ++e) dst[e] = e0 + e >= 0 && e0 + e < n ? src[e0 + e] : value_of<T>(-INFINITY);
         }
     }
+    if (tid < kTable) {
+        constexpr F2 t[kTable] = {BDLM_POW2_TABLE};
+        F2 v = t[0];
+#pragma unroll
+        for (int i = 1; i < kTable; ++i)
+            if (tid == i) v = t[i];
+        s_table[tid] = v;
+    }
+    if (tid == 0) {
+        s_n = 0;
+        s_listed = 0;
+    }
     const float temp = a.temperature ? __ldg(a.temperature + row) : a.temperature_all;
     const int top_k = a.top_k ? __ldg(a.top_k + row) : a.top_k_all;
     const float top_p = a.top_p ? __ldg(a.top_p + row) : a.top_p_all;
     const float min_p = a.min_p ? __ldg(a.min_p + row) : a.min_p_all;
     const float u = fminf(fmaxf(__ldg(a.u + row), 0.f), 1.f);
-    const bool greedy = !(temp >= kGreedyBelow);
-    const double cd = 2.8853900817779268 / (double)(greedy ? 1.f : fminf(temp, kHottest));
-    R.c = F2{(float)cd, (float)(cd - (double)(float)cd)};
-    R.c2 = -(float)cd;
+    const bool greedy = !(temp >= kGreedyBelow) || top_p <= 0.f;  // the first of the largest
+    const bool by_k = !greedy && top_k > 0 && top_k < a.vocab, by_p = !greedy && top_p < 1.f, by_min = !greedy && min_p > 0.f;
+    const bool cuts = greedy || by_k || by_p || by_min;
+    const float T_ = greedy ? 1.f : fminf(temp, kHottest), p = top_p;
+    {  // 2 log2(e) / T in two floats: the remainder of the quotient of the high parts, and the low parts
+        constexpr float hi = 0x1.715476p+1f, lo = 0x1.4ae0c0p-25f;  // 2 log2(e)
+        const float q = __fdiv_rn(hi, T_);
+        R.c = F2{q, __fdiv_rn(__fmaf_rn(-q, T_, hi) + lo, T_)};
+        R.c2 = -q;
+    }
     asm volatile("cp.async.wait_all;" ::: "memory");
 
     // ---- the largest logit
     R.mine = -INFINITY;
     for (int v = v0 + lane; v < v1; v += 32) R.mine = fmaxf(R.mine, top_of<T>(s_data[v]));
     {
-        const float x = warp_max(R.mine);
-        if (lane == 0) s_top[warp] = x;
-        __syncthreads();
-        if (tid == 0) {
-            float y = s_top[0];
-            for (int w = 1; w < kWarps; ++w) y = fmaxf(y, s_top[w]);
-            s_shown.top = y;
-        }
-        cl.sync();
-        R.m = -INFINITY;
-        for (int r = 0; r < a.ctas; ++r) R.m = fmaxf(R.m, cl.map_shared_rank(&s_shown, r)->top);
+        const int groups = kMaxCtas / a.ctas;  // of a warp's lanes
+        float x = R.mine;
+        for (int o = 1; o < 32 / groups; o *= 2) x = fmaxf(x, __shfl_xor_sync(0xffffffffu, x, o));
+        cl.barrier_wait(std::move(started));  // every CTA's shared memory is there
+        if (lane % (32 / groups) == 0)
+            for (int r = 0; r < a.ctas; ++r) cl.map_shared_rank(s_all.top, r)[(rank * kWarps + warp) * groups + lane / (32 / groups)] = x;
     }
+    cl.sync();
+    float tops[kPer];
+    R.m = -INFINITY;
+#pragma unroll
+    for (int k = 0; k < kPer; ++k) {
+        tops[k] = s_all.top[k * 32 + lane];
+        R.m = fmaxf(R.m, tops[k]);
+    }
+    R.m = warp_max(R.m);
     if (R.m == -INFINITY) {  // nothing is left to choose from
         if (rank == 0 && tid == 0) {
             a.token[row] = -1;
             a.logprob[row] = -INFINITY;
         }
-        cl.sync();  // the others may still read what this CTA shows
         return;
     }
-    if (R.m == INFINITY) {  // the infinite logits share everything
+    // Tokens from x0 on are listed: the k-th largest of the 128 maxima has at least k tokens from it on, and the 80th, where
+    // weights decide, about 125. A list that turns out too short or too long is not used.
+    float x0 = R.m;
+    const bool infinite = R.m == INFINITY;
+    if (infinite) {  // the infinite logits share everything
         R.mine = -INFINITY;
         for (int v = v0 + lane; v < v1; v += 32) {
             T* x = reinterpret_cast<T*>(s_data + v);
@@ -464,20 +562,38 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
                 if (top) R.mine = 0.f;
             }
         }
-        R.m = 0.f;
+        R.m = x0 = 0.f;
+    } else if (!greedy && cuts) {
+        const int want = by_k ? imin(top_k, 120) : 80;
+        uint32_t key = 0;
+#pragma unroll 1
+        for (int bit = 31; bit >= 16; --bit) {
+            const uint32_t next = key | 1u << bit;
+            int have = 0;
+#pragma unroll
+            for (int k = 0; k < kPer; ++k) have += __popc(__ballot_sync(0xffffffffu, order_key(__float_as_uint(tops[k])) >= next));
+            if (have >= want) key = next;
+        }
+        x0 = __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key);
+        x0 = x0 == x0 ? fminf(x0, R.m) : -INFINITY;  // (fewer groups have anything: the key is below that of -infinity)
+        if (by_min && !by_k && !by_p)  // a little below what min-p keeps
+            x0 = fmaxf(x0, R.m + T_ * __logf(fminf(min_p, 1.f)) - fabsf(R.m) * 0x1p-10f - T_ * 0x1p-6f);
+        if (!(x0 > -INFINITY)) x0 = -3.402823466e38f;
     }
 
     // ---- sums of the quick weights, at T = 1 for the log-probability and, where they are asked for, at T
-    const bool by_k = !greedy && top_k > 0 && top_k < a.vocab, by_p = !greedy && top_p < 1.f, by_min = !greedy && min_p > 0.f;
     const bool quick = !greedy && !by_k && (by_p || !by_min);
     const bool two = quick && temp != 1.f;
-    double quick_z = 0.0, whole_z = 0.0;
+    u64 quick_z = 0, whole_z = 0;
+    List& list = s_work.list;
     for (int turn = 0;; ++turn) {
         const float half_m = 0.5f * R.m, c1 = -2.8853900817779268f;
         float s1 = 0.f, st = 0.f;
+        u64 mine = 0;
         for (int v = v0 + lane; v < v1; v += 32) {
+            const uint4 raw = s_data[v];
             float x[VE], y = 0.f, yt = 0.f;
-            unpack<T>(s_data[v], x);
+            unpack<T>(raw, x);
 #pragma unroll
             for (int e = 0; e < VE; e += 2) {
                 const float h0 = fmaf(-0.5f, x[e], half_m), h1 = fmaf(-0.5f, x[e + 1], half_m);
@@ -486,220 +602,356 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
             }
             s1 += y;
             st += yt;
+            if (cuts && top_of<T>(raw) >= x0) {
+#pragma unroll
+                for (int e = 0; e < VE; ++e)
+                    if (x[e] >= x0) {
+                        const int i = atomicAdd(&s_n, 1);
+                        mine += R.exact(x[e]);
+                        if (i < kList / a.ctas)
+                            cl.map_shared_rank(&s_work.list, 0)->raw[rank * (kList / a.ctas) + i] =
+                                make_uint2(order_key(__float_as_uint(x[e])), (uint32_t)(first + v * VE + e - skew));
+                    }
+            }
         }
-        const double w1 = warp_sum((double)s1), wt = two ? warp_sum((double)st) : w1;
-        if (lane == 0) {
-            s_shown.whole[warp] = w1;
-            s_shown.quick[warp] = wt;
+        const bool nan = s1 != s1;
+        const u64 w1 = warp_sum(nan ? 0ull : (u64)__float2ull_rn(s1 * 0x1p44f)), wt = two ? warp_sum((u64)__float2ull_rn(st * 0x1p44f)) : w1;
+        R.tell(cl, s_all.whole, __any_sync(0xffffffffu, nan) ? ~0ull : w1);
+        R.tell(cl, s_all.quick, wt);
+        if (cuts) {
+            mine = warp_sum(mine);
+            if (lane == 0 && mine) atomicAdd(&s_listed, mine);
+            __syncthreads();
+            if (tid < a.ctas) {
+                All* o = cl.map_shared_rank(&s_all, tid);
+                o->listed[rank] = s_listed;
+                o->n[rank] = s_n;
+            }
+        } else if (tid < a.ctas) {
+            cl.map_shared_rank(&s_all, tid)->done[rank] = 0;
         }
         cl.sync();
-        whole_z = quick_z = 0.0;
+        whole_z = quick_z = 0;
+        bool bad = false;
         for (int i = lane; i < a.ctas * kWarps; i += 32) {
-            const Shown* o = cl.map_shared_rank(&s_shown, i / kWarps);
-            whole_z += o->whole[i % kWarps];
-            quick_z += o->quick[i % kWarps];
+            const u64 y = s_all.whole[i];
+            bad = bad || y == ~0ull;
+            whole_z += y;
+            quick_z += s_all.quick[i];
         }
-        whole_z = warp_sum(whole_z);
-        quick_z = warp_sum(quick_z);
-        if (whole_z == whole_z || turn == 1) break;
+        if (!__any_sync(0xffffffffu, bad)) break;
         // a NaN counts as a logit of -infinity
-        cl.sync();
         for (int v = v0 + lane; v < v1; v += 32) {
             T* x = reinterpret_cast<T*>(s_data + v);
             for (int e = 0; e < VE; ++e)
                 if ((float)x[e] != (float)x[e]) x[e] = value_of<T>(-INFINITY);
         }
+        cl.sync();
+        if (tid == 0) {
+            s_n = 0;
+            s_listed = 0;
+        }
+        __syncthreads();
     }
+    whole_z = warp_sum(whole_z);
+    quick_z = warp_sum(quick_z);
+    const u64 off = (u64)((float)quick_z * (float)kQuick) + 1;
+    const u64 least_w = by_min ? mul_ceil(fminf(min_p, 1.f), 1ull << kFrac) : 0;  // min-p keeps weights from here on
 
-    // ---- the cut
-    Cut cut{0, 0, -INFINITY};
-    const double unit = 17592186044416.0;  // 2^44
-    if (greedy) {
-        cut = Cut{R.key_of(R.m), 1, R.m};
-    } else {
-        if (by_k) {
-            R.template select<COUNT>(cl, (double)top_k, 0.0, 0u, -INFINITY, &cut);
-            if (by_p) R.show_kept(cl, cut);
-        }
-        if (by_p) {
-            Cut by{0, 0, -INFINITY};
-            double z = quick_z * unit, off = quick_z * unit * kQuick;
-            if (by_k) {
-                z = (double)R.kept_weight(cl, cut);
-                off = 0.0;
-            }
-            const double p = (double)fmaxf(top_p, 0.f);
-            bool sure = false;
-            if (p == 0.0) {
-                by = Cut{R.key_of(R.m), 1, R.m};
-                sure = true;
-            } else if (off == 0.0 || p * off < 0.25 * p * z) {
-                sure = R.template select<MASS>(cl, p * z, p * off, cut.key, cut.x, &by);
-            }
-            if (!sure) {  // the sum of all weights again, exactly
-                cl.sync();
-                R.show_kept(cl, cut);
-                z = (double)R.kept_weight(cl, cut);
-                R.template select<MASS>(cl, p * z, 0.0, cut.key, cut.x, &by);
-            }
-            if (by.key > cut.key || !by_k) cut = by;
-            else cut.ties = by.ties < cut.ties ? by.ties : cut.ties;
-        }
-        if (by_min) {
-            const double thr = (double)R.m + (double)fminf(temp, kHottest) * log((double)fminf(min_p, 1.f));
-            const float x = fminf(__double2float_ru(thr), R.m);
-            // the least value of the type that is not below it
-            uint32_t k = R.key_of(x);
-            if (R.at_key(k) < x) ++k;
-            if (k > cut.key) cut = Cut{k, 1LL << 40, R.at_key(k)};
-        }
-    }
-
-    // ---- the token
     int token = -1;
     float at = 0.f;
-    bool mine = false;
-    bool done = false;
-    if (!greedy && !by_k && !by_p && !by_min) {
-        // all tokens, by quick weights
-        const double target = (double)u * quick_z, slack = 2.0 * kQuick * quick_z;
-        double sum = 0.0;
-        int who = -1;
-        double base = 0.0;
-        for (int i = 0; i < a.ctas * kWarps; ++i) {
-            const double y = cl.map_shared_rank(&s_shown, i / kWarps)->quick[i % kWarps];
-            if (who < 0 && sum + y > target) {
-                who = i;
-                base = sum;
-            }
-            sum += y;
+    bool mine = false;  // this thread has the token
+    // ---- the list, if all that may be kept is in it
+    bool listed = cuts;
+    int ln = 0;
+    if (cuts) {
+        u64 lw = 0;
+        for (int r = 0; r < a.ctas; ++r) {
+            listed = listed && s_all.n[r] <= kList / a.ctas;
+            ln += s_all.n[r];
+            lw += s_all.listed[r];
         }
-        if (tid == 0) s_shown.done = 0;
+        const bool by_min_all = by_min && R.exact(x0) < least_w;
+        if (!greedy)
+            listed = listed && (by_min_all || (by_k ? ln >= top_k : by_p && lw >= mul_ceil(p, quick_z + off)));
+    }
+    if (listed) {
+        if (rank != 0) return;
+        u64 me = 0, w = 0;
+        if (tid < ln) {
+            int i = tid, r = 0;
+            for (; i >= s_all.n[r]; ++r) i -= s_all.n[r];
+            const uint2 y = list.raw[r * (kList / a.ctas) + i];
+            list.order[tid] = (u64)y.x << 32 | ~y.y;
+            list.w[tid] = R.exact(__uint_as_float(y.x & 0x80000000u ? y.x ^ 0x80000000u : ~y.x));
+        }
         __syncthreads();
-        if (who >= 0 && who == rank * kWarps + warp) {
-            for (int vb = v0; vb < v1; vb += 32) {
-                const int v = vb + lane;
-                float x[VE], w[VE];
-                double s = 0.0;
-                if (v < v1) {
-                    unpack<T>(s_data[v], x);
-#pragma unroll
-                    for (int e = 0; e < VE; ++e) {
-                        w[e] = ex2(fmaf(-0.5f, x[e], 0.5f * R.m) * R.c2);
-                        s += w[e];
-                    }
+        // G threads for each token, each looks at every G-th other
+        int G = 1;
+        while (2 * G * ln <= kThreads && G < 32) G *= 2;
+        const int i = tid / G, g = tid % G;
+        u64 before = 0;
+        int ahead = 0;
+        if (i < ln) {
+            me = list.order[i];
+            w = list.w[i];
+            for (int j = g; j < ln; j += G)
+                if (list.order[j] > me) {
+                    before += list.w[j];
+                    ++ahead;
                 }
-                const double in = warp_scan(s) + base;
-                const unsigned hit = __ballot_sync(0xffffffffu, in > target);
-                if (hit) {
-                    if (lane == __ffs(hit) - 1) {
-                        double run = in - s;
+        }
+        for (int o = 1; o < G; o *= 2) {
+            before += __shfl_xor_sync(0xffffffffu, before, o);
+            ahead += __shfl_xor_sync(0xffffffffu, ahead, o);
+        }
+        bool keep = i < ln && (greedy ? ahead == 0 : !by_k || ahead < top_k);
+        if (by_p) {
+            u64 lo, hi;
+            if (by_k) {
+                lo = hi = mul_ceil(p, R.cta_sum(keep && g == 0 ? w : 0));
+            } else {
+                lo = mul_ceil(p, quick_z - off);
+                hi = mul_ceil(p, quick_z + off);
+                if (__syncthreads_or(keep && ahead > 0 && before >= lo && before < hi)) {
+                    // the sum of all weights exactly, from the row itself: the other CTAs are gone
+                    const T* x = static_cast<const T*>(a.x) + (long long)row * a.stride;
+                    u64 s = 0;
+                    for (int j = tid; j < a.vocab; j += kThreads) {
+                        float y = (float)x[j];
+                        if (infinite) y = y == INFINITY ? 0.f : -INFINITY;
+                        if (y > -INFINITY) s += R.exact(y);
+                    }
+                    lo = hi = mul_ceil(p, R.cta_sum(s));
+                }
+            }
+            keep = keep && (ahead == 0 || before < lo);
+        }
+        if (by_min) keep = keep && w >= least_w;
+        if (g == 0 && i < ln) list.kept[i] = keep ? w : 0;
+        const u64 all = R.cta_sum(keep && g == 0 ? w : 0);  // (its barriers order list.kept)
+        u64 target = mul_floor(u, all), upto = 0;
+        target = target < all ? target : all - 1;
+        if (i < ln)
+            for (int j = g; j < ln; j += G)
+                if ((uint32_t)list.order[j] >= (uint32_t)me) upto += list.kept[j];
+        for (int o = 1; o < G; o *= 2) upto += __shfl_xor_sync(0xffffffffu, upto, o);
+        if (keep && g == 0 && upto > target && upto - w <= target) {
+            const uint32_t k = (uint32_t)(me >> 32);
+            token = (int)~(uint32_t)me;
+            at = __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
+            mine = true;
+        }
+    } else {
+        // ---- the whole row
+        bool found = false;
+        uint32_t cut = 0;  // kept: tokens above this key, and the first `ties` at it
+        long long ties = 0;
+        if (!cuts) {
+            // all tokens, by quick weights
+            const u64 target = mul_floor(u, quick_z);
+            u64 y[kPer], s4 = 0;
+#pragma unroll
+            for (int k = 0; k < kPer; ++k) {
+                const int i = lane * kPer + k;
+                y[k] = i < a.ctas * kWarps ? s_all.quick[i] : 0;
+                s4 += y[k];
+            }
+            const u64 upto = warp_scan(s4);
+            const unsigned hit = __ballot_sync(0xffffffffu, upto > target);
+            int who = -1;
+            u64 base = 0;
+            if (hit) {
+                u64 run = upto - s4;
+#pragma unroll
+                for (int k = 0; k < kPer; ++k) {
+                    if (who < 0 && run + y[k] > target) {
+                        who = lane * kPer + k;
+                        base = run;
+                    }
+                    run += y[k];
+                }
+                who = __shfl_sync(0xffffffffu, who, __ffs(hit) - 1);
+                base = __shfl_sync(0xffffffffu, base, __ffs(hit) - 1);
+            }
+            if (who >= 0 && who == rank * kWarps + warp) {
+                for (int vb = v0; vb < v1; vb += 32) {
+                    const int v = vb + lane;
+                    float x[VE], wf[VE], sf = 0.f;
+                    if (v < v1) {
+                        unpack<T>(s_data[v], x);
 #pragma unroll
                         for (int e = 0; e < VE; ++e) {
-                            if (token < 0 && run + w[e] > target) {
-                                token = first + v * VE + e - skew;
-                                at = x[e];
-                                mine = run < target - slack && run + w[e] > target + slack;
+                            wf[e] = ex2(fmaf(-0.5f, x[e], 0.5f * R.m) * R.c2);
+                            sf += wf[e];
+                        }
+                    }
+                    const u64 s = __float2ull_rn(sf * 0x1p44f), in = warp_scan(s) + base;
+                    const unsigned at_lane = __ballot_sync(0xffffffffu, in > target);
+                    if (at_lane) {
+                        if (lane == __ffs(at_lane) - 1) {
+                            u64 run = in - s;
+#pragma unroll
+                            for (int e = 0; e < VE; ++e) {
+                                const u64 we = __float2ull_rn(wf[e] * 0x1p44f);
+                                if (token < 0 && run + we > target) {
+                                    token = first + v * VE + e - skew;
+                                    at = x[e];
+                                    mine = run + 2 * off < target && run + we > target + 2 * off;
+                                }
+                                run += we;
                             }
-                            run += w[e];
+                            if (mine)
+                                for (int r = 0; r < a.ctas; ++r) cl.map_shared_rank(&s_all, r)->done[rank] = 1;
                         }
-                        s_shown.done = mine;
+                        break;
                     }
-                    break;
+                    base = __shfl_sync(0xffffffffu, in, 31);
                 }
-                base = __shfl_sync(0xffffffffu, in, 31);
+            }
+            cl.sync();
+            found = __any_sync(0xffffffffu, lane < a.ctas && s_all.done[lane]);
+            if (!found) {
+                token = -1;
+                mine = false;
+                R.weigh(cl, cut, false);
+            }
+        } else if (greedy) {
+            cut = R.key_of(R.m);
+            ties = 1;
+            R.weigh(cl, cut, false);
+        } else {
+            uint32_t key_k = 0;
+            long long ties_k = 0;
+            u64 skipped;
+            if (by_k) {
+                cut = key_k = R.template select<COUNT>(cl, (u64)top_k, 0u, -INFINITY, &skipped);
+                ties = ties_k = top_k - (long long)skipped;
+                R.weigh(cl, cut, false);
+            }
+            if (by_p) {
+                u64 z = quick_z;
+                if (by_k) {
+                    const long long have = R.total_ties();
+                    z = R.total(s_all.quick) + (u64)(have < ties_k ? have : ties_k) * R.exact(R.at_key(key_k));
+                }
+                cut = R.template select<MASS>(cl, mul_ceil(p, z), key_k, by_k ? R.at_key(key_k) : -INFINITY, &skipped);
+                // from quick weights that key is the right one or next to it; exact ones tell
+                for (;;) {
+                    R.weigh(cl, cut, !by_k);
+                    const u64 above = R.total(s_all.quick), w = R.exact(R.at_key(cut));
+                    long long have = R.total_ties();
+                    if (!by_k) z = above + (u64)have * w + R.total(s_all.whole);
+                    else if (cut == key_k) have = have < ties_k ? have : ties_k;
+                    const u64 target = mul_ceil(p, z);
+                    if (above < target && above + (u64)have * w >= target) {
+                        ties = (long long)((target - above + w - 1) / w);
+                        break;
+                    }
+                    cut = R.next_key(cl, cut, above >= target);
+                }
+            }
+            if (by_min) {
+                const uint32_t k = R.key_from(least_w);
+                if (k > cut) {
+                    cut = k;
+                    ties = 1ll << 40;
+                    R.weigh(cl, cut, false);
+                }
             }
         }
-        cl.sync();
-        for (int r = 0; r < a.ctas; ++r) done = done || cl.map_shared_rank(&s_shown, r)->done;
-        if (!done) {
-            token = -1;
-            mine = false;
-        }
-    }
-    if (!done) {
-        cl.sync();
-        R.show_kept(cl, cut);
-        const unsigned long long tie_w = cut.ties ? R.exact(cut.x) : 0;
-        const unsigned long long all = R.kept_weight(cl, cut);
-        const double target = (double)u * (double)all;
-        // the part in which the sum passes the target; if roundings (or u = 1) leave none, the last that weighs anything
-        unsigned long long sum = 0, base = 0;
-        long long ties = 0;
-        int who = -1, allowed = 0;
-        bool passed = false;
-        for (int i = 0; i < a.ctas * kWarps; ++i) {
-            const Shown* o = cl.map_shared_rank(&s_shown, i / kWarps);
-            const int have = o->ties[i % kWarps];
-            const long long rest = cut.ties - ties;
-            const int take = rest <= 0 ? 0 : rest < have ? (int)rest : have;
-            const unsigned long long y = o->sum[i % kWarps] + (unsigned long long)take * tie_w;
-            if (!passed && y > 0) {
-                who = i;
-                base = sum;
-                allowed = take;
-                passed = (double)(sum + y) > target;
+        if (!found) {
+            // what each warp's part keeps, and the part in which the sum passes u times all of it
+            const u64 tie_w = ties ? R.exact(R.at_key(cut)) : 0;
+            int have[kPer], take[kPer], n4 = 0;
+            u64 y[kPer], s4 = 0;
+#pragma unroll
+            for (int k = 0; k < kPer; ++k) {
+                const int i = lane * kPer + k;
+                have[k] = i < a.ctas * kWarps ? s_all.ties[i] : 0;
+                n4 += have[k];
             }
-            sum += y;
-            ties += have;
-        }
-        if (who == rank * kWarps + warp) {
-            int last_token = -1;
-            float last_at = 0.f;
-            for (int vb = v0; vb < v1; vb += 32) {
-                const int v = vb + lane;
-                float x[VE];
-                unsigned long long w[VE], s = 0;
-                int tied = 0;
-                if (v < v1) {
-                    unpack<T>(s_data[v], x);
+            long long rest = ties - (warp_scan(n4) - n4);
 #pragma unroll
-                    for (int e = 0; e < VE; ++e) tied += R.key_of(x[e]) == cut.key;
+            for (int k = 0; k < kPer; ++k) {
+                const int i = lane * kPer + k;
+                take[k] = rest <= 0 ? 0 : rest < have[k] ? (int)rest : have[k];
+                rest -= have[k];
+                y[k] = i < a.ctas * kWarps ? s_all.quick[i] + (u64)take[k] * tie_w : 0;
+                s4 += y[k];
+            }
+            const u64 upto = warp_scan(s4), all = __shfl_sync(0xffffffffu, upto, 31);
+            u64 target = mul_floor(u, all);
+            target = target < all ? target : all - 1;  // (the largest logit weighs something, so all > 0)
+            const int l = __ffs(__ballot_sync(0xffffffffu, upto > target)) - 1;
+            int who = -1, allowed = 0;
+            u64 run = upto - s4, base = 0;
+#pragma unroll
+            for (int k = 0; k < kPer; ++k) {
+                if (who < 0 && run + y[k] > target) {
+                    who = lane * kPer + k;
+                    base = run;
+                    allowed = take[k];
                 }
-                int before = warp_scan(tied);
-                const int all_tied = __shfl_sync(0xffffffffu, before, 31);
-                before -= tied;
-                if (v < v1) {
+                run += y[k];
+            }
+            who = __shfl_sync(0xffffffffu, who, l);
+            base = __shfl_sync(0xffffffffu, base, l);
+            allowed = __shfl_sync(0xffffffffu, allowed, l);
+            if (who == rank * kWarps + warp) {
+                for (int vb = v0; vb < v1; vb += 32) {
+                    const int v = vb + lane;
+                    float x[VE];
+                    u64 w[VE], s = 0;
+                    int tied = 0;
+                    if (v < v1) {
+                        unpack<T>(s_data[v], x);
 #pragma unroll
-                    for (int e = 0; e < VE; ++e) {
-                        const uint32_t k = R.key_of(x[e]);
-                        w[e] = 0;
-                        if (k > cut.key) w[e] = R.exact(x[e]);
-                        else if (k == cut.key) w[e] = before++ < allowed ? tie_w : 0;
-                        s += w[e];
+                        for (int e = 0; e < VE; ++e) tied += R.key_of(x[e]) == cut;
                     }
-                }
-                allowed -= all_tied;
-                const unsigned long long in = warp_scan(s) + base;
-                const unsigned hit = __ballot_sync(0xffffffffu, (double)in > target);
-                if (v < v1 && (!hit || lane == __ffs(hit) - 1)) {
-                    unsigned long long run = in - s;
+                    int before = warp_scan(tied);
+                    const int all_tied = __shfl_sync(0xffffffffu, before, 31);
+                    before -= tied;
+                    if (v < v1) {
 #pragma unroll
-                    for (int e = 0; e < VE; ++e) {
-                        run += w[e];
-                        if (w[e] > 0 && !mine) {
-                            last_token = first + v * VE + e - skew;
-                            last_at = x[e];
-                            mine = hit && (double)run > target;
+                        for (int e = 0; e < VE; ++e) {
+                            const uint32_t k = R.key_of(x[e]);
+                            w[e] = 0;
+                            if (k > cut) w[e] = R.exact(x[e]);
+                            else if (k == cut) w[e] = before++ < allowed ? tie_w : 0;
+                            s += w[e];
                         }
                     }
+                    allowed -= all_tied;
+                    const u64 in = warp_scan(s) + base;
+                    const unsigned hit = __ballot_sync(0xffffffffu, in > target);
+                    if (hit) {
+                        if (lane == __ffs(hit) - 1) {
+                            u64 sum = in - s;
+#pragma unroll
+                            for (int e = 0; e < VE; ++e) {
+                                sum += w[e];
+                                if (!mine && sum > target) {
+                                    token = first + v * VE + e - skew;
+                                    at = x[e];
+                                    mine = true;
+                                }
+                            }
+                        }
+                        break;
+                    }
+                    base = __shfl_sync(0xffffffffu, in, 31);
                 }
-                if (hit) break;
-                base = __shfl_sync(0xffffffffu, in, 31);
             }
-            if (!__any_sync(0xffffffffu, mine)) {  // the last token that weighs anything
-                const int most = (int)__reduce_max_sync(0xffffffffu, (unsigned)(last_token + 1)) - 1;
-                mine = last_token == most;
-            }
-            token = last_token;
-            at = last_at;
         }
     }
     if (mine) {
+        // whole_z is at least 1; near it the logarithm is taken of what it is more
+        constexpr u64 one = 1ull << kFrac;
+        const float lz = whole_z < 2 * one ? log1pf((float)(whole_z > one ? whole_z - one : 0) * 0x1p-44f) : logf((float)whole_z * 0x1p-44f);
         a.token[row] = token;
-        a.logprob[row] = (float)((double)at - (double)R.m - log(whole_z));
+        a.logprob[row] = at - R.m - lz;
     }
-    cl.sync();  // no CTA leaves while another may read what it shows
 }
 
 template <typename T>
