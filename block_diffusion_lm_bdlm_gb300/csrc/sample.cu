@@ -40,7 +40,11 @@ namespace {
 using namespace sample;
 namespace cg = cooperative_groups;
 
-constexpr int kThreads = 512;
+#ifndef KT
+#define KT 512
+#define KM 2
+#endif
+constexpr int kThreads = KT;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 512;
 constexpr int kMaxCtas = 8;
@@ -156,7 +160,8 @@ __device__ __forceinline__ u64 mul_floor(float f, u64 z, bool up = false) {
 __device__ __forceinline__ u64 mul_ceil(float f, u64 z) { return mul_floor(f, z, true); }
 
 constexpr int kList = kThreads;  // listed tokens of a row
-constexpr int kParts = kMaxCtas * kWarps;
+constexpr int kParts = kMaxCtas * kWarps;  // maxima, and warps of the largest cluster
+static_assert(kParts % 32 == 0, "");
 constexpr int kPer = kParts / 32;
 
 enum : int { COUNT = 0, MASS = 1 };
@@ -167,8 +172,8 @@ struct All {
     u64 quick[kParts];   // quick weights at T; later exact weights above the cut
     u64 whole[kParts];   // quick weights at T = 1; later exact weights below the cut
     int ties[kParts];    // tokens at the cut
-    u64 listed[kMaxCtas];  // weight and number of the listed tokens of each CTA
-    int n[kMaxCtas];
+    u64 sums[kMaxCtas][3];  // of each CTA: quick weights at T = 1, at T, and of what it has listed (~0: a NaN)
+    int n[kMaxCtas];         // tokens that each CTA has listed
     uint32_t key_lo[kMaxCtas], key_hi[kMaxCtas];
     int done[kMaxCtas];
 };
@@ -449,15 +454,15 @@ struct Row {
 };
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a) {
+__global__ void __launch_bounds__(kThreads, KM) sample_kernel(const SampleArgs a) {
     constexpr int VE = Type<T>::VE;
     extern __shared__ uint4 s_data[];
     __shared__ All s_all;
     __shared__ Work s_work;
     __shared__ F2 s_table[kTable];
     __shared__ u64 s_scan[kWarps], s_found[2];
-    __shared__ int s_n;
-    __shared__ u64 s_listed;
+    __shared__ int s_n, s_nan;
+    __shared__ u64 s_part[3][kWarps];
     cg::cluster_group cl = cg::this_cluster();
     // (rows that are left leave with all of their CTAs)
     const int rank = (int)cl.block_rank(), row = blockIdx.x / a.ctas;
@@ -501,8 +506,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
         s_table[tid] = v;
     }
     if (tid == 0) {
-        s_n = 0;
-        s_listed = 0;
+        s_n = s_nan = 0;
     }
     const float temp = a.temperature ? __ldg(a.temperature + row) : a.temperature_all;
     const int top_k = a.top_k ? __ldg(a.top_k + row) : a.top_k_all;
@@ -548,8 +552,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
         }
         return;
     }
-    // Tokens from x0 on are listed: the k-th largest of the 128 maxima has at least k tokens from it on, and the 80th, where
-    // weights decide, about 125. A list that turns out too short or too long is not used.
+    // Tokens from x0 on are listed. The least of the 32 largest logits of as many parts of the row has 32 tokens from it on and
+    // about 130 where they lie anywhere, the k-th largest of the 128 maxima at least k. A list that turns out too short
+    // or too long is not used.
     float x0 = R.m;
     const bool infinite = R.m == INFINITY;
     if (infinite) {  // the infinite logits share everything
@@ -564,18 +569,26 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
         }
         R.m = x0 = 0.f;
     } else if (!greedy && cuts) {
-        const int want = by_k ? imin(top_k, 120) : 80;
-        uint32_t key = 0;
-#pragma unroll 1
-        for (int bit = 31; bit >= 16; --bit) {
-            const uint32_t next = key | 1u << bit;
-            int have = 0;
+        uint32_t key;
+        if (!by_k || top_k <= 32) {
+            uint32_t best = 0;
 #pragma unroll
-            for (int k = 0; k < kPer; ++k) have += __popc(__ballot_sync(0xffffffffu, order_key(__float_as_uint(tops[k])) >= next));
-            if (have >= want) key = next;
+            for (int k = 0; k < kPer; ++k) best = max(best, order_key(__float_as_uint(tops[k])));
+            key = __reduce_min_sync(0xffffffffu, best);
+        } else {
+            const int want = imin(top_k, 120);
+            key = 0;
+#pragma unroll 1
+            for (int bit = 31; bit >= 16; --bit) {
+                const uint32_t next = key | 1u << bit;
+                int have = 0;
+#pragma unroll
+                for (int k = 0; k < kPer; ++k) have += __popc(__ballot_sync(0xffffffffu, order_key(__float_as_uint(tops[k])) >= next));
+                if (have >= want) key = next;
+            }
         }
         x0 = __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key);
-        x0 = x0 == x0 ? fminf(x0, R.m) : -INFINITY;  // (fewer groups have anything: the key is below that of -infinity)
+        x0 = x0 == x0 ? fminf(x0, R.m) : -INFINITY;  // (few groups have anything: the key is below that of -infinity)
         if (by_min && !by_k && !by_p)  // a little below what min-p keeps
             x0 = fmaxf(x0, R.m + T_ * __logf(fminf(min_p, 1.f)) - fabsf(R.m) * 0x1p-10f - T_ * 0x1p-6f);
         if (!(x0 > -INFINITY)) x0 = -3.402823466e38f;
@@ -586,10 +599,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
     const bool two = quick && temp != 1.f;
     u64 quick_z = 0, whole_z = 0;
     List& list = s_work.list;
+    uint2* to = cl.map_shared_rank(&s_work, 0)->list.raw + rank * (kList / a.ctas);
     for (int turn = 0;; ++turn) {
         const float half_m = 0.5f * R.m, c1 = -2.8853900817779268f;
         float s1 = 0.f, st = 0.f;
-        u64 mine = 0;
+        float mine = 0.f;  // weight of what this thread has listed
         for (int v = v0 + lane; v < v1; v += 32) {
             const uint4 raw = s_data[v];
             float x[VE], y = 0.f, yt = 0.f;
@@ -603,43 +617,50 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
             s1 += y;
             st += yt;
             if (cuts && top_of<T>(raw) >= x0) {
+                unsigned hits = 0;
 #pragma unroll
-                for (int e = 0; e < VE; ++e)
-                    if (x[e] >= x0) {
-                        const int i = atomicAdd(&s_n, 1);
-                        mine += R.exact(x[e]);
-                        if (i < kList / a.ctas)
-                            cl.map_shared_rank(&s_work.list, 0)->raw[rank * (kList / a.ctas) + i] =
-                                make_uint2(order_key(__float_as_uint(x[e])), (uint32_t)(first + v * VE + e - skew));
-                    }
+                for (int e = 0; e < VE; ++e) hits |= x[e] >= x0 ? 1u << e : 0u;
+                int i = atomicAdd(&s_n, __popc(hits));
+                for (; hits; hits &= hits - 1, ++i) {
+                    const int e = __ffs(hits) - 1;
+                    const float z = (float)reinterpret_cast<const T*>(s_data + v)[e];
+                    mine += ex2(fmaf(-0.5f, z, half_m) * R.c2);
+                    if (i < kList / a.ctas) to[i] = make_uint2(order_key(__float_as_uint(z)), (uint32_t)(first + v * VE + e - skew));
+                }
             }
         }
         const bool nan = s1 != s1;
         const u64 w1 = warp_sum(nan ? 0ull : (u64)__float2ull_rn(s1 * 0x1p44f)), wt = two ? warp_sum((u64)__float2ull_rn(st * 0x1p44f)) : w1;
-        R.tell(cl, s_all.whole, __any_sync(0xffffffffu, nan) ? ~0ull : w1);
-        R.tell(cl, s_all.quick, wt);
-        if (cuts) {
-            mine = warp_sum(mine);
-            if (lane == 0 && mine) atomicAdd(&s_listed, mine);
-            __syncthreads();
-            if (tid < a.ctas) {
-                All* o = cl.map_shared_rank(&s_all, tid);
-                o->listed[rank] = s_listed;
+        if (!cuts) R.tell(cl, s_all.quick, wt);
+        const float wl = cuts ? warp_sum(mine) : 0.f;
+        if (lane == 0) {
+            s_part[0][warp] = w1;
+            s_part[1][warp] = wt;
+            s_part[2][warp] = __float2ull_rn(wl * 0x1p44f);
+        }
+        if (nan) s_nan = 1;
+        __syncthreads();
+        if (tid < 3 * a.ctas) {  // three sums for each CTA
+            const int what = tid % 3;
+            All* o = cl.map_shared_rank(&s_all, tid / 3);
+            u64 s = 0;
+#pragma unroll
+            for (int w = 0; w < kWarps; ++w) s += s_part[what][w];
+            o->sums[rank][what] = s_nan ? ~0ull : s;
+            if (what == 0) {
                 o->n[rank] = s_n;
+                o->done[rank] = 0;
             }
-        } else if (tid < a.ctas) {
-            cl.map_shared_rank(&s_all, tid)->done[rank] = 0;
         }
         cl.sync();
         whole_z = quick_z = 0;
         bool bad = false;
-        for (int i = lane; i < a.ctas * kWarps; i += 32) {
-            const u64 y = s_all.whole[i];
-            bad = bad || y == ~0ull;
-            whole_z += y;
-            quick_z += s_all.quick[i];
+        for (int r = 0; r < a.ctas; ++r) {
+            bad = bad || s_all.sums[r][0] == ~0ull;
+            whole_z += s_all.sums[r][0];
+            quick_z += s_all.sums[r][1];
         }
-        if (!__any_sync(0xffffffffu, bad)) break;
+        if (!bad) break;
         // a NaN counts as a logit of -infinity
         for (int v = v0 + lane; v < v1; v += 32) {
             T* x = reinterpret_cast<T*>(s_data + v);
@@ -648,13 +669,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
         }
         cl.sync();
         if (tid == 0) {
-            s_n = 0;
-            s_listed = 0;
+            s_n = s_nan = 0;
         }
         __syncthreads();
     }
-    whole_z = warp_sum(whole_z);
-    quick_z = warp_sum(quick_z);
     const u64 off = (u64)((float)quick_z * (float)kQuick) + 1;
     const u64 least_w = by_min ? mul_ceil(fminf(min_p, 1.f), 1ull << kFrac) : 0;  // min-p keeps weights from here on
 
@@ -669,11 +687,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
         for (int r = 0; r < a.ctas; ++r) {
             listed = listed && s_all.n[r] <= kList / a.ctas;
             ln += s_all.n[r];
-            lw += s_all.listed[r];
+            lw += s_all.sums[r][2];
         }
         const bool by_min_all = by_min && R.exact(x0) < least_w;
         if (!greedy)
-            listed = listed && (by_min_all || (by_k ? ln >= top_k : by_p && lw >= mul_ceil(p, quick_z + off)));
+            listed = listed && (by_min_all || (by_k ? ln >= top_k : by_p && lw >= mul_ceil(p, quick_z + off) + off));
     }
     if (listed) {
         if (rank != 0) return;
@@ -695,11 +713,12 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
         if (i < ln) {
             me = list.order[i];
             w = list.w[i];
-            for (int j = g; j < ln; j += G)
-                if (list.order[j] > me) {
-                    before += list.w[j];
-                    ++ahead;
-                }
+#pragma unroll 4
+            for (int j = g; j < ln; j += G) {
+                const u64 other = list.order[j], ow = list.w[j];
+                before += other > me ? ow : 0;
+                ahead += other > me;
+            }
         }
         for (int o = 1; o < G; o *= 2) {
             before += __shfl_xor_sync(0xffffffffu, before, o);
@@ -733,8 +752,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
         u64 target = mul_floor(u, all), upto = 0;
         target = target < all ? target : all - 1;
         if (i < ln)
-            for (int j = g; j < ln; j += G)
-                if ((uint32_t)list.order[j] >= (uint32_t)me) upto += list.kept[j];
+#pragma unroll 4
+            for (int j = g; j < ln; j += G) {
+                const u64 ow = list.kept[j];
+                upto += (uint32_t)list.order[j] >= (uint32_t)me ? ow : 0;
+            }
         for (int o = 1; o < G; o *= 2) upto += __shfl_xor_sync(0xffffffffu, upto, o);
         if (keep && g == 0 && upto > target && upto - w <= target) {
             const uint32_t k = (uint32_t)(me >> 32);
