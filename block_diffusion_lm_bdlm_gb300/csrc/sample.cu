@@ -416,15 +416,14 @@ struct Row {
         cl.sync();  // what is told is read no more
         each(below || cut == 0 ? -INFINITY : at_key(cut), [&](int, const float(&x)[VE]) {
 #pragma unroll
-            for (int e = 0; e < VE; ++e) {
-                const uint32_t k = key_of(x[e]);
-                if (k == cut) {
-                    ++n;
-                } else if (k > cut || below) {
-                    const u64 w = exact(x[e]);
-                    if (k > cut) s += w;
-                    else z += w;
-                }
+            for (int e = 0; e < VE; e += 2) {
+                const uint32_t k0 = key_of(x[e]), k1 = key_of(x[e + 1]);
+                n += (k0 == cut) + (k1 == cut);
+                if (!below && k0 <= cut && k1 <= cut) continue;
+                u64 w0, w1;
+                exact_weights(x[e], x[e + 1], m, c, table, w0, w1);
+                s += (k0 > cut ? w0 : 0) + (k1 > cut ? w1 : 0);
+                z += (k0 < cut ? w0 : 0) + (k1 < cut ? w1 : 0);
             }
         });
         tell(cl, all->quick, warp_sum(s));

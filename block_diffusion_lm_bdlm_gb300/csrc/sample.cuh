@@ -18,6 +18,7 @@
 #include <cstdint>
 
 #include "common.cuh"
+#include "tc_ptx.cuh"
 
 namespace bdlm {
 namespace sample {
@@ -63,28 +64,68 @@ __host__ __device__ __forceinline__ uint64_t exact_weight(float x, float m, F2 c
     const float tl = BDLM_ADD(BDLM_FMA(h, c.hi, -th), BDLM_FMA(h, c.lo, BDLM_MUL(hl, c.hi)));
     const int n = BDLM_RINT(th);
     const float f = BDLM_ADD((float)n, -th);  // exact; the weight is 2^-n 2^(f - tl)
-    const float gh = BDLM_ADD(f, -tl);
-    const float fb = BDLM_ADD(gh, -f);
-    const float gl = BDLM_ADD(BDLM_ADD(f, -BDLM_ADD(gh, -fb)), BDLM_ADD(-tl, -fb));
-    const int j = BDLM_RINT(BDLM_MUL(gh, 16.f));
-    const float r = BDLM_FMA((float)j, -0.0625f, gh);  // exact
+    const int j = BDLM_RINT(BDLM_MUL(f, 16.f));
+    const float r = BDLM_FMA((float)j, -0.0625f, f);  // exact
     constexpr float lh = 0x1.62e430p-1f, ll = -0x1.05c610p-29f;  // ln 2
-    const float y0 = BDLM_MUL(r, lh), y1 = BDLM_ADD(BDLM_FMA(r, lh, -y0), BDLM_FMA(r, ll, BDLM_MUL(gl, lh)));
+    const float y0 = BDLM_MUL(r, lh), y1 = BDLM_ADD(BDLM_FMA(r, lh, -y0), BDLM_FMA(r, ll, BDLM_MUL(-lh, tl)));
     const float yh = BDLM_ADD(y0, y1), yl = BDLM_ADD(y1, -BDLM_ADD(yh, -y0));
     const float qh = BDLM_MUL(yh, yh), ql = BDLM_FMA(BDLM_MUL(2.f, yh), yl, BDLM_FMA(yh, yh, -qh));
     float p = BDLM_FMA(yh, 1.f / 720.f, 1.f / 120.f);
     p = BDLM_FMA(yh, p, 1.f / 24.f);
     p = BDLM_FMA(yh, p, 1.f / 6.f);
-    const float q2 = BDLM_MUL(0.5f, qh), sh = BDLM_ADD(yh, q2), se = BDLM_ADD(q2, -BDLM_ADD(sh, -yh));
+    const float sh = BDLM_FMA(0.5f, qh, yh), se = BDLM_FMA(0.5f, qh, -BDLM_ADD(sh, -yh));
     const float low = BDLM_ADD(BDLM_FMA(BDLM_MUL(qh, yh), p, se), BDLM_FMA(0.5f, ql, yl));
     const F2 t = table[j + 8];
     const float ph = BDLM_MUL(t.hi, sh), pl = BDLM_FMA(t.hi, sh, -ph);
     const float rh = BDLM_ADD(t.hi, ph), re = BDLM_ADD(ph, -BDLM_ADD(rh, -t.hi));
     const float rl = BDLM_ADD(BDLM_ADD(re, pl), BDLM_ADD(t.lo, BDLM_FMA(t.hi, low, BDLM_MUL(t.lo, sh))));
-    // rh is a multiple of 2^-24 (or of 2^-25 below one half, which 2^-44 holds as well)
+    // rh is a multiple of 2^-25
     const int64_t w = ((int64_t)BDLM_RINT(BDLM_MUL(rh, 0x1p25f)) << (kFrac - 25)) + BDLM_RINT(BDLM_MUL(rl, 0x1p44f));
-    return n <= 0 ? (uint64_t)w << -n : (uint64_t)((w + ((int64_t)1 << (n - 1))) >> n);
+    return (uint64_t)((2 * w + ((int64_t)1 << n)) >> (n + 1));
 }
+
+#ifdef __CUDACC__
+// Two of them at once: the same steps on pairs (two operations per instruction), the roundings of n and j to whole
+// numbers by adding and taking off 1.5 * 2^23.
+__device__ __forceinline__ void exact_weights(float x0, float x1, float m, F2 c, const F2* table, unsigned long long& w0,
+                                              unsigned long long& w1) {
+    using tc::add2;
+    using tc::fma2;
+    using tc::mul2;
+    auto two = [](float v) { return make_float2(v, v); };
+    auto neg = [](float2 v) { return make_float2(-v.x, -v.y); };
+    constexpr float whole = 12582912.f, lh = 0x1.62e430p-1f, ll = -0x1.05c610p-29f;
+    const float2 a = two(0.5f * m), b = mul2(two(-0.5f), make_float2(x0, x1));
+    const float2 h = add2(a, b), bb = add2(h, neg(a));
+    const float2 hl = add2(add2(a, neg(add2(h, neg(bb)))), add2(b, neg(bb)));
+    const float2 th = mul2(h, two(c.hi));
+    const float2 tl = add2(fma2(h, two(c.hi), neg(th)), fma2(h, two(c.lo), mul2(hl, two(c.hi))));
+    const float2 nw = add2(th, two(whole)), f = add2(add2(nw, two(-whole)), neg(th));
+    const float2 jw = fma2(f, two(16.f), two(whole)), r = fma2(add2(jw, two(-whole)), two(-0.0625f), f);
+    const float2 y0 = mul2(r, two(lh)), y1 = add2(fma2(r, two(lh), neg(y0)), fma2(r, two(ll), mul2(two(-lh), tl)));
+    const float2 yh = add2(y0, y1), yl = add2(y1, neg(add2(yh, neg(y0))));
+    const float2 qh = mul2(yh, yh), ql = fma2(mul2(two(2.f), yh), yl, fma2(yh, yh, neg(qh)));
+    float2 p = fma2(yh, two(1.f / 720.f), two(1.f / 120.f));
+    p = fma2(yh, p, two(1.f / 24.f));
+    p = fma2(yh, p, two(1.f / 6.f));
+    const float2 sh = fma2(two(0.5f), qh, yh), se = fma2(two(0.5f), qh, neg(add2(sh, neg(yh))));
+    const float2 low = add2(fma2(mul2(qh, yh), p, se), fma2(two(0.5f), ql, yl));
+    const bool some0 = th.x < 46.f, some1 = th.y < 46.f;
+    const F2 t0 = table[some0 ? __float_as_int(jw.x) - 0x4b400000 + 8 : 0], t1 = table[some1 ? __float_as_int(jw.y) - 0x4b400000 + 8 : 0];
+    const float2 ht = make_float2(t0.hi, t1.hi), lt = make_float2(t0.lo, t1.lo);
+    const float2 ph = mul2(ht, sh), pl = fma2(ht, sh, neg(ph));
+    const float2 rh = add2(ht, ph), re = add2(ph, neg(add2(rh, neg(ht))));
+    const float2 rl = add2(add2(re, pl), add2(lt, fma2(ht, low, mul2(lt, sh))));
+    const float2 big = mul2(rh, two(0x1p25f)), small = mul2(rl, two(0x1p44f));
+    auto join = [](float hi, float lo, float nw) {
+        const int n = (__float_as_int(nw) - 0x4b400000) & 63;
+        const int64_t w = ((int64_t)__float2int_rn(hi) << (kFrac - 25)) + __float2int_rn(lo);
+        return (uint64_t)((2 * w + ((int64_t)1 << n)) >> (n + 1));
+    };
+    w0 = some0 ? join(big.x, small.x, nw.x) : 0;
+    w1 = some1 ? join(big.y, small.y, nw.y) : 0;
+}
+#endif
 
 // A key that orders floats as their values do; -0 and 0 have the same.
 __host__ __device__ __forceinline__ uint32_t order_key(uint32_t bits) {
