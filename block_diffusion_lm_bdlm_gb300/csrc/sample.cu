@@ -48,6 +48,8 @@ constexpr int kThreads = KT;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 512;
 constexpr int kMaxCtas = 8;
+constexpr float kWhole = 12582912.f;  // 1.5 * 2^23: adding it rounds to whole numbers
+constexpr int kWholeBits = 0x4b400000;
 constexpr float kBinsPerOctave = 8.f;  // bins of the first level: an eighth of a factor of two in weight
 constexpr float kGreedyBelow = 0x1p-20f;
 constexpr float kHottest = 0x1p40f;
@@ -212,9 +214,17 @@ struct Row {
         return __uint_as_float(u & 0x80000000u ? u ^ 0x80000000u : ~(u | ((1u << SHIFT) - 1u)));
     }
     __device__ __forceinline__ u64 exact(float x) const { return exact_weight(x, m, c, table); }
-    __device__ __forceinline__ int bin_of(float x) const {
-        const float t = fmaf(-0.5f, x, 0.5f * m) * (c2 * -kBinsPerOctave);
-        return t < (float)(kBins - 1) ? (int)t : kBins - 1;
+    // Distance from the largest logit in bins, and the bin, to which it is rounded (as bits of that plus 1.5 * 2^23).
+    __device__ __forceinline__ float bins_off(float x) const {
+        return fminf(fmaf(-0.5f, x, 0.5f * m) * (c2 * -kBinsPerOctave), (float)(kBins - 1));
+    }
+    __device__ __forceinline__ int bin_of(float x) const { return __float_as_int(bins_off(x) + kWhole) - kWholeBits; }
+    // No logit of bin b lies above (below) this one. c2 is negative; the margins cover roundings.
+    __device__ __forceinline__ float above_bin(int b) const {
+        return fminf(m, m + (b - 0.51f) * 2.f / (kBinsPerOctave * c2) + fabsf(m) * 0x1p-20f);
+    }
+    __device__ __forceinline__ float below_bin(int b) const {
+        return b == kBins - 1 ? -INFINITY : m + (b + 0.51f) * 2.f / (kBinsPerOctave * c2) - fabsf(m) * 0x1p-20f;
     }
     // Tells every CTA of the cluster a value for this warp; all lanes hold it.
     template <typename V>
@@ -238,15 +248,10 @@ struct Row {
         for (int i = threadIdx.x; i < kBins; i += kThreads) work->bins.n[i] = 0;
         __syncthreads();
     }
-    // MASS: the quick weight in units of 2^-16 of the bin's largest
+    // Counts x in place `at`. MASS: its quick weight in units of 2^-16 of 2^(-bin / 8), at most 2^16.1 of them.
     template <int MODE>
-    __device__ __forceinline__ void add(int at, int bin, float x) {
-        if (MODE == COUNT) {
-            atomicAdd(&work->bins.n[at], 1u);
-        } else {
-            const float t = fmaf(-0.5f, x, 0.5f * m) * c2 + (float)bin * (1.f / kBinsPerOctave);
-            atomicAdd(&work->bins.n[at], (uint32_t)__float2int_rn(ex2(t) * 65536.f));
-        }
+    __device__ __forceinline__ void add(int at, float off_bin) {
+        atomicAdd(&work->bins.n[at], MODE == COUNT ? 1u : (uint32_t)(__float_as_int(fmaf(ex2(off_bin * (-1.f / kBinsPerOctave)), 65536.f, kWhole)) - kWholeBits));
     }
     // Adds up the cluster's bins, each thread one, and finds the one in which the sum from `base` on passes the target:
     // its number, and in *before the sum of those before it. Bin i holds weights of octave bin `bin0` + i (MASS, first
@@ -288,51 +293,42 @@ struct Row {
         *before = found[1];
         return bin;
     }
+    // Whether the last cross found a bin that passes.
+    __device__ __forceinline__ bool passed() const { return *reinterpret_cast<const unsigned*>(found) & 0x80000000u; }
 
     // The key of the token at which the sum over falling logits, of tokens (COUNT) or of quick weights (MASS), passes the
-    // target; only tokens from key `floor` on count. *before (COUNT): tokens above that key.
+    // target; only tokens from logit `floor_x` on count. *before (COUNT): tokens above that key.
     template <int MODE>
-    __device__ __forceinline__ uint32_t select(cg::cluster_group& cl, u64 target, uint32_t floor, float floor_x, u64* before) {
-        // The threads' largest logits alone pass the target by bin `last`, so the cut lies no further.
-        cl.sync();
-        clear();
-        if (mine > -INFINITY && key_of(mine) >= floor) add<MODE>(bin_of(mine), bin_of(mine), mine);
-        cl.sync();
+    __device__ __forceinline__ uint32_t select(cg::cluster_group& cl, u64 target, float floor_x, u64* before) {
         u64 base;
-        int last = cross<MODE>(cl, kBins, 0, true, MODE == MASS ? target + (target >> 14) : target, 0, &base);
-        {  // (`last` may be the last filled bin without passing)
-            const unsigned got = *reinterpret_cast<unsigned*>(found);
-            if (!(got & 0x80000000u)) last = kBins - 1;
-        }
-        // no logit below this one lies in bin `last` (c2 is negative; the margin covers roundings)
-        const float edge = last == kBins - 1 ? -INFINITY : m + (last + 1.01f) * 2.f / (kBinsPerOctave * c2) - fabsf(m) * 0x1p-20f;
-        float least = fmaxf(edge, floor_x);
+        int last = kBins - 1;
         cl.sync();
+        if (MODE == COUNT && target <= (u64)C * kThreads / 2) {
+            // the threads' largest logits alone pass the target by bin `last`, so the cut lies no further
+            clear();
+            if (mine > -INFINITY) add<MODE>(bin_of(mine), 0.f);
+            cl.sync();
+            last = cross<MODE>(cl, kBins, 0, true, target, 0, &base);
+            if (!passed()) last = kBins - 1;
+            cl.sync();
+        }
+        float least = fmaxf(below_bin(last), floor_x);
         clear();
         each(least, [&](int, const float(&x)[VE]) {
 #pragma unroll
             for (int e = 0; e < VE; ++e) {
-                if (!(x[e] >= least) || key_of(x[e]) < floor) continue;
-                const int b = bin_of(x[e]);
-                if (b <= last) add<MODE>(b, b, x[e]);
+                if (!(x[e] >= least)) continue;
+                const float t = bins_off(x[e]), b = t + kWhole;
+                add<MODE>(__float_as_int(b) - kWholeBits, t - (b - kWhole));  // (a bin beyond `last` does no harm)
             }
         });
         cl.sync();
         const int bin = cross<MODE>(cl, last + 1, 0, true, target, 0, &base);
-        // the keys of that bin
-        uint32_t lo = 0xffffffffu, hi = 0;
-        each(least, [&](int, const float(&x)[VE]) {
-#pragma unroll
-            for (int e = 0; e < VE; ++e) {
-                if (!(x[e] >= least) || bin_of(x[e]) != bin) continue;
-                const uint32_t k = key_of(x[e]);
-                if (k < floor) continue;
-                lo = min(lo, k);
-                hi = max(hi, k);
-            }
-        });
-        span(cl, lo, hi);
-        least = at_key(lo);
+        cl.sync();
+        // the keys of that bin, coarsely and finer until it is a single one
+        least = fmaxf(below_bin(bin), floor_x);
+        const float most = above_bin(bin);
+        uint32_t lo = key_of(least), hi = key_of(most);
         while (lo < hi) {
             const int shift = imax(0, 32 - __clz(hi - lo) - 9);
             const int n = (int)((hi - lo) >> shift) + 1;
@@ -340,8 +336,10 @@ struct Row {
             each(least, [&](int, const float(&x)[VE]) {
 #pragma unroll
                 for (int e = 0; e < VE; ++e) {
+                    if (!(x[e] >= least && x[e] <= most)) continue;
+                    const float t = bins_off(x[e]), b = t + kWhole;
                     const uint32_t k = key_of(x[e]);
-                    if (x[e] >= least && k >= lo && k <= hi) add<MODE>((int)((hi - k) >> shift), bin, x[e]);
+                    if (__float_as_int(b) - kWholeBits == bin && k >= lo && k <= hi) add<MODE>((int)((hi - k) >> shift), t - (b - kWhole));
                 }
             });
             cl.sync();
@@ -413,17 +411,17 @@ struct Row {
     __device__ __forceinline__ void weigh(cg::cluster_group& cl, uint32_t cut, bool below) {
         u64 s = 0, z = 0;
         int n = 0;
+        const float at = cut ? at_key(cut) : -INFINITY;
         cl.sync();  // what is told is read no more
-        each(below || cut == 0 ? -INFINITY : at_key(cut), [&](int, const float(&x)[VE]) {
+        each(below ? -INFINITY : at, [&](int, const float(&x)[VE]) {
 #pragma unroll
             for (int e = 0; e < VE; e += 2) {
-                const uint32_t k0 = key_of(x[e]), k1 = key_of(x[e + 1]);
-                n += (k0 == cut) + (k1 == cut);
-                if (!below && k0 <= cut && k1 <= cut) continue;
+                n += (x[e] == at) + (x[e + 1] == at);
+                if (!below && !(x[e] > at || x[e + 1] > at)) continue;
                 u64 w0, w1;
                 exact_weights(x[e], x[e + 1], m, c, table, w0, w1);
-                s += (k0 > cut ? w0 : 0) + (k1 > cut ? w1 : 0);
-                z += (k0 < cut ? w0 : 0) + (k1 < cut ? w1 : 0);
+                s += (x[e] > at ? w0 : 0) + (x[e + 1] > at ? w1 : 0);
+                if (below) z += (x[e] < at ? w0 : 0) + (x[e + 1] < at ? w1 : 0);
             }
         });
         tell(cl, all->quick, warp_sum(s));
@@ -605,16 +603,21 @@ __global__ void __launch_bounds__(kThreads, KM) sample_kernel(const SampleArgs a
         float mine = 0.f;  // weight of what this thread has listed
         for (int v = v0 + lane; v < v1; v += 32) {
             const uint4 raw = s_data[v];
-            float x[VE], y = 0.f, yt = 0.f;
+            float x[VE];
+            float2 y = make_float2(0.f, 0.f), yt = y;
             unpack<T>(raw, x);
 #pragma unroll
             for (int e = 0; e < VE; e += 2) {
-                const float h0 = fmaf(-0.5f, x[e], half_m), h1 = fmaf(-0.5f, x[e + 1], half_m);
-                y += ex2(h0 * c1) + ex2(h1 * c1);
-                if (two) yt += ex2(h0 * R.c2) + ex2(h1 * R.c2);
+                const float2 h = tc::fma2(make_float2(x[e], x[e + 1]), make_float2(-0.5f, -0.5f), make_float2(half_m, half_m));
+                const float2 t1 = tc::mul2(h, make_float2(c1, c1));
+                y = tc::add2(y, make_float2(ex2(t1.x), ex2(t1.y)));
+                if (two) {
+                    const float2 tt = tc::mul2(h, make_float2(R.c2, R.c2));
+                    yt = tc::add2(yt, make_float2(ex2(tt.x), ex2(tt.y)));
+                }
             }
-            s1 += y;
-            st += yt;
+            s1 += y.x + y.y;
+            st += yt.x + yt.y;
             if (cuts && top_of<T>(raw) >= x0) {
                 unsigned hits = 0;
 #pragma unroll
@@ -846,7 +849,7 @@ __global__ void __launch_bounds__(kThreads, KM) sample_kernel(const SampleArgs a
             long long ties_k = 0;
             u64 skipped;
             if (by_k) {
-                cut = key_k = R.template select<COUNT>(cl, (u64)top_k, 0u, -INFINITY, &skipped);
+                cut = key_k = R.template select<COUNT>(cl, (u64)top_k, -INFINITY, &skipped);
                 ties = ties_k = top_k - (long long)skipped;
                 R.weigh(cl, cut, false);
             }
@@ -856,7 +859,7 @@ __global__ void __launch_bounds__(kThreads, KM) sample_kernel(const SampleArgs a
                     const long long have = R.total_ties();
                     z = R.total(s_all.quick) + (u64)(have < ties_k ? have : ties_k) * R.exact(R.at_key(key_k));
                 }
-                cut = R.template select<MASS>(cl, mul_ceil(p, z), key_k, by_k ? R.at_key(key_k) : -INFINITY, &skipped);
+                cut = R.template select<MASS>(cl, mul_ceil(p, z), by_k ? R.at_key(key_k) : -INFINITY, &skipped);
                 // from quick weights that key is the right one or next to it; exact ones tell
                 for (;;) {
                     R.weigh(cl, cut, !by_k);

@@ -93,28 +93,30 @@ __device__ __forceinline__ void exact_weights(float x0, float x1, float m, F2 c,
     using tc::fma2;
     using tc::mul2;
     auto two = [](float v) { return make_float2(v, v); };
-    auto neg = [](float2 v) { return make_float2(-v.x, -v.y); };
+    auto less = [&](float2 u, float2 v) { return fma2(v, two(-1.f), u); };  // u - v (a negated operand would cost two more)
     constexpr float whole = 12582912.f, lh = 0x1.62e430p-1f, ll = -0x1.05c610p-29f;
     const float2 a = two(0.5f * m), b = mul2(two(-0.5f), make_float2(x0, x1));
-    const float2 h = add2(a, b), bb = add2(h, neg(a));
-    const float2 hl = add2(add2(a, neg(add2(h, neg(bb)))), add2(b, neg(bb)));
+    const float2 h = add2(a, b), bb = less(h, a);
+    const float2 hl = add2(less(a, less(h, bb)), less(b, bb));
     const float2 th = mul2(h, two(c.hi));
-    const float2 tl = add2(fma2(h, two(c.hi), neg(th)), fma2(h, two(c.lo), mul2(hl, two(c.hi))));
-    const float2 nw = add2(th, two(whole)), f = add2(add2(nw, two(-whole)), neg(th));
+    const float2 tm = mul2(h, two(-c.hi));  // -th
+    const float2 tl = add2(fma2(h, two(c.hi), tm), fma2(h, two(c.lo), mul2(hl, two(c.hi))));
+    const float2 nw = add2(th, two(whole)), f = add2(add2(nw, two(-whole)), tm);
     const float2 jw = fma2(f, two(16.f), two(whole)), r = fma2(add2(jw, two(-whole)), two(-0.0625f), f);
-    const float2 y0 = mul2(r, two(lh)), y1 = add2(fma2(r, two(lh), neg(y0)), fma2(r, two(ll), mul2(two(-lh), tl)));
-    const float2 yh = add2(y0, y1), yl = add2(y1, neg(add2(yh, neg(y0))));
-    const float2 qh = mul2(yh, yh), ql = fma2(mul2(two(2.f), yh), yl, fma2(yh, yh, neg(qh)));
+    const float2 y0 = mul2(r, two(lh)), ym = mul2(r, two(-lh));
+    const float2 y1 = add2(fma2(r, two(lh), ym), fma2(r, two(ll), mul2(two(-lh), tl)));
+    const float2 yh = add2(y0, y1), yl = less(y1, less(yh, y0));
+    const float2 qh = mul2(yh, yh), ql = fma2(mul2(two(2.f), yh), yl, fma2(yh, yh, mul2(qh, two(-1.f))));
     float2 p = fma2(yh, two(1.f / 720.f), two(1.f / 120.f));
     p = fma2(yh, p, two(1.f / 24.f));
     p = fma2(yh, p, two(1.f / 6.f));
-    const float2 sh = fma2(two(0.5f), qh, yh), se = fma2(two(0.5f), qh, neg(add2(sh, neg(yh))));
+    const float2 sh = fma2(two(0.5f), qh, yh), se = fma2(two(0.5f), qh, less(yh, sh));
     const float2 low = add2(fma2(mul2(qh, yh), p, se), fma2(two(0.5f), ql, yl));
     const bool some0 = th.x < 46.f, some1 = th.y < 46.f;
     const F2 t0 = table[some0 ? __float_as_int(jw.x) - 0x4b400000 + 8 : 0], t1 = table[some1 ? __float_as_int(jw.y) - 0x4b400000 + 8 : 0];
     const float2 ht = make_float2(t0.hi, t1.hi), lt = make_float2(t0.lo, t1.lo);
-    const float2 ph = mul2(ht, sh), pl = fma2(ht, sh, neg(ph));
-    const float2 rh = add2(ht, ph), re = add2(ph, neg(add2(rh, neg(ht))));
+    const float2 ph = mul2(ht, sh), pl = fma2(ht, sh, mul2(ph, two(-1.f)));
+    const float2 rh = add2(ht, ph), re = less(ph, less(rh, ht));
     const float2 rl = add2(add2(re, pl), add2(lt, fma2(ht, low, mul2(lt, sh))));
     const float2 big = mul2(rh, two(0x1p25f)), small = mul2(rl, two(0x1p44f));
     auto join = [](float hi, float lo, float nw) {
