@@ -168,6 +168,12 @@ constexpr int kPer = kParts / 32;
 
 enum : int { COUNT = 0, MASS = 1 };
 
+// A cut by value: kept are logits above x and the first `ties` that are x, of weight w each; `above`: weight above x.
+struct Cut {
+    float x;
+    long long ties;
+    u64 w, above;
+};
 // What the cluster's CTAs tell each other: every CTA has all of it. Entry r * kWarps + w is of warp w of CTA r.
 struct All {
     float top[kParts];   // largest logits of the threads in equal groups, 128 in the cluster
@@ -178,6 +184,10 @@ struct All {
     int n[kMaxCtas];         // tokens that each CTA has listed
     uint32_t key_lo[kMaxCtas], key_hi[kMaxCtas];
     int done[kMaxCtas];
+    // of the values that each CTA looks after: how many tokens have them and what they weigh; what of each CTA's is kept
+    int count[kMaxCtas], odd[kMaxCtas], tied[kMaxCtas];
+    u64 weight[kMaxCtas], kept[kMaxCtas][kMaxCtas];
+    Cut cut;
 };
 // The list of the row's first tokens, in the cluster's first CTA.
 struct List {
@@ -188,9 +198,16 @@ struct List {
 struct Bins {
     uint32_t n[kBins];
 };
+constexpr int kBase = 105 << 7;  // bits of 2^-22 as bf16
+// Numbers of the bf16 logits of each value from the largest down, two to a word: 2^10 > |x| > 2^-22, and 0.
+constexpr int kValues = 8192;
+struct Values {
+    uint32_t n[kValues / 2];
+};
 union Work {
     List list;
     Bins bins;
+    Values values;
 };
 
 template <typename T>
@@ -202,6 +219,7 @@ struct Row {
     const F2* table;
     u64* scan;   // [kWarps]
     u64* found;  // [2]
+    u64* part;   // [kWarps][kMaxCtas]
     int nv, vw;  // vectors; vectors of each warp, a multiple of 32
     int C, rank;
     float m, c2;  // largest logit; -2 log2(e) / T
@@ -429,6 +447,165 @@ struct Row {
         if (below) tell(cl, all->whole, warp_sum(z));
         cl.sync();
     }
+    // Place of a bf16 logit among the values; -1: none.
+    __device__ __forceinline__ static int place_of(uint32_t u) {
+        const int a = (int)(u & 0x7fffu), r = a - kBase;
+        const int p = u & 0x8000u ? kValues / 2 + r : kValues / 2 - 1 - r;
+        return (unsigned)(r - 1) < (unsigned)(kValues / 2 - 1) ? p : a == 0 ? kValues / 2 - 1 : -1;
+    }
+    __device__ __forceinline__ static float value_at(int p) {
+        const uint32_t u = p < kValues / 2 - 1 ? kValues / 2 - 1 - p + kBase : p == kValues / 2 - 1 ? 0u : 0x8000u + p - kValues / 2 + kBase;
+        return __uint_as_float(u << 16);
+    }
+    // Counts this CTA's values; false if the cluster has one without a place. All of the cluster has counted then.
+    __device__ __forceinline__ bool count_values(cg::cluster_group& cl) {
+        for (int i = threadIdx.x; i < kValues / 2; i += kThreads) work->values.n[i] = 0;
+        if (threadIdx.x < kMaxCtas) all->tied[threadIdx.x] = 0;
+        __syncthreads();
+        const int lane = threadIdx.x & 31, v0 = (threadIdx.x >> 5) * vw, v1 = imin(nv, v0 + vw);
+        bool odd = false;
+        for (int v = v0 + lane; v < v1; v += 32) {
+            const uint4 y = data[v];
+            const uint32_t w[4] = {y.x, y.y, y.z, y.w};
+#pragma unroll
+            for (int i = 0; i < 8; ++i) {
+                const uint32_t u = i & 1 ? w[i >> 1] >> 16 : w[i >> 1] & 0xffffu;
+                const int p = place_of(u);
+                if (p >= 0) atomicAdd(&work->values.n[p >> 1], p & 1 ? 0x10000u : 1u);
+                else odd = odd || u != 0xff80u;
+            }
+        }
+        const int any = __syncthreads_or(odd);
+        if (threadIdx.x < C) cl.map_shared_rank(all, threadIdx.x)->odd[rank] = any;
+        cl.sync();
+        return !__any_sync(0xffffffffu, all->odd[(threadIdx.x & 31) % C]);
+    }
+    // f(place, counts, w0, w1) for the pairs of places that this thread looks after; counts[r]: of the two in CTA r
+    template <typename F>
+    __device__ __forceinline__ void each_pair(cg::cluster_group& cl, F f) {
+        const int pairs = kValues / 2 / kThreads / C, at = (rank * kThreads + threadIdx.x) * pairs;
+#pragma unroll 1
+        for (int q = at; q < at + pairs; ++q) {
+            uint32_t n[kMaxCtas], some = 0;
+#pragma unroll
+            for (int r = 0; r < kMaxCtas; ++r) {
+                n[r] = r < C ? cl.map_shared_rank(&work->values, r)->n[q] : 0;
+                some |= n[r];
+            }
+            if (!some) continue;
+            u64 w0, w1;
+            exact_weights(value_at(2 * q), value_at(2 * q + 1), m, c, table, w0, w1);
+            f(2 * q, n, w0, w1);
+        }
+    }
+    // Numbers and weights of the values before this thread's (of all the cluster's; all->count, weight hold the CTAs').
+    __device__ __forceinline__ void sum_values(cg::cluster_group& cl, long long& n_before, u64& w_before, long long& n_mine, u64& w_mine) {
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+        u64 w = 0;
+        int n = 0;
+        each_pair(cl, [&](int, const uint32_t(&k)[kMaxCtas], u64 w0, u64 w1) {
+            uint32_t k0 = 0, k1 = 0;
+#pragma unroll
+            for (int r = 0; r < kMaxCtas; ++r) {
+                k0 += k[r] & 0xffffu;
+                k1 += k[r] >> 16;
+            }
+            n += (int)(k0 + k1);
+            w += k0 * w0 + k1 * w1;
+        });
+        const u64 w_in = warp_scan(w);
+        const int n_in = warp_scan(n);
+        if (lane == 31) {
+            scan[warp] = w_in;
+            reinterpret_cast<int*>(part)[warp] = n_in;
+        }
+        __syncthreads();
+        n_before = n_in - n;
+        w_before = w_in - w;
+        int n_all = 0;
+        u64 w_all = 0;
+        for (int i = 0; i < kWarps; ++i) {
+            if (i < warp) {
+                n_before += reinterpret_cast<int*>(part)[i];
+                w_before += scan[i];
+            }
+            n_all += reinterpret_cast<int*>(part)[i];
+            w_all += scan[i];
+        }
+        if (threadIdx.x < C) {
+            All* o = cl.map_shared_rank(all, threadIdx.x);
+            o->count[rank] = n_all;
+            o->weight[rank] = w_all;
+        }
+        cl.sync();
+        for (int r = 0; r < rank; ++r) {
+            n_before += all->count[r];
+            w_before += all->weight[r];
+        }
+        n_mine = n;
+        w_mine = w;
+    }
+    // The value at which the count (MODE COUNT) or the weight passes the target: told to all of the cluster.
+    template <int MODE>
+    __device__ __forceinline__ Cut cut_values(cg::cluster_group& cl, u64 target, long long n_before, u64 w_before, long long n_mine,
+                                              u64 w_mine) {
+        const u64 before = MODE == COUNT ? (u64)n_before : w_before, mine_ = MODE == COUNT ? (u64)n_mine : w_mine;
+        cl.sync();  // the last cut is read no more
+        if (before < target && before + mine_ >= target) {
+            u64 sum = before, above = w_before;
+            bool done = false;
+            each_pair(cl, [&](int place, const uint32_t(&k)[kMaxCtas], u64 w0, u64 w1) {
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    uint32_t n = 0;
+#pragma unroll
+                    for (int r = 0; r < kMaxCtas; ++r) n += h ? k[r] >> 16 : k[r] & 0xffffu;
+                    const u64 w = h ? w1 : w0, add = MODE == COUNT ? n : n * w;
+                    if (!done && sum + add >= target) {
+                        done = true;
+                        const Cut cut{value_at(place + h), (long long)(MODE == COUNT ? target - sum : (target - sum + w - 1) / w), w, above};
+                        for (int r = 0; r < C; ++r) cl.map_shared_rank(all, r)->cut = cut;
+                    }
+                    sum += add;
+                    above += n * w;
+                }
+            });
+        }
+        cl.sync();
+        return all->cut;
+    }
+    // What of each CTA's tokens a cut keeps: weight above it in all->kept (one share from each CTA), numbers at it in all->tied.
+    __device__ __forceinline__ void keep_values(cg::cluster_group& cl, float x) {
+        u64 s[kMaxCtas] = {};
+        each_pair(cl, [&](int place, const uint32_t(&k)[kMaxCtas], u64 w0, u64 w1) {
+            const float x0 = value_at(place), x1 = value_at(place + 1);
+#pragma unroll
+            for (int r = 0; r < kMaxCtas; ++r) {
+                const uint32_t k0 = k[r] & 0xffffu, k1 = k[r] >> 16;
+                s[r] += (x0 > x ? k0 * w0 : 0) + (x1 > x ? k1 * w1 : 0);
+                if (x0 == x && k0)
+                    for (int o = 0; o < C; ++o) cl.map_shared_rank(all, o)->tied[r] = (int)k0;
+                if (x1 == x && k1)
+                    for (int o = 0; o < C; ++o) cl.map_shared_rank(all, o)->tied[r] = (int)k1;
+            }
+        });
+        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+        u64* per_warp = reinterpret_cast<u64*>(part);  // [kWarps][kMaxCtas]
+        __syncthreads();
+#pragma unroll
+        for (int r = 0; r < kMaxCtas; ++r)
+            if (r < C) {
+                const u64 y = warp_sum(s[r]);
+                if (lane == 0) per_warp[warp * kMaxCtas + r] = y;
+            }
+        __syncthreads();
+        if (threadIdx.x < C) {
+            u64 y = 0;
+            for (int w = 0; w < kWarps; ++w) y += per_warp[w * kMaxCtas + threadIdx.x];
+            for (int o = 0; o < C; ++o) cl.map_shared_rank(all, o)->kept[rank][threadIdx.x] = y;
+        }
+        cl.sync();
+    }
     __device__ __forceinline__ u64 total(const u64* of) const {
         u64 s = 0;
         for (int i = threadIdx.x & 31; i < C * kWarps; i += 32) s += of[i];
@@ -438,6 +615,92 @@ struct Row {
         int n = 0;
         for (int i = threadIdx.x & 31; i < C * kWarps; i += 32) n += all->ties[i];
         return (int)__reduce_add_sync(0xffffffffu, (unsigned)n);
+    }
+    // This warp's kept weight above x, exact or quick, and its numbers of logits that are x.
+    template <bool EXACT>
+    __device__ __forceinline__ void kept_here(float cut, u64* sum, int* ties) const {
+        u64 s = 0;
+        float q = 0.f;
+        int n = 0;
+        each(cut, [&](int, const float(&x)[VE]) {
+#pragma unroll
+            for (int e = 0; e < VE; e += 2) {
+                n += (x[e] == cut) + (x[e + 1] == cut);
+                if (!(x[e] > cut || x[e + 1] > cut)) continue;
+                if (EXACT) {
+                    u64 w0, w1;
+                    exact_weights(x[e], x[e + 1], m, c, table, w0, w1);
+                    s += (x[e] > cut ? w0 : 0) + (x[e + 1] > cut ? w1 : 0);
+                } else {
+                    q += (x[e] > cut ? quick(x[e]) : 0.f) + (x[e + 1] > cut ? quick(x[e + 1]) : 0.f);
+                }
+            }
+        });
+        *sum = warp_sum(EXACT ? s : (u64)__float2ull_rn(q * 0x1p44f));
+        *ties = (int)__reduce_add_sync(0xffffffffu, (unsigned)n);
+    }
+    __device__ __forceinline__ float quick(float x) const { return ex2(fmaf(-0.5f, x, 0.5f * m) * c2); }
+    // The token of this warp's part at which the kept weights, from `base` on, pass the target; `allowed` of those that are
+    // cut.x count. The lane that has it returns true; `slack`: it is sure of it by that much.
+    template <bool EXACT>
+    __device__ __forceinline__ bool walk(float cut, int allowed, u64 tie_w, u64 base, u64 target, u64 slack, int* index, float* at) const {
+        const int lane = threadIdx.x & 31, v0 = (threadIdx.x >> 5) * vw, v1 = imin(nv, v0 + vw);
+        for (int vb = v0; vb < v1; vb += 32) {
+            const int v = vb + lane;
+            float x[VE];
+            int tied = 0;
+#pragma unroll
+            for (int e = 0; e < VE; ++e) x[e] = -INFINITY;
+            if (v < v1) unpack<T>(data[v], x);
+#pragma unroll
+            for (int e = 0; e < VE; ++e) tied += x[e] == cut;
+            int mine_ = 0;  // of the tied ones, those that count
+            if (__any_sync(0xffffffffu, tied)) {
+                const int upto = warp_scan(tied);
+                mine_ = imax(0, imin(tied, allowed - (upto - tied)));
+                allowed -= __shfl_sync(0xffffffffu, upto, 31);
+            }
+            u64 s = (u64)mine_ * tie_w;
+            float q = 0.f;
+            if (EXACT) {
+#pragma unroll
+                for (int e = 0; e < VE; e += 2) {
+                    u64 w0, w1;
+                    if (!(x[e] > cut || x[e + 1] > cut)) continue;
+                    exact_weights(x[e], x[e + 1], m, c, table, w0, w1);
+                    s += (x[e] > cut ? w0 : 0) + (x[e + 1] > cut ? w1 : 0);
+                }
+            } else {
+#pragma unroll
+                for (int e = 0; e < VE; ++e) q += x[e] > cut ? quick(x[e]) : 0.f;
+                s += __float2ull_rn(q * 0x1p44f);
+            }
+            const u64 in = warp_scan(s) + base;
+            const unsigned hit = __ballot_sync(0xffffffffu, in > target);
+            if (hit) {
+                bool got = false;
+                if (lane == __ffs(hit) - 1) {
+                    u64 run = in - s;
+#pragma unroll 1
+                    for (int e = 0; e < VE; ++e) {
+                        const float y = (float)reinterpret_cast<const T*>(data + v)[e];
+                        u64 w = 0;
+                        if (y > cut) w = EXACT ? exact(y) : (u64)__float2ull_rn(quick(y) * 0x1p44f);
+                        else if (y == cut) w = mine_-- > 0 ? tie_w : 0;
+                        if (run + w > target) {
+                            *index = v * VE + e;
+                            *at = y;
+                            got = run + slack <= target && run + w > target + slack;
+                            break;
+                        }
+                        run += w;
+                    }
+                }
+                return got;
+            }
+            base = __shfl_sync(0xffffffffu, in, 31);
+        }
+        return false;
     }
     __device__ __forceinline__ u64 cta_sum(u64 x) {
         x = warp_sum(x);
@@ -459,7 +722,7 @@ __global__ void __launch_bounds__(kThreads, KM) sample_kernel(const SampleArgs a
     __shared__ F2 s_table[kTable];
     __shared__ u64 s_scan[kWarps], s_found[2];
     __shared__ int s_n, s_nan;
-    __shared__ u64 s_part[3][kWarps];
+    __shared__ u64 s_part[kMaxCtas][kWarps];
     cg::cluster_group cl = cg::this_cluster();
     // (rows that are left leave with all of their CTAs)
     const int rank = (int)cl.block_rank(), row = blockIdx.x / a.ctas;
@@ -477,6 +740,7 @@ __global__ void __launch_bounds__(kThreads, KM) sample_kernel(const SampleArgs a
     R.table = s_table;
     R.scan = s_scan;
     R.found = s_found;
+    R.part = s_part[0];
     R.nv = n ? (skew + n + VE - 1) / VE : 0;
     R.vw = ((R.nv + kWarps - 1) / kWarps + 31) & ~31;
     R.C = a.ctas;
@@ -799,47 +1063,103 @@ __global__ void __launch_bounds__(kThreads, KM) sample_kernel(const SampleArgs a
                 base = __shfl_sync(0xffffffffu, base, __ffs(hit) - 1);
             }
             if (who >= 0 && who == rank * kWarps + warp) {
-                for (int vb = v0; vb < v1; vb += 32) {
-                    const int v = vb + lane;
-                    float x[VE], wf[VE], sf = 0.f;
-                    if (v < v1) {
-                        unpack<T>(s_data[v], x);
-#pragma unroll
-                        for (int e = 0; e < VE; ++e) {
-                            wf[e] = ex2(fmaf(-0.5f, x[e], 0.5f * R.m) * R.c2);
-                            sf += wf[e];
-                        }
-                    }
-                    const u64 s = __float2ull_rn(sf * 0x1p44f), in = warp_scan(s) + base;
-                    const unsigned at_lane = __ballot_sync(0xffffffffu, in > target);
-                    if (at_lane) {
-                        if (lane == __ffs(at_lane) - 1) {
-                            u64 run = in - s;
-#pragma unroll
-                            for (int e = 0; e < VE; ++e) {
-                                const u64 we = __float2ull_rn(wf[e] * 0x1p44f);
-                                if (token < 0 && run + we > target) {
-                                    token = first + v * VE + e - skew;
-                                    at = x[e];
-                                    mine = run + 2 * off < target && run + we > target + 2 * off;
-                                }
-                                run += we;
-                            }
-                            if (mine)
-                                for (int r = 0; r < a.ctas; ++r) cl.map_shared_rank(&s_all, r)->done[rank] = 1;
-                        }
-                        break;
-                    }
-                    base = __shfl_sync(0xffffffffu, in, 31);
-                }
+                mine = R.template walk<false>(-INFINITY, 0, 0, base, target, 2 * off, &token, &at);
+                if (mine)
+                    for (int r = 0; r < a.ctas; ++r) cl.map_shared_rank(&s_all, r)->done[rank] = 1;
             }
             cl.sync();
             found = __any_sync(0xffffffffu, lane < a.ctas && s_all.done[lane]);
-            if (!found) {
-                token = -1;
-                mine = false;
-                R.weigh(cl, cut, false);
+        }
+        bool valued = false;  // the token is found from counted values
+        if constexpr (sizeof(T) == 2 && Type<T>::SHIFT == 16) {
+            if (!found && !greedy && R.count_values(cl)) {
+                valued = true;
+                long long n_before, n_mine;
+                u64 w_before, w_mine;
+                R.sum_values(cl, n_before, w_before, n_mine, w_mine);
+                Cut by{-INFINITY, 0, 0, 0};
+                long long counted = 0;  // (masked tokens are not)
+                u64 z = 0;
+                for (int r = 0; r < a.ctas; ++r) {
+                    counted += s_all.count[r];
+                    z += s_all.weight[r];
+                }
+                if (by_k && counted > top_k) {
+                    by = R.template cut_values<COUNT>(cl, (u64)top_k, n_before, w_before, n_mine, w_mine);
+                    z = by.above + (u64)by.ties * by.w;
+                }
+                if (by_p) {
+                    by = R.template cut_values<MASS>(cl, mul_ceil(p, z), n_before, w_before, n_mine, w_mine);
+                }
+                if (by_min) {
+                    const float x = R.at_key(R.key_from(least_w));
+                    if (x > by.x) by = Cut{x, 1ll << 40, R.exact(x), 0};
+                }
+                R.keep_values(cl, by.x);
+                // the CTA in which the sum passes u times all of it: it alone goes on
+                u64 kept[kMaxCtas], sum = 0;
+                long long rest = by.ties;
+                int take[kMaxCtas];
+#pragma unroll
+                for (int r = 0; r < kMaxCtas; ++r) {
+                    kept[r] = 0;
+                    take[r] = 0;
+                    if (r < a.ctas) {
+                        for (int o = 0; o < a.ctas; ++o) kept[r] += s_all.kept[o][r];
+                        take[r] = (int)(rest < s_all.tied[r] ? rest : s_all.tied[r]);
+                        rest -= take[r];
+                        kept[r] += (u64)take[r] * by.w;
+                        sum += kept[r];
+                    }
+                }
+                u64 target = mul_floor(u, sum), base = 0, have = 0;
+                target = target < sum ? target : sum - 1;
+                int who = -1, allowed = 0;
+#pragma unroll
+                for (int r = 0; r < kMaxCtas; ++r) {
+                    if (who < 0 && base + kept[r] > target) {
+                        who = r;
+                        allowed = take[r];
+                        have = kept[r];
+                    }
+                    if (who < 0) base += kept[r];
+                }
+                if (who != rank) return;
+                target -= base;
+                if (tid == 0) s_n = 0;
+                // its warps' parts and the token, by quick weights and, where their error leaves it open, by exact ones
+                for (int exact = 0; exact < 2; ++exact) {
+                    u64 s;
+                    int n;
+                    if (exact) R.template kept_here<true>(by.x, &s, &n);
+                    else R.template kept_here<false>(by.x, &s, &n);
+                    __syncthreads();
+                    if (lane == 0) {
+                        s_scan[warp] = s;
+                        s_all.ties[warp] = n;
+                    }
+                    __syncthreads();
+                    const int at_warp = lane < kWarps ? s_all.ties[lane] : 0, left = allowed - (warp_scan(at_warp) - at_warp);
+                    const int count = imax(0, imin(left, at_warp));
+                    const u64 y = lane < kWarps ? s_scan[lane] + (u64)count * by.w : 0, upto = warp_scan(y);
+                    const unsigned hit = __ballot_sync(0xffffffffu, upto > target);
+                    if (hit) {
+                        const int l = __ffs(hit) - 1, mine_ = __shfl_sync(0xffffffffu, count, l);
+                        const u64 from = __shfl_sync(0xffffffffu, upto - y, l);
+                        if (warp == l) {
+                            if (exact) mine = R.template walk<true>(by.x, mine_, by.w, from, target, 0, &token, &at);
+                            else mine = R.template walk<false>(by.x, mine_, by.w, from, target, (u64)((float)have * (float)kQuick) + 64, &token, &at);
+                            if (mine) s_n = 1;
+                        }
+                    }
+                    __syncthreads();
+                    if (s_n) break;
+                }
             }
+        }
+        if (found || valued) {
+        } else if (!cuts) {
+            R.weigh(cl, cut, false);
         } else if (greedy) {
             cut = R.key_of(R.m);
             ties = 1;
@@ -884,7 +1204,7 @@ __global__ void __launch_bounds__(kThreads, KM) sample_kernel(const SampleArgs a
                 }
             }
         }
-        if (!found) {
+        if (!found && !valued) {
             // what each warp's part keeps, and the part in which the sum passes u times all of it
             const u64 tie_w = ties ? R.exact(R.at_key(cut)) : 0;
             int have[kPer], take[kPer], n4 = 0;
@@ -922,52 +1242,10 @@ __global__ void __launch_bounds__(kThreads, KM) sample_kernel(const SampleArgs a
             who = __shfl_sync(0xffffffffu, who, l);
             base = __shfl_sync(0xffffffffu, base, l);
             allowed = __shfl_sync(0xffffffffu, allowed, l);
-            if (who == rank * kWarps + warp) {
-                for (int vb = v0; vb < v1; vb += 32) {
-                    const int v = vb + lane;
-                    float x[VE];
-                    u64 w[VE], s = 0;
-                    int tied = 0;
-                    if (v < v1) {
-                        unpack<T>(s_data[v], x);
-#pragma unroll
-                        for (int e = 0; e < VE; ++e) tied += R.key_of(x[e]) == cut;
-                    }
-                    int before = warp_scan(tied);
-                    const int all_tied = __shfl_sync(0xffffffffu, before, 31);
-                    before -= tied;
-                    if (v < v1) {
-#pragma unroll
-                        for (int e = 0; e < VE; ++e) {
-                            const uint32_t k = R.key_of(x[e]);
-                            w[e] = 0;
-                            if (k > cut) w[e] = R.exact(x[e]);
-                            else if (k == cut) w[e] = before++ < allowed ? tie_w : 0;
-                            s += w[e];
-                        }
-                    }
-                    allowed -= all_tied;
-                    const u64 in = warp_scan(s) + base;
-                    const unsigned hit = __ballot_sync(0xffffffffu, in > target);
-                    if (hit) {
-                        if (lane == __ffs(hit) - 1) {
-                            u64 sum = in - s;
-#pragma unroll
-                            for (int e = 0; e < VE; ++e) {
-                                sum += w[e];
-                                if (!mine && sum > target) {
-                                    token = first + v * VE + e - skew;
-                                    at = x[e];
-                                    mine = true;
-                                }
-                            }
-                        }
-                        break;
-                    }
-                    base = __shfl_sync(0xffffffffu, in, 31);
-                }
-            }
+            if (who == rank * kWarps + warp)
+                mine = R.template walk<true>(cut ? R.at_key(cut) : -INFINITY, allowed, tie_w, base, target, 0, &token, &at);
         }
+        token += first - skew;
     }
     if (mine) {
         // whole_z is at least 1; near it the logarithm is taken of what it is more
