@@ -40,11 +40,7 @@ namespace {
 using namespace sample;
 namespace cg = cooperative_groups;
 
-#ifndef KT
-#define KT 512
-#define KM 2
-#endif
-constexpr int kThreads = KT;
+constexpr int kThreads = 512;
 constexpr int kWarps = kThreads / 32;
 constexpr int kBins = 512;
 constexpr int kMaxCtas = 8;
@@ -168,11 +164,13 @@ constexpr int kPer = kParts / 32;
 
 enum : int { COUNT = 0, MASS = 1 };
 
-// A cut by value: kept are logits above x and the first `ties` that are x, of weight w each; `above`: weight above x.
+// A cut by value: kept are the logits before place `at` and the first `ties` that have its value x, of weight w each;
+// `above`: what those before it weigh.
 struct Cut {
-    float x;
+    int at;
     long long ties;
     u64 w, above;
+    float x;
 };
 // What the cluster's CTAs tell each other: every CTA has all of it. Entry r * kWarps + w is of warp w of CTA r.
 struct All {
@@ -184,15 +182,12 @@ struct All {
     int n[kMaxCtas];         // tokens that each CTA has listed
     uint32_t key_lo[kMaxCtas], key_hi[kMaxCtas];
     int done[kMaxCtas];
-    // of the values that each CTA looks after: how many tokens have them and what they weigh; what of each CTA's is kept
-    int count[kMaxCtas], odd[kMaxCtas], tied[kMaxCtas];
-    u64 weight[kMaxCtas], kept[kMaxCtas][kMaxCtas];
-    Cut cut;
+    int odd[kMaxCtas];  // whether it has a logit without a place
 };
 // The list of the row's first tokens, in the cluster's first CTA.
 struct List {
     uint2 raw[kList];  // key, number; each CTA has an equal part of it
-    u64 order[kList], w[kList], kept[kList];
+    ulonglong2 tokens[kList], kept[kList];  // order, weight
 };
 // Bins of a select; the list is done with by then.
 struct Bins {
@@ -203,6 +198,12 @@ constexpr int kBase = 105 << 7;  // bits of 2^-22 as bf16
 constexpr int kValues = 8192;
 struct Values {
     uint32_t n[kValues / 2];
+};
+constexpr int kStretch = kValues / kThreads;  // places that a thread looks after
+// What the values before each stretch of places number and weigh, in this CTA and (sum) in the cluster.
+struct Upto {
+    u64 weight[kThreads + 1], sum_weight[kThreads + 1];
+    int count[kThreads + 1], sum_count[kThreads + 1];
 };
 union Work {
     List list;
@@ -219,7 +220,8 @@ struct Row {
     const F2* table;
     u64* scan;   // [kWarps]
     u64* found;  // [2]
-    u64* part;   // [kWarps][kMaxCtas]
+    u64* part;   // [kWarps]
+    Upto* upto;
     int nv, vw;  // vectors; vectors of each warp, a multiple of 32
     int C, rank;
     float m, c2;  // largest logit; -2 log2(e) / T
@@ -449,20 +451,26 @@ struct Row {
     }
     // Place of a bf16 logit among the values; -1: none.
     __device__ __forceinline__ static int place_of(uint32_t u) {
-        const int a = (int)(u & 0x7fffu), r = a - kBase;
-        const int p = u & 0x8000u ? kValues / 2 + r : kValues / 2 - 1 - r;
-        return (unsigned)(r - 1) < (unsigned)(kValues / 2 - 1) ? p : a == 0 ? kValues / 2 - 1 : -1;
+        const int a = (int)(u & 0x7fffu), r = a - kBase, sign = (int)(u << 16) >> 31;
+        return (unsigned)(r - 1) < (unsigned)(kValues / 2 - 1) ? kValues / 2 - 1 - (r ^ sign) : a == 0 ? kValues / 2 - 1 : -1;
     }
     __device__ __forceinline__ static float value_at(int p) {
         const uint32_t u = p < kValues / 2 - 1 ? kValues / 2 - 1 - p + kBase : p == kValues / 2 - 1 ? 0u : 0x8000u + p - kValues / 2 + kBase;
         return __uint_as_float(u << 16);
     }
-    // Counts this CTA's values; false if the cluster has one without a place. All of the cluster has counted then.
+    // The first place whose value is not above x.
+    __device__ __forceinline__ static int place_from(float x) {
+        const int r = (int)(__float_as_uint(fabsf(x)) >> 16) - kBase;
+        if (x > 0.f) return kValues / 2 - 1 - imax(0, imin(r, kValues / 2 - 1));
+        return x == 0.f ? kValues / 2 - 1 : kValues / 2 + imax(0, imin(r, kValues / 2));
+    }
+    // Counts the values of this CTA's part, and sums up what those before each stretch number and weigh; false if the
+    // cluster has a logit without a place. All of the cluster has summed up then.
     __device__ __forceinline__ bool count_values(cg::cluster_group& cl) {
-        for (int i = threadIdx.x; i < kValues / 2; i += kThreads) work->values.n[i] = 0;
-        if (threadIdx.x < kMaxCtas) all->tied[threadIdx.x] = 0;
+        uint32_t* count = work->values.n;
+        for (int i = threadIdx.x; i < kValues / 2; i += kThreads) count[i] = 0;
         __syncthreads();
-        const int lane = threadIdx.x & 31, v0 = (threadIdx.x >> 5) * vw, v1 = imin(nv, v0 + vw);
+        const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, v0 = warp * vw, v1 = imin(nv, v0 + vw);
         bool odd = false;
         for (int v = v0 + lane; v < v1; v += 32) {
             const uint4 y = data[v];
@@ -471,140 +479,110 @@ struct Row {
             for (int i = 0; i < 8; ++i) {
                 const uint32_t u = i & 1 ? w[i >> 1] >> 16 : w[i >> 1] & 0xffffu;
                 const int p = place_of(u);
-                if (p >= 0) atomicAdd(&work->values.n[p >> 1], p & 1 ? 0x10000u : 1u);
+                if (p >= 0) atomicAdd(count + (p >> 1), p & 1 ? 0x10000u : 1u);
                 else odd = odd || u != 0xff80u;
             }
         }
         const int any = __syncthreads_or(odd);
-        if (threadIdx.x < C) cl.map_shared_rank(all, threadIdx.x)->odd[rank] = any;
-        cl.sync();
-        return !__any_sync(0xffffffffu, all->odd[(threadIdx.x & 31) % C]);
-    }
-    // f(place, counts, w0, w1) for the pairs of places that this thread looks after; counts[r]: of the two in CTA r
-    template <typename F>
-    __device__ __forceinline__ void each_pair(cg::cluster_group& cl, F f) {
-        const int pairs = kValues / 2 / kThreads / C, at = (rank * kThreads + threadIdx.x) * pairs;
-#pragma unroll 1
-        for (int q = at; q < at + pairs; ++q) {
-            uint32_t n[kMaxCtas], some = 0;
-#pragma unroll
-            for (int r = 0; r < kMaxCtas; ++r) {
-                n[r] = r < C ? cl.map_shared_rank(&work->values, r)->n[q] : 0;
-                some |= n[r];
-            }
-            if (!some) continue;
-            u64 w0, w1;
-            exact_weights(value_at(2 * q), value_at(2 * q + 1), m, c, table, w0, w1);
-            f(2 * q, n, w0, w1);
-        }
-    }
-    // Numbers and weights of the values before this thread's (of all the cluster's; all->count, weight hold the CTAs').
-    __device__ __forceinline__ void sum_values(cg::cluster_group& cl, long long& n_before, u64& w_before, long long& n_mine, u64& w_mine) {
-        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
+        if (tid < C) cl.map_shared_rank(all, tid)->odd[rank] = any;
         u64 w = 0;
         int n = 0;
-        each_pair(cl, [&](int, const uint32_t(&k)[kMaxCtas], u64 w0, u64 w1) {
-            uint32_t k0 = 0, k1 = 0;
-#pragma unroll
-            for (int r = 0; r < kMaxCtas; ++r) {
-                k0 += k[r] & 0xffffu;
-                k1 += k[r] >> 16;
-            }
-            n += (int)(k0 + k1);
-            w += k0 * w0 + k1 * w1;
-        });
-        const u64 w_in = warp_scan(w);
-        const int n_in = warp_scan(n);
+#pragma unroll 1
+        for (int q = tid * (kStretch / 2); q < (tid + 1) * (kStretch / 2); ++q) {
+            const uint32_t y = count[q];
+            if (!y) continue;
+            u64 w0, w1;
+            exact_weights(value_at(2 * q), value_at(2 * q + 1), m, c, table, w0, w1);
+            n += (int)((y & 0xffffu) + (y >> 16));
+            w += (y & 0xffffu) * w0 + (y >> 16) * w1;
+        }
+        u64 w_in = warp_scan(w);
+        int n_in = warp_scan(n);
         if (lane == 31) {
             scan[warp] = w_in;
-            reinterpret_cast<int*>(part)[warp] = n_in;
+            part[warp] = (u64)n_in;
         }
         __syncthreads();
-        n_before = n_in - n;
-        w_before = w_in - w;
-        int n_all = 0;
-        u64 w_all = 0;
-        for (int i = 0; i < kWarps; ++i) {
-            if (i < warp) {
-                n_before += reinterpret_cast<int*>(part)[i];
-                w_before += scan[i];
-            }
-            n_all += reinterpret_cast<int*>(part)[i];
-            w_all += scan[i];
+        for (int i = 0; i < warp; ++i) {
+            w_in += scan[i];
+            n_in += (int)part[i];
         }
-        if (threadIdx.x < C) {
-            All* o = cl.map_shared_rank(all, threadIdx.x);
-            o->count[rank] = n_all;
-            o->weight[rank] = w_all;
+        upto->weight[tid + 1] = w_in;
+        upto->count[tid + 1] = n_in;
+        if (tid == 0) {
+            upto->weight[0] = 0;
+            upto->count[0] = 0;
         }
         cl.sync();
-        for (int r = 0; r < rank; ++r) {
-            n_before += all->count[r];
-            w_before += all->weight[r];
-        }
-        n_mine = n;
-        w_mine = w;
-    }
-    // The value at which the count (MODE COUNT) or the weight passes the target: told to all of the cluster.
-    template <int MODE>
-    __device__ __forceinline__ Cut cut_values(cg::cluster_group& cl, u64 target, long long n_before, u64 w_before, long long n_mine,
-                                              u64 w_mine) {
-        const u64 before = MODE == COUNT ? (u64)n_before : w_before, mine_ = MODE == COUNT ? (u64)n_mine : w_mine;
-        cl.sync();  // the last cut is read no more
-        if (before < target && before + mine_ >= target) {
-            u64 sum = before, above = w_before;
-            bool done = false;
-            each_pair(cl, [&](int place, const uint32_t(&k)[kMaxCtas], u64 w0, u64 w1) {
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    uint32_t n = 0;
-#pragma unroll
-                    for (int r = 0; r < kMaxCtas; ++r) n += h ? k[r] >> 16 : k[r] & 0xffffu;
-                    const u64 w = h ? w1 : w0, add = MODE == COUNT ? n : n * w;
-                    if (!done && sum + add >= target) {
-                        done = true;
-                        const Cut cut{value_at(place + h), (long long)(MODE == COUNT ? target - sum : (target - sum + w - 1) / w), w, above};
-                        for (int r = 0; r < C; ++r) cl.map_shared_rank(all, r)->cut = cut;
-                    }
-                    sum += add;
-                    above += n * w;
-                }
-            });
-        }
-        cl.sync();
-        return all->cut;
-    }
-    // What of each CTA's tokens a cut keeps: weight above it in all->kept (one share from each CTA), numbers at it in all->tied.
-    __device__ __forceinline__ void keep_values(cg::cluster_group& cl, float x) {
-        u64 s[kMaxCtas] = {};
-        each_pair(cl, [&](int place, const uint32_t(&k)[kMaxCtas], u64 w0, u64 w1) {
-            const float x0 = value_at(place), x1 = value_at(place + 1);
-#pragma unroll
-            for (int r = 0; r < kMaxCtas; ++r) {
-                const uint32_t k0 = k[r] & 0xffffu, k1 = k[r] >> 16;
-                s[r] += (x0 > x ? k0 * w0 : 0) + (x1 > x ? k1 * w1 : 0);
-                if (x0 == x && k0)
-                    for (int o = 0; o < C; ++o) cl.map_shared_rank(all, o)->tied[r] = (int)k0;
-                if (x1 == x && k1)
-                    for (int o = 0; o < C; ++o) cl.map_shared_rank(all, o)->tied[r] = (int)k1;
-            }
-        });
-        const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-        u64* per_warp = reinterpret_cast<u64*>(part);  // [kWarps][kMaxCtas]
-        __syncthreads();
+        if (__any_sync(0xffffffffu, all->odd[lane % C])) return false;
+        u64 sw = 0;
+        int sn = 0;
 #pragma unroll
         for (int r = 0; r < kMaxCtas; ++r)
             if (r < C) {
-                const u64 y = warp_sum(s[r]);
-                if (lane == 0) per_warp[warp * kMaxCtas + r] = y;
+                const Upto* o = cl.map_shared_rank(upto, r);
+                sw += o->weight[tid + 1];
+                sn += o->count[tid + 1];
             }
-        __syncthreads();
-        if (threadIdx.x < C) {
-            u64 y = 0;
-            for (int w = 0; w < kWarps; ++w) y += per_warp[w * kMaxCtas + threadIdx.x];
-            for (int o = 0; o < C; ++o) cl.map_shared_rank(all, o)->kept[rank][threadIdx.x] = y;
+        upto->sum_weight[tid + 1] = sw;
+        upto->sum_count[tid + 1] = sn;
+        if (tid == 0) {
+            upto->sum_weight[0] = 0;
+            upto->sum_count[0] = 0;
         }
-        cl.sync();
+        __syncthreads();
+        return true;
+    }
+    // Numbers of a place's value in the cluster's CTAs, by the lanes of a warp together: lane l has CTA l's.
+    __device__ __forceinline__ int count_at(cg::cluster_group& cl, int place) const {
+        const int lane = threadIdx.x & 31;
+        const uint32_t y = lane < C ? cl.map_shared_rank(&work->values, lane)->n[place >> 1] : 0;
+        return (int)(place & 1 ? y >> 16 : y & 0xffffu);
+    }
+    // The place at which the count (MODE COUNT) or the weight passes the target, by every warp for itself.
+    template <int MODE>
+    __device__ __forceinline__ Cut cut_values(cg::cluster_group& cl, u64 target) {
+        const int tid = threadIdx.x, lane = tid & 31;
+        const u64 lo = MODE == COUNT ? (u64)upto->sum_count[tid] : upto->sum_weight[tid];
+        const u64 hi = MODE == COUNT ? (u64)upto->sum_count[tid + 1] : upto->sum_weight[tid + 1];
+        __syncthreads();
+        if (lo < target && hi >= target) found[0] = tid;
+        __syncthreads();
+        // the places of that stretch, one per lane (two lanes' worth of sums: all are kept by every warp)
+        const int t = (int)found[0], place = t * kStretch + lane;
+        int n = 0;
+        u64 w = 0;
+        if (lane < kStretch) {
+#pragma unroll
+            for (int r = 0; r < kMaxCtas; ++r)
+                if (r < C) {
+                    const uint32_t y = cl.map_shared_rank(&work->values, r)->n[place >> 1];
+                    n += (int)(place & 1 ? y >> 16 : y & 0xffffu);
+                }
+            if (n) w = exact(value_at(place));
+        }
+        const u64 add = MODE == COUNT ? (u64)n : (u64)n * w, base = MODE == COUNT ? (u64)upto->sum_count[t] : upto->sum_weight[t];
+        const u64 in = warp_scan(add) + base, above = warp_scan((u64)n * w) - (u64)n * w + upto->sum_weight[t];
+        const int l = __ffs(__ballot_sync(0xffffffffu, in >= target)) - 1;
+        Cut cut;
+        cut.at = t * kStretch + l;
+        cut.x = value_at(cut.at);
+        cut.w = __shfl_sync(0xffffffffu, w, l);
+        cut.above = __shfl_sync(0xffffffffu, above, l);
+        const u64 rest = target - __shfl_sync(0xffffffffu, in - add, l);
+        cut.ties = (long long)(MODE == COUNT ? rest : (rest + cut.w - 1) / cut.w);
+        return cut;
+    }
+    // What a cut keeps of CTA `lane`'s tokens: what those before it weigh, and the number of those at it.
+    __device__ __forceinline__ u64 kept_of(cg::cluster_group& cl, const Cut& cut, int* tied) const {
+        const int lane = threadIdx.x & 31, t = imin(cut.at, kValues) / kStretch;
+        u64 s = lane < C ? cl.map_shared_rank(upto, lane)->weight[t] : 0;
+        for (int p = t * kStretch; p < imin(cut.at, kValues); ++p) {
+            const int n = count_at(cl, p);
+            if (__any_sync(0xffffffffu, n)) s += (u64)n * exact(value_at(p));
+        }
+        *tied = cut.at < kValues && value_at(cut.at) == cut.x ? count_at(cl, cut.at) : 0;
+        return s;
     }
     __device__ __forceinline__ u64 total(const u64* of) const {
         u64 s = 0;
@@ -714,7 +692,7 @@ struct Row {
 };
 
 template <typename T>
-__global__ void __launch_bounds__(kThreads, KM) sample_kernel(const SampleArgs a) {
+__global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a) {
     constexpr int VE = Type<T>::VE;
     extern __shared__ uint4 s_data[];
     __shared__ All s_all;
@@ -722,7 +700,8 @@ __global__ void __launch_bounds__(kThreads, KM) sample_kernel(const SampleArgs a
     __shared__ F2 s_table[kTable];
     __shared__ u64 s_scan[kWarps], s_found[2];
     __shared__ int s_n, s_nan;
-    __shared__ u64 s_part[kMaxCtas][kWarps];
+    __shared__ u64 s_part[3][kWarps];
+    __shared__ Upto s_upto;
     cg::cluster_group cl = cg::this_cluster();
     // (rows that are left leave with all of their CTAs)
     const int rank = (int)cl.block_rank(), row = blockIdx.x / a.ctas;
@@ -741,6 +720,7 @@ __global__ void __launch_bounds__(kThreads, KM) sample_kernel(const SampleArgs a
     R.scan = s_scan;
     R.found = s_found;
     R.part = s_part[0];
+    R.upto = &s_upto;
     R.nv = n ? (skew + n + VE - 1) / VE : 0;
     R.vw = ((R.nv + kWarps - 1) / kWarps + 31) & ~31;
     R.C = a.ctas;
@@ -966,8 +946,7 @@ __global__ void __launch_bounds__(kThreads, KM) sample_kernel(const SampleArgs a
             int i = tid, r = 0;
             for (; i >= s_all.n[r]; ++r) i -= s_all.n[r];
             const uint2 y = list.raw[r * (kList / a.ctas) + i];
-            list.order[tid] = (u64)y.x << 32 | ~y.y;
-            list.w[tid] = R.exact(__uint_as_float(y.x & 0x80000000u ? y.x ^ 0x80000000u : ~y.x));
+            list.tokens[tid] = make_ulonglong2((u64)y.x << 32 | ~y.y, R.exact(__uint_as_float(y.x & 0x80000000u ? y.x ^ 0x80000000u : ~y.x)));
         }
         __syncthreads();
         // G threads for each token, each looks at every G-th other
@@ -977,13 +956,13 @@ __global__ void __launch_bounds__(kThreads, KM) sample_kernel(const SampleArgs a
         u64 before = 0;
         int ahead = 0;
         if (i < ln) {
-            me = list.order[i];
-            w = list.w[i];
+            me = list.tokens[i].x;
+            w = list.tokens[i].y;
 #pragma unroll 4
             for (int j = g; j < ln; j += G) {
-                const u64 other = list.order[j], ow = list.w[j];
-                before += other > me ? ow : 0;
-                ahead += other > me;
+                const ulonglong2 o = list.tokens[j];
+                before += o.x > me ? o.y : 0;
+                ahead += o.x > me;
             }
         }
         for (int o = 1; o < G; o *= 2) {
@@ -1013,18 +992,28 @@ __global__ void __launch_bounds__(kThreads, KM) sample_kernel(const SampleArgs a
             keep = keep && (ahead == 0 || before < lo);
         }
         if (by_min) keep = keep && w >= least_w;
-        if (g == 0 && i < ln) list.kept[i] = keep ? w : 0;
-        const u64 all = R.cta_sum(keep && g == 0 ? w : 0);  // (its barriers order list.kept)
+        // the kept ones, and of each the weight of those up to its number
+        if (tid == 0) s_n = 0;
+        const u64 all = R.cta_sum(keep && g == 0 ? w : 0);  // (its barriers order s_n)
+        if (keep && g == 0) list.kept[atomicAdd(&s_n, 1)] = make_ulonglong2(me, w);
+        __syncthreads();
+        const int kn = s_n;
         u64 target = mul_floor(u, all), upto = 0;
         target = target < all ? target : all - 1;
-        if (i < ln)
+        G = 1;
+        while (2 * G * kn <= kThreads && G < 32) G *= 2;
+        const int ki = tid / G;
+        if (ki < kn) {
+            me = list.kept[ki].x;
+            w = list.kept[ki].y;
 #pragma unroll 4
-            for (int j = g; j < ln; j += G) {
-                const u64 ow = list.kept[j];
-                upto += (uint32_t)list.order[j] >= (uint32_t)me ? ow : 0;
+            for (int j = tid % G; j < kn; j += G) {
+                const ulonglong2 o = list.kept[j];
+                upto += (uint32_t)o.x >= (uint32_t)me ? o.y : 0;
             }
+        }
         for (int o = 1; o < G; o *= 2) upto += __shfl_xor_sync(0xffffffffu, upto, o);
-        if (keep && g == 0 && upto > target && upto - w <= target) {
+        if (ki < kn && tid % G == 0 && upto > target && upto - w <= target) {
             const uint32_t k = (uint32_t)(me >> 32);
             token = (int)~(uint32_t)me;
             at = __uint_as_float(k & 0x80000000u ? k ^ 0x80000000u : ~k);
@@ -1074,58 +1063,33 @@ __global__ void __launch_bounds__(kThreads, KM) sample_kernel(const SampleArgs a
         if constexpr (sizeof(T) == 2 && Type<T>::SHIFT == 16) {
             if (!found && !greedy && R.count_values(cl)) {
                 valued = true;
-                long long n_before, n_mine;
-                u64 w_before, w_mine;
-                R.sum_values(cl, n_before, w_before, n_mine, w_mine);
-                Cut by{-INFINITY, 0, 0, 0};
-                long long counted = 0;  // (masked tokens are not)
-                u64 z = 0;
-                for (int r = 0; r < a.ctas; ++r) {
-                    counted += s_all.count[r];
-                    z += s_all.weight[r];
-                }
-                if (by_k && counted > top_k) {
-                    by = R.template cut_values<COUNT>(cl, (u64)top_k, n_before, w_before, n_mine, w_mine);
+                Cut by{kValues, 0, 0, 0, -INFINITY};
+                u64 z = s_upto.sum_weight[kThreads];
+                if (by_k && s_upto.sum_count[kThreads] > top_k) {  // (masked tokens are not counted)
+                    by = R.template cut_values<COUNT>(cl, (u64)top_k);
                     z = by.above + (u64)by.ties * by.w;
                 }
-                if (by_p) {
-                    by = R.template cut_values<MASS>(cl, mul_ceil(p, z), n_before, w_before, n_mine, w_mine);
-                }
+                if (by_p) by = R.template cut_values<MASS>(cl, mul_ceil(p, z));
                 if (by_min) {
                     const float x = R.at_key(R.key_from(least_w));
-                    if (x > by.x) by = Cut{x, 1ll << 40, R.exact(x), 0};
+                    if (x > by.x) by = Cut{R.place_from(x), 1ll << 40, R.exact(x), 0, x};
                 }
-                R.keep_values(cl, by.x);
-                // the CTA in which the sum passes u times all of it: it alone goes on
-                u64 kept[kMaxCtas], sum = 0;
-                long long rest = by.ties;
-                int take[kMaxCtas];
-#pragma unroll
-                for (int r = 0; r < kMaxCtas; ++r) {
-                    kept[r] = 0;
-                    take[r] = 0;
-                    if (r < a.ctas) {
-                        for (int o = 0; o < a.ctas; ++o) kept[r] += s_all.kept[o][r];
-                        take[r] = (int)(rest < s_all.tied[r] ? rest : s_all.tied[r]);
-                        rest -= take[r];
-                        kept[r] += (u64)take[r] * by.w;
-                        sum += kept[r];
-                    }
-                }
-                u64 target = mul_floor(u, sum), base = 0, have = 0;
+                // the CTA in which the sum passes u times all of it: it alone goes on. Lane r has CTA r's
+                int tied;
+                u64 have = R.kept_of(cl, by, &tied);
+                cl.sync();  // nothing of another CTA is read from here on
+                const int upto_tied = warp_scan(tied);
+                const long long rest = by.ties - (upto_tied - tied);
+                int allowed = rest <= 0 ? 0 : rest < tied ? (int)rest : tied;
+                have += (u64)allowed * by.w;
+                const u64 in = warp_scan(have), sum = __shfl_sync(0xffffffffu, in, 31);
+                u64 target = mul_floor(u, sum);
                 target = target < sum ? target : sum - 1;
-                int who = -1, allowed = 0;
-#pragma unroll
-                for (int r = 0; r < kMaxCtas; ++r) {
-                    if (who < 0 && base + kept[r] > target) {
-                        who = r;
-                        allowed = take[r];
-                        have = kept[r];
-                    }
-                    if (who < 0) base += kept[r];
-                }
+                const int who = __ffs(__ballot_sync(0xffffffffu, in > target)) - 1;
+                target -= __shfl_sync(0xffffffffu, in - have, who);
+                allowed = __shfl_sync(0xffffffffu, allowed, who);
+                have = __shfl_sync(0xffffffffu, have, who);
                 if (who != rank) return;
-                target -= base;
                 if (tid == 0) s_n = 0;
                 // its warps' parts and the token, by quick weights and, where their error leaves it open, by exact ones
                 for (int exact = 0; exact < 2; ++exact) {
