@@ -485,17 +485,30 @@ struct Row {
         }
         const int any = __syncthreads_or(odd);
         if (tid < C) cl.map_shared_rank(all, tid)->odd[rank] = any;
-        u64 w = 0;
-        int n = 0;
+        // of each stretch, kStretch / 2 pairs of places, as many lanes have one pair each
 #pragma unroll 1
-        for (int q = tid * (kStretch / 2); q < (tid + 1) * (kStretch / 2); ++q) {
+        for (int q = tid; q < kValues / 2; q += kThreads) {
             const uint32_t y = count[q];
-            if (!y) continue;
-            u64 w0, w1;
-            exact_weights(value_at(2 * q), value_at(2 * q + 1), m, c, table, w0, w1);
-            n += (int)((y & 0xffffu) + (y >> 16));
-            w += (y & 0xffffu) * w0 + (y >> 16) * w1;
+            u64 w0 = 0, w1 = 0, w = 0;
+            int n = 0;
+            if (__any_sync(0xffffffffu, y)) {
+                exact_weights(value_at(2 * q), value_at(2 * q + 1), m, c, table, w0, w1);
+                n = (int)((y & 0xffffu) + (y >> 16));
+                w = (y & 0xffffu) * w0 + (y >> 16) * w1;
+#pragma unroll
+                for (int o = 1; o < kStretch / 2; o *= 2) {
+                    n += __shfl_xor_sync(0xffffffffu, n, o);
+                    w += __shfl_xor_sync(0xffffffffu, w, o);
+                }
+            }
+            if (lane % (kStretch / 2) == 0) {
+                upto->sum_weight[q / (kStretch / 2)] = w;
+                upto->sum_count[q / (kStretch / 2)] = n;
+            }
         }
+        __syncthreads();
+        const u64 w = upto->sum_weight[tid];
+        const int n = upto->sum_count[tid];
         u64 w_in = warp_scan(w);
         int n_in = warp_scan(n);
         if (lane == 31) {
@@ -533,12 +546,6 @@ struct Row {
         __syncthreads();
         return true;
     }
-    // Numbers of a place's value in the cluster's CTAs, by the lanes of a warp together: lane l has CTA l's.
-    __device__ __forceinline__ int count_at(cg::cluster_group& cl, int place) const {
-        const int lane = threadIdx.x & 31;
-        const uint32_t y = lane < C ? cl.map_shared_rank(&work->values, lane)->n[place >> 1] : 0;
-        return (int)(place & 1 ? y >> 16 : y & 0xffffu);
-    }
     // The place at which the count (MODE COUNT) or the weight passes the target, by every warp for itself.
     template <int MODE>
     __device__ __forceinline__ Cut cut_values(cg::cluster_group& cl, u64 target) {
@@ -575,13 +582,21 @@ struct Row {
     }
     // What a cut keeps of CTA `lane`'s tokens: what those before it weigh, and the number of those at it.
     __device__ __forceinline__ u64 kept_of(cg::cluster_group& cl, const Cut& cut, int* tied) const {
-        const int lane = threadIdx.x & 31, t = imin(cut.at, kValues) / kStretch;
-        u64 s = lane < C ? cl.map_shared_rank(upto, lane)->weight[t] : 0;
-        for (int p = t * kStretch; p < imin(cut.at, kValues); ++p) {
-            const int n = count_at(cl, p);
-            if (__any_sync(0xffffffffu, n)) s += (u64)n * exact(value_at(p));
+        const int lane = threadIdx.x & 31, t = imin(cut.at, kValues) / kStretch, place = t * kStretch + lane;
+        u64 s = lane < C ? cl.map_shared_rank(upto, lane)->weight[t] : 0, w = 0;
+        if (lane < kStretch && place < imin(cut.at, kValues)) w = exact(value_at(place));
+#pragma unroll
+        for (int r = 0; r < kMaxCtas; ++r)
+            if (r < C) {
+                const uint32_t y = w ? cl.map_shared_rank(&work->values, r)->n[place >> 1] : 0;
+                const u64 more = warp_sum((u64)(place & 1 ? y >> 16 : y & 0xffffu) * w);
+                if (lane == r) s += more;
+            }
+        *tied = 0;
+        if (cut.at < kValues && value_at(cut.at) == cut.x && lane < C) {
+            const uint32_t y = cl.map_shared_rank(&work->values, lane)->n[cut.at >> 1];
+            *tied = (int)(cut.at & 1 ? y >> 16 : y & 0xffffu);
         }
-        *tied = cut.at < kValues && value_at(cut.at) == cut.x ? count_at(cl, cut.at) : 0;
         return s;
     }
     __device__ __forceinline__ u64 total(const u64* of) const {
