@@ -63,8 +63,6 @@ __global__ void __launch_bounds__(kMergeThreads) cache_merge_kernel(const CacheA
     const int lo = rows * slice / slices, hi = rows * (slice + 1) / slices;
     const int R = slot_rows(a.total_rows, a.G);
     const bool plane = RUNS && r.part != PART_WHOLE;
-    float* o_f32 = plane ? plane_o(a, D, r.part) : a.o_f32;
-    float* lse = plane ? plane_lse(a, D, r.part) : a.lse;
     auto slot = [&](int p) { return slot_at(a.scratch, p == 0 ? 2 * (c0 - 1) + 1 : 2 * (c0 - 1 + p), R, D); };
     for (int i0 = lo; i0 < hi; i0 += 32) {
         const int n = imin(32, hi - i0);
@@ -88,7 +86,7 @@ __global__ void __launch_bounds__(kMergeThreads) cache_merge_kernel(const CacheA
             const float inv = nan ? NAN : z > 0.f ? 1.f / z : 0.f;
             // -1: the row sees no key of the partial, which is not read; a weight of 0 is (it may hold NaN)
             for (int p = 0; p < parts; ++p) s_w[p][lane] = s_w[p][lane] < 0.f ? -1.f : s_w[p][lane] * inv;
-            s_lse[lane] = nan ? NAN : z > 0.f ? (mx + log2f(z)) * 0.69314718055994531f : -INFINITY;
+            s_lse[lane] = nan ? NAN : z > 0.f ? mx + log2f(z) : -INFINITY;  // base 2
         }
         __syncthreads();
         // item: eight columns of one row; consecutive threads take consecutive rows
@@ -117,10 +115,18 @@ __global__ void __launch_bounds__(kMergeThreads) cache_merge_kernel(const CacheA
                     }
             }
             const int m = r.m0 + i0 + k, row = r.row0 + m / a.G, h = r.head * a.G + m % a.G;
+            if (plane) {
+                const long long flat = (long long)a.total_rows * a.G, to = (long long)r.row0 * a.G + m;
+                float4* dst = reinterpret_cast<float4*>(plane_o(a, D, r.part, r.head)) + 2 * q * flat + to;
+                dst[0] = make_float4(o[0], o[1], o[2], o[3]);
+                dst[flat] = make_float4(o[4], o[5], o[6], o[7]);
+                if (q == 0) plane_lse(a, D, r.part, r.head)[to] = s_lse[k];
+                continue;
+            }
             const long long at = ((long long)row * a.H + h) * D + 8 * q;
-            if (o_f32) {
-                *reinterpret_cast<float4*>(o_f32 + at) = make_float4(o[0], o[1], o[2], o[3]);
-                *reinterpret_cast<float4*>(o_f32 + at + 4) = make_float4(o[4], o[5], o[6], o[7]);
+            if (a.o_f32) {
+                *reinterpret_cast<float4*>(a.o_f32 + at) = make_float4(o[0], o[1], o[2], o[3]);
+                *reinterpret_cast<float4*>(a.o_f32 + at + 4) = make_float4(o[4], o[5], o[6], o[7]);
             } else {
                 uint32_t b[4];
 #pragma unroll
@@ -130,37 +136,42 @@ __global__ void __launch_bounds__(kMergeThreads) cache_merge_kernel(const CacheA
                 }
                 *reinterpret_cast<uint4*>(a.o + at) = make_uint4(b[0], b[1], b[2], b[3]);
             }
-            if (q == 0) lse[(long long)h * a.total_rows + row] = s_lse[k];
+            if (q == 0) a.lse[(long long)h * a.total_rows + row] = s_lse[k] * 0.69314718055994531f;
         }
         __syncthreads();
     }
 }
 
 // Joins the two planes for the rows of runs: a thread takes eight columns of a
-// (row, head). blockIdx.x is the sequence, blockIdx.y a run of its (row, head)s.
-// Bound by what it moves, 8 bytes a value read and 2 written, most of it out of L2.
+// flat row of a kv head. A warp reads eight rows' float4 of four pairs of columns,
+// runs of 128 bytes, and writes runs of 64 (bf16). blockIdx.x is the sequence,
+// blockIdx.y a run of its items. Bound by what it moves, 8 bytes a value
+// read and 2 written, most of it out of L2.
 constexpr int kJoinThreads = 256;
 
 template <int D>
 __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const CacheAttnArgs a) {
     asm volatile("griddepcontrol.wait;" ::: "memory");
     if (share_recs(a.scratch)[0].bad) return;
-    const int n = a.c.n_seqs, s = blockIdx.x;
-    if (__ldg(a.runs + 2 * (long long)n + s) == 0) return;
-    const int row0 = __ldg(a.cu_rows + s), rows = __ldg(a.cu_rows + s + 1) - row0;
-    constexpr int PER = D / 8;
-    const int c = threadIdx.x % PER;
-    const long long all = (long long)rows * a.H, step = (long long)gridDim.y * (kJoinThreads / PER);
-    for (long long i = (long long)blockIdx.y * (kJoinThreads / PER) + threadIdx.x / PER; i < all; i += step) {
-        const int h = (int)(i % a.H), row = row0 + (int)(i / a.H);
-        const long long at = ((long long)row * a.H + h) * D + 8 * c, al = (long long)h * a.total_rows + row;
-        const float l0 = __ldcg(plane_lse(a, D, PART_SHARED) + al), l1 = __ldcg(plane_lse(a, D, PART_OWN) + al);
-        const float4* p0 = reinterpret_cast<const float4*>(plane_o(a, D, PART_SHARED) + at);
-        const float4* p1 = reinterpret_cast<const float4*>(plane_o(a, D, PART_OWN) + at);
-        const float4 x0 = __ldcg(p0), x1 = __ldcg(p0 + 1), y0 = __ldcg(p1), y1 = __ldcg(p1 + 1);
+    const int s = blockIdx.x, lane = threadIdx.x & 31;
+    const SeqRows q = seq_rows(a.c, a.cu_rows, a.q_pos, a.total_rows, s);
+    if (q.rows == 0 || run_of(a, s, q).shared == 0) return;
+    constexpr int CG = D / 32;  // groups of four pairs of float4
+    const long long flat = (long long)a.total_rows * a.G;
+    const int groups = (q.rows * a.G + 7) / 8, each = kJoinThreads / 32;
+    const long long items = (long long)a.c.Hk * groups * CG;
+    for (long long it = (long long)blockIdx.y * each + (threadIdx.x >> 5); it < items; it += (long long)gridDim.y * each) {
+        const int cg = (int)(it % CG), c = cg * 4 + (lane >> 3);  // eight columns from 8 c on
+        const int m = (int)(it / CG % groups) * 8 + (lane & 7), head = (int)(it / CG / groups);
+        if (m >= q.rows * a.G) continue;
+        const long long at = (long long)q.row0 * a.G + m;
+        const float l0 = __ldcg(plane_lse(a, D, PART_SHARED, head) + at), l1 = __ldcg(plane_lse(a, D, PART_OWN, head) + at);
+        const float4* p0 = reinterpret_cast<const float4*>(plane_o(a, D, PART_SHARED, head)) + 2 * c * flat + at;
+        const float4* p1 = reinterpret_cast<const float4*>(plane_o(a, D, PART_OWN, head)) + 2 * c * flat + at;
+        const float4 x0 = __ldcg(p0), x1 = __ldcg(p0 + flat), y0 = __ldcg(p1), y1 = __ldcg(p1 + flat);
         const float mx = fmaxf(l0, l1);
         const bool nan = l0 != l0 || l1 != l1;
-        float w0 = l0 == -INFINITY ? 0.f : expf(l0 - mx), w1 = l1 == -INFINITY ? 0.f : expf(l1 - mx);
+        float w0 = l0 == -INFINITY ? 0.f : exp2f(l0 - mx), w1 = l1 == -INFINITY ? 0.f : exp2f(l1 - mx);
         const float z = w0 + w1, inv = nan ? NAN : z > 0.f ? 1.f / z : 0.f;
         w0 *= inv;
         w1 *= inv;
@@ -169,9 +180,11 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const CacheAtt
 #pragma unroll
         for (int e = 0; e < 8; ++e)  // a part that sees no key holds zeros; a weight of 0 does not hide a NaN
             o[e] = fmaf(w0, x[e], w1 * y[e]);
+        const int row = q.row0 + m / a.G, h = head * a.G + m % a.G;
+        const long long to = ((long long)row * a.H + h) * D + 8 * c;
         if (a.o_f32) {
-            *reinterpret_cast<float4*>(a.o_f32 + at) = make_float4(o[0], o[1], o[2], o[3]);
-            *reinterpret_cast<float4*>(a.o_f32 + at + 4) = make_float4(o[4], o[5], o[6], o[7]);
+            *reinterpret_cast<float4*>(a.o_f32 + to) = make_float4(o[0], o[1], o[2], o[3]);
+            *reinterpret_cast<float4*>(a.o_f32 + to + 4) = make_float4(o[4], o[5], o[6], o[7]);
         } else {
             uint32_t b[4];
 #pragma unroll
@@ -179,9 +192,9 @@ __global__ void __launch_bounds__(kJoinThreads) cache_join_kernel(const CacheAtt
                 const __nv_bfloat162 v = __floats2bfloat162_rn(o[2 * e], o[2 * e + 1]);
                 b[e] = *reinterpret_cast<const uint32_t*>(&v);
             }
-            *reinterpret_cast<uint4*>(a.o + at) = make_uint4(b[0], b[1], b[2], b[3]);
+            *reinterpret_cast<uint4*>(a.o + to) = make_uint4(b[0], b[1], b[2], b[3]);
         }
-        if (c == 0) a.lse[al] = nan ? NAN : z > 0.f ? mx + logf(z) : -INFINITY;
+        if (c == 0) a.lse[(long long)h * a.total_rows + row] = nan ? NAN : z > 0.f ? (mx + log2f(z)) * 0.69314718055994531f : -INFINITY;
     }
 }
 
@@ -222,8 +235,9 @@ cudaError_t launch_cache_attn(const CacheAttnArgs& a, int num_sms, cudaStream_t 
     if (e != cudaSuccess) return e;
     *launches += 2;
     if (!a.runs) return cudaSuccess;
-    const int per = kJoinThreads / (a.c.D / 8), n = a.c.n_seqs;
-    const long long most = ((long long)a.total_rows * a.H + per - 1) / per, fill = (4LL * num_sms + n - 1) / n;
+    const int per = kJoinThreads / 32, n = a.c.n_seqs;
+    const long long items = (long long)a.c.Hk * (((long long)a.total_rows * a.G + 7) / 8) * (a.c.D / 32);
+    const long long most = (items + per - 1) / per, fill = (4LL * num_sms + n - 1) / n;
     cfg.gridDim = dim3((unsigned)n, (unsigned)(most < fill ? most : fill));
     cfg.blockDim = dim3(kJoinThreads);
     e = a.c.D == 128 ? cudaLaunchKernelEx(&cfg, cache_join_kernel<128>, a) : cudaLaunchKernelEx(&cfg, cache_join_kernel<64>, a);

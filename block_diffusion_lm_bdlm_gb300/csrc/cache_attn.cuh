@@ -17,9 +17,9 @@
 // 2 s is the pages that a run led by sequence s shares, read by the rows of
 // all of the run's sequences (they lie side by side) as if they were one
 // sequence's; item 2 s + 1 is what sequence s reads alone. Rows of a run get
-// two partial results, one of each kind, in two planes (o fp32 [T, H, d] twice,
-// then lse fp32 [H, T] twice), which are joined at the end. They lie in rows'
-// order, so that units of either kind may be cut anywhere.
+// two partial results, one of each kind, in two planes, which are joined at the
+// end. A plane holds all of the call's flat rows, of each kv head, as a slot
+// holds a unit's, so units of either kind may be cut anywhere.
 #pragma once
 
 #include "cache.cuh"
@@ -79,6 +79,15 @@ struct Rows : SeqRows {
 };
 enum : int { PART_WHOLE = 0, PART_SHARED = 1, PART_OWN = 2 };
 
+// Whether n sequences with `rows` rows in all gain from reading `shared` positions together. Alone, each takes an MMA tile
+// of 128 flat rows through them, however few it has; together they take what their rows fill. Against that stand
+// two more units and a join for each sequence, about kJoinCost tiles' time.
+constexpr int kJoinCost = 12;
+__device__ __forceinline__ bool worth(const CacheAttnArgs& a, int n, int rows, int shared) {
+    const float each = (float)rows * a.G / n;
+    return shared * (1.f / kTileKeys) * (1.f - fminf(each, 128.f) * (1.f / 128.f)) > (float)kJoinCost;
+}
+
 // What the run of sequence s is, and whether it is well-formed: all of its
 // sequences name the same one, and share no more than each of their rows sees.
 struct Run {
@@ -93,6 +102,7 @@ __device__ __forceinline__ Run run_of(const CacheAttnArgs& a, int s, const SeqRo
     if (u.ok && u.first < s) u.ok = __ldg(f + s - 1) == u.first && __ldg(e + s - 1) == u.end && __ldg(h + s - 1) == u.shared;
     if (u.ok && u.end > s + 1) u.ok = __ldg(f + s + 1) == u.first && __ldg(e + s + 1) == u.end && __ldg(h + s + 1) == u.shared;
     if (u.shared > 0 && (s == u.first || r.rows > 0)) u.ok = u.ok && u.shared <= r.len && (r.rows == 0 || u.shared <= r.pos0);
+    if (u.ok && u.shared > 0 && !worth(a, u.end - u.first, __ldg(a.cu_rows + u.end) - __ldg(a.cu_rows + u.first), u.shared)) u.shared = 0;
     return u;
 }
 
@@ -134,11 +144,14 @@ __device__ __forceinline__ int keys_of(const CacheAttnArgs& a, const T& r, int p
     return key_end(r.len, a.block, p) - (RUNS ? r.key0 : 0);
 }
 
-__device__ __forceinline__ float* plane_o(const CacheAttnArgs& a, int D, int part) {
-    return a.planes + (long long)(part - 1) * a.total_rows * a.H * D;
+// A plane: for each kv head normalised fp32 rows as [D / 4][T G] float4; behind both planes the rows' base-2 lse [Hk][T G] twice.
+__device__ __forceinline__ float* plane_o(const CacheAttnArgs& a, int D, int part, int head) {
+    const long long flat = (long long)a.total_rows * a.G;
+    return a.planes + ((part - 1) * (long long)a.c.Hk + head) * D * flat;
 }
-__device__ __forceinline__ float* plane_lse(const CacheAttnArgs& a, int D, int part) {
-    return a.planes + ((long long)2 * D + (part - 1)) * a.total_rows * a.H;
+__device__ __forceinline__ float* plane_lse(const CacheAttnArgs& a, int D, int part, int head) {
+    const long long flat = (long long)a.total_rows * a.G;
+    return a.planes + (2LL * a.c.Hk * D + (part - 1) * (long long)a.c.Hk + head) * flat;
 }
 
 struct Unit {

@@ -989,19 +989,22 @@ __device__ __forceinline__ void softmax_part(uint32_t (&r)[2][32], uint32_t tC, 
 
 // Where the results of a unit's flat rows go.
 struct Out {
-    float* slot;  // partial: the share's slot (nullptr: the unit is complete)
-    int slot_r;   // its rows
-    float* o_f32;  // else: fp32 rows (nullptr: bf16 to a.o)
-    float* lse;
+    float* slot;       // partial or (with runs) in a plane: the unit's first row in [D / 4][slot_r] float4; nullptr: complete rows
+    float* slot_lse;
+    long long slot_r;
 };
 template <int D, bool RUNS>
 __device__ __forceinline__ Out out_of(const CacheAttnArgs& a, const Seg& g) {
     Out out;
     out.slot_r = slot_rows(a.total_rows, a.G);
-    out.slot = g.whole ? nullptr : slot_at(a.scratch, 2 * (int)blockIdx.x + (g.kt0 > 0 ? 0 : 1), out.slot_r, D);
-    const bool plane = RUNS && g.part != PART_WHOLE;
-    out.o_f32 = plane ? plane_o(a, D, g.part) : a.o_f32;
-    out.lse = plane ? plane_lse(a, D, g.part) : a.lse;
+    out.slot = g.whole ? nullptr : slot_at(a.scratch, 2 * (int)blockIdx.x + (g.kt0 > 0 ? 0 : 1), (int)out.slot_r, D);
+    out.slot_lse = out.slot + out.slot_r * D;
+    if (RUNS && g.whole && g.part != PART_WHOLE) {
+        const long long at = (long long)g.row0 * a.G + g.m0;
+        out.slot_r = (long long)a.total_rows * a.G;
+        out.slot = plane_o(a, D, g.part, g.h) + 4 * at;
+        out.slot_lse = plane_lse(a, D, g.part, g.h) + at;
+    }
     return out;
 }
 
@@ -1012,13 +1015,13 @@ __device__ __forceinline__ void put_cols(const CacheAttnArgs& a, const Seg& g, c
                                          int q, const float (&v)[32]) {
     if (out.slot) {
         if (m < g.last) {
-            float4* dst = reinterpret_cast<float4*>(out.slot) + (8 * q) * out.slot_r + (m - g.m0);
+            float4* dst = reinterpret_cast<float4*>(out.slot) + 8 * q * out.slot_r + (m - g.m0);
 #pragma unroll
             for (int e = 0; e < 8; ++e) dst[e * out.slot_r] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
         }
-    } else if (out.o_f32) {
+    } else if (a.o_f32) {
         if (m < g.last) {
-            float4* dst = reinterpret_cast<float4*>(out.o_f32 + ((long long)(g.row0 + m / a.G) * a.H + g.h * a.G + m % a.G) * D + 32 * q);
+            float4* dst = reinterpret_cast<float4*>(a.o_f32 + ((long long)(g.row0 + m / a.G) * a.H + g.h * a.G + m % a.G) * D + 32 * q);
 #pragma unroll
             for (int e = 0; e < 8; ++e) dst[e] = make_float4(v[4 * e], v[4 * e + 1], v[4 * e + 2], v[4 * e + 3]);
         }
@@ -1053,13 +1056,13 @@ __device__ __forceinline__ void put_rows(const CacheAttnArgs& a, const Seg& g, i
     }
 }
 
-__device__ __forceinline__ void put_lse(const CacheAttnArgs& a, const Seg& g, const Out& out, int D, int m, float l2) {
+__device__ __forceinline__ void put_lse(const CacheAttnArgs& a, const Seg& g, const Out& out, int m, float l2) {
     if (m >= g.last) return;
     if (out.slot) {
-        out.slot[(long long)out.slot_r * D + m - g.m0] = l2;
+        out.slot_lse[m - g.m0] = l2;
     } else {
         const int row = m / a.G;
-        out.lse[(long long)(g.h * a.G + m - row * a.G) * a.total_rows + g.row0 + row] = l2 * 0.69314718055994531f;
+        a.lse[(long long)(g.h * a.G + m - row * a.G) * a.total_rows + g.row0 + row] = l2 * 0.69314718055994531f;
     }
 }
 
@@ -1092,14 +1095,17 @@ __device__ __forceinline__ void softmax(const Ctx<D>& x, const CacheAttnArgs& a,
                     const Out out = out_of<D, RUNS>(a, g);
                     const long long at = ((long long)(g.row0 + m / a.G) * a.H + g.h * a.G + m % a.G) * D;
                     for (int c = 0; c < D; c += 8) {
-                        if (out.o_f32) {
-                            *reinterpret_cast<float4*>(out.o_f32 + at + c) = make_float4(0.f, 0.f, 0.f, 0.f);
-                            *reinterpret_cast<float4*>(out.o_f32 + at + c + 4) = make_float4(0.f, 0.f, 0.f, 0.f);
+                        if (RUNS && out.slot) {
+                            float4* dst = reinterpret_cast<float4*>(out.slot) + c / 4 * out.slot_r + (m - g.m0);
+                            dst[0] = dst[out.slot_r] = make_float4(0.f, 0.f, 0.f, 0.f);
+                        } else if (a.o_f32) {
+                            *reinterpret_cast<float4*>(a.o_f32 + at + c) = make_float4(0.f, 0.f, 0.f, 0.f);
+                            *reinterpret_cast<float4*>(a.o_f32 + at + c + 4) = make_float4(0.f, 0.f, 0.f, 0.f);
                         } else {
                             *reinterpret_cast<uint4*>(a.o + at + c) = make_uint4(0, 0, 0, 0);
                         }
                     }
-                    put_lse(a, g, out, D, m, -INFINITY);
+                    put_lse(a, g, out, m, -INFINITY);
                 }
                 continue;
             }
@@ -1204,7 +1210,7 @@ __device__ __forceinline__ void softmax(const Ctx<D>& x, const CacheAttnArgs& a,
         int* nan_first = reinterpret_cast<int*>(g_smem + L::kNan) + (seg & 3) * D;
         int* nan_any = reinterpret_cast<int*>(g_smem + L::kNanAny) + (seg & 3);
         ++seg;
-        const bool staged = !out.slot && !out.o_f32;
+        const bool staged = !out.slot && !a.o_f32;
         const bool nans = *nan_any < g.end;
         float mj = sums.m, lj = sums.l, f0, f1 = 0.f;
         bool use0 = sums.l != 0.f, use1 = false;  // NaN counts as something
@@ -1253,7 +1259,7 @@ __device__ __forceinline__ void softmax(const Ctx<D>& x, const CacheAttnArgs& a,
                 put_cols<D>(a, g, out, m, row, tile, q, v);
             }
         }
-        if (two || i == 0) put_lse(a, g, out, D, m, lj != 0.f ? mj + __log2f(lj) : -INFINITY);
+        if (two || i == 0) put_lse(a, g, out, m, lj != 0.f ? mj + __log2f(lj) : -INFINITY);
         tc::tc_fence_before();
         if (staged) {
             if (two) {
