@@ -57,6 +57,10 @@ __host__ __device__ __forceinline__ int slot_rows(long long total_rows, int G) {
     const long long flat = total_rows * G;
     return flat >= kUnitRows ? kUnitRows : (int)((flat + 7) / 8 * 8);
 }
+// With runs a unit is one MMA tile: what is read together is seldom long enough for units of two to pay for their longer
+// beginnings and ends (64 single rows over 32768 shared keys: 93 us whole with two, 66 with one).
+template <bool RUNS>
+__host__ __device__ constexpr int unit_rows() { return RUNS ? kUnitRows / 2 : kUnitRows; }
 
 // A slot: normalised fp32 rows as [D / 4][rows] float4 (a warp's rows are
 // consecutive), then the rows' base-2 lse.
@@ -94,22 +98,35 @@ struct Run {
     int first, end, shared;
     bool ok;
 };
+template <bool CHECK>
 __device__ __forceinline__ Run run_of(const CacheAttnArgs& a, int s, const SeqRows& r) {
     const int n = a.c.n_seqs;
     const int *f = a.runs, *e = a.runs + n, *h = a.runs + 2 * (long long)n;
     Run u{__ldg(f + s), __ldg(e + s), __ldg(h + s), true};
+    if (!CHECK) {  // another kernel, or this one's beginning, has looked it over
+        if (u.shared > 0 && !worth(a, u.end - u.first, __ldg(a.cu_rows + u.end) - __ldg(a.cu_rows + u.first), u.shared)) u.shared = 0;
+        return u;
+    }
+    // the neighbours' too at once: loads that wait for one another are what this costs
+    const int i = imax(s - 1, 0), j = imin(s + 1, n - 1);
+    const bool before = __ldg(f + i) == u.first && __ldg(e + i) == u.end && __ldg(h + i) == u.shared;
+    const bool behind = __ldg(f + j) == u.first && __ldg(e + j) == u.end && __ldg(h + j) == u.shared;
     u.ok = u.first >= 0 && u.first <= s && u.end > s && u.end <= n && u.shared >= 0 && (u.shared & (a.c.page - 1)) == 0;
-    if (u.ok && u.first < s) u.ok = __ldg(f + s - 1) == u.first && __ldg(e + s - 1) == u.end && __ldg(h + s - 1) == u.shared;
-    if (u.ok && u.end > s + 1) u.ok = __ldg(f + s + 1) == u.first && __ldg(e + s + 1) == u.end && __ldg(h + s + 1) == u.shared;
+    u.ok = u.ok && (u.first == s || before) && (u.end == s + 1 || behind);
     if (u.shared > 0 && (s == u.first || r.rows > 0)) u.ok = u.ok && u.shared <= r.len && (r.rows == 0 || u.shared <= r.pos0);
     if (u.ok && u.shared > 0 && !worth(a, u.end - u.first, __ldg(a.cu_rows + u.end) - __ldg(a.cu_rows + u.first), u.shared)) u.shared = 0;
     return u;
 }
 
+// Sequences with few flat rows and few keys of their own (`own`: those behind what they share) do not pay for an MMA tile:
+// cache_own_kernel reads those keys.
+constexpr int kFewRows = 8, kFewKeys = 2048;
+__device__ __forceinline__ bool is_few(const CacheAttnArgs& a, int rows, int own) { return rows * (long long)a.G <= kFewRows && own <= kFewKeys; }
+
 template <bool RUNS>
 __device__ __forceinline__ int items_of(const CacheAttnArgs& a) { return RUNS ? 2 * a.c.n_seqs : a.c.n_seqs; }
 
-template <bool RUNS>
+template <bool RUNS, bool CHECK = false>
 __device__ __forceinline__ Rows item_rows(const CacheAttnArgs& a, int item) {
     Rows r;
     r.seq = RUNS ? item >> 1 : item;
@@ -117,13 +134,14 @@ __device__ __forceinline__ Rows item_rows(const CacheAttnArgs& a, int item) {
     r.key0 = 0;
     r.part = PART_WHOLE;
     if (RUNS) {
-        const Run u = run_of(a, r.seq, r);
+        const Run u = run_of<CHECK>(a, r.seq, r);
         r.ok = r.ok && u.ok;
         if (item & 1) {
             if (u.shared > 0) {
                 r.key0 = u.shared;
                 r.part = PART_OWN;
             }
+            if (r.ok && is_few(a, r.rows, r.len - r.key0)) r.rows = 0;
         } else if (!r.ok || u.shared == 0 || u.first != r.seq) {
             r.rows = 0;
         } else {
@@ -167,10 +185,10 @@ __device__ __forceinline__ int lead_of(int rows) { return kLead + ((rows + 31) >
 template <bool RUNS>
 __device__ __forceinline__ Unit unit_of(const CacheAttnArgs& a, const Rows& r, int m0) {
     Unit u;
-    u.last = imin(r.rows * a.G, m0 + kUnitRows);
+    u.last = imin(r.rows * a.G, m0 + unit_rows<RUNS>());
     u.end = keys_of<RUNS>(a, r, r.pos0 + (u.last - 1) / a.G);
     u.tiles = imax(1, (u.end + kTileKeys - 1) / kTileKeys);
-    u.two = is_two(u.last - m0);
+    u.two = RUNS ? 0 : is_two(u.last - m0);
     u.lead = lead_of(u.last - m0);
     return u;
 }

@@ -171,7 +171,7 @@ __device__ __forceinline__ bool next_run(const CacheAttnArgs& a, Place* p) {
         }
         left -= n;
         if (left > 0) {  // the unit is done
-            m0 += kUnitRows;
+            m0 += unit_rows<RUNS>();
             if (m0 >= r.rows * a.G) {
                 m0 = 0;
                 if (++h == a.c.Hk) {
@@ -347,10 +347,11 @@ __device__ __forceinline__ long long cta_scan(long long x, long long* total, lon
 template <bool RUNS>
 __device__ __forceinline__ long long head_cost(const CacheAttnArgs& a, const Rows& r, bool have) {
     constexpr int kFew = 2;
-    const int units = have ? (r.rows * a.G + kUnitRows - 1) / kUnitRows : 0, lane = threadIdx.x & 31;
+    constexpr int U = unit_rows<RUNS>();
+    const int units = have ? (r.rows * a.G + U - 1) / U : 0, lane = threadIdx.x & 31;
     long long c = 0;
     if (units <= kFew)
-        for (int i = 0; i < units; ++i) c += unit_of<RUNS>(a, r, i * kUnitRows).cost();
+        for (int i = 0; i < units; ++i) c += unit_of<RUNS>(a, r, i * U).cost();
     for (unsigned todo = __ballot_sync(0xffffffffu, units > kFew); todo; todo &= todo - 1) {
         const int src = __ffs(todo) - 1, n = __shfl_sync(0xffffffffu, units, src);
         Rows q;
@@ -359,7 +360,7 @@ __device__ __forceinline__ long long head_cost(const CacheAttnArgs& a, const Row
         q.pos0 = __shfl_sync(0xffffffffu, r.pos0, src);
         if (RUNS) q.key0 = __shfl_sync(0xffffffffu, r.key0, src);
         long long x = 0;
-        for (int i = lane; i < n; i += 32) x += unit_of<RUNS>(a, q, i * kUnitRows).cost();
+        for (int i = lane; i < n; i += 32) x += unit_of<RUNS>(a, q, i * U).cost();
 #pragma unroll
         for (int o = 16; o; o >>= 1) x += __shfl_xor_sync(0xffffffffu, x, o);
         if (lane == src) c = x;
@@ -372,7 +373,7 @@ template <bool RUNS>
 __device__ __forceinline__ int find_unit(const CacheAttnArgs& a, const Rows& r, long long* off) {
     const int lane = threadIdx.x & 31;
     for (int i0 = 0;; i0 += 32) {
-        const int m0 = (i0 + lane) * kUnitRows;
+        const int m0 = (i0 + lane) * unit_rows<RUNS>();
         const long long c = m0 < r.rows * a.G ? unit_of<RUNS>(a, r, m0).cost() : 0;
         long long v = c;
 #pragma unroll
@@ -384,7 +385,7 @@ __device__ __forceinline__ int find_unit(const CacheAttnArgs& a, const Rows& r, 
         if (hit) {
             const int k = __ffs(hit) - 1;
             *off -= __shfl_sync(0xffffffffu, v - c, k);
-            return (i0 + k) * kUnitRows;
+            return (i0 + k) * unit_rows<RUNS>();
         }
         const long long all = __shfl_sync(0xffffffffu, v, 31);
         if (all == 0) return 0;  // not reached: the offset lies within the head's cost
@@ -407,7 +408,7 @@ __device__ __forceinline__ void find_start(const CacheAttnArgs& a, Start* st, lo
         const int s = s0 + tid;
         bool have = s < n;
         if (have) {
-            r = item_rows<RUNS>(a, s);
+            r = item_rows<RUNS, true>(a, s);
             if (!r.ok) atomicMin(&st->bad, r.seq);
             have = r.ok;
         }
@@ -716,7 +717,7 @@ __device__ __forceinline__ void issue(const CacheAttnArgs& a, const Start& st) {
     while (__any_sync(0xffffffffu, next_run<RUNS>(a, place))) {
         const int nt = __reduce_max_sync(0xffffffffu, place->g.tiles());
         if (nt == 0) continue;
-        const int two = __reduce_max_sync(0xffffffffu, (int)place->g.two);
+        const int two = RUNS ? 0 : __reduce_max_sync(0xffffffffu, (int)place->g.two);
         if (!wait(B_Q, 0, q)) return;
         q ^= 1;
         tc::tc_fence_after();
@@ -1083,7 +1084,7 @@ __device__ __forceinline__ void softmax(const Ctx<D>& x, const CacheAttnArgs& a,
     };
     while (next_run<RUNS>(a, place)) {
         const int nt = place->g.tiles();
-        const bool two = place->g.two;
+        const bool two = !RUNS && place->g.two;
         float cs;
         int sees, all_see;
         bool warp_live;
