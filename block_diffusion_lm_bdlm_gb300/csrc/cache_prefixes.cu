@@ -21,7 +21,7 @@ namespace {
 
 constexpr int kLongest = 256;
 constexpr int kThreads = 256;
-constexpr int kMost = 1 << 22;  // pages that count, so that savings of a run stay in 32 bits
+constexpr int kMost = 32767;  // pages that count, so that 256 times what a run saves stays in 32 bits
 constexpr int kNoRows = -1, kMalformed = -2;
 
 // Pages of sequence r that lie wholly below its rows.
@@ -119,44 +119,42 @@ __global__ void __launch_bounds__(kThreads) cut_kernel(const CachePrefixArgs a) 
     }
     if (s_bad != 0x7fffffff) return;  // nothing is shared then
     if (warp == 0) {
-        // start i lies in lane i % 32, slot (i / 32) % 8: the least c behind it, and best[i] - best[j - 1]
-        int low[8], rel[8];
+        // Start i lies in lane i % 32, slot (i / 32) % 8. Of each: 256 low - 1 with the least c behind it, 256 (best[i] -
+        // best[j - 1]) + 255, and how far back it is. Their product and sum is 256 times what it saves, and 255 less
+        // the distance, so that the largest is the best cut with the shortest last run. (It is never below 0 for the
+        // last start, and a saving grows by at most one c a step.)
+        int low[8], rel[8], far[8];
 #pragma unroll
         for (int k = 0; k < 8; ++k) {
             low[k] = 0;
-            rel[k] = -(1 << 30);
+            rel[k] = -1;
+            far[k] = 0;
         }
+        int next = m > 1 ? 256 * c[0] - 1 : 0;
         for (int j0 = 0; j0 < m; j0 += 256) {
 #pragma unroll
             for (int k8 = 0; k8 < 8; ++k8)  // the slot of the starts that this stretch of 32 steps adds
                 for (int l = 0; l < 32; ++l) {
                     const int i = j0 + 32 * k8 + l;  // the step's new start; j = i + 1
                     if (i >= m) break;
-                    const int cj = i > 0 ? c[i - 1] : 0;
-#pragma unroll
-                    for (int k = 0; k < 8; ++k) low[k] = min(low[k], cj);
-                    if (lane == l) {
-                        low[k8] = kMost;
-                        rel[k8] = 0;
-                    }
-                    int val[8], top = 0;
+                    const int between = next;  // to the sequence before
+                    next = 256 * c[i] - 1;
+                    int key = 0;
 #pragma unroll
                     for (int k = 0; k < 8; ++k) {
-                        const int dist = ((k8 - k) & 7) * 32 + l - lane;  // i minus the slot's start; in the own slot the
-                        const int d = dist < 0 ? dist + 256 : dist;       // lanes above l still hold starts of 256 steps ago
-                        val[k] = rel[k] + d * low[k];
-                        top = max(top, val[k]);
+                        low[k] = i > 0 ? min(low[k], between) : 0;
+                        ++far[k];
+                        if (k == k8 && lane == l) {
+                            low[k] = 256 * kMost - 1;
+                            rel[k] = 255;
+                            far[k] = 0;
+                        }
+                        key = max(key, rel[k] + far[k] * low[k]);
                     }
-                    top = __reduce_max_sync(0xffffffffu, top);
-                    int near = 256;
+                    key = __reduce_max_sync(0xffffffffu, key);
+                    if (lane == 0) back[i] = (uint8_t)(255 - (key & 255));
 #pragma unroll
-                    for (int k = 0; k < 8; ++k) {
-                        const int dist = ((k8 - k) & 7) * 32 + l - lane;
-                        if (val[k] == top) near = min(near, dist < 0 ? dist + 256 : dist);
-                        rel[k] = max(rel[k] - top, -(1 << 30));
-                    }
-                    near = __reduce_min_sync(0xffffffffu, near);
-                    if (lane == 0) back[i] = (uint8_t)near;
+                    for (int k = 0; k < 8; ++k) rel[k] -= key & ~255;
                 }
         }
         __syncwarp();

@@ -89,7 +89,7 @@ int bdlm_unmask(const int32_t* tokens, const int32_t* sampled, const float* logp
         overlap(left, m, tokens, n) || overlap(left, m, sampled, n) || overlap(left, m, logprob, n) ||
         overlap(left, m, cu_rows, m + 4) || overlap(left, m, n_min, m) || overlap(left, m, threshold, m))
         return BDLM_ERR_INVALID_ARG;
-    if (!good_ptr(workspace, 256) || workspace_bytes < sizeof(WsHeader)) return BDLM_ERR_WORKSPACE;
+    if (workspace && (!aligned(workspace, 256) || workspace_bytes < sizeof(WsHeader))) return BDLM_ERR_WORKSPACE;
     UnmaskArgs a{};
     a.now = tokens;
     a.sampled = sampled;

@@ -35,7 +35,7 @@ __global__ void __launch_bounds__(kThreads) unmask_kernel(const UnmaskArgs a) {
         return y;
     };
     int lo, hi;
-    if (s == 0) {  // the first CTA looks all offsets over
+    if (s == 0 && a.hdr) {  // the first CTA looks all offsets over
         int bad = 0x7fffffff;
         for (int i = tid; i < a.n_seqs; i += kThreads)
             if (!fine(i, lo, hi)) bad = min(bad, i);

@@ -36,18 +36,19 @@ def _on(device, stream):
     return stream.cuda_stream, torch.cuda.stream(stream)
 
 
-def _vector(name, t, dtype, n, device):
-    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.dim() != 1 or not t.is_contiguous() or t.device != device:
-        raise ValueError(f"{name} must be a contiguous {dtype} tensor of one dimension on {device}")
-    if n is not None and t.shape[0] != n:
-        raise ValueError(f"{name} must have {n} entries, got {t.shape[0]}")
+def _vector(name, t, dtype, n, index):
+    if not isinstance(t, torch.Tensor) or t.dtype != dtype or t.dim() != 1 or not t.is_contiguous() \
+            or t.get_device() != index:
+        raise ValueError(f"{name} must be a contiguous {dtype} tensor of one dimension on cuda:{index}")
+    if n is not None and t.numel() != n:
+        raise ValueError(f"{name} must have {n} entries, got {t.numel()}")
     return t.data_ptr()
 
 
-def _either(name, x, dtype, n, device):
+def _either(name, x, dtype, n, index):
     """(pointer, value) of a parameter that is a tensor or one number for all."""
     if isinstance(x, torch.Tensor):
-        return _vector(name, x, dtype, n, device), 0
+        return _vector(name, x, dtype, n, index), 0
     if dtype == torch.int32:
         if not -2 ** 31 <= int(x) < 2 ** 31:
             raise ValueError(f"{name} must fit 32 bits, got {x}")
@@ -68,17 +69,18 @@ def bdlm_sample(logits, u, *, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, to
     lib = load_library()
     if not isinstance(logits, torch.Tensor) or not logits.is_cuda or logits.dtype not in _DTYPES or logits.dim() != 2:
         raise ValueError("logits must be a bf16, fp16 or fp32 CUDA tensor [rows, vocab]")
-    (n, vocab), device = logits.shape, logits.device
+    n, vocab = logits.shape
+    device, index = logits.device, logits.get_device()
     if vocab == 0 or (vocab > 1 and logits.stride(1) != 1) or (n > 1 and logits.stride(0) < vocab):
         raise ValueError("the logits of a row must be contiguous, at least one, and rows must not overlap")
     if not -2 ** 31 <= int(mask_id) < 2 ** 31:
         raise ValueError(f"mask_id must fit 32 bits, got {mask_id}")
-    pu = _vector("u", u, torch.float32, n, device)
-    t, t_all = _either("temperature", temperature, torch.float32, n, device)
-    k, k_all = _either("top_k", top_k, torch.int32, n, device)
-    p, p_all = _either("top_p", top_p, torch.float32, n, device)
-    m, m_all = _either("min_p", min_p, torch.float32, n, device)
-    now = None if tokens is None else _vector("tokens", tokens, torch.int32, n, device)
+    pu = _vector("u", u, torch.float32, n, index)
+    t, t_all = _either("temperature", temperature, torch.float32, n, index)
+    k, k_all = _either("top_k", top_k, torch.int32, n, index)
+    p, p_all = _either("top_p", top_p, torch.float32, n, index)
+    m, m_all = _either("min_p", min_p, torch.float32, n, index)
+    now = None if tokens is None else _vector("tokens", tokens, torch.int32, n, index)
     if tokens is not None and (out is None or logprob is None):
         raise ValueError("with tokens, out and logprob hold what the other rows keep: pass them")
     how = _CSampling(t, k, p, m, t_all, k_all, p_all, m_all)
@@ -88,7 +90,7 @@ def bdlm_sample(logits, u, *, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, to
             out = torch.empty(n, dtype=torch.int32, device=device)
         if logprob is None:
             logprob = torch.empty(n, dtype=torch.float32, device=device)
-        po, pl = _vector("out", out, torch.int32, n, device), _vector("logprob", logprob, torch.float32, n, device)
+        po, pl = _vector("out", out, torch.int32, n, index), _vector("logprob", logprob, torch.float32, n, index)
         if n == 0:
             return out, logprob
         st = lib.bdlm_sample(logits.data_ptr(), _DTYPES[logits.dtype], n, vocab, max(logits.stride(0), vocab), pu,
@@ -110,25 +112,25 @@ def bdlm_unmask(tokens, sampled, logprob, cu_rows, mask_id: int, *, n_min=0, thr
         raise ValueError("tokens must be an int32 CUDA tensor")
     if not -2 ** 31 <= int(mask_id) < 2 ** 31:
         raise ValueError(f"mask_id must fit 32 bits, got {mask_id}")
-    device, total = tokens.device, tokens.shape[0] if tokens.dim() else 0
-    pt = _vector("tokens", tokens, torch.int32, total, device)
-    ps = _vector("sampled", sampled, torch.int32, total, device)
-    pl = _vector("logprob", logprob, torch.float32, total, device)
-    pc = _vector("cu_rows", cu_rows, torch.int32, None, device)
-    n = cu_rows.shape[0] - 1
+    device, index, total = tokens.device, tokens.get_device(), tokens.numel()
+    pt = _vector("tokens", tokens, torch.int32, None, index)
+    ps = _vector("sampled", sampled, torch.int32, total, index)
+    pl = _vector("logprob", logprob, torch.float32, total, index)
+    pc = _vector("cu_rows", cu_rows, torch.int32, None, index)
+    n = cu_rows.numel() - 1
     if n < 1:
         raise ValueError("cu_rows must have at least two entries")
-    k, k_all = _either("n_min", n_min, torch.int32, n, device)
-    x, x_all = _either("threshold", threshold, torch.float32, n, device)
+    k, k_all = _either("n_min", n_min, torch.int32, n, index)
+    x, x_all = _either("threshold", threshold, torch.float32, n, index)
     if workspace is not None:
-        _vector("workspace", workspace, torch.uint8, None, device)
+        _vector("workspace", workspace, torch.uint8, None, index)
     handle, here = _on(device, stream)
     with here:
         if out is None:
             out = torch.empty_like(tokens)
         if left is None:
             left = torch.empty(n, dtype=torch.int32, device=device)
-        po, pn = _vector("out", out, torch.int32, total, device), _vector("left", left, torch.int32, n, device)
+        po, pn = _vector("out", out, torch.int32, total, index), _vector("left", left, torch.int32, n, index)
         if total == 0:  # no rows: nothing is masked, and offsets that count any are malformed
             left.zero_()
             bad = (cu_rows != 0).any().int() * 6
@@ -137,11 +139,11 @@ def bdlm_unmask(tokens, sampled, logprob, cu_rows, mask_id: int, *, n_min=0, thr
             if check:
                 _check(int(bad), "bdlm_unmask (device)")
             return out, left
-        if workspace is None:
+        if workspace is None and check:
             workspace = torch.empty(256, dtype=torch.uint8, device=device)
-        st = lib.bdlm_unmask(pt, ps, pl, total, pc, n, int(mask_id), k, k_all, x, x_all, po, pn, workspace.data_ptr(),
-                             workspace.numel(), handle)
+        ws, size = (None, 0) if workspace is None else (workspace.data_ptr(), workspace.numel())
+        st = lib.bdlm_unmask(pt, ps, pl, total, pc, n, int(mask_id), k, k_all, x, x_all, po, pn, ws, size, handle)
         _check(st, "bdlm_unmask")
         if check:
-            _check(lib.bdlm_read_error(workspace.data_ptr(), handle), "bdlm_unmask (device)")
+            _check(lib.bdlm_read_error(ws, handle), "bdlm_unmask (device)")
     return out, left

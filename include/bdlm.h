@@ -466,7 +466,7 @@ BDLM_API size_t bdlm_cache_prefixes_workspace_bytes(int32_t n_seqs);
  * a run and lie wholly below every row of it, so that all rows see them. Of
  * all cuts of the sequences into runs of at most 256 with rows the one is taken
  * that saves most pages: the sum of (sequences with rows - 1) times shared
- * pages; of cuts as good, from the last run to the first, the shorter run. (At most 2^22
+ * pages; of cuts as good, from the last run to the first, the shorter run. (At most 32767
  * pages of a run count.)
  * One plan serves all layers and steps of a block: it changes with the table,
  * the lengths and the rows.
@@ -613,7 +613,8 @@ BDLM_API size_t bdlm_unmask_workspace_bytes(void);
  * largest logprob, of equal ones the first; a logprob of NaN comes last. out is
  * the drawn token of kept rows and the present one of others. Rows behind
  * cu_rows[n_seqs] are neither read nor written. Malformed offsets
- * (BDLM_ERR_DEVICE_CHECK) leave their sequences' out and left unwritten.
+ * (BDLM_ERR_DEVICE_CHECK) leave their sequences' out and left unwritten. The
+ * workspace holds nothing but the error word: NULL does without it.
  */
 BDLM_API int bdlm_unmask(const int32_t* tokens, const int32_t* sampled, const float* logprob, int64_t total_rows,
                   const int32_t* cu_rows, int32_t n_seqs, int32_t mask_id, const int32_t* n_min, int32_t n_min_all,

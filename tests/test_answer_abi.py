@@ -82,8 +82,8 @@ def test_unmask(bd, kw):
 
 def test_unmask_workspace(bd):
     assert bd.bdlm_unmask_workspace_bytes() == 256
-    assert unmask(bd, ws=None) == WS and unmask(bd, ws=264) == WS and unmask(bd, bytes=255) == WS
-    assert unmask(bd, out=256, ws=None) == WS  # in place passes on to the next check
+    assert unmask(bd, ws=264) == WS and unmask(bd, bytes=255) == WS
+    assert unmask(bd, out=256, bytes=255) == WS  # in place passes on to the next check
 
 
 def test_bindings_refuse_host_tensors(bd):
