@@ -6,13 +6,18 @@ bdlm_cache_* calls that one model's attention layers need.
     for step in range(steps):         # a prompt takes one step, a block several: its rows are written anew in each
         for layer in range(n_layers):
             o, _ = dec.attend(layer, q, k, v)
+        left = dec.choose(tokens, logits, u, mask_id)  # draw tokens, keep the surest; rows still masked
     ...                               # keep the rows: begin the next block; or dec.rewind() and begin again
     dec.branch(parents, children)     # candidates that share what was written so far; behind a block's last step
     dec.end(seqs)                     # their pages are free again
 
+With share=True the candidates' attention reads the pages that they share once
+for all of them: begin finds the runs of neighbouring sequences that do
+(bdlm_cache_prefixes), so children should be numbered side by side.
+
 All state is on the device, the cache's table and lens and the present block's
-offsets: begin, attend, rewind, branch and end only launch work on the current
-stream and can be captured into graphs. begin's first step of a whole prompt
+offsets: begin, attend, choose, rewind, branch and end only launch work on the
+current stream and can be captured into graphs. begin's first step of a whole prompt
 and a denoising step of one block are the same call: under the block-causal
 mask a prompt's rows see the blocks up to their own, and the rows of a block
 that starts at a block boundary see everything before it and each other.
@@ -28,14 +33,15 @@ from __future__ import annotations
 
 import torch
 
-from . import PageCache, bdlm_cache_attn_fwd, bdlm_cache_fork, bdlm_cache_reserve, bdlm_cache_write
+from . import (PageCache, bdlm_cache_attn_fwd, bdlm_cache_attn_shared_fwd, bdlm_cache_fork, bdlm_cache_prefixes,
+               bdlm_cache_reserve, bdlm_cache_write, bdlm_sample, bdlm_unmask)
 
 
 _NONE = -2 ** 31
 
 
 class BlockDecoder:
-    def __init__(self, cache: PageCache, block: int, softmax_scale: float = 0.0):
+    def __init__(self, cache: PageCache, block: int, softmax_scale: float = 0.0, share: bool = False):
         if block < 1:
             raise ValueError("block must be positive")
         self.cache, self.block, self.softmax_scale = cache, int(block), float(softmax_scale)
@@ -43,6 +49,8 @@ class BlockDecoder:
         self._cu = torch.zeros_like(self.cu_rows)  # those of cu_rows that attend goes by: all 0 once the block is over
         self._kept = cache.lens.clone()            # lengths before the last begin
         self._rows = torch.zeros_like(cache.lens)  # rows that it gave and rewind may still take; _NONE: none
+        self._runs = torch.empty((3, cache.n_seqs), dtype=torch.int32, device=cache.device) if share else None
+        self._plan()
 
     def begin(self, rows: torch.Tensor, *, check: bool = False) -> torch.Tensor:
         """Make room for `rows` new rows of every sequence behind what it
@@ -60,7 +68,13 @@ class BlockDecoder:
             torch.sub(self.cache.lens, self._kept, out=self._rows)
             torch.cumsum(self._rows, 0, dtype=torch.int32, out=self._cu[1:])
             self.cu_rows.copy_(self._cu)
+            self._plan()
         return self.cu_rows
+
+    def _plan(self) -> None:
+        """Which sequences' rows read which pages together, from here on."""
+        if self._runs is not None:
+            bdlm_cache_prefixes(self.cache, self._cu, q_pos=self._kept, out=self._runs)
 
     def attend(self, layer: int, q, k, v, *, out=None, lse=None, check: bool = False):
         """Write the rows' keys and values and attend; (o, lse). The rows of a
@@ -73,8 +87,23 @@ class BlockDecoder:
             raise RuntimeError("no sequence has rows: begin a block before attend")
         bdlm_cache_write(self.cache, k, v, self._cu, layer=layer)
         # The positions come from begin: lengths say nothing about those of a sequence that has ended.
-        return bdlm_cache_attn_fwd(self.cache, q, self._cu, self.block, layer=layer, q_pos=self._kept,
-                                   softmax_scale=self.softmax_scale, out=out, lse=lse, check=check)
+        more = dict(layer=layer, q_pos=self._kept, softmax_scale=self.softmax_scale, out=out, lse=lse, check=check)
+        if self._runs is None:
+            return bdlm_cache_attn_fwd(self.cache, q, self._cu, self.block, **more)
+        return bdlm_cache_attn_shared_fwd(self.cache, q, self._cu, self.block, self._runs, **more)
+
+    def choose(self, tokens, logits, u, mask_id: int, *, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, n_min=1,
+               threshold=float("nan"), check: bool = False) -> torch.Tensor:
+        """Draw a token for every row that has none yet (tokens[i] == mask_id;
+        int32, a row of logits and of u for each) and enter, in tokens, those
+        with a log-probability of at least `threshold` (NaN: none) and at
+        least the n_min surest of every sequence. Returns the rows of each
+        sequence that are still masked (int32 [n_seqs])."""
+        drawn, logprob = torch.empty_like(tokens), torch.empty_like(u)
+        bdlm_sample(logits, u, temperature=temperature, top_k=top_k, top_p=top_p, min_p=min_p, tokens=tokens,
+                    mask_id=mask_id, out=drawn, logprob=logprob)
+        return bdlm_unmask(tokens, drawn, logprob, self._cu, mask_id, n_min=n_min, threshold=threshold, out=tokens,
+                           check=check)[1]
 
     def rewind(self) -> None:
         """Drop the rows of the last begin. Sequences that have ended or
@@ -82,6 +111,7 @@ class BlockDecoder:
         lens = self.cache.lens
         lens.copy_(torch.where(self._untouched(), self._kept, lens))
         self._cu.zero_()
+        self._plan()
 
     def _untouched(self) -> torch.Tensor:
         """The sequences whose lengths are those that begin left."""
@@ -105,6 +135,7 @@ class BlockDecoder:
         shared = took & (lens // page * page > self._kept) & self._named(parents)  # below lens // page * page pages are shared
         over = (shared | took & self._named(children)).any() & (lens != before).any()  # a fork that failed shares nothing
         self._cu.masked_fill_(over, 0)
+        self._plan()
 
     def end(self, seqs: torch.Tensor) -> None:
         """Empty the sequences; pages that no other one names are free. seqs
@@ -112,6 +143,7 @@ class BlockDecoder:
         a number that no sequence has is passed over."""
         self.cache.lens.masked_fill_(self._named(seqs), 0)
         self._settle()
+        self._plan()
 
     def _named(self, seqs: torch.Tensor) -> torch.Tensor:
         """Which sequences the numbers name (bool [n_seqs]). A number out of
