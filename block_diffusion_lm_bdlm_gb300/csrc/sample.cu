@@ -174,7 +174,7 @@ struct Cut {
 };
 // What the cluster's CTAs tell each other: every CTA has all of it. Entry r * kWarps + w is of warp w of CTA r.
 struct All {
-    float top[kParts];   // largest logits of the threads in equal groups, 128 in the cluster
+    alignas(16) float top[kParts];   // largest logits of the threads in equal groups, 128 in the cluster
     u64 quick[kParts];   // quick weights at T; later exact weights above the cut
     u64 whole[kParts];   // quick weights at T = 1; later exact weights below the cut
     int ties[kParts];    // tokens at the cut
@@ -753,6 +753,17 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
             for (int e = 0; e < VE; ++e) dst[e] = e0 + e >= 0 && e0 + e < n ? src[e0 + e] : value_of<T>(-INFINITY);
         }
     }
+    // The part that a CTA behind those that run now will read goes to L2.
+    if (tid == 0) {
+        const long long later = blockIdx.x + a.ahead;
+        if (later < (long long)a.rows * a.ctas) {
+            const int r = (int)(later / a.ctas);
+            const uintptr_t from = reinterpret_cast<uintptr_t>(static_cast<const T*>(a.x) + (long long)r * a.stride + first), at = (from + 15) & ~(uintptr_t)15;
+            const uint32_t bytes = (uint32_t)((from + n * sizeof(T) > at ? from + n * sizeof(T) - at : 0) & ~(uintptr_t)15);
+            if (bytes && (!a.now || __ldg(a.now + r) == a.want))
+                asm volatile("cp.async.bulk.prefetch.L2.global [%0], %1;" ::"l"(at), "r"(bytes) : "memory");
+        }
+    }
     if (tid < kTable) {
         constexpr F2 t[kTable] = {BDLM_POW2_TABLE};
         F2 v = t[0];
@@ -832,16 +843,19 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
             for (int k = 0; k < kPer; ++k) best = max(best, order_key(__float_as_uint(tops[k])));
             key = __reduce_min_sync(0xffffffffu, best);
         } else {
-            const int want = imin(top_k, 120);
-            key = 0;
-#pragma unroll 1
-            for (int bit = 31; bit >= 16; --bit) {
-                const uint32_t next = key | 1u << bit;
-                int have = 0;
-#pragma unroll
-                for (int k = 0; k < kPer; ++k) have += __popc(__ballot_sync(0xffffffffu, order_key(__float_as_uint(tops[k])) >= next));
-                if (have >= want) key = next;
+            // each of 128 threads finds its maximum's place among all of them
+            if (tid < kParts) {
+                const float y = s_all.top[tid];
+                int ahead = 0;
+                for (int i = 0; i < kParts; i += 4) {
+                    const float4 z = *reinterpret_cast<const float4*>(s_all.top + i);
+                    ahead += (z.x > y || (z.x == y && i < tid)) + (z.y > y || (z.y == y && i + 1 < tid)) +
+                             (z.z > y || (z.z == y && i + 2 < tid)) + (z.w > y || (z.w == y && i + 3 < tid));
+                }
+                if (ahead == imin(top_k, 120) - 1) s_found[0] = order_key(__float_as_uint(y));
             }
+            __syncthreads();
+            key = (uint32_t)s_found[0];
         }
         x0 = __uint_as_float(key & 0x80000000u ? key ^ 0x80000000u : ~key);
         x0 = x0 == x0 ? fminf(x0, R.m) : -INFINITY;  // (few groups have anything: the key is below that of -infinity)
@@ -1067,7 +1081,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
                 base = __shfl_sync(0xffffffffu, base, __ffs(hit) - 1);
             }
             if (who >= 0 && who == rank * kWarps + warp) {
-                mine = R.template walk<false>(-INFINITY, 0, 0, base, target, 2 * off, &token, &at);
+                // The error of a sum up to a token less u times all of it: each weight's counts (1 - u)-fold before the token,
+                // u-fold behind it, so 2 u (1 - u) of the bound for all (and the walk's own roundings)
+                const u64 slack = (u64)((float)off * 2.f * u * (1.f - u)) + (off >> 6) + 64;
+                mine = R.template walk<false>(-INFINITY, 0, 0, base, target, slack, &token, &at);
                 if (mine)
                     for (int r = 0; r < a.ctas; ++r) cl.map_shared_rank(&s_all, r)->done[rank] = 1;
             }
@@ -1246,6 +1263,7 @@ cudaError_t launch(SampleArgs a, int num_sms, cudaStream_t st, int* launches) {
     while (c < kMaxCtas && (long long)a.rows * c * 2 <= num_sms && parts(c) > kThreads * VE) c *= 2;
     a.ctas = c;
     a.per = parts(c);
+    a.ahead = 2 * num_sms / c * c;  // two CTAs on an SM
     const size_t smem = ((size_t)a.per / VE + 1) * 16;
     cudaError_t e = cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
     if (e != cudaSuccess) return e;

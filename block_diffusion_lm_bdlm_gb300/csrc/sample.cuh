@@ -154,7 +154,8 @@ struct SampleArgs {
     int* token;
     float* logprob;
     int ctas;  // CTAs of a row, one cluster
-    int per;   // elements of each
+    int per;    // elements of each
+    int ahead;  // CTAs that run at a time, whole clusters
 };
 cudaError_t launch_sample(SampleArgs a, int dtype, int num_sms, cudaStream_t st, int* launches);
 
