@@ -874,6 +874,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
         const float half_m = 0.5f * R.m, c1 = -2.8853900817779268f;
         float s1 = 0.f, st = 0.f;
         float mine = 0.f;  // weight of what this thread has listed
+        int largest = 0;
         for (int v = v0 + lane; v < v1; v += 32) {
             const uint4 raw = s_data[v];
             float x[VE];
@@ -889,9 +890,20 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
                     yt = tc::add2(yt, make_float2(ex2(tt.x), ex2(tt.y)));
                 }
             }
+            const float top = top_of<T>(raw);
+            if (top == R.m) {  // the largest weigh 1 and are counted, so that the sum of the others keeps its own precision
+                y = yt = make_float2(0.f, 0.f);
+#pragma unroll
+                for (int e = 0; e < VE; ++e) {
+                    const float h = fmaf(-0.5f, x[e], half_m);
+                    if (x[e] == R.m) ++largest;
+                    y.x += x[e] == R.m ? 0.f : ex2(h * c1);
+                    if (two) yt.x += x[e] == R.m ? 0.f : ex2(h * R.c2);
+                }
+            }
             s1 += y.x + y.y;
             st += yt.x + yt.y;
-            if (cuts && top_of<T>(raw) >= x0) {
+            if (cuts && top >= x0) {
                 unsigned hits = 0;
 #pragma unroll
                 for (int e = 0; e < VE; ++e) hits |= x[e] >= x0 ? 1u << e : 0u;
@@ -905,7 +917,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
             }
         }
         const bool nan = s1 != s1;
-        const u64 w1 = warp_sum(nan ? 0ull : (u64)__float2ull_rn(s1 * 0x1p44f)), wt = two ? warp_sum((u64)__float2ull_rn(st * 0x1p44f)) : w1;
+        const u64 ones = (u64)largest << kFrac;
+        const u64 w1 = warp_sum(ones + (nan ? 0ull : (u64)__float2ull_rn(s1 * 0x1p44f)));
+        const u64 wt = two ? warp_sum(ones + (u64)__float2ull_rn(st * 0x1p44f)) : w1;
         if (!cuts) R.tell(cl, s_all.quick, wt);
         const float wl = cuts ? warp_sum(mine) : 0.f;
         if (lane == 0) {

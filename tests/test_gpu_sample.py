@@ -160,6 +160,20 @@ def test_captured_and_on_another_stream(bd):
     assert torch.equal(out, want[0]) and torch.equal(lp, want[1])
 
 
+def test_logprobs_near_0(bd):
+    """A token that has nearly all of the weight: its log-probability is -log(1 + rest), and the rest, summed apart from
+    it, is good to kQuick = 4e-6 of itself (sample.cuh); the logarithm and its rounding add 2^-22."""
+    rng = np.random.default_rng(3)
+    for dtype in DTYPES.values():
+        x = torch.from_numpy(rng.standard_normal((40, 3000))).to(dtype).cuda()
+        x[:, 77] = torch.linspace(9, 17, 40).to(dtype).cuda()
+        for how in (dict(temperature=0.0), dict(top_k=1), dict(top_p=0.1), dict(min_p=0.9), dict()):
+            token, lp = bd.bdlm_sample(x, torch.full((40,), 0.5, device="cuda"), **how)
+            for i in range(40):
+                want, wlp = ao.sample_row(x[i].double().cpu().numpy(), 0.5, **how)
+                assert token[i].item() == want == 77 and abs(lp[i].item() - wlp) <= (4e-6 + 2.0 ** -22) * abs(wlp), (how, i)
+
+
 def test_no_rows(bd):
     token, lp = bd.bdlm_sample(torch.zeros((0, 5), device="cuda"), torch.zeros(0, device="cuda"))
     assert token.shape == lp.shape == (0,)
