@@ -852,7 +852,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
                     ahead += (z.x > y || (z.x == y && i < tid)) + (z.y > y || (z.y == y && i + 1 < tid)) +
                              (z.z > y || (z.z == y && i + 2 < tid)) + (z.w > y || (z.w == y && i + 3 < tid));
                 }
-                if (ahead == imin(top_k, 120) - 1) s_found[0] = order_key(__float_as_uint(y));
+                if (ahead == imin(top_k, kParts - 8) - 1) s_found[0] = order_key(__float_as_uint(y));
             }
             __syncthreads();
             key = (uint32_t)s_found[0];
@@ -1269,7 +1269,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
 template <typename T>
 cudaError_t launch(SampleArgs a, int num_sms, cudaStream_t st, int* launches) {
     constexpr int VE = Type<T>::VE;
-    // A CTA's part of a row: at most 64 KB, so that three CTAs share an SM; parts of a lone row may be smaller, so that
+    // A CTA's part of a row: at most 64 KB, so that two CTAs share an SM; parts of a lone row may be smaller, so that
     // more SMs take part, but a warp should have a vector for each lane.
     auto parts = [&](int c) { return ((a.vocab + c - 1) / c + 63) / 64 * 64; };
     int c = 1;

@@ -60,7 +60,7 @@ __host__ __device__ __forceinline__ uint64_t exact_weight(float x, float m, F2 c
     const float bb = BDLM_ADD(h, -a);
     const float hl = BDLM_ADD(BDLM_ADD(a, -BDLM_ADD(h, -bb)), BDLM_ADD(b, -bb));
     const float th = BDLM_MUL(h, c.hi);
-    if (!(th < 46.f)) return 0;  // below half of 2^-44 (and x = -inf)
+    if (!(th < 46.f && th > -1.f)) return 0;  // below half of 2^-44 (and x = -inf); logits above m have no weight
     const float tl = BDLM_ADD(BDLM_FMA(h, c.hi, -th), BDLM_FMA(h, c.lo, BDLM_MUL(hl, c.hi)));
     const int n = BDLM_RINT(th);
     const float f = BDLM_ADD((float)n, -th);  // exact; the weight is 2^-n 2^(f - tl)
@@ -112,7 +112,7 @@ __device__ __forceinline__ void exact_weights(float x0, float x1, float m, F2 c,
     p = fma2(yh, p, two(1.f / 6.f));
     const float2 sh = fma2(two(0.5f), qh, yh), se = fma2(two(0.5f), qh, less(yh, sh));
     const float2 low = add2(fma2(mul2(qh, yh), p, se), fma2(two(0.5f), ql, yl));
-    const bool some0 = th.x < 46.f, some1 = th.y < 46.f;
+    const bool some0 = th.x < 46.f && th.x > -1.f, some1 = th.y < 46.f && th.y > -1.f;
     const F2 t0 = table[some0 ? __float_as_int(jw.x) - 0x4b400000 + 8 : 0], t1 = table[some1 ? __float_as_int(jw.y) - 0x4b400000 + 8 : 0];
     const float2 ht = make_float2(t0.hi, t1.hi), lt = make_float2(t0.lo, t1.lo);
     const float2 ph = mul2(ht, sh), pl = fma2(ht, sh, mul2(ph, two(-1.f)));

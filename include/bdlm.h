@@ -586,7 +586,8 @@ typedef struct {
  * all others nothing. logprob is the token's under softmax(logits), without
  * temperature and cuts. A row without any logit above -inf gets token -1,
  * logprob -inf.
- * The choice is made from weights that are exact to 2^-40, summed as whole
+ * The choice is made from weights that are exact to 2^-40 and multiples of
+ * 2^-44 (what is below 2^-45 of the largest weighs nothing), summed as whole
  * numbers: it does not depend on the order of any sum. No workspace is used.
  */
 BDLM_API int bdlm_sample(const void* logits, int32_t dtype, int64_t rows, int32_t vocab, int64_t row_stride,

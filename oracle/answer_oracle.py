@@ -37,7 +37,8 @@ def sample_row(x, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0):
     if min_p > 0:
         keep = gap >= math.log(min(float(min_p), 1.0))
         ranked, w = ranked[keep], w[keep]
-    ranked, w = ranked[w > 0], w[w > 0]
+    # weights are multiples of 2^-44: only where u is 1 does it show that the smallest ones are nothing
+    ranked, w = ranked[w >= 2.0 ** -45], w[w >= 2.0 ** -45]
     order = np.argsort(ranked)
     ranked, sums = ranked[order], np.cumsum(w[order])
     hit = np.flatnonzero(sums > min(max(float(u), 0.0), 1.0) * sums[-1])

@@ -123,6 +123,18 @@ def test_extreme_parameters(bd):
             check(bd, x, uu, **how)
 
 
+@pytest.mark.parametrize("dtype", DTYPES)
+def test_cold_rows_of_equal_logits(bd, dtype):
+    """More equal logits than a list holds, at temperatures at which every other value of the type is many octaves away."""
+    x = torch.full((4, 9000), -3.0, dtype=DTYPES[dtype], device="cuda")
+    x[:, 5::9] = 2.0
+    x[2, 7] = 2.015625
+    u = torch.tensor([0.1, 0.5, 0.9, 1.0], device="cuda")
+    for t in (1e-5, 3e-6, 1e-3, 0.03):
+        for how in (dict(), dict(top_k=600), dict(top_p=0.5), dict(min_p=0.3), dict(top_k=700, top_p=0.7, min_p=0.9)):
+            check(bd, x, u, temperature=t, **how)
+
+
 def test_rows_with_their_token_are_left(bd):
     x = logits_of(3, 50, 1000, torch.bfloat16)
     x[1::3] = math.nan
