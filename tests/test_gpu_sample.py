@@ -88,6 +88,18 @@ def test_many_rows_of_every_kind(bd):
 
 
 @pytest.mark.parametrize("dtype", DTYPES)
+def test_cuts_about_the_number_of_listed_tokens(bd, dtype):
+    """top-k from below the parts that a row is looked at in to above what a list holds, with and without the other cuts, in rows
+    that several CTAs share: all of them must take the same way."""
+    ks = [31, 32, 33, 63, 64, 65, 100, 119, 120, 121, 127, 128, 129, 200, 255, 256, 257, 400, 511, 512, 513, 800]
+    x = logits_of(21, len(ks), 140001, DTYPES[dtype], pad=3, head=10)
+    u = torch.rand(len(ks), generator=torch.Generator("cuda").manual_seed(2), device="cuda")
+    k = torch.tensor(ks, dtype=torch.int32, device="cuda")
+    for how in (dict(), dict(min_p=0.02), dict(min_p=1e-4, temperature=1.5), dict(top_p=0.9), dict(top_p=0.99, min_p=0.3)):
+        check(bd, x, u, top_k=k, **how)
+
+
+@pytest.mark.parametrize("dtype", DTYPES)
 def test_equal_logits(bd, dtype):
     """Every border is hit exactly: u, p and k at whole numbers of equal tokens."""
     vocab = 4096
