@@ -124,6 +124,7 @@ size_t cache_attn_plane_bytes(long long total_rows, int H, int D);
 size_t cache_pages_scratch_bytes(int n_pages, int n_seqs);
 cudaError_t launch_cache_write(const CacheWriteArgs& a, int num_sms, cudaStream_t st, int* launches);
 cudaError_t launch_cache_attn(const CacheAttnArgs& a, int num_sms, cudaStream_t st, int* launches);
+cudaError_t launch_cache_attn_shared(const CacheAttnArgs& a, int num_sms, cudaStream_t st, int* launches);
 cudaError_t launch_cache_pages(const CachePagesArgs& a, int num_sms, cudaStream_t st, int* launches);
 
 size_t cache_prefixes_scratch_bytes(int n_seqs);

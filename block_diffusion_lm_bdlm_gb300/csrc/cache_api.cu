@@ -122,8 +122,8 @@ int run_attn(CacheAttnArgs& a, void* workspace, size_t workspace_bytes, size_t n
     }
     const int sms = device_sms();
     int launches = 0;
-    if (sms <= 0 || launch_cache_attn(a, sms, reinterpret_cast<cudaStream_t>(stream), &launches) != cudaSuccess)
-        return BDLM_ERR_CUDA;
+    const auto launch = a.runs ? launch_cache_attn_shared : launch_cache_attn;
+    if (sms <= 0 || launch(a, sms, reinterpret_cast<cudaStream_t>(stream), &launches) != cudaSuccess) return BDLM_ERR_CUDA;
     set_last_launches(launches);
     return BDLM_OK;
 }
