@@ -194,6 +194,40 @@ def test_no_number_in_one_branch(bd):
         cu.check_attention(*bd.bdlm_cache_attn_shared_fwd(cache, q, dev(off), 1, dev(plan_of(4, shares, page)), check=True), ref, str(where))
 
 
+@pytest.mark.parametrize("d,page,G,rows,block", [(64, 16, 1, 8, 1), (128, 16, 1, 8, 3), (64, 32, 2, 4, 2), (128, 64, 4, 2, 1), (64, 128, 8, 1, 1),
+                                                 (128, 32, 3, 2, 1), (128, 16, 5, 1, 1), (64, 16, 1, 7, 4)])
+def test_few_rows(bd, d, page, G, rows, block):
+    """Up to eight flat rows, with blocks that end within 16 keys: rows see different numbers of them, and NaN among the values
+    that only the later rows see reaches those alone. Rows of q far from 1, and pages of unlike magnitude."""
+    Hk, prefix = 2, 1792
+    own = [rows, rows + 1, rows + 5, 15 + rows, 16 + rows, 37, 128 + rows, 300, 2048]
+    lens, n = [prefix + x for x in own], len(own)
+    shares = [(0, n, prefix // page)]
+    c = tree(page + G, lens, shares, page=page, Hk=Hk, d=d, page_spread=3.0)
+    off = cu.offsets([rows] * n)
+    rng = np.random.default_rng(rows)
+    q = torch.from_numpy(rng.standard_normal((int(off[-1]), Hk * G, d)) * np.exp2(rng.choice([-70, -8, 0, 0, 0, 3, 20], (int(off[-1]), Hk * G, 1))))
+    q = q.bfloat16().cuda()
+    for marks in (0, 1):
+        if marks:
+            for s in range(n):  # the last row's own key, and the one in the middle of the rows
+                for back, col in ((1, 3), (rows // 2 + 1, d - 1)):
+                    at = lens[s] - back
+                    c["v"][0, c["table"][s, at // page], s % 2, at % page, col] = 127
+        cache = cu.to_device(bd, c)
+        ref = co.attention(c, 0, q.double().cpu().numpy(), off, block, d ** -0.5)
+        runs = bd.bdlm_cache_prefixes(cache, dev(off), check=True)
+        for plan in (runs, dev(plan_of(n, [], page))):
+            o, lse = torch.empty(q.shape, dtype=torch.float32, device="cuda"), torch.empty((Hk * G, q.shape[0]), device="cuda")
+            bd.bdlm_cache_attn_shared_fwd(cache, q, dev(off), block, plan, out=o, lse=lse, check=True)
+            # An o is at most A, so where the scores' own error of 2^-15 S1 allows a difference of 2 A and more, as it does from
+            # S1 = 2^15 on, the bound says nothing of o; the weights of scores from 2^23 on, which fp32 holds to whole
+            # octaves, may be anything.
+            void = 2.0 ** -14 * ref[3].T >= 2
+            o[torch.from_numpy(void).cuda()] = torch.from_numpy(ref[0][void]).float().cuda()
+            cu.check_attention(o, lse, ref, f"NaN {marks}")
+
+
 BAD_PLANS = [
     [[0, 0, 0], [3, 3, 3], [32, 32, 16]],   # not the same
     [[0, 0, 2], [3, 3, 3], [32, 32, 32]],
