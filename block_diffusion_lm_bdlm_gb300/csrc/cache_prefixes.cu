@@ -194,8 +194,8 @@ cudaError_t launch_cache_prefixes(const CachePrefixArgs& a, cudaStream_t st, int
     cudaError_t e = cudaGetLastError();
     if (e != cudaSuccess) return e;
     const size_t smem = cut_smem(n);
-    if (smem > 48 * 1024) {
-        e = cudaFuncSetAttribute(cut_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    if (smem > 48 * 1024) {  // (what the longest call needs, whatever this one does: calls of several threads set the same)
+        e = cudaFuncSetAttribute(cut_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)cut_smem(cache_prefixes_most_seqs()));
         if (e != cudaSuccess) return e;
     }
     cudaLaunchConfig_t cfg{};

@@ -1279,7 +1279,9 @@ cudaError_t launch(SampleArgs a, int num_sms, cudaStream_t st, int* launches) {
     a.per = parts(c);
     a.ahead = 2 * num_sms / c * c;  // two CTAs on an SM
     const size_t smem = ((size_t)a.per / VE + 1) * 16;
-    cudaError_t e = cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)smem);
+    // (what the longest row needs, whatever this one does: calls of several threads set the same)
+    constexpr int most = kMaxVocab / kMaxCtas * (int)sizeof(T) + 16;
+    cudaError_t e = cudaFuncSetAttribute(sample_kernel<T>, cudaFuncAttributeMaxDynamicSharedMemorySize, most);
     if (e != cudaSuccess) return e;
     cudaLaunchConfig_t cfg{};
     cfg.gridDim = dim3((unsigned)(a.rows * c));

@@ -17,6 +17,8 @@
 
 #include <cstdint>
 
+#include <cmath>
+
 #include "common.cuh"
 #include "tc_ptx.cuh"
 
@@ -24,6 +26,7 @@ namespace bdlm {
 namespace sample {
 
 constexpr double kQuick = 4e-6;
+constexpr int kMaxVocab = 1 << 18;
 constexpr int kFrac = 44;  // a weight of 1 is 2^44: 2^18 of them stay below 2^62
 
 #ifdef __CUDA_ARCH__
@@ -32,7 +35,6 @@ constexpr int kFrac = 44;  // a weight of 1 is 2^44: 2^18 of them stay below 2^6
 #define BDLM_FMA(a, b, c) __fmaf_rn(a, b, c)
 #define BDLM_RINT(x) __float2int_rn(x)
 #else
-#include <cmath>
 #define BDLM_MUL(a, b) ((a) * (b))
 #define BDLM_ADD(a, b) ((a) + (b))
 #define BDLM_FMA(a, b, c) std::fma(a, b, c)

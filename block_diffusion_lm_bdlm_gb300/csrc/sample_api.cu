@@ -11,7 +11,6 @@ using namespace bdlm;
 namespace {
 
 constexpr long long kMaxRows = 1LL << 26;  // eight CTAs of each are a grid
-constexpr int kMaxVocab = 1 << 18;
 constexpr int kMaxSeqs = 1 << 16;
 
 bool aligned(const void* p, uintptr_t a) { return (reinterpret_cast<uintptr_t>(p) & (a - 1)) == 0; }
@@ -36,7 +35,7 @@ int bdlm_sample(const void* logits, int32_t dtype, int64_t rows, int32_t vocab, 
     if (!aligned(how->temperature, 4) || !aligned(how->top_k, 4) || !aligned(how->top_p, 4) || !aligned(how->min_p, 4))
         return BDLM_ERR_INVALID_ARG;
     if (rows < 1 || rows > kMaxRows || vocab < 1 || row_stride < vocab || row_stride > (1LL << 40)) return BDLM_ERR_INVALID_ARG;
-    if (vocab > kMaxVocab) return BDLM_ERR_UNSUPPORTED;
+    if (vocab > sample::kMaxVocab) return BDLM_ERR_UNSUPPORTED;
     const size_t n = (size_t)rows, logits_bytes = ((n - 1) * (size_t)row_stride + vocab) * size;
     const void* in[] = {u, how->temperature, how->top_k, how->top_p, how->min_p, tokens};
     for (const void* p : in)

@@ -133,3 +133,31 @@ def test_captured_step(bd):
         tokens.copy_(was)
         again = step()
         assert torch.equal(got[0], o) and torch.equal(got[1], lse) and torch.equal(got[2], tokens) and torch.equal(got[3], again)
+
+
+def test_calls_of_several_threads(bd):
+    """Calls of unlike sizes from four threads at once, each on a stream of its own, give what they give one after the other."""
+    from concurrent.futures import ThreadPoolExecutor
+
+    gen = torch.Generator("cuda").manual_seed(9)
+    jobs = []
+    for vocab, dtype, n in ((100, torch.float32, 5), (262144, torch.float32, 12000), (32001, torch.bfloat16, 40), (131072, torch.float16, 16384)):
+        logits, u = (2 * torch.randn(3, vocab, device="cuda", generator=gen)).to(dtype), torch.rand(3, device="cuda", generator=gen)
+        cache = bd.PageCache.empty(1, 4, 16, 1, 64, n, 2)
+        cache.lens.fill_(17)  # all in the same pages: runs of 256
+        jobs.append((logits, u, cache, torch.arange(n + 1, dtype=torch.int32, device="cuda"), torch.cuda.Stream()))
+
+    def work(job, times):
+        logits, u, cache, cu_rows, stream = job
+        got = []
+        for _ in range(times):
+            token, lp = bd.bdlm_sample(logits, u, top_p=0.9, stream=stream)
+            got.append((token, lp, bd.bdlm_cache_prefixes(cache, cu_rows, stream=stream)))
+        stream.synchronize()
+        return got
+
+    torch.cuda.synchronize()
+    want = [work(job, 1)[0] for job in jobs]
+    with ThreadPoolExecutor(len(jobs)) as pool:
+        for ref, got in zip(want, pool.map(lambda job: work(job, 50), jobs)):
+            assert all(torch.equal(x, y) for one in got for x, y in zip(ref, one))
