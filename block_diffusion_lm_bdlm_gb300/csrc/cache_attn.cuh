@@ -119,9 +119,14 @@ __device__ __forceinline__ Run run_of(const CacheAttnArgs& a, int s, const SeqRo
 }
 
 // Sequences with few flat rows and few keys of their own (`own`: those behind what they share) do not pay for an MMA tile:
-// cache_own_kernel reads those keys.
-constexpr int kFewRows = 8, kFewKeys = 2048;
-__device__ __forceinline__ bool is_few(const CacheAttnArgs& a, int rows, int own) { return rows * (long long)a.G <= kFewRows && own <= kFewKeys; }
+// cache_own_kernel reads those keys, one CTA for a sequence's head. One row each of n sequences over 8192 shared keys and 256,
+// 1024, 2048, 4096 own ones (8 kv heads, d = 128, G = 4), us by tiles: 33, 32, 35, 36 for n = 4, 71, 97, 127, 179 for 64, 205,
+// 287, 397, 610 for 256; by that kernel 34, 34, 36, 49, then 49, 75, 97, 140, and 125, 178, 252, 401. So the longest
+// are left to it where there are CTAs enough to fill the SMs.
+constexpr int kFewRows = 8, kFewKeys = 2048, kMostKeys = 4096, kManyCtas = 256;
+__device__ __forceinline__ bool is_few(const CacheAttnArgs& a, int rows, int own) {
+    return rows * (long long)a.G <= kFewRows && own <= (a.c.n_seqs * a.c.Hk >= kManyCtas ? kMostKeys : kFewKeys);
+}
 
 template <bool RUNS>
 __device__ __forceinline__ int items_of(const CacheAttnArgs& a) { return RUNS ? 2 * a.c.n_seqs : a.c.n_seqs; }

@@ -228,6 +228,23 @@ def test_few_rows(bd, d, page, G, rows, block):
             cu.check_attention(o, lse, ref, f"NaN {marks}")
 
 
+@pytest.mark.parametrize("d,page", [(64, 16), (128, 128)])
+def test_few_rows_of_many_sequences(bd, d, page):
+    """Enough sequences that own keys up to 4096 count as few; one has more."""
+    n, Hk, prefix = 33, 8, 2048
+    own = [1 + 7 * s for s in range(n)]
+    own[3], own[7], own[8], own[20], own[32] = 2049, 4095, 4096, 4097, 3000
+    lens = [prefix + x for x in own]
+    c = tree(d, lens, [(0, n, prefix // page)], page=page, Hk=Hk, d=d)
+    off = cu.offsets([1] * n)
+    q = torch.from_numpy(np.random.default_rng(d).standard_normal((n, Hk, d))).bfloat16().cuda()
+    cache = cu.to_device(bd, c)
+    ref = co.attention(c, 0, q.double().cpu().numpy(), off, 1, d ** -0.5)
+    runs = bd.bdlm_cache_prefixes(cache, dev(off), check=True)
+    assert runs[2].tolist() == [prefix] * n
+    cu.check_attention(*bd.bdlm_cache_attn_shared_fwd(cache, q, dev(off), 1, runs, check=True), ref)
+
+
 BAD_PLANS = [
     [[0, 0, 0], [3, 3, 3], [32, 32, 16]],   # not the same
     [[0, 0, 2], [3, 3, 3], [32, 32, 32]],
