@@ -438,6 +438,9 @@ BDLM_API size_t bdlm_cache_attn_fwd_workspace_bytes(int64_t total_rows, int32_t 
  *          the result is a partial one for bdlm_lse_merge.
  * A row that sees no key gets o = 0, lse = -inf. What a masked key or value
  * holds (NaN among it) reaches no row that does not see it.
+ * Scores are held in fp32: where |scale q.k| passes 2^22, neighbouring values
+ * of them are a quarter apart and more, and o may be anything (infinite among
+ * it).
  * Malformed offsets or lengths (BDLM_ERR_DEVICE_CHECK) leave o and lse
  * unwritten; a table entry outside [0, n_pages) turns the rows of its
  * sequence that see it, and possibly others of that sequence, into NaN.
