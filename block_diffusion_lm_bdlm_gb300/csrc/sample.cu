@@ -11,21 +11,28 @@
 // Which token that is must not depend on roundings. Sums are first taken from
 // the quick weights (sample.cuh), whose error is bounded: where the bound says
 // that the decision stands, it does; else it is made from the exact ones. Few
-// tokens are near the top of a usual row, so cuts are found from exact weights
-// at once.
+// tokens are near the top of a usual row, so their weights are exact at once.
 //
 // One cluster of CTAs takes one row. Each CTA copies its part of the row to
 // shared memory, where every later pass reads it: the row comes from memory
-// once. Passes: the largest logit; sums of the quick weights; for a cut, the
-// weights (or for top-k numbers) of the tokens in bins of falling logit, where
-// only those bins are filled that the threads' largest logits cannot rule out,
-// and the bin with the cut again in finer ones until it is a single logit; the
-// kept weights of each warp's part; the tokens of the one part in which the sum
-// passes u.
+// once. The first pass finds the largest logit, and from the largest of 128
+// parts of the row a logit from which on as many tokens as top-k asks for, or
+// about 130, will lie; the second takes the sums of the quick weights and lists
+// those tokens in the first CTA. If the list has all that may be kept, that CTA
+// ranks it and draws, and the others are done. Without cuts the token is where
+// the quick sums pass u times all. Else the cut is searched in the whole row:
+// bf16 logits are counted by value, of which there are so few that one pass
+// gives every later sum; others in bins of falling logit, where only those bins
+// are filled that the threads' largest logits cannot rule out, and the bin with
+// the cut again in finer ones until it is a single logit. The part in which the
+// kept weights pass u times all of them then finds the token.
 //
-// Bound. Memory, for peaked rows; each pass is 64 KB from shared memory and 1
-// to 8 instructions a logit. What it takes besides are five to ten barriers of
-// the cluster, which the other clusters on the SM fill.
+// Bound. Instruction issue (60 % of the slots) and the barriers of the cluster, of
+// which a listed row takes three. 512 rows of 131072 bf16 logits, 134 MB (20 us
+// of memory), take 101 us with top-k 50, 198 with top-p 0.95 where most rows are
+// listed and some count their values, 312 where all do, 141 without cuts. One
+// row of 32001 takes 10 us. Two CTAs of 512 threads share an SM; three of 256
+// were no faster on the whole.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
