@@ -83,13 +83,32 @@ struct Rows : SeqRows {
 };
 enum : int { PART_WHOLE = 0, PART_SHARED = 1, PART_OWN = 2 };
 
-// Whether n sequences with `rows` rows in all gain from reading `shared` positions together. Alone, each takes an MMA tile
-// of 128 flat rows through them, however few it has; together they take what their rows fill. Against that stand
-// two more units and a join for each sequence, about kJoinCost tiles' time.
-constexpr int kJoinCost = 12;
+// Sequences with few flat rows and few keys of their own (`own`: those behind what they share) do not pay for an MMA tile:
+// cache_own_kernel reads those keys, one CTA for a sequence's head. One row each of n sequences over 8192 shared keys and 256,
+// 1024, 2048, 4096 own ones (8 kv heads, d = 128, G = 4), us by tiles: 33, 32, 35, 36 for n = 4, 71, 97, 127, 179 for 64, 205,
+// 287, 397, 610 for 256; by that kernel 34, 34, 36, 49, then 49, 75, 97, 140, and 125, 178, 252, 401. So the longest
+// are left to it where there are CTAs enough to fill the SMs.
+constexpr int kFewRows = 8, kFewKeys = 2048, kMostKeys = 4096, kManyCtas = 256;
+__device__ __forceinline__ int few_keys(const CacheAttnArgs& a) { return a.c.n_seqs * a.c.Hk >= kManyCtas ? kMostKeys : kFewKeys; }
+__device__ __forceinline__ bool is_few(const CacheAttnArgs& a, int rows, int own) { return rows * (long long)a.G <= kFewRows && own <= few_keys(a); }
+
+// Whether n sequences with `rows` rows in all gain from reading `shared` positions together, in keys of a tile's time. Alone,
+// each takes MMA tiles of 128 flat rows through them, however few it has, or, if those are few, cache_own_kernel, in which a
+// key takes four fifths of that; together they take what their rows fill (those that fill a tile each gain nothing). Against
+// that stand, in tiles, the units that this adds and the joins, kRowCost for a flat row, or, where rows are few, kOwnCost for a
+// sequence; and 32 for the call (a.call_tiles for each of its sequences), if nothing else in it is read together. Twice as
+// many tiles of d = 64, which take half the time.
+// Alone and together, us, with 1024 shared keys (d = 128, G = 4, 100 own keys): 64 sequences of 1 row 38, 33; 16 runs of 4 38,
+// 45; 16 of 16 116, 85; with 8 rows each 100, 71; 97, 76; 361, 244; a run of 8 with 8 rows 31, 32; with 16 rows 16 runs of 4 105,
+// 108; 16 of 16 358, 345. (Without contractions: every kernel must come to the same.)
+constexpr float kRowCost = 0.053f, kOwnCost = 4.f;
 __device__ __forceinline__ bool worth(const CacheAttnArgs& a, int n, int rows, int shared) {
-    const float each = (float)rows * a.G / n;
-    return shared * (1.f / kTileKeys) * (1.f - fminf(each, 128.f) * (1.f / 128.f)) > (float)kJoinCost;
+    const int flat = rows * a.G, together = (flat + 127) >> 7;
+    const float wide = a.c.D == 128 ? (float)kTileKeys : 2.f * kTileKeys;
+    if (flat <= kFewRows * n && shared <= few_keys(a))
+        return __fmul_rn((float)shared, (float)(4 * n - 5 * together)) > __fmul_rn(__fmul_rn(5.f * wide, (float)n), __fadd_rn(kOwnCost, a.call_tiles));
+    return flat < 128 * n && __fmul_rn((float)shared, (float)(n - together)) >
+                                 __fmul_rn(wide, __fadd_rn(__fmul_rn(kRowCost, (float)flat), __fmul_rn((float)n, a.call_tiles)));
 }
 
 // What the run of sequence s is, and whether it is well-formed: all of its
@@ -116,16 +135,6 @@ __device__ __forceinline__ Run run_of(const CacheAttnArgs& a, int s, const SeqRo
     if (u.shared > 0 && (s == u.first || r.rows > 0)) u.ok = u.ok && u.shared <= r.len && (r.rows == 0 || u.shared <= r.pos0);
     if (u.ok && u.shared > 0 && !worth(a, u.end - u.first, __ldg(a.cu_rows + u.end) - __ldg(a.cu_rows + u.first), u.shared)) u.shared = 0;
     return u;
-}
-
-// Sequences with few flat rows and few keys of their own (`own`: those behind what they share) do not pay for an MMA tile:
-// cache_own_kernel reads those keys, one CTA for a sequence's head. One row each of n sequences over 8192 shared keys and 256,
-// 1024, 2048, 4096 own ones (8 kv heads, d = 128, G = 4), us by tiles: 33, 32, 35, 36 for n = 4, 71, 97, 127, 179 for 64, 205,
-// 287, 397, 610 for 256; by that kernel 34, 34, 36, 49, then 49, 75, 97, 140, and 125, 178, 252, 401. So the longest
-// are left to it where there are CTAs enough to fill the SMs.
-constexpr int kFewRows = 8, kFewKeys = 2048, kMostKeys = 4096, kManyCtas = 256;
-__device__ __forceinline__ bool is_few(const CacheAttnArgs& a, int rows, int own) {
-    return rows * (long long)a.G <= kFewRows && own <= (a.c.n_seqs * a.c.Hk >= kManyCtas ? kMostKeys : kFewKeys);
 }
 
 template <bool RUNS>
