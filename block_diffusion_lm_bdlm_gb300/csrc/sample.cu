@@ -985,7 +985,9 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
             ln += s_all.n[r];
             lw += s_all.sums[r][2];
         }
-        const bool by_min_all = by_min && R.exact(x0) < least_w;
+        // What min-p keeps is all in the list. That is enough unless top-p goes by what the first k weigh together: min-p drops
+        // some of those only afterwards, so the list has to have all k, or every token above -infinity.
+        const bool by_min_all = by_min && R.exact(x0) < least_w && (!(by_k && by_p) || x0 == -3.402823466e38f);
         if (!greedy)
             listed = listed && (by_min_all || (by_k ? ln >= top_k : by_p && lw >= mul_ceil(p, quick_z + off) + off));
     }
