@@ -54,7 +54,9 @@ __global__ void __launch_bounds__(kThreads) unmask_kernel(const UnmaskArgs a) {
     const float threshold = a.threshold ? __ldg(a.threshold + s) : a.threshold_all;
     // 0: keeps its token; else the order of its log-probability. NaN comes below everything.
     auto key_at = [&](int i) -> uint32_t {
-        if (i >= rows || __ldg(a.now + lo + i) != a.mask_id || __ldg(a.sampled + lo + i) < 0) return 0u;
+        if (i >= rows || __ldg(a.now + lo + i) != a.mask_id) return 0u;
+        const int drawn = __ldg(a.sampled + lo + i);
+        if (drawn < 0 || drawn == a.mask_id) return 0u;  // (a row that was given the mask would still be masked)
         const float x = __ldg(a.logprob + lo + i);
         return x != x ? 1u : order_key(__float_as_uint(x));
     };

@@ -103,8 +103,8 @@ def bdlm_unmask(tokens, sampled, logprob, cu_rows, mask_id: int, *, n_min=0, thr
                 workspace=None, stream=None, check: bool = False):
     """Which masked rows (tokens[i] == mask_id) keep their drawn token: those
     whose logprob is at least `threshold` (NaN: none), and at least the n_min
-    surest of every sequence. n_min (int32) and threshold (fp32) are numbers
-    or tensors [n_seqs]. Returns (tokens int32 [T], left int32 [n_seqs]: rows
+    surest of every sequence; a drawn token below 0, or mask_id itself, is none.
+    n_min (int32) and threshold (fp32) are numbers or tensors [n_seqs]. Returns (tokens int32 [T], left int32 [n_seqs]: rows
     still masked); `out` may be tokens itself. Rows behind cu_rows[-1] are left
     unwritten. check=True synchronises and raises on malformed offsets."""
     lib = load_library()

@@ -605,7 +605,8 @@ BDLM_API size_t bdlm_unmask_workspace_bytes(void);
  *   denoising step.
  *
  *   tokens, sampled  int32 [total_rows]: the rows' present tokens (mask_id where
- *                    there is none yet) and the drawn ones (< 0: none)
+ *                    there is none yet) and the drawn ones (none: < 0, or
+ *                    mask_id, with which a row would still be masked)
  *   logprob          fp32 [total_rows]: the drawn ones' log-probabilities
  *   cu_rows          as for the cache calls: DEVICE int32 [n_seqs + 1]
  *   n_min            int32 [n_seqs] on the device, or NULL: n_min_all for all

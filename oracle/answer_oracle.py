@@ -47,11 +47,11 @@ def sample_row(x, u, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0):
 
 
 def unmask(tokens, sampled, logprob, cu_rows, mask_id, n_min, threshold):
-    """(tokens, left); n_min and threshold one per sequence. Rows behind the last offset stay."""
+    """(tokens, left); n_min and threshold one per sequence. Rows behind the last offset stay. A drawn mask is no token."""
     out, left = np.array(tokens), []
     for s in range(len(cu_rows) - 1):
         rows = [i for i in range(cu_rows[s], cu_rows[s + 1]) if tokens[i] == mask_id]
-        can = [i for i in rows if sampled[i] >= 0]
+        can = [i for i in rows if sampled[i] >= 0 and sampled[i] != mask_id]
         rank = sorted(can, key=lambda i: (math.isnan(logprob[i]), -logprob[i] if not math.isnan(logprob[i]) else 0.0, i))
         keep = {i for i in can if logprob[i] >= threshold[s]}
         if len(keep) < n_min[s]:

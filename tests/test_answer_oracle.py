@@ -61,3 +61,8 @@ def test_runs_save_most(seed):
         if shared:
             inside = [i for i in range(m) if first <= busy[i] < end]
             assert len(inside) > 1 and shared == 16 * min(c[i] for i in inside[:-1])
+
+
+def test_unmask_keeps_no_mask():
+    out, left = ao.unmask([9, 9, 9, 4], [9, 1, 2, 3], [0.0, -1.0, -2.0, 0.0], [0, 4], 9, [1], [-0.5])
+    assert out.tolist() == [9, 1, 9, 4] and left.tolist() == [2]
