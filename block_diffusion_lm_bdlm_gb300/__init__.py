@@ -62,6 +62,7 @@ BDLM_OK = 0
 BDLM_BF16, BDLM_F32, BDLM_F16 = 0, 1, 2
 PART_NONE, PART_KEY_WINDOW, PART_BLOCK_GROUP = 0, 1, 2
 PART_ACCUMULATE = 1
+SAMPLE_NO_MASK = 1
 
 EXPORTED_SYMBOLS = (
     "bdlm_attn_fwd_workspace_bytes", "bdlm_attn_bwd_workspace_bytes", "bdlm_attn_fwd", "bdlm_attn_bwd",
@@ -147,7 +148,8 @@ class _CCache(ctypes.Structure):
 class _CSampling(ctypes.Structure):
     _fields_ = [("temperature", ctypes.c_void_p), ("top_k", ctypes.c_void_p), ("top_p", ctypes.c_void_p),
                 ("min_p", ctypes.c_void_p), ("temperature_all", ctypes.c_float), ("top_k_all", ctypes.c_int32),
-                ("top_p_all", ctypes.c_float), ("min_p_all", ctypes.c_float)]
+                ("top_p_all", ctypes.c_float), ("min_p_all", ctypes.c_float), ("flags", ctypes.c_int32),
+                ("reserved", ctypes.c_int32)]
 
 
 class _CTask(ctypes.Structure):

@@ -798,6 +798,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
         R.c2 = -q;
     }
     asm volatile("cp.async.wait_all;" ::: "memory");
+    if (a.barred >= first && a.barred < first + n) {  // who copied it takes it out
+        const int e = a.barred - first + skew, v = e / VE;
+        if (v >= v0 && v < v1 && (v & 31) == lane) reinterpret_cast<T*>(s_data)[e] = value_of<T>(-INFINITY);
+    }
 
     // ---- the largest logit
     R.mine = -INFINITY;
@@ -1036,7 +1040,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
                     for (int j = tid; j < a.vocab; j += kThreads) {
                         float y = (float)x[j];
                         if (infinite) y = y == INFINITY ? 0.f : -INFINITY;
-                        if (y > -INFINITY) s += R.exact(y);
+                        if (y > -INFINITY && j != a.barred) s += R.exact(y);
                     }
                     lo = hi = mul_ceil(p, R.cta_sum(s));
                 }

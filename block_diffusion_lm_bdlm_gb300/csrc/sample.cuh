@@ -153,6 +153,7 @@ struct SampleArgs {
     int top_k_all;
     const int* now;  // rows whose entry is not `want` are left (nullptr: none are)
     int want;
+    int barred;  // token without weight (-1: none)
     int* token;
     float* logprob;
     int ctas;  // CTAs of a row, one cluster

@@ -32,6 +32,7 @@ int bdlm_sample(const void* logits, int32_t dtype, int64_t rows, int32_t vocab, 
     const size_t size = dtype == BDLM_F32 ? 4 : 2;
     if (!good_ptr(logits, size) || !good_ptr(u, 4) || !aligned(tokens, 4) || !good_ptr(token, 4) || !good_ptr(logprob, 4) || !how)
         return BDLM_ERR_INVALID_ARG;
+    if ((how->flags & ~BDLM_SAMPLE_NO_MASK) || how->reserved) return BDLM_ERR_INVALID_ARG;
     if (!aligned(how->temperature, 4) || !aligned(how->top_k, 4) || !aligned(how->top_p, 4) || !aligned(how->min_p, 4))
         return BDLM_ERR_INVALID_ARG;
     if (rows < 1 || rows > kMaxRows || vocab < 1 || row_stride < vocab || row_stride > (1LL << 40)) return BDLM_ERR_INVALID_ARG;
@@ -61,6 +62,7 @@ int bdlm_sample(const void* logits, int32_t dtype, int64_t rows, int32_t vocab, 
     a.min_p_all = how->min_p_all;
     a.now = tokens;
     a.want = mask_id;
+    a.barred = (how->flags & BDLM_SAMPLE_NO_MASK) && mask_id >= 0 && mask_id < vocab ? mask_id : -1;
     a.token = token;
     a.logprob = logprob;
     const int sms = device_sms();

@@ -97,11 +97,13 @@ class BlockDecoder:
         """Draw a token for every row that has none yet (tokens[i] == mask_id;
         int32, a row of logits and of u for each) and enter, in tokens, those
         with a log-probability of at least `threshold` (NaN: none) and at
-        least the n_min surest of every sequence. Returns the rows of each
-        sequence that are still masked (int32 [n_seqs])."""
+        least the n_min surest of every sequence. mask_id itself is never
+        drawn: where it is a token of the vocabulary its logit counts as -inf,
+        for the log-probabilities as well. Returns the rows of each sequence
+        that are still masked (int32 [n_seqs])."""
         drawn, logprob = torch.empty_like(tokens), torch.empty_like(u)
         bdlm_sample(logits, u, temperature=temperature, top_k=top_k, top_p=top_p, min_p=min_p, tokens=tokens,
-                    mask_id=mask_id, out=drawn, logprob=logprob)
+                    mask_id=mask_id, out=drawn, logprob=logprob, draw_mask=False)
         return bdlm_unmask(tokens, drawn, logprob, self._cu, mask_id, n_min=n_min, threshold=threshold, out=tokens,
                            check=check)[1]
 

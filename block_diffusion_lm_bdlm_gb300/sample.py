@@ -13,7 +13,7 @@ from contextlib import nullcontext
 
 import torch
 
-from . import BDLM_BF16, BDLM_F16, BDLM_F32, _check, _CSampling, load_library
+from . import BDLM_BF16, BDLM_F16, BDLM_F32, _check, _CSampling, SAMPLE_NO_MASK, load_library
 
 _DTYPES = {torch.bfloat16: BDLM_BF16, torch.float16: BDLM_F16, torch.float32: BDLM_F32}
 _NULL = nullcontext()
@@ -57,14 +57,15 @@ def _either(name, x, dtype, n, index):
 
 
 def bdlm_sample(logits, u, *, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, tokens=None, mask_id: int = 0, out=None,
-                logprob=None, stream=None):
+                logprob=None, stream=None, draw_mask: bool = True):
     """Draw a token for each row of logits [rows, vocab] (bf16, fp16 or fp32;
     rows may be strided) with the random numbers u (fp32 [rows], in [0, 1]).
     Returns (token int32 [rows], logprob fp32 [rows]); logprob is that of the
     token under softmax(logits). temperature, top_p, min_p (fp32) and top_k
     (int32) are numbers or tensors [rows]. With `tokens` (int32 [rows]) only
     rows whose token is mask_id are drawn: `out` (which may be tokens itself)
-    and `logprob` stay as they were in the others. -1 and -inf stand in rows
+    and `logprob` stay as they were in the others. With draw_mask=False token
+    mask_id counts as if its logit were -inf. -1 and -inf stand in rows
     without any logit above -inf. rows may be 0."""
     lib = load_library()
     if not isinstance(logits, torch.Tensor) or not logits.is_cuda or logits.dtype not in _DTYPES or logits.dim() != 2:
@@ -83,7 +84,7 @@ def bdlm_sample(logits, u, *, temperature=1.0, top_k=0, top_p=1.0, min_p=0.0, to
     now = None if tokens is None else _vector("tokens", tokens, torch.int32, n, index)
     if tokens is not None and (out is None or logprob is None):
         raise ValueError("with tokens, out and logprob hold what the other rows keep: pass them")
-    how = _CSampling(t, k, p, m, t_all, k_all, p_all, m_all)
+    how = _CSampling(t, k, p, m, t_all, k_all, p_all, m_all, 0 if draw_mask else SAMPLE_NO_MASK)
     handle, here = _on(device, stream)
     with here:
         if out is None:

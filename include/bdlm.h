@@ -565,7 +565,11 @@ typedef struct {
     int32_t top_k_all;     /* < 1 or >= vocab: off                                       */
     float top_p_all;       /* >= 1 (and NaN): off; <= 0: the first token alone           */
     float min_p_all;       /* <= 0 (and NaN): off; above 1: 1                            */
+    int32_t flags;         /* BDLM_SAMPLE_*; 0                                           */
+    int32_t reserved;      /* 0                                                          */
 } bdlm_sampling;
+
+enum { BDLM_SAMPLE_NO_MASK = 1 }; /* mask_id counts as masked: as if its logit were -inf */
 
 /*
  * bdlm_sample - draw a token for each row of logits with a random number that
@@ -587,7 +591,9 @@ typedef struct {
  * last one of any weight). With temperature 0 it is the first of the largest.
  * If the largest logit is +inf, the logits that are +inf weigh the same and
  * all others nothing. logprob is the token's under softmax(logits), without
- * temperature and cuts. A row without any logit above -inf gets token -1,
+ * temperature and cuts. With BDLM_SAMPLE_NO_MASK (with or without `tokens`)
+ * mask_id's logit is -inf for all of this; a mask_id outside [0, vocab) is no
+ * token of the row. A row without any logit above -inf gets token -1,
  * logprob -inf.
  * The choice is made from weights that are exact to 2^-40 and multiples of
  * 2^-44 (what is below 2^-45 of the largest weighs nothing), summed as whole

@@ -94,3 +94,11 @@ def test_bindings_refuse_host_tensors(bd):
     with pytest.raises(ValueError):
         bd.bdlm_unmask(torch.zeros(2, dtype=torch.int32), torch.zeros(2, dtype=torch.int32), torch.zeros(2),
                        torch.zeros(2, dtype=torch.int32), 7)
+
+
+def test_sampling_flags(bd):
+    """Flags that there are not, and a reserved word that is set, are refused."""
+    for more in ((2, 0), (-1, 0), (1 << 31 - 1, 0), (0, 1), (1, -1)):
+        h = ctypes.byref(bd._CSampling(None, None, None, None, 1.0, 0, 1.0, 0.0, *more))
+        assert bd.load_library().bdlm_sample(1 << 20, 0, 4, 100, 100, 64, h, None, 7, 128, 256, None) == INVALID
+    assert ctypes.sizeof(bd._CSampling) == 56
