@@ -993,7 +993,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
         // some of those only afterwards, so the list has to have all k, or every token above -infinity.
         const bool by_min_all = by_min && R.exact(x0) < least_w && (!(by_k && by_p) || x0 == -3.402823466e38f);
         if (!greedy)
-            listed = listed && (by_min_all || (by_k ? ln >= top_k : by_p && lw >= mul_ceil(p, quick_z + off) + off));
+            // (a thread may have added up as many as 64 of the listed weights, 3.8e-6 of them: twice kQuick covers that)
+            listed = listed && (by_min_all || (by_k ? ln >= top_k : by_p && lw >= mul_ceil(p, quick_z + off) + 2 * off));
     }
     if (listed) {
         if (rank != 0) return;
@@ -1109,7 +1110,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
             }
             if (who >= 0 && who == rank * kWarps + warp) {
                 // The error of a sum up to a token less u times all of it: each weight's counts (1 - u)-fold before the token,
-                // u-fold behind it, so 2 u (1 - u) of the bound for all (and the walk's own roundings)
+                // u-fold behind it, so 2 u (1 - u) of the bound for all. The log2(n / Z) of sums of u and 1 - u of Z are larger by
+                // log2(1 / u) and log2(1 / (1 - u)), which come to 6.6e-8 Z at most: a 64th of the bound covers it
                 const u64 slack = (u64)((float)off * 2.f * u * (1.f - u)) + (off >> 6) + 64;
                 mine = R.template walk<false>(-INFINITY, 0, 0, base, target, slack, &token, &at);
                 if (mine)
@@ -1150,6 +1152,8 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
                 have = __shfl_sync(0xffffffffu, have, who);
                 if (who != rank) return;
                 if (tid == 0) s_n = 0;
+                const int below = imax(0, kFrac - 63 + __clzll(have));  // factors of two by which its sum is below 1
+                const u64 slack = (u64)((float)have * ((float)kPart + below * (float)kPartOctave)) + (1ull << 15);
                 // its warps' parts and the token, by quick weights and, where their error leaves it open, by exact ones
                 for (int exact = 0; exact < 2; ++exact) {
                     u64 s;
@@ -1171,7 +1175,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
                         const u64 from = __shfl_sync(0xffffffffu, upto - y, l);
                         if (warp == l) {
                             if (exact) mine = R.template walk<true>(by.x, mine_, by.w, from, target, 0, &token, &at);
-                            else mine = R.template walk<false>(by.x, mine_, by.w, from, target, (u64)((float)have * (float)kQuick) + 64, &token, &at);
+                            else mine = R.template walk<false>(by.x, mine_, by.w, from, target, slack, &token, &at);
                             if (mine) s_n = 1;
                         }
                     }

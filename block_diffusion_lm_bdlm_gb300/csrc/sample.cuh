@@ -4,10 +4,19 @@
 // forms of it are used. The quick one is a multiplication and an exponential of
 // the special-function unit. Its errors, 2^-22 of the exponential, the roundings
 // of the argument and those of the sums, move any sum of weights of a row by
-// less than kQuick of the row's sum Z: an argument t = -log2 w is off by at most
-// |t| 2^-23, and the sum of w |t| is at most Z log2(vocabulary), which gives
-// 18 * 2^-23 * ln 2 = 1.5e-6; 2.4e-7 come from the exponential, and at most
-// 20 * 2^-24 = 1.2e-6 from additions in 32 bits.
+// less than kQuick of the row's sum Z. An argument t = -log2 w is half the
+// distance times 2 log2(e) / T: three roundings and the constant's own, a fifth
+// of one, so it is off by at most 3.2 |t| 2^-24. The sum of w |t| over n tokens
+// is at most Z log2(n / Z), and Z >= 1: 18 * 3.2 * 2^-24 * ln 2 = 2.4e-6. The
+// exponential adds 2.4e-7, and at most 20 additions in 32 bits 20 * 2^-24 =
+// 1.2e-6, together 3.9e-6.
+//
+// A sum z over one CTA's part of a row (of counted values: at most 2^15 tokens
+// of 16 bits, 33 additions) may be far below 1: 15 + log2(1 / z) take the place of
+// 18. With 2.4e-7 and 33 * 2^-24 that is 4.2e-6 z and 1.33e-7 z for each factor
+// of two by which z is below 1. Sums of whole multiples of 2^-44 are off by up to
+// half a unit for each of 2^15 tokens (the exact ones leave out what is below
+// 2^-45) and 2^10 partial sums, less than 2^15 units.
 //
 // The exact one is a whole multiple of 2^-44, from two-float arithmetic (sums
 // and products with their errors after Dekker and Knuth; a table of 2^(j/16)
@@ -25,7 +34,7 @@
 namespace bdlm {
 namespace sample {
 
-constexpr double kQuick = 4e-6;
+constexpr double kQuick = 4e-6, kPart = 4.3e-6, kPartOctave = 1.4e-7;
 constexpr int kMaxVocab = 1 << 18;
 constexpr int kFrac = 44;  // a weight of 1 is 2^44: 2^18 of them stay below 2^62
 

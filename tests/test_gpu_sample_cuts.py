@@ -64,3 +64,17 @@ def test_all_cuts_over_few_tokens(bd, dtype):
     u = torch.rand(rows, generator=torch.Generator("cuda").manual_seed(5), device="cuda")
     for how in (dict(top_k=2000, top_p=0.5, min_p=0.05), dict(top_k=100, top_p=0.9, min_p=0.2), dict(top_k=400, top_p=0.7, min_p=0.001)):
         check(bd, x, u, **how)
+
+
+@pytest.mark.parametrize("rows", [24, 9])
+def test_border_between_light_tokens(bd, rows):
+    """Rows of four and eight CTAs without cuts, whose counted values decide. The first CTA has tokens of 0.47 units of 2^-44 each, which
+    weigh nothing, and two of 59844 units behind them: a draw that falls between those two goes by exact weights alone."""
+    vocab = 131072
+    part = vocab // (4 if rows > 19 else 8)
+    x = torch.zeros((rows, vocab), dtype=torch.bfloat16, device="cuda")
+    x[:, :part - 2] = -31.25
+    x[:, part - 2:part] = -19.5
+    units = (vocab - part) * 2.0 ** 44
+    at = torch.tensor([1000, 30000, 52000, 59000, 61000, 63000, 67000, 75000, 100000] * 3, dtype=torch.float64)[:rows]
+    check(bd, x, (at / units).float().cuda())
