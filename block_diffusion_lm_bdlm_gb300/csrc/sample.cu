@@ -1207,8 +1207,11 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
                     z = R.total(s_all.quick) + (u64)(have < ties_k ? have : ties_k) * R.exact(R.at_key(key_k));
                 }
                 cut = R.template select<MASS>(cl, mul_ceil(p, z), by_k ? R.at_key(key_k) : -INFINITY, &skipped);
-                // from quick weights that key is the right one or next to it; exact ones tell
-                for (;;) {
+                // From quick weights that key is the right one or near it; exact ones tell. The next keys are tried first. Where
+                // single tokens weigh much less than the quick sums are off by, the cut lies thousands of tokens away: then steps grow
+                // fourfold until they pass it, and what is known of it is halved (fewer than 50 times in all).
+                uint32_t lo = by_k ? key_k - 1 : R.key_of(-INFINITY), hi = R.key_of(R.m) + 1;  // lo < the cut's key < hi
+                for (int turn = 0;; ++turn) {
                     R.weigh(cl, cut, !by_k);
                     const u64 above = R.total(s_all.quick), w = R.exact(R.at_key(cut));
                     long long have = R.total_ties();
@@ -1219,7 +1222,15 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
                         ties = (long long)((target - above + w - 1) / w);
                         break;
                     }
-                    cut = R.next_key(cl, cut, above >= target);
+                    const bool up = above >= target;
+                    if (up) lo = cut;
+                    else hi = cut;
+                    if (turn < 3) {
+                        cut = R.next_key(cl, cut, up);
+                    } else {
+                        const uint32_t half = (hi - lo) / 2, step = min(1u << 2 * min(turn - 2, 15), half);
+                        cut = up ? lo + step : hi - step;
+                    }
                 }
             }
             if (by_min) {

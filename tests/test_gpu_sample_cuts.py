@@ -1,5 +1,7 @@
 """Sampling where the three cuts meet: top-p goes by what the first k tokens weigh together, also those that min-p drops
 afterwards. Tokens have to equal the float64 oracle's; log-probabilities have test_gpu_sample's bound."""
+import math
+
 import numpy as np
 import pytest
 import torch
@@ -78,3 +80,31 @@ def test_border_between_light_tokens(bd, rows):
     units = (vocab - part) * 2.0 ** 44
     at = torch.tensor([1000, 30000, 52000, 59000, 61000, 63000, 67000, 75000, 100000] * 3, dtype=torch.float64)[:rows]
     check(bd, x, (at / units).float().cuda())
+
+
+@pytest.mark.parametrize("dtype", ["fp16", "fp32"])
+def test_top_p_far_from_where_quick_sums_put_it(bd, dtype):
+    """200 heavy tokens whose bins' sums are off by 4e-6 of themselves, more than thousands of the light ones weigh, and top-p
+    cuts among those: the cut is found in a few tens of passes (of about 15 us), not one token at a time."""
+    vocab, rows = 131072, 3
+    rng = np.random.default_rng(8)
+    x = rng.uniform(-1, 1, (rows, vocab))
+    for r in range(rows):
+        some = rng.choice(vocab, 201, replace=False)
+        x[r, some] = 15 - math.log(2) / 8
+        x[r, some[0]] = 15
+    x = torch.from_numpy(x).to(DTYPES[dtype]).cuda()
+    w = torch.exp(x.double() - x.double().amax(1, keepdim=True))
+    top = x.double() > 5
+    heavy, light = (w * top).sum(1), (w * ~top).sum(1)
+    p = ((heavy + light * torch.tensor([0.1, 0.5, 0.9], device="cuda", dtype=torch.float64)) / (heavy + light)).float()
+    for u in (1.0, 0.9999, 0.99995, 0.3):
+        check(bd, x, torch.full((rows,), u, device="cuda"), top_p=p)
+    start, end = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+    u = torch.full((rows,), 0.5, device="cuda")
+    start.record()
+    for _ in range(10):
+        bd.bdlm_sample(x, u, top_p=p)
+    end.record()
+    end.synchronize()
+    assert start.elapsed_time(end) / 10 < 5.0  # ms
