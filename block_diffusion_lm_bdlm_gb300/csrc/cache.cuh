@@ -95,7 +95,7 @@ struct CacheAttnArgs {
     uint8_t* scratch;  // behind the header
     const int* runs;   // int32 [3, n_seqs]: sequences that share pages (nullptr: each reads its own)
     float* planes;     // with runs: fp32 partial results, see cache_attn.cuh
-    float call_tiles;  // with runs: tiles that reading together costs a call, by sequence
+    float call_tiles;  // with runs: tiles that reading together costs a call, by sequence that may have rows
 };
 struct CachePrefixArgs {
     CacheView c;

@@ -118,7 +118,7 @@ int run_attn(CacheAttnArgs& a, void* workspace, size_t workspace_bytes, size_t n
     a.scratch = static_cast<uint8_t*>(workspace) + sizeof(WsHeader);
     if (a.runs) {
         a.planes = reinterpret_cast<float*>(a.scratch);
-        a.call_tiles = 32.f / a.c.n_seqs;
+        a.call_tiles = 32.f / imin(a.c.n_seqs, a.total_rows);
         a.scratch += cache_attn_plane_bytes(a.total_rows, a.H, a.c.D);
     }
     const int sms = device_sms();

@@ -92,11 +92,11 @@ constexpr int kFewRows = 8, kFewKeys = 2048, kMostKeys = 4096, kManyCtas = 256;
 __device__ __forceinline__ int few_keys(const CacheAttnArgs& a) { return a.c.n_seqs * a.c.Hk >= kManyCtas ? kMostKeys : kFewKeys; }
 __device__ __forceinline__ bool is_few(const CacheAttnArgs& a, int rows, int own) { return rows * (long long)a.G <= kFewRows && own <= few_keys(a); }
 
-// Whether n sequences with `rows` rows in all gain from reading `shared` positions together, in keys of a tile's time. Alone,
+// Whether n sequences with rows, `rows` in all, gain from reading `shared` positions together, in keys of a tile's time. Alone,
 // each takes MMA tiles of 128 flat rows through them, however few it has, or, if those are few, cache_own_kernel, in which a
 // key takes four fifths of that; together they take what their rows fill (those that fill a tile each gain nothing). Against
 // that stand, in tiles, the units that this adds and the joins, kRowCost for a flat row, or, where rows are few, kOwnCost for a
-// sequence; and 32 for the call (a.call_tiles for each of its sequences), if nothing else in it is read together. Twice as
+// sequence; and 32 for the call (a.call_tiles for each of the sequences that may have rows), if nothing else in it is read together. Twice as
 // many tiles of d = 64, which take half the time.
 // Alone and together, us, with 1024 shared keys (d = 128, G = 4, 100 own keys): 64 sequences of 1 row 38, 33; 16 runs of 4 38,
 // 45; 16 of 16 116, 85; with 8 rows each 100, 71; 97, 76; 361, 244; a run of 8 with 8 rows 31, 32; with 16 rows 16 runs of 4 105,
@@ -111,44 +111,85 @@ __device__ __forceinline__ bool worth(const CacheAttnArgs& a, int n, int rows, i
                                  __fmul_rn(wide, __fadd_rn(__fmul_rn(kRowCost, (float)flat), __fmul_rn((float)n, a.call_tiles)));
 }
 
+// Those without rows among a run's sequences read nothing and are not joined, so they do not count. A whole warp counts the
+// others: for all of its lanes at once where they name the SAME run, else for one run after the other, of which `last` is
+// kept. Short ones a lane counts by itself.
+struct Busy {
+    int first = -1, end = -1, n = 0;
+};
+__device__ __forceinline__ int busy_in(const CacheAttnArgs& a, int first, int end) {
+    int n = 0;
+    for (int i = first + (int)(threadIdx.x & 31); i < end; i += 32) n += __ldg(a.cu_rows + i + 1) > __ldg(a.cu_rows + i);
+    return __reduce_add_sync(0xffffffffu, n);
+}
+constexpr int kCounted = 128;
+template <bool SAME>
+__device__ __forceinline__ int busy_of(const CacheAttnArgs& a, int first, int end, bool ask, Busy* last) {
+    constexpr int kShort = 8;
+    if (SAME) return ask ? busy_in(a, first, end) : 0;
+    int n = 0;
+    if (ask && end - first <= kShort) {
+#pragma unroll
+        for (int k = 0; k < kShort; ++k) n += first + k < end && __ldg(a.cu_rows + first + k + 1) > __ldg(a.cu_rows + first + k);
+        ask = false;
+    }
+    for (;;) {
+        if (ask && first == last->first && end == last->end) {
+            n = last->n;
+            ask = false;
+        }
+        const unsigned todo = __ballot_sync(0xffffffffu, ask);
+        if (!todo) return n;
+        const int src = __ffs(todo) - 1;
+        last->first = __shfl_sync(0xffffffffu, first, src);
+        last->end = __shfl_sync(0xffffffffu, end, src);
+        last->n = busy_in(a, last->first, last->end);
+    }
+}
+
 // What the run of sequence s is, and whether it is well-formed: all of its
 // sequences name the same one, and share no more than each of their rows sees.
+// Called by whole warps.
 struct Run {
     int first, end, shared;
     bool ok;
 };
-template <bool CHECK>
-__device__ __forceinline__ Run run_of(const CacheAttnArgs& a, int s, const SeqRows& r) {
+template <bool CHECK, bool SAME>
+__device__ __forceinline__ Run run_of(const CacheAttnArgs& a, int s, const SeqRows& r, Busy* last) {
     const int n = a.c.n_seqs;
     const int *f = a.runs, *e = a.runs + n, *h = a.runs + 2 * (long long)n;
     Run u{__ldg(f + s), __ldg(e + s), __ldg(h + s), true};
-    if (!CHECK) {  // another kernel, or this one's beginning, has looked it over
-        if (u.shared > 0 && !worth(a, u.end - u.first, __ldg(a.cu_rows + u.end) - __ldg(a.cu_rows + u.first), u.shared)) u.shared = 0;
-        return u;
+    if (CHECK) {  // (else another kernel, or this one's beginning, has looked it over)
+        // the neighbours' too at once: loads that wait for one another are what this costs
+        const int i = imax(s - 1, 0), j = imin(s + 1, n - 1);
+        const bool before = __ldg(f + i) == u.first && __ldg(e + i) == u.end && __ldg(h + i) == u.shared;
+        const bool behind = __ldg(f + j) == u.first && __ldg(e + j) == u.end && __ldg(h + j) == u.shared;
+        u.ok = u.first >= 0 && u.first <= s && u.end > s && u.end <= n && u.shared >= 0 && (u.shared & (a.c.page - 1)) == 0;
+        u.ok = u.ok && (u.first == s || before) && (u.end == s + 1 || behind);
+        if (u.shared > 0 && (s == u.first || r.rows > 0)) u.ok = u.ok && u.shared <= r.len && (r.rows == 0 || u.shared <= r.pos0);
     }
-    // the neighbours' too at once: loads that wait for one another are what this costs
-    const int i = imax(s - 1, 0), j = imin(s + 1, n - 1);
-    const bool before = __ldg(f + i) == u.first && __ldg(e + i) == u.end && __ldg(h + i) == u.shared;
-    const bool behind = __ldg(f + j) == u.first && __ldg(e + j) == u.end && __ldg(h + j) == u.shared;
-    u.ok = u.first >= 0 && u.first <= s && u.end > s && u.end <= n && u.shared >= 0 && (u.shared & (a.c.page - 1)) == 0;
-    u.ok = u.ok && (u.first == s || before) && (u.end == s + 1 || behind);
-    if (u.shared > 0 && (s == u.first || r.rows > 0)) u.ok = u.ok && u.shared <= r.len && (r.rows == 0 || u.shared <= r.pos0);
-    if (u.ok && u.shared > 0 && !worth(a, u.end - u.first, __ldg(a.cu_rows + u.end) - __ldg(a.cu_rows + u.first), u.shared)) u.shared = 0;
+    // (a long run that would not gain if all that may have rows had some is not counted)
+    const bool asked = u.ok && u.shared > 0;
+    const int span = u.end - u.first, rows = asked ? __ldg(a.cu_rows + u.end) - __ldg(a.cu_rows + u.first) : 0;
+    const bool count = asked && (span <= kCounted || worth(a, imin(span, rows), rows, u.shared));
+    const int busy = busy_of<SAME>(a, u.first, u.end, count, last);
+    if (u.ok && !(count && worth(a, busy, rows, u.shared))) u.shared = 0;
     return u;
 }
 
 template <bool RUNS>
 __device__ __forceinline__ int items_of(const CacheAttnArgs& a) { return RUNS ? 2 * a.c.n_seqs : a.c.n_seqs; }
 
-template <bool RUNS, bool CHECK = false>
-__device__ __forceinline__ Rows item_rows(const CacheAttnArgs& a, int item) {
+// All lanes of a warp ask for the same item, or with `last` each for one of its own.
+template <bool RUNS, bool CHECK = false, bool SAME = true>
+__device__ __forceinline__ Rows item_rows(const CacheAttnArgs& a, int item, Busy* last = nullptr) {
     Rows r;
     r.seq = RUNS ? item >> 1 : item;
     static_cast<SeqRows&>(r) = seq_rows(a.c, a.cu_rows, a.q_pos, a.total_rows, r.seq);
     r.key0 = 0;
     r.part = PART_WHOLE;
     if (RUNS) {
-        const Run u = run_of<CHECK>(a, r.seq, r);
+        const Run u = run_of<CHECK, SAME>(a, r.seq, r, last);
         r.ok = r.ok && u.ok;
         if (item & 1) {
             if (u.shared > 0) {

@@ -110,7 +110,7 @@ __global__ void __launch_bounds__(kOwnThreads, 2) cache_own_kernel(const CacheAt
     __shared__ float s_top[WARPS][R], s_sum[WARPS][R];
     const int s = blockIdx.x, head = blockIdx.y, tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const SeqRows q = seq_rows(a.c, a.cu_rows, a.q_pos, a.total_rows, s);
-    const Run run = run_of<true>(a, s, q);  // (malformed ones must not be followed)
+    const Run run = run_of<true, true>(a, s, q, nullptr);  // (malformed ones must not be followed)
     const bool few = q.ok && run.ok && q.rows > 0 && is_few(a, q.rows, q.len - run.shared);
     if (!few) {
         asm volatile("griddepcontrol.wait;" ::: "memory");

@@ -106,7 +106,7 @@ struct Smem {
     static constexpr int kBar = kNanAny + 16;
     static constexpr int kWords = kBar + B_COUNT * 8;             // tmem, abort, error, info
     static constexpr int kStart = kWords + 16;                    // Start
-    static constexpr int kQExp = kStart + 64;                     // uint8 [256]: exponent of the rows' scale
+    static constexpr int kQExp = kStart + 96;                     // uint8 [256]: exponent of the rows' scale
     static constexpr int kPlace = kQExp + kUnitRows;              // Place of each warp
     static constexpr int kBytes = kPlace + (kThreads / 32) * kPlaceBytes;
 };
@@ -116,8 +116,9 @@ static_assert(Smem<128>::kBytes <= 232448, "shared memory");
 struct Start {
     long long per, left;
     int more, C, s, h, m0, off, bad;
+    Rows r;  // with runs: of item s (what a run is takes a warp some time to find out)
 };
-static_assert(sizeof(Start) <= 64, "");
+static_assert(sizeof(Start) <= 96, "");
 
 // A run of tiles of one unit.
 struct Seg {
@@ -147,7 +148,7 @@ __device__ __forceinline__ void begin_share(const CacheAttnArgs& a, const Start&
     p->off = st.off;
     p->left = st.left;
     if (st.left > 0) {
-        p->r = item_rows<RUNS>(a, st.s);
+        p->r = RUNS ? st.r : item_rows<RUNS>(a, st.s);
         p->u = unit_of<RUNS>(a, p->r, st.m0);
     }
     __syncwarp();
@@ -404,11 +405,13 @@ __device__ __forceinline__ void find_start(const CacheAttnArgs& a, Start* st, lo
     __syncthreads();
     long long W = 0, before = 0, cost = 0, sum;
     Rows r{};
+    Busy last;
     for (int s0 = 0; s0 < n; s0 += kThreads) {
         const int s = s0 + tid;
         bool have = s < n;
+        // (with runs whole warps ask)
+        if (RUNS || have) r = item_rows<RUNS, true, false>(a, imin(s, n - 1), &last);
         if (have) {
-            r = item_rows<RUNS, true>(a, s);
             if (!r.ok) atomicMin(&st->bad, r.seq);
             have = r.ok;
         }
@@ -435,7 +438,7 @@ __device__ __forceinline__ void find_start(const CacheAttnArgs& a, Start* st, lo
         for (int s0 = 0; s0 < n; s0 += kThreads) {
             const int s = s0 + tid;
             if (n > kThreads) {  // more than one pass: the costs again
-                if (s < n) r = item_rows<RUNS>(a, s);
+                if (RUNS || s < n) r = item_rows<RUNS, false, false>(a, imin(s, n - 1), &last);
                 cost = head_cost<RUNS>(a, r, s < n);
                 before = base + cta_scan(cost * a.c.Hk, &sum, buf);
                 base += sum;
@@ -460,6 +463,7 @@ __device__ __forceinline__ void find_start(const CacheAttnArgs& a, Start* st, lo
                     st->h = h;
                     st->m0 = m0;
                     st->off = (int)off;
+                    if (RUNS) st->r = r;
                 }
             }
         }
@@ -1345,7 +1349,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         r.more = st->more;
         r.C = st->C;
         if (st->left > 0) {
-            const Rows q = item_rows<RUNS>(a, st->s);
+            const Rows q = RUNS ? st->r : item_rows<RUNS>(a, st->s);
             r.row0 = q.row0;
             r.rows = q.rows;
             r.pos0 = q.pos0;
