@@ -95,6 +95,7 @@ struct CacheAttnArgs {
     uint8_t* scratch;  // behind the header
     const int* runs;   // int32 [3, n_seqs]: sequences that share pages (nullptr: each reads its own)
     float* planes;     // with runs: fp32 partial results, see cache_attn.cuh
+    int plane_rows;    // flat rows of each
     float call_tiles;  // with runs: tiles that reading together costs a call, by sequence that may have rows
 };
 struct CachePrefixArgs {
@@ -121,7 +122,8 @@ struct CachePagesArgs {
 };
 
 size_t cache_attn_scratch_bytes(long long total_rows, int H, int Hk, int D, int n_seqs);
-size_t cache_attn_plane_bytes(long long total_rows, int H, int D);
+long long cache_attn_plane_rows(long long total_rows, int G, int n_seqs);
+size_t cache_attn_plane_bytes(long long plane_rows, int Hk, int D);
 size_t cache_pages_scratch_bytes(int n_pages, int n_seqs);
 cudaError_t launch_cache_write(const CacheWriteArgs& a, int num_sms, cudaStream_t st, int* launches);
 cudaError_t launch_cache_attn(const CacheAttnArgs& a, int num_sms, cudaStream_t st, int* launches);

@@ -119,7 +119,8 @@ int run_attn(CacheAttnArgs& a, void* workspace, size_t workspace_bytes, size_t n
     if (a.runs) {
         a.planes = reinterpret_cast<float*>(a.scratch);
         a.call_tiles = 32.f / imin(a.c.n_seqs, a.total_rows);
-        a.scratch += cache_attn_plane_bytes(a.total_rows, a.H, a.c.D);
+        a.plane_rows = (int)cache_attn_plane_rows(a.total_rows, a.G, a.c.n_seqs);
+        a.scratch += cache_attn_plane_bytes(a.plane_rows, a.c.Hk, a.c.D);
     }
     const int sms = device_sms();
     int launches = 0;
@@ -181,7 +182,8 @@ int bdlm_cache_attn_fwd(const bdlm_cache* cache, int32_t layer, const void* q, v
 size_t bdlm_cache_attn_shared_fwd_workspace_bytes(int64_t total_rows, int32_t heads, int32_t kv_heads, int32_t head_dim,
                                                   int32_t n_seqs) {
     const size_t alone = bdlm_cache_attn_fwd_workspace_bytes(total_rows, heads, kv_heads, head_dim, n_seqs);
-    return alone ? cache_attn_plane_bytes(total_rows, heads, head_dim) + alone : 0;
+    if (!alone) return 0;
+    return cache_attn_plane_bytes(cache_attn_plane_rows(total_rows, heads / kv_heads, n_seqs), kv_heads, head_dim) + alone;
 }
 
 int bdlm_cache_attn_shared_fwd(const bdlm_cache* cache, int32_t layer, const void* q, void* o, float* lse,

@@ -18,8 +18,12 @@
 // all of the run's sequences (they lie side by side) as if they were one
 // sequence's; item 2 s + 1 is what sequence s reads alone. Rows of a run get
 // two partial results, one of each kind, in two planes, which are joined at the
-// end. A plane holds all of the call's flat rows, of each kv head, as a slot
-// holds a unit's, so units of either kind may be cut anywhere.
+// end. A plane holds flat rows, of each kv head, as a slot holds a unit's, so
+// units of either kind may be cut anywhere: all of the call's, or, where those
+// are more, 128 for each sequence. A run that is read together has fewer than
+// that for each of its sequences with rows, and its rows lie side by side from
+// the place of its first sequence on (69500 rows of 32 heads in 16 sequences,
+// d = 128: 34 MB instead of 2.3 GB).
 #pragma once
 
 #include "cache.cuh"
@@ -42,7 +46,7 @@ constexpr int kMinShare = 3;
 
 // What CTA c leaves for the merge: where its share begins, and its errors.
 struct ShareRec {
-    int row0, rows, pos0, len;  // the sequence (SeqRows) whose unit the share begins in
+    int row0, rows, pos0, len;  // the sequence (SeqRows) whose unit the share begins in; row0 of rows in a plane: Rows::plane
     int head, m0;               // kv head and first flat row of that unit
     int off, cost;              // where in the unit's cost the share begins, the unit's cost
     long long per;              // share_begin's constants
@@ -80,6 +84,7 @@ struct Rows : SeqRows {
     int seq;
     int key0;
     int part;  // where results go: 0 to o and lse, 1 and 2 into the first and second plane
+    int plane;  // there: the first flat row's place
 };
 enum : int { PART_WHOLE = 0, PART_SHARED = 1, PART_OWN = 2 };
 
@@ -102,12 +107,14 @@ __device__ __forceinline__ bool is_few(const CacheAttnArgs& a, int rows, int own
 // 45; 16 of 16 116, 85; with 8 rows each 100, 71; 97, 76; 361, 244; a run of 8 with 8 rows 31, 32; with 16 rows 16 runs of 4 105,
 // 108; 16 of 16 358, 345. (Without contractions: every kernel must come to the same.)
 constexpr float kRowCost = 0.053f, kOwnCost = 4.f;
+constexpr int kPlaneRows = 128;  // an MMA tile's
+static_assert(kFewRows < kPlaneRows, "rows of a run have places in the planes");
 __device__ __forceinline__ bool worth(const CacheAttnArgs& a, int n, int rows, int shared) {
     const int flat = rows * a.G, together = (flat + 127) >> 7;
     const float wide = a.c.D == 128 ? (float)kTileKeys : 2.f * kTileKeys;
     if (flat <= kFewRows * n && shared <= few_keys(a))
         return __fmul_rn((float)shared, (float)(4 * n - 5 * together)) > __fmul_rn(__fmul_rn(5.f * wide, (float)n), __fadd_rn(kOwnCost, a.call_tiles));
-    return flat < 128 * n && __fmul_rn((float)shared, (float)(n - together)) >
+    return flat < kPlaneRows * n && __fmul_rn((float)shared, (float)(n - together)) >
                                  __fmul_rn(wide, __fadd_rn(__fmul_rn(kRowCost, (float)flat), __fmul_rn((float)n, a.call_tiles)));
 }
 
@@ -152,13 +159,14 @@ __device__ __forceinline__ int busy_of(const CacheAttnArgs& a, int first, int en
 // Called by whole warps.
 struct Run {
     int first, end, shared;
+    int plane;  // place of the sequence's first flat row in the planes, if it is read together
     bool ok;
 };
 template <bool CHECK, bool SAME>
 __device__ __forceinline__ Run run_of(const CacheAttnArgs& a, int s, const SeqRows& r, Busy* last) {
     const int n = a.c.n_seqs;
     const int *f = a.runs, *e = a.runs + n, *h = a.runs + 2 * (long long)n;
-    Run u{__ldg(f + s), __ldg(e + s), __ldg(h + s), true};
+    Run u{__ldg(f + s), __ldg(e + s), __ldg(h + s), 0, true};
     if (CHECK) {  // (else another kernel, or this one's beginning, has looked it over)
         // the neighbours' too at once: loads that wait for one another are what this costs
         const int i = imax(s - 1, 0), j = imin(s + 1, n - 1);
@@ -170,10 +178,13 @@ __device__ __forceinline__ Run run_of(const CacheAttnArgs& a, int s, const SeqRo
     }
     // (a long run that would not gain if all that may have rows had some is not counted)
     const bool asked = u.ok && u.shared > 0;
-    const int span = u.end - u.first, rows = asked ? __ldg(a.cu_rows + u.end) - __ldg(a.cu_rows + u.first) : 0;
+    const int row0 = asked ? __ldg(a.cu_rows + u.first) : 0;
+    const int span = u.end - u.first, rows = asked ? __ldg(a.cu_rows + u.end) - row0 : 0;
     const bool count = asked && (span <= kCounted || worth(a, imin(span, rows), rows, u.shared));
     const int busy = busy_of<SAME>(a, u.first, u.end, count, last);
     if (u.ok && !(count && worth(a, busy, rows, u.shared))) u.shared = 0;
+    // (worth: fewer than kPlaneRows flat rows for each that is counted)
+    u.plane = a.plane_rows < a.total_rows * a.G ? kPlaneRows * u.first + (r.row0 - row0) * a.G : r.row0 * a.G;
     return u;
 }
 
@@ -188,9 +199,11 @@ __device__ __forceinline__ Rows item_rows(const CacheAttnArgs& a, int item, Busy
     static_cast<SeqRows&>(r) = seq_rows(a.c, a.cu_rows, a.q_pos, a.total_rows, r.seq);
     r.key0 = 0;
     r.part = PART_WHOLE;
+    r.plane = 0;
     if (RUNS) {
         const Run u = run_of<CHECK, SAME>(a, r.seq, r, last);
         r.ok = r.ok && u.ok;
+        r.plane = u.plane;
         if (item & 1) {
             if (u.shared > 0) {
                 r.key0 = u.shared;
@@ -217,13 +230,14 @@ __device__ __forceinline__ int keys_of(const CacheAttnArgs& a, const T& r, int p
     return key_end(r.len, a.block, p) - (RUNS ? r.key0 : 0);
 }
 
-// A plane: for each kv head normalised fp32 rows as [D / 4][T G] float4; behind both planes the rows' base-2 lse [Hk][T G] twice.
+// A plane: for each kv head normalised fp32 rows as [D / 4][plane_rows] float4; behind both planes the rows' base-2 lse
+// [Hk][plane_rows] twice.
 __device__ __forceinline__ float* plane_o(const CacheAttnArgs& a, int D, int part, int head) {
-    const long long flat = (long long)a.total_rows * a.G;
+    const long long flat = a.plane_rows;
     return a.planes + ((part - 1) * (long long)a.c.Hk + head) * D * flat;
 }
 __device__ __forceinline__ float* plane_lse(const CacheAttnArgs& a, int D, int part, int head) {
-    const long long flat = (long long)a.total_rows * a.G;
+    const long long flat = a.plane_rows;
     return a.planes + (2LL * a.c.Hk * D + (part - 1) * (long long)a.c.Hk + head) * flat;
 }
 

@@ -70,14 +70,14 @@ __device__ __forceinline__ void put_row(const CacheAttnArgs& a, int row, int h, 
 }
 
 template <int D>
-__device__ __forceinline__ void join_planes(const CacheAttnArgs& a, const SeqRows& q, int head) {
+__device__ __forceinline__ void join_planes(const CacheAttnArgs& a, const SeqRows& q, int plane, int head) {
     constexpr int CG = D / 32;  // groups of four pairs of float4
     const int lane = threadIdx.x & 31, groups = (q.rows * a.G + 7) / 8, each = kOwnThreads / 32;
-    const long long flat = (long long)a.total_rows * a.G;
+    const long long flat = a.plane_rows;
     for (int it = blockIdx.z * each + (threadIdx.x >> 5); it < groups * CG; it += gridDim.z * each) {
         const int c = it % CG * 4 + (lane >> 3), m = it / CG * 8 + (lane & 7);  // eight columns from 8 c on of flat row m
         if (m >= q.rows * a.G) continue;
-        const long long at = (long long)q.row0 * a.G + m;
+        const long long at = (long long)plane + m;
         const float l0 = __ldcg(plane_lse(a, D, PART_SHARED, head) + at), l1 = __ldcg(plane_lse(a, D, PART_OWN, head) + at);
         const float4* p0 = reinterpret_cast<const float4*>(plane_o(a, D, PART_SHARED, head)) + 2 * c * flat + at;
         const float4* p1 = reinterpret_cast<const float4*>(plane_o(a, D, PART_OWN, head)) + 2 * c * flat + at;
@@ -114,7 +114,7 @@ __global__ void __launch_bounds__(kOwnThreads, 2) cache_own_kernel(const CacheAt
     const bool few = q.ok && run.ok && q.rows > 0 && is_few(a, q.rows, q.len - run.shared);
     if (!few) {
         asm volatile("griddepcontrol.wait;" ::: "memory");
-        if (!share_recs(a.scratch)[0].bad && q.rows > 0 && run.shared > 0) join_planes<D>(a, q, head);
+        if (!share_recs(a.scratch)[0].bad && q.rows > 0 && run.shared > 0) join_planes<D>(a, q, run.plane, head);
         return;
     }
     if (blockIdx.z > 0) return;
@@ -306,13 +306,13 @@ __global__ void __launch_bounds__(kOwnThreads, 2) cache_own_kernel(const CacheAt
     asm volatile("griddepcontrol.wait;" ::: "memory");  // what the run shares, and the error word
     if (share_recs(a.scratch)[0].bad) return;
     if (bad) set_error(a.hdr, DEV_CHECK, s);
-    const long long all = (long long)a.total_rows * a.G;
+    const long long all = a.plane_rows;
     for (int it = tid; it < flat * (D / 8); it += kOwnThreads) {
         const int m = it / (D / 8), c = it % (D / 8);
         float top = -INFINITY, z = 0.f, y[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f}, w0 = 0.f, l0 = -INFINITY;
         float4 x0 = make_float4(0.f, 0.f, 0.f, 0.f), x1 = x0;
         if (key0 > 0) {
-            const long long at = (long long)q.row0 * a.G + m;
+            const long long at = (long long)run.plane + m;
             l0 = __ldcg(plane_lse(a, D, PART_SHARED, head) + at);
             const float4* p0 = reinterpret_cast<const float4*>(plane_o(a, D, PART_SHARED, head)) + 2 * c * all + at;
             x0 = __ldcg(p0);
@@ -352,8 +352,12 @@ __global__ void __launch_bounds__(kOwnThreads, 2) cache_own_kernel(const CacheAt
 
 }  // namespace
 
-size_t cache_attn_plane_bytes(long long total_rows, int H, int D) {
-    return (sizeof(float) * 2 * (size_t)total_rows * H * (D + 1) + 255) / 256 * 256;
+long long cache_attn_plane_rows(long long total_rows, int G, int n_seqs) {
+    const long long flat = total_rows * G, most = (long long)kPlaneRows * n_seqs;
+    return flat < most ? flat : most;
+}
+size_t cache_attn_plane_bytes(long long plane_rows, int Hk, int D) {
+    return (sizeof(float) * 2 * (size_t)plane_rows * Hk * (D + 1) + 255) / 256 * 256;
 }
 
 cudaError_t launch_cache_attn_shared(const CacheAttnArgs& a, int num_sms, cudaStream_t st, int* launches) {

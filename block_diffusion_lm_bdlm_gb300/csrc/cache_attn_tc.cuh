@@ -125,7 +125,7 @@ struct Seg {
     int row0, pos0, len;  // the sequence
     int s, h, m0, last, end;
     int kt0, kt1;
-    int key0, part;  // with runs (Rows)
+    int key0, part, plane;  // with runs (Rows)
     bool two, whole;
     __device__ __forceinline__ int tiles() const { return end ? kt1 - kt0 : 0; }
 };
@@ -168,7 +168,7 @@ __device__ __forceinline__ bool next_run(const CacheAttnArgs& a, Place* p) {
         found = kt1 > kt0;
         __syncwarp();
         if (found) {
-            p->g = Seg{r.row0, r.pos0, r.len, RUNS ? r.seq : s, h, m0, u.last, u.end, kt0, kt1, r.key0, r.part, u.two != 0, kt0 == 0 && kt1 == u.tiles};
+            p->g = Seg{r.row0, r.pos0, r.len, RUNS ? r.seq : s, h, m0, u.last, u.end, kt0, kt1, r.key0, r.part, r.plane, u.two != 0, kt0 == 0 && kt1 == u.tiles};
         }
         left -= n;
         if (left > 0) {  // the unit is done
@@ -1005,8 +1005,8 @@ __device__ __forceinline__ Out out_of(const CacheAttnArgs& a, const Seg& g) {
     out.slot = g.whole ? nullptr : slot_at(a.scratch, 2 * (int)blockIdx.x + (g.kt0 > 0 ? 0 : 1), (int)out.slot_r, D);
     out.slot_lse = out.slot + out.slot_r * D;
     if (RUNS && g.whole && g.part != PART_WHOLE) {
-        const long long at = (long long)g.row0 * a.G + g.m0;
-        out.slot_r = (long long)a.total_rows * a.G;
+        const long long at = (long long)g.plane + g.m0;
+        out.slot_r = a.plane_rows;
         out.slot = plane_o(a, D, g.part, g.h) + 4 * at;
         out.slot_lse = plane_lse(a, D, g.part, g.h) + at;
     }
@@ -1350,7 +1350,7 @@ __global__ void __launch_bounds__(kThreads, 1)
         r.C = st->C;
         if (st->left > 0) {
             const Rows q = RUNS ? st->r : item_rows<RUNS>(a, st->s);
-            r.row0 = q.row0;
+            r.row0 = RUNS && q.part != PART_WHOLE ? q.plane : q.row0;
             r.rows = q.rows;
             r.pos0 = q.pos0;
             r.len = q.len;

@@ -122,7 +122,7 @@ __global__ void __launch_bounds__(kMergeThreads) cache_merge_kernel(const CacheA
             }
             const int m = r.m0 + i0 + k, row = r.row0 + m / a.G, h = r.head * a.G + m % a.G;
             if (plane) {
-                const long long flat = (long long)a.total_rows * a.G, to = (long long)r.row0 * a.G + m;
+                const long long flat = a.plane_rows, to = (long long)r.row0 + m;
                 float4* dst = reinterpret_cast<float4*>(plane_o(a, D, r.part, r.head)) + 2 * q * flat + to;
                 dst[0] = make_float4(o[0], o[1], o[2], o[3]);
                 dst[flat] = make_float4(o[4], o[5], o[6], o[7]);
