@@ -126,8 +126,11 @@ struct Busy {
 };
 __device__ __forceinline__ int busy_in(const CacheAttnArgs& a, int first, int end) {
     int n = 0;
-    for (int i = first + (int)(threadIdx.x & 31); i < end; i += 32) n += __ldg(a.cu_rows + i + 1) > __ldg(a.cu_rows + i);
-    return __reduce_add_sync(0xffffffffu, n);
+    for (int i0 = first; i0 < end; i0 += 32) {
+        const int i = i0 + (int)(threadIdx.x & 31);
+        n += __popc(__ballot_sync(0xffffffffu, i < end && __ldg(a.cu_rows + i + 1) > __ldg(a.cu_rows + i)));
+    }
+    return n;
 }
 constexpr int kCounted = 128;
 template <bool SAME>
@@ -136,8 +139,11 @@ __device__ __forceinline__ int busy_of(const CacheAttnArgs& a, int first, int en
     if (SAME) return ask ? busy_in(a, first, end) : 0;
     int n = 0;
     if (ask && end - first <= kShort) {
+        int at[kShort + 1];
 #pragma unroll
-        for (int k = 0; k < kShort; ++k) n += first + k < end && __ldg(a.cu_rows + first + k + 1) > __ldg(a.cu_rows + first + k);
+        for (int k = 0; k <= kShort; ++k) at[k] = first + k <= end ? __ldg(a.cu_rows + first + k) : 0;
+#pragma unroll
+        for (int k = 0; k < kShort; ++k) n += at[k + 1] > at[k];  // (0 is no more than what is before it)
         ask = false;
     }
     for (;;) {

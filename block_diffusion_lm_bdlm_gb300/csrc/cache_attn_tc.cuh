@@ -410,7 +410,7 @@ __device__ __forceinline__ void find_start(const CacheAttnArgs& a, Start* st, lo
         const int s = s0 + tid;
         bool have = s < n;
         // (with runs whole warps ask)
-        if (RUNS || have) r = item_rows<RUNS, true, false>(a, imin(s, n - 1), &last);
+        if (RUNS ? s0 + (tid & ~31) < n : have) r = item_rows<RUNS, true, false>(a, imin(s, n - 1), &last);
         if (have) {
             if (!r.ok) atomicMin(&st->bad, r.seq);
             have = r.ok;
@@ -438,7 +438,7 @@ __device__ __forceinline__ void find_start(const CacheAttnArgs& a, Start* st, lo
         for (int s0 = 0; s0 < n; s0 += kThreads) {
             const int s = s0 + tid;
             if (n > kThreads) {  // more than one pass: the costs again
-                if (RUNS || s < n) r = item_rows<RUNS, false, false>(a, imin(s, n - 1), &last);
+                if (RUNS ? s0 + (tid & ~31) < n : s < n) r = item_rows<RUNS, false, false>(a, imin(s, n - 1), &last);
                 cost = head_cost<RUNS>(a, r, s < n);
                 before = base + cta_scan(cost * a.c.Hk, &sum, buf);
                 base += sum;

@@ -29,8 +29,9 @@ constexpr int kMergeThreads = 256;
 constexpr int kSlices = 3;
 constexpr int kMaxParts = kMaxCtas + 1;
 
+// (four CTAs to an SM: the compiler takes 79 registers for d = 64 unless it is told, and a short call then 1.3 us more of 13)
 template <int D, bool RUNS>
-__global__ void __launch_bounds__(kMergeThreads) cache_merge_kernel(const CacheAttnArgs a, int ctas) {
+__global__ void __launch_bounds__(kMergeThreads, D == 64 ? 4 : 0) cache_merge_kernel(const CacheAttnArgs a, int ctas) {
     __shared__ float s_w[kMaxParts][32];  // weights of 32 rows at a time
     __shared__ float s_lse[32];
     __shared__ int s_err[2];
