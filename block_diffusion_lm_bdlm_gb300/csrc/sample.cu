@@ -1290,7 +1290,10 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
         constexpr u64 one = 1ull << kFrac;
         const float lz = whole_z < 2 * one ? log1pf((float)(whole_z > one ? whole_z - one : 0) * 0x1p-44f) : logf((float)whole_z * 0x1p-44f);
         a.token[row] = token;
-        a.logprob[row] = at - R.m - lz;
+        // at - m - lz, the two sums with their errors (Knuth), so that it is rounded once
+        const float d = BDLM_ADD(at, -R.m), db = BDLM_ADD(d, -at), s = BDLM_ADD(d, -lz), sb = BDLM_ADD(s, -d);
+        const float de = BDLM_ADD(BDLM_ADD(at, -BDLM_ADD(d, -db)), BDLM_ADD(-R.m, -db)), se = BDLM_ADD(BDLM_ADD(d, -BDLM_ADD(s, -sb)), BDLM_ADD(-lz, -sb));
+        a.logprob[row] = BDLM_ADD(s, BDLM_ADD(de, se));
     }
 }
 
