@@ -27,12 +27,18 @@
 // the cut again in finer ones until it is a single logit. The part in which the
 // kept weights pass u times all of them then finds the token.
 //
-// Bound. Instruction issue (60 % of the slots) and the barriers of the cluster, of
-// which a listed row takes three. 512 rows of 131072 bf16 logits, 134 MB (20 us
-// of memory), take 101 us with top-k 50, 198 with top-p 0.95 where most rows are
-// listed and some count their values, 312 where all do, 141 without cuts. One
-// row of 32001 takes 10 us. Two CTAs of 512 threads share an SM; three of 256
-// were no faster on the whole.
+// Bound. No one thing. 512 rows of 131072 bf16 logits, a quarter left out, top-p 0.95
+// (104 MB, 15 us of memory, 186 us under the profiler): an SM has a CTA for 55 % of
+// that time, between clusters of four that need four free places at once, and then
+// issues in 61 % of its slots: 48 instructions a logit. A CTA of a listed row takes
+// 31 thousand clocks if it is the first and 21 thousand if not, of which the copy is
+// 3.8, the maximum and its barrier 4.9, the sums and the list 6.2, their barrier 4.4,
+// ranking and drawing 9.2. One of a row that counts its values goes on for 14 to
+// count, 6 to weigh the places, 6 to sum up the cluster's, 8 to cut, and 14 to draw.
+// 512 whole rows take 84 us greedy, 99 with top-k 50, 133 without cuts, 171 with top-p
+// 0.95 where most rows are listed, 305 where all are counted; of fp16 logits where
+// none is listed 566, of fp32 ones 1140 (bins, several passes). One row of 32001 takes
+// 10 us. Two CTAs of 512 threads share an SM; three of 256 were no faster on the whole.
 #include <cooperative_groups.h>
 #include <cuda_bf16.h>
 #include <cuda_fp16.h>
