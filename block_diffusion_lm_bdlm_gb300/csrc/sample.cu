@@ -999,7 +999,7 @@ __global__ void __launch_bounds__(kThreads, 2) sample_kernel(const SampleArgs a)
         // some of those only afterwards, so the list has to have all k, or every token above -infinity.
         const bool by_min_all = by_min && R.exact(x0) < least_w && (!(by_k && by_p) || x0 == -3.402823466e38f);
         if (!greedy)
-            // (a thread may have added up as many as 64 of the listed weights, 3.8e-6 of them: twice kQuick covers that)
+            // (a thread may have added up as many as 72 of the listed weights, 72 * 2^-24 = 4.3e-6: twice kQuick covers that)
             listed = listed && (by_min_all || (by_k ? ln >= top_k : by_p && lw >= mul_ceil(p, quick_z + off) + 2 * off));
     }
     if (listed) {

@@ -12,9 +12,9 @@
 // 1.2e-6, together 3.9e-6.
 //
 // A sum z over one CTA's part of a row (of counted values: at most 2^15 tokens
-// of 16 bits, 33 additions) may be far below 1: 15 + log2(1 / z) take the place of
-// 18. With 2.4e-7 and 33 * 2^-24 that is 4.2e-6 z and 1.33e-7 z for each factor
-// of two by which z is below 1. Sums of whole multiples of 2^-44 are off by up to
+// of 16 bits, nine vectors of a thread and so 37 additions) may be far below 1: 15
+// + log2(1 / z) take the place of 18. With 2.4e-7 and 37 * 2^-24 that is 4.5e-6 z
+// and 1.33e-7 z for each factor of two by which z is below 1. Sums of whole multiples of 2^-44 are off by up to
 // half a unit for each of 2^15 tokens (the exact ones leave out what is below
 // 2^-45) and 2^10 partial sums, less than 2^15 units.
 //
@@ -34,7 +34,7 @@
 namespace bdlm {
 namespace sample {
 
-constexpr double kQuick = 4e-6, kPart = 4.3e-6, kPartOctave = 1.4e-7;
+constexpr double kQuick = 4e-6, kPart = 4.6e-6, kPartOctave = 1.4e-7;
 constexpr int kMaxVocab = 1 << 18;
 constexpr int kFrac = 44;  // a weight of 1 is 2^44: 2^18 of them stay below 2^62
 
